@@ -476,6 +476,117 @@ int ddp_allreduce_mean_from_host_h(zero_ddp_host_t *h, const void *const *host_g
                                    void *host_mean_out, int64_t chunk_bytes, zero_stream_t compute,
                                    zero_stream_t h2d, zero_stream_t d2h);
 
+/* -------------------------------------------------- vocabulary losses -- */
+
+/* The losses a language model's gradients begin with, taken from the hidden
+ * states and the head's weight without ever storing the logits
+ * z = hidden * weight^T (T x V): the vocabulary is worked off in pieces, the
+ * forward pass keeps the running maximum and sum of each row's softmax, and
+ * the backward pass forms a piece's logits again. Their gradients are written
+ * where zero_step reads them: dweight may be a view into a rank's flat
+ * gradient buffer.
+ *
+ * zero_xent_*: softmax cross entropy,
+ *     loss_t = lse_t - z[t][y_t],           lse_t = log sum_v exp z[t][v].
+ * zero_distill_*: distillation from a teacher's top K logits u at temperature
+ * tau, mixed with the cross entropy when labels are given,
+ *     q_t    = softmax over the row's present entries of u / tau,
+ *     kl_t   = sum_k q_tk (log q_tk - z[t][id_k] / tau + lse'_t),
+ *     lse'_t = log sum_v exp(z[t][v] / tau),
+ *     loss_t = (1 - alpha) (lse_t - z[t][y_t]) + alpha tau^2 kl_t.
+ * A term whose row has no label, or no teacher entry, is zero; a row with
+ * neither is empty: its loss is 0, its dhidden row is zero, it adds nothing to
+ * dweight, is not counted by the mean, and its hidden state is not read (it
+ * may hold anything, NaN included).
+ *
+ * Arithmetic: products of the stored values summed in fp32 on the tensor cores
+ * (ZERO_FP32 values are split into three bf16 parts, whose six largest
+ * products keep fp32's precision); softmax statistics, losses and the sums of
+ * both gradients are fp32 or wider; in ZERO_BF16_MIXED the gradient of the
+ * logits is rounded to bf16 once, as the operand of the two gradient products.
+ * No atomics add values: equal inputs give equal bits. */
+
+/* Reduction of the rows' losses, and what dloss is a gradient of. */
+enum {
+  ZERO_REDUCE_NONE = 0, /* loss[T] only; dloss has T entries               */
+  ZERO_REDUCE_MEAN = 1, /* the mean over the rows that are not empty (0 when
+                           every row is); dloss is one value               */
+  ZERO_REDUCE_SUM = 2   /* the sum; dloss is one value                     */
+};
+
+#define ZERO_DISTILL_MAX_K 1024
+
+/* One call's problem. Pointers are DEVICE pointers; T, V and D are below 2^31
+ * (V and D at least 1, T may be 0). Strides are in elements and at least D;
+ * the elements of a row are adjacent. Every layout and alignment down to the
+ * element's own is served; 16-byte aligned bf16 weight rows are read in place
+ * (others are copied to the workspace first). */
+typedef struct zero_head_loss {
+  int64_t T, V, D;        /* tokens, vocabulary, hidden width                  */
+  int32_t precision;      /* of hidden, weight, dhidden, dweight: ZERO_FP32
+                             (float) or ZERO_BF16_MIXED (bf16)                 */
+  int32_t reduction;      /* ZERO_REDUCE_*                                     */
+  const void *hidden;     /* [T][D], rows hidden_stride apart                  */
+  int64_t hidden_stride;
+  const void *weight;     /* [V][D], rows weight_stride apart                  */
+  int64_t weight_stride;
+  const int64_t *labels;  /* [T], or NULL (distillation alone). A label equal
+                             to ignore_index or outside [0, V) is no label     */
+  int64_t ignore_index;
+  /* Distillation; NULL, 0 and unused for zero_xent_*. */
+  const int64_t *teacher_ids;   /* [T][teacher_k]; an id outside [0, V) is an
+                                   absent entry, and so is a logit of -inf;
+                                   entries of equal id add their q             */
+  const float *teacher_logits;  /* [T][teacher_k]                              */
+  int64_t teacher_k;            /* 1 .. ZERO_DISTILL_MAX_K                     */
+  double temperature;           /* tau: finite, > 0                            */
+  double alpha;                 /* in [0, 1]; 1 when labels is NULL            */
+  /* Written by the forward pass, read by the backward pass (lse, lse_tau). */
+  float *loss;            /* [T]; 0 for an empty row                           */
+  float *lse;             /* [T]: lse_t; needed with labels                    */
+  float *lse_tau;         /* [T]: lse'_t; needed for distillation              */
+  float *reduced;         /* one value: the mean or sum (ignored for NONE)     */
+  /* Backward pass. */
+  const float *dloss;     /* gradient of the total with respect to the losses
+                             (NONE: [T]; entries of empty rows are not read) or
+                             to the reduced loss (one value); NULL: ones       */
+  double grad_scale;      /* multiplies both gradients (1.0: none); finite     */
+  void *dhidden;          /* [T][D], rows dhidden_stride apart; NULL: not taken */
+  int64_t dhidden_stride;
+  void *dweight;          /* [V][D], rows dweight_stride apart; NULL: not taken */
+  int64_t dweight_stride;
+  int32_t accumulate;     /* nonzero: dweight += its gradient (one rounding),
+                             e.g. a tied embedding or a further micro-batch    */
+  /* Caller-owned scratch, 256-byte aligned, at least the bytes that the
+   * workspace query gives; contents overwritten, nothing kept between calls. */
+  void *workspace;
+  int64_t workspace_bytes;
+} zero_head_loss_t;
+
+/* Workspace of any call on this problem (the three calls below need no more;
+ * with neither dhidden nor dweight set, the forward pass's own, smaller need).
+ * The pointers' values matter only for their alignment and for NULL.
+ * Errors: as the calls', where they concern sizes and options. */
+int zero_xent_workspace_bytes(const zero_head_loss_t *p, int64_t *bytes);
+int zero_distill_workspace_bytes(const zero_head_loss_t *p, int64_t *bytes);
+
+/* forward: loss, lse (and lse_tau), reduced.
+ * backward: dhidden and/or dweight from the inputs and the forward pass's lse
+ * (and lse_tau) on the same inputs. step: both in one call, which prepares the
+ * inputs once; the same bits. Everything is queued on `stream`.
+ * Errors: EINVAL (sizes, strides below D, precision or reduction, a NULL
+ * input or output, teacher_k, temperature, alpha or grad_scale out of range,
+ * teacher fields given to zero_xent_*, neither gradient asked for, a workspace
+ * that is too small, an output or the workspace overlapping another buffer),
+ * EALIGN (a pointer not aligned to its element, a workspace not to 256 bytes),
+ * ECUDA. */
+int zero_xent_forward(const zero_head_loss_t *p, zero_stream_t stream);
+int zero_xent_backward(const zero_head_loss_t *p, zero_stream_t stream);
+int zero_xent_step(const zero_head_loss_t *p, zero_stream_t stream);
+int zero_distill_forward(const zero_head_loss_t *p, zero_stream_t stream);
+int zero_distill_backward(const zero_head_loss_t *p, zero_stream_t stream);
+int zero_distill_step(const zero_head_loss_t *p, zero_stream_t stream);
+
 /* ---------------------------------------------------------------- memory -- */
 
 /* Model-state bytes per rank after a step, by stage: 0 = plain DDP, 1 = shard

@@ -1,0 +1,391 @@
+"""The vocabulary losses on the GPU against their definition in 64 bits, within
+bounds derived from their arithmetic (loss_util). Matrices sit between guard
+regions, with sentinels in the gaps of their rows: a read past a row's end
+brings a NaN into the result, a write past it is found afterwards."""
+
+import math
+
+import pytest
+import torch
+
+import parity_util
+from loss_util import IGNORE, bounds, check, reference
+
+pytestmark = pytest.mark.gpu
+
+TYPES = {"bf16": torch.bfloat16, "fp32": torch.float32}
+
+
+@pytest.fixture(scope="module")
+def losses(abi, cuda):
+    from zero_sharded_optimizer_gb300 import losses as module
+    return module
+
+
+def matrix(values, device, pad=0, offset=0, what="matrix"):
+    """`values` in a guarded buffer of rows `pad` elements apart."""
+    n, d = values.shape
+    buf = parity_util.guarded_empty(max(n * (d + pad), 1), values.dtype, device, offset, what)
+    m = torch.as_strided(buf, (n, d), (d + pad, 1), buf.storage_offset())
+    m.copy_(values)
+    return m
+
+
+def empty_matrix(n, d, dtype, device, pad=0, offset=0, what="output"):
+    buf = parity_util.guarded_empty(max(n * (d + pad), 1), dtype, device, offset, what)
+    return torch.as_strided(buf, (n, d), (d + pad, 1), buf.storage_offset()), buf
+
+
+def gaps_untouched(buf, n, d, pad):
+    """The gaps between an output's rows still hold the sentinel."""
+    if pad == 0 or n < 2:
+        return
+    bits = buf.view(torch.int32 if buf.dtype == torch.float32 else torch.int16)
+    s = 0x7FA5A5A5 if buf.dtype == torch.float32 else 0x7FA5
+    assert bool((bits[:n * (d + pad)].view(n, d + pad)[:, d:] == s).all())
+
+
+def inputs(T, V, D, dtype, seed, device, masked=0.0):
+    g = torch.Generator().manual_seed(seed)
+    labels = torch.randint(0, V, (T,), generator=g)
+    w = torch.randn(V, D, generator=g) * 0.7 / math.sqrt(D)
+    h = torch.randn(T, D, generator=g) + 4.0 * torch.rand(T, 1, generator=g) * w[labels]
+    labels[torch.rand(T, generator=g) < masked] = IGNORE
+    return h.to(dtype).to(device), w.to(dtype).to(device), labels.to(device), g
+
+
+def teacher(T, V, K, g, device, absent=0.0):
+    ids = torch.stack([torch.randperm(V, generator=g)[:K] for _ in range(T)]) if T else \
+        torch.zeros(0, K, dtype=torch.int64)
+    logits = 3.0 * torch.randn(T, K, generator=g)
+    ids[torch.rand(T, K, generator=g) < absent] = -1
+    return ids.to(device), logits.to(device)
+
+
+# One to a few tiles in each direction, on and around their edges.
+SIZES = [(1, 1, 1), (1, 257, 64), (2, 255, 7), (3, 256, 8), (127, 300, 65), (128, 512, 64),
+         (129, 513, 128), (300, 1000, 96), (257, 2049, 192), (64, 700, 513), (130, 259, 1032)]
+
+
+@pytest.mark.parametrize("T,V,D", SIZES)
+@pytest.mark.parametrize("kind", TYPES)
+def test_xent_step(losses, cuda, kind, T, V, D):
+    dt = TYPES[kind]
+    h, w, y, _ = inputs(T, V, D, dt, 1000 + T + V + D, cuda, masked=0.2 if T > 2 else 0.0)
+    h, w = matrix(h, cuda), matrix(w, cuda)
+    for reduction in ("mean", "sum"):
+        r = reference(h, w, y, reduction=reduction)
+        got = losses.xent_step(h, w, y, reduction=reduction)
+        check(got, r, dt, f"{kind} {reduction}")
+
+
+@pytest.mark.parametrize("pad,offset", [(0, 1), (1, 0), (3, 5), (8, 0), (8, 8), (5, 3)])
+@pytest.mark.parametrize("kind", TYPES)
+def test_strides_and_alignment(losses, cuda, kind, pad, offset):
+    dt = TYPES[kind]
+    for T, V, D in [(70, 515, 72), (33, 300, 67)]:
+        h, w, y, g = inputs(T, V, D, dt, 7 + pad + offset, cuda, masked=0.3)
+        h = matrix(h, cuda, pad, offset, "hidden")
+        w = matrix(w, cuda, pad, offset, "weight")
+        dh, dh_buf = empty_matrix(T, D, dt, cuda, pad, offset, "dhidden")
+        dw, dw_buf = empty_matrix(V, D, dt, cuda, pad, offset, "dweight")
+        dloss = torch.rand(T, generator=g).to(cuda)
+        got = losses.xent_step(h, w, y, reduction="none", dloss=dloss, dhidden=dh, dweight=dw)
+        check(got, reference(h, w, y, reduction="none", dloss=dloss), dt, f"{kind} {pad} {offset}")
+        gaps_untouched(dh_buf, T, D, pad)
+        gaps_untouched(dw_buf, V, D, pad)
+
+
+@pytest.mark.parametrize("kind", TYPES)
+def test_empty_rows_are_not_read(losses, cuda, kind):
+    """Rows without a target hold NaN and infinities, in the hidden states and
+    in dloss; an ignore index inside the vocabulary; labels out of range."""
+    dt = TYPES[kind]
+    T, V, D = 200, 777, 80
+    h, w, y, g = inputs(T, V, D, dt, 5, cuda)
+    gone = torch.rand(T, generator=g).to(cuda) < 0.5
+    for mark, ignore in [(IGNORE, IGNORE), (0, 0), (V, IGNORE), (-1, IGNORE), (2 ** 40, IGNORE)]:
+        labels = torch.where(gone, mark, y.clamp(min=1))
+        bad = h.clone()
+        bad[gone] = math.nan
+        bad[torch.nonzero(gone)[::2, 0]] = math.inf
+        dloss = torch.where(gone, math.nan, torch.rand(T, generator=g).to(cuda))
+        r = reference(bad, w, labels, ignore_index=ignore, reduction="none", dloss=dloss)
+        got = losses.xent_step(bad, w, labels, ignore_index=ignore, reduction="none", dloss=dloss)
+        check(got, r, dt, f"{kind} {mark}")
+        assert bool((got.loss[gone] == 0).all()) and bool((got.dhidden[gone] == 0).all())
+        mean = losses.xent_forward(bad, w, labels, ignore_index=ignore)
+        assert float(mean.reduced) == pytest.approx(float(got.loss.double().sum()) / int((~gone).sum()), rel=1e-6)
+
+
+@pytest.mark.parametrize("kind", TYPES)
+def test_no_row_has_a_target(losses, cuda, kind):
+    dt = TYPES[kind]
+    h, w, _, _ = inputs(5, 300, 40, dt, 3, cuda)
+    y = torch.full((5,), IGNORE, device=cuda)
+    got = losses.xent_step(torch.full_like(h, math.nan), w, y)
+    assert float(got.reduced) == 0.0 and not got.loss.any()
+    assert not got.dhidden.any() and not got.dweight.any()
+    ids = torch.full((5, 3), -1, device=cuda)
+    got = losses.distill_step(torch.full_like(h, math.nan), w, ids, torch.zeros(5, 3, device=cuda))
+    assert float(got.reduced) == 0.0 and not got.dhidden.any() and not got.dweight.any()
+
+
+@pytest.mark.parametrize("kind", TYPES)
+def test_no_rows(losses, cuda, kind):
+    dt = TYPES[kind]
+    w = torch.ones(300, 40, dtype=dt, device=cuda)
+    got = losses.xent_step(torch.empty(0, 40, dtype=dt, device=cuda), w,
+                           torch.empty(0, dtype=torch.int64, device=cuda))
+    assert got.loss.shape == (0,) and got.dhidden.shape == (0, 40)
+    assert float(got.reduced) == 0.0 and not got.dweight.any()
+    before = torch.randn(300, 40, device=cuda).to(dt)
+    dw = before.clone()
+    losses.xent_step(torch.empty(0, 40, dtype=dt, device=cuda), w,
+                     torch.empty(0, dtype=torch.int64, device=cuda), dweight=dw, accumulate=True)
+    assert torch.equal(dw, before)
+
+
+@pytest.mark.parametrize("kind", TYPES)
+def test_a_row_that_is_not_finite_shows(losses, cuda, kind):
+    """A NaN in a row with a target makes that row's loss NaN, and no other's."""
+    dt = TYPES[kind]
+    h, w, y, _ = inputs(140, 600, 72, dt, 11, cuda)
+    h[3, 5] = math.nan
+    got = losses.xent_forward(h, w, y, reduction="none")
+    assert math.isnan(float(got.loss[3]))
+    rest = torch.arange(140, device=cuda) != 3
+    assert bool(torch.isfinite(got.loss[rest]).all())
+
+
+@pytest.mark.parametrize("K,absent", [(1, 0.0), (5, 0.4), (32, 0.0), (64, 0.2), (200, 0.1)])
+@pytest.mark.parametrize("kind", TYPES)
+def test_distill_step(losses, cuda, kind, K, absent):
+    dt = TYPES[kind]
+    for T, V, D, tau, alpha, with_labels in [(150, 1000, 96, 2.0, 0.5, True), (37, 300, 33, 1.0, 1.0, False),
+                                             (130, 513, 64, 0.5, 0.25, True), (64, 400, 64, 4.0, 1.0, True),
+                                             (20, 400, 64, 4.0, 0.0, True)]:
+        h, w, y, g = inputs(T, V, D, dt, K + T, cuda, masked=0.3)
+        ids, logits = teacher(T, V, K, g, cuda, absent)
+        ids[::9] = -1
+        labels = y if with_labels else None
+        for reduction in ("mean", "none"):
+            dloss = torch.rand(T, generator=g).to(cuda) if reduction == "none" else None
+            more = dict(tau=tau, alpha=alpha, reduction=reduction, dloss=dloss)
+            r = reference(h, w, labels, ids, logits, **more)
+            got = losses.distill_step(h, w, ids, logits, temperature=tau, labels=labels, alpha=alpha,
+                                      reduction=reduction, dloss=dloss)
+            check(got, r, dt, f"{kind} {T} {reduction}")
+
+
+@pytest.mark.parametrize("kind", TYPES)
+def test_teacher_entries_at_their_edges(losses, cuda, kind):
+    """Equal ids, ids out of range, logits of minus infinity and of the type's
+    lowest value, the label inside and outside the list, ids at tile edges."""
+    dt = TYPES[kind]
+    T, V, D, K = 140, 700, 64, 6
+    h, w, y, g = inputs(T, V, D, dt, 21, cuda)
+    ids, logits = teacher(T, V, K, g, cuda)
+    lowest = torch.finfo(torch.float32).min
+    ids[0] = 7                                    # one id six times
+    ids[1] = torch.tensor([255, 256, 511, 512, 699, 0])
+    ids[2] = torch.tensor([-1, V, 2 ** 33, 5, 5, 9])
+    logits[3] = -math.inf                         # all absent, but a label
+    logits[4, 1:] = -math.inf
+    logits[5] = lowest                            # uniform
+    logits[6, 1:] = lowest                        # one entry has everything
+    ids[7, 0] = y[7]
+    ids[8, :3] = y[8]
+    y[9] = IGNORE
+    y[10] = IGNORE
+    ids[10] = -1                                  # neither: empty
+    h[10] = math.nan
+    for labels, alpha in [(y, 0.5), (None, 1.0)]:
+        bad = h.clone()
+        if labels is None:
+            bad[3] = math.nan
+        r = reference(bad, w, labels, ids, logits, tau=1.5, alpha=alpha, reduction="sum")
+        got = losses.distill_step(bad, w, ids, logits, temperature=1.5, labels=labels, alpha=alpha,
+                                  reduction="sum")
+        check(got, r, dt, f"{kind} {alpha}")
+
+
+def test_distill_many_entries(losses, cuda):
+    T, V, D, K = 9, 5000, 64, 1024
+    h, w, y, g = inputs(T, V, D, torch.bfloat16, 2, cuda)
+    ids, logits = teacher(T, V, K, g, cuda)
+    r = reference(h, w, y, ids, logits, tau=2.0, alpha=0.5)
+    check(losses.distill_step(h, w, ids, logits, temperature=2.0, labels=y, alpha=0.5), r,
+          torch.bfloat16)
+
+
+@pytest.mark.parametrize("kind", TYPES)
+def test_backward_alone_equals_step(losses, cuda, kind):
+    dt = TYPES[kind]
+    T, V, D = 190, 900, 104
+    h, w, y, g = inputs(T, V, D, dt, 8, cuda, masked=0.2)
+    ids, logits = teacher(T, V, 12, g, cuda, 0.1)
+    dloss = torch.tensor(0.37, device=cuda)
+    a = losses.xent_step(h, w, y, dloss=dloss, grad_scale=0.5)
+    f = losses.xent_forward(h, w, y)
+    b = losses.xent_backward(h, w, y, f.lse, dloss=dloss, grad_scale=0.5)
+    assert torch.equal(a.loss, f.loss) and torch.equal(a.reduced, f.reduced)
+    assert torch.equal(a.dhidden, b.dhidden) and torch.equal(a.dweight, b.dweight)
+    check(b, reference(h, w, y, dloss=dloss, grad_scale=0.5), dt)
+    a = losses.distill_step(h, w, ids, logits, temperature=2.0, labels=y, alpha=0.3)
+    f = losses.distill_forward(h, w, ids, logits, temperature=2.0, labels=y, alpha=0.3)
+    b = losses.distill_backward(h, w, ids, logits, f.lse, f.lse_tau, temperature=2.0, labels=y, alpha=0.3)
+    assert torch.equal(a.loss, f.loss)
+    assert torch.equal(a.dhidden, b.dhidden) and torch.equal(a.dweight, b.dweight)
+    # one gradient alone, and equal inputs give equal bits
+    only = losses.xent_step(h, w, y, dloss=dloss, grad_scale=0.5, dweight=False)
+    again = losses.xent_step(h, w, y, dloss=dloss, grad_scale=0.5, dhidden=False)
+    both = losses.xent_step(h, w, y, dloss=dloss, grad_scale=0.5)
+    assert only.dweight is None and again.dhidden is None
+    assert torch.equal(only.dhidden, both.dhidden) and torch.equal(again.dweight, both.dweight)
+
+
+@pytest.mark.parametrize("kind", TYPES)
+def test_accumulate_adds_with_one_rounding(losses, cuda, kind):
+    dt = TYPES[kind]
+    T, V, D = 100, 530, 72
+    h, w, y, g = inputs(T, V, D, dt, 31, cuda)
+    r = reference(h, w, y)
+    before = (torch.randn(V, D, generator=g) * 1e-2).to(dt).to(cuda)
+    dw = before.clone()
+    losses.xent_step(h, w, y, dweight=dw, accumulate=True)
+    want = before.double() + r["dweight"]
+    unit = 2.0 ** -24 if dt == torch.float32 else 2.0 ** -8
+    allowed = bounds(r, dt)["dweight"] + unit * 1.01 * want.abs()
+    assert bool(((dw.double() - want).abs() <= allowed).all())
+
+
+def test_another_stream(losses, cuda):
+    """Inputs made and outputs used on a side stream, named or current."""
+    side = torch.cuda.Stream()
+    T, V, D = 300, 3000, 128
+    h, w, y, _ = inputs(T, V, D, torch.bfloat16, 4, cuda)
+    r = reference(h, w, y)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        x = h * 1.0
+        got = losses.xent_step(x, w, y)
+    side.synchronize()
+    check(got, r, torch.bfloat16)
+    side.wait_stream(torch.cuda.current_stream())
+    got = losses.xent_step(h, w, y, stream=side)
+    side.synchronize()
+    check(got, r, torch.bfloat16)
+
+
+@pytest.mark.parametrize("kind", TYPES)
+def test_gradient_against_differences(losses, cuda, kind):
+    """The losses' own central difference along a direction, against the
+    gradient along it. What the difference itself is off by comes from the
+    definition in 64 bits; what is left is the losses' error over the step."""
+    dt = torch.float32
+    T, V, D = 40, 600, 48
+    h, w, y, g = inputs(T, V, D, dt, 17, cuda)
+    ids, logits = teacher(T, V, 9, g, cuda, 0.2)
+    u = torch.randn(T, D, generator=g).to(cuda)
+    x = (torch.randn(V, D, generator=g) / math.sqrt(D)).to(cuda)
+    eps = 2.0 ** -5
+    if kind == "bf16":     # the same with the gradient taken in the mixed mode
+        h, w = h.bfloat16().float(), w.bfloat16().float()
+    for own, args in [("xent", (y,)), ("distill", (ids, logits))]:
+        more = {} if own == "xent" else dict(tau=2.0, alpha=0.6, ids=ids, logits=logits)
+        call = {} if own == "xent" else dict(temperature=2.0, alpha=0.6, labels=y)
+        fwd = getattr(losses, own + "_forward")
+        step = getattr(losses, own + "_step")
+        store = TYPES[kind]
+        got = step(h.to(store), w.to(store), *args, reduction="sum", **call)
+        for dh, dw in [(u, torch.zeros_like(w)), (torch.zeros_like(h), x)]:
+            ends, exact, allowed = [], [], 0.0
+            for sign in (1, -1):
+                a, b = h + sign * eps * dh, w + sign * eps * dw
+                ends.append(float(fwd(a, b, *args, reduction="sum", **call).loss.double().sum()))
+                r = reference(a, b, y, reduction="sum", **more)
+                exact.append(float(r["loss"].sum()))
+                allowed += float(bounds(r, dt)["loss"].sum())
+            r = reference(h, w, y, reduction="sum", **more)
+            along = float((r["dhidden"] * dh.double()).sum() + (r["dweight"] * dw.double()).sum())
+            b = bounds(r, store)
+            allowed = allowed / (2 * eps) + float((b["dhidden"] * dh.abs()).sum() + (b["dweight"] * dw.abs()).sum())
+            curve = (exact[0] - exact[1]) / (2 * eps) - along
+            mine = float((got.dhidden.double() * dh).sum() + (got.dweight.double() * dw).sum())
+            assert abs((ends[0] - ends[1]) / (2 * eps) - curve - mine) <= allowed, own
+
+
+def test_autograd(losses, cuda):
+    T, V, D = 60, 500, 64
+    h, w, y, g = inputs(T, V, D, torch.float32, 41, cuda, masked=0.2)
+    ids, logits = teacher(T, V, 6, g, cuda)
+    scale = 0.3
+    a, b = h.clone().requires_grad_(), w.clone().requires_grad_()
+    (scale * losses.linear_cross_entropy(a.view(4, 15, D), b, y)).backward()
+    r = reference(h, w, y, dloss=scale)
+    lim = bounds(r, torch.float32)
+    assert bool(((a.grad.double() - r["dhidden"]).abs() <= lim["dhidden"]).all())
+    assert bool(((b.grad.double() - r["dweight"]).abs() <= lim["dweight"]).all())
+    a, b = h.clone().requires_grad_(), w.clone()
+    per_row = losses.linear_distillation(a, b, ids, logits, 2.0, y, 0.5, reduction="none")
+    rows = torch.rand(T, generator=g).to(cuda)
+    (per_row * rows).sum().backward()
+    r = reference(h, w, y, ids, logits, tau=2.0, alpha=0.5, reduction="none", dloss=rows)
+    assert bool(((a.grad.double() - r["dhidden"]).abs() <= bounds(r, torch.float32)["dhidden"]).all())
+
+
+@pytest.mark.parametrize("kind,T,V,D", [("bf16", 8200, 21000, 64), ("fp32", 4100, 13000, 64)])
+def test_several_pieces_of_the_vocabulary(losses, cuda, kind, T, V, D):
+    """Enough rows that the gradient of the logits is formed in several pieces."""
+    dt = TYPES[kind]
+    h, w, y, g = inputs(T, V, D, dt, 51, cuda, masked=0.1)
+    r = reference(h, w, y)
+    got = losses.xent_step(h, w, y)
+    check(got, r, dt)
+
+
+def test_offsets_beyond_32_bits(losses, cuda):
+    """A weight whose last rows lie more than 2^32 bytes from its first."""
+    V, D, stride = 600, 64, 4_000_000
+    buf = torch.empty((V - 1) * stride + D, dtype=torch.bfloat16, device=cuda)
+    w = torch.as_strided(buf, (V, D), (stride, 1))
+    h, values, y, _ = inputs(50, V, D, torch.bfloat16, 6, cuda)
+    w.copy_(values)
+    dbuf = torch.empty((V - 1) * stride + D, dtype=torch.bfloat16, device=cuda)
+    dw = torch.as_strided(dbuf, (V, D), (stride, 1))
+    got = losses.xent_step(h, w, y, dweight=dw)
+    check(got, reference(h, values, y), torch.bfloat16)
+
+
+def test_refusals_of_the_binding(losses, cuda):
+    h, w, y, _ = inputs(10, 50, 16, torch.bfloat16, 1, cuda)
+    with pytest.raises(TypeError):
+        losses.xent_forward(h.half(), w.half(), y)
+    with pytest.raises(TypeError):
+        losses.xent_forward(h, w.float(), y)
+    with pytest.raises(TypeError):
+        losses.xent_forward(h, w, y.int())
+    with pytest.raises(TypeError):
+        losses.xent_forward(h.cpu(), w, y)
+    with pytest.raises(ValueError):
+        losses.xent_forward(h, w[:, :8], y)
+    with pytest.raises(ValueError):
+        losses.xent_forward(h.t().contiguous().t(), w, y)
+    with pytest.raises(ValueError):
+        losses.xent_forward(h, w, y[:5])
+    with pytest.raises(ValueError):
+        losses.xent_forward(h, w, y, reduction="average")
+    with pytest.raises(ValueError):
+        losses.xent_step(h, w, y, accumulate=True)
+    with pytest.raises(ValueError):
+        losses.distill_forward(h, w, y.view(10, 1), torch.zeros(10, 2, device=cuda))
+    from zero_sharded_optimizer_gb300 import abi
+    for bad in (dict(dhidden=h), dict(dweight=w)):                 # an output over an input
+        with pytest.raises(abi.ZeroError) as e:
+            losses.xent_step(h, w, y, **bad)
+        assert e.value.code == abi.ZERO_EINVAL and "overlap" in str(e.value)
+    wide = torch.zeros(10, 32, dtype=torch.bfloat16, device=cuda)  # column blocks of one buffer
+    wide[:, :16] = h
+    got = losses.xent_step(wide[:, :16], w, y, dhidden=wide[:, 16:])
+    check(got, reference(h, w, y), torch.bfloat16)

@@ -9,7 +9,7 @@ the C-ABI library ``libzero_gb300.so`` (declared in ``include/zero_gb300.h``).
 raises at import when the library has not been built.
 """
 
-__all__ = ["abi", "inputs", "optimizer"]
+__all__ = ["abi", "inputs", "losses", "optimizer"]
 
 
 def __getattr__(name):

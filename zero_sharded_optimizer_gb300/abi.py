@@ -40,6 +40,11 @@ ZERO_ETIMEDOUT = -4
 ZERO_ENOMEM = -5
 ZERO_MAX_RANKS = 64
 
+ZERO_REDUCE_NONE = 0
+ZERO_REDUCE_MEAN = 1
+ZERO_REDUCE_SUM = 2
+ZERO_DISTILL_MAX_K = 1024
+
 _i64 = ctypes.c_int64
 _i32 = ctypes.c_int32
 _u64 = ctypes.c_uint64
@@ -89,6 +94,14 @@ _SIGNATURES = {
     "zero_gather": (ctypes.c_int, [_P(_vp), _vp, _i64, _i64, _vp]),
     "zero_step_sgd": (ctypes.c_int, [_P(_vp), _P(_vp), _vp, _vp, _vp]),
     "zero_grad_norm_sq_noalloc": (ctypes.c_int, [_P(_vp), _i64, _i32, _i32, _vp, _vp]),
+    "zero_xent_workspace_bytes": (ctypes.c_int, [_vp, _P(_i64)]),
+    "zero_xent_forward": (ctypes.c_int, [_vp, _vp]),
+    "zero_xent_backward": (ctypes.c_int, [_vp, _vp]),
+    "zero_xent_step": (ctypes.c_int, [_vp, _vp]),
+    "zero_distill_workspace_bytes": (ctypes.c_int, [_vp, _P(_i64)]),
+    "zero_distill_forward": (ctypes.c_int, [_vp, _vp]),
+    "zero_distill_backward": (ctypes.c_int, [_vp, _vp]),
+    "zero_distill_step": (ctypes.c_int, [_vp, _vp]),
     "zero_strerror": (ctypes.c_char_p, [ctypes.c_int]),
     "zero_last_error": (ctypes.c_char_p, []),
 }
@@ -558,6 +571,58 @@ class DdpHost:
             self.close()
         except Exception:
             pass
+
+
+# ------------------------------------------------------ vocabulary losses --
+
+class HeadLoss(ctypes.Structure):
+    """zero_head_loss_t."""
+    _fields_ = [("T", _i64), ("V", _i64), ("D", _i64), ("precision", _i32), ("reduction", _i32),
+                ("hidden", _vp), ("hidden_stride", _i64), ("weight", _vp), ("weight_stride", _i64),
+                ("labels", _vp), ("ignore_index", _i64), ("teacher_ids", _vp),
+                ("teacher_logits", _vp), ("teacher_k", _i64), ("temperature", _dbl),
+                ("alpha", _dbl), ("loss", _vp), ("lse", _vp), ("lse_tau", _vp), ("reduced", _vp),
+                ("dloss", _vp), ("grad_scale", _dbl), ("dhidden", _vp), ("dhidden_stride", _i64),
+                ("dweight", _vp), ("dweight_stride", _i64), ("accumulate", _i32),
+                ("workspace", _vp), ("workspace_bytes", _i64)]
+
+
+def zero_xent_workspace_bytes(p: HeadLoss) -> int:
+    out = _i64()
+    _check(_lib.zero_xent_workspace_bytes(ctypes.byref(p), ctypes.byref(out)),
+           "zero_xent_workspace_bytes")
+    return out.value
+
+
+def zero_distill_workspace_bytes(p: HeadLoss) -> int:
+    out = _i64()
+    _check(_lib.zero_distill_workspace_bytes(ctypes.byref(p), ctypes.byref(out)),
+           "zero_distill_workspace_bytes")
+    return out.value
+
+
+def zero_xent_forward(p: HeadLoss, stream=None):
+    _check(_lib.zero_xent_forward(ctypes.byref(p), _stream(stream)), "zero_xent_forward")
+
+
+def zero_xent_backward(p: HeadLoss, stream=None):
+    _check(_lib.zero_xent_backward(ctypes.byref(p), _stream(stream)), "zero_xent_backward")
+
+
+def zero_xent_step(p: HeadLoss, stream=None):
+    _check(_lib.zero_xent_step(ctypes.byref(p), _stream(stream)), "zero_xent_step")
+
+
+def zero_distill_forward(p: HeadLoss, stream=None):
+    _check(_lib.zero_distill_forward(ctypes.byref(p), _stream(stream)), "zero_distill_forward")
+
+
+def zero_distill_backward(p: HeadLoss, stream=None):
+    _check(_lib.zero_distill_backward(ctypes.byref(p), _stream(stream)), "zero_distill_backward")
+
+
+def zero_distill_step(p: HeadLoss, stream=None):
+    _check(_lib.zero_distill_step(ctypes.byref(p), _stream(stream)), "zero_distill_step")
 
 
 def zero_last_error() -> str:

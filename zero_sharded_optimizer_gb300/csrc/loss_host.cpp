@@ -1,0 +1,329 @@
+// Host side of the vocabulary losses: argument checks, the workspace's layout
+// and the order of the launches. Device work is in loss_kernels.cu.
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "loss_internal.h"
+
+namespace {
+
+using zl::Args;
+using zl::set_error;
+
+constexpr int64_t kMostSize = 0x7fffffff - 1024;  // T, V and D: 32-bit tile coordinates
+// A piece of the logits' gradient is at most this many bytes (one tile's width
+// of columns at least).
+constexpr int64_t kPieceBytes = int64_t(128) << 20;
+
+int64_t round_up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
+
+int elem_size(int32_t precision) { return precision == ZERO_FP32 ? 4 : 2; }
+
+enum Pass { kForward = 1, kBackward = 2 };
+
+// A buffer the call touches: `rows` rows of `bytes` bytes, `stride` bytes apart.
+struct Span {
+  const void* p;
+  int64_t rows, bytes, stride;
+  const char* what;
+  bool written;
+};
+
+// Whether two buffers share a byte. Rows of equal stride are compared by their
+// phase, so that column blocks of one wider buffer pass.
+bool overlap(const Span& x, const Span& y) {
+  if (!x.p || !y.p || !x.rows || !y.rows) return false;
+  const uintptr_t a = reinterpret_cast<uintptr_t>(x.p), b = reinterpret_cast<uintptr_t>(y.p);
+  const uintptr_t a1 = a + uintptr_t((x.rows - 1) * x.stride + x.bytes);
+  const uintptr_t b1 = b + uintptr_t((y.rows - 1) * y.stride + y.bytes);
+  if (a1 <= b || b1 <= a) return false;
+  if (x.stride == y.stride && x.rows > 1 && y.rows > 1) {
+    const uintptr_t s = uintptr_t(x.stride);
+    const uintptr_t d = b >= a ? (b - a) % s : (s - (a - b) % s) % s;
+    if (d >= uintptr_t(x.bytes) && s - d >= uintptr_t(y.bytes)) return false;
+  }
+  return true;
+}
+
+int check_sizes(const zero_head_loss_t* p, bool distill) {
+  if (!p) return set_error(ZERO_EINVAL, "the problem is NULL");
+  if (p->T < 0 || p->T > kMostSize) return set_error(ZERO_EINVAL, "T=%lld is out of range", (long long)p->T);
+  if (p->V < 1 || p->V > kMostSize) return set_error(ZERO_EINVAL, "V=%lld is out of range", (long long)p->V);
+  if (p->D < 1 || p->D > kMostSize) return set_error(ZERO_EINVAL, "D=%lld is out of range", (long long)p->D);
+  if (p->precision != ZERO_FP32 && p->precision != ZERO_BF16_MIXED)
+    return set_error(ZERO_EINVAL, "precision %d is neither ZERO_FP32 nor ZERO_BF16_MIXED", p->precision);
+  if (p->reduction != ZERO_REDUCE_NONE && p->reduction != ZERO_REDUCE_MEAN &&
+      p->reduction != ZERO_REDUCE_SUM)
+    return set_error(ZERO_EINVAL, "unknown reduction %d", p->reduction);
+  const int64_t most = INT64_MAX / 8;
+  struct { int64_t stride, rows; const char* what; bool used; } strides[] = {
+      {p->hidden_stride, p->T, "hidden_stride", true},
+      {p->weight_stride, p->V, "weight_stride", true},
+      {p->dhidden_stride, p->T, "dhidden_stride", p->dhidden != nullptr},
+      {p->dweight_stride, p->V, "dweight_stride", p->dweight != nullptr}};
+  for (const auto& s : strides) {
+    if (!s.used) continue;
+    if (s.stride < p->D)
+      return set_error(ZERO_EINVAL, "%s=%lld is below D=%lld", s.what, (long long)s.stride, (long long)p->D);
+    if (s.rows > 1 && s.stride > most / s.rows)
+      return set_error(ZERO_EINVAL, "%s=%lld is out of range", s.what, (long long)s.stride);
+  }
+  if (distill) {
+    if (p->teacher_k < 1 || p->teacher_k > ZERO_DISTILL_MAX_K)
+      return set_error(ZERO_EINVAL, "teacher_k=%lld is not in [1, %d]", (long long)p->teacher_k, ZERO_DISTILL_MAX_K);
+    if (!std::isfinite(p->temperature) || !(p->temperature > 0.0) ||
+        !std::isfinite(float(p->temperature)) || !(float(p->temperature) > 0.0f) ||
+        !std::isfinite(float(1.0 / p->temperature)))
+      return set_error(ZERO_EINVAL, "temperature must be finite and > 0");
+    if (!(p->alpha >= 0.0 && p->alpha <= 1.0)) return set_error(ZERO_EINVAL, "alpha must lie in [0, 1]");
+    if (!p->labels && p->alpha != 1.0)
+      return set_error(ZERO_EINVAL, "without labels alpha must be 1");
+  } else if (p->teacher_ids || p->teacher_logits || p->teacher_k || p->lse_tau) {
+    return set_error(ZERO_EINVAL, "teacher fields are set: use the zero_distill calls");
+  }
+  return ZERO_OK;
+}
+
+int check_pointer(const void* ptr, int64_t count, size_t align, const char* what) {
+  if (!ptr && count > 0) return set_error(ZERO_EINVAL, "%s is NULL", what);
+  if (reinterpret_cast<uintptr_t>(ptr) % align)
+    return set_error(ZERO_EALIGN, "%s is not aligned to %zu bytes", what, align);
+  return ZERO_OK;
+}
+
+int check_buffers(const zero_head_loss_t* p, bool distill, int pass) {
+  const int es = elem_size(p->precision);
+  const int64_t T = p->T, V = p->V, D = p->D;
+  int e;
+  if ((e = check_pointer(p->hidden, T, es, "hidden"))) return e;
+  if ((e = check_pointer(p->weight, V, es, "weight"))) return e;
+  if ((e = check_pointer(p->labels, distill ? 0 : T, 8, "labels"))) return e;
+  const bool ce = !distill || p->labels;
+  if (distill) {
+    if ((e = check_pointer(p->teacher_ids, T, 8, "teacher_ids"))) return e;
+    if ((e = check_pointer(p->teacher_logits, T, 4, "teacher_logits"))) return e;
+    if ((e = check_pointer(p->lse_tau, T, 4, "lse_tau"))) return e;
+  }
+  if ((e = check_pointer(p->lse, ce ? T : 0, 4, "lse"))) return e;
+  const bool reduce = p->reduction != ZERO_REDUCE_NONE;
+  if (pass & kForward) {
+    if ((e = check_pointer(p->loss, T, 4, "loss"))) return e;
+    if (reduce && (e = check_pointer(p->reduced, 1, 4, "reduced"))) return e;
+  }
+  if (pass & kBackward) {
+    if (!p->dhidden && !p->dweight) return set_error(ZERO_EINVAL, "neither dhidden nor dweight is given");
+    if ((e = check_pointer(p->dhidden, 0, es, "dhidden"))) return e;
+    if ((e = check_pointer(p->dweight, 0, es, "dweight"))) return e;
+    if ((e = check_pointer(p->dloss, 0, 4, "dloss"))) return e;
+    if (!std::isfinite(p->grad_scale)) return set_error(ZERO_EINVAL, "grad_scale must be finite");
+  }
+  const bool fwd = pass & kForward, bwd = pass & kBackward;
+  const Span spans[] = {
+      {p->hidden, T, D * es, p->hidden_stride * es, "hidden", false},
+      {p->weight, V, D * es, p->weight_stride * es, "weight", false},
+      {p->labels, 1, 8 * T, 8 * T, "labels", false},
+      {distill ? p->teacher_ids : nullptr, 1, 8 * T * p->teacher_k, 8 * T * p->teacher_k, "teacher_ids", false},
+      {distill ? p->teacher_logits : nullptr, 1, 4 * T * p->teacher_k, 4 * T * p->teacher_k, "teacher_logits", false},
+      {fwd ? p->loss : nullptr, 1, 4 * T, 4 * T, "loss", true},
+      {ce ? p->lse : nullptr, 1, 4 * T, 4 * T, "lse", fwd},
+      {distill ? p->lse_tau : nullptr, 1, 4 * T, 4 * T, "lse_tau", fwd},
+      {fwd && reduce ? p->reduced : nullptr, 1, 4, 4, "reduced", true},
+      {bwd ? p->dloss : nullptr, 1, reduce ? 4 : 4 * T, reduce ? 4 : 4 * T, "dloss", false},
+      {bwd ? p->dhidden : nullptr, T, D * es, p->dhidden_stride * es, "dhidden", true},
+      {bwd ? p->dweight : nullptr, V, D * es, p->dweight_stride * es, "dweight", true},
+      {p->workspace, 1, p->workspace_bytes, p->workspace_bytes, "workspace", true}};
+  const int n = int(sizeof(spans) / sizeof(spans[0]));
+  for (int i = 0; i < n; ++i)
+    for (int j = 0; j < i; ++j)
+      if ((spans[i].written || spans[j].written) && overlap(spans[i], spans[j]))
+        return set_error(ZERO_EINVAL, "buffers overlap (%s and %s)", spans[j].what, spans[i].what);
+  return ZERO_OK;
+}
+
+// Places the call's arrays in the workspace (base NULL: only counts bytes).
+// Returns false when the size overflows.
+struct Layout {
+  uint8_t* base;
+  int64_t at = 0;
+  bool fits = true;
+  template <typename T>
+  T* take(int64_t count, int64_t times = 1) {
+    const int64_t size = int64_t(sizeof(T));
+    if (!fits || (times && count > (INT64_MAX / 4) / times / size)) {
+      fits = false;
+      return nullptr;
+    }
+    T* p = reinterpret_cast<T*>(base + at);
+    at = round_up(at + count * times * size, 256);
+    if (at > INT64_MAX / 4) fits = false;
+    return p;
+  }
+};
+
+// The weight can be read in place by 16-byte copies of whole rows.
+bool weight_in_place(const zero_head_loss_t* p) {
+  return p->precision == ZERO_BF16_MIXED && reinterpret_cast<uintptr_t>(p->weight) % 16 == 0 &&
+         p->weight_stride % 8 == 0;
+}
+
+int plan(const zero_head_loss_t* p, bool distill, int pass, Args* a, __nv_bfloat16** packed_weight,
+         int64_t* bytes) {
+  *a = Args{};
+  a->T = p->T;
+  a->V = p->V;
+  a->D = p->D;
+  a->Tp = std::max<int64_t>(round_up(p->T, zl::kTileM), zl::kTileM);
+  a->Dp = round_up(p->D, zl::kPadD);
+  a->planes = p->precision == ZERO_FP32 ? 3 : 1;
+  a->has_ce = p->labels != nullptr || !distill;
+  a->has_kd = distill;
+  a->K = distill ? int32_t(p->teacher_k) : 0;
+  a->L = a->K + (a->has_ce ? 1 : 0);
+  a->tau = distill ? p->temperature : 1.0;
+  a->inv_tau = float(1.0 / a->tau);
+  a->ce = distill ? float(1.0 - p->alpha) : 1.0f;
+  a->kd = distill ? float(p->alpha * p->temperature) : 0.0f;
+  a->reduction = p->reduction;
+  a->ignore_index = p->ignore_index;
+  a->grad_scale = p->grad_scale;
+  a->accumulate = p->accumulate != 0;
+  a->forward = (pass & kForward) != 0;
+  a->hidden = p->hidden;
+  a->hidden_stride = p->hidden_stride;
+  a->weight = p->weight;
+  a->weight_stride = p->weight_stride;
+  a->labels = p->labels;
+  a->teacher_ids = p->teacher_ids;
+  a->teacher_logits = p->teacher_logits;
+  a->loss = p->loss;
+  a->lse = p->lse;
+  a->lse_tau = p->lse_tau;
+  a->reduced = p->reduced;
+  a->dloss = p->dloss;
+  a->dhidden = p->dhidden;
+  a->dhidden_stride = p->dhidden_stride;
+  a->dweight = p->dweight;
+  a->dweight_stride = p->dweight_stride;
+  a->tiles = (p->V + zl::kTileN - 1) / zl::kTileN;
+
+  Layout w{static_cast<uint8_t*>(p->workspace)};
+  a->head = w.take<zl::Head>(1);
+  a->rowpos = w.take<int32_t>(a->T);
+  a->rowmap = w.take<int32_t>(a->Tp);
+  a->coef = w.take<float2>(a->T);
+  a->konst = w.take<float>(a->T);
+  a->ids = w.take<int32_t>(a->T, a->L);
+  a->weights = w.take<float>(a->T, a->L);
+  a->hp = w.take<__nv_bfloat16>(a->Tp * a->planes, a->Dp);
+  if (weight_in_place(p)) {
+    *packed_weight = nullptr;
+    a->wp = static_cast<const __nv_bfloat16*>(p->weight);
+    a->wp_ld = p->weight_stride;
+    a->wp_plane = 0;
+  } else {
+    *packed_weight = w.take<__nv_bfloat16>(a->V * a->planes, a->Dp);
+    a->wp = *packed_weight;
+    a->wp_ld = a->Dp;
+    a->wp_plane = a->V * a->Dp;
+  }
+  // The forward pass's arrays and the backward pass's lie over one another.
+  const int64_t common = w.at;
+  a->zent = w.take<float>(a->T, a->L);
+  if (a->has_ce) a->stats = w.take<float2>(a->tiles, a->Tp);
+  if (a->has_kd) a->stats_tau = w.take<float2>(a->tiles, a->Tp);
+  int64_t most = w.at;
+  if (pass & kBackward) {
+    w.at = common;
+    const int64_t widest = std::max<int64_t>(
+        kPieceBytes / (2 * a->planes * a->Tp) / zl::kTileN * zl::kTileN, zl::kTileN);
+    const int64_t pieces = (a->V + widest - 1) / widest;
+    a->piece = round_up((a->V + pieces - 1) / pieces, zl::kTileN);
+    a->g = w.take<__nv_bfloat16>(a->Tp * a->planes, a->piece);
+    if (p->dhidden) a->dh = w.take<float>(a->Tp, a->Dp);
+    most = std::max(most, w.at);
+  }
+  if (!w.fits) return set_error(ZERO_EINVAL, "the problem's workspace overflows 64 bits");
+  *bytes = most;
+  return ZERO_OK;
+}
+
+int workspace_bytes(const zero_head_loss_t* p, bool distill, int64_t* bytes) {
+  if (!bytes) return set_error(ZERO_EINVAL, "bytes is NULL");
+  if (int e = check_sizes(p, distill)) return e;
+  Args a;
+  __nv_bfloat16* packed;
+  zero_head_loss_t q = *p;
+  q.workspace = nullptr;
+  return plan(&q, distill, kForward | (p->dhidden || p->dweight ? kBackward : 0), &a, &packed, bytes);
+}
+
+int run(const zero_head_loss_t* p, bool distill, int pass, cudaStream_t s) {
+  if (int e = check_sizes(p, distill)) return e;
+  if (int e = check_buffers(p, distill, pass)) return e;
+  if (reinterpret_cast<uintptr_t>(p->workspace) % 256)
+    return set_error(ZERO_EALIGN, "the workspace is not aligned to 256 bytes");
+  Args a;
+  __nv_bfloat16* packed;
+  int64_t bytes = 0;
+  if (int e = plan(p, distill, pass, &a, &packed, &bytes)) return e;
+  if (!p->workspace || p->workspace_bytes < bytes)
+    return set_error(ZERO_EINVAL, "the workspace has %lld bytes, %lld are needed",
+                     (long long)(p->workspace ? p->workspace_bytes : 0), (long long)bytes);
+  const char* what = "rows";
+  cudaError_t e = zl::launch_rows(a, s);
+  auto next = [&](const char* name, auto&& launch) {
+    if (e != cudaSuccess) return;
+    what = name;
+    e = launch();
+  };
+  next("packing hidden", [&] { return zl::launch_pack_hidden(a, s); });
+  if (packed) next("packing weight", [&] { return zl::launch_pack_weight(a, packed, s); });
+  if (pass & kForward) {
+    next("logits", [&] { return zl::launch_logits_forward(a, s); });
+    next("losses", [&] { return zl::launch_losses(a, s); });
+  }
+  if (pass & kBackward) {
+    for (int64_t c0 = 0; c0 < a.V; c0 += a.piece) {
+      next("logits' gradient", [&] { return zl::launch_logits_backward(a, c0, s); });
+      if (p->dhidden) next("dhidden", [&] { return zl::launch_dhidden(a, c0, s); });
+      if (p->dweight) next("dweight", [&] { return zl::launch_dweight(a, c0, s); });
+    }
+    if (p->dhidden && p->T) next("dhidden", [&] { return zl::launch_dhidden_out(a, s); });
+  }
+  if (e != cudaSuccess)
+    return set_error(ZERO_ECUDA, "%s: %s (%s)", what, cudaGetErrorString(e), cudaGetErrorName(e));
+  return ZERO_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int zero_xent_workspace_bytes(const zero_head_loss_t* p, int64_t* bytes) {
+  return workspace_bytes(p, false, bytes);
+}
+int zero_distill_workspace_bytes(const zero_head_loss_t* p, int64_t* bytes) {
+  return workspace_bytes(p, true, bytes);
+}
+int zero_xent_forward(const zero_head_loss_t* p, zero_stream_t stream) {
+  return run(p, false, kForward, stream);
+}
+int zero_xent_backward(const zero_head_loss_t* p, zero_stream_t stream) {
+  return run(p, false, kBackward, stream);
+}
+int zero_xent_step(const zero_head_loss_t* p, zero_stream_t stream) {
+  return run(p, false, kForward | kBackward, stream);
+}
+int zero_distill_forward(const zero_head_loss_t* p, zero_stream_t stream) {
+  return run(p, true, kForward, stream);
+}
+int zero_distill_backward(const zero_head_loss_t* p, zero_stream_t stream) {
+  return run(p, true, kBackward, stream);
+}
+int zero_distill_step(const zero_head_loss_t* p, zero_stream_t stream) {
+  return run(p, true, kForward | kBackward, stream);
+}
+
+}  // extern "C"

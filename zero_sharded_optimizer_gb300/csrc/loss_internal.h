@@ -1,0 +1,97 @@
+// Internal interface between the host side of the vocabulary losses
+// (loss_host.cpp) and their kernels (loss_kernels.cu). Not part of the public
+// C ABI.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "zero_gb300.h"
+
+namespace zl {
+
+// Sets the calling thread's error message and returns `code` (zero_host.cpp).
+int set_error(int code, const char* fmt, ...);
+
+// Tile of the logits: rows (tokens) by columns (vocabulary).
+constexpr int kTileM = 128;
+constexpr int kTileN = 256;
+constexpr int kPadD = 64;       // packed operands are padded to this width
+constexpr int32_t kNoId = 0x7fffffff;
+
+// Device-side scalars of a call, at the start of the workspace.
+struct Head {
+  int32_t rows;    // rows with a target (the compact rows)
+  int32_t ticket;  // blocks of the reduction that are done
+};
+
+// Everything the kernels read or write. Rows with a target are packed densely:
+// compact row i stands for row rowmap[i], and the matrix kernels see only
+// compact rows, head->rows of them. Per-row arrays of T entries are indexed
+// by the row, those of Tp entries by the compact row.
+struct Args {
+  int64_t T, V, D;
+  int64_t Tp, Dp;         // T and D padded to the tiles
+  int32_t planes;         // bf16 parts of a value: 1, or 3 for fp32 storage
+  int32_t L;              // sparse entries per row
+  int32_t K;              // teacher entries per row
+  int32_t has_ce, has_kd;
+  float ce, kd;           // weights of the two terms' gradients: 1 - alpha, alpha * tau
+  float inv_tau;
+  double tau;
+  int32_t reduction;
+  int64_t ignore_index;
+  double grad_scale;
+  int32_t accumulate;
+  int32_t forward;        // the call writes losses
+
+  const void* hidden;
+  int64_t hidden_stride;
+  const void* weight;
+  int64_t weight_stride;
+  const int64_t* labels;
+  const int64_t* teacher_ids;
+  const float* teacher_logits;
+  float* loss;
+  float* lse;
+  float* lse_tau;
+  float* reduced;
+  const float* dloss;
+  void* dhidden;
+  int64_t dhidden_stride;
+  void* dweight;
+  int64_t dweight_stride;
+
+  // workspace
+  Head* head;
+  int32_t* rowpos;        // [T] the row's compact row, -1 for an empty row
+  int32_t* rowmap;        // [Tp] the compact row's row
+  float2* coef;           // [T] (ce or 0, kd or 0)
+  float* konst;           // [T] the loss's part that no logit enters
+  int32_t* ids;           // [T][L] ascending, kNoId after the last
+  float* weights;         // [T][L] weight of each entry's logit in loss and gradient
+  float* zent;            // [T][L] logits of the entries
+  __nv_bfloat16* hp;      // [planes][Tp][Dp] packed hidden states
+  const __nv_bfloat16* wp;  // [planes][V][Dp], or the caller's weight (then wp_ld)
+  int64_t wp_ld, wp_plane;
+  int64_t tiles;          // vocabulary tiles
+  float2* stats;          // [tiles][Tp] (max, sum of exp) of z
+  float2* stats_tau;      // [tiles][Tp] of z / tau
+  __nv_bfloat16* g;       // [planes][Tp][piece] gradient of a piece's logits
+  int64_t piece;          // columns of a piece, a multiple of kTileN
+  float* dh;              // [Tp][Dp] running sum of dhidden over the pieces
+};
+
+cudaError_t launch_rows(const Args& a, cudaStream_t s);
+cudaError_t launch_pack_hidden(const Args& a, cudaStream_t s);
+cudaError_t launch_pack_weight(const Args& a, __nv_bfloat16* to, cudaStream_t s);
+cudaError_t launch_logits_forward(const Args& a, cudaStream_t s);
+cudaError_t launch_losses(const Args& a, cudaStream_t s);
+// The piece [c0, min(c0 + piece, V)): its logits' gradient, and the products with it.
+cudaError_t launch_logits_backward(const Args& a, int64_t c0, cudaStream_t s);
+cudaError_t launch_dhidden(const Args& a, int64_t c0, cudaStream_t s);
+cudaError_t launch_dweight(const Args& a, int64_t c0, cudaStream_t s);
+cudaError_t launch_dhidden_out(const Args& a, cudaStream_t s);
+
+}  // namespace zl

@@ -1,0 +1,544 @@
+// Kernels of the vocabulary losses (zero_xent_*, zero_distill_*).
+#include <math.h>
+
+#include "loss_internal.h"
+
+namespace zl {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ float warp_max(float x) {
+  for (int o = 16; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(~0u, x, o));
+  return x;
+}
+__device__ __forceinline__ float warp_sum(float x) {
+  for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
+  return x;
+}
+
+// The factor of both gradients that does not depend on the row: grad_scale,
+// the mean's count, and the reduced loss's own gradient.
+__device__ __forceinline__ float grad_factor(const Args& a) {
+  double f = a.grad_scale;
+  if (a.reduction == ZERO_REDUCE_MEAN) f /= double(max(1, a.head->rows));
+  if (a.reduction != ZERO_REDUCE_NONE && a.dloss) f *= double(*a.dloss);
+  return float(f);
+}
+
+// ------------------------------------------------------------------- rows --
+
+// One warp per row: its terms, and its sparse entries -- the ids whose logits
+// enter the loss one by one -- with the weights c in
+//   loss = ce*lse + kd*tau*lse' + konst - sum_e c_e z_e,
+//   dloss/dz_v = ce*p_v + kd*p'_v - sum_{e: id_e = v} c_e
+// (c = ce for the label, kd*q for a teacher entry; kd = alpha*tau). Equal ids
+// are merged, in entry order, and the ids are sorted so that a tile's entries
+// are found by bisection.
+__global__ void rows_kernel(const Args a) {
+  extern __shared__ int32_t sh[];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t t = int64_t(blockIdx.x) * (blockDim.x >> 5) + warp;
+  if (t >= a.T) return;
+  const int K = a.K;
+  int64_t y = a.has_ce ? a.labels[t] : -1;
+  const bool has_y = a.has_ce && y != a.ignore_index && y >= 0 && y < a.V;
+  int32_t* ids = a.ids + t * a.L;
+  float* weights = a.weights + t * a.L;
+  bool has_kd = false;
+  if (K == 0) {
+    if (lane == 0) {
+      ids[0] = has_y ? int32_t(y) : kNoId;
+      weights[0] = a.ce;
+      a.konst[t] = 0.0f;
+    }
+  } else {
+    int32_t* id = sh + warp * 4 * (K + 1);
+    float* c = reinterpret_cast<float*>(id + (K + 1));
+    int32_t* id2 = id + 2 * (K + 1);
+    float* c2 = reinterpret_cast<float*>(id + 3 * (K + 1));
+    float top = -INFINITY;
+    for (int k = lane; k < K; k += 32) {
+      const int64_t v = a.teacher_ids[t * K + k];
+      const float u = a.teacher_logits[t * K + k] / float(a.tau);
+      const bool there = v >= 0 && v < a.V && u != -INFINITY;
+      id[k] = there ? int32_t(v) : kNoId;
+      c[k] = u;
+      if (there) {
+        has_kd = true;
+        top = fmaxf(top, u);
+      }
+    }
+    has_kd = __any_sync(~0u, has_kd);
+    top = warp_max(top);
+    float sum = 0.0f;
+    for (int k = lane; k < K; k += 32) {
+      const float e = id[k] == kNoId ? 0.0f : expf(c[k] - top);
+      c[k] = e;
+      sum += e;
+    }
+    sum = warp_sum(sum);
+    float entropy = 0.0f;
+    for (int k = lane; k < K; k += 32) {
+      const float q = has_kd ? c[k] / sum : 0.0f;
+      if (q != 0.0f) entropy += q * logf(q);
+      c[k] = a.kd * q;
+    }
+    entropy = warp_sum(entropy);
+    __syncwarp();
+    bool found = false;
+    for (int k = lane; k < K; k += 32) {
+      const int32_t v = id[k];
+      float w = 0.0f;
+      bool first = v != kNoId;
+      for (int j = 0; first && j < K; ++j) {
+        if (id[j] != v) continue;
+        if (j < k) first = false;
+        w += c[j];
+      }
+      if (first && has_y && v == y) {
+        w += a.ce;
+        found = true;
+      }
+      id2[k] = first ? v : kNoId;
+      c2[k] = w;
+    }
+    found = __any_sync(~0u, found);
+    if (lane == 0) {
+      id2[K] = has_y && !found ? int32_t(y) : kNoId;
+      c2[K] = a.ce;
+      a.konst[t] = has_kd ? float(double(a.kd) * a.tau * entropy) : 0.0f;
+    }
+    __syncwarp();
+    int kept = 0;
+    for (int k = lane; k <= K; k += 32) kept += id2[k] != kNoId;
+    kept = __reduce_add_sync(~0u, kept);
+    for (int k = lane; k <= K; k += 32) {
+      const int32_t v = id2[k];
+      if (v == kNoId) continue;
+      int rank = 0;
+      for (int j = 0; j <= K; ++j) rank += id2[j] < v;
+      ids[rank] = v;
+      weights[rank] = c2[k];
+    }
+    for (int k = kept + lane; k < a.L; k += 32) {
+      ids[k] = kNoId;
+      weights[k] = 0.0f;
+    }
+  }
+  if (lane == 0) {
+    a.coef[t] = make_float2(has_y ? a.ce : 0.0f, has_kd ? a.kd : 0.0f);
+    a.rowpos[t] = has_y || has_kd ? 0 : -1;
+    if (a.forward && !(has_y || has_kd)) {
+      a.loss[t] = 0.0f;
+      if (a.has_ce) a.lse[t] = 0.0f;
+      if (a.has_kd) a.lse_tau[t] = 0.0f;
+    }
+  }
+}
+
+// One block: numbers the rows that have a target, in order.
+__global__ void __launch_bounds__(1024) number_rows_kernel(const Args a) {
+  __shared__ int32_t warps[32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int32_t base = 0;
+  for (int64_t t0 = 0; t0 < a.T; t0 += 1024) {
+    const int64_t t = t0 + threadIdx.x;
+    const bool there = t < a.T && a.rowpos[t] >= 0;
+    const unsigned mask = __ballot_sync(~0u, there);
+    if (lane == 0) warps[warp] = __popc(mask);
+    __syncthreads();
+    int32_t before = base, all = base;
+    for (int w = 0; w < 32; ++w) {
+      if (w < warp) before += warps[w];
+      all += warps[w];
+    }
+    if (there) {
+      const int32_t i = before + __popc(mask & ((1u << lane) - 1));
+      a.rowpos[t] = i;
+      a.rowmap[i] = int32_t(t);
+    }
+    base = all;
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) {
+    a.head->rows = base;
+    a.head->ticket = 0;
+  }
+}
+
+// ------------------------------------------------------------------- pack --
+
+// A value as bf16 parts: x = p0 + p1 + p2 up to fp32's rounding (each part
+// holds the next 8 bits; the rests are exact differences). An infinity and
+// a value that would round to one keep the parts finite or zero.
+__device__ __forceinline__ void split(float x, __nv_bfloat16 (&part)[3]) {
+  part[0] = __float2bfloat16_rn(x);
+  if (isinf(__bfloat162float(part[0])) && !isinf(x)) part[0] = __float2bfloat16_rz(x);
+  if (isinf(x)) {
+    part[1] = part[2] = __float2bfloat16_rn(0.0f);
+    return;
+  }
+  const float r = x - __bfloat162float(part[0]);
+  part[1] = __float2bfloat16_rn(r);
+  part[2] = __float2bfloat16_rn(r - __bfloat162float(part[1]));
+}
+
+template <bool F32>
+__device__ __forceinline__ void pack_row(const void* from, int64_t offset, bool there, int64_t D,
+                                         int64_t Dp, __nv_bfloat16* to, int64_t plane) {
+  for (int64_t k = threadIdx.x; k < Dp; k += blockDim.x) {
+    const bool in = there && k < D;
+    if (F32) {
+      __nv_bfloat16 part[3];
+      split(in ? static_cast<const float*>(from)[offset + k] : 0.0f, part);
+      for (int p = 0; p < 3; ++p) to[p * plane + k] = part[p];
+    } else {
+      to[k] = in ? static_cast<const __nv_bfloat16*>(from)[offset + k] : __nv_bfloat16(0.0f);
+    }
+  }
+}
+
+// Rows with a target side by side; zeros after the last, up to the tile.
+template <bool F32>
+__global__ void pack_hidden_kernel(const Args a) {
+  const int64_t i = blockIdx.x;
+  const int32_t rows = a.head->rows;
+  if (i >= (int64_t(rows) + kTileM - 1) / kTileM * kTileM) return;
+  const bool there = i < rows;
+  const int64_t t = there ? a.rowmap[i] : 0;
+  pack_row<F32>(a.hidden, t * a.hidden_stride, there, a.D, a.Dp, a.hp + i * a.Dp, a.Tp * a.Dp);
+}
+
+template <bool F32>
+__global__ void pack_weight_kernel(const Args a, __nv_bfloat16* to) {
+  const int64_t v = blockIdx.x;
+  pack_row<F32>(a.weight, v * a.weight_stride, true, a.D, a.Dp, to + v * a.Dp, a.V * a.Dp);
+}
+
+// ----------------------------------------------------------------- products --
+
+constexpr int kRows = 32, kCols = 256, kDepth = 16;
+
+// C[32][256] = sum_k A(r, k) B(c, k) over [0, depth), in fp32, into shared memory.
+template <typename FA, typename FB>
+__device__ __forceinline__ void product(int64_t depth, FA fa, FB fb, float (*c)[kCols + 1]) {
+  __shared__ float as[kDepth][kRows + 1];
+  __shared__ float bs[kDepth][kCols + 1];
+  const int tx = threadIdx.x & 63, ty = threadIdx.x >> 6;
+  float acc[8][4] = {};
+  for (int64_t k0 = 0; k0 < depth; k0 += kDepth) {
+    for (int i = threadIdx.x; i < kRows * kDepth; i += 256) {
+      const int64_t k = k0 + i % kDepth;
+      as[i % kDepth][i / kDepth] = k < depth ? fa(i / kDepth, k) : 0.0f;
+    }
+    for (int i = threadIdx.x; i < kCols * kDepth; i += 256) {
+      const int64_t k = k0 + i % kDepth;
+      bs[i % kDepth][i / kDepth] = k < depth ? fb(i / kDepth, k) : 0.0f;
+    }
+    __syncthreads();
+    for (int k = 0; k < kDepth; ++k)
+      for (int r = 0; r < 8; ++r)
+        for (int j = 0; j < 4; ++j) acc[r][j] += as[k][ty * 8 + r] * bs[k][tx + 64 * j];
+    __syncthreads();
+  }
+  for (int r = 0; r < 8; ++r)
+    for (int j = 0; j < 4; ++j) c[ty * 8 + r][tx + 64 * j] = acc[r][j];
+  __syncthreads();
+}
+
+__device__ __forceinline__ float joined(const __nv_bfloat16* p, int64_t plane, int planes) {
+  float x = 0.0f;
+  for (int i = planes - 1; i >= 0; --i) x += __bfloat162float(p[i * plane]);
+  return x;
+}
+
+__device__ __forceinline__ void logits_tile(const Args& a, int64_t i0, int64_t v0,
+                                            float (*z)[kCols + 1]) {
+  product(
+      a.D,
+      [&](int r, int64_t k) { return joined(a.hp + (i0 + r) * a.Dp + k, a.Tp * a.Dp, a.planes); },
+      [&](int c, int64_t k) {
+        return v0 + c < a.V ? joined(a.wp + (v0 + c) * a.wp_ld + k, a.wp_plane, a.planes) : 0.0f;
+      },
+      z);
+}
+
+// First entry of the row whose id is not below v.
+__device__ __forceinline__ int first_entry(const int32_t* ids, int L, int64_t v) {
+  int lo = 0, hi = L;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (ids[mid] < v) lo = mid + 1;
+    else hi = mid;
+  }
+  return lo;
+}
+
+// Each tile's maximum and sum of exponentials of every row, and the logits of
+// the entries that fall in it.
+__global__ void __launch_bounds__(256) logits_forward_kernel(const Args a) {
+  __shared__ float z[kRows][kCols + 1];
+  const int32_t rows = a.head->rows;
+  const int64_t i0 = int64_t(blockIdx.y) * kRows, v0 = int64_t(blockIdx.x) * kCols;
+  if (i0 >= rows) return;
+  logits_tile(a, i0, v0, z);
+  const int lane = threadIdx.x & 31;
+  const int cols = int(min(int64_t(kCols), a.V - v0));
+  for (int r = threadIdx.x >> 5; r < kRows && i0 + r < rows; r += 8) {
+    float top = -INFINITY;
+    for (int c = lane; c < cols; c += 32) top = fmaxf(top, z[r][c]);
+    top = warp_max(top);
+    const float base = top == -INFINITY ? 0.0f : top;
+    float sum = 0.0f, sum_tau = 0.0f;
+    for (int c = lane; c < cols; c += 32) {
+      const float d = z[r][c] - base;
+      sum += exp2f(d * kLog2e);
+      if (a.has_kd) sum_tau += exp2f(d * a.inv_tau * kLog2e);
+    }
+    sum = warp_sum(sum);
+    sum_tau = warp_sum(sum_tau);
+    const int64_t at = int64_t(blockIdx.x) * a.Tp + i0 + r;
+    if (isnan(sum + sum_tau)) top = NAN;
+    if (lane == 0) {
+      if (a.has_ce) a.stats[at] = make_float2(top, sum);
+      if (a.has_kd) a.stats_tau[at] = make_float2(top * a.inv_tau, sum_tau);
+      const int64_t t = a.rowmap[i0 + r];
+      const int32_t* ids = a.ids + t * a.L;
+      for (int e = first_entry(ids, a.L, v0); e < a.L && ids[e] < v0 + cols; ++e)
+        a.zent[t * a.L + e] = z[r][ids[e] - v0];
+    }
+  }
+}
+
+// The gradient of a piece's logits (without the factor common to all rows).
+__global__ void __launch_bounds__(256) logits_backward_kernel(const Args a, int64_t c0) {
+  __shared__ float z[kRows][kCols + 1];
+  const int32_t rows = a.head->rows;
+  const int64_t i0 = int64_t(blockIdx.y) * kRows, v0 = c0 + int64_t(blockIdx.x) * kCols;
+  if (i0 >= (int64_t(rows) + kTileM - 1) / kTileM * kTileM) return;
+  logits_tile(a, i0, v0, z);
+  const int lane = threadIdx.x & 31;
+  for (int r = threadIdx.x >> 5; r < kRows; r += 8) {
+    const int64_t i = i0 + r;
+    const bool there = i < rows;
+    const int64_t t = there ? a.rowmap[i] : 0;
+    const float2 f = there ? a.coef[t] : make_float2(0.0f, 0.0f);
+    const float lse = f.x != 0.0f ? a.lse[t] : 0.0f, lse_tau = f.y != 0.0f ? a.lse_tau[t] : 0.0f;
+    const float scale = a.reduction == ZERO_REDUCE_NONE && a.dloss && there ? a.dloss[t] : 1.0f;
+    const int32_t* ids = a.ids + t * a.L;
+    for (int c = lane; c < kCols; c += 32) {
+      float g = 0.0f;
+      if (there && v0 + c < a.V) {
+        const float x = z[r][c];
+        if (f.x != 0.0f) g += f.x * exp2f((x - lse) * kLog2e);
+        if (f.y != 0.0f) g += f.y * exp2f((x * a.inv_tau - lse_tau) * kLog2e);
+        const int e = first_entry(ids, a.L, v0 + c);
+        if (e < a.L && ids[e] == v0 + c) g -= a.weights[t * a.L + e];
+        g *= scale;
+      }
+      __nv_bfloat16* out = a.g + i * a.piece + (v0 - c0) + c;
+      if (a.planes == 1) {
+        *out = __float2bfloat16_rn(g);
+      } else {
+        __nv_bfloat16 part[3];
+        split(g, part);
+        for (int p = 0; p < 3; ++p) out[p * a.Tp * a.piece] = part[p];
+      }
+    }
+  }
+}
+
+__global__ void __launch_bounds__(256) dhidden_kernel(const Args a, int64_t c0) {
+  __shared__ float c[kRows][kCols + 1];
+  const int32_t rows = a.head->rows;
+  const int64_t i0 = int64_t(blockIdx.y) * kRows, d0 = int64_t(blockIdx.x) * kCols;
+  if (i0 >= rows) return;
+  product(
+      min(a.piece, a.V - c0),
+      [&](int r, int64_t k) {
+        return joined(a.g + (i0 + r) * a.piece + k, a.Tp * a.piece, a.planes);
+      },
+      [&](int d, int64_t k) {
+        return d0 + d < a.D ? joined(a.wp + (c0 + k) * a.wp_ld + d0 + d, a.wp_plane, a.planes)
+                            : 0.0f;
+      },
+      c);
+  for (int j = threadIdx.x; j < kRows * kCols; j += 256) {
+    const int64_t i = i0 + j / kCols, d = d0 + j % kCols;
+    if (i >= rows || d >= a.D) continue;
+    float* to = a.dh + i * a.Dp + d;
+    *to = (c0 == 0 ? 0.0f : *to) + c[j / kCols][j % kCols];
+  }
+}
+
+template <bool F32>
+__global__ void __launch_bounds__(256) dweight_kernel(const Args a, int64_t c0) {
+  __shared__ float c[kRows][kCols + 1];
+  const int64_t v0 = int64_t(blockIdx.y) * kRows, d0 = int64_t(blockIdx.x) * kCols;
+  product(
+      a.head->rows,
+      [&](int r, int64_t k) { return joined(a.g + k * a.piece + v0 + r, a.Tp * a.piece, a.planes); },
+      [&](int d, int64_t k) {
+        return d0 + d < a.D ? joined(a.hp + k * a.Dp + d0 + d, a.Tp * a.Dp, a.planes) : 0.0f;
+      },
+      c);
+  const float f = grad_factor(a);
+  for (int j = threadIdx.x; j < kRows * kCols; j += 256) {
+    const int64_t v = c0 + v0 + j / kCols, d = d0 + j % kCols;
+    if (v >= a.V || d >= a.D) continue;
+    float x = f * c[j / kCols][j % kCols];
+    if (F32) {
+      float* to = static_cast<float*>(a.dweight) + v * a.dweight_stride + d;
+      *to = a.accumulate ? *to + x : x;
+    } else {
+      __nv_bfloat16* to = static_cast<__nv_bfloat16*>(a.dweight) + v * a.dweight_stride + d;
+      *to = __float2bfloat16_rn(a.accumulate ? __bfloat162float(*to) + x : x);
+    }
+  }
+}
+
+template <bool F32>
+__global__ void dhidden_out_kernel(const Args a) {
+  const int64_t t = blockIdx.x;
+  const int32_t i = a.rowpos[t];
+  const float f = i < 0 ? 0.0f : grad_factor(a);
+  for (int64_t d = threadIdx.x; d < a.D; d += blockDim.x) {
+    const float x = i < 0 ? 0.0f : f * a.dh[int64_t(i) * a.Dp + d];
+    if (F32) static_cast<float*>(a.dhidden)[t * a.dhidden_stride + d] = x;
+    else static_cast<__nv_bfloat16*>(a.dhidden)[t * a.dhidden_stride + d] = __float2bfloat16_rn(x);
+  }
+}
+
+// ------------------------------------------------------------------- losses --
+
+// log of the sum over the tiles: 8 lanes of a row, each every eighth tile.
+__device__ __forceinline__ double row_lse(const float2* stats, int64_t tiles, int64_t Tp, int64_t i,
+                                          int lane, float2 (*sh)[33], int r) {
+  float m = -INFINITY, s = 0.0f;
+  for (int64_t j = lane; j < tiles; j += 8) {
+    const float2 x = stats[j * Tp + i];
+    if (!(x.x <= m)) {      // a NaN maximum goes on
+      s = s * (m == -INFINITY ? 0.0f : expf(m - x.x)) + x.y;
+      m = x.x;
+    } else {
+      s += x.x == -INFINITY ? 0.0f : x.y * expf(x.x - m);
+    }
+  }
+  sh[lane][r] = make_float2(m, s);
+  __syncthreads();
+  double top = -INFINITY, sum = 0.0;
+  if (lane == 0) {
+    for (int j = 0; j < 8; ++j)
+      if (!(sh[j][r].x <= top)) top = sh[j][r].x;
+    for (int j = 0; j < 8; ++j)
+      if (sh[j][r].x != -INFINITY) sum += double(sh[j][r].y) * exp(double(sh[j][r].x) - top);
+  }
+  __syncthreads();
+  return top + log(sum);
+}
+
+__global__ void __launch_bounds__(256) losses_kernel(const Args a) {
+  __shared__ float2 sh[8][33];
+  __shared__ double part[256];
+  __shared__ bool last;
+  const int r = threadIdx.x & 31, lane = threadIdx.x >> 5;
+  const int32_t rows = a.head->rows;
+  for (int64_t i0 = int64_t(blockIdx.x) * 32; i0 < rows; i0 += int64_t(gridDim.x) * 32) {
+    const int64_t i = i0 + r;
+    const int64_t at = min(i, int64_t(rows) - 1);
+    const double lse = a.has_ce ? row_lse(a.stats, a.tiles, a.Tp, at, lane, sh, r) : 0.0;
+    const double lse_tau = a.has_kd ? row_lse(a.stats_tau, a.tiles, a.Tp, at, lane, sh, r) : 0.0;
+    if (lane == 0 && i < rows) {
+      const int64_t t = a.rowmap[i];
+      const float2 f = a.coef[t];
+      double loss = double(a.konst[t]);
+      if (f.x != 0.0f) loss += double(f.x) * lse;
+      if (f.y != 0.0f) loss += double(f.y) * a.tau * lse_tau;
+      for (int e = 0; e < a.L && a.ids[t * a.L + e] != kNoId; ++e)
+        loss -= double(a.weights[t * a.L + e]) * double(a.zent[t * a.L + e]);
+      a.loss[t] = float(loss);
+      if (a.has_ce) a.lse[t] = float(lse);
+      if (a.has_kd) a.lse_tau[t] = float(lse_tau);
+    }
+  }
+  if (a.reduction == ZERO_REDUCE_NONE) return;
+  // The last block to finish adds the losses in a fixed order.
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x == 0)
+    last = atomicAdd(&a.head->ticket, 1) == int32_t(gridDim.x) - 1;
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
+  double sum = 0.0;
+  for (int64_t t = threadIdx.x; t < a.T; t += 256) sum += double(__ldcg(a.loss + t));
+  part[threadIdx.x] = sum;
+  __syncthreads();
+  for (int w = 128; w; w >>= 1) {
+    if (int(threadIdx.x) < w) part[threadIdx.x] += part[threadIdx.x + w];
+    __syncthreads();
+  }
+  if (threadIdx.x == 0)
+    *a.reduced = float(a.reduction == ZERO_REDUCE_MEAN ? part[0] / double(max(1, rows)) : part[0]);
+}
+
+}  // namespace
+
+cudaError_t launch_rows(const Args& a, cudaStream_t s) {
+  if (a.T > 0) {
+    const int warps = a.K > 256 ? 1 : 4;
+    const size_t sh = a.K ? size_t(warps) * 16 * (a.K + 1) : 0;
+    rows_kernel<<<unsigned((a.T + warps - 1) / warps), warps * 32, sh, s>>>(a);
+  }
+  number_rows_kernel<<<1, 1024, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_pack_hidden(const Args& a, cudaStream_t s) {
+  if (a.planes == 3) pack_hidden_kernel<true><<<unsigned(a.Tp), 128, 0, s>>>(a);
+  else pack_hidden_kernel<false><<<unsigned(a.Tp), 128, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_pack_weight(const Args& a, __nv_bfloat16* to, cudaStream_t s) {
+  if (a.planes == 3) pack_weight_kernel<true><<<unsigned(a.V), 128, 0, s>>>(a, to);
+  else pack_weight_kernel<false><<<unsigned(a.V), 128, 0, s>>>(a, to);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_logits_forward(const Args& a, cudaStream_t s) {
+  logits_forward_kernel<<<dim3(unsigned(a.tiles), unsigned(a.Tp / kRows)), 256, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_losses(const Args& a, cudaStream_t s) {
+  const int64_t blocks = a.Tp / 32;
+  losses_kernel<<<unsigned(blocks < 608 ? blocks : 608), 256, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_logits_backward(const Args& a, int64_t c0, cudaStream_t s) {
+  logits_backward_kernel<<<dim3(unsigned(a.piece / kCols), unsigned(a.Tp / kRows)), 256, 0, s>>>(a, c0);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_dhidden(const Args& a, int64_t c0, cudaStream_t s) {
+  dhidden_kernel<<<dim3(unsigned((a.D + kCols - 1) / kCols), unsigned(a.Tp / kRows)), 256, 0, s>>>(a, c0);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_dweight(const Args& a, int64_t c0, cudaStream_t s) {
+  const dim3 grid(unsigned((a.D + kCols - 1) / kCols), unsigned(a.piece / kRows));
+  if (a.planes == 3) dweight_kernel<true><<<grid, 256, 0, s>>>(a, c0);
+  else dweight_kernel<false><<<grid, 256, 0, s>>>(a, c0);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_dhidden_out(const Args& a, cudaStream_t s) {
+  if (a.planes == 3) dhidden_out_kernel<true><<<unsigned(a.T), 128, 0, s>>>(a);
+  else dhidden_out_kernel<false><<<unsigned(a.T), 128, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace zl

@@ -17,6 +17,7 @@
 #include <thread>
 #include <vector>
 
+#include "loss_internal.h"
 #include "zero_internal.h"
 
 struct zero_states {
@@ -64,6 +65,11 @@ int fail(int code, const char* fmt, ...) {
   va_start(ap, fmt);
   vsnprintf(g_last_error, sizeof(g_last_error), fmt, ap);
   va_end(ap);
+  return code;
+}
+
+int fail_list(int code, const char* fmt, va_list ap) {
+  vsnprintf(g_last_error, sizeof(g_last_error), fmt, ap);
   return code;
 }
 
@@ -324,6 +330,14 @@ std::vector<Range> grad_ranges(const void* const* grads, int64_t n, int32_t N, i
 }
 
 }  // namespace
+
+int zl::set_error(int code, const char* fmt, ...) {
+  va_list ap;
+  va_start(ap, fmt);
+  fail_list(code, fmt, ap);
+  va_end(ap);
+  return code;
+}
 
 extern "C" {
 

@@ -1,0 +1,324 @@
+"""Losses at the vocabulary, from hidden states and the head's weight, with
+their gradients, without ever holding the logits.
+
+``xent_*`` is softmax cross entropy; ``distill_*`` is distillation from a
+teacher's top-K logits at a temperature, alone or mixed with the cross entropy
+(the definitions, and what an empty row is, stand in ``include/zero_gb300.h``
+at ``zero_head_loss_t``). Each comes as
+
+- ``*_forward``: the losses;
+- ``*_backward``: the gradients, from the forward pass's result;
+- ``*_step``: both in one call.
+
+``hidden`` is a [T, D] (or [..., D]) and ``weight`` a [V, D] CUDA tensor, both
+float32 or both bfloat16, with adjacent elements in a row and any row stride.
+``dhidden`` and ``dweight`` may be given as outputs -- for ``dweight`` typically
+the head's view into a rank's flat gradient buffer, which the ZeRO step then
+reads -- and are allocated otherwise; ``accumulate`` adds to ``dweight``.
+
+``linear_cross_entropy`` and ``linear_distillation`` are the same losses as
+differentiable functions for torch.autograd.
+
+Work is queued on ``stream`` (the current stream by default). The workspace is
+taken from PyTorch's allocator for each call, on the current stream; another
+``stream`` is told of it, as of every tensor the call allocates.
+"""
+
+from __future__ import annotations
+
+from typing import NamedTuple
+
+import torch
+
+from . import abi
+
+_REDUCE = {"none": abi.ZERO_REDUCE_NONE, "mean": abi.ZERO_REDUCE_MEAN, "sum": abi.ZERO_REDUCE_SUM}
+
+
+class Losses(NamedTuple):
+    """``loss`` [T] float32 (0 for an empty row); ``reduced``, its mean over the
+    rows that are not empty, or its sum (None for reduction "none"); ``lse`` and
+    ``lse_tau``, the rows' log-sum-exp for a backward pass; the gradients, where
+    they were taken."""
+    loss: torch.Tensor | None
+    reduced: torch.Tensor | None
+    lse: torch.Tensor | None
+    lse_tau: torch.Tensor | None
+    dhidden: torch.Tensor | None = None
+    dweight: torch.Tensor | None = None
+
+
+def _matrix(t, what: str, dtype=None, rows=None, cols=None, device=None):
+    """``t`` as a matrix [rows, cols] without a copy; (tensor, row stride)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{what} must be a CUDA tensor")
+    if t.dtype not in (torch.float32, torch.bfloat16) or (dtype is not None and t.dtype != dtype):
+        want = "float32 or bfloat16" if dtype is None else dtype
+        raise TypeError(f"{what} has dtype {t.dtype}, expected {want}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{what} is on {t.device}, expected {device}")
+    if t.dim() < 2:
+        raise ValueError(f"{what} must have at least 2 dimensions")
+    if t.dim() > 2:
+        try:
+            t = t.view(-1, t.shape[-1])
+        except RuntimeError:
+            raise ValueError(f"{what}'s rows must lie one stride apart") from None
+    if (rows is not None and t.shape[0] != rows) or (cols is not None and t.shape[1] != cols):
+        raise ValueError(f"{what} has shape {tuple(t.shape)}, expected ({rows}, {cols})")
+    n, d = t.shape
+    if d > 1 and n > 0 and t.stride(1) != 1:
+        raise ValueError(f"the elements of {what}'s rows must be adjacent")
+    stride = t.stride(0) if n > 1 else max(d, 1)
+    return t, stride
+
+
+def _vector(t, what: str, dtype, count: int, device):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != dtype:
+        raise TypeError(f"{what} must be a {dtype} CUDA tensor")
+    if t.device != device:
+        raise ValueError(f"{what} is on {t.device}, expected {device}")
+    if t.numel() != count or not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous with {count} elements")
+    return t
+
+
+class _Call:
+    """One call's zero_head_loss_t and the tensors behind its pointers."""
+
+    def __init__(self, hidden, weight, labels, reduction, ignore_index, stream, teacher=None):
+        hidden2, hs = _matrix(hidden, "hidden")
+        self.dtype, self.device = hidden2.dtype, hidden2.device
+        T, D = hidden2.shape
+        weight2, ws = _matrix(weight, "weight", self.dtype, cols=D, device=self.device)
+        if reduction not in _REDUCE:
+            raise ValueError('reduction must be "none", "mean" or "sum"')
+        self.T, self.V, self.D = T, weight2.shape[0], D
+        self.shape = hidden.shape
+        self.stream = stream
+        self.distill = teacher is not None
+        self.keep = [hidden2, weight2]
+        p = self.p = abi.HeadLoss()
+        p.T, p.V, p.D = T, self.V, D
+        p.precision = abi.ZERO_FP32 if self.dtype == torch.float32 else abi.ZERO_BF16_MIXED
+        p.reduction = _REDUCE[reduction]
+        p.hidden, p.hidden_stride = hidden2.data_ptr(), hs
+        p.weight, p.weight_stride = weight2.data_ptr(), ws
+        p.ignore_index = ignore_index
+        p.grad_scale = 1.0
+        if labels is not None:
+            p.labels = _vector(labels, "labels", torch.int64, T, self.device).data_ptr()
+            self.keep.append(labels)
+        elif teacher is None:
+            raise TypeError("labels must be a torch.int64 CUDA tensor")
+        if teacher is not None:
+            ids, logits, temperature, alpha = teacher
+            if not isinstance(ids, torch.Tensor) or ids.dim() < 2:
+                raise ValueError("teacher_ids must have at least 2 dimensions")
+            K = ids.shape[-1]
+            _vector(ids, "teacher_ids", torch.int64, T * K, self.device)
+            if isinstance(logits, torch.Tensor) and logits.dtype == torch.bfloat16:
+                logits = logits.float()
+            _vector(logits, "teacher_logits", torch.float32, T * K, self.device)
+            p.teacher_ids, p.teacher_logits = ids.data_ptr(), logits.data_ptr()
+            p.teacher_k = K
+            p.temperature, p.alpha = float(temperature), float(alpha)
+            self.keep += [ids, logits]
+
+    def new(self, *shape, dtype=torch.float32):
+        t = torch.empty(shape, dtype=dtype, device=self.device)
+        self.keep.append(t)
+        return t
+
+    def outputs(self, lse=None, lse_tau=None):
+        """Rows' statistics: given (backward) or to be written (forward)."""
+        T, p = self.T, self.p
+        if p.labels or not self.distill:
+            lse = self.new(T) if lse is None else _vector(lse, "lse", torch.float32, T, self.device)
+            p.lse = lse.data_ptr()
+        if self.distill:
+            lse_tau = self.new(T) if lse_tau is None else \
+                _vector(lse_tau, "lse_tau", torch.float32, T, self.device)
+            p.lse_tau = lse_tau.data_ptr()
+        return lse, lse_tau
+
+    def losses(self):
+        loss = self.new(*self.shape[:-1])
+        self.p.loss = loss.data_ptr()
+        reduced = None
+        if self.p.reduction != abi.ZERO_REDUCE_NONE:
+            reduced = self.new()
+            self.p.reduced = reduced.data_ptr()
+        return loss, reduced
+
+    def gradients(self, dloss, grad_scale, dhidden, dweight, accumulate):
+        """dhidden / dweight: a tensor to write, None to allocate one, False to leave it out."""
+        p = self.p
+        p.grad_scale = float(grad_scale)
+        p.accumulate = 1 if accumulate else 0
+        if dloss is not None:
+            count = self.T if p.reduction == abi.ZERO_REDUCE_NONE else 1
+            p.dloss = _vector(dloss, "dloss", torch.float32, count, self.device).data_ptr()
+            self.keep.append(dloss)
+        if dhidden is None:
+            dhidden = self.new(*self.shape, dtype=self.dtype)
+        if dweight is None:
+            if accumulate:
+                raise ValueError("accumulate adds to a dweight that is given")
+            dweight = self.new(self.V, self.D, dtype=self.dtype)
+        if dhidden is not False:
+            m, stride = _matrix(dhidden, "dhidden", self.dtype, self.T, self.D, self.device)
+            p.dhidden, p.dhidden_stride = m.data_ptr(), stride
+        if dweight is not False:
+            m, stride = _matrix(dweight, "dweight", self.dtype, self.V, self.D, self.device)
+            p.dweight, p.dweight_stride = m.data_ptr(), stride
+        self.keep += [dhidden, dweight]
+        return (None if dhidden is False else dhidden), (None if dweight is False else dweight)
+
+    def run(self, name: str):
+        kind = "distill" if self.distill else "xent"
+        with torch.cuda.device(self.device):
+            size = getattr(abi, f"zero_{kind}_workspace_bytes")(self.p)
+            space = self.new(size, dtype=torch.uint8)
+            self.p.workspace, self.p.workspace_bytes = space.data_ptr(), size
+            getattr(abi, f"zero_{kind}_{name}")(self.p, self.stream)
+            if isinstance(self.stream, torch.cuda.Stream):
+                for t in self.keep:
+                    if isinstance(t, torch.Tensor):
+                        t.record_stream(self.stream)
+
+
+def xent_forward(hidden, weight, labels, *, reduction: str = "mean", ignore_index: int = -100,
+                 stream=None) -> Losses:
+    """Cross entropy of every row against ``labels`` (int64 [T])."""
+    c = _Call(hidden, weight, labels, reduction, ignore_index, stream)
+    lse, _ = c.outputs()
+    loss, reduced = c.losses()
+    c.run("forward")
+    return Losses(loss, reduced, lse, None)
+
+
+def xent_backward(hidden, weight, labels, lse, *, reduction: str = "mean",
+                  ignore_index: int = -100, dloss=None, grad_scale: float = 1.0, dhidden=None,
+                  dweight=None, accumulate: bool = False, stream=None) -> Losses:
+    """The gradients, given ``lse`` of xent_forward on the same inputs.
+    ``dloss`` (float32): the gradient of the total with respect to ``loss``
+    (reduction "none") or to ``reduced``; ones when None."""
+    c = _Call(hidden, weight, labels, reduction, ignore_index, stream)
+    c.outputs(lse)
+    dh, dw = c.gradients(dloss, grad_scale, dhidden, dweight, accumulate)
+    c.run("backward")
+    return Losses(None, None, lse, None, dh, dw)
+
+
+def xent_step(hidden, weight, labels, *, reduction: str = "mean", ignore_index: int = -100,
+              dloss=None, grad_scale: float = 1.0, dhidden=None, dweight=None,
+              accumulate: bool = False, stream=None) -> Losses:
+    """xent_forward and xent_backward in one call."""
+    c = _Call(hidden, weight, labels, reduction, ignore_index, stream)
+    lse, _ = c.outputs()
+    loss, reduced = c.losses()
+    dh, dw = c.gradients(dloss, grad_scale, dhidden, dweight, accumulate)
+    c.run("step")
+    return Losses(loss, reduced, lse, None, dh, dw)
+
+
+def distill_forward(hidden, weight, teacher_ids, teacher_logits, *, temperature: float = 1.0,
+                    labels=None, alpha: float = 1.0, reduction: str = "mean",
+                    ignore_index: int = -100, stream=None) -> Losses:
+    """Distillation from the teacher's top logits (``teacher_ids`` int64 [T, K],
+    ``teacher_logits`` float32 or bfloat16 [T, K]; an id outside [0, V) is an
+    absent entry), weighted ``alpha``, and with ``labels`` the cross entropy,
+    weighted ``1 - alpha``."""
+    c = _Call(hidden, weight, labels, reduction, ignore_index, stream,
+              (teacher_ids, teacher_logits, temperature, alpha))
+    lse, lse_tau = c.outputs()
+    loss, reduced = c.losses()
+    c.run("forward")
+    return Losses(loss, reduced, lse, lse_tau)
+
+
+def distill_backward(hidden, weight, teacher_ids, teacher_logits, lse, lse_tau, *,
+                     temperature: float = 1.0, labels=None, alpha: float = 1.0,
+                     reduction: str = "mean", ignore_index: int = -100, dloss=None,
+                     grad_scale: float = 1.0, dhidden=None, dweight=None,
+                     accumulate: bool = False, stream=None) -> Losses:
+    """The gradients, given ``lse`` and ``lse_tau`` of distill_forward on the
+    same inputs; ``dloss`` as in xent_backward."""
+    c = _Call(hidden, weight, labels, reduction, ignore_index, stream,
+              (teacher_ids, teacher_logits, temperature, alpha))
+    c.outputs(lse, lse_tau)
+    dh, dw = c.gradients(dloss, grad_scale, dhidden, dweight, accumulate)
+    c.run("backward")
+    return Losses(None, None, lse, lse_tau, dh, dw)
+
+
+def distill_step(hidden, weight, teacher_ids, teacher_logits, *, temperature: float = 1.0,
+                 labels=None, alpha: float = 1.0, reduction: str = "mean",
+                 ignore_index: int = -100, dloss=None, grad_scale: float = 1.0, dhidden=None,
+                 dweight=None, accumulate: bool = False, stream=None) -> Losses:
+    """distill_forward and distill_backward in one call."""
+    c = _Call(hidden, weight, labels, reduction, ignore_index, stream,
+              (teacher_ids, teacher_logits, temperature, alpha))
+    lse, lse_tau = c.outputs()
+    loss, reduced = c.losses()
+    dh, dw = c.gradients(dloss, grad_scale, dhidden, dweight, accumulate)
+    c.run("step")
+    return Losses(loss, reduced, lse, lse_tau, dh, dw)
+
+
+# -------------------------------------------------------------- autograd --
+
+class _Xent(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, hidden, weight, labels, reduction, ignore_index):
+        r = xent_forward(hidden, weight, labels, reduction=reduction, ignore_index=ignore_index)
+        ctx.save_for_backward(hidden, weight, labels, r.lse)
+        ctx.options = dict(reduction=reduction, ignore_index=ignore_index)
+        return r.loss if reduction == "none" else r.reduced
+
+    @staticmethod
+    def backward(ctx, dloss):
+        hidden, weight, labels, lse = ctx.saved_tensors
+        if not any(ctx.needs_input_grad[:2]):
+            return None, None, None, None, None
+        r = xent_backward(hidden, weight, labels, lse, dloss=dloss.contiguous(),
+                          dhidden=None if ctx.needs_input_grad[0] else False,
+                          dweight=None if ctx.needs_input_grad[1] else False, **ctx.options)
+        return r.dhidden, r.dweight, None, None, None
+
+
+class _Distill(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, hidden, weight, ids, logits, labels, options):
+        r = distill_forward(hidden, weight, ids, logits, labels=labels, **options)
+        ctx.save_for_backward(hidden, weight, ids, logits, labels, r.lse, r.lse_tau)
+        ctx.options = options
+        return r.loss if options["reduction"] == "none" else r.reduced
+
+    @staticmethod
+    def backward(ctx, dloss):
+        hidden, weight, ids, logits, labels, lse, lse_tau = ctx.saved_tensors
+        if not any(ctx.needs_input_grad[:2]):
+            return None, None, None, None, None, None
+        r = distill_backward(hidden, weight, ids, logits, lse, lse_tau, labels=labels,
+                             dloss=dloss.contiguous(),
+                             dhidden=None if ctx.needs_input_grad[0] else False,
+                             dweight=None if ctx.needs_input_grad[1] else False, **ctx.options)
+        return r.dhidden, r.dweight, None, None, None, None
+
+
+def linear_cross_entropy(hidden, weight, labels, reduction: str = "mean",
+                         ignore_index: int = -100):
+    """Cross entropy of ``hidden @ weight.T``, differentiable in ``hidden`` and ``weight``."""
+    return _Xent.apply(hidden, weight, labels, reduction, ignore_index)
+
+
+def linear_distillation(hidden, weight, teacher_ids, teacher_logits, temperature: float = 1.0,
+                        labels=None, alpha: float = 1.0, reduction: str = "mean",
+                        ignore_index: int = -100):
+    """The distillation loss, differentiable in ``hidden`` and ``weight`` (the
+    teacher's logits are constants)."""
+    options = dict(temperature=temperature, alpha=alpha, reduction=reduction,
+                   ignore_index=ignore_index)
+    return _Distill.apply(hidden, weight, teacher_ids, teacher_logits, labels, options)
