@@ -70,6 +70,7 @@ def reference(hidden, weight, labels=None, ids=None, logits=None, tau=1.0, alpha
         out["lse_tau"] = torch.where(valid, lse, 0.0)
     count = max(1, int(valid.sum()))
     out["loss"] = loss
+    out["share"] = 1.0 / count if reduction == "mean" else 1.0   # of a row's loss in the reduced one
     out["reduced"] = {"none": None, "sum": loss.sum(), "mean": loss.sum() / count}[reduction]
     row = torch.ones(T, dtype=torch.float64, device=dev)
     if reduction == "none":
@@ -119,6 +120,5 @@ def check(got, r, dtype, what=""):
                 f"got {float(x.flatten()[i])!r}, exact {float(r[name].flatten()[i])!r}, "
                 f"bound {float(b[name].flatten()[i]):.3g}")
     if got.reduced is not None:
-        total = float(b["loss"].sum()) * (1.0 if r["loss"].numel() == 0 else
-                                          float(r["reduced"].abs() / r["loss"].sum().abs().clamp(min=1e-300)))
+        total = float(b["loss"].sum()) * r["share"]
         assert abs(float(got.reduced) - float(r["reduced"])) <= total + 2.0 ** -22 * abs(float(r["reduced"])) + 1e-30, what

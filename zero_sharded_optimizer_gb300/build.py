@@ -19,9 +19,10 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libzero_gb300.so")
 
-SOURCES = ["zero_kernels.cu", "zero_host.cpp", "loss_kernels.cu", "loss_host.cpp"]
+SOURCES = ["zero_kernels.cu", "zero_host.cpp", "loss_kernels.cu", "loss_mma.cu",
+           "loss_host.cpp"]
 HEADERS = [os.path.join(CSRC, "zero_internal.h"), os.path.join(CSRC, "loss_internal.h"),
-           os.path.join(INCLUDE, "zero_gb300.h")]
+           os.path.join(CSRC, "loss_device.cuh"), os.path.join(INCLUDE, "zero_gb300.h")]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-ffp-contract=off",

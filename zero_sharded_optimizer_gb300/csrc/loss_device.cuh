@@ -1,0 +1,45 @@
+// Device functions shared by the vocabulary losses' kernels.
+#pragma once
+
+#include "loss_internal.h"
+
+namespace zl {
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// The factor of both gradients that does not depend on the row: grad_scale,
+// the mean's count, and the reduced loss's own gradient.
+__device__ __forceinline__ float grad_factor(const Args& a) {
+  double f = a.grad_scale;
+  if (a.reduction == ZERO_REDUCE_MEAN) f /= double(max(1, a.head->rows));
+  if (a.reduction != ZERO_REDUCE_NONE && a.dloss) f *= double(*a.dloss);
+  return float(f);
+}
+
+// A value as bf16 parts: x = p0 + p1 + p2 up to fp32's rounding (each part
+// holds the next 8 bits; the rests are exact differences). An infinity and
+// a value that would round to one keep the parts finite or zero.
+__device__ __forceinline__ void split(float x, __nv_bfloat16 (&part)[3]) {
+  part[0] = __float2bfloat16_rn(x);
+  if (isinf(__bfloat162float(part[0])) && !isinf(x)) part[0] = __float2bfloat16_rz(x);
+  if (isinf(x)) {
+    part[1] = part[2] = __float2bfloat16_rn(0.0f);
+    return;
+  }
+  const float r = x - __bfloat162float(part[0]);
+  part[1] = __float2bfloat16_rn(r);
+  part[2] = __float2bfloat16_rn(r - __bfloat162float(part[1]));
+}
+
+// First entry of the row whose id is not below v.
+__device__ __forceinline__ int first_entry(const int32_t* ids, int L, int64_t v) {
+  int lo = 0, hi = L;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (ids[mid] < v) lo = mid + 1;
+    else hi = mid;
+  }
+  return lo;
+}
+
+}  // namespace zl

@@ -1,5 +1,6 @@
 // Host side of the vocabulary losses: argument checks, the workspace's layout
-// and the order of the launches. Device work is in loss_kernels.cu.
+// the tensor maps and the order of the launches. Device work is in
+// loss_kernels.cu and loss_mma.cu.
 
 #include <algorithm>
 #include <cmath>
@@ -10,6 +11,8 @@
 namespace {
 
 using zl::Args;
+using zl::Job;
+using zl::Jobs;
 using zl::set_error;
 
 constexpr int64_t kMostSize = 0x7fffffff - 1024;  // T, V and D: 32-bit tile coordinates
@@ -165,7 +168,7 @@ struct Layout {
 // The weight can be read in place by 16-byte copies of whole rows.
 bool weight_in_place(const zero_head_loss_t* p) {
   return p->precision == ZERO_BF16_MIXED && reinterpret_cast<uintptr_t>(p->weight) % 16 == 0 &&
-         p->weight_stride % 8 == 0;
+         p->weight_stride % 8 == 0 && p->weight_stride < (int64_t(1) << 39);
 }
 
 int plan(const zero_head_loss_t* p, bool distill, int pass, Args* a, __nv_bfloat16** packed_weight,
@@ -231,8 +234,8 @@ int plan(const zero_head_loss_t* p, bool distill, int pass, Args* a, __nv_bfloat
   // The forward pass's arrays and the backward pass's lie over one another.
   const int64_t common = w.at;
   a->zent = w.take<float>(a->T, a->L);
-  if (a->has_ce) a->stats = w.take<float2>(a->tiles, a->Tp);
-  if (a->has_kd) a->stats_tau = w.take<float2>(a->tiles, a->Tp);
+  if (a->has_ce) a->stats = w.take<float2>(2 * a->tiles, a->Tp);
+  if (a->has_kd) a->stats_tau = w.take<float2>(2 * a->tiles, a->Tp);
   int64_t most = w.at;
   if (pass & kBackward) {
     w.at = common;
@@ -241,12 +244,113 @@ int plan(const zero_head_loss_t* p, bool distill, int pass, Args* a, __nv_bfloat
     const int64_t pieces = (a->V + widest - 1) / widest;
     a->piece = round_up((a->V + pieces - 1) / pieces, zl::kTileN);
     a->g = w.take<__nv_bfloat16>(a->Tp * a->planes, a->piece);
-    if (p->dhidden) a->dh = w.take<float>(a->Tp, a->Dp);
+    // dhidden's sums over a piece are split while its tiles and dweight's do
+    // not fill the machine four times over and a part is 512 long at least.
+    const int64_t wide = (a->D + zl::kTileN - 1) / zl::kTileN;
+    const int64_t hidden = a->Tp / zl::kTileM * wide;
+    const int64_t weight = p->dweight ? a->piece / zl::kTileM * wide : 0;
+    a->splits = 1;
+    while (a->splits < 16 && weight + a->splits * hidden < 4 * 76 && a->piece / (2 * a->splits) >= 512)
+      a->splits *= 2;
+    if (p->dhidden) a->dh = w.take<float>(a->splits * a->Tp, a->Dp);
     most = std::max(most, w.at);
   }
   if (!w.fits) return set_error(ZERO_EINVAL, "the problem's workspace overflows 64 bits");
   *bytes = most;
   return ZERO_OK;
+}
+
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// The driver's encoder, looked up once (the library does not link the driver).
+EncodeTiled encoder() {
+  static const EncodeTiled fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found) !=
+            cudaSuccess || found != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<EncodeTiled>(p);
+  }();
+  return fn;
+}
+
+// A bf16 array [planes][rows][cols] as boxes of 64 columns by `box_rows` rows,
+// in shared memory with the 128-byte swizzle; elements outside read as zero.
+bool tensor_map(CUtensorMap* map, const void* base, int64_t cols, int64_t rows, int64_t ld, int64_t planes,
+                int64_t plane, uint32_t box_rows) {
+  const cuuint64_t dims[3] = {cuuint64_t(cols), cuuint64_t(rows), cuuint64_t(planes)};
+  const cuuint64_t strides[2] = {cuuint64_t(ld) * 2, cuuint64_t(planes > 1 ? plane : ld) * 2};
+  const cuuint32_t box[3] = {64, box_rows, 1}, unit[3] = {1, 1, 1};
+  return encoder()(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, unit,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The operands, each once read along K (boxes of 128 rows) and once across it
+// (boxes of 64 rows of K).
+struct Maps {
+  CUtensorMap hidden, hidden_mn, weight, weight_mn, g, g_mn;
+  bool make(const Args& a, bool backward) {
+    bool ok = tensor_map(&hidden, a.hp, a.Dp, a.Tp, a.Dp, a.planes, a.Tp * a.Dp, 128);
+    const int64_t wide = a.wp_plane ? a.Dp : a.D;
+    ok = ok && tensor_map(&weight, a.wp, wide, a.V, a.wp_ld, a.planes, a.wp_plane, 128);
+    if (!backward) return ok;
+    return ok && tensor_map(&hidden_mn, a.hp, a.Dp, a.Tp, a.Dp, a.planes, a.Tp * a.Dp, 64) &&
+           tensor_map(&weight_mn, a.wp, wide, a.V, a.wp_ld, a.planes, a.wp_plane, 64) &&
+           tensor_map(&g, a.g, a.piece, a.Tp, a.piece, a.planes, a.Tp * a.piece, 128) &&
+           tensor_map(&g_mn, a.g, a.piece, a.Tp, a.piece, a.planes, a.Tp * a.piece, 64);
+  }
+};
+
+int32_t tiles_of(int64_t n) { return int32_t((n + 255) / 256); }
+
+Job logits_job(const Args& a, const Maps& maps, bool gradient, int64_t c0) {
+  const int64_t cols = gradient ? std::min(a.piece, a.V - c0) : a.V;
+  Job j{};
+  j.a = maps.hidden;
+  j.b = maps.weight;
+  if (gradient) j.out = maps.g;
+  j.mode = gradient ? zl::kGradient : zl::kForward;
+  j.n_tiles = tiles_of(cols);
+  j.n_cols = int32_t(cols);
+  j.depth = int32_t(a.D);
+  j.splits = 1;
+  j.b_row0 = int32_t(c0);
+  j.c0 = c0;
+  return j;
+}
+
+Job hidden_job(const Args& a, const Maps& maps, int64_t c0) {
+  Job j{};
+  j.a = maps.g;
+  j.b = maps.weight_mn;
+  j.mode = zl::kHidden;
+  j.n_tiles = tiles_of(a.D);
+  j.n_cols = int32_t(a.D);
+  j.depth = int32_t(std::min(a.piece, a.V - c0));
+  j.splits = a.splits;
+  j.b_k0 = int32_t(c0);
+  j.first = c0 == 0;
+  j.c0 = c0;
+  return j;
+}
+
+Job weight_job(const Args& a, const Maps& maps, int64_t c0) {
+  const int es = a.planes == 1 ? 2 : 4;
+  Job j{};
+  j.a = maps.g_mn;
+  j.b = maps.hidden_mn;
+  j.mode = zl::kWeight;
+  j.m_tiles = tiles_of(std::min(a.piece, a.V - c0));
+  j.n_tiles = tiles_of(a.D);
+  j.n_cols = int32_t(a.D);
+  j.splits = 1;
+  j.vector = reinterpret_cast<uintptr_t>(a.dweight) % 16 == 0 && a.dweight_stride * es % 16 == 0;
+  j.c0 = c0;
+  return j;
 }
 
 int workspace_bytes(const zero_head_loss_t* p, bool distill, int64_t* bytes) {
@@ -271,6 +375,15 @@ int run(const zero_head_loss_t* p, bool distill, int pass, cudaStream_t s) {
   if (!p->workspace || p->workspace_bytes < bytes)
     return set_error(ZERO_EINVAL, "the workspace has %lld bytes, %lld are needed",
                      (long long)(p->workspace ? p->workspace_bytes : 0), (long long)bytes);
+  if (!encoder()) return set_error(ZERO_ECUDA, "the CUDA driver has no cuTensorMapEncodeTiled");
+  Maps maps;
+  if (!maps.make(a, pass & kBackward))
+    return set_error(ZERO_EINVAL, "the problem's arrays are too large for tensor maps");
+  int device = 0, sms = 0;
+  cudaError_t q = cudaGetDevice(&device);
+  if (q == cudaSuccess) q = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device);
+  if (q != cudaSuccess)
+    return set_error(ZERO_ECUDA, "device: %s (%s)", cudaGetErrorString(q), cudaGetErrorName(q));
   const char* what = "rows";
   cudaError_t e = zl::launch_rows(a, s);
   auto next = [&](const char* name, auto&& launch) {
@@ -281,14 +394,24 @@ int run(const zero_head_loss_t* p, bool distill, int pass, cudaStream_t s) {
   next("packing hidden", [&] { return zl::launch_pack_hidden(a, s); });
   if (packed) next("packing weight", [&] { return zl::launch_pack_weight(a, packed, s); });
   if (pass & kForward) {
-    next("logits", [&] { return zl::launch_logits_forward(a, s); });
+    next("logits", [&] {
+      Jobs jobs{{logits_job(a, maps, false, 0)}, 1};
+      return zl::launch_products(a, jobs, sms, s);
+    });
     next("losses", [&] { return zl::launch_losses(a, s); });
   }
   if (pass & kBackward) {
     for (int64_t c0 = 0; c0 < a.V; c0 += a.piece) {
-      next("logits' gradient", [&] { return zl::launch_logits_backward(a, c0, s); });
-      if (p->dhidden) next("dhidden", [&] { return zl::launch_dhidden(a, c0, s); });
-      if (p->dweight) next("dweight", [&] { return zl::launch_dweight(a, c0, s); });
+      next("the logits' gradient", [&] {
+        Jobs jobs{{logits_job(a, maps, true, c0)}, 1};
+        return zl::launch_products(a, jobs, sms, s);
+      });
+      next("the gradients", [&] {
+        Jobs jobs{};
+        if (p->dweight) jobs.job[jobs.count++] = weight_job(a, maps, c0);
+        if (p->dhidden) jobs.job[jobs.count++] = hidden_job(a, maps, c0);
+        return zl::launch_products(a, jobs, sms, s);
+      });
     }
     if (p->dhidden && p->T) next("dhidden", [&] { return zl::launch_dhidden_out(a, s); });
   }

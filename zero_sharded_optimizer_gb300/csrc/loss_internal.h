@@ -1,8 +1,10 @@
 // Internal interface between the host side of the vocabulary losses
-// (loss_host.cpp) and their kernels (loss_kernels.cu). Not part of the public
+// (loss_host.cpp) and their kernels (loss_kernels.cu, and the matrix products
+// in loss_mma.cu). Not part of the public
 // C ABI.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -15,7 +17,7 @@ namespace zl {
 int set_error(int code, const char* fmt, ...);
 
 // Tile of the logits: rows (tokens) by columns (vocabulary).
-constexpr int kTileM = 128;
+constexpr int kTileM = 256;
 constexpr int kTileN = 256;
 constexpr int kPadD = 64;       // packed operands are padded to this width
 constexpr int32_t kNoId = 0x7fffffff;
@@ -24,6 +26,7 @@ constexpr int32_t kNoId = 0x7fffffff;
 struct Head {
   int32_t rows;    // rows with a target (the compact rows)
   int32_t ticket;  // blocks of the reduction that are done
+  int32_t fault;   // a wait of the matrix kernel ran out: the results are not valid
 };
 
 // Everything the kernels read or write. Rows with a target are packed densely:
@@ -76,22 +79,42 @@ struct Args {
   const __nv_bfloat16* wp;  // [planes][V][Dp], or the caller's weight (then wp_ld)
   int64_t wp_ld, wp_plane;
   int64_t tiles;          // vocabulary tiles
-  float2* stats;          // [tiles][Tp] (max, sum of exp) of z
-  float2* stats_tau;      // [tiles][Tp] of z / tau
+  float2* stats;          // [2 tiles][Tp] half a tile's (m, sum of 2^(z log2(e) - m))
+  float2* stats_tau;      // [2 tiles][Tp] of z / tau
   __nv_bfloat16* g;       // [planes][Tp][piece] gradient of a piece's logits
   int64_t piece;          // columns of a piece, a multiple of kTileN
-  float* dh;              // [Tp][Dp] running sum of dhidden over the pieces
+  int32_t splits;         // parts of a piece's columns that dhidden is summed in
+  float* dh;              // [splits][Tp][Dp] running sums of dhidden over the pieces
+};
+
+// The matrix kernel's work: see loss_mma.cu.
+enum Mode : int32_t { kForward, kGradient, kHidden, kWeight };
+
+struct Job {
+  CUtensorMap a, b, out;
+  Mode mode;
+  int32_t m_tiles;   // kWeight: row tiles (else they follow from the rows with a target)
+  int32_t n_tiles;
+  int32_t n_cols;    // columns of the product
+  int32_t depth;     // length of the sums (kWeight: the rows with a target)
+  int32_t splits;
+  int32_t b_k0;      // where B's K begins, or (b_row0) its columns
+  int32_t b_row0;
+  int32_t first;     // kHidden: the sums begin here
+  int32_t vector;    // kWeight: rows of dweight take 16-byte accesses
+  int64_t c0;        // the piece's first vocabulary column
+};
+
+struct Jobs {
+  Job job[2];
+  int32_t count;
 };
 
 cudaError_t launch_rows(const Args& a, cudaStream_t s);
 cudaError_t launch_pack_hidden(const Args& a, cudaStream_t s);
 cudaError_t launch_pack_weight(const Args& a, __nv_bfloat16* to, cudaStream_t s);
-cudaError_t launch_logits_forward(const Args& a, cudaStream_t s);
 cudaError_t launch_losses(const Args& a, cudaStream_t s);
-// The piece [c0, min(c0 + piece, V)): its logits' gradient, and the products with it.
-cudaError_t launch_logits_backward(const Args& a, int64_t c0, cudaStream_t s);
-cudaError_t launch_dhidden(const Args& a, int64_t c0, cudaStream_t s);
-cudaError_t launch_dweight(const Args& a, int64_t c0, cudaStream_t s);
 cudaError_t launch_dhidden_out(const Args& a, cudaStream_t s);
+cudaError_t launch_products(const Args& a, const Jobs& jobs, int sms, cudaStream_t s);
 
 }  // namespace zl

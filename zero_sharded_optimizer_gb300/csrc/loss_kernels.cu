@@ -1,12 +1,10 @@
 // Kernels of the vocabulary losses (zero_xent_*, zero_distill_*).
 #include <math.h>
 
-#include "loss_internal.h"
+#include "loss_device.cuh"
 
 namespace zl {
 namespace {
-
-constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ float warp_max(float x) {
   for (int o = 16; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(~0u, x, o));
@@ -15,15 +13,6 @@ __device__ __forceinline__ float warp_max(float x) {
 __device__ __forceinline__ float warp_sum(float x) {
   for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
   return x;
-}
-
-// The factor of both gradients that does not depend on the row: grad_scale,
-// the mean's count, and the reduced loss's own gradient.
-__device__ __forceinline__ float grad_factor(const Args& a) {
-  double f = a.grad_scale;
-  if (a.reduction == ZERO_REDUCE_MEAN) f /= double(max(1, a.head->rows));
-  if (a.reduction != ZERO_REDUCE_NONE && a.dloss) f *= double(*a.dloss);
-  return float(f);
 }
 
 // ------------------------------------------------------------------- rows --
@@ -164,25 +153,11 @@ __global__ void __launch_bounds__(1024) number_rows_kernel(const Args a) {
   if (threadIdx.x == 0) {
     a.head->rows = base;
     a.head->ticket = 0;
+    a.head->fault = 0;
   }
 }
 
 // ------------------------------------------------------------------- pack --
-
-// A value as bf16 parts: x = p0 + p1 + p2 up to fp32's rounding (each part
-// holds the next 8 bits; the rests are exact differences). An infinity and
-// a value that would round to one keep the parts finite or zero.
-__device__ __forceinline__ void split(float x, __nv_bfloat16 (&part)[3]) {
-  part[0] = __float2bfloat16_rn(x);
-  if (isinf(__bfloat162float(part[0])) && !isinf(x)) part[0] = __float2bfloat16_rz(x);
-  if (isinf(x)) {
-    part[1] = part[2] = __float2bfloat16_rn(0.0f);
-    return;
-  }
-  const float r = x - __bfloat162float(part[0]);
-  part[1] = __float2bfloat16_rn(r);
-  part[2] = __float2bfloat16_rn(r - __bfloat162float(part[1]));
-}
 
 template <bool F32>
 __device__ __forceinline__ void pack_row(const void* from, int64_t offset, bool there, int64_t D,
@@ -216,195 +191,17 @@ __global__ void pack_weight_kernel(const Args a, __nv_bfloat16* to) {
   pack_row<F32>(a.weight, v * a.weight_stride, true, a.D, a.Dp, to + v * a.Dp, a.V * a.Dp);
 }
 
-// ----------------------------------------------------------------- products --
-
-constexpr int kRows = 32, kCols = 256, kDepth = 16;
-
-// C[32][256] = sum_k A(r, k) B(c, k) over [0, depth), in fp32, into shared memory.
-template <typename FA, typename FB>
-__device__ __forceinline__ void product(int64_t depth, FA fa, FB fb, float (*c)[kCols + 1]) {
-  __shared__ float as[kDepth][kRows + 1];
-  __shared__ float bs[kDepth][kCols + 1];
-  const int tx = threadIdx.x & 63, ty = threadIdx.x >> 6;
-  float acc[8][4] = {};
-  for (int64_t k0 = 0; k0 < depth; k0 += kDepth) {
-    for (int i = threadIdx.x; i < kRows * kDepth; i += 256) {
-      const int64_t k = k0 + i % kDepth;
-      as[i % kDepth][i / kDepth] = k < depth ? fa(i / kDepth, k) : 0.0f;
-    }
-    for (int i = threadIdx.x; i < kCols * kDepth; i += 256) {
-      const int64_t k = k0 + i % kDepth;
-      bs[i % kDepth][i / kDepth] = k < depth ? fb(i / kDepth, k) : 0.0f;
-    }
-    __syncthreads();
-    for (int k = 0; k < kDepth; ++k)
-      for (int r = 0; r < 8; ++r)
-        for (int j = 0; j < 4; ++j) acc[r][j] += as[k][ty * 8 + r] * bs[k][tx + 64 * j];
-    __syncthreads();
-  }
-  for (int r = 0; r < 8; ++r)
-    for (int j = 0; j < 4; ++j) c[ty * 8 + r][tx + 64 * j] = acc[r][j];
-  __syncthreads();
-}
-
-__device__ __forceinline__ float joined(const __nv_bfloat16* p, int64_t plane, int planes) {
-  float x = 0.0f;
-  for (int i = planes - 1; i >= 0; --i) x += __bfloat162float(p[i * plane]);
-  return x;
-}
-
-__device__ __forceinline__ void logits_tile(const Args& a, int64_t i0, int64_t v0,
-                                            float (*z)[kCols + 1]) {
-  product(
-      a.D,
-      [&](int r, int64_t k) { return joined(a.hp + (i0 + r) * a.Dp + k, a.Tp * a.Dp, a.planes); },
-      [&](int c, int64_t k) {
-        return v0 + c < a.V ? joined(a.wp + (v0 + c) * a.wp_ld + k, a.wp_plane, a.planes) : 0.0f;
-      },
-      z);
-}
-
-// First entry of the row whose id is not below v.
-__device__ __forceinline__ int first_entry(const int32_t* ids, int L, int64_t v) {
-  int lo = 0, hi = L;
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (ids[mid] < v) lo = mid + 1;
-    else hi = mid;
-  }
-  return lo;
-}
-
-// Each tile's maximum and sum of exponentials of every row, and the logits of
-// the entries that fall in it.
-__global__ void __launch_bounds__(256) logits_forward_kernel(const Args a) {
-  __shared__ float z[kRows][kCols + 1];
-  const int32_t rows = a.head->rows;
-  const int64_t i0 = int64_t(blockIdx.y) * kRows, v0 = int64_t(blockIdx.x) * kCols;
-  if (i0 >= rows) return;
-  logits_tile(a, i0, v0, z);
-  const int lane = threadIdx.x & 31;
-  const int cols = int(min(int64_t(kCols), a.V - v0));
-  for (int r = threadIdx.x >> 5; r < kRows && i0 + r < rows; r += 8) {
-    float top = -INFINITY;
-    for (int c = lane; c < cols; c += 32) top = fmaxf(top, z[r][c]);
-    top = warp_max(top);
-    const float base = top == -INFINITY ? 0.0f : top;
-    float sum = 0.0f, sum_tau = 0.0f;
-    for (int c = lane; c < cols; c += 32) {
-      const float d = z[r][c] - base;
-      sum += exp2f(d * kLog2e);
-      if (a.has_kd) sum_tau += exp2f(d * a.inv_tau * kLog2e);
-    }
-    sum = warp_sum(sum);
-    sum_tau = warp_sum(sum_tau);
-    const int64_t at = int64_t(blockIdx.x) * a.Tp + i0 + r;
-    if (isnan(sum + sum_tau)) top = NAN;
-    if (lane == 0) {
-      if (a.has_ce) a.stats[at] = make_float2(top, sum);
-      if (a.has_kd) a.stats_tau[at] = make_float2(top * a.inv_tau, sum_tau);
-      const int64_t t = a.rowmap[i0 + r];
-      const int32_t* ids = a.ids + t * a.L;
-      for (int e = first_entry(ids, a.L, v0); e < a.L && ids[e] < v0 + cols; ++e)
-        a.zent[t * a.L + e] = z[r][ids[e] - v0];
-    }
-  }
-}
-
-// The gradient of a piece's logits (without the factor common to all rows).
-__global__ void __launch_bounds__(256) logits_backward_kernel(const Args a, int64_t c0) {
-  __shared__ float z[kRows][kCols + 1];
-  const int32_t rows = a.head->rows;
-  const int64_t i0 = int64_t(blockIdx.y) * kRows, v0 = c0 + int64_t(blockIdx.x) * kCols;
-  if (i0 >= (int64_t(rows) + kTileM - 1) / kTileM * kTileM) return;
-  logits_tile(a, i0, v0, z);
-  const int lane = threadIdx.x & 31;
-  for (int r = threadIdx.x >> 5; r < kRows; r += 8) {
-    const int64_t i = i0 + r;
-    const bool there = i < rows;
-    const int64_t t = there ? a.rowmap[i] : 0;
-    const float2 f = there ? a.coef[t] : make_float2(0.0f, 0.0f);
-    const float lse = f.x != 0.0f ? a.lse[t] : 0.0f, lse_tau = f.y != 0.0f ? a.lse_tau[t] : 0.0f;
-    const float scale = a.reduction == ZERO_REDUCE_NONE && a.dloss && there ? a.dloss[t] : 1.0f;
-    const int32_t* ids = a.ids + t * a.L;
-    for (int c = lane; c < kCols; c += 32) {
-      float g = 0.0f;
-      if (there && v0 + c < a.V) {
-        const float x = z[r][c];
-        if (f.x != 0.0f) g += f.x * exp2f((x - lse) * kLog2e);
-        if (f.y != 0.0f) g += f.y * exp2f((x * a.inv_tau - lse_tau) * kLog2e);
-        const int e = first_entry(ids, a.L, v0 + c);
-        if (e < a.L && ids[e] == v0 + c) g -= a.weights[t * a.L + e];
-        g *= scale;
-      }
-      __nv_bfloat16* out = a.g + i * a.piece + (v0 - c0) + c;
-      if (a.planes == 1) {
-        *out = __float2bfloat16_rn(g);
-      } else {
-        __nv_bfloat16 part[3];
-        split(g, part);
-        for (int p = 0; p < 3; ++p) out[p * a.Tp * a.piece] = part[p];
-      }
-    }
-  }
-}
-
-__global__ void __launch_bounds__(256) dhidden_kernel(const Args a, int64_t c0) {
-  __shared__ float c[kRows][kCols + 1];
-  const int32_t rows = a.head->rows;
-  const int64_t i0 = int64_t(blockIdx.y) * kRows, d0 = int64_t(blockIdx.x) * kCols;
-  if (i0 >= rows) return;
-  product(
-      min(a.piece, a.V - c0),
-      [&](int r, int64_t k) {
-        return joined(a.g + (i0 + r) * a.piece + k, a.Tp * a.piece, a.planes);
-      },
-      [&](int d, int64_t k) {
-        return d0 + d < a.D ? joined(a.wp + (c0 + k) * a.wp_ld + d0 + d, a.wp_plane, a.planes)
-                            : 0.0f;
-      },
-      c);
-  for (int j = threadIdx.x; j < kRows * kCols; j += 256) {
-    const int64_t i = i0 + j / kCols, d = d0 + j % kCols;
-    if (i >= rows || d >= a.D) continue;
-    float* to = a.dh + i * a.Dp + d;
-    *to = (c0 == 0 ? 0.0f : *to) + c[j / kCols][j % kCols];
-  }
-}
-
-template <bool F32>
-__global__ void __launch_bounds__(256) dweight_kernel(const Args a, int64_t c0) {
-  __shared__ float c[kRows][kCols + 1];
-  const int64_t v0 = int64_t(blockIdx.y) * kRows, d0 = int64_t(blockIdx.x) * kCols;
-  product(
-      a.head->rows,
-      [&](int r, int64_t k) { return joined(a.g + k * a.piece + v0 + r, a.Tp * a.piece, a.planes); },
-      [&](int d, int64_t k) {
-        return d0 + d < a.D ? joined(a.hp + k * a.Dp + d0 + d, a.Tp * a.Dp, a.planes) : 0.0f;
-      },
-      c);
-  const float f = grad_factor(a);
-  for (int j = threadIdx.x; j < kRows * kCols; j += 256) {
-    const int64_t v = c0 + v0 + j / kCols, d = d0 + j % kCols;
-    if (v >= a.V || d >= a.D) continue;
-    float x = f * c[j / kCols][j % kCols];
-    if (F32) {
-      float* to = static_cast<float*>(a.dweight) + v * a.dweight_stride + d;
-      *to = a.accumulate ? *to + x : x;
-    } else {
-      __nv_bfloat16* to = static_cast<__nv_bfloat16*>(a.dweight) + v * a.dweight_stride + d;
-      *to = __float2bfloat16_rn(a.accumulate ? __bfloat162float(*to) + x : x);
-    }
-  }
-}
-
 template <bool F32>
 __global__ void dhidden_out_kernel(const Args a) {
   const int64_t t = blockIdx.x;
   const int32_t i = a.rowpos[t];
-  const float f = i < 0 ? 0.0f : grad_factor(a);
+  const float f = a.head->fault ? NAN : grad_factor(a);
   for (int64_t d = threadIdx.x; d < a.D; d += blockDim.x) {
-    const float x = i < 0 ? 0.0f : f * a.dh[int64_t(i) * a.Dp + d];
+    float x = 0.0f;
+    if (i >= 0) {
+      for (int p = 0; p < a.splits; ++p) x += a.dh[(p * a.Tp + i) * a.Dp + d];
+      x *= f;
+    }
     if (F32) static_cast<float*>(a.dhidden)[t * a.dhidden_stride + d] = x;
     else static_cast<__nv_bfloat16*>(a.dhidden)[t * a.dhidden_stride + d] = __float2bfloat16_rn(x);
   }
@@ -412,17 +209,18 @@ __global__ void dhidden_out_kernel(const Args a) {
 
 // ------------------------------------------------------------------- losses --
 
-// log of the sum over the tiles: 8 lanes of a row, each every eighth tile.
-__device__ __forceinline__ double row_lse(const float2* stats, int64_t tiles, int64_t Tp, int64_t i,
+// The row's log-sum-exp from its partial maxima and sums (maxima in powers of
+// two): 8 lanes of a row, each every eighth partial.
+__device__ __forceinline__ double row_lse(const float2* stats, int64_t count, int64_t Tp, int64_t i,
                                           int lane, float2 (*sh)[33], int r) {
   float m = -INFINITY, s = 0.0f;
-  for (int64_t j = lane; j < tiles; j += 8) {
+  for (int64_t j = lane; j < count; j += 8) {
     const float2 x = stats[j * Tp + i];
     if (!(x.x <= m)) {      // a NaN maximum goes on
-      s = s * (m == -INFINITY ? 0.0f : expf(m - x.x)) + x.y;
+      s = s * (m == -INFINITY ? 0.0f : exp2f(m - x.x)) + x.y;
       m = x.x;
     } else {
-      s += x.x == -INFINITY ? 0.0f : x.y * expf(x.x - m);
+      s += x.x == -INFINITY ? 0.0f : x.y * exp2f(x.x - m);
     }
   }
   sh[lane][r] = make_float2(m, s);
@@ -432,10 +230,10 @@ __device__ __forceinline__ double row_lse(const float2* stats, int64_t tiles, in
     for (int j = 0; j < 8; ++j)
       if (!(sh[j][r].x <= top)) top = sh[j][r].x;
     for (int j = 0; j < 8; ++j)
-      if (sh[j][r].x != -INFINITY) sum += double(sh[j][r].y) * exp(double(sh[j][r].x) - top);
+      if (sh[j][r].x != -INFINITY) sum += double(sh[j][r].y) * exp2(double(sh[j][r].x) - top);
   }
   __syncthreads();
-  return top + log(sum);
+  return (top + log2(sum)) * 0.69314718055994530942;
 }
 
 __global__ void __launch_bounds__(256) losses_kernel(const Args a) {
@@ -447,8 +245,8 @@ __global__ void __launch_bounds__(256) losses_kernel(const Args a) {
   for (int64_t i0 = int64_t(blockIdx.x) * 32; i0 < rows; i0 += int64_t(gridDim.x) * 32) {
     const int64_t i = i0 + r;
     const int64_t at = min(i, int64_t(rows) - 1);
-    const double lse = a.has_ce ? row_lse(a.stats, a.tiles, a.Tp, at, lane, sh, r) : 0.0;
-    const double lse_tau = a.has_kd ? row_lse(a.stats_tau, a.tiles, a.Tp, at, lane, sh, r) : 0.0;
+    const double lse = a.has_ce ? row_lse(a.stats, 2 * a.tiles, a.Tp, at, lane, sh, r) : 0.0;
+    const double lse_tau = a.has_kd ? row_lse(a.stats_tau, 2 * a.tiles, a.Tp, at, lane, sh, r) : 0.0;
     if (lane == 0 && i < rows) {
       const int64_t t = a.rowmap[i];
       const float2 f = a.coef[t];
@@ -457,6 +255,7 @@ __global__ void __launch_bounds__(256) losses_kernel(const Args a) {
       if (f.y != 0.0f) loss += double(f.y) * a.tau * lse_tau;
       for (int e = 0; e < a.L && a.ids[t * a.L + e] != kNoId; ++e)
         loss -= double(a.weights[t * a.L + e]) * double(a.zent[t * a.L + e]);
+      if (a.head->fault) loss = NAN;
       a.loss[t] = float(loss);
       if (a.has_ce) a.lse[t] = float(lse);
       if (a.has_kd) a.lse_tau[t] = float(lse_tau);
@@ -507,31 +306,9 @@ cudaError_t launch_pack_weight(const Args& a, __nv_bfloat16* to, cudaStream_t s)
   return cudaGetLastError();
 }
 
-cudaError_t launch_logits_forward(const Args& a, cudaStream_t s) {
-  logits_forward_kernel<<<dim3(unsigned(a.tiles), unsigned(a.Tp / kRows)), 256, 0, s>>>(a);
-  return cudaGetLastError();
-}
-
 cudaError_t launch_losses(const Args& a, cudaStream_t s) {
   const int64_t blocks = a.Tp / 32;
   losses_kernel<<<unsigned(blocks < 608 ? blocks : 608), 256, 0, s>>>(a);
-  return cudaGetLastError();
-}
-
-cudaError_t launch_logits_backward(const Args& a, int64_t c0, cudaStream_t s) {
-  logits_backward_kernel<<<dim3(unsigned(a.piece / kCols), unsigned(a.Tp / kRows)), 256, 0, s>>>(a, c0);
-  return cudaGetLastError();
-}
-
-cudaError_t launch_dhidden(const Args& a, int64_t c0, cudaStream_t s) {
-  dhidden_kernel<<<dim3(unsigned((a.D + kCols - 1) / kCols), unsigned(a.Tp / kRows)), 256, 0, s>>>(a, c0);
-  return cudaGetLastError();
-}
-
-cudaError_t launch_dweight(const Args& a, int64_t c0, cudaStream_t s) {
-  const dim3 grid(unsigned((a.D + kCols - 1) / kCols), unsigned(a.piece / kRows));
-  if (a.planes == 3) dweight_kernel<true><<<grid, 256, 0, s>>>(a, c0);
-  else dweight_kernel<false><<<grid, 256, 0, s>>>(a, c0);
   return cudaGetLastError();
 }
 

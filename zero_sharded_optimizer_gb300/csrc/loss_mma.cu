@@ -1,0 +1,690 @@
+// The matrix products of the vocabulary losses on the tensor cores (tcgen05).
+//
+// One persistent kernel works off a list of jobs, each a grid of tiles:
+//   kForward   z = H W^T, kept only as each row's maximum and sum of exponentials
+//   kGradient  z again, as the logits' gradient G of one piece of the vocabulary
+//   kHidden    dH += G W over that piece
+//   kWeight    dW = G^T H of that piece's rows
+// A pair of CTAs (a cluster on two neighbouring SMs) forms one 256 x 256 tile
+// with one tcgen05.mma.cta_group::2 stream: each CTA holds 128 rows of A and
+// half of B's columns, so an operand byte read from L2 feeds twice the
+// multiplications of a single CTA's 128 x 256 tile.
+//
+// Warps: 0 copies operand tiles by TMA into a ring of stages, 1 (of the pair's
+// first CTA) issues the products, 4..11 read finished accumulators from tensor
+// memory; two accumulators of 256 columns let the next tile's products run
+// under this tile's epilogue.
+//
+// fp32 storage: each operand is three bf16 parts and the products of the parts
+// are summed into one accumulator, smallest first, in six passes over K.
+
+#include <cuda.h>
+#include <math.h>
+
+#include <type_traits>
+
+#include "loss_device.cuh"
+
+namespace zl {
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kEpilogueWarp = 4;   // first of eight
+constexpr int kBlockK = 64;        // elements of K a stage holds: 128 bytes
+constexpr int kHalf = 128;         // rows of A, and of B, that a CTA holds
+constexpr int kOperandBytes = kHalf * kBlockK * 2;
+constexpr int kStageBytes = 2 * kOperandBytes;
+constexpr int kBoxBytes = kHalf * 64 * 2;  // 128 rows x 64 columns of G on their way out
+
+template <int PLANES>
+struct Shape {
+  static constexpr int stages = PLANES == 1 ? 6 : 4;
+  static constexpr int boxes = 2 * PLANES;  // staging: one box per plane for each half of the columns
+  static constexpr int bytes = stages * kStageBytes + boxes * kBoxBytes + 1024 + 256;
+};
+
+// ------------------------------------------------------------------- PTX --
+
+__device__ __forceinline__ uint32_t smem_u32(const void* p) {
+  return uint32_t(__cvta_generic_to_shared(p));
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint64_t timer_ns() {
+  uint64_t t;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+  return t;
+}
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.b32 %0, 1, 0, p;\n}" : "=r"(p));
+  return p != 0;
+}
+
+__device__ __forceinline__ void barrier_init(uint32_t bar, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void barrier_expect(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void barrier_arrive_remote(uint32_t cluster_bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
+__device__ __forceinline__ bool barrier_try(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n.reg .pred p;\n"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+      "selp.b32 %0, 1, 0, p;\n}"
+      : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+  return ok != 0;
+}
+
+// A wait gives up after ten seconds, or when another warp of the CTA has: the
+// kernel then ends without its results, the fault is kept in the workspace's
+// head and the losses become NaN.
+constexpr uint64_t kWaitLimitNs = 10ull * 1000 * 1000 * 1000;
+
+struct Waiter {
+  volatile uint32_t* given_up;  // shared
+  Head* head;
+  __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity) const {
+    if (barrier_try(bar, parity)) return true;
+    const uint64_t begin = timer_ns();
+    for (uint32_t n = 1;; ++n) {
+      if (barrier_try(bar, parity)) return true;
+      if ((n & 63) == 0 && (*given_up || timer_ns() - begin > kWaitLimitNs)) {
+        *given_up = 1;
+        head->fault = 1;
+        return false;
+      }
+    }
+  }
+};
+
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int x, int y, int z,
+                                         uint32_t cluster_bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst), "l"(map), "r"(cluster_bar), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+__device__ __forceinline__ void tma_store(const CUtensorMap* map, uint32_t src, int x, int y, int z) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(map),
+               "r"(src), "r"(x), "r"(y), "r"(z) : "memory");
+}
+__device__ __forceinline__ void store_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void store_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void store_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+__device__ __forceinline__ void proxy_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void named_barrier(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+// Over the eight epilogue warps.
+__device__ __forceinline__ bool all_agree(bool mine) {
+  uint32_t all;
+  asm volatile(
+      "{\n.reg .pred p, q;\nsetp.ne.u32 p, %1, 0;\n"
+      "barrier.cta.red.and.pred.aligned q, 3, 256, p;\n"
+      "selp.b32 %0, 1, 0, q;\n}" : "=r"(all) : "r"(uint32_t(mine)) : "memory");
+  return all != 0;
+}
+
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
+      "r"(uint32_t(add)) : "memory");
+}
+// The barrier at this offset in both CTAs gets one arrival when the products issued so far are done.
+__device__ __forceinline__ void mma_commit(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          bar), "h"(uint16_t(3)) : "memory");
+}
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+__device__ __forceinline__ void tmem_load32(uint32_t addr, float (&v)[32]) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  __syncwarp();
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr) : "memory");
+}
+__device__ __forceinline__ float tmem_load1(uint32_t addr) {
+  float v;
+  __syncwarp();
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\ntcgen05.wait::ld.sync.aligned;"
+               : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Shared-memory matrix descriptor, 128-byte swizzle, 8-row groups 1024 bytes
+// apart. K-major (a row of K is 128 bytes): the leading offset is not used.
+// MN-major (64 elements of M or N are 128 bytes, one row per k): the leading
+// offset is the distance of the next 64 elements.
+__device__ __forceinline__ uint64_t operand_desc(uint32_t addr, bool mn_major) {
+  const uint64_t lead = mn_major ? (64 * kBlockK * 2) >> 4 : 1;
+  return uint64_t((addr & 0x3ffff) >> 4) | lead << 16 | uint64_t(1024 >> 4) << 32 | uint64_t(1) << 46 |
+         uint64_t(2) << 61;
+}
+
+// ------------------------------------------------------------------ units --
+
+// The six products of three-part operands, smallest first.
+__device__ constexpr int kTermA[6] = {0, 1, 2, 0, 1, 0};
+__device__ constexpr int kTermB[6] = {2, 1, 0, 1, 0, 0};
+
+struct Unit {
+  int job;
+  int m0, n0;         // first row and column of the pair's tile
+  int n;              // columns of the product: up to 256, a multiple of 32
+  int k0, blocks;     // first K element and number of 64-element blocks
+  int split;
+};
+
+template <int PLANES>
+__device__ __forceinline__ bool unit_at(const Jobs& jobs, int rows, int64_t u, Unit* unit) {
+  const int row_tiles = (rows + 255) / 256;
+  for (int j = 0; j < jobs.count; ++j) {
+    const Job& job = jobs.job[j];
+    const int mt = job.mode == kWeight ? job.m_tiles : row_tiles;
+    const int64_t all = int64_t(mt) * job.n_tiles * job.splits;
+    if (u >= all) {
+      u -= all;
+      continue;
+    }
+    unit->job = j;
+    const int64_t tile = u % (int64_t(mt) * job.n_tiles);
+    unit->split = int(u / (int64_t(mt) * job.n_tiles));
+    const int m = int(job.mode == kWeight ? tile / job.n_tiles : tile % mt);
+    const int n = int(job.mode == kWeight ? tile % job.n_tiles : tile / mt);
+    unit->m0 = m * 256;
+    unit->n0 = n * 256;
+    unit->n = min(256, (job.n_cols - unit->n0 + 31) / 32 * 32);
+    const int depth = job.mode == kWeight ? rows : job.depth;
+    const int blocks = (depth + kBlockK - 1) / kBlockK;
+    const int first = int(int64_t(blocks) * unit->split / job.splits);
+    unit->k0 = first * kBlockK;
+    unit->blocks = int(int64_t(blocks) * (unit->split + 1) / job.splits) - first;
+    return true;
+  }
+  return false;
+}
+
+// --------------------------------------------------------------- epilogues --
+
+struct Thread {          // of the epilogue
+  int row;               // of the CTA's 128
+  int half;              // columns [128 half, 128 half + 128)
+  uint32_t lane_addr;    // its quarter of the lanes, in the address's upper half
+};
+
+// A row of the logits: what the epilogues of kForward and kGradient need of it.
+struct Row {
+  int i;                 // compact row
+  int64_t t;
+  bool there;
+};
+
+__device__ __forceinline__ Row row_of(const Args& a, int rows, const Unit& u, const Thread& th, uint32_t rank) {
+  Row r;
+  r.i = u.m0 + int(rank) * kHalf + th.row;
+  r.there = r.i < rows;
+  r.t = r.there ? a.rowmap[r.i] : 0;
+  return r;
+}
+
+// Calls f(entry, column) for each of the row's sparse entries with a column in
+// [begin, end) relative to v0, with the column's logit read from the
+// accumulator: all lanes of the warp read the same column, lowest first.
+template <typename F>
+__device__ __forceinline__ void each_entry(const int32_t* ids, int L, bool there, int& e, int32_t& id, int64_t v0,
+                                           int end, uint32_t acc, F f) {
+  for (;;) {
+    const int mine = there && id < v0 + end ? int(id - v0) : 0x7fffffff;
+    const int c = __reduce_min_sync(~0u, mine);
+    if (c == 0x7fffffff) break;
+    const float z = tmem_load1(acc + c);
+    if (mine == c) {
+      f(e, c, z);
+      ++e;
+      id = e < L ? ids[e] : kNoId;
+    }
+    __syncwarp();
+  }
+}
+
+// sum of 2^(c z - m) with m moved to the maximum. m is the rounded product, the
+// reference that the sum is stored with, so its rounding cancels.
+__device__ __forceinline__ void add_exponentials(const float (&z)[32], float top, float c, float& m, float& sum) {
+  const float next = __fmul_rn(top, c);
+  const float base = next == -INFINITY ? 0.0f : next;
+  float s0 = m == -INFINITY ? 0.0f : sum * exp2_fast(m - base), s1 = 0.0f;
+#pragma unroll
+  for (int j = 0; j < 32; j += 2) {
+    s0 += exp2_fast(fmaf(z[j], c, -base));
+    s1 += exp2_fast(fmaf(z[j + 1], c, -base));
+  }
+  sum = s0 + s1;
+  m = next;
+}
+
+template <bool CE, bool KD>
+__device__ __forceinline__ void forward_epilogue(const Args& a, const Unit& u, const Thread& th, const Row& r,
+                                                 uint32_t acc, int& e, int32_t& id) {
+  const int64_t v0 = u.n0;
+  const int begin = th.half * 128;
+  const int cols = int(min(int64_t(256), a.V - v0));
+  const float c_ce = kLog2e, c_kd = a.inv_tau * kLog2e;
+  // Running maximum, and sums relative to it, in powers of two: exp(z) = 2^(c z).
+  float top = -INFINITY, sum = 0.0f, sum_kd = 0.0f, m_ce = -INFINITY, m_kd = -INFINITY;
+#pragma unroll 1
+  for (int k = 0; k < 4; ++k) {
+    const int valid = cols - begin - 32 * k;
+    if (valid <= 0) break;
+    float z[32];
+    tmem_load32(acc + begin + 32 * k, z);
+    if (valid < 32) {
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        if (j >= valid) z[j] = -INFINITY;
+    }
+    float t0 = top, t1 = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < 32; j += 2) {
+      t0 = fmaxf(t0, z[j]);
+      t1 = fmaxf(t1, z[j + 1]);
+    }
+    top = fmaxf(t0, t1);
+    if (CE) add_exponentials(z, top, c_ce, m_ce, sum);
+    if (KD) add_exponentials(z, top, c_kd, m_kd, sum_kd);
+  }
+  each_entry(a.ids + r.t * a.L, a.L, r.there, e, id, v0, begin + 128, acc,
+             [&](int k, int, float z) { a.zent[r.t * a.L + k] = z; });
+  if (!r.there) return;
+  const int64_t at = (v0 / 256 * 2 + th.half) * a.Tp + r.i;
+  const bool nan = isnan(sum + sum_kd);
+  if (CE) a.stats[at] = make_float2(nan ? NAN : m_ce, sum);
+  if (KD) a.stats_tau[at] = make_float2(nan ? NAN : m_kd, sum_kd);
+}
+
+// The logits' gradient without the factor that all rows share, as the bf16
+// operand of the two products: rounded once (fp32 storage: in three parts).
+template <int PLANES, bool CE, bool KD>
+__device__ __forceinline__ void gradient_epilogue(const Args& a, const Job& job, const Unit& u, const Thread& th,
+                                                  const Row& r, uint32_t acc, uint32_t rank, uint8_t* staging,
+                                                  int& e, int32_t& id) {
+  const int64_t v0 = job.c0 + u.n0;
+  const int begin = th.half * 128;
+  const int cols = int(min(int64_t(256), a.V - v0));
+  const float2 f = r.there ? a.coef[r.t] : make_float2(0.0f, 0.0f);
+  const float scale = a.reduction == ZERO_REDUCE_NONE && a.dloss && r.there ? a.dloss[r.t] : 1.0f;
+  const float w_ce = f.x * scale, w_kd = f.y * scale;
+  // Terms that the row does not have are exp2(-inf) = 0, whatever the accumulator holds.
+  const float lse = CE && f.x != 0.0f ? a.lse[r.t] : INFINITY;
+  const float lse_kd = KD && f.y != 0.0f ? a.lse_tau[r.t] : INFINITY;
+  auto value = [&](float z) {
+    float g = 0.0f;
+    if (CE) g = w_ce * exp2_fast((z - lse) * kLog2e);
+    if (KD) g = fmaf(w_kd, exp2_fast(fmaf(z, a.inv_tau, -lse_kd) * kLog2e), g);
+    return g;
+  };
+  uint8_t* box = staging + th.half * PLANES * kBoxBytes;
+  const int issuer = (th.row == 0);
+#pragma unroll 1
+  for (int b = 0; b < 2; ++b) {
+    if (issuer) store_wait_read();
+    named_barrier(1 + th.half, 128);
+#pragma unroll 1
+    for (int k = 0; k < 2; ++k) {
+      const int c0 = begin + 64 * b + 32 * k;
+      float z[32];
+      tmem_load32(acc + c0, z);
+      const int valid = r.there ? cols - c0 : 0;
+#pragma unroll
+      for (int j = 0; j < 32; j += 8) {
+        uint32_t word[PLANES][4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const float x0 = j + 2 * q < valid ? value(z[j + 2 * q]) : 0.0f;
+          const float x1 = j + 2 * q + 1 < valid ? value(z[j + 2 * q + 1]) : 0.0f;
+          if (PLANES == 1) {
+            __nv_bfloat162 h = __floats2bfloat162_rn(x0, x1);
+            word[0][q] = *reinterpret_cast<uint32_t*>(&h);
+          } else {
+            __nv_bfloat16 p0[3], p1[3];
+            split(x0, p0);
+            split(x1, p1);
+#pragma unroll
+            for (int p = 0; p < PLANES; ++p)
+              word[p][q] = uint32_t(__bfloat16_as_ushort(p0[p])) | uint32_t(__bfloat16_as_ushort(p1[p])) << 16;
+          }
+        }
+        const int chunk = (4 * k + j / 8) ^ (th.row & 7);
+#pragma unroll
+        for (int p = 0; p < PLANES; ++p)
+          *reinterpret_cast<uint4*>(box + p * kBoxBytes + th.row * 128 + chunk * 16) =
+              make_uint4(word[p][0], word[p][1], word[p][2], word[p][3]);
+      }
+    }
+    each_entry(a.ids + r.t * a.L, a.L, r.there, e, id, v0, begin + 64 * (b + 1), acc, [&](int k, int c, float z) {
+      const float g = value(z) - scale * a.weights[r.t * a.L + k];
+      const int at = c - begin - 64 * b;
+      uint8_t* to = box + th.row * 128 + (((at / 8) ^ (th.row & 7)) * 16) + (at % 8) * 2;
+      if (PLANES == 1) {
+        *reinterpret_cast<__nv_bfloat16*>(to) = __float2bfloat16_rn(g);
+      } else {
+        __nv_bfloat16 part[3];
+        split(g, part);
+#pragma unroll
+        for (int p = 0; p < PLANES; ++p) *reinterpret_cast<__nv_bfloat16*>(to + p * kBoxBytes) = part[p];
+      }
+    });
+    proxy_fence();
+    named_barrier(1 + th.half, 128);
+    if (issuer) {
+#pragma unroll
+      for (int p = 0; p < PLANES; ++p)
+        tma_store(&job.out, smem_u32(box + p * kBoxBytes), u.n0 + begin + 64 * b, u.m0 + int(rank) * kHalf, p);
+      store_commit();
+    }
+  }
+}
+
+// dH of a piece, fp32: stored by the first piece, added by the others. Each
+// element gets one addition per launch, so the order is fixed.
+__device__ __forceinline__ void hidden_epilogue(const Args& a, const Job& job, const Unit& u, const Thread& th,
+                                                int rows, uint32_t acc, uint32_t rank) {
+  const int i = u.m0 + int(rank) * kHalf + th.row;
+  float* to = a.dh + (int64_t(u.split) * a.Tp + i) * a.Dp + u.n0;
+  for (int c = th.half * 128; c < min(u.n, th.half * 128 + 128); c += 32) {
+    float x[32];
+    if (u.blocks) {
+      tmem_load32(acc + c, x);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 32; ++j) x[j] = 0.0f;
+    }
+#pragma unroll
+    for (int j = 0; j < 32; j += 4) {
+      if (i >= rows) break;
+      if (job.first)
+        *reinterpret_cast<float4*>(to + c + j) = make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
+      else
+        asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(to + c + j), "f"(x[j]), "f"(x[j + 1]),
+                     "f"(x[j + 2]), "f"(x[j + 3]) : "memory");
+    }
+  }
+}
+
+template <int PLANES>
+__device__ __forceinline__ void weight_epilogue(const Args& a, const Job& job, const Unit& u, const Thread& th,
+                                                float factor, uint32_t acc, uint32_t rank) {
+  const int64_t v = job.c0 + u.m0 + int(rank) * kHalf + th.row;
+  using T = typename std::conditional<PLANES == 1, __nv_bfloat16, float>::type;
+  T* to = static_cast<T*>(a.dweight) + v * a.dweight_stride + u.n0;
+  for (int c = th.half * 128; c < min(u.n, th.half * 128 + 128); c += 32) {
+    float x[32];
+    if (u.blocks) {
+      tmem_load32(acc + c, x);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 32; ++j) x[j] = 0.0f;
+    }
+    if (v >= a.V) continue;
+    const int valid = int(min(int64_t(32), a.D - u.n0 - c));
+    if (job.vector && valid == 32) {
+      constexpr int per = 16 / sizeof(T);
+#pragma unroll
+      for (int j = 0; j < 32; j += per) {
+        uint4 w;
+        T* out = reinterpret_cast<T*>(&w);
+        if (a.accumulate) w = *reinterpret_cast<const uint4*>(to + c + j);
+#pragma unroll
+        for (int q = 0; q < per; ++q) {
+          const float y = factor * x[j + q];
+          out[q] = T(a.accumulate ? float(out[q]) + y : y);
+        }
+        *reinterpret_cast<uint4*>(to + c + j) = w;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 32; ++j) {
+        if (j >= valid) break;
+        const float y = factor * x[j];
+        to[c + j] = T(a.accumulate ? float(to[c + j]) + y : y);
+      }
+    }
+  }
+}
+
+// ----------------------------------------------------------------- kernel --
+
+template <int PLANES, bool CE, bool KD>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    products_kernel(const __grid_constant__ Args a, const __grid_constant__ Jobs jobs) {
+  constexpr int kStages = Shape<PLANES>::stages;
+  constexpr int kTerms = PLANES == 1 ? 1 : 6;
+  extern __shared__ uint8_t raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* staging = base + kStages * kStageBytes;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(staging + Shape<PLANES>::boxes * kBoxBytes);
+  // barriers: stage full [kStages], stage empty [kStages], accumulator full [2], empty [2]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kStages + 4);
+  volatile uint32_t* given_up = tmem_slot + 1;
+  const uint32_t full = smem_u32(bars), empty = full + 8 * kStages, acc_full = empty + 8 * kStages,
+                 acc_empty = acc_full + 16;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+
+  if (warp == 0 && lane == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      barrier_init(full + 8 * s, 1);
+      barrier_init(empty + 8 * s, 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      barrier_init(acc_full + 8 * b, 1);
+      barrier_init(acc_empty + 8 * b, 16);  // eight warps of each CTA
+    }
+    *given_up = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(tmem_slot))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  fence_before();
+  __syncthreads();
+  cluster_sync();
+  fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int rows = a.head->rows;
+  const Waiter wait{given_up, a.head};
+  const int64_t first = blockIdx.x / 2, step = gridDim.x / 2;
+  Unit u;
+
+  if (warp == 0) {
+    // ---- copies
+    if (elect_one()) {
+      const uint32_t full0 = in_cta(full, 0);
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int64_t n = first; ok && unit_at<PLANES>(jobs, rows, n, &u); n += step) {
+        const Job& job = jobs.job[u.job];
+        const bool a_mn = job.mode == kWeight, b_mn = job.mode == kWeight || job.mode == kHidden;
+        const int am = u.m0 + int(rank) * kHalf, bn = u.n0 + int(rank) * (u.n / 2);
+        const int b_boxes = b_mn ? (u.n / 2 + 63) / 64 : 0;
+        const uint32_t bytes = 2 * (kOperandBytes + (b_mn ? b_boxes * 64 * kBlockK * 2 : kOperandBytes));
+        for (int term = 0; ok && term < kTerms; ++term) {
+          const int pa = kTerms == 1 ? 0 : kTermA[term], pb = kTerms == 1 ? 0 : kTermB[term];
+          for (int k = 0; k < u.blocks; ++k) {
+            if (!(ok = wait(empty + 8 * stage, phase ^ 1))) break;
+            const uint32_t sa = smem_u32(base + stage * kStageBytes), sb = sa + kOperandBytes;
+            const uint32_t bar = full0 + 8 * stage;
+            if (rank == 0) barrier_expect(full + 8 * stage, bytes);
+            const int kk = u.k0 + k * kBlockK;
+            if (a_mn) {
+              tma_load(sa, &job.a, am, kk, pa, bar);
+              tma_load(sa + 64 * kBlockK * 2, &job.a, am + 64, kk, pa, bar);
+            } else {
+              tma_load(sa, &job.a, kk, am, pa, bar);
+            }
+            if (b_mn) {
+              for (int c = 0; c < b_boxes; ++c)
+                tma_load(sb + c * 64 * kBlockK * 2, &job.b, bn + 64 * c, kk + job.b_k0, pb, bar);
+            } else {
+              tma_load(sb, &job.b, kk, bn + job.b_row0, pb, bar);
+            }
+            if (++stage == kStages) {
+              stage = 0;
+              phase ^= 1;
+            }
+          }
+        }
+      }
+      if (!ok) {  // let the copies in flight land before the CTA's memory goes
+        const uint64_t begin = timer_ns();
+        while (timer_ns() - begin < 2000000) __nanosleep(1000);
+      }
+    }
+  } else if (warp == 1 && rank == 0) {
+    // ---- products
+    if (elect_one()) {
+      int stage = 0;
+      uint32_t phase = 0, acc_phase = 0;
+      int buffer = 0;
+      bool ok = true;
+      for (int64_t n = first; ok && unit_at<PLANES>(jobs, rows, n, &u); n += step) {
+        const Job& job = jobs.job[u.job];
+        const bool a_mn = job.mode == kWeight, b_mn = job.mode == kWeight || job.mode == kHidden;
+        // fp32 accumulator, bf16 operands, majors, N, M = 256
+        const uint32_t idesc = 1u << 4 | 1u << 7 | 1u << 10 | uint32_t(a_mn) << 15 | uint32_t(b_mn) << 16 |
+                               uint32_t(u.n / 8) << 17 | uint32_t(256 / 16) << 24;
+        const uint64_t a_step = (a_mn ? 16 * 128 : 32) >> 4, b_step = (b_mn ? 16 * 128 : 32) >> 4;
+        const uint32_t d = tmem + buffer * 256;
+        if (!(ok = wait(acc_empty + 8 * buffer, acc_phase ^ 1))) break;
+        fence_after();
+        bool add = false;
+        for (int k = 0; k < u.blocks * kTerms; ++k) {
+          if (!(ok = wait(full + 8 * stage, phase))) break;
+          fence_after();
+          const uint32_t sa = smem_u32(base + stage * kStageBytes);
+          const uint64_t da = operand_desc(sa, a_mn), db = operand_desc(sa + kOperandBytes, b_mn);
+#pragma unroll
+          for (int q = 0; q < kBlockK / 16; ++q) {
+            mma(d, da + q * a_step, db + q * b_step, idesc, add);
+            add = true;
+          }
+          mma_commit(empty + 8 * stage);
+          if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+        mma_commit(acc_full + 8 * buffer);
+        if (++buffer == 2) {
+          buffer = 0;
+          acc_phase ^= 1;
+        }
+      }
+    }
+  } else if (warp >= kEpilogueWarp) {
+    // ---- epilogues
+    Thread th;
+    th.row = (warp & 3) * 32 + lane;
+    th.half = (warp - kEpilogueWarp) / 4;
+    th.lane_addr = uint32_t((warp & 3) * 32) << 16;
+    const uint32_t acc_empty0 = in_cta(acc_empty, 0);
+    const float factor = grad_factor(a);
+    int buffer = 0;
+    uint32_t phase = 0;
+    for (int64_t n = first; unit_at<PLANES>(jobs, rows, n, &u); n += step) {
+      const Job& job = jobs.job[u.job];
+      const uint32_t acc = tmem + th.lane_addr + buffer * 256;
+      Row r{};
+      int e = 0;
+      int32_t id = kNoId;
+      if (job.mode == kForward || job.mode == kGradient) {
+        r = row_of(a, rows, u, th, rank);
+        if (r.there) {
+          const int32_t* ids = a.ids + r.t * a.L;
+          e = first_entry(ids, a.L, job.c0 + u.n0 + th.half * 128);
+          id = e < a.L ? ids[e] : kNoId;
+        }
+      }
+      // The eight warps go on together, or none does: they meet at barriers below.
+      if (!all_agree(wait(acc_full + 8 * buffer, phase))) break;
+      fence_after();
+      if (job.mode == kForward) forward_epilogue<CE, KD>(a, u, th, r, acc, e, id);
+      else if (job.mode == kGradient)
+        gradient_epilogue<PLANES, CE, KD>(a, job, u, th, r, acc, rank, staging, e, id);
+      else if (job.mode == kHidden) hidden_epilogue(a, job, u, th, rows, acc, rank);
+      else weight_epilogue<PLANES>(a, job, u, th, factor, acc, rank);
+      fence_before();
+      __syncwarp();
+      if (lane == 0) barrier_arrive_remote(acc_empty0 + 8 * buffer);
+      if (++buffer == 2) {
+        buffer = 0;
+        phase ^= 1;
+      }
+    }
+    if (th.row == 0) store_wait();
+  }
+  __syncwarp();
+  fence_before();
+  __syncthreads();
+  cluster_sync();
+  fence_after();
+  if (warp == 1)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+}
+
+template <int PLANES, bool CE, bool KD>
+cudaError_t launch(const Args& a, const Jobs& jobs, int sms, cudaStream_t s) {
+  auto* kernel = products_kernel<PLANES, CE, KD>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<PLANES>::bytes);
+  if (e != cudaSuccess) return e;
+  kernel<<<unsigned(sms / 2 * 2), kThreads, Shape<PLANES>::bytes, s>>>(a, jobs);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_products(const Args& a, const Jobs& jobs, int sms, cudaStream_t s) {
+  if (a.planes == 1) {
+    if (!a.has_kd) return launch<1, true, false>(a, jobs, sms, s);
+    return a.has_ce ? launch<1, true, true>(a, jobs, sms, s) : launch<1, false, true>(a, jobs, sms, s);
+  }
+  if (!a.has_kd) return launch<3, true, false>(a, jobs, sms, s);
+  return a.has_ce ? launch<3, true, true>(a, jobs, sms, s) : launch<3, false, true>(a, jobs, sms, s);
+}
+
+}  // namespace zl
