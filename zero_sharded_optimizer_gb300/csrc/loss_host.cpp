@@ -17,8 +17,9 @@ using zl::set_error;
 
 constexpr int64_t kMostSize = 0x7fffffff - 1024;  // T, V and D: 32-bit tile coordinates
 // A piece of the logits' gradient is at most this many bytes (one tile's width
-// of columns at least).
-constexpr int64_t kPieceBytes = int64_t(128) << 20;
+// of columns at least); two are held, so that the next piece is formed while
+// this one's products run.
+constexpr int64_t kPieceBytes = int64_t(64) << 20;
 
 int64_t round_up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
 
@@ -231,6 +232,16 @@ int plan(const zero_head_loss_t* p, bool distill, int pass, Args* a, __nv_bfloat
     a->wp_ld = a->Dp;
     a->wp_plane = a->V * a->Dp;
   }
+  int64_t pieces = 0;
+  if (pass & kBackward) {
+    const int64_t widest = std::max<int64_t>(
+        kPieceBytes / (2 * a->planes * a->Tp) / zl::kTileN * zl::kTileN, zl::kTileN);
+    pieces = (a->V + widest - 1) / widest;
+    a->piece = round_up((a->V + pieces - 1) / pieces, zl::kTileN);
+    pieces = (a->V + a->piece - 1) / a->piece;
+  }
+  a->launches = 2 + pieces;
+  a->counters = w.take<int32_t>(a->launches);
   // The forward pass's arrays and the backward pass's lie over one another.
   const int64_t common = w.at;
   a->zent = w.take<float>(a->T, a->L);
@@ -239,19 +250,18 @@ int plan(const zero_head_loss_t* p, bool distill, int pass, Args* a, __nv_bfloat
   int64_t most = w.at;
   if (pass & kBackward) {
     w.at = common;
-    const int64_t widest = std::max<int64_t>(
-        kPieceBytes / (2 * a->planes * a->Tp) / zl::kTileN * zl::kTileN, zl::kTileN);
-    const int64_t pieces = (a->V + widest - 1) / widest;
-    a->piece = round_up((a->V + pieces - 1) / pieces, zl::kTileN);
-    a->g = w.take<__nv_bfloat16>(a->Tp * a->planes, a->piece);
-    // dhidden's sums over a piece are split while its tiles and dweight's do
-    // not fill the machine four times over and a part is 512 long at least.
+    for (int b = 0; b < (pieces > 1 ? 2 : 1); ++b)
+      a->g[b] = w.take<__nv_bfloat16>(a->Tp * a->planes, a->piece);
+    if (pieces == 1) a->g[1] = a->g[0];
+    // dhidden's sums over a piece are split where one of its tiles would be
+    // more than half of what each of 76 CTA pairs has to do in a launch.
+    const int64_t blocks_t = (a->Tp + 63) / 64, blocks_v = a->piece / 64, blocks_d = a->Dp / 64;
     const int64_t wide = (a->D + zl::kTileN - 1) / zl::kTileN;
-    const int64_t hidden = a->Tp / zl::kTileM * wide;
-    const int64_t weight = p->dweight ? a->piece / zl::kTileM * wide : 0;
+    const int64_t rows = a->Tp / zl::kTileM, cols = a->piece / zl::kTileN;
+    const int64_t work = rows * wide * blocks_v + (p->dweight ? cols * wide * blocks_t : 0) +
+                         (pieces > 1 ? rows * cols * blocks_d : 0);
     a->splits = 1;
-    while (a->splits < 16 && weight + a->splits * hidden < 4 * 76 && a->piece / (2 * a->splits) >= 512)
-      a->splits *= 2;
+    while (a->splits < 64 && blocks_v / a->splits > std::max<int64_t>(work / (2 * 76), 8)) a->splits *= 2;
     if (p->dhidden) a->dh = w.take<float>(a->splits * a->Tp, a->Dp);
     most = std::max(most, w.at);
   }
@@ -290,18 +300,23 @@ bool tensor_map(CUtensorMap* map, const void* base, int64_t cols, int64_t rows, 
 }
 
 // The operands, each once read along K (boxes of 128 rows) and once across it
-// (boxes of 64 rows of K).
+// (boxes of 64 rows of K); G also as it is written (boxes of a warp's 32 rows).
 struct Maps {
-  CUtensorMap hidden, hidden_mn, weight, weight_mn, g, g_mn;
+  CUtensorMap hidden, hidden_mn, weight, weight_mn, g[2], g_mn[2], g_out[2];
   bool make(const Args& a, bool backward) {
     bool ok = tensor_map(&hidden, a.hp, a.Dp, a.Tp, a.Dp, a.planes, a.Tp * a.Dp, 128);
     const int64_t wide = a.wp_plane ? a.Dp : a.D;
     ok = ok && tensor_map(&weight, a.wp, wide, a.V, a.wp_ld, a.planes, a.wp_plane, 128);
     if (!backward) return ok;
-    return ok && tensor_map(&hidden_mn, a.hp, a.Dp, a.Tp, a.Dp, a.planes, a.Tp * a.Dp, 64) &&
-           tensor_map(&weight_mn, a.wp, wide, a.V, a.wp_ld, a.planes, a.wp_plane, 64) &&
-           tensor_map(&g, a.g, a.piece, a.Tp, a.piece, a.planes, a.Tp * a.piece, 128) &&
-           tensor_map(&g_mn, a.g, a.piece, a.Tp, a.piece, a.planes, a.Tp * a.piece, 64);
+    ok = ok && tensor_map(&hidden_mn, a.hp, a.Dp, a.Tp, a.Dp, a.planes, a.Tp * a.Dp, 64) &&
+         tensor_map(&weight_mn, a.wp, wide, a.V, a.wp_ld, a.planes, a.wp_plane, 64);
+    for (int b = 0; b < 2; ++b) {
+      CUtensorMap* const to[3] = {&g[b], &g_mn[b], &g_out[b]};
+      const uint32_t box[3] = {128, 64, 32};
+      for (int i = 0; i < 3; ++i)
+        ok = ok && tensor_map(to[i], a.g[b], a.piece, a.Tp, a.piece, a.planes, a.Tp * a.piece, box[i]);
+    }
+    return ok;
   }
 };
 
@@ -312,7 +327,7 @@ Job logits_job(const Args& a, const Maps& maps, bool gradient, int64_t c0) {
   Job j{};
   j.a = maps.hidden;
   j.b = maps.weight;
-  if (gradient) j.out = maps.g;
+  if (gradient) j.out = maps.g_out[c0 / a.piece & 1];
   j.mode = gradient ? zl::kGradient : zl::kForward;
   j.n_tiles = tiles_of(cols);
   j.n_cols = int32_t(cols);
@@ -325,7 +340,7 @@ Job logits_job(const Args& a, const Maps& maps, bool gradient, int64_t c0) {
 
 Job hidden_job(const Args& a, const Maps& maps, int64_t c0) {
   Job j{};
-  j.a = maps.g;
+  j.a = maps.g[c0 / a.piece & 1];
   j.b = maps.weight_mn;
   j.mode = zl::kHidden;
   j.n_tiles = tiles_of(a.D);
@@ -341,7 +356,7 @@ Job hidden_job(const Args& a, const Maps& maps, int64_t c0) {
 Job weight_job(const Args& a, const Maps& maps, int64_t c0) {
   const int es = a.planes == 1 ? 2 : 4;
   Job j{};
-  j.a = maps.g_mn;
+  j.a = maps.g_mn[c0 / a.piece & 1];
   j.b = maps.hidden_mn;
   j.mode = zl::kWeight;
   j.m_tiles = tiles_of(std::min(a.piece, a.V - c0));
@@ -395,21 +410,23 @@ int run(const zero_head_loss_t* p, bool distill, int pass, cudaStream_t s) {
   if (packed) next("packing weight", [&] { return zl::launch_pack_weight(a, packed, s); });
   if (pass & kForward) {
     next("logits", [&] {
-      Jobs jobs{{logits_job(a, maps, false, 0)}, 1};
+      Jobs jobs{};
+      jobs.job[jobs.count++] = logits_job(a, maps, false, 0);
+      jobs.counter = a.counters;
       return zl::launch_products(a, jobs, sms, s);
     });
     next("losses", [&] { return zl::launch_losses(a, s); });
   }
   if (pass & kBackward) {
-    for (int64_t c0 = 0; c0 < a.V; c0 += a.piece) {
-      next("the logits' gradient", [&] {
-        Jobs jobs{{logits_job(a, maps, true, c0)}, 1};
-        return zl::launch_products(a, jobs, sms, s);
-      });
+    // Each launch takes one piece's two products and forms the next piece.
+    int64_t n = 1;
+    for (int64_t c0 = -a.piece; c0 < a.V; c0 += a.piece, ++n) {
       next("the gradients", [&] {
         Jobs jobs{};
-        if (p->dweight) jobs.job[jobs.count++] = weight_job(a, maps, c0);
-        if (p->dhidden) jobs.job[jobs.count++] = hidden_job(a, maps, c0);
+        if (c0 >= 0 && p->dweight) jobs.job[jobs.count++] = weight_job(a, maps, c0);
+        if (c0 >= 0 && p->dhidden) jobs.job[jobs.count++] = hidden_job(a, maps, c0);
+        if (c0 + a.piece < a.V) jobs.job[jobs.count++] = logits_job(a, maps, true, c0 + a.piece);
+        jobs.counter = a.counters + n;
         return zl::launch_products(a, jobs, sms, s);
       });
     }

@@ -81,7 +81,9 @@ struct Args {
   int64_t tiles;          // vocabulary tiles
   float2* stats;          // [2 tiles][Tp] half a tile's (m, sum of 2^(z log2(e) - m))
   float2* stats_tau;      // [2 tiles][Tp] of z / tau
-  __nv_bfloat16* g;       // [planes][Tp][piece] gradient of a piece's logits
+  int32_t* counters;      // [launches] tiles handed out
+  int64_t launches;
+  __nv_bfloat16* g[2];    // [planes][Tp][piece] gradients of two pieces' logits
   int64_t piece;          // columns of a piece, a multiple of kTileN
   int32_t splits;         // parts of a piece's columns that dhidden is summed in
   float* dh;              // [splits][Tp][Dp] running sums of dhidden over the pieces
@@ -105,9 +107,11 @@ struct Job {
   int64_t c0;        // the piece's first vocabulary column
 };
 
+// A launch's work, the longest tiles first.
 struct Jobs {
-  Job job[2];
+  Job job[3];
   int32_t count;
+  int32_t* counter;
 };
 
 cudaError_t launch_rows(const Args& a, cudaStream_t s);

@@ -150,6 +150,7 @@ __global__ void __launch_bounds__(1024) number_rows_kernel(const Args a) {
     base = all;
     __syncthreads();
   }
+  for (int64_t n = threadIdx.x; n < a.launches; n += 1024) a.counters[n] = 0;
   if (threadIdx.x == 0) {
     a.head->rows = base;
     a.head->ticket = 0;

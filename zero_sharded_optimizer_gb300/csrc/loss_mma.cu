@@ -13,10 +13,18 @@
 // Warps: 0 copies operand tiles by TMA into a ring of stages, 1 (of the pair's
 // first CTA) issues the products, 4..11 read finished accumulators from tensor
 // memory; two accumulators of 256 columns let the next tile's products run
-// under this tile's epilogue.
+// under this tile's epilogue. Tiles are handed out by a counter, the long ones
+// first: the pair's first copying thread takes a number and passes it to the
+// other warps of both CTAs through a small ring.
 //
 // fp32 storage: each operand is three bf16 parts and the products of the parts
 // are summed into one accumulator, smallest first, in six passes over K.
+//
+// The tensor cores' fp32 accumulators truncate: a chain of n additions of one
+// sign loses about n 2^-24 of the sum (measured: 1.4e-5 over K = 4096, where
+// fp32 additions that round lose 5e-8). Where the sum is kept in fp32 -- the
+// logits of the losses, everything of fp32 storage -- it is therefore taken in
+// segments of K, which the epilogue adds in registers with rounding.
 
 #include <cuda.h>
 #include <math.h>
@@ -34,13 +42,21 @@ constexpr int kBlockK = 64;        // elements of K a stage holds: 128 bytes
 constexpr int kHalf = 128;         // rows of A, and of B, that a CTA holds
 constexpr int kOperandBytes = kHalf * kBlockK * 2;
 constexpr int kStageBytes = 2 * kOperandBytes;
-constexpr int kBoxBytes = kHalf * 64 * 2;  // 128 rows x 64 columns of G on their way out
+
+constexpr int kWarpBox = 32 * 64 * 2;      // 32 rows x 64 columns of G on their way out
+constexpr int kRing = 4;                   // unit numbers on their way to the warps
+constexpr int kConsumers = 18;             // of a ring entry: 8 warps of each CTA, products, other copies
+constexpr int kRegsCopies = 88, kRegsEpilogue = 208;  // 128 x 88 + 256 x 208 = 384 x 168, the launch's
 
 template <int PLANES>
 struct Shape {
-  static constexpr int stages = PLANES == 1 ? 6 : 4;
-  static constexpr int boxes = 2 * PLANES;  // staging: one box per plane for each half of the columns
-  static constexpr int bytes = stages * kStageBytes + boxes * kBoxBytes + 1024 + 256;
+  static constexpr int stages = PLANES == 1 ? 5 : 3;
+  static constexpr int boxes = PLANES == 1 ? 2 : PLANES;  // of each epilogue warp
+  static constexpr int bytes = stages * kStageBytes + 8 * boxes * kWarpBox + 1024 + 512;
+  // 64-element blocks of K in a segment.
+  __host__ __device__ static constexpr int segment(Mode mode) {
+    return PLANES == 3 ? 8 : mode == kForward ? 16 : 1 << 24;
+  }
 };
 
 // ------------------------------------------------------------------- PTX --
@@ -125,21 +141,10 @@ __device__ __forceinline__ void tma_store(const CUtensorMap* map, uint32_t src, 
                "r"(src), "r"(x), "r"(y), "r"(z) : "memory");
 }
 __device__ __forceinline__ void store_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
-__device__ __forceinline__ void store_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 __device__ __forceinline__ void store_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 __device__ __forceinline__ void proxy_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-__device__ __forceinline__ void named_barrier(int id, int threads) {
-  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
-}
-
-// Over the eight epilogue warps.
-__device__ __forceinline__ bool all_agree(bool mine) {
-  uint32_t all;
-  asm volatile(
-      "{\n.reg .pred p, q;\nsetp.ne.u32 p, %1, 0;\n"
-      "barrier.cta.red.and.pred.aligned q, 3, 256, p;\n"
-      "selp.b32 %0, 1, 0, q;\n}" : "=r"(all) : "r"(uint32_t(mine)) : "memory");
-  return all != 0;
+__device__ __forceinline__ void store_remote(uint32_t cluster_addr, int32_t x) {
+  asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(cluster_addr), "r"(x) : "memory");
 }
 
 __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
@@ -170,6 +175,31 @@ __device__ __forceinline__ void tmem_load32(uint32_t addr, float (&v)[32]) {
         "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
         "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void tmem_load16(uint32_t addr, float (&v)[16]) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  __syncwarp();
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void tmem_store32(uint32_t addr, const float (&v)[32]) {
+  const uint32_t* r = reinterpret_cast<const uint32_t*>(v);
+  __syncwarp();
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};\n"
+      "tcgen05.wait::st.sync.aligned;" ::
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+      "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
+      "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(addr)
+      : "memory");
 }
 __device__ __forceinline__ float tmem_load1(uint32_t addr) {
   float v;
@@ -206,24 +236,26 @@ struct Unit {
   int n;              // columns of the product: up to 256, a multiple of 32
   int k0, blocks;     // first K element and number of 64-element blocks
   int split;
+  int segment, segments;  // blocks of a segment; number of segments (at least 1)
 };
 
 template <int PLANES>
-__device__ __forceinline__ bool unit_at(const Jobs& jobs, int rows, int64_t u, Unit* unit) {
+__device__ __forceinline__ bool unit_at(const Jobs& jobs, int rows, int32_t u, Unit* unit) {
   const int row_tiles = (rows + 255) / 256;
+  if (u < 0) return false;
   for (int j = 0; j < jobs.count; ++j) {
     const Job& job = jobs.job[j];
     const int mt = job.mode == kWeight ? job.m_tiles : row_tiles;
-    const int64_t all = int64_t(mt) * job.n_tiles * job.splits;
+    const int all = mt * job.n_tiles * job.splits;
     if (u >= all) {
       u -= all;
       continue;
     }
     unit->job = j;
-    const int64_t tile = u % (int64_t(mt) * job.n_tiles);
-    unit->split = int(u / (int64_t(mt) * job.n_tiles));
-    const int m = int(job.mode == kWeight ? tile / job.n_tiles : tile % mt);
-    const int n = int(job.mode == kWeight ? tile % job.n_tiles : tile / mt);
+    const int tile = u % (mt * job.n_tiles);
+    unit->split = u / (mt * job.n_tiles);
+    const int m = job.mode == kWeight ? tile / job.n_tiles : tile % mt;
+    const int n = job.mode == kWeight ? tile % job.n_tiles : tile / mt;
     unit->m0 = m * 256;
     unit->n0 = n * 256;
     unit->n = min(256, (job.n_cols - unit->n0 + 31) / 32 * 32);
@@ -232,6 +264,8 @@ __device__ __forceinline__ bool unit_at(const Jobs& jobs, int rows, int64_t u, U
     const int first = int(int64_t(blocks) * unit->split / job.splits);
     unit->k0 = first * kBlockK;
     unit->blocks = int(int64_t(blocks) * (unit->split + 1) / job.splits) - first;
+    unit->segment = Shape<PLANES>::segment(job.mode);
+    unit->segments = max(1, (unit->blocks + unit->segment - 1) / unit->segment);
     return true;
   }
   return false;
@@ -242,21 +276,42 @@ __device__ __forceinline__ bool unit_at(const Jobs& jobs, int rows, int64_t u, U
 struct Thread {          // of the epilogue
   int row;               // of the CTA's 128
   int half;              // columns [128 half, 128 half + 128)
-  uint32_t lane_addr;    // its quarter of the lanes, in the address's upper half
 };
 
-// A row of the logits: what the epilogues of kForward and kGradient need of it.
+// A row of the logits: what the epilogues of kForward and kGradient need of
+// it, read while the products are still running.
 struct Row {
-  int i;                 // compact row
+  int i;                   // compact row
   int64_t t;
   bool there;
+  int e;                   // its next sparse entry
+  int32_t id;
+  float scale, w_ce, w_kd, lse, lse_kd;  // kGradient
 };
 
-__device__ __forceinline__ Row row_of(const Args& a, int rows, const Unit& u, const Thread& th, uint32_t rank) {
-  Row r;
+template <bool CE, bool KD>
+__device__ __forceinline__ Row row_of(const Args& a, const Job& job, int rows, const Unit& u, const Thread& th,
+                                      uint32_t rank) {
+  Row r{};
   r.i = u.m0 + int(rank) * kHalf + th.row;
   r.there = r.i < rows;
-  r.t = r.there ? a.rowmap[r.i] : 0;
+  r.id = kNoId;
+  r.lse = r.lse_kd = INFINITY;
+  if (!r.there) return r;
+  r.t = a.rowmap[r.i];
+  if (job.mode == kGradient) {
+    const float2 f = a.coef[r.t];
+    // A term that the row does not have is 2^-inf = 0, whatever the accumulator holds.
+    if (CE && f.x != 0.0f) r.lse = a.lse[r.t];
+    if (KD && f.y != 0.0f) r.lse_kd = a.lse_tau[r.t];
+    r.scale = a.reduction == ZERO_REDUCE_NONE && a.dloss ? a.dloss[r.t] : 1.0f;
+    r.w_ce = f.x * r.scale;
+    r.w_kd = f.y * r.scale;
+  }
+  const int32_t* ids = a.ids + r.t * a.L;
+  r.e = a.L == 1 ? 0 : first_entry(ids, a.L, job.c0 + u.n0 + th.half * 128);
+  r.id = r.e < a.L ? ids[r.e] : kNoId;
+  if (r.id < job.c0 + u.n0 + th.half * 128) r.id = kNoId;
   return r;
 }
 
@@ -264,17 +319,16 @@ __device__ __forceinline__ Row row_of(const Args& a, int rows, const Unit& u, co
 // [begin, end) relative to v0, with the column's logit read from the
 // accumulator: all lanes of the warp read the same column, lowest first.
 template <typename F>
-__device__ __forceinline__ void each_entry(const int32_t* ids, int L, bool there, int& e, int32_t& id, int64_t v0,
-                                           int end, uint32_t acc, F f) {
+__device__ __forceinline__ void each_entry(const Args& a, Row& r, int64_t v0, int end, uint32_t acc, F f) {
   for (;;) {
-    const int mine = there && id < v0 + end ? int(id - v0) : 0x7fffffff;
+    const int mine = r.id < v0 + end ? int(r.id - v0) : 0x7fffffff;
     const int c = __reduce_min_sync(~0u, mine);
     if (c == 0x7fffffff) break;
     const float z = tmem_load1(acc + c);
     if (mine == c) {
-      f(e, c, z);
-      ++e;
-      id = e < L ? ids[e] : kNoId;
+      f(r.e, c, z);
+      ++r.e;
+      r.id = r.e < a.L ? a.ids[r.t * a.L + r.e] : kNoId;
     }
     __syncwarp();
   }
@@ -296,8 +350,8 @@ __device__ __forceinline__ void add_exponentials(const float (&z)[32], float top
 }
 
 template <bool CE, bool KD>
-__device__ __forceinline__ void forward_epilogue(const Args& a, const Unit& u, const Thread& th, const Row& r,
-                                                 uint32_t acc, int& e, int32_t& id) {
+__device__ __forceinline__ void forward_epilogue(const Args& a, const Unit& u, const Thread& th, Row& r,
+                                                 uint32_t acc) {
   const int64_t v0 = u.n0;
   const int begin = th.half * 128;
   const int cols = int(min(int64_t(256), a.V - v0));
@@ -325,8 +379,7 @@ __device__ __forceinline__ void forward_epilogue(const Args& a, const Unit& u, c
     if (CE) add_exponentials(z, top, c_ce, m_ce, sum);
     if (KD) add_exponentials(z, top, c_kd, m_kd, sum_kd);
   }
-  each_entry(a.ids + r.t * a.L, a.L, r.there, e, id, v0, begin + 128, acc,
-             [&](int k, int, float z) { a.zent[r.t * a.L + k] = z; });
+  each_entry(a, r, v0, begin + 128, acc, [&](int k, int, float z) { a.zent[r.t * a.L + k] = z; });
   if (!r.there) return;
   const int64_t at = (v0 / 256 * 2 + th.half) * a.Tp + r.i;
   const bool nan = isnan(sum + sum_kd);
@@ -334,84 +387,94 @@ __device__ __forceinline__ void forward_epilogue(const Args& a, const Unit& u, c
   if (KD) a.stats_tau[at] = make_float2(nan ? NAN : m_kd, sum_kd);
 }
 
+// Two neighbouring values of G as their words of the operand's parts.
+template <int PLANES>
+__device__ __forceinline__ void pack_parts(float x0, float x1, uint32_t (&word)[PLANES]) {
+  if (PLANES == 1) {
+    __nv_bfloat162 h = __floats2bfloat162_rn(x0, x1);
+    word[0] = *reinterpret_cast<uint32_t*>(&h);
+  } else {
+    __nv_bfloat16 p0[3], p1[3];
+    split(x0, p0);
+    split(x1, p1);
+#pragma unroll
+    for (int p = 0; p < PLANES; ++p)
+      word[p] = uint32_t(__bfloat16_as_ushort(p0[p])) | uint32_t(__bfloat16_as_ushort(p1[p])) << 16;
+  }
+}
+
 // The logits' gradient without the factor that all rows share, as the bf16
 // operand of the two products: rounded once (fp32 storage: in three parts).
+// Each warp stages boxes of its 32 rows by 64 columns and stores them by TMA.
 template <int PLANES, bool CE, bool KD>
 __device__ __forceinline__ void gradient_epilogue(const Args& a, const Job& job, const Unit& u, const Thread& th,
-                                                  const Row& r, uint32_t acc, uint32_t rank, uint8_t* staging,
-                                                  int& e, int32_t& id) {
+                                                  Row& r, uint32_t acc, uint32_t rank, uint8_t* staging) {
   const int64_t v0 = job.c0 + u.n0;
-  const int begin = th.half * 128;
+  const int begin = th.half * 128, lane = th.row & 31;
   const int cols = int(min(int64_t(256), a.V - v0));
-  const float2 f = r.there ? a.coef[r.t] : make_float2(0.0f, 0.0f);
-  const float scale = a.reduction == ZERO_REDUCE_NONE && a.dloss && r.there ? a.dloss[r.t] : 1.0f;
-  const float w_ce = f.x * scale, w_kd = f.y * scale;
-  // Terms that the row does not have are exp2(-inf) = 0, whatever the accumulator holds.
-  const float lse = CE && f.x != 0.0f ? a.lse[r.t] : INFINITY;
-  const float lse_kd = KD && f.y != 0.0f ? a.lse_tau[r.t] : INFINITY;
+  const float c_ce = kLog2e, c_kd = a.inv_tau * kLog2e;
+  const float m_ce = r.lse * kLog2e, m_kd = r.lse_kd * kLog2e;
   auto value = [&](float z) {
     float g = 0.0f;
-    if (CE) g = w_ce * exp2_fast((z - lse) * kLog2e);
-    if (KD) g = fmaf(w_kd, exp2_fast(fmaf(z, a.inv_tau, -lse_kd) * kLog2e), g);
+    if (PLANES == 1) {
+      if (CE) g = r.w_ce * exp2_fast(fmaf(z, c_ce, -m_ce));
+      if (KD) g = fmaf(r.w_kd, exp2_fast(fmaf(z, c_kd, -m_kd)), g);
+    } else {  // the difference first: its rounding is relative to it, not to the logit
+      if (CE) g = r.w_ce * exp2_fast((z - r.lse) * kLog2e);
+      if (KD) g = fmaf(r.w_kd, exp2_fast(fmaf(z, a.inv_tau, -r.lse_kd) * kLog2e), g);
+    }
     return g;
   };
-  uint8_t* box = staging + th.half * PLANES * kBoxBytes;
-  const int issuer = (th.row == 0);
 #pragma unroll 1
   for (int b = 0; b < 2; ++b) {
-    if (issuer) store_wait_read();
-    named_barrier(1 + th.half, 128);
+    uint8_t* box = staging + (PLANES == 1 ? b * kWarpBox : 0);
+    // The box's last store has read it (bf16: it was issued before the last one).
+    if (lane == 0) {
+      if (PLANES == 1) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+      else asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+    }
+    __syncwarp();
 #pragma unroll 1
     for (int k = 0; k < 2; ++k) {
       const int c0 = begin + 64 * b + 32 * k;
       float z[32];
       tmem_load32(acc + c0, z);
-      const int valid = r.there ? cols - c0 : 0;
+      const int valid = cols - c0;
+#pragma unroll
+      for (int j = 0; j < 32; ++j) z[j] = value(z[j]);
+      if (valid < 32) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          if (j >= valid) z[j] = 0.0f;
+      }
 #pragma unroll
       for (int j = 0; j < 32; j += 8) {
-        uint32_t word[PLANES][4];
+        uint32_t word[4][PLANES];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const float x0 = j + 2 * q < valid ? value(z[j + 2 * q]) : 0.0f;
-          const float x1 = j + 2 * q + 1 < valid ? value(z[j + 2 * q + 1]) : 0.0f;
-          if (PLANES == 1) {
-            __nv_bfloat162 h = __floats2bfloat162_rn(x0, x1);
-            word[0][q] = *reinterpret_cast<uint32_t*>(&h);
-          } else {
-            __nv_bfloat16 p0[3], p1[3];
-            split(x0, p0);
-            split(x1, p1);
-#pragma unroll
-            for (int p = 0; p < PLANES; ++p)
-              word[p][q] = uint32_t(__bfloat16_as_ushort(p0[p])) | uint32_t(__bfloat16_as_ushort(p1[p])) << 16;
-          }
-        }
-        const int chunk = (4 * k + j / 8) ^ (th.row & 7);
+        for (int q = 0; q < 4; ++q) pack_parts<PLANES>(z[j + 2 * q], z[j + 2 * q + 1], word[q]);
+        const int chunk = (4 * k + j / 8) ^ (lane & 7);
 #pragma unroll
         for (int p = 0; p < PLANES; ++p)
-          *reinterpret_cast<uint4*>(box + p * kBoxBytes + th.row * 128 + chunk * 16) =
-              make_uint4(word[p][0], word[p][1], word[p][2], word[p][3]);
+          *reinterpret_cast<uint4*>(box + p * kWarpBox + lane * 128 + chunk * 16) =
+              make_uint4(word[0][p], word[1][p], word[2][p], word[3][p]);
       }
     }
-    each_entry(a.ids + r.t * a.L, a.L, r.there, e, id, v0, begin + 64 * (b + 1), acc, [&](int k, int c, float z) {
-      const float g = value(z) - scale * a.weights[r.t * a.L + k];
+    each_entry(a, r, v0, begin + 64 * (b + 1), acc, [&](int k, int c, float z) {
+      const float g = value(z) - r.scale * a.weights[r.t * a.L + k];
       const int at = c - begin - 64 * b;
-      uint8_t* to = box + th.row * 128 + (((at / 8) ^ (th.row & 7)) * 16) + (at % 8) * 2;
-      if (PLANES == 1) {
-        *reinterpret_cast<__nv_bfloat16*>(to) = __float2bfloat16_rn(g);
-      } else {
-        __nv_bfloat16 part[3];
-        split(g, part);
+      uint8_t* to = box + lane * 128 + (((at / 8) ^ (lane & 7)) * 16) + (at % 8) * 2;
+      uint32_t word[PLANES];
+      pack_parts<PLANES>(g, 0.0f, word);
 #pragma unroll
-        for (int p = 0; p < PLANES; ++p) *reinterpret_cast<__nv_bfloat16*>(to + p * kBoxBytes) = part[p];
-      }
+      for (int p = 0; p < PLANES; ++p) *reinterpret_cast<uint16_t*>(to + p * kWarpBox) = uint16_t(word[p]);
     });
     proxy_fence();
-    named_barrier(1 + th.half, 128);
-    if (issuer) {
+    __syncwarp();
+    if (lane == 0) {
 #pragma unroll
       for (int p = 0; p < PLANES; ++p)
-        tma_store(&job.out, smem_u32(box + p * kBoxBytes), u.n0 + begin + 64 * b, u.m0 + int(rank) * kHalf, p);
+        tma_store(&job.out, smem_u32(box + p * kWarpBox), u.n0 + begin + 64 * b,
+                  u.m0 + int(rank) * kHalf + th.row, p);
       store_commit();
     }
   }
@@ -494,12 +557,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   uint8_t* staging = base + kStages * kStageBytes;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(staging + Shape<PLANES>::boxes * kBoxBytes);
-  // barriers: stage full [kStages], stage empty [kStages], accumulator full [2], empty [2]
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kStages + 4);
-  volatile uint32_t* given_up = tmem_slot + 1;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(staging + 8 * Shape<PLANES>::boxes * kWarpBox);
+  // Barriers: stage full and empty, accumulator full and empty, ring full and empty.
   const uint32_t full = smem_u32(bars), empty = full + 8 * kStages, acc_full = empty + 8 * kStages,
-                 acc_empty = acc_full + 16;
+                 acc_empty = acc_full + 16, ring_full = acc_empty + 16, ring_empty = ring_full + 8 * kRing;
+  volatile int32_t* ring = reinterpret_cast<int32_t*>(bars + 2 * kStages + 4 + 2 * kRing);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kStages + 4 + 2 * kRing) + kRing;
+  volatile uint32_t* given_up = tmem_slot + 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
 
@@ -511,6 +575,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     for (int b = 0; b < 2; ++b) {
       barrier_init(acc_full + 8 * b, 1);
       barrier_init(acc_empty + 8 * b, 16);  // eight warps of each CTA
+    }
+    for (int q = 0; q < kRing; ++q) {
+      barrier_init(ring_full + 8 * q, 1);
+      barrier_init(ring_empty + 8 * q, kConsumers);
     }
     *given_up = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -527,127 +595,162 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tmem_slot;
   const int rows = a.head->rows;
   const Waiter wait{given_up, a.head};
-  const int64_t first = blockIdx.x / 2, step = gridDim.x / 2;
   Unit u;
+  // The ring's next entry, for one thread of a consumer: waits for it, reads
+  // it, and gives it back to the pair's first CTA.
+  int slot = 0;
+  uint32_t slot_phase = 0;
+  const uint32_t ring_empty0 = in_cta(ring_empty, 0);
+  auto next_unit = [&](int32_t* n) {
+    if (!wait(ring_full + 8 * slot, slot_phase)) return false;
+    *n = ring[slot];
+    barrier_arrive_remote(ring_empty0 + 8 * slot);
+    if (++slot == kRing) {
+      slot = 0;
+      slot_phase ^= 1;
+    }
+    return true;
+  };
 
-  if (warp == 0) {
-    // ---- copies
-    if (elect_one()) {
-      const uint32_t full0 = in_cta(full, 0);
-      int stage = 0;
-      uint32_t phase = 0;
-      bool ok = true;
-      for (int64_t n = first; ok && unit_at<PLANES>(jobs, rows, n, &u); n += step) {
-        const Job& job = jobs.job[u.job];
-        const bool a_mn = job.mode == kWeight, b_mn = job.mode == kWeight || job.mode == kHidden;
-        const int am = u.m0 + int(rank) * kHalf, bn = u.n0 + int(rank) * (u.n / 2);
-        const int b_boxes = b_mn ? (u.n / 2 + 63) / 64 : 0;
-        const uint32_t bytes = 2 * (kOperandBytes + (b_mn ? b_boxes * 64 * kBlockK * 2 : kOperandBytes));
-        for (int term = 0; ok && term < kTerms; ++term) {
-          const int pa = kTerms == 1 ? 0 : kTermA[term], pb = kTerms == 1 ? 0 : kTermB[term];
-          for (int k = 0; k < u.blocks; ++k) {
-            if (!(ok = wait(empty + 8 * stage, phase ^ 1))) break;
-            const uint32_t sa = smem_u32(base + stage * kStageBytes), sb = sa + kOperandBytes;
-            const uint32_t bar = full0 + 8 * stage;
-            if (rank == 0) barrier_expect(full + 8 * stage, bytes);
-            const int kk = u.k0 + k * kBlockK;
-            if (a_mn) {
-              tma_load(sa, &job.a, am, kk, pa, bar);
-              tma_load(sa + 64 * kBlockK * 2, &job.a, am + 64, kk, pa, bar);
-            } else {
-              tma_load(sa, &job.a, kk, am, pa, bar);
-            }
-            if (b_mn) {
-              for (int c = 0; c < b_boxes; ++c)
-                tma_load(sb + c * 64 * kBlockK * 2, &job.b, bn + 64 * c, kk + job.b_k0, pb, bar);
-            } else {
-              tma_load(sb, &job.b, kk, bn + job.b_row0, pb, bar);
-            }
-            if (++stage == kStages) {
-              stage = 0;
-              phase ^= 1;
+  if (warp < kEpilogueWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsCopies));
+    if (warp == 0) {
+      // ---- copies
+      if (elect_one()) {
+        const uint32_t full0 = in_cta(full, 0);
+        int stage = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        int32_t n = int32_t(blockIdx.x / 2);
+        // Passes a number to both CTAs' warps (first CTA's thread alone).
+        auto publish = [&](int32_t x) {
+          if (!wait(ring_empty + 8 * slot, slot_phase ^ 1)) return false;
+          for (uint32_t c = 0; c < 2; ++c) {
+            store_remote(in_cta(smem_u32(const_cast<int32_t*>(ring) + slot), c), x);
+            barrier_arrive_remote(in_cta(ring_full + 8 * slot, c));
+          }
+          if (++slot == kRing) {
+            slot = 0;
+            slot_phase ^= 1;
+          }
+          return true;
+        };
+        if (rank == 0) ok = publish(unit_at<PLANES>(jobs, rows, n, &u) ? n : -1);
+        else ok = next_unit(&n);
+        while (ok && unit_at<PLANES>(jobs, rows, n, &u)) {
+          int32_t next = 0;
+          if (rank == 0) next = int32_t(gridDim.x / 2) + atomicAdd(jobs.counter, 1);
+          const Job& job = jobs.job[u.job];
+          const bool a_mn = job.mode == kWeight, b_mn = job.mode == kWeight || job.mode == kHidden;
+          const int am = u.m0 + int(rank) * kHalf, bn = u.n0 + int(rank) * (u.n / 2);
+          const int b_boxes = b_mn ? (u.n / 2 + 63) / 64 : 0;
+          const uint32_t bytes = 2 * (kOperandBytes + (b_mn ? b_boxes * 64 * kBlockK * 2 : kOperandBytes));
+          for (int s = 0; ok && s < u.segments; ++s) {
+            const int k_begin = s * u.segment, k_end = min(u.blocks, k_begin + u.segment);
+            for (int term = 0; ok && term < kTerms; ++term) {
+              const int pa = kTerms == 1 ? 0 : kTermA[term], pb = kTerms == 1 ? 0 : kTermB[term];
+              for (int k = k_begin; k < k_end; ++k) {
+                if (!(ok = wait(empty + 8 * stage, phase ^ 1))) break;
+                const uint32_t sa = smem_u32(base + stage * kStageBytes), sb = sa + kOperandBytes;
+                const uint32_t bar = full0 + 8 * stage;
+                if (rank == 0) barrier_expect(full + 8 * stage, bytes);
+                const int kk = u.k0 + k * kBlockK;
+                if (a_mn) {
+                  tma_load(sa, &job.a, am, kk, pa, bar);
+                  tma_load(sa + 64 * kBlockK * 2, &job.a, am + 64, kk, pa, bar);
+                } else {
+                  tma_load(sa, &job.a, kk, am, pa, bar);
+                }
+                if (b_mn) {
+                  for (int c = 0; c < b_boxes; ++c)
+                    tma_load(sb + c * 64 * kBlockK * 2, &job.b, bn + 64 * c, kk + job.b_k0, pb, bar);
+                } else {
+                  tma_load(sb, &job.b, kk, bn + job.b_row0, pb, bar);
+                }
+                if (++stage == kStages) {
+                  stage = 0;
+                  phase ^= 1;
+                }
+              }
             }
           }
+          if (!ok) break;
+          if (rank == 0) {
+            n = unit_at<PLANES>(jobs, rows, next, &u) ? next : -1;
+            ok = publish(n);
+          } else {
+            ok = next_unit(&n);
+          }
+        }
+        if (!ok) {  // let the copies in flight land before the CTA's memory goes
+          const uint64_t begin = timer_ns();
+          while (timer_ns() - begin < 2000000) __nanosleep(1000);
         }
       }
-      if (!ok) {  // let the copies in flight land before the CTA's memory goes
-        const uint64_t begin = timer_ns();
-        while (timer_ns() - begin < 2000000) __nanosleep(1000);
-      }
-    }
-  } else if (warp == 1 && rank == 0) {
-    // ---- products
-    if (elect_one()) {
-      int stage = 0;
-      uint32_t phase = 0, acc_phase = 0;
-      int buffer = 0;
-      bool ok = true;
-      for (int64_t n = first; ok && unit_at<PLANES>(jobs, rows, n, &u); n += step) {
-        const Job& job = jobs.job[u.job];
-        const bool a_mn = job.mode == kWeight, b_mn = job.mode == kWeight || job.mode == kHidden;
-        // fp32 accumulator, bf16 operands, majors, N, M = 256
-        const uint32_t idesc = 1u << 4 | 1u << 7 | 1u << 10 | uint32_t(a_mn) << 15 | uint32_t(b_mn) << 16 |
-                               uint32_t(u.n / 8) << 17 | uint32_t(256 / 16) << 24;
-        const uint64_t a_step = (a_mn ? 16 * 128 : 32) >> 4, b_step = (b_mn ? 16 * 128 : 32) >> 4;
-        const uint32_t d = tmem + buffer * 256;
-        if (!(ok = wait(acc_empty + 8 * buffer, acc_phase ^ 1))) break;
-        fence_after();
-        bool add = false;
-        for (int k = 0; k < u.blocks * kTerms; ++k) {
-          if (!(ok = wait(full + 8 * stage, phase))) break;
-          fence_after();
-          const uint32_t sa = smem_u32(base + stage * kStageBytes);
-          const uint64_t da = operand_desc(sa, a_mn), db = operand_desc(sa + kOperandBytes, b_mn);
+    } else if (warp == 1 && rank == 0) {
+      // ---- products
+      if (elect_one()) {
+        int stage = 0;
+        uint32_t phase = 0, acc_phase = 0;
+        int buffer = 0;
+        int32_t n;
+        bool ok = true;
+        while (ok && next_unit(&n) && unit_at<PLANES>(jobs, rows, n, &u)) {
+          const Job& job = jobs.job[u.job];
+          const bool a_mn = job.mode == kWeight, b_mn = job.mode == kWeight || job.mode == kHidden;
+          // fp32 accumulator, bf16 operands, majors, N, M = 256
+          const uint32_t idesc = 1u << 4 | 1u << 7 | 1u << 10 | uint32_t(a_mn) << 15 | uint32_t(b_mn) << 16 |
+                                 uint32_t(u.n / 8) << 17 | uint32_t(256 / 16) << 24;
+          const uint64_t a_step = (a_mn ? 16 * 128 : 32) >> 4, b_step = (b_mn ? 16 * 128 : 32) >> 4;
+          for (int s = 0; ok && s < u.segments; ++s) {
+            const uint32_t d = tmem + buffer * 256;
+            if (!(ok = wait(acc_empty + 8 * buffer, acc_phase ^ 1))) break;
+            fence_after();
+            bool add = false;
+            const int count = (min(u.blocks, (s + 1) * u.segment) - s * u.segment) * kTerms;
+            for (int k = 0; k < count; ++k) {
+              if (!(ok = wait(full + 8 * stage, phase))) break;
+              fence_after();
+              const uint32_t sa = smem_u32(base + stage * kStageBytes);
+              const uint64_t da = operand_desc(sa, a_mn), db = operand_desc(sa + kOperandBytes, b_mn);
 #pragma unroll
-          for (int q = 0; q < kBlockK / 16; ++q) {
-            mma(d, da + q * a_step, db + q * b_step, idesc, add);
-            add = true;
+              for (int q = 0; q < kBlockK / 16; ++q) {
+                mma(d, da + q * a_step, db + q * b_step, idesc, add);
+                add = true;
+              }
+              mma_commit(empty + 8 * stage);
+              if (++stage == kStages) {
+                stage = 0;
+                phase ^= 1;
+              }
+            }
+            mma_commit(acc_full + 8 * buffer);
+            if (++buffer == 2) {
+              buffer = 0;
+              acc_phase ^= 1;
+            }
           }
-          mma_commit(empty + 8 * stage);
-          if (++stage == kStages) {
-            stage = 0;
-            phase ^= 1;
-          }
-        }
-        mma_commit(acc_full + 8 * buffer);
-        if (++buffer == 2) {
-          buffer = 0;
-          acc_phase ^= 1;
         }
       }
     }
-  } else if (warp >= kEpilogueWarp) {
+  } else {
     // ---- epilogues
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsEpilogue));
     Thread th;
     th.row = (warp & 3) * 32 + lane;
     th.half = (warp - kEpilogueWarp) / 4;
-    th.lane_addr = uint32_t((warp & 3) * 32) << 16;
+    uint8_t* boxes = staging + (warp - kEpilogueWarp) * Shape<PLANES>::boxes * kWarpBox;
+    const uint32_t lanes = tmem + (uint32_t((warp & 3) * 32) << 16);
     const uint32_t acc_empty0 = in_cta(acc_empty, 0);
     const float factor = grad_factor(a);
     int buffer = 0;
     uint32_t phase = 0;
-    for (int64_t n = first; unit_at<PLANES>(jobs, rows, n, &u); n += step) {
-      const Job& job = jobs.job[u.job];
-      const uint32_t acc = tmem + th.lane_addr + buffer * 256;
-      Row r{};
-      int e = 0;
-      int32_t id = kNoId;
-      if (job.mode == kForward || job.mode == kGradient) {
-        r = row_of(a, rows, u, th, rank);
-        if (r.there) {
-          const int32_t* ids = a.ids + r.t * a.L;
-          e = first_entry(ids, a.L, job.c0 + u.n0 + th.half * 128);
-          id = e < a.L ? ids[e] : kNoId;
-        }
-      }
-      // The eight warps go on together, or none does: they meet at barriers below.
-      if (!all_agree(wait(acc_full + 8 * buffer, phase))) break;
+    auto full_accumulator = [&] {
+      if (!wait(acc_full + 8 * buffer, phase)) return false;
       fence_after();
-      if (job.mode == kForward) forward_epilogue<CE, KD>(a, u, th, r, acc, e, id);
-      else if (job.mode == kGradient)
-        gradient_epilogue<PLANES, CE, KD>(a, job, u, th, r, acc, rank, staging, e, id);
-      else if (job.mode == kHidden) hidden_epilogue(a, job, u, th, rows, acc, rank);
-      else weight_epilogue<PLANES>(a, job, u, th, factor, acc, rank);
+      return true;
+    };
+    auto give_back = [&] {
       fence_before();
       __syncwarp();
       if (lane == 0) barrier_arrive_remote(acc_empty0 + 8 * buffer);
@@ -655,8 +758,49 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         buffer = 0;
         phase ^= 1;
       }
+    };
+    for (;;) {
+      int32_t n = -1;
+      if (lane == 0 && !next_unit(&n)) n = -1;
+      n = __shfl_sync(~0u, n, 0);
+      if (!unit_at<PLANES>(jobs, rows, n, &u)) break;
+      const Job& job = jobs.job[u.job];
+      const bool logits = job.mode == kForward || job.mode == kGradient;
+      Row r{};
+      bool ok = true;
+      if (u.segments == 1) {
+        if (logits) r = row_of<CE, KD>(a, job, rows, u, th, rank);
+        ok = __all_sync(~0u, full_accumulator());
+      } else {
+        const int begin = th.half * 128;
+        float sum[4][32] = {};
+        for (int s = 0; ok && s < u.segments; ++s) {
+          if (!(ok = __all_sync(~0u, full_accumulator()))) break;
+          const uint32_t acc = lanes + buffer * 256 + begin;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            float x[16];
+            tmem_load16(acc + 16 * k, x);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) sum[k / 2][k % 2 * 16 + j] += x[j];
+          }
+          if (s == u.segments - 1) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) tmem_store32(acc + 32 * k, sum[k]);
+          }
+          if (s < u.segments - 1) give_back();
+        }
+        if (logits) r = row_of<CE, KD>(a, job, rows, u, th, rank);
+      }
+      if (!ok) break;
+      const uint32_t acc = lanes + buffer * 256;
+      if (job.mode == kForward) forward_epilogue<CE, KD>(a, u, th, r, acc);
+      else if (job.mode == kGradient) gradient_epilogue<PLANES, CE, KD>(a, job, u, th, r, acc, rank, boxes);
+      else if (job.mode == kHidden) hidden_epilogue(a, job, u, th, rows, acc, rank);
+      else weight_epilogue<PLANES>(a, job, u, th, factor, acc, rank);
+      give_back();
     }
-    if (th.row == 0) store_wait();
+    if (lane == 0) store_wait();
   }
   __syncwarp();
   fence_before();
@@ -670,8 +814,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 template <int PLANES, bool CE, bool KD>
 cudaError_t launch(const Args& a, const Jobs& jobs, int sms, cudaStream_t s) {
   auto* kernel = products_kernel<PLANES, CE, KD>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<PLANES>::bytes);
-  if (e != cudaSuccess) return e;
+  // The register shares of the warps must not exceed what the launch brings.
+  static const cudaError_t ready = [&] {
+    cudaFuncAttributes at;
+    cudaError_t e = cudaFuncGetAttributes(&at, kernel);
+    if (e != cudaSuccess) return e;
+    if (at.numRegs * kThreads < 128 * kRegsCopies + 256 * kRegsEpilogue) return cudaErrorLaunchOutOfResources;
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<PLANES>::bytes);
+  }();
+  if (ready != cudaSuccess) return ready;
   kernel<<<unsigned(sms / 2 * 2), kThreads, Shape<PLANES>::bytes, s>>>(a, jobs);
   return cudaGetLastError();
 }
