@@ -14,8 +14,10 @@
 // first CTA) issues the products, 4..11 read finished accumulators from tensor
 // memory; two accumulators of 256 columns let the next tile's products run
 // under this tile's epilogue. Tiles are handed out by a counter, the long ones
-// first: the pair's first copying thread takes a number and passes it to the
-// other warps of both CTAs through a small ring.
+// first: warp 2 of the pair's first CTA takes a number, works out what it
+// stands for and passes that to the other warps of both CTAs through a small
+// ring, ahead of their need (worked out by the copying thread itself, between
+// two tiles, it held the copies up: 26 % on a forward pass of width 768).
 //
 // fp32 storage: each operand is three bf16 parts and the products of the parts
 // are summed into one accumulator, smallest first, in six passes over K.
@@ -44,8 +46,7 @@ constexpr int kOperandBytes = kHalf * kBlockK * 2;
 constexpr int kStageBytes = 2 * kOperandBytes;
 
 constexpr int kWarpBox = 32 * 64 * 2;      // 32 rows x 64 columns of G on their way out
-constexpr int kRing = 4;                   // unit numbers on their way to the warps
-constexpr int kConsumers = 18;             // of a ring entry: 8 warps of each CTA, products, other copies
+constexpr int kRing = 3;                   // units on their way to the warps
 constexpr int kRegsCopies = 88, kRegsEpilogue = 208;  // 128 x 88 + 256 x 208 = 384 x 168, the launch's
 
 template <int PLANES>
@@ -97,13 +98,22 @@ __device__ __forceinline__ void barrier_expect(uint32_t bar, uint32_t bytes) {
 __device__ __forceinline__ void barrier_arrive_remote(uint32_t cluster_bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
+// `Cluster`: the wait also orders memory that threads of the other CTA wrote.
+template <bool Cluster>
 __device__ __forceinline__ bool barrier_try(uint32_t bar, uint32_t parity) {
   uint32_t ok;
-  asm volatile(
-      "{\n.reg .pred p;\n"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
-      "selp.b32 %0, 1, 0, p;\n}"
-      : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+  if (Cluster)
+    asm volatile(
+        "{\n.reg .pred p;\n"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+        "selp.b32 %0, 1, 0, p;\n}"
+        : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+  else
+    asm volatile(
+        "{\n.reg .pred p;\n"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+        "selp.b32 %0, 1, 0, p;\n}"
+        : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
   return ok != 0;
 }
 
@@ -115,11 +125,12 @@ constexpr uint64_t kWaitLimitNs = 10ull * 1000 * 1000 * 1000;
 struct Waiter {
   volatile uint32_t* given_up;  // shared
   Head* head;
+  template <bool Cluster = false>
   __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity) const {
-    if (barrier_try(bar, parity)) return true;
+    if (barrier_try<Cluster>(bar, parity)) return true;
     const uint64_t begin = timer_ns();
     for (uint32_t n = 1;; ++n) {
-      if (barrier_try(bar, parity)) return true;
+      if (barrier_try<Cluster>(bar, parity)) return true;
       if ((n & 63) == 0 && (*given_up || timer_ns() - begin > kWaitLimitNs)) {
         *given_up = 1;
         head->fault = 1;
@@ -143,8 +154,9 @@ __device__ __forceinline__ void tma_store(const CUtensorMap* map, uint32_t src, 
 __device__ __forceinline__ void store_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void store_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 __device__ __forceinline__ void proxy_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-__device__ __forceinline__ void store_remote(uint32_t cluster_addr, int32_t x) {
-  asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(cluster_addr), "r"(x) : "memory");
+__device__ __forceinline__ void store_remote(uint32_t cluster_addr, int4 x) {
+  asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(cluster_addr), "r"(x.x), "r"(x.y),
+               "r"(x.z), "r"(x.w) : "memory");
 }
 
 __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
@@ -231,18 +243,23 @@ __device__ constexpr int kTermA[6] = {0, 1, 2, 0, 1, 0};
 __device__ constexpr int kTermB[6] = {2, 1, 0, 1, 0, 0};
 
 struct Unit {
-  int job;
+  int job;            // negative: no more
   int m0, n0;         // first row and column of the pair's tile
   int n;              // columns of the product: up to 256, a multiple of 32
   int k0, blocks;     // first K element and number of 64-element blocks
   int split;
-  int segment, segments;  // blocks of a segment; number of segments (at least 1)
+  int segments;       // of segment() blocks each
 };
 
+// A unit without terms (no rows, or an empty split) still goes through one
+// block, whose product the epilogue does not read: blocks is negative.
+__device__ __forceinline__ int blocks_of(const Unit& u) { return u.blocks < 0 ? 1 : u.blocks; }
+
 template <int PLANES>
-__device__ __forceinline__ bool unit_at(const Jobs& jobs, int rows, int32_t u, Unit* unit) {
+__device__ __forceinline__ Unit unit_at(const Jobs& jobs, int rows, int32_t u) {
   const int row_tiles = (rows + 255) / 256;
-  if (u < 0) return false;
+  Unit unit{};
+  unit.job = -1;
   for (int j = 0; j < jobs.count; ++j) {
     const Job& job = jobs.job[j];
     const int mt = job.mode == kWeight ? job.m_tiles : row_tiles;
@@ -251,24 +268,25 @@ __device__ __forceinline__ bool unit_at(const Jobs& jobs, int rows, int32_t u, U
       u -= all;
       continue;
     }
-    unit->job = j;
     const int tile = u % (mt * job.n_tiles);
-    unit->split = u / (mt * job.n_tiles);
+    unit.split = u / (mt * job.n_tiles);
     const int m = job.mode == kWeight ? tile / job.n_tiles : tile % mt;
     const int n = job.mode == kWeight ? tile % job.n_tiles : tile / mt;
-    unit->m0 = m * 256;
-    unit->n0 = n * 256;
-    unit->n = min(256, (job.n_cols - unit->n0 + 31) / 32 * 32);
+    unit.job = j;
+    unit.m0 = m * 256;
+    unit.n0 = n * 256;
+    unit.n = min(256, (job.n_cols - unit.n0 + 31) / 32 * 32);
     const int depth = job.mode == kWeight ? rows : job.depth;
     const int blocks = (depth + kBlockK - 1) / kBlockK;
-    const int first = int(int64_t(blocks) * unit->split / job.splits);
-    unit->k0 = first * kBlockK;
-    unit->blocks = int(int64_t(blocks) * (unit->split + 1) / job.splits) - first;
-    unit->segment = Shape<PLANES>::segment(job.mode);
-    unit->segments = max(1, (unit->blocks + unit->segment - 1) / unit->segment);
-    return true;
+    const int first = int(int64_t(blocks) * unit.split / job.splits);
+    unit.k0 = first * kBlockK;
+    unit.blocks = int(int64_t(blocks) * (unit.split + 1) / job.splits) - first;
+    if (unit.blocks == 0) unit.blocks = -1;
+    const int segment = Shape<PLANES>::segment(job.mode);
+    unit.segments = (blocks_of(unit) + segment - 1) / segment;
+    break;
   }
-  return false;
+  return unit;
 }
 
 // --------------------------------------------------------------- epilogues --
@@ -488,7 +506,7 @@ __device__ __forceinline__ void hidden_epilogue(const Args& a, const Job& job, c
   float* to = a.dh + (int64_t(u.split) * a.Tp + i) * a.Dp + u.n0;
   for (int c = th.half * 128; c < min(u.n, th.half * 128 + 128); c += 32) {
     float x[32];
-    if (u.blocks) {
+    if (u.blocks > 0) {
       tmem_load32(acc + c, x);
     } else {
 #pragma unroll
@@ -514,7 +532,7 @@ __device__ __forceinline__ void weight_epilogue(const Args& a, const Job& job, c
   T* to = static_cast<T*>(a.dweight) + v * a.dweight_stride + u.n0;
   for (int c = th.half * 128; c < min(u.n, th.half * 128 + 128); c += 32) {
     float x[32];
-    if (u.blocks) {
+    if (u.blocks > 0) {
       tmem_load32(acc + c, x);
     } else {
 #pragma unroll
@@ -561,8 +579,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   // Barriers: stage full and empty, accumulator full and empty, ring full and empty.
   const uint32_t full = smem_u32(bars), empty = full + 8 * kStages, acc_full = empty + 8 * kStages,
                  acc_empty = acc_full + 16, ring_full = acc_empty + 16, ring_empty = ring_full + 8 * kRing;
-  volatile int32_t* ring = reinterpret_cast<int32_t*>(bars + 2 * kStages + 4 + 2 * kRing);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kStages + 4 + 2 * kRing) + kRing;
+  int4* ring = reinterpret_cast<int4*>(bars + 2 * kStages + 4 + 2 * kRing);
+  static_assert((2 * kStages + 4 + 2 * kRing) % 2 == 0, "the ring is read 16 bytes at a time");
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ring + 2 * kRing);
   volatile uint32_t* given_up = tmem_slot + 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
@@ -578,7 +597,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     for (int q = 0; q < kRing; ++q) {
       barrier_init(ring_full + 8 * q, 1);
-      barrier_init(ring_empty + 8 * q, kConsumers);
+      barrier_init(ring_empty + 8 * q, 16);
     }
     *given_up = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -596,15 +615,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int rows = a.head->rows;
   const Waiter wait{given_up, a.head};
   Unit u;
-  // The ring's next entry, for one thread of a consumer: waits for it, reads
-  // it, and gives it back to the pair's first CTA.
+  // The ring's next entry. The epilogue warps give it back to the pair's first
+  // CTA once the unit's first accumulator is full: by then the copies and the
+  // products have read it too. (Arrivals of theirs, across the pair, cost the
+  // forward pass of width 768 a further 13 %.)
   int slot = 0;
   uint32_t slot_phase = 0;
-  const uint32_t ring_empty0 = in_cta(ring_empty, 0);
-  auto next_unit = [&](int32_t* n) {
-    if (!wait(ring_full + 8 * slot, slot_phase)) return false;
-    *n = ring[slot];
-    barrier_arrive_remote(ring_empty0 + 8 * slot);
+  auto next_unit = [&] {
+    if (!wait.operator()<true>(ring_full + 8 * slot, slot_phase)) return false;
+    const int4 x = ring[2 * slot], y = ring[2 * slot + 1];
+    u = Unit{x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
     if (++slot == kRing) {
       slot = 0;
       slot_phase ^= 1;
@@ -621,32 +641,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         int stage = 0;
         uint32_t phase = 0;
         bool ok = true;
-        int32_t n = int32_t(blockIdx.x / 2);
-        // Passes a number to both CTAs' warps (first CTA's thread alone).
-        auto publish = [&](int32_t x) {
-          if (!wait(ring_empty + 8 * slot, slot_phase ^ 1)) return false;
-          for (uint32_t c = 0; c < 2; ++c) {
-            store_remote(in_cta(smem_u32(const_cast<int32_t*>(ring) + slot), c), x);
-            barrier_arrive_remote(in_cta(ring_full + 8 * slot, c));
-          }
-          if (++slot == kRing) {
-            slot = 0;
-            slot_phase ^= 1;
-          }
-          return true;
-        };
-        if (rank == 0) ok = publish(unit_at<PLANES>(jobs, rows, n, &u) ? n : -1);
-        else ok = next_unit(&n);
-        while (ok && unit_at<PLANES>(jobs, rows, n, &u)) {
-          int32_t next = 0;
-          if (rank == 0) next = int32_t(gridDim.x / 2) + atomicAdd(jobs.counter, 1);
+        for (;;) {
+          if (!(ok = next_unit()) || u.job < 0) break;
           const Job& job = jobs.job[u.job];
           const bool a_mn = job.mode == kWeight, b_mn = job.mode == kWeight || job.mode == kHidden;
           const int am = u.m0 + int(rank) * kHalf, bn = u.n0 + int(rank) * (u.n / 2);
           const int b_boxes = b_mn ? (u.n / 2 + 63) / 64 : 0;
           const uint32_t bytes = 2 * (kOperandBytes + (b_mn ? b_boxes * 64 * kBlockK * 2 : kOperandBytes));
+          const int segment = Shape<PLANES>::segment(job.mode);
           for (int s = 0; ok && s < u.segments; ++s) {
-            const int k_begin = s * u.segment, k_end = min(u.blocks, k_begin + u.segment);
+            const int k_begin = s * segment, k_end = min(blocks_of(u), k_begin + segment);
             for (int term = 0; ok && term < kTerms; ++term) {
               const int pa = kTerms == 1 ? 0 : kTermA[term], pb = kTerms == 1 ? 0 : kTermB[term];
               for (int k = k_begin; k < k_end; ++k) {
@@ -675,12 +679,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
           }
           if (!ok) break;
-          if (rank == 0) {
-            n = unit_at<PLANES>(jobs, rows, next, &u) ? next : -1;
-            ok = publish(n);
-          } else {
-            ok = next_unit(&n);
-          }
         }
         if (!ok) {  // let the copies in flight land before the CTA's memory goes
           const uint64_t begin = timer_ns();
@@ -693,21 +691,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         int stage = 0;
         uint32_t phase = 0, acc_phase = 0;
         int buffer = 0;
-        int32_t n;
         bool ok = true;
-        while (ok && next_unit(&n) && unit_at<PLANES>(jobs, rows, n, &u)) {
+        while (ok && next_unit() && u.job >= 0) {
           const Job& job = jobs.job[u.job];
           const bool a_mn = job.mode == kWeight, b_mn = job.mode == kWeight || job.mode == kHidden;
           // fp32 accumulator, bf16 operands, majors, N, M = 256
           const uint32_t idesc = 1u << 4 | 1u << 7 | 1u << 10 | uint32_t(a_mn) << 15 | uint32_t(b_mn) << 16 |
                                  uint32_t(u.n / 8) << 17 | uint32_t(256 / 16) << 24;
           const uint64_t a_step = (a_mn ? 16 * 128 : 32) >> 4, b_step = (b_mn ? 16 * 128 : 32) >> 4;
+          const int segment = Shape<PLANES>::segment(job.mode);
           for (int s = 0; ok && s < u.segments; ++s) {
             const uint32_t d = tmem + buffer * 256;
             if (!(ok = wait(acc_empty + 8 * buffer, acc_phase ^ 1))) break;
             fence_after();
             bool add = false;
-            const int count = (min(u.blocks, (s + 1) * u.segment) - s * u.segment) * kTerms;
+            const int count = (min(blocks_of(u), (s + 1) * segment) - s * segment) * kTerms;
             for (int k = 0; k < count; ++k) {
               if (!(ok = wait(full + 8 * stage, phase))) break;
               fence_after();
@@ -730,6 +728,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               acc_phase ^= 1;
             }
           }
+        }
+      }
+    } else if (warp == 2 && rank == 0) {
+      // ---- hands out the units
+      if (elect_one()) {
+        const int32_t pairs = int32_t(gridDim.x / 2);
+        for (int32_t n = int32_t(blockIdx.x / 2);; n = pairs + atomicAdd(jobs.counter, 1)) {
+          const Unit x = unit_at<PLANES>(jobs, rows, n);
+          if (!wait(ring_empty + 8 * slot, slot_phase ^ 1)) break;
+          for (uint32_t c = 0; c < 2; ++c) {
+            const uint32_t to = in_cta(smem_u32(ring + 2 * slot), c);
+            store_remote(to, make_int4(x.job, x.m0, x.n0, x.n));
+            store_remote(to + 16, make_int4(x.k0, x.blocks, x.split, x.segments));
+            barrier_arrive_remote(in_cta(ring_full + 8 * slot, c));
+          }
+          if (++slot == kRing) {
+            slot = 0;
+            slot_phase ^= 1;
+          }
+          if (x.job < 0) break;
         }
       }
     }
@@ -760,10 +778,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
     };
     for (;;) {
-      int32_t n = -1;
-      if (lane == 0 && !next_unit(&n)) n = -1;
-      n = __shfl_sync(~0u, n, 0);
-      if (!unit_at<PLANES>(jobs, rows, n, &u)) break;
+      const uint32_t entry = in_cta(ring_empty + 8 * slot, 0);
+      if (!__all_sync(~0u, next_unit()) || u.job < 0) break;
       const Job& job = jobs.job[u.job];
       const bool logits = job.mode == kForward || job.mode == kGradient;
       Row r{};
@@ -771,11 +787,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (u.segments == 1) {
         if (logits) r = row_of<CE, KD>(a, job, rows, u, th, rank);
         ok = __all_sync(~0u, full_accumulator());
+        if (lane == 0) barrier_arrive_remote(entry);
       } else {
         const int begin = th.half * 128;
         float sum[4][32] = {};
         for (int s = 0; ok && s < u.segments; ++s) {
           if (!(ok = __all_sync(~0u, full_accumulator()))) break;
+          if (s == 0 && lane == 0) barrier_arrive_remote(entry);
           const uint32_t acc = lanes + buffer * 256 + begin;
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
