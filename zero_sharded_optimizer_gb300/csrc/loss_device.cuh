@@ -7,15 +7,6 @@ namespace zl {
 
 constexpr float kLog2e = 1.4426950408889634f;
 
-// The factor of both gradients that does not depend on the row: grad_scale,
-// the mean's count, and the reduced loss's own gradient.
-__device__ __forceinline__ float grad_factor(const Args& a) {
-  double f = a.grad_scale;
-  if (a.reduction == ZERO_REDUCE_MEAN) f /= double(max(1, a.head->rows));
-  if (a.reduction != ZERO_REDUCE_NONE && a.dloss) f *= double(*a.dloss);
-  return float(f);
-}
-
 // A value as bf16 parts: x = p0 + p1 + p2 up to fp32's rounding (each part
 // holds the next 8 bits; the rests are exact differences). An infinity and
 // a value that would round to one keep the parts finite or zero.

@@ -244,6 +244,7 @@ int plan(const zero_head_loss_t* p, bool distill, int pass, Args* a, __nv_bfloat
   a->counters = w.take<int32_t>(a->launches);
   // The forward pass's arrays and the backward pass's lie over one another.
   const int64_t common = w.at;
+  a->sums = w.take<double>(zl::kLossBlocks);
   a->zent = w.take<float>(a->T, a->L);
   if (a->has_ce) a->stats = w.take<float2>(2 * a->tiles, a->Tp);
   if (a->has_kd) a->stats_tau = w.take<float2>(2 * a->tiles, a->Tp);

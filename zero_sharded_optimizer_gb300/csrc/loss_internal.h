@@ -21,12 +21,14 @@ constexpr int kTileM = 256;
 constexpr int kTileN = 256;
 constexpr int kPadD = 64;       // packed operands are padded to this width
 constexpr int32_t kNoId = 0x7fffffff;
+constexpr int kLossBlocks = 608; // most blocks of the losses' kernel
 
 // Device-side scalars of a call, at the start of the workspace.
 struct Head {
   int32_t rows;    // rows with a target (the compact rows)
   int32_t ticket;  // blocks of the reduction that are done
   int32_t fault;   // a wait of the matrix kernel ran out: the results are not valid
+  float factor;    // of both gradients, the same for every row
 };
 
 // Everything the kernels read or write. Rows with a target are packed densely:
@@ -74,6 +76,7 @@ struct Args {
   float* konst;           // [T] the loss's part that no logit enters
   int32_t* ids;           // [T][L] ascending, kNoId after the last
   float* weights;         // [T][L] weight of each entry's logit in loss and gradient
+  double* sums;           // [kLossBlocks] parts of the reduced loss
   float* zent;            // [T][L] logits of the entries
   __nv_bfloat16* hp;      // [planes][Tp][Dp] packed hidden states
   const __nv_bfloat16* wp;  // [planes][V][Dp], or the caller's weight (then wp_ld)

@@ -760,7 +760,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     uint8_t* boxes = staging + (warp - kEpilogueWarp) * Shape<PLANES>::boxes * kWarpBox;
     const uint32_t lanes = tmem + (uint32_t((warp & 3) * 32) << 16);
     const uint32_t acc_empty0 = in_cta(acc_empty, 0);
-    const float factor = grad_factor(a);
+    const float factor = a.head->factor;
     int buffer = 0;
     uint32_t phase = 0;
     auto full_accumulator = [&] {
