@@ -79,7 +79,7 @@ def test_xent_step(losses, cuda, kind, T, V, D):
         check(got, r, dt, f"{kind} {reduction}")
 
 
-@pytest.mark.parametrize("pad,offset", [(0, 1), (1, 0), (3, 5), (8, 0), (8, 8), (5, 3)])
+@pytest.mark.parametrize("pad,offset", [(0, 1), (1, 0), (3, 5), (8, 0), (8, 8), (5, 3), (5, 0), (13, 0)])
 @pytest.mark.parametrize("kind", TYPES)
 def test_strides_and_alignment(losses, cuda, kind, pad, offset):
     dt = TYPES[kind]

@@ -11,15 +11,16 @@
 namespace {
 
 using zl::Args;
-using zl::Job;
-using zl::Jobs;
+using zl::Program;
 using zl::set_error;
 
+#ifndef PIECEMB
+#define PIECEMB 40
+#endif
 constexpr int64_t kMostSize = 0x7fffffff - 1024;  // T, V and D: 32-bit tile coordinates
 // A piece of the logits' gradient is at most this many bytes (one tile's width
-// of columns at least); two are held, so that the next piece is formed while
-// this one's products run.
-constexpr int64_t kPieceBytes = int64_t(64) << 20;
+// of columns at least); kBuffers of them are held.
+constexpr int64_t kPieceBytes = int64_t(PIECEMB) << 20;
 
 int64_t round_up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
 
@@ -240,8 +241,10 @@ int plan(const zero_head_loss_t* p, bool distill, int pass, Args* a, __nv_bfloat
     a->piece = round_up((a->V + pieces - 1) / pieces, zl::kTileN);
     pieces = (a->V + a->piece - 1) / a->piece;
   }
-  a->launches = 2 + pieces;
-  a->counters = w.take<int32_t>(a->launches);
+  a->counters = w.take<int32_t>(2 + 2 * pieces);
+  a->formed = reinterpret_cast<uint32_t*>(a->counters + 2);
+  a->used = a->formed + pieces;
+  a->zeros = 2 + 2 * pieces;
   // The forward pass's arrays and the backward pass's lie over one another.
   const int64_t common = w.at;
   a->sums = w.take<double>(zl::kLossBlocks);
@@ -251,9 +254,8 @@ int plan(const zero_head_loss_t* p, bool distill, int pass, Args* a, __nv_bfloat
   int64_t most = w.at;
   if (pass & kBackward) {
     w.at = common;
-    for (int b = 0; b < (pieces > 1 ? 2 : 1); ++b)
-      a->g[b] = w.take<__nv_bfloat16>(a->Tp * a->planes, a->piece);
-    if (pieces == 1) a->g[1] = a->g[0];
+    for (int b = 0; b < zl::kBuffers; ++b)
+      a->g[b] = b < pieces ? w.take<__nv_bfloat16>(a->Tp * a->planes, a->piece) : a->g[0];
     // dhidden's sums over a piece are split where one of its tiles would be
     // more than half of what each of 76 CTA pairs has to do in a launch.
     const int64_t blocks_t = (a->Tp + 63) / 64, blocks_v = a->piece / 64, blocks_d = a->Dp / 64;
@@ -288,85 +290,43 @@ EncodeTiled encoder() {
   return fn;
 }
 
-// A bf16 array [planes][rows][cols] as boxes of 64 columns by `box_rows` rows,
-// in shared memory with the 128-byte swizzle; elements outside read as zero.
+// An array [planes][rows][cols] as boxes of 128 bytes of columns by `box_rows`
+// rows, in shared memory with the 128-byte swizzle; elements outside it read
+// as zero and are not written.
 bool tensor_map(CUtensorMap* map, const void* base, int64_t cols, int64_t rows, int64_t ld, int64_t planes,
-                int64_t plane, uint32_t box_rows) {
+                int64_t plane, uint32_t box_rows, bool fp32 = false) {
+  const int es = fp32 ? 4 : 2;
   const cuuint64_t dims[3] = {cuuint64_t(cols), cuuint64_t(rows), cuuint64_t(planes)};
-  const cuuint64_t strides[2] = {cuuint64_t(ld) * 2, cuuint64_t(planes > 1 ? plane : ld) * 2};
-  const cuuint32_t box[3] = {64, box_rows, 1}, unit[3] = {1, 1, 1};
-  return encoder()(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, unit,
-                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+  const cuuint64_t strides[2] = {cuuint64_t(ld) * es, cuuint64_t(planes > 1 ? plane : ld) * es};
+  const cuuint32_t box[3] = {cuuint32_t(128 / es), box_rows, 1}, unit[3] = {1, 1, 1};
+  return encoder()(map, fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+                   const_cast<void*>(base), dims, strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// The operands, each once read along K (boxes of 128 rows) and once across it
-// (boxes of 64 rows of K); G also as it is written (boxes of a warp's 32 rows).
-struct Maps {
-  CUtensorMap hidden, hidden_mn, weight, weight_mn, g[2], g_mn[2], g_out[2];
-  bool make(const Args& a, bool backward) {
-    bool ok = tensor_map(&hidden, a.hp, a.Dp, a.Tp, a.Dp, a.planes, a.Tp * a.Dp, 128);
-    const int64_t wide = a.wp_plane ? a.Dp : a.D;
-    ok = ok && tensor_map(&weight, a.wp, wide, a.V, a.wp_ld, a.planes, a.wp_plane, 128);
-    if (!backward) return ok;
-    ok = ok && tensor_map(&hidden_mn, a.hp, a.Dp, a.Tp, a.Dp, a.planes, a.Tp * a.Dp, 64) &&
-         tensor_map(&weight_mn, a.wp, wide, a.V, a.wp_ld, a.planes, a.wp_plane, 64);
-    for (int b = 0; b < 2; ++b) {
-      CUtensorMap* const to[3] = {&g[b], &g_mn[b], &g_out[b]};
-      const uint32_t box[3] = {128, 64, 32};
-      for (int i = 0; i < 3; ++i)
-        ok = ok && tensor_map(to[i], a.g[b], a.piece, a.Tp, a.piece, a.planes, a.Tp * a.piece, box[i]);
-    }
-    return ok;
+bool make_program(const Args& a, bool backward, Program* p) {
+  const bool f32 = a.planes == 3;
+  const int64_t wide = a.wp_plane ? a.Dp : a.D;
+  bool ok = tensor_map(&p->hidden, a.hp, a.Dp, a.Tp, a.Dp, a.planes, a.Tp * a.Dp, 128) &&
+            tensor_map(&p->weight, a.wp, wide, a.V, a.wp_ld, a.planes, a.wp_plane, 128);
+  if (!backward) return ok;
+  ok = ok && tensor_map(&p->hidden_mn, a.hp, a.Dp, a.Tp, a.Dp, a.planes, a.Tp * a.Dp, 64) &&
+       tensor_map(&p->weight_mn, a.wp, wide, a.V, a.wp_ld, a.planes, a.wp_plane, 64);
+  for (int b = 0; b < zl::kBuffers; ++b) {
+    CUtensorMap* const to[3] = {&p->g[b], &p->g_mn[b], &p->g_out[b]};
+    const uint32_t box[3] = {128, 64, 32};
+    for (int i = 0; i < 3; ++i)
+      ok = ok && tensor_map(to[i], a.g[b], a.piece, a.Tp, a.piece, a.planes, a.Tp * a.piece, box[i]);
   }
-};
-
-int32_t tiles_of(int64_t n) { return int32_t((n + 255) / 256); }
-
-Job logits_job(const Args& a, const Maps& maps, bool gradient, int64_t c0) {
-  const int64_t cols = gradient ? std::min(a.piece, a.V - c0) : a.V;
-  Job j{};
-  j.a = maps.hidden;
-  j.b = maps.weight;
-  if (gradient) j.out = maps.g_out[c0 / a.piece & 1];
-  j.mode = gradient ? zl::kGradient : zl::kForward;
-  j.n_tiles = tiles_of(cols);
-  j.n_cols = int32_t(cols);
-  j.depth = int32_t(a.D);
-  j.splits = 1;
-  j.b_row0 = int32_t(c0);
-  j.c0 = c0;
-  return j;
-}
-
-Job hidden_job(const Args& a, const Maps& maps, int64_t c0) {
-  Job j{};
-  j.a = maps.g[c0 / a.piece & 1];
-  j.b = maps.weight_mn;
-  j.mode = zl::kHidden;
-  j.n_tiles = tiles_of(a.D);
-  j.n_cols = int32_t(a.D);
-  j.depth = int32_t(std::min(a.piece, a.V - c0));
-  j.splits = a.splits;
-  j.b_k0 = int32_t(c0);
-  j.first = c0 == 0;
-  j.c0 = c0;
-  return j;
-}
-
-Job weight_job(const Args& a, const Maps& maps, int64_t c0) {
-  const int es = a.planes == 1 ? 2 : 4;
-  Job j{};
-  j.a = maps.g_mn[c0 / a.piece & 1];
-  j.b = maps.hidden_mn;
-  j.mode = zl::kWeight;
-  j.m_tiles = tiles_of(std::min(a.piece, a.V - c0));
-  j.n_tiles = tiles_of(a.D);
-  j.n_cols = int32_t(a.D);
-  j.splits = 1;
-  j.vector = reinterpret_cast<uintptr_t>(a.dweight) % 16 == 0 && a.dweight_stride * es % 16 == 0;
-  j.c0 = c0;
-  return j;
+  if (a.dhidden) ok = ok && tensor_map(&p->dh, a.dh, a.Dp, a.Tp, a.Dp, a.splits, a.Tp * a.Dp, 32, true);
+  const int es = f32 ? 4 : 2;
+  // TMA writes whole 16-byte units: a row that ends inside one is left to the threads.
+  p->weight_tma = a.dweight && a.D * es % 16 == 0 && reinterpret_cast<uintptr_t>(a.dweight) % 16 == 0 && a.dweight_stride * es % 16 == 0 &&
+                  a.dweight_stride < (int64_t(1) << 37) && (f32 || !a.accumulate);
+  if (p->weight_tma) ok = ok && tensor_map(&p->dweight, a.dweight, a.D, a.V, a.dweight_stride, 1, 0, 32, f32);
+  p->pieces = int32_t((a.V + a.piece - 1) / a.piece);
+  return ok;
 }
 
 int workspace_bytes(const zero_head_loss_t* p, bool distill, int64_t* bytes) {
@@ -392,8 +352,8 @@ int run(const zero_head_loss_t* p, bool distill, int pass, cudaStream_t s) {
     return set_error(ZERO_EINVAL, "the workspace has %lld bytes, %lld are needed",
                      (long long)(p->workspace ? p->workspace_bytes : 0), (long long)bytes);
   if (!encoder()) return set_error(ZERO_ECUDA, "the CUDA driver has no cuTensorMapEncodeTiled");
-  Maps maps;
-  if (!maps.make(a, pass & kBackward))
+  Program program{};
+  if (!make_program(a, pass & kBackward, &program))
     return set_error(ZERO_EINVAL, "the problem's arrays are too large for tensor maps");
   int device = 0, sms = 0;
   cudaError_t q = cudaGetDevice(&device);
@@ -410,27 +370,15 @@ int run(const zero_head_loss_t* p, bool distill, int pass, cudaStream_t s) {
   next("packing hidden", [&] { return zl::launch_pack_hidden(a, s); });
   if (packed) next("packing weight", [&] { return zl::launch_pack_weight(a, packed, s); });
   if (pass & kForward) {
-    next("logits", [&] {
-      Jobs jobs{};
-      jobs.job[jobs.count++] = logits_job(a, maps, false, 0);
-      jobs.counter = a.counters;
-      return zl::launch_products(a, jobs, sms, s);
-    });
+    program.forward = 1;
+    program.counter = a.counters;
+    next("logits", [&] { return zl::launch_products(a, program, sms, s); });
     next("losses", [&] { return zl::launch_losses(a, s); });
   }
   if (pass & kBackward) {
-    // Each launch takes one piece's two products and forms the next piece.
-    int64_t n = 1;
-    for (int64_t c0 = -a.piece; c0 < a.V; c0 += a.piece, ++n) {
-      next("the gradients", [&] {
-        Jobs jobs{};
-        if (c0 >= 0 && p->dweight) jobs.job[jobs.count++] = weight_job(a, maps, c0);
-        if (c0 >= 0 && p->dhidden) jobs.job[jobs.count++] = hidden_job(a, maps, c0);
-        if (c0 + a.piece < a.V) jobs.job[jobs.count++] = logits_job(a, maps, true, c0 + a.piece);
-        jobs.counter = a.counters + n;
-        return zl::launch_products(a, jobs, sms, s);
-      });
-    }
+    program.forward = 0;
+    program.counter = a.counters + 1;
+    next("the gradients", [&] { return zl::launch_products(a, program, sms, s); });
     if (p->dhidden && p->T) next("dhidden", [&] { return zl::launch_dhidden_out(a, s); });
   }
   if (e != cudaSuccess)

@@ -21,6 +21,7 @@ constexpr int kTileM = 256;
 constexpr int kTileN = 256;
 constexpr int kPadD = 64;       // packed operands are padded to this width
 constexpr int32_t kNoId = 0x7fffffff;
+constexpr int kBuffers = 3;      // of G
 constexpr int kLossBlocks = 608; // most blocks of the losses' kernel
 
 // Device-side scalars of a call, at the start of the workspace.
@@ -84,9 +85,11 @@ struct Args {
   int64_t tiles;          // vocabulary tiles
   float2* stats;          // [2 tiles][Tp] half a tile's (m, sum of 2^(z log2(e) - m))
   float2* stats_tau;      // [2 tiles][Tp] of z / tau
-  int32_t* counters;      // [launches] tiles handed out
-  int64_t launches;
-  __nv_bfloat16* g[2];    // [planes][Tp][piece] gradients of two pieces' logits
+  int32_t* counters;      // [2] units handed out, forward and backward
+  uint32_t* formed;       // [pieces] finished units of a piece's gradient
+  uint32_t* used;         // [pieces] finished units of the products with it
+  int64_t zeros;          // 32-bit words from `counters` on that begin as zero
+  __nv_bfloat16* g[kBuffers];  // [planes][Tp][piece] gradients of pieces of the logits
   int64_t piece;          // columns of a piece, a multiple of kTileN
   int32_t splits;         // parts of a piece's columns that dhidden is summed in
   float* dh;              // [splits][Tp][Dp] running sums of dhidden over the pieces
@@ -95,26 +98,16 @@ struct Args {
 // The matrix kernel's work: see loss_mma.cu.
 enum Mode : int32_t { kForward, kGradient, kHidden, kWeight };
 
-struct Job {
-  CUtensorMap a, b, out;
-  Mode mode;
-  int32_t m_tiles;   // kWeight: row tiles (else they follow from the rows with a target)
-  int32_t n_tiles;
-  int32_t n_cols;    // columns of the product
-  int32_t depth;     // length of the sums (kWeight: the rows with a target)
-  int32_t splits;
-  int32_t b_k0;      // where B's K begins, or (b_row0) its columns
-  int32_t b_row0;
-  int32_t first;     // kHidden: the sums begin here
-  int32_t vector;    // kWeight: rows of dweight take 16-byte accesses
-  int64_t c0;        // the piece's first vocabulary column
-};
-
-// A launch's work, the longest tiles first.
-struct Jobs {
-  Job job[3];
-  int32_t count;
-  int32_t* counter;
+struct Program {
+  // Operands read along K (boxes of 128 rows) and across it (_mn, boxes of 64
+  // rows of K); G, the sums of dhidden and dweight as a warp writes them.
+  CUtensorMap hidden, hidden_mn, weight, weight_mn;
+  CUtensorMap g[kBuffers], g_mn[kBuffers], g_out[kBuffers];
+  CUtensorMap dh, dweight;
+  int32_t forward;     // the forward pass (else the backward pass)
+  int32_t pieces;
+  int32_t weight_tma;  // dweight can be written by TMA
+  int32_t* counter;    // units handed out
 };
 
 cudaError_t launch_rows(const Args& a, cudaStream_t s);
@@ -122,6 +115,6 @@ cudaError_t launch_pack_hidden(const Args& a, cudaStream_t s);
 cudaError_t launch_pack_weight(const Args& a, __nv_bfloat16* to, cudaStream_t s);
 cudaError_t launch_losses(const Args& a, cudaStream_t s);
 cudaError_t launch_dhidden_out(const Args& a, cudaStream_t s);
-cudaError_t launch_products(const Args& a, const Jobs& jobs, int sms, cudaStream_t s);
+cudaError_t launch_products(const Args& a, const Program& prog, int sms, cudaStream_t s);
 
 }  // namespace zl

@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(1024) number_rows_kernel(const Args a) {
     for (int64_t t = warp; t < a.T; t += 32) prepare_row(a, t, sh + warp * 4 * (a.K + 1));
     __syncthreads();
   }
-  for (int64_t n = threadIdx.x; n < a.launches; n += 1024) a.counters[n] = 0;
+  for (int64_t n = threadIdx.x; n < a.zeros; n += 1024) a.counters[n] = 0;
   int32_t base = 0;
   for (int64_t t0 = 0; t0 < a.T; t0 += 16 * 1024) {
     uint32_t mask[16];

@@ -1,10 +1,16 @@
 // The matrix products of the vocabulary losses on the tensor cores (tcgen05).
 //
-// One persistent kernel works off a list of jobs, each a grid of tiles:
+// One persistent kernel works off a list of phases, each a grid of tiles:
 //   kForward   z = H W^T, kept only as each row's maximum and sum of exponentials
 //   kGradient  z again, as the logits' gradient G of one piece of the vocabulary
-//   kHidden    dH += G W over that piece
 //   kWeight    dW = G^T H of that piece's rows
+//   kHidden    dH += G W over that piece
+// The forward pass is one phase; the backward pass is G_0 G_1 W_0 H_0 G_2 W_1
+// H_1 G_3 ..., one launch: G has three buffers, so that a piece is formed while
+// the two products of an earlier one run, and no launch's beginning and end
+// leave the machine idle between pieces. Order between phases is kept by
+// counters in global memory (see Progress).
+//
 // A pair of CTAs (a cluster on two neighbouring SMs) forms one 256 x 256 tile
 // with one tcgen05.mma.cta_group::2 stream: each CTA holds 128 rows of A and
 // half of B's columns, so an operand byte read from L2 feeds twice the
@@ -140,6 +146,39 @@ struct Waiter {
   }
 };
 
+// Counts of finished units, one arrival of each epilogue warp (16 a unit),
+// made when the warp's stores are complete. A unit waits only for units that
+// were handed out before it and a pair works its units off in order, so the
+// first unfinished unit never waits: no wait is for ever, however few of the
+// grid's pairs run.
+struct Progress {
+  volatile uint32_t* given_up;
+  Head* head;
+  __device__ __forceinline__ bool reached(const uint32_t* count, uint32_t target) const {
+    uint64_t begin = 0;
+    for (uint32_t n = 0;; ++n) {
+      uint32_t x;
+      asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(x) : "l"(count) : "memory");
+      if (x >= target) break;
+      if (n == 0) begin = timer_ns();
+      __nanosleep(100);
+      if ((n & 63) == 63 && (*given_up || timer_ns() - begin > kWaitLimitNs)) {
+        *given_up = 1;
+        head->fault = 1;
+        return false;
+      }
+    }
+    // What follows reads, or writes over, data that TMA wrote or read.
+    asm volatile("fence.proxy.async.global;" ::: "memory");
+    return true;
+  }
+  // One thread, after its stores are complete.
+  __device__ __forceinline__ void arrive(uint32_t* count) const {
+    asm volatile("fence.proxy.async.global;" ::: "memory");
+    asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(count) : "memory");
+  }
+};
+
 __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int x, int y, int z,
                                          uint32_t cluster_bar) {
   asm volatile(
@@ -150,6 +189,11 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, i
 __device__ __forceinline__ void tma_store(const CUtensorMap* map, uint32_t src, int x, int y, int z) {
   asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(map),
                "r"(src), "r"(x), "r"(y), "r"(z) : "memory");
+}
+// The same as an addition of fp32 values.
+__device__ __forceinline__ void tma_add(const CUtensorMap* map, uint32_t src, int x, int y, int z) {
+  asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                   map), "r"(src), "r"(x), "r"(y), "r"(z) : "memory");
 }
 __device__ __forceinline__ void store_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void store_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
@@ -243,12 +287,12 @@ __device__ constexpr int kTermA[6] = {0, 1, 2, 0, 1, 0};
 __device__ constexpr int kTermB[6] = {2, 1, 0, 1, 0, 0};
 
 struct Unit {
-  int job;            // negative: no more
+  int mode;           // negative: no more
+  int piece;
   int m0, n0;         // first row and column of the pair's tile
   int n;              // columns of the product: up to 256, a multiple of 32
   int k0, blocks;     // first K element and number of 64-element blocks
   int split;
-  int segments;       // of segment() blocks each
 };
 
 // A unit without terms (no rows, or an empty split) still goes through one
@@ -256,38 +300,84 @@ struct Unit {
 __device__ __forceinline__ int blocks_of(const Unit& u) { return u.blocks < 0 ? 1 : u.blocks; }
 
 template <int PLANES>
-__device__ __forceinline__ Unit unit_at(const Jobs& jobs, int rows, int32_t u) {
-  const int row_tiles = (rows + 255) / 256;
-  Unit unit{};
-  unit.job = -1;
-  for (int j = 0; j < jobs.count; ++j) {
-    const Job& job = jobs.job[j];
-    const int mt = job.mode == kWeight ? job.m_tiles : row_tiles;
-    const int all = mt * job.n_tiles * job.splits;
-    if (u >= all) {
-      u -= all;
-      continue;
-    }
-    const int tile = u % (mt * job.n_tiles);
-    unit.split = u / (mt * job.n_tiles);
-    const int m = job.mode == kWeight ? tile / job.n_tiles : tile % mt;
-    const int n = job.mode == kWeight ? tile % job.n_tiles : tile / mt;
-    unit.job = j;
-    unit.m0 = m * 256;
-    unit.n0 = n * 256;
-    unit.n = min(256, (job.n_cols - unit.n0 + 31) / 32 * 32);
-    const int depth = job.mode == kWeight ? rows : job.depth;
-    const int blocks = (depth + kBlockK - 1) / kBlockK;
-    const int first = int(int64_t(blocks) * unit.split / job.splits);
-    unit.k0 = first * kBlockK;
-    unit.blocks = int(int64_t(blocks) * (unit.split + 1) / job.splits) - first;
-    if (unit.blocks == 0) unit.blocks = -1;
-    const int segment = Shape<PLANES>::segment(job.mode);
-    unit.segments = (blocks_of(unit) + segment - 1) / segment;
-    break;
-  }
-  return unit;
+__device__ __forceinline__ int segments_of(const Unit& u) {
+  const int segment = Shape<PLANES>::segment(Mode(u.mode));
+  return (blocks_of(u) + segment - 1) / segment;
 }
+
+__device__ __forceinline__ int piece_cols(const Args& a, int p) {
+  return int(min(a.piece, a.V - p * a.piece));
+}
+__device__ __forceinline__ int tiles_of(int n) { return (n + 255) / 256; }
+
+// Units of a piece's phases.
+__device__ __forceinline__ int gradient_units(const Args& a, int rows, int p) {
+  return tiles_of(rows) * tiles_of(piece_cols(a, p));
+}
+__device__ __forceinline__ int weight_units(const Args& a, int p) {
+  return a.dweight ? tiles_of(piece_cols(a, p)) * tiles_of(int(a.D)) : 0;
+}
+__device__ __forceinline__ int hidden_units(const Args& a, int rows) {
+  return a.dhidden ? tiles_of(rows) * tiles_of(int(a.D)) * a.splits : 0;
+}
+
+// The phases in order; the units are numbered through them.
+struct Phases {
+  int phase = 0, base = 0;
+  // The phase's mode and piece; false after the last.
+  __device__ __forceinline__ bool at(const Args& a, const Program& prog, int* mode, int* piece) const {
+    if (prog.forward) {
+      *mode = kForward;
+      *piece = 0;
+      return phase < 1;
+    }
+    const int lead = min(2, prog.pieces);
+    if (phase < lead) {
+      *mode = kGradient;
+      *piece = phase;
+      return true;
+    }
+    const int p = (phase - lead) / 3, which = (phase - lead) % 3;
+    *mode = which == 0 ? kWeight : which == 1 ? kHidden : kGradient;
+    *piece = which == 2 ? p + 2 : p;
+    return p < prog.pieces;
+  }
+  __device__ __forceinline__ Unit unit(const Args& a, const Program& prog, int rows, int u) {
+    Unit x{};
+    x.mode = -1;
+    int mode, p;
+    for (; at(a, prog, &mode, &p); ++phase) {
+      const int cols = mode == kForward ? int(a.V) : p < prog.pieces ? piece_cols(a, p) : 0;
+      const int mt = mode == kWeight ? tiles_of(cols) : tiles_of(rows);
+      const int nt = mode == kForward || mode == kGradient ? tiles_of(cols) : tiles_of(int(a.D));
+      const int splits = mode == kHidden ? a.splits : 1;
+      const int count = mode == kWeight && !a.dweight || mode == kHidden && !a.dhidden ? 0 : mt * nt * splits;
+      if (u >= base + count) {
+        base += count;
+        continue;
+      }
+      u -= base;
+      const int tile = u % (mt * nt);
+      x.split = u / (mt * nt);
+      const int m = mode == kWeight ? tile / nt : tile % mt;
+      const int n = mode == kWeight ? tile % nt : tile / mt;
+      x.mode = mode;
+      x.piece = p;
+      x.m0 = m * 256;
+      x.n0 = n * 256;
+      const int width = mode == kForward || mode == kGradient ? cols : int(a.D);
+      x.n = min(256, (width - x.n0 + 31) / 32 * 32);
+      const int depth = mode == kWeight ? rows : mode == kHidden ? cols : int(a.D);
+      const int blocks = (depth + kBlockK - 1) / kBlockK;
+      const int first = int(int64_t(blocks) * x.split / splits);
+      x.k0 = first * kBlockK;
+      x.blocks = int(int64_t(blocks) * (x.split + 1) / splits) - first;
+      if (x.blocks == 0) x.blocks = -1;
+      break;
+    }
+    return x;
+  }
+};
 
 // --------------------------------------------------------------- epilogues --
 
@@ -308,8 +398,7 @@ struct Row {
 };
 
 template <bool CE, bool KD>
-__device__ __forceinline__ Row row_of(const Args& a, const Job& job, int rows, const Unit& u, const Thread& th,
-                                      uint32_t rank) {
+__device__ __forceinline__ Row row_of(const Args& a, int rows, const Unit& u, const Thread& th, uint32_t rank) {
   Row r{};
   r.i = u.m0 + int(rank) * kHalf + th.row;
   r.there = r.i < rows;
@@ -317,7 +406,7 @@ __device__ __forceinline__ Row row_of(const Args& a, const Job& job, int rows, c
   r.lse = r.lse_kd = INFINITY;
   if (!r.there) return r;
   r.t = a.rowmap[r.i];
-  if (job.mode == kGradient) {
+  if (u.mode == kGradient) {
     const float2 f = a.coef[r.t];
     // A term that the row does not have is 2^-inf = 0, whatever the accumulator holds.
     if (CE && f.x != 0.0f) r.lse = a.lse[r.t];
@@ -327,9 +416,10 @@ __device__ __forceinline__ Row row_of(const Args& a, const Job& job, int rows, c
     r.w_kd = f.y * r.scale;
   }
   const int32_t* ids = a.ids + r.t * a.L;
-  r.e = a.L == 1 ? 0 : first_entry(ids, a.L, job.c0 + u.n0 + th.half * 128);
+  const int64_t v = u.piece * a.piece + u.n0 + th.half * 128;
+  r.e = a.L == 1 ? 0 : first_entry(ids, a.L, v);
   r.id = r.e < a.L ? ids[r.e] : kNoId;
-  if (r.id < job.c0 + u.n0 + th.half * 128) r.id = kNoId;
+  if (r.id < v) r.id = kNoId;
   return r;
 }
 
@@ -421,13 +511,33 @@ __device__ __forceinline__ void pack_parts(float x0, float x1, uint32_t (&word)[
   }
 }
 
+// A warp's staging box may be written again: its last store has read it.
+// `Two`: boxes are used in turn, the other one's store may still be reading.
+template <bool Two>
+__device__ __forceinline__ void box_free(int lane) {
+  if (lane == 0) {
+    if (Two) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+    else asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+  }
+  __syncwarp();
+}
+
+// 32 fp32 values of the lane's row into a box of 32 rows x 128 bytes.
+__device__ __forceinline__ void stage_fp32(uint8_t* box, int lane, const float (&x)[32]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    *reinterpret_cast<float4*>(box + lane * 128 + ((j ^ (lane & 7)) * 16)) =
+        make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
+}
+
 // The logits' gradient without the factor that all rows share, as the bf16
 // operand of the two products: rounded once (fp32 storage: in three parts).
 // Each warp stages boxes of its 32 rows by 64 columns and stores them by TMA.
 template <int PLANES, bool CE, bool KD>
-__device__ __forceinline__ void gradient_epilogue(const Args& a, const Job& job, const Unit& u, const Thread& th,
-                                                  Row& r, uint32_t acc, uint32_t rank, uint8_t* staging) {
-  const int64_t v0 = job.c0 + u.n0;
+__device__ __forceinline__ void gradient_epilogue(const Args& a, const CUtensorMap* out, const Unit& u,
+                                                  const Thread& th, Row& r, uint32_t acc, uint32_t rank,
+                                                  uint8_t* staging) {
+  const int64_t v0 = u.piece * a.piece + u.n0;
   const int begin = th.half * 128, lane = th.row & 31;
   const int cols = int(min(int64_t(256), a.V - v0));
   const float c_ce = kLog2e, c_kd = a.inv_tau * kLog2e;
@@ -446,12 +556,7 @@ __device__ __forceinline__ void gradient_epilogue(const Args& a, const Job& job,
 #pragma unroll 1
   for (int b = 0; b < 2; ++b) {
     uint8_t* box = staging + (PLANES == 1 ? b * kWarpBox : 0);
-    // The box's last store has read it (bf16: it was issued before the last one).
-    if (lane == 0) {
-      if (PLANES == 1) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-      else asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-    }
-    __syncwarp();
+    box_free<PLANES == 1>(lane);
 #pragma unroll 1
     for (int k = 0; k < 2; ++k) {
       const int c0 = begin + 64 * b + 32 * k;
@@ -491,76 +596,107 @@ __device__ __forceinline__ void gradient_epilogue(const Args& a, const Job& job,
     if (lane == 0) {
 #pragma unroll
       for (int p = 0; p < PLANES; ++p)
-        tma_store(&job.out, smem_u32(box + p * kWarpBox), u.n0 + begin + 64 * b,
-                  u.m0 + int(rank) * kHalf + th.row, p);
+        tma_store(out, smem_u32(box + p * kWarpBox), u.n0 + begin + 64 * b, u.m0 + int(rank) * kHalf + th.row,
+                  p);
       store_commit();
     }
   }
 }
 
-// dH of a piece, fp32: stored by the first piece, added by the others. Each
-// element gets one addition per launch, so the order is fixed.
-__device__ __forceinline__ void hidden_epilogue(const Args& a, const Job& job, const Unit& u, const Thread& th,
-                                                int rows, uint32_t acc, uint32_t rank) {
-  const int i = u.m0 + int(rank) * kHalf + th.row;
-  float* to = a.dh + (int64_t(u.split) * a.Tp + i) * a.Dp + u.n0;
-  for (int c = th.half * 128; c < min(u.n, th.half * 128 + 128); c += 32) {
+// 32 columns of the accumulator, or zeros for a unit without terms.
+__device__ __forceinline__ void load_terms(const Unit& u, uint32_t addr, float (&x)[32]) {
+  if (u.blocks > 0) {
+    tmem_load32(addr, x);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) x[j] = 0.0f;
+  }
+}
+
+// dH of a piece, fp32: stored by the first piece, added by the others (TMA
+// reductions). An element gets one addition of each piece, and a piece's come
+// after the one before is complete, so the order is fixed.
+__device__ __forceinline__ void hidden_epilogue(const CUtensorMap* out, const Unit& u, const Thread& th, uint32_t acc,
+                                                uint32_t rank, uint8_t* staging) {
+  const int lane = th.row & 31, begin = th.half * 128;
+#pragma unroll 1
+  for (int k = 0; k < 4; ++k) {
+    const int c = begin + 32 * k;
+    if (c >= u.n) break;
+    uint8_t* box = staging + (k & 1) * kWarpBox;
     float x[32];
-    if (u.blocks > 0) {
-      tmem_load32(acc + c, x);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 32; ++j) x[j] = 0.0f;
-    }
-#pragma unroll
-    for (int j = 0; j < 32; j += 4) {
-      if (i >= rows) break;
-      if (job.first)
-        *reinterpret_cast<float4*>(to + c + j) = make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
-      else
-        asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(to + c + j), "f"(x[j]), "f"(x[j + 1]),
-                     "f"(x[j + 2]), "f"(x[j + 3]) : "memory");
+    load_terms(u, acc + c, x);
+    box_free<true>(lane);
+    stage_fp32(box, lane, x);
+    proxy_fence();
+    __syncwarp();
+    if (lane == 0) {
+      const int row = u.m0 + int(rank) * kHalf + th.row;
+      if (u.piece == 0) tma_store(out, smem_u32(box), u.n0 + c, row, u.split);
+      else tma_add(out, smem_u32(box), u.n0 + c, row, u.split);
+      store_commit();
     }
   }
 }
 
+// dW of a piece's rows, by TMA where the caller's rows are 16-byte aligned
+// (fp32: also the addition to what is there; bf16 would round it twice), else
+// by the threads.
 template <int PLANES>
-__device__ __forceinline__ void weight_epilogue(const Args& a, const Job& job, const Unit& u, const Thread& th,
-                                                float factor, uint32_t acc, uint32_t rank) {
-  const int64_t v = job.c0 + u.m0 + int(rank) * kHalf + th.row;
+__device__ __forceinline__ void weight_epilogue(const Args& a, const Program& prog, const Unit& u, const Thread& th,
+                                                float factor, uint32_t acc, uint32_t rank, uint8_t* staging) {
   using T = typename std::conditional<PLANES == 1, __nv_bfloat16, float>::type;
-  T* to = static_cast<T*>(a.dweight) + v * a.dweight_stride + u.n0;
-  for (int c = th.half * 128; c < min(u.n, th.half * 128 + 128); c += 32) {
-    float x[32];
-    if (u.blocks > 0) {
-      tmem_load32(acc + c, x);
-    } else {
+  const int lane = th.row & 31, begin = th.half * 128;
+  const int64_t v = u.piece * a.piece + u.m0 + int(rank) * kHalf + th.row;
+  if (prog.weight_tma) {
+    constexpr int wide = 128 / sizeof(T);  // columns of a box
+#pragma unroll 1
+    for (int k = 0; k < 128 / wide; ++k) {
+      const int c = begin + wide * k;
+      if (c >= u.n) break;
+      uint8_t* box = staging + (k & 1) * kWarpBox;
+      box_free<true>(lane);
 #pragma unroll
-      for (int j = 0; j < 32; ++j) x[j] = 0.0f;
-    }
-    if (v >= a.V) continue;
-    const int valid = int(min(int64_t(32), a.D - u.n0 - c));
-    if (job.vector && valid == 32) {
-      constexpr int per = 16 / sizeof(T);
+      for (int h = 0; h < wide / 32; ++h) {
+        float x[32];
+        load_terms(u, acc + c + 32 * h, x);
 #pragma unroll
-      for (int j = 0; j < 32; j += per) {
-        uint4 w;
-        T* out = reinterpret_cast<T*>(&w);
-        if (a.accumulate) w = *reinterpret_cast<const uint4*>(to + c + j);
+        for (int j = 0; j < 32; ++j) x[j] *= factor;
+        if (PLANES == 3) {
+          stage_fp32(box, lane, x);
+        } else {
 #pragma unroll
-        for (int q = 0; q < per; ++q) {
-          const float y = factor * x[j + q];
-          out[q] = T(a.accumulate ? float(out[q]) + y : y);
+          for (int j = 0; j < 4; ++j) {
+            uint32_t word[4][1];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) pack_parts<1>(x[8 * j + 2 * q], x[8 * j + 2 * q + 1], word[q]);
+            *reinterpret_cast<uint4*>(box + lane * 128 + (((4 * h + j) ^ (lane & 7)) * 16)) =
+                make_uint4(word[0][0], word[1][0], word[2][0], word[3][0]);
+          }
         }
-        *reinterpret_cast<uint4*>(to + c + j) = w;
       }
-    } else {
+      proxy_fence();
+      __syncwarp();
+      if (lane == 0 && v < a.V) {
+        // Rows and columns past the matrix are not written.
+        if (a.accumulate) tma_add(&prog.dweight, smem_u32(box), u.n0 + c, int(v), 0);
+        else tma_store(&prog.dweight, smem_u32(box), u.n0 + c, int(v), 0);
+        store_commit();
+      }
+    }
+    return;
+  }
+  T* to = static_cast<T*>(a.dweight) + v * a.dweight_stride + u.n0;
+#pragma unroll 1
+  for (int c = begin; c < min(u.n, begin + 128); c += 32) {
+    float x[32];
+    load_terms(u, acc + c, x);
+    const int valid = v < a.V ? int(min(int64_t(32), a.D - u.n0 - c)) : 0;
 #pragma unroll
-      for (int j = 0; j < 32; ++j) {
-        if (j >= valid) break;
-        const float y = factor * x[j];
-        to[c + j] = T(a.accumulate ? float(to[c + j]) + y : y);
-      }
+    for (int j = 0; j < 32; ++j) {
+      if (j >= valid) break;
+      const float y = factor * x[j];
+      to[c + j] = T(a.accumulate ? float(to[c + j]) + y : y);
     }
   }
 }
@@ -569,7 +705,7 @@ __device__ __forceinline__ void weight_epilogue(const Args& a, const Job& job, c
 
 template <int PLANES, bool CE, bool KD>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-    products_kernel(const __grid_constant__ Args a, const __grid_constant__ Jobs jobs) {
+    products_kernel(const __grid_constant__ Args a, const __grid_constant__ Program prog) {
   constexpr int kStages = Shape<PLANES>::stages;
   constexpr int kTerms = PLANES == 1 ? 1 : 6;
   extern __shared__ uint8_t raw[];
@@ -614,6 +750,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tmem_slot;
   const int rows = a.head->rows;
   const Waiter wait{given_up, a.head};
+  const Progress progress{given_up, a.head};
   Unit u;
   // The ring's next entry. The epilogue warps give it back to the pair's first
   // CTA once the unit's first accumulator is full: by then the copies and the
@@ -641,15 +778,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         int stage = 0;
         uint32_t phase = 0;
         bool ok = true;
+        int formed = -1;  // the last piece known to be there
         for (;;) {
-          if (!(ok = next_unit()) || u.job < 0) break;
-          const Job& job = jobs.job[u.job];
-          const bool a_mn = job.mode == kWeight, b_mn = job.mode == kWeight || job.mode == kHidden;
-          const int am = u.m0 + int(rank) * kHalf, bn = u.n0 + int(rank) * (u.n / 2);
+          if (!(ok = next_unit()) || u.mode < 0) break;
+          const bool a_mn = u.mode == kWeight, b_mn = u.mode == kWeight || u.mode == kHidden;
+          if (b_mn && u.piece > formed) {
+            if (!(ok = progress.reached(a.formed + u.piece, 16 * gradient_units(a, rows, u.piece)))) break;
+            formed = u.piece;
+          }
+          const int c0 = int(u.piece * a.piece), buffer = u.piece % kBuffers;
+          const CUtensorMap* map_a = u.mode == kWeight ? &prog.g_mn[buffer]
+                                     : u.mode == kHidden ? &prog.g[buffer] : &prog.hidden;
+          const CUtensorMap* map_b = u.mode == kWeight ? &prog.hidden_mn
+                                     : u.mode == kHidden ? &prog.weight_mn : &prog.weight;
+          const int am = u.m0 + int(rank) * kHalf;
+          const int bn = u.n0 + int(rank) * (u.n / 2) + (u.mode == kGradient ? c0 : 0);
+          const int b_k0 = u.mode == kHidden ? c0 : 0;
           const int b_boxes = b_mn ? (u.n / 2 + 63) / 64 : 0;
           const uint32_t bytes = 2 * (kOperandBytes + (b_mn ? b_boxes * 64 * kBlockK * 2 : kOperandBytes));
-          const int segment = Shape<PLANES>::segment(job.mode);
-          for (int s = 0; ok && s < u.segments; ++s) {
+          const int segments = segments_of<PLANES>(u);
+          const int segment = Shape<PLANES>::segment(Mode(u.mode));
+          for (int s = 0; ok && s < segments; ++s) {
             const int k_begin = s * segment, k_end = min(blocks_of(u), k_begin + segment);
             for (int term = 0; ok && term < kTerms; ++term) {
               const int pa = kTerms == 1 ? 0 : kTermA[term], pb = kTerms == 1 ? 0 : kTermB[term];
@@ -660,16 +809,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (rank == 0) barrier_expect(full + 8 * stage, bytes);
                 const int kk = u.k0 + k * kBlockK;
                 if (a_mn) {
-                  tma_load(sa, &job.a, am, kk, pa, bar);
-                  tma_load(sa + 64 * kBlockK * 2, &job.a, am + 64, kk, pa, bar);
+                  tma_load(sa, map_a, am, kk, pa, bar);
+                  tma_load(sa + 64 * kBlockK * 2, map_a, am + 64, kk, pa, bar);
                 } else {
-                  tma_load(sa, &job.a, kk, am, pa, bar);
+                  tma_load(sa, map_a, kk, am, pa, bar);
                 }
                 if (b_mn) {
                   for (int c = 0; c < b_boxes; ++c)
-                    tma_load(sb + c * 64 * kBlockK * 2, &job.b, bn + 64 * c, kk + job.b_k0, pb, bar);
+                    tma_load(sb + c * 64 * kBlockK * 2, map_b, bn + 64 * c, kk + b_k0, pb, bar);
                 } else {
-                  tma_load(sb, &job.b, kk, bn + job.b_row0, pb, bar);
+                  tma_load(sb, map_b, kk, bn, pb, bar);
                 }
                 if (++stage == kStages) {
                   stage = 0;
@@ -692,15 +841,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         uint32_t phase = 0, acc_phase = 0;
         int buffer = 0;
         bool ok = true;
-        while (ok && next_unit() && u.job >= 0) {
-          const Job& job = jobs.job[u.job];
-          const bool a_mn = job.mode == kWeight, b_mn = job.mode == kWeight || job.mode == kHidden;
+        while (ok && next_unit() && u.mode >= 0) {
+          const bool a_mn = u.mode == kWeight, b_mn = u.mode == kWeight || u.mode == kHidden;
+          const int segments = segments_of<PLANES>(u);
           // fp32 accumulator, bf16 operands, majors, N, M = 256
           const uint32_t idesc = 1u << 4 | 1u << 7 | 1u << 10 | uint32_t(a_mn) << 15 | uint32_t(b_mn) << 16 |
                                  uint32_t(u.n / 8) << 17 | uint32_t(256 / 16) << 24;
           const uint64_t a_step = (a_mn ? 16 * 128 : 32) >> 4, b_step = (b_mn ? 16 * 128 : 32) >> 4;
-          const int segment = Shape<PLANES>::segment(job.mode);
-          for (int s = 0; ok && s < u.segments; ++s) {
+          const int segment = Shape<PLANES>::segment(Mode(u.mode));
+          for (int s = 0; ok && s < segments; ++s) {
             const uint32_t d = tmem + buffer * 256;
             if (!(ok = wait(acc_empty + 8 * buffer, acc_phase ^ 1))) break;
             fence_after();
@@ -734,20 +883,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // ---- hands out the units
       if (elect_one()) {
         const int32_t pairs = int32_t(gridDim.x / 2);
-        for (int32_t n = int32_t(blockIdx.x / 2);; n = pairs + atomicAdd(jobs.counter, 1)) {
-          const Unit x = unit_at<PLANES>(jobs, rows, n);
+        Phases phases;
+        for (int32_t n = int32_t(blockIdx.x / 2);; n = pairs + atomicAdd(prog.counter, 1)) {
+          const Unit x = phases.unit(a, prog, rows, n);
           if (!wait(ring_empty + 8 * slot, slot_phase ^ 1)) break;
           for (uint32_t c = 0; c < 2; ++c) {
             const uint32_t to = in_cta(smem_u32(ring + 2 * slot), c);
-            store_remote(to, make_int4(x.job, x.m0, x.n0, x.n));
-            store_remote(to + 16, make_int4(x.k0, x.blocks, x.split, x.segments));
+            store_remote(to, make_int4(x.mode, x.piece, x.m0, x.n0));
+            store_remote(to + 16, make_int4(x.n, x.k0, x.blocks, x.split));
             barrier_arrive_remote(in_cta(ring_full + 8 * slot, c));
           }
           if (++slot == kRing) {
             slot = 0;
             slot_phase ^= 1;
           }
-          if (x.job < 0) break;
+          if (x.mode < 0) break;
         }
       }
     }
@@ -761,7 +911,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t lanes = tmem + (uint32_t((warp & 3) * 32) << 16);
     const uint32_t acc_empty0 = in_cta(acc_empty, 0);
     const float factor = a.head->factor;
-    int buffer = 0;
+    int buffer = 0, used = -1;  // used: the last piece known to be through
     uint32_t phase = 0;
     auto full_accumulator = [&] {
       if (!wait(acc_full + 8 * buffer, phase)) return false;
@@ -777,21 +927,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         phase ^= 1;
       }
     };
+    // A finished unit is counted once its stores are complete, which is waited
+    // for when the next unit is at hand.
+    uint32_t* finished = nullptr;
+    auto count_finished = [&] {
+      if (lane == 0 && finished) {
+        store_wait();
+        progress.arrive(finished);
+      }
+      finished = nullptr;
+    };
     for (;;) {
       const uint32_t entry = in_cta(ring_empty + 8 * slot, 0);
-      if (!__all_sync(~0u, next_unit()) || u.job < 0) break;
-      const Job& job = jobs.job[u.job];
-      const bool logits = job.mode == kForward || job.mode == kGradient;
+      if (!__all_sync(~0u, next_unit()) || u.mode < 0) break;
+      const bool logits = u.mode == kForward || u.mode == kGradient;
       Row r{};
       bool ok = true;
-      if (u.segments == 1) {
-        if (logits) r = row_of<CE, KD>(a, job, rows, u, th, rank);
+      const int segments = segments_of<PLANES>(u);
+      if (logits && segments == 1) r = row_of<CE, KD>(a, rows, u, th, rank);
+      count_finished();
+      if (segments == 1) {
         ok = __all_sync(~0u, full_accumulator());
         if (lane == 0) barrier_arrive_remote(entry);
       } else {
         const int begin = th.half * 128;
         float sum[4][32] = {};
-        for (int s = 0; ok && s < u.segments; ++s) {
+        for (int s = 0; ok && s < segments; ++s) {
           if (!(ok = __all_sync(~0u, full_accumulator()))) break;
           if (s == 0 && lane == 0) barrier_arrive_remote(entry);
           const uint32_t acc = lanes + buffer * 256 + begin;
@@ -802,22 +963,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int j = 0; j < 16; ++j) sum[k / 2][k % 2 * 16 + j] += x[j];
           }
-          if (s == u.segments - 1) {
+          if (s == segments - 1) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) tmem_store32(acc + 32 * k, sum[k]);
           }
-          if (s < u.segments - 1) give_back();
+          if (s < segments - 1) give_back();
         }
-        if (logits) r = row_of<CE, KD>(a, job, rows, u, th, rank);
+        if (logits) r = row_of<CE, KD>(a, rows, u, th, rank);
       }
       if (!ok) break;
+      // The buffer that G goes to has been read by both products of the piece
+      // that was there; dH's sums have their earlier additions.
+      const int earlier = u.mode == kGradient ? u.piece - kBuffers : u.mode == kHidden ? u.piece - 1 : -1;
+      if (earlier >= 0 && earlier > used) {
+        ok = progress.reached(a.used + earlier, 16 * (weight_units(a, earlier) + hidden_units(a, rows)));
+        if (!__all_sync(~0u, ok)) break;
+        used = earlier;
+      }
       const uint32_t acc = lanes + buffer * 256;
-      if (job.mode == kForward) forward_epilogue<CE, KD>(a, u, th, r, acc);
-      else if (job.mode == kGradient) gradient_epilogue<PLANES, CE, KD>(a, job, u, th, r, acc, rank, boxes);
-      else if (job.mode == kHidden) hidden_epilogue(a, job, u, th, rows, acc, rank);
-      else weight_epilogue<PLANES>(a, job, u, th, factor, acc, rank);
+      if (u.mode == kForward) {
+        forward_epilogue<CE, KD>(a, u, th, r, acc);
+      } else if (u.mode == kGradient) {
+        gradient_epilogue<PLANES, CE, KD>(a, &prog.g_out[u.piece % kBuffers], u, th, r, acc, rank, boxes);
+        finished = a.formed + u.piece;
+      } else {
+        if (u.mode == kHidden) hidden_epilogue(&prog.dh, u, th, acc, rank, boxes);
+        else weight_epilogue<PLANES>(a, prog, u, th, factor, acc, rank, boxes);
+        finished = a.used + u.piece;
+      }
       give_back();
     }
+    count_finished();
     if (lane == 0) store_wait();
   }
   __syncwarp();
@@ -830,7 +1006,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 }
 
 template <int PLANES, bool CE, bool KD>
-cudaError_t launch(const Args& a, const Jobs& jobs, int sms, cudaStream_t s) {
+cudaError_t launch(const Args& a, const Program& prog, int sms, cudaStream_t s) {
   auto* kernel = products_kernel<PLANES, CE, KD>;
   // The register shares of the warps must not exceed what the launch brings.
   static const cudaError_t ready = [&] {
@@ -841,19 +1017,19 @@ cudaError_t launch(const Args& a, const Jobs& jobs, int sms, cudaStream_t s) {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<PLANES>::bytes);
   }();
   if (ready != cudaSuccess) return ready;
-  kernel<<<unsigned(sms / 2 * 2), kThreads, Shape<PLANES>::bytes, s>>>(a, jobs);
+  kernel<<<unsigned(sms / 2 * 2), kThreads, Shape<PLANES>::bytes, s>>>(a, prog);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_products(const Args& a, const Jobs& jobs, int sms, cudaStream_t s) {
+cudaError_t launch_products(const Args& a, const Program& prog, int sms, cudaStream_t s) {
   if (a.planes == 1) {
-    if (!a.has_kd) return launch<1, true, false>(a, jobs, sms, s);
-    return a.has_ce ? launch<1, true, true>(a, jobs, sms, s) : launch<1, false, true>(a, jobs, sms, s);
+    if (!a.has_kd) return launch<1, true, false>(a, prog, sms, s);
+    return a.has_ce ? launch<1, true, true>(a, prog, sms, s) : launch<1, false, true>(a, prog, sms, s);
   }
-  if (!a.has_kd) return launch<3, true, false>(a, jobs, sms, s);
-  return a.has_ce ? launch<3, true, true>(a, jobs, sms, s) : launch<3, false, true>(a, jobs, sms, s);
+  if (!a.has_kd) return launch<3, true, false>(a, prog, sms, s);
+  return a.has_ce ? launch<3, true, true>(a, prog, sms, s) : launch<3, false, true>(a, prog, sms, s);
 }
 
 }  // namespace zl
