@@ -221,6 +221,7 @@ int plan(const zero_head_loss_t* p, bool distill, int pass, Args* a, __nv_bfloat
   a->konst = w.take<float>(a->T);
   a->ids = w.take<int32_t>(a->T, a->L);
   a->weights = w.take<float>(a->T, a->L);
+  if (a->K) a->starts = w.take<uint16_t>(2 * a->tiles + 1, a->T);
   a->hp = w.take<__nv_bfloat16>(a->Tp * a->planes, a->Dp);
   if (weight_in_place(p)) {
     *packed_weight = nullptr;

@@ -77,6 +77,7 @@ struct Args {
   float* konst;           // [T] the loss's part that no logit enters
   int32_t* ids;           // [T][L] ascending, kNoId after the last
   float* weights;         // [T][L] weight of each entry's logit in loss and gradient
+  uint16_t* starts;       // distillation: [2 tiles + 1][T] first entry of each half tile
   double* sums;           // [kLossBlocks] parts of the reduced loss
   float* zent;            // [T][L] logits of the entries
   __nv_bfloat16* hp;      // [planes][Tp][Dp] packed hidden states

@@ -17,129 +17,170 @@ __device__ __forceinline__ float warp_sum(float x) {
 
 // ------------------------------------------------------------------- rows --
 
-// One warp per row: its terms, and its sparse entries -- the ids whose logits
-// enter the loss one by one -- with the weights c in
+// Rows are prepared for the products: each row's terms, and its sparse entries
+// -- the ids whose logits enter the loss one by one -- with the weights c in
 //   loss = ce*lse + kd*tau*lse' + konst - sum_e c_e z_e,
 //   dloss/dz_v = ce*p_v + kd*p'_v - sum_{e: id_e = v} c_e
-// (c = ce for the label, kd*q for a teacher entry; kd = alpha*tau). Equal ids
-// are merged, in entry order, and the ids are sorted so that a tile's entries
-// are found by bisection.
-__device__ __forceinline__ void prepare_row(const Args& a, int64_t t, int32_t* sh) {
-  const int lane = threadIdx.x & 31;
-  const int K = a.K;
-  int64_t y = a.has_ce ? a.labels[t] : -1;
-  const bool has_y = a.has_ce && y != a.ignore_index && y >= 0 && y < a.V;
-  int32_t* ids = a.ids + t * a.L;
-  float* weights = a.weights + t * a.L;
-  bool has_kd = false;
-  if (K == 0) {
-    if (lane == 0) {
-      ids[0] = has_y ? int32_t(y) : kNoId;
-      weights[0] = a.ce;
-      a.konst[t] = 0.0f;
-    }
-  } else {
-    int32_t* id = sh;
-    float* c = reinterpret_cast<float*>(id + (K + 1));
-    int32_t* id2 = id + 2 * (K + 1);
-    float* c2 = reinterpret_cast<float*>(id + 3 * (K + 1));
-    float top = -INFINITY;
-    for (int k = lane; k < K; k += 32) {
-      const int64_t v = a.teacher_ids[t * K + k];
-      const float u = a.teacher_logits[t * K + k] / float(a.tau);
-      const bool there = v >= 0 && v < a.V && u != -INFINITY;
-      id[k] = there ? int32_t(v) : kNoId;
-      c[k] = u;
-      if (there) {
-        has_kd = true;
-        top = fmaxf(top, u);
-      }
-    }
-    has_kd = __any_sync(~0u, has_kd);
-    top = warp_max(top);
-    float sum = 0.0f;
-    for (int k = lane; k < K; k += 32) {
-      const float e = id[k] == kNoId ? 0.0f : expf(c[k] - top);
-      c[k] = e;
-      sum += e;
-    }
-    sum = warp_sum(sum);
-    float entropy = 0.0f;
-    for (int k = lane; k < K; k += 32) {
-      const float q = has_kd ? c[k] / sum : 0.0f;
-      if (q != 0.0f) entropy += q * logf(q);
-      c[k] = a.kd * q;
-    }
-    entropy = warp_sum(entropy);
-    __syncwarp();
-    bool found = false;
-    for (int k = lane; k < K; k += 32) {
-      const int32_t v = id[k];
-      float w = 0.0f;
-      bool first = v != kNoId;
-      for (int j = 0; first && j < K; ++j) {
-        if (id[j] != v) continue;
-        if (j < k) first = false;
-        w += c[j];
-      }
-      if (first && has_y && v == y) {
-        w += a.ce;
-        found = true;
-      }
-      id2[k] = first ? v : kNoId;
-      c2[k] = w;
-    }
-    found = __any_sync(~0u, found);
-    if (lane == 0) {
-      id2[K] = has_y && !found ? int32_t(y) : kNoId;
-      c2[K] = a.ce;
-      a.konst[t] = has_kd ? float(double(a.kd) * a.tau * entropy) : 0.0f;
-    }
-    __syncwarp();
-    int kept = 0;
-    for (int k = lane; k <= K; k += 32) kept += id2[k] != kNoId;
-    kept = __reduce_add_sync(~0u, kept);
-    for (int k = lane; k <= K; k += 32) {
-      const int32_t v = id2[k];
-      if (v == kNoId) continue;
-      int rank = 0;
-      for (int j = 0; j <= K; ++j) rank += id2[j] < v;
-      ids[rank] = v;
-      weights[rank] = c2[k];
-    }
-    for (int k = kept + lane; k < a.L; k += 32) {
-      ids[k] = kNoId;
-      weights[k] = 0.0f;
-    }
-  }
-  if (lane == 0) {
-    a.coef[t] = make_float2(has_y ? a.ce : 0.0f, has_kd ? a.kd : 0.0f);
-    a.rowpos[t] = has_y || has_kd ? 0 : -1;
-    if (a.forward && !(has_y || has_kd)) {
-      a.loss[t] = 0.0f;
-      if (a.has_ce) a.lse[t] = 0.0f;
-      if (a.has_kd) a.lse_tau[t] = 0.0f;
-    }
+// (c = ce for the label, kd*q for a teacher entry; kd = alpha*tau).
+
+__device__ __forceinline__ int64_t label_of(const Args& a, int64_t t) {  // -1: none
+  if (!a.has_ce) return -1;
+  const int64_t y = a.labels[t];
+  return y != a.ignore_index && y >= 0 && y < a.V ? y : -1;
+}
+
+__device__ __forceinline__ void finish_row(const Args& a, int64_t t, bool has_y, bool has_kd, float konst) {
+  a.konst[t] = konst;
+  a.coef[t] = make_float2(has_y ? a.ce : 0.0f, has_kd ? a.kd : 0.0f);
+  a.rowpos[t] = has_y || has_kd ? 0 : -1;
+  if (a.forward && !(has_y || has_kd)) {
+    a.loss[t] = 0.0f;
+    if (a.has_ce) a.lse[t] = 0.0f;
+    if (a.has_kd) a.lse_tau[t] = 0.0f;
   }
 }
 
-__global__ void rows_kernel(const Args a) {
-  extern __shared__ int32_t sh[];
-  const int warp = threadIdx.x >> 5;
-  const int64_t t = int64_t(blockIdx.x) * (blockDim.x >> 5) + warp;
-  if (t < a.T) prepare_row(a, t, sh + warp * 4 * (a.K + 1));
+// Cross entropy: the label is the only entry. One thread per row.
+__device__ __forceinline__ void prepare_label(const Args& a, int64_t t) {
+  const int64_t y = label_of(a, t);
+  a.ids[t] = y >= 0 ? int32_t(y) : kNoId;
+  a.weights[t] = a.ce;
+  finish_row(a, t, y >= 0, false, 0.0f);
+}
+
+// Distillation: one warp per row. The entries are sorted by id, equal ids
+// merged (in the order given, the label last), so that a tile's entries are a
+// range of them. `id` and `c` hold n4 = K + 1 rounded up to 4 values each, as
+// do `sid` and `sc`, in shared memory. Leaves the merged ids in `id`, ended by
+// kNoId, and returns their number.
+__device__ __forceinline__ int prepare_teacher(const Args& a, int64_t t, int n4, int32_t* id, float* c, int32_t* sid,
+                                               float* sc) {
+  const int lane = threadIdx.x & 31, K = a.K;
+  const int64_t y = label_of(a, t);
+  bool has_kd = false;
+  float top = -INFINITY;
+  for (int k = lane; k < K; k += 32) {
+    const int64_t v = a.teacher_ids[t * K + k];
+    const float u = a.teacher_logits[t * K + k] / float(a.tau);
+    const bool there = v >= 0 && v < a.V && u != -INFINITY;
+    id[k] = there ? int32_t(v) : kNoId;
+    c[k] = u;
+    if (there) {
+      has_kd = true;
+      top = fmaxf(top, u);
+    }
+  }
+  for (int k = K + lane; k < n4; k += 32) {
+    id[k] = k == K && y >= 0 ? int32_t(y) : kNoId;
+    c[k] = a.ce;
+  }
+  has_kd = __any_sync(~0u, has_kd);
+  top = warp_max(top);
+  float sum = 0.0f;
+  for (int k = lane; k < K; k += 32) {
+    const float e = id[k] == kNoId ? 0.0f : expf(c[k] - top);
+    c[k] = e;
+    sum += e;
+  }
+  sum = warp_sum(sum);
+  float entropy = 0.0f;
+  for (int k = lane; k < K; k += 32) {
+    const float q = has_kd ? c[k] / sum : 0.0f;
+    if (q != 0.0f) entropy += q * logf(q);
+    c[k] = a.kd * q;
+  }
+  entropy = warp_sum(entropy);
+  __syncwarp();
+  // Each entry's place: the entries before it by id, then by position. Four
+  // entries a lane at a time against all of them.
+  for (int k0 = 0; k0 < n4; k0 += 128) {
+    int32_t mine[4];
+    int place[4] = {};
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int k = k0 + lane + 32 * q;
+      mine[q] = k < n4 ? id[k] : kNoId;
+    }
+    for (int j = 0; j < n4; j += 4) {
+      const int4 v = *reinterpret_cast<const int4*>(id + j);
+      const int32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        if (k0 + 32 * q >= n4) break;
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          place[q] += w[r] < mine[q] || (w[r] == mine[q] && j + r < k0 + lane + 32 * q);
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int k = k0 + lane + 32 * q;
+      if (k < n4) {
+        sid[place[q]] = mine[q];
+        sc[place[q]] = c[k];
+      }
+    }
+  }
+  __syncwarp();
+  int kept = 0;
+  for (int p0 = 0; p0 < n4; p0 += 32) {
+    const int p = p0 + lane;
+    const int32_t v = p < n4 ? sid[p] : kNoId;
+    const bool first = v != kNoId && (p == 0 || sid[p - 1] != v);
+    const unsigned mask = __ballot_sync(~0u, first);
+    if (first) {
+      float w = sc[p];
+      for (int q = p + 1; q < n4 && sid[q] == v; ++q) w += sc[q];
+      const int at = kept + __popc(mask & ((1u << lane) - 1));
+      id[at] = v;
+      a.ids[t * a.L + at] = v;
+      a.weights[t * a.L + at] = w;
+    }
+    kept += __popc(mask);
+  }
+  for (int k = kept + lane; k < a.L; k += 32) a.ids[t * a.L + k] = kNoId;
+  if (lane == 0) finish_row(a, t, y >= 0, has_kd, has_kd ? float(double(a.kd) * a.tau * entropy) : 0.0f);
+  return kept;
+}
+
+__global__ void __launch_bounds__(256) label_rows_kernel(const Args a) {
+  const int64_t t = int64_t(blockIdx.x) * 256 + threadIdx.x;
+  if (t < a.T) prepare_label(a, t);
+}
+
+// A block's rows, one a warp, and where each half tile's entries begin in
+// them: starts[h][t] is the first entry with an id of 128 h at least.
+__global__ void teacher_rows_kernel(const Args a) {
+  extern __shared__ __align__(16) int32_t sh[];
+  __shared__ int kept[16];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rows = blockDim.x >> 5;
+  const int n4 = (a.K + 4) / 4 * 4;
+  const int64_t t0 = int64_t(blockIdx.x) * rows, t = t0 + warp;
+  int32_t* id = sh + warp * 4 * n4;
+  if (t < a.T) {
+    const int n = prepare_teacher(a, t, n4, id, reinterpret_cast<float*>(id + n4), id + 2 * n4,
+                                  reinterpret_cast<float*>(id + 3 * n4));
+    if (lane == 0) kept[warp] = n;
+  }
+  __syncthreads();
+  const int64_t halves = 2 * a.tiles + 1;
+  const int there = int(min(int64_t(rows), a.T - t0));
+  for (int64_t x = threadIdx.x; x < halves * rows; x += blockDim.x) {
+    const int r = int(x % rows);
+    const int64_t h = x / rows;
+    if (r < there) a.starts[h * a.T + t0 + r] = uint16_t(first_entry(sh + r * 4 * n4, kept[r], h * 128));
+  }
 }
 
 // One block: numbers the rows that have a target, in order, up to 16 times
-// 1024 rows at a time. With `Prepare` (few rows) it prepares them first, which
-// saves a launch.
+// 1024 rows at a time. With `Prepare` (few rows, labels alone) it prepares them
+// first, which saves a launch.
 template <bool Prepare>
 __global__ void __launch_bounds__(1024) number_rows_kernel(const Args a) {
-  extern __shared__ int32_t sh[];
   __shared__ int32_t before[16][32], total[16];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (Prepare) {
-    for (int64_t t = warp; t < a.T; t += 32) prepare_row(a, t, sh + warp * 4 * (a.K + 1));
+    for (int64_t t = threadIdx.x; t < a.T; t += 1024) prepare_label(a, t);
     __syncthreads();
   }
   for (int64_t n = threadIdx.x; n < a.zeros; n += 1024) a.counters[n] = 0;
@@ -301,16 +342,17 @@ __global__ void __launch_bounds__(256) dhidden_out_kernel(const Args a) {
 // ------------------------------------------------------------------- losses --
 
 // The row's log-sum-exp from its partial maxima and sums (maxima in powers of
-// two): 8 lanes of a row, each every eighth partial, eight loads in flight.
-__device__ __forceinline__ double row_lse(const float2* stats, int64_t count, int64_t Tp, int64_t i,
-                                          int lane, float2 (*sh)[33], int r) {
+// two): each of the row's lanes takes every lanes-th partial, eight loads in
+// flight; the first lane joins them.
+__device__ __forceinline__ double row_lse(const float2* stats, int64_t count, int64_t Tp, int64_t i, int lane,
+                                          int lanes, float2* sh, int r, int rows) {
   float m = -INFINITY, s = 0.0f;
-  for (int64_t j0 = lane; j0 < count; j0 += 64) {
+  for (int64_t j0 = lane; j0 < count; j0 += 8 * lanes) {
     float2 x[8];
     float top = m;
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
-      x[q] = j0 + 8 * q < count ? stats[(j0 + 8 * q) * Tp + i] : make_float2(-INFINITY, 0.0f);
+      x[q] = j0 + lanes * q < count ? stats[(j0 + lanes * q) * Tp + i] : make_float2(-INFINITY, 0.0f);
       top = fmaxf(top, x[q].x);
     }
     if (top == -INFINITY) {
@@ -324,55 +366,64 @@ __device__ __forceinline__ double row_lse(const float2* stats, int64_t count, in
     for (int q = 0; q < 8; ++q) s += x[q].y * exp2f(x[q].x - top);  // 0 where x is -inf
     m = top;
   }
-  sh[lane][r] = make_float2(m, s);
+  // A tree over the lanes, in a fixed order.
+  sh[lane * rows + r] = make_float2(m, s);
   __syncthreads();
-  float top = -INFINITY, sum = 0.0f;
-  if (lane == 0) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) top = fmaxf(top, sh[j][r].x);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) sum += top == -INFINITY ? sh[j][r].y : sh[j][r].y * exp2f(sh[j][r].x - top);
+  for (int w = lanes / 2; w; w >>= 1) {
+    if (lane < w) {
+      const float2 x = sh[lane * rows + r], y = sh[(lane + w) * rows + r];
+      const float top = fmaxf(x.x, y.x);
+      const float sum = top == -INFINITY ? x.y + y.y : x.y * exp2f(x.x - top) + y.y * exp2f(y.x - top);
+      sh[lane * rows + r] = make_float2(top, sum);
+    }
+    __syncthreads();
   }
+  const float2 x = sh[r];
   __syncthreads();
-  return lane == 0 ? (double(top) + log2(double(sum))) * 0.69314718055994530942 : 0.0;
+  return lane == 0 ? (double(x.x) + log2(double(x.y))) * 0.69314718055994530942 : 0.0;
 }
 
-__global__ void __launch_bounds__(256) losses_kernel(const Args a) {
-  __shared__ float2 sh[8][33];
+// 256 threads: `block_rows` rows (a power of two, up to 32), 256 / block_rows lanes each.
+__global__ void __launch_bounds__(256) losses_kernel(const Args a, int block_rows) {
+  __shared__ float2 sh[256];
   __shared__ double part[256];
   __shared__ bool last;
-  const int r = threadIdx.x & 31, lane = threadIdx.x >> 5;
+  const int r = threadIdx.x % block_rows, lane = threadIdx.x / block_rows, lanes = 256 / block_rows;
   const int32_t rows = a.head->rows;
   double mine = 0.0;
-  for (int64_t i0 = int64_t(blockIdx.x) * 32; i0 < rows; i0 += int64_t(gridDim.x) * 32) {
-    const int64_t i = i0 + r;
-    const int64_t at = min(i, int64_t(rows) - 1);
-    const double lse = a.has_ce ? row_lse(a.stats, 2 * a.tiles, a.Tp, at, lane, sh, r) : 0.0;
-    const double lse_tau = a.has_kd ? row_lse(a.stats_tau, 2 * a.tiles, a.Tp, at, lane, sh, r) : 0.0;
-    if (lane == 0 && i < rows) {
-      const int64_t t = a.rowmap[i];
+  for (int64_t i0 = int64_t(blockIdx.x) * block_rows; i0 < rows; i0 += int64_t(gridDim.x) * block_rows) {
+    const int64_t i = min(i0 + r, int64_t(rows) - 1);
+    const int64_t t = a.rowmap[i];
+    double entries = 0.0;
+    for (int e = lane; e < a.L; e += lanes)
+      if (a.ids[t * a.L + e] != kNoId) entries += double(a.weights[t * a.L + e]) * double(a.zent[t * a.L + e]);
+    part[threadIdx.x] = entries;
+    const double lse = a.has_ce ? row_lse(a.stats, 2 * a.tiles, a.Tp, i, lane, lanes, sh, r, block_rows) : 0.0;
+    const double lse_tau =
+        a.has_kd ? row_lse(a.stats_tau, 2 * a.tiles, a.Tp, i, lane, lanes, sh, r, block_rows) : 0.0;
+    if (lane == 0 && i0 + r < rows) {
       const float2 f = a.coef[t];
       double loss = double(a.konst[t]);
       if (f.x != 0.0f) loss += double(f.x) * lse;
       if (f.y != 0.0f) loss += double(f.y) * a.tau * lse_tau;
-      for (int e = 0; e < a.L && a.ids[t * a.L + e] != kNoId; ++e)
-        loss -= double(a.weights[t * a.L + e]) * double(a.zent[t * a.L + e]);
+      for (int q = 0; q < min(lanes, a.L); ++q) loss -= part[q * block_rows + r];
       if (a.head->fault) loss = NAN;
       a.loss[t] = float(loss);
       if (a.has_ce) a.lse[t] = float(lse);
       if (a.has_kd) a.lse_tau[t] = float(lse_tau);
       mine += double(float(loss));
     }
+    __syncthreads();
   }
   if (a.reduction == ZERO_REDUCE_NONE) return;
-  // Each block's sum in lane order; the last block to finish adds the blocks'.
-  if (lane == 0) {
-    for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(~0u, mine, o);
-    if (r == 0) {
-      a.sums[blockIdx.x] = mine;
-      __threadfence();
-      last = atomicAdd(&a.head->ticket, 1) == int32_t(gridDim.x) - 1;
-    }
+  // Each block's sum in a fixed order; the last block to finish adds the blocks'.
+  part[threadIdx.x] = mine;  // zero but for the rows' first lanes
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int q = 1; q < block_rows; ++q) mine += part[q];
+    a.sums[blockIdx.x] = mine;
+    __threadfence();
+    last = atomicAdd(&a.head->ticket, 1) == int32_t(gridDim.x) - 1;
   }
   __syncthreads();
   if (!last) return;
@@ -406,15 +457,18 @@ bool aligned16(const void* p, int64_t stride_bytes) {
 }  // namespace
 
 cudaError_t launch_rows(const Args& a, cudaStream_t s) {
-  // Few rows: one block prepares them too (32 warps, a row each at a time).
-  const size_t row = a.K ? size_t(16) * (a.K + 1) : 0;
-  if (a.T <= 256 && 32 * row <= 48 * 1024) {
-    number_rows_kernel<true><<<1, 1024, 32 * row, s>>>(a);
+  if (a.K == 0 && a.T <= 2048) {
+    number_rows_kernel<true><<<1, 1024, 0, s>>>(a);
     return cudaGetLastError();
   }
   if (a.T > 0) {
-    const int warps = a.K > 256 ? 1 : 4;
-    rows_kernel<<<unsigned((a.T + warps - 1) / warps), warps * 32, warps * row, s>>>(a);
+    if (a.K == 0) {
+      label_rows_kernel<<<unsigned((a.T + 255) / 256), 256, 0, s>>>(a);
+    } else {
+      const size_t row = size_t(16) * ((a.K + 4) / 4 * 4);
+      const int rows = 16 * row <= 48 * 1024 ? 16 : 2;
+      teacher_rows_kernel<<<unsigned((a.T + rows - 1) / rows), rows * 32, rows * row, s>>>(a);
+    }
   }
   number_rows_kernel<false><<<1, 1024, 0, s>>>(a);
   return cudaGetLastError();
@@ -445,8 +499,11 @@ cudaError_t launch_pack_weight(const Args& a, __nv_bfloat16* to, cudaStream_t s)
 }
 
 cudaError_t launch_losses(const Args& a, cudaStream_t s) {
-  const int64_t blocks = (a.T + 31) / 32;
-  losses_kernel<<<unsigned(blocks < 1 ? 1 : blocks < kLossBlocks ? blocks : kLossBlocks), 256, 0, s>>>(a);
+  // As many lanes to a row as leave a block for each SM.
+  int rows = 32;
+  while (rows > 1 && a.T / rows < 152) rows /= 2;
+  const int64_t blocks = (a.T + rows - 1) / rows;
+  losses_kernel<<<unsigned(blocks < 1 ? 1 : blocks < kLossBlocks ? blocks : kLossBlocks), 256, 0, s>>>(a, rows);
   return cudaGetLastError();
 }
 

@@ -392,17 +392,23 @@ struct Row {
   int i;                   // compact row
   int64_t t;
   bool there;
-  int e;                   // its next sparse entry
-  int32_t id;
+  int e, end;              // its sparse entries in the thread's columns
+  int32_t id, next_id;     // of entry e and the one after it
+  float w, next_w;         // their weights (kGradient)
   float scale, w_ce, w_kd, lse, lse_kd;  // kGradient
 };
+
+__device__ __forceinline__ void entry_ahead(const Args& a, const Unit& u, const Row& r, int e, int32_t& id, float& w) {
+  id = e < r.end ? a.ids[r.t * a.L + e] : kNoId;
+  w = e < r.end && u.mode == kGradient ? a.weights[r.t * a.L + e] : 0.0f;
+}
 
 template <bool CE, bool KD>
 __device__ __forceinline__ Row row_of(const Args& a, int rows, const Unit& u, const Thread& th, uint32_t rank) {
   Row r{};
   r.i = u.m0 + int(rank) * kHalf + th.row;
   r.there = r.i < rows;
-  r.id = kNoId;
+  r.id = r.next_id = kNoId;
   r.lse = r.lse_kd = INFINITY;
   if (!r.there) return r;
   r.t = a.rowmap[r.i];
@@ -415,28 +421,39 @@ __device__ __forceinline__ Row row_of(const Args& a, int rows, const Unit& u, co
     r.w_ce = f.x * r.scale;
     r.w_kd = f.y * r.scale;
   }
-  const int32_t* ids = a.ids + r.t * a.L;
   const int64_t v = u.piece * a.piece + u.n0 + th.half * 128;
-  r.e = a.L == 1 ? 0 : first_entry(ids, a.L, v);
-  r.id = r.e < a.L ? ids[r.e] : kNoId;
-  if (r.id < v) r.id = kNoId;
+  if (a.K == 0) {
+    r.id = a.ids[r.t];
+    if (u.mode == kGradient) r.w = a.weights[r.t];
+    r.end = 1;
+    if (r.id < v) r.id = kNoId;
+  } else {
+    const uint16_t* at = a.starts + v / 128 * a.T + r.t;
+    r.e = at[0];
+    r.end = at[a.T];
+    entry_ahead(a, u, r, r.e, r.id, r.w);
+    entry_ahead(a, u, r, r.e + 1, r.next_id, r.next_w);
+  }
   return r;
 }
 
-// Calls f(entry, column) for each of the row's sparse entries with a column in
-// [begin, end) relative to v0, with the column's logit read from the
+// Calls f(column, logit) for each of the row's sparse entries (r.e, weight
+// r.w) with a column below `end` relative to v0, the logit read from the
 // accumulator: all lanes of the warp read the same column, lowest first.
 template <typename F>
-__device__ __forceinline__ void each_entry(const Args& a, Row& r, int64_t v0, int end, uint32_t acc, F f) {
+__device__ __forceinline__ void each_entry(const Args& a, const Unit& u, Row& r, int64_t v0, int end, uint32_t acc,
+                                           F f) {
   for (;;) {
     const int mine = r.id < v0 + end ? int(r.id - v0) : 0x7fffffff;
     const int c = __reduce_min_sync(~0u, mine);
     if (c == 0x7fffffff) break;
     const float z = tmem_load1(acc + c);
     if (mine == c) {
-      f(r.e, c, z);
+      f(c, z);
       ++r.e;
-      r.id = r.e < a.L ? a.ids[r.t * a.L + r.e] : kNoId;
+      r.id = r.next_id;
+      r.w = r.next_w;
+      entry_ahead(a, u, r, r.e + 1, r.next_id, r.next_w);
     }
     __syncwarp();
   }
@@ -487,7 +504,7 @@ __device__ __forceinline__ void forward_epilogue(const Args& a, const Unit& u, c
     if (CE) add_exponentials(z, top, c_ce, m_ce, sum);
     if (KD) add_exponentials(z, top, c_kd, m_kd, sum_kd);
   }
-  each_entry(a, r, v0, begin + 128, acc, [&](int k, int, float z) { a.zent[r.t * a.L + k] = z; });
+  each_entry(a, u, r, v0, begin + 128, acc, [&](int, float z) { a.zent[r.t * a.L + r.e] = z; });
   if (!r.there) return;
   const int64_t at = (v0 / 256 * 2 + th.half) * a.Tp + r.i;
   const bool nan = isnan(sum + sum_kd);
@@ -582,8 +599,8 @@ __device__ __forceinline__ void gradient_epilogue(const Args& a, const CUtensorM
               make_uint4(word[0][p], word[1][p], word[2][p], word[3][p]);
       }
     }
-    each_entry(a, r, v0, begin + 64 * (b + 1), acc, [&](int k, int c, float z) {
-      const float g = value(z) - r.scale * a.weights[r.t * a.L + k];
+    each_entry(a, u, r, v0, begin + 64 * (b + 1), acc, [&](int c, float z) {
+      const float g = value(z) - r.scale * r.w;
       const int at = c - begin - 64 * b;
       uint8_t* to = box + lane * 128 + (((at / 8) ^ (lane & 7)) * 16) + (at % 8) * 2;
       uint32_t word[PLANES];
@@ -686,17 +703,24 @@ __device__ __forceinline__ void weight_epilogue(const Args& a, const Program& pr
     }
     return;
   }
-  T* to = static_cast<T*>(a.dweight) + v * a.dweight_stride + u.n0;
+  // 32 columns at a time through shared memory, so that a warp's accesses run
+  // along a row.
+  const int64_t v_warp = v - lane;
+  float* box = reinterpret_cast<float*>(staging);
 #pragma unroll 1
   for (int c = begin; c < min(u.n, begin + 128); c += 32) {
     float x[32];
     load_terms(u, acc + c, x);
-    const int valid = v < a.V ? int(min(int64_t(32), a.D - u.n0 - c)) : 0;
-#pragma unroll
-    for (int j = 0; j < 32; ++j) {
-      if (j >= valid) break;
-      const float y = factor * x[j];
-      to[c + j] = T(a.accumulate ? float(to[c + j]) + y : y);
+    __syncwarp();
+    stage_fp32(staging, lane, x);
+    __syncwarp();
+    const bool in = u.n0 + c + lane < a.D;
+    T* to = static_cast<T*>(a.dweight) + v_warp * a.dweight_stride + u.n0 + c + lane;
+#pragma unroll 4
+    for (int i = 0; i < 32; ++i, to += a.dweight_stride) {
+      if (!in || v_warp + i >= a.V) continue;
+      const float y = factor * box[i * 32 + (((lane / 4) ^ (i & 7)) * 4) + lane % 4];
+      *to = T(a.accumulate ? float(*to) + y : y);
     }
   }
 }
