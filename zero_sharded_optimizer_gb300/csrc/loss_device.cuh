@@ -22,15 +22,10 @@ __device__ __forceinline__ void split(float x, __nv_bfloat16 (&part)[3]) {
   part[2] = __float2bfloat16_rn(r - __bfloat162float(part[1]));
 }
 
-// First entry of the row whose id is not below v.
-__device__ __forceinline__ int first_entry(const int32_t* ids, int L, int64_t v) {
-  int lo = 0, hi = L;
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (ids[mid] < v) lo = mid + 1;
-    else hi = mid;
-  }
-  return lo;
-}
+// Programmatic launches: every kernel of a call lets the next one start when
+// its own blocks run, and waits for the one before it (complete, and so for all
+// before that) before it touches what they wrote.
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 }  // namespace zl

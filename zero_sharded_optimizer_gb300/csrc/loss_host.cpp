@@ -309,14 +309,17 @@ bool tensor_map(CUtensorMap* map, const void* base, int64_t cols, int64_t rows, 
 bool make_program(const Args& a, bool backward, Program* p) {
   const bool f32 = a.planes == 3;
   const int64_t wide = a.wp_plane ? a.Dp : a.D;
-  bool ok = tensor_map(&p->hidden, a.hp, a.Dp, a.Tp, a.Dp, a.planes, a.Tp * a.Dp, 128) &&
+  // With few rows the rest of a tile's rows is not fetched: what the products
+  // make of whatever lies there is not read.
+  p->box_rows = int32_t(std::min<int64_t>(round_up(std::max<int64_t>(a.T, 1), 8), 128));
+  bool ok = tensor_map(&p->hidden, a.hp, a.Dp, a.Tp, a.Dp, a.planes, a.Tp * a.Dp, p->box_rows) &&
             tensor_map(&p->weight, a.wp, wide, a.V, a.wp_ld, a.planes, a.wp_plane, 128);
   if (!backward) return ok;
   ok = ok && tensor_map(&p->hidden_mn, a.hp, a.Dp, a.Tp, a.Dp, a.planes, a.Tp * a.Dp, 64) &&
        tensor_map(&p->weight_mn, a.wp, wide, a.V, a.wp_ld, a.planes, a.wp_plane, 64);
   for (int b = 0; b < zl::kBuffers; ++b) {
     CUtensorMap* const to[3] = {&p->g[b], &p->g_mn[b], &p->g_out[b]};
-    const uint32_t box[3] = {128, 64, 32};
+    const uint32_t box[3] = {uint32_t(p->box_rows), 64, 32};
     for (int i = 0; i < 3; ++i)
       ok = ok && tensor_map(to[i], a.g[b], a.piece, a.Tp, a.piece, a.planes, a.Tp * a.piece, box[i]);
   }
@@ -368,8 +371,7 @@ int run(const zero_head_loss_t* p, bool distill, int pass, cudaStream_t s) {
     what = name;
     e = launch();
   };
-  next("packing hidden", [&] { return zl::launch_pack_hidden(a, s); });
-  if (packed) next("packing weight", [&] { return zl::launch_pack_weight(a, packed, s); });
+  next("packing", [&] { return zl::launch_pack(a, packed, s); });
   if (pass & kForward) {
     program.forward = 1;
     program.counter = a.counters;

@@ -20,7 +20,7 @@ int set_error(int code, const char* fmt, ...);
 constexpr int kTileM = 256;
 constexpr int kTileN = 256;
 constexpr int kPadD = 64;       // packed operands are padded to this width
-constexpr int32_t kNoId = 0x7fffffff;
+constexpr int32_t kNoId = 0x7ffffffe;  // above every id, and so is kNoId + 1
 constexpr int kBuffers = 3;      // of G
 constexpr int kLossBlocks = 608; // most blocks of the losses' kernel
 
@@ -100,20 +100,21 @@ struct Args {
 enum Mode : int32_t { kForward, kGradient, kHidden, kWeight };
 
 struct Program {
-  // Operands read along K (boxes of 128 rows) and across it (_mn, boxes of 64
-  // rows of K); G, the sums of dhidden and dweight as a warp writes them.
+  // Operands read along K (boxes of 128 rows, box_rows of them for the rows with
+  // a target) and across it (_mn, boxes of 64 rows of K); G, the sums of dhidden and dweight as a warp writes them.
   CUtensorMap hidden, hidden_mn, weight, weight_mn;
   CUtensorMap g[kBuffers], g_mn[kBuffers], g_out[kBuffers];
   CUtensorMap dh, dweight;
   int32_t forward;     // the forward pass (else the backward pass)
+  int32_t box_rows;    // rows of the boxes of `hidden` and `g`: 128, or fewer for few rows
   int32_t pieces;
   int32_t weight_tma;  // dweight can be written by TMA
   int32_t* counter;    // units handed out
 };
 
 cudaError_t launch_rows(const Args& a, cudaStream_t s);
-cudaError_t launch_pack_hidden(const Args& a, cudaStream_t s);
-cudaError_t launch_pack_weight(const Args& a, __nv_bfloat16* to, cudaStream_t s);
+// Rows with a target side by side, and the weight's rows to `weight` (NULL: read in place).
+cudaError_t launch_pack(const Args& a, __nv_bfloat16* weight, cudaStream_t s);
 cudaError_t launch_losses(const Args& a, cudaStream_t s);
 cudaError_t launch_dhidden_out(const Args& a, cudaStream_t s);
 cudaError_t launch_products(const Args& a, const Program& prog, int sms, cudaStream_t s);

@@ -17,6 +17,17 @@ __device__ __forceinline__ float warp_sum(float x) {
 
 // ------------------------------------------------------------------- rows --
 
+// First entry of the row whose id is not below v.
+__device__ __forceinline__ int first_entry(const int32_t* ids, int L, int32_t v) {
+  int lo = 0, hi = L;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (ids[mid] < v) lo = mid + 1;
+    else hi = mid;
+  }
+  return lo;
+}
+
 // Rows are prepared for the products: each row's terms, and its sparse entries
 // -- the ids whose logits enter the loss one by one -- with the weights c in
 //   loss = ce*lse + kd*tau*lse' + konst - sum_e c_e z_e,
@@ -63,7 +74,7 @@ __device__ __forceinline__ int prepare_teacher(const Args& a, int64_t t, int n4,
     const int64_t v = a.teacher_ids[t * K + k];
     const float u = a.teacher_logits[t * K + k] / float(a.tau);
     const bool there = v >= 0 && v < a.V && u != -INFINITY;
-    id[k] = there ? int32_t(v) : kNoId;
+    id[k] = there ? int32_t(v) : kNoId;  // (ids end below kNoId - 1, so that one can be added)
     c[k] = u;
     if (there) {
       has_kd = true;
@@ -99,7 +110,7 @@ __device__ __forceinline__ int prepare_teacher(const Args& a, int64_t t, int n4,
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const int k = k0 + lane + 32 * q;
-      mine[q] = k < n4 ? id[k] : kNoId;
+      mine[q] = k < n4 ? id[k] : 0;
     }
     for (int j = 0; j < n4; j += 4) {
       const int4 v = *reinterpret_cast<const int4*>(id + j);
@@ -109,7 +120,7 @@ __device__ __forceinline__ int prepare_teacher(const Args& a, int64_t t, int n4,
         if (k0 + 32 * q >= n4) break;
 #pragma unroll
         for (int r = 0; r < 4; ++r)
-          place[q] += w[r] < mine[q] || (w[r] == mine[q] && j + r < k0 + lane + 32 * q);
+          place[q] += w[r] < mine[q] + (j + r < k0 + lane + 32 * q);
       }
     }
 #pragma unroll
@@ -144,6 +155,7 @@ __device__ __forceinline__ int prepare_teacher(const Args& a, int64_t t, int n4,
 }
 
 __global__ void __launch_bounds__(256) label_rows_kernel(const Args a) {
+  let_next_start();
   const int64_t t = int64_t(blockIdx.x) * 256 + threadIdx.x;
   if (t < a.T) prepare_label(a, t);
 }
@@ -153,6 +165,7 @@ __global__ void __launch_bounds__(256) label_rows_kernel(const Args a) {
 __global__ void teacher_rows_kernel(const Args a) {
   extern __shared__ __align__(16) int32_t sh[];
   __shared__ int kept[16];
+  let_next_start();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rows = blockDim.x >> 5;
   const int n4 = (a.K + 4) / 4 * 4;
   const int64_t t0 = int64_t(blockIdx.x) * rows, t = t0 + warp;
@@ -163,13 +176,12 @@ __global__ void teacher_rows_kernel(const Args a) {
     if (lane == 0) kept[warp] = n;
   }
   __syncthreads();
-  const int64_t halves = 2 * a.tiles + 1;
-  const int there = int(min(int64_t(rows), a.T - t0));
-  for (int64_t x = threadIdx.x; x < halves * rows; x += blockDim.x) {
-    const int r = int(x % rows);
-    const int64_t h = x / rows;
-    if (r < there) a.starts[h * a.T + t0 + r] = uint16_t(first_entry(sh + r * 4 * n4, kept[r], h * 128));
-  }
+  const int halves = int(2 * a.tiles + 1), r = threadIdx.x & (rows - 1);  // rows: a power of two
+  if (t0 + r >= a.T) return;
+  const int32_t* ids = sh + r * 4 * n4;
+  const int n = kept[r];
+  for (int h = threadIdx.x / rows; h < halves; h += 32)
+    a.starts[h * a.T + t0 + r] = uint16_t(first_entry(ids, n, h * 128));
 }
 
 // One block: numbers the rows that have a target, in order, up to 16 times
@@ -179,6 +191,8 @@ template <bool Prepare>
 __global__ void __launch_bounds__(1024) number_rows_kernel(const Args a) {
   __shared__ int32_t before[16][32], total[16];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  let_next_start();
+  if (!Prepare) wait_for_previous();
   if (Prepare) {
     for (int64_t t = threadIdx.x; t < a.T; t += 1024) prepare_label(a, t);
     __syncthreads();
@@ -233,14 +247,15 @@ __global__ void __launch_bounds__(1024) number_rows_kernel(const Args a) {
 
 // ------------------------------------------------------------------- pack --
 
-// Eight elements of a row from `from` (16-byte aligned where `Vector`), those
+// Eight elements of a row from `from` (16-byte aligned where `vector`), those
 // from D on as zeros, as 16-byte words of the planes.
-template <bool F32, bool Vector>
-__device__ __forceinline__ void pack8(const void* from, int64_t offset, int valid, __nv_bfloat16* to, int64_t plane) {
+template <bool F32>
+__device__ __forceinline__ void pack8(const void* from, int64_t offset, int valid, bool vector, __nv_bfloat16* to,
+                                      int64_t plane) {
   if (F32) {
     const float* p = static_cast<const float*>(from) + offset;
     float x[8];
-    if (Vector && valid >= 8) {
+    if (vector && valid >= 8) {
       *reinterpret_cast<float4*>(x) = reinterpret_cast<const float4*>(p)[0];
       *reinterpret_cast<float4*>(x + 4) = reinterpret_cast<const float4*>(p)[1];
     } else {
@@ -261,7 +276,7 @@ __device__ __forceinline__ void pack8(const void* from, int64_t offset, int vali
   } else {
     const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(from) + offset;
     uint4 w;
-    if (Vector && valid >= 8) {
+    if (vector && valid >= 8) {
       w = *reinterpret_cast<const uint4*>(p);
     } else {
       __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(&w);
@@ -272,32 +287,37 @@ __device__ __forceinline__ void pack8(const void* from, int64_t offset, int vali
   }
 }
 
-// Rows with a target side by side; zeros after the last, up to the tile.
-template <bool F32, bool Vector>
-__global__ void __launch_bounds__(256) pack_hidden_kernel(const Args a) {
-  const int32_t rows = a.head->rows;
-  const int32_t wide = int32_t(a.Dp / 8), all = (rows + kTileM - 1) / kTileM * kTileM;
-  for (int64_t n = int64_t(blockIdx.x) * 256 + threadIdx.x; n < int64_t(all) * wide; n += int64_t(gridDim.x) * 256) {
+// The weight's rows (where it is not read in place; this does not wait for the
+// kernels before), and the rows with a target side by side, zeros after the
+// last up to the tile.
+template <bool F32>
+__global__ void __launch_bounds__(256) pack_kernel(const Args a, __nv_bfloat16* packed_weight, bool hidden_vector,
+                                                   bool weight_vector) {
+  let_next_start();
+  const int32_t wide = int32_t(a.Dp / 8);
+  const int64_t first = int64_t(blockIdx.x) * 256 + threadIdx.x, step = int64_t(gridDim.x) * 256;
+  if (packed_weight) {
+    for (int64_t n = first; n < a.V * wide; n += step) {
+      const int64_t v = n / wide, k = n % wide * 8;
+      pack8<F32>(a.weight, v * a.weight_stride + k, int(min(a.D - k, int64_t(8))), weight_vector,
+                 packed_weight + v * a.Dp + k, a.V * a.Dp);
+    }
+  }
+  wait_for_previous();
+  const int32_t rows = a.head->rows, all = (rows + kTileM - 1) / kTileM * kTileM;
+  for (int64_t n = first; n < int64_t(all) * wide; n += step) {
     const int32_t i = int32_t(n / wide), k = int32_t(n % wide) * 8;
     const int64_t t = i < rows ? a.rowmap[i] : 0;
-    pack8<F32, Vector>(a.hidden, t * a.hidden_stride + k, i < rows ? int(min(a.D - k, int64_t(8))) : 0,
-                       a.hp + i * a.Dp + k, a.Tp * a.Dp);
-  }
-}
-
-template <bool F32, bool Vector>
-__global__ void __launch_bounds__(256) pack_weight_kernel(const Args a, __nv_bfloat16* to) {
-  const int32_t wide = int32_t(a.Dp / 8);
-  for (int64_t n = int64_t(blockIdx.x) * 256 + threadIdx.x; n < a.V * wide; n += int64_t(gridDim.x) * 256) {
-    const int64_t v = n / wide, k = n % wide * 8;
-    pack8<F32, Vector>(a.weight, v * a.weight_stride + k, int(min(a.D - k, int64_t(8))), to + v * a.Dp + k,
-                       a.V * a.Dp);
+    pack8<F32>(a.hidden, t * a.hidden_stride + k, i < rows ? int(min(a.D - k, int64_t(8))) : 0, hidden_vector,
+               a.hp + i * a.Dp + k, a.Tp * a.Dp);
   }
 }
 
 // The rows' sums over all pieces, with the common factor, four elements a thread.
 template <bool F32, bool Vector>
 __global__ void __launch_bounds__(256) dhidden_out_kernel(const Args a) {
+  let_next_start();
+  wait_for_previous();
   const float f = a.head->fault ? NAN : a.head->factor;
   const int32_t wide = int32_t((a.D + 3) / 4);
   for (int64_t n = int64_t(blockIdx.x) * 256 + threadIdx.x; n < a.T * wide; n += int64_t(gridDim.x) * 256) {
@@ -388,6 +408,8 @@ __global__ void __launch_bounds__(256) losses_kernel(const Args a, int block_row
   __shared__ float2 sh[256];
   __shared__ double part[256];
   __shared__ bool last;
+  let_next_start();
+  wait_for_previous();
   const int r = threadIdx.x % block_rows, lane = threadIdx.x / block_rows, lanes = 256 / block_rows;
   const int32_t rows = a.head->rows;
   double mine = 0.0;
@@ -450,6 +472,23 @@ unsigned blocks_for(int64_t n) {
   return unsigned(blocks < 1 ? 1 : blocks > 152 * 32 ? 152 * 32 : blocks);
 }
 
+// `dependent`: a programmatic launch behind the kernel before it.
+template <typename... P, typename... A>
+cudaError_t launch(void (*kernel)(P...), unsigned blocks, int threads, size_t shared, cudaStream_t s, bool dependent,
+                   const A&... args) {
+  cudaLaunchConfig_t c = {};
+  c.gridDim = dim3(blocks);
+  c.blockDim = dim3(unsigned(threads));
+  c.dynamicSmemBytes = shared;
+  c.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = at;
+  c.numAttrs = dependent ? 1 : 0;
+  return cudaLaunchKernelEx(&c, kernel, P(args)...);
+}
+
 bool aligned16(const void* p, int64_t stride_bytes) {
   return reinterpret_cast<uintptr_t>(p) % 16 == 0 && stride_bytes % 16 == 0;
 }
@@ -457,45 +496,26 @@ bool aligned16(const void* p, int64_t stride_bytes) {
 }  // namespace
 
 cudaError_t launch_rows(const Args& a, cudaStream_t s) {
-  if (a.K == 0 && a.T <= 2048) {
-    number_rows_kernel<true><<<1, 1024, 0, s>>>(a);
-    return cudaGetLastError();
-  }
+  if (a.K == 0 && a.T <= 2048) return launch(number_rows_kernel<true>, 1, 1024, 0, s, false, a);
+  cudaError_t e = cudaSuccess;
   if (a.T > 0) {
     if (a.K == 0) {
-      label_rows_kernel<<<unsigned((a.T + 255) / 256), 256, 0, s>>>(a);
+      e = launch(label_rows_kernel, unsigned((a.T + 255) / 256), 256, 0, s, false, a);
     } else {
       const size_t row = size_t(16) * ((a.K + 4) / 4 * 4);
       const int rows = 16 * row <= 48 * 1024 ? 16 : 2;
-      teacher_rows_kernel<<<unsigned((a.T + rows - 1) / rows), rows * 32, rows * row, s>>>(a);
+      e = launch(teacher_rows_kernel, unsigned((a.T + rows - 1) / rows), rows * 32, rows * row, s, false, a);
     }
   }
-  number_rows_kernel<false><<<1, 1024, 0, s>>>(a);
-  return cudaGetLastError();
+  return e != cudaSuccess ? e : launch(number_rows_kernel<false>, 1, 1024, 0, s, a.T > 0, a);
 }
 
-cudaError_t launch_pack_hidden(const Args& a, cudaStream_t s) {
-  const bool vector = aligned16(a.hidden, a.hidden_stride * (a.planes == 3 ? 4 : 2));
-  const unsigned blocks = blocks_for(a.Tp * a.Dp / 8);
-  if (a.planes == 3) {
-    if (vector) pack_hidden_kernel<true, true><<<blocks, 256, 0, s>>>(a);
-    else pack_hidden_kernel<true, false><<<blocks, 256, 0, s>>>(a);
-  } else {
-    if (vector) pack_hidden_kernel<false, true><<<blocks, 256, 0, s>>>(a);
-    else pack_hidden_kernel<false, false><<<blocks, 256, 0, s>>>(a);
-  }
-  return cudaGetLastError();
-}
-
-cudaError_t launch_pack_weight(const Args& a, __nv_bfloat16* to, cudaStream_t s) {
-  const unsigned blocks = blocks_for(a.V * a.Dp / 8);
-  if (a.planes == 3) {
-    if (aligned16(a.weight, a.weight_stride * 4)) pack_weight_kernel<true, true><<<blocks, 256, 0, s>>>(a, to);
-    else pack_weight_kernel<true, false><<<blocks, 256, 0, s>>>(a, to);
-  } else {  // bf16 that is aligned is read in place
-    pack_weight_kernel<false, false><<<blocks, 256, 0, s>>>(a, to);
-  }
-  return cudaGetLastError();
+cudaError_t launch_pack(const Args& a, __nv_bfloat16* weight, cudaStream_t s) {
+  const int es = a.planes == 3 ? 4 : 2;
+  const bool hv = aligned16(a.hidden, a.hidden_stride * es), wv = aligned16(a.weight, a.weight_stride * es);
+  const unsigned blocks = blocks_for((weight && a.V > a.Tp ? a.V : a.Tp) * a.Dp / 8);
+  if (a.planes == 3) return launch(pack_kernel<true>, blocks, 256, 0, s, true, a, weight, hv, wv);
+  return launch(pack_kernel<false>, blocks, 256, 0, s, true, a, weight, hv, wv);
 }
 
 cudaError_t launch_losses(const Args& a, cudaStream_t s) {
@@ -503,21 +523,16 @@ cudaError_t launch_losses(const Args& a, cudaStream_t s) {
   int rows = 32;
   while (rows > 1 && a.T / rows < 152) rows /= 2;
   const int64_t blocks = (a.T + rows - 1) / rows;
-  losses_kernel<<<unsigned(blocks < 1 ? 1 : blocks < kLossBlocks ? blocks : kLossBlocks), 256, 0, s>>>(a, rows);
-  return cudaGetLastError();
+  return launch(losses_kernel, unsigned(blocks < 1 ? 1 : blocks < kLossBlocks ? blocks : kLossBlocks), 256, 0, s,
+                true, a, rows);
 }
 
 cudaError_t launch_dhidden_out(const Args& a, cudaStream_t s) {
   const bool vector = aligned16(a.dhidden, a.dhidden_stride * (a.planes == 3 ? 4 : 2));
   const unsigned blocks = blocks_for(a.T * ((a.D + 3) / 4));
-  if (a.planes == 3) {
-    if (vector) dhidden_out_kernel<true, true><<<blocks, 256, 0, s>>>(a);
-    else dhidden_out_kernel<true, false><<<blocks, 256, 0, s>>>(a);
-  } else {
-    if (vector) dhidden_out_kernel<false, true><<<blocks, 256, 0, s>>>(a);
-    else dhidden_out_kernel<false, false><<<blocks, 256, 0, s>>>(a);
-  }
-  return cudaGetLastError();
+  auto* kernel = a.planes == 3 ? (vector ? dhidden_out_kernel<true, true> : dhidden_out_kernel<true, false>)
+                               : (vector ? dhidden_out_kernel<false, true> : dhidden_out_kernel<false, false>);
+  return launch(kernel, blocks, 256, 0, s, true, a);
 }
 
 }  // namespace zl

@@ -582,10 +582,10 @@ __device__ __forceinline__ void gradient_epilogue(const Args& a, const CUtensorM
       const int valid = cols - c0;
 #pragma unroll
       for (int j = 0; j < 32; ++j) z[j] = value(z[j]);
-      if (valid < 32) {
+      if (valid < 32 || !r.there) {
 #pragma unroll
         for (int j = 0; j < 32; ++j)
-          if (j >= valid) z[j] = 0.0f;
+          if (j >= valid || !r.there) z[j] = 0.0f;
       }
 #pragma unroll
       for (int j = 0; j < 32; j += 8) {
@@ -746,6 +746,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
 
+  let_next_start();
   if (warp == 0 && lane == 0) {
     for (int s = 0; s < kStages; ++s) {
       barrier_init(full + 8 * s, 1);
@@ -772,6 +773,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   cluster_sync();
   fence_after();
   const uint32_t tmem = *tmem_slot;
+  wait_for_previous();
   const int rows = a.head->rows;
   const Waiter wait{given_up, a.head};
   const Progress progress{given_up, a.head};
@@ -819,7 +821,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const int bn = u.n0 + int(rank) * (u.n / 2) + (u.mode == kGradient ? c0 : 0);
           const int b_k0 = u.mode == kHidden ? c0 : 0;
           const int b_boxes = b_mn ? (u.n / 2 + 63) / 64 : 0;
-          const uint32_t bytes = 2 * (kOperandBytes + (b_mn ? b_boxes * 64 * kBlockK * 2 : kOperandBytes));
+          const uint32_t bytes = 2 * ((a_mn ? kOperandBytes : prog.box_rows * kBlockK * 2) +
+                                      (b_mn ? b_boxes * 64 * kBlockK * 2 : kOperandBytes));
           const int segments = segments_of<PLANES>(u);
           const int segment = Shape<PLANES>::segment(Mode(u.mode));
           for (int s = 0; ok && s < segments; ++s) {
@@ -1041,8 +1044,17 @@ cudaError_t launch(const Args& a, const Program& prog, int sms, cudaStream_t s) 
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<PLANES>::bytes);
   }();
   if (ready != cudaSuccess) return ready;
-  kernel<<<unsigned(sms / 2 * 2), kThreads, Shape<PLANES>::bytes, s>>>(a, prog);
-  return cudaGetLastError();
+  cudaLaunchConfig_t c = {};
+  c.gridDim = dim3(unsigned(sms / 2 * 2));
+  c.blockDim = dim3(kThreads);
+  c.dynamicSmemBytes = Shape<PLANES>::bytes;
+  c.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = at;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, kernel, a, prog);
 }
 
 }  // namespace

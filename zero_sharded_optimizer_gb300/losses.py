@@ -176,16 +176,18 @@ class _Call:
         return (None if dhidden is False else dhidden), (None if dweight is False else dweight)
 
     def run(self, name: str):
+        if self.device.index != torch.cuda.current_device():
+            with torch.cuda.device(self.device):
+                return self.run(name)
         kind = "distill" if self.distill else "xent"
-        with torch.cuda.device(self.device):
-            size = getattr(abi, f"zero_{kind}_workspace_bytes")(self.p)
-            space = self.new(size, dtype=torch.uint8)
-            self.p.workspace, self.p.workspace_bytes = space.data_ptr(), size
-            getattr(abi, f"zero_{kind}_{name}")(self.p, self.stream)
-            if isinstance(self.stream, torch.cuda.Stream):
-                for t in self.keep:
-                    if isinstance(t, torch.Tensor):
-                        t.record_stream(self.stream)
+        size = getattr(abi, f"zero_{kind}_workspace_bytes")(self.p)
+        space = self.new(size, dtype=torch.uint8)
+        self.p.workspace, self.p.workspace_bytes = space.data_ptr(), size
+        getattr(abi, f"zero_{kind}_{name}")(self.p, self.stream)
+        if isinstance(self.stream, torch.cuda.Stream):
+            for t in self.keep:
+                if isinstance(t, torch.Tensor):
+                    t.record_stream(self.stream)
 
 
 def xent_forward(hidden, weight, labels, *, reduction: str = "mean", ignore_index: int = -100,
