@@ -258,14 +258,15 @@ int plan(const zero_head_loss_t* p, bool distill, int pass, Args* a, __nv_bfloat
     for (int b = 0; b < zl::kBuffers; ++b)
       a->g[b] = b < pieces ? w.take<__nv_bfloat16>(a->Tp * a->planes, a->piece) : a->g[0];
     // dhidden's sums over a piece are split where one of its tiles would be
-    // more than half of what each of 76 CTA pairs has to do in a launch.
-    const int64_t blocks_t = (a->Tp + 63) / 64, blocks_v = a->piece / 64, blocks_d = a->Dp / 64;
+    // more than half of what each of 76 CTA pairs has to do for the piece, while
+    // two blocks of K are left to a part.
+    const int64_t blocks_t = (a->T + 63) / 64, blocks_v = a->piece / 64, blocks_d = a->Dp / 64;
     const int64_t wide = (a->D + zl::kTileN - 1) / zl::kTileN;
     const int64_t rows = a->Tp / zl::kTileM, cols = a->piece / zl::kTileN;
     const int64_t work = rows * wide * blocks_v + (p->dweight ? cols * wide * blocks_t : 0) +
                          (pieces > 1 ? rows * cols * blocks_d : 0);
     a->splits = 1;
-    while (a->splits < 64 && blocks_v / a->splits > std::max<int64_t>(work / (2 * 76), 8)) a->splits *= 2;
+    while (a->splits < 64 && blocks_v / a->splits > std::max<int64_t>(work / (2 * 76), 2)) a->splits *= 2;
     if (p->dhidden) a->dh = w.take<float>(a->splits * a->Tp, a->Dp);
     most = std::max(most, w.at);
   }
@@ -365,13 +366,14 @@ int run(const zero_head_loss_t* p, bool distill, int pass, cudaStream_t s) {
   if (q != cudaSuccess)
     return set_error(ZERO_ECUDA, "device: %s (%s)", cudaGetErrorString(q), cudaGetErrorName(q));
   const char* what = "rows";
-  cudaError_t e = zl::launch_rows(a, s);
+  bool rows_packed = false;
+  cudaError_t e = zl::launch_rows(a, packed != nullptr, &rows_packed, s);
   auto next = [&](const char* name, auto&& launch) {
     if (e != cudaSuccess) return;
     what = name;
     e = launch();
   };
-  next("packing", [&] { return zl::launch_pack(a, packed, s); });
+  if (!rows_packed) next("packing", [&] { return zl::launch_pack(a, packed, s); });
   if (pass & kForward) {
     program.forward = 1;
     program.counter = a.counters;

@@ -184,11 +184,66 @@ __global__ void teacher_rows_kernel(const Args a) {
     a.starts[h * a.T + t0 + r] = uint16_t(first_entry(ids, n, h * 128));
 }
 
+// ------------------------------------------------------------------- pack --
+
+// Eight elements of a row from `from` (16-byte aligned where `vector`), those
+// from D on as zeros, as 16-byte words of the planes.
+template <bool F32>
+__device__ __forceinline__ void pack8(const void* from, int64_t offset, int valid, bool vector, __nv_bfloat16* to,
+                                      int64_t plane) {
+  if (F32) {
+    const float* p = static_cast<const float*>(from) + offset;
+    float x[8];
+    if (vector && valid >= 8) {
+      *reinterpret_cast<float4*>(x) = reinterpret_cast<const float4*>(p)[0];
+      *reinterpret_cast<float4*>(x + 4) = reinterpret_cast<const float4*>(p)[1];
+    } else {
+#pragma unroll
+      for (int q = 0; q < 8; ++q) x[q] = q < valid ? p[q] : 0.0f;
+    }
+    __nv_bfloat16 part[8][3];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) split(x[q], part[q]);
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      uint4 w;
+      __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(&w);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) out[q] = part[q][i];
+      *reinterpret_cast<uint4*>(to + i * plane) = w;
+    }
+  } else {
+    const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(from) + offset;
+    uint4 w;
+    if (vector && valid >= 8) {
+      w = *reinterpret_cast<const uint4*>(p);
+    } else {
+      __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(&w);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) out[q] = q < valid ? p[q] : __nv_bfloat16(0.0f);
+    }
+    *reinterpret_cast<uint4*>(to) = w;
+  }
+}
+
+// Rows with a target side by side, and zeros after the last up to the next
+// block of K (of dweight's products; other rows past the last are not read).
+template <bool F32>
+__device__ __forceinline__ void pack_rows(const Args& a, int32_t rows, bool vector, int64_t first, int64_t step) {
+  const int32_t wide = int32_t(a.Dp / 8), all = (rows + 63) / 64 * 64;
+  for (int64_t n = first; n < int64_t(all) * wide; n += step) {
+    const int32_t i = int32_t(n / wide), k = int32_t(n % wide) * 8;
+    const int64_t t = i < rows ? a.rowmap[i] : 0;
+    pack8<F32>(a.hidden, t * a.hidden_stride + k, i < rows ? int(min(a.D - k, int64_t(8))) : 0, vector,
+               a.hp + i * a.Dp + k, a.Tp * a.Dp);
+  }
+}
+
 // One block: numbers the rows that have a target, in order, up to 16 times
 // 1024 rows at a time. With `Prepare` (few rows, labels alone) it prepares them
-// first, which saves a launch.
-template <bool Prepare>
-__global__ void __launch_bounds__(1024) number_rows_kernel(const Args a) {
+// first, with `Pack` (very few, bf16) it also packs them: a launch saved each.
+template <bool Prepare, bool Pack>
+__global__ void __launch_bounds__(1024) number_rows_kernel(const Args a, bool vector) {
   __shared__ int32_t before[16][32], total[16];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   let_next_start();
@@ -243,53 +298,14 @@ __global__ void __launch_bounds__(1024) number_rows_kernel(const Args a) {
     if (a.reduction != ZERO_REDUCE_NONE && a.dloss) f *= double(*a.dloss);
     *a.head = Head{base, 0, 0, float(f)};
   }
-}
-
-// ------------------------------------------------------------------- pack --
-
-// Eight elements of a row from `from` (16-byte aligned where `vector`), those
-// from D on as zeros, as 16-byte words of the planes.
-template <bool F32>
-__device__ __forceinline__ void pack8(const void* from, int64_t offset, int valid, bool vector, __nv_bfloat16* to,
-                                      int64_t plane) {
-  if (F32) {
-    const float* p = static_cast<const float*>(from) + offset;
-    float x[8];
-    if (vector && valid >= 8) {
-      *reinterpret_cast<float4*>(x) = reinterpret_cast<const float4*>(p)[0];
-      *reinterpret_cast<float4*>(x + 4) = reinterpret_cast<const float4*>(p)[1];
-    } else {
-#pragma unroll
-      for (int q = 0; q < 8; ++q) x[q] = q < valid ? p[q] : 0.0f;
-    }
-    __nv_bfloat16 part[8][3];
-#pragma unroll
-    for (int q = 0; q < 8; ++q) split(x[q], part[q]);
-#pragma unroll
-    for (int i = 0; i < 3; ++i) {
-      uint4 w;
-      __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(&w);
-#pragma unroll
-      for (int q = 0; q < 8; ++q) out[q] = part[q][i];
-      *reinterpret_cast<uint4*>(to + i * plane) = w;
-    }
-  } else {
-    const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(from) + offset;
-    uint4 w;
-    if (vector && valid >= 8) {
-      w = *reinterpret_cast<const uint4*>(p);
-    } else {
-      __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(&w);
-#pragma unroll
-      for (int q = 0; q < 8; ++q) out[q] = q < valid ? p[q] : __nv_bfloat16(0.0f);
-    }
-    *reinterpret_cast<uint4*>(to) = w;
+  if (Pack) {
+    __syncthreads();
+    pack_rows<false>(a, base, vector, threadIdx.x, 1024);
   }
 }
 
 // The weight's rows (where it is not read in place; this does not wait for the
-// kernels before), and the rows with a target side by side, zeros after the
-// last up to the tile.
+// kernels before), and the rows with a target.
 template <bool F32>
 __global__ void __launch_bounds__(256) pack_kernel(const Args a, __nv_bfloat16* packed_weight, bool hidden_vector,
                                                    bool weight_vector) {
@@ -304,13 +320,7 @@ __global__ void __launch_bounds__(256) pack_kernel(const Args a, __nv_bfloat16* 
     }
   }
   wait_for_previous();
-  const int32_t rows = a.head->rows, all = (rows + kTileM - 1) / kTileM * kTileM;
-  for (int64_t n = first; n < int64_t(all) * wide; n += step) {
-    const int32_t i = int32_t(n / wide), k = int32_t(n % wide) * 8;
-    const int64_t t = i < rows ? a.rowmap[i] : 0;
-    pack8<F32>(a.hidden, t * a.hidden_stride + k, i < rows ? int(min(a.D - k, int64_t(8))) : 0, hidden_vector,
-               a.hp + i * a.Dp + k, a.Tp * a.Dp);
-  }
+  pack_rows<F32>(a, a.head->rows, hidden_vector, first, step);
 }
 
 // The rows' sums over all pieces, with the common factor, four elements a thread.
@@ -495,8 +505,11 @@ bool aligned16(const void* p, int64_t stride_bytes) {
 
 }  // namespace
 
-cudaError_t launch_rows(const Args& a, cudaStream_t s) {
-  if (a.K == 0 && a.T <= 2048) return launch(number_rows_kernel<true>, 1, 1024, 0, s, false, a);
+cudaError_t launch_rows(const Args& a, bool pack_weight, bool* packed, cudaStream_t s) {
+  const bool vector = aligned16(a.hidden, a.hidden_stride * 2);
+  *packed = a.K == 0 && a.T <= 16 && a.planes == 1 && !pack_weight;
+  if (*packed) return launch(number_rows_kernel<true, true>, 1, 1024, 0, s, false, a, vector);
+  if (a.K == 0 && a.T <= 2048) return launch(number_rows_kernel<true, false>, 1, 1024, 0, s, false, a, vector);
   cudaError_t e = cudaSuccess;
   if (a.T > 0) {
     if (a.K == 0) {
@@ -507,7 +520,7 @@ cudaError_t launch_rows(const Args& a, cudaStream_t s) {
       e = launch(teacher_rows_kernel, unsigned((a.T + rows - 1) / rows), rows * 32, rows * row, s, false, a);
     }
   }
-  return e != cudaSuccess ? e : launch(number_rows_kernel<false>, 1, 1024, 0, s, a.T > 0, a);
+  return e != cudaSuccess ? e : launch(number_rows_kernel<false, false>, 1, 1024, 0, s, a.T > 0, a, vector);
 }
 
 cudaError_t launch_pack(const Args& a, __nv_bfloat16* weight, cudaStream_t s) {

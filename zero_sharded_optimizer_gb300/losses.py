@@ -48,39 +48,44 @@ class Losses(NamedTuple):
     dweight: torch.Tensor | None = None
 
 
+_PRECISION = {torch.float32: abi.ZERO_FP32, torch.bfloat16: abi.ZERO_BF16_MIXED}
+
+
 def _matrix(t, what: str, dtype=None, rows=None, cols=None, device=None):
     """``t`` as a matrix [rows, cols] without a copy; (tensor, row stride)."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{what} must be a CUDA tensor")
-    if t.dtype not in (torch.float32, torch.bfloat16) or (dtype is not None and t.dtype != dtype):
+    own = t.dtype
+    if own is not dtype and (dtype is not None or own not in _PRECISION):
         want = "float32 or bfloat16" if dtype is None else dtype
-        raise TypeError(f"{what} has dtype {t.dtype}, expected {want}")
+        raise TypeError(f"{what} has dtype {own}, expected {want}")
     if device is not None and t.device != device:
         raise ValueError(f"{what} is on {t.device}, expected {device}")
-    if t.dim() < 2:
-        raise ValueError(f"{what} must have at least 2 dimensions")
-    if t.dim() > 2:
+    if t.dim() != 2:
+        if t.dim() < 2:
+            raise ValueError(f"{what} must have at least 2 dimensions")
         try:
             t = t.view(-1, t.shape[-1])
         except RuntimeError:
             raise ValueError(f"{what}'s rows must lie one stride apart") from None
-    if (rows is not None and t.shape[0] != rows) or (cols is not None and t.shape[1] != cols):
-        raise ValueError(f"{what} has shape {tuple(t.shape)}, expected ({rows}, {cols})")
     n, d = t.shape
-    if d > 1 and n > 0 and t.stride(1) != 1:
+    if (rows is not None and n != rows) or (cols is not None and d != cols):
+        raise ValueError(f"{what} has shape {tuple(t.shape)}, expected ({rows}, {cols})")
+    stride, unit = t.stride()
+    if unit != 1 and d > 1 and n > 0:
         raise ValueError(f"the elements of {what}'s rows must be adjacent")
-    stride = t.stride(0) if n > 1 else max(d, 1)
-    return t, stride
+    return t, stride if n > 1 else max(d, 1)
 
 
-def _vector(t, what: str, dtype, count: int, device):
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != dtype:
+def _vector(t, what: str, dtype, count: int, device) -> int:
+    """The address of ``count`` contiguous elements."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype is not dtype:
         raise TypeError(f"{what} must be a {dtype} CUDA tensor")
     if t.device != device:
         raise ValueError(f"{what} is on {t.device}, expected {device}")
     if t.numel() != count or not t.is_contiguous():
         raise ValueError(f"{what} must be contiguous with {count} elements")
-    return t
+    return t.data_ptr()
 
 
 class _Call:
@@ -93,100 +98,117 @@ class _Call:
         weight2, ws = _matrix(weight, "weight", self.dtype, cols=D, device=self.device)
         if reduction not in _REDUCE:
             raise ValueError('reduction must be "none", "mean" or "sum"')
-        self.T, self.V, self.D = T, weight2.shape[0], D
+        V = weight2.shape[0]
+        self.T, self.V, self.D = T, V, D
         self.shape = hidden.shape
         self.stream = stream
         self.distill = teacher is not None
-        self.keep = [hidden2, weight2]
-        p = self.p = abi.HeadLoss()
-        p.T, p.V, p.D = T, self.V, D
-        p.precision = abi.ZERO_FP32 if self.dtype == torch.float32 else abi.ZERO_BF16_MIXED
-        p.reduction = _REDUCE[reduction]
-        p.hidden, p.hidden_stride = hidden2.data_ptr(), hs
-        p.weight, p.weight_stride = weight2.data_ptr(), ws
-        p.ignore_index = ignore_index
-        p.grad_scale = 1.0
+        self.labels = labels is not None
+        self.none = reduction == "none"
+        self.keep = [hidden2, weight2, labels]
+        y = None
         if labels is not None:
-            p.labels = _vector(labels, "labels", torch.int64, T, self.device).data_ptr()
-            self.keep.append(labels)
+            y = _vector(labels, "labels", torch.int64, T, self.device)
         elif teacher is None:
             raise TypeError("labels must be a torch.int64 CUDA tensor")
+        # the fields in order: up to ignore_index
+        p = self.p = abi.HeadLoss(T, V, D, _PRECISION[self.dtype], _REDUCE[reduction],
+                                  hidden2.data_ptr(), hs, weight2.data_ptr(), ws, y, ignore_index)
+        p.grad_scale = 1.0
         if teacher is not None:
             ids, logits, temperature, alpha = teacher
             if not isinstance(ids, torch.Tensor) or ids.dim() < 2:
                 raise ValueError("teacher_ids must have at least 2 dimensions")
             K = ids.shape[-1]
-            _vector(ids, "teacher_ids", torch.int64, T * K, self.device)
+            p.teacher_ids = _vector(ids, "teacher_ids", torch.int64, T * K, self.device)
             if isinstance(logits, torch.Tensor) and logits.dtype == torch.bfloat16:
                 logits = logits.float()
-            _vector(logits, "teacher_logits", torch.float32, T * K, self.device)
-            p.teacher_ids, p.teacher_logits = ids.data_ptr(), logits.data_ptr()
+            p.teacher_logits = _vector(logits, "teacher_logits", torch.float32, T * K, self.device)
             p.teacher_k = K
             p.temperature, p.alpha = float(temperature), float(alpha)
             self.keep += [ids, logits]
 
-    def new(self, *shape, dtype=torch.float32):
+    def new(self, shape, dtype=torch.float32):
         t = torch.empty(shape, dtype=dtype, device=self.device)
         self.keep.append(t)
         return t
 
-    def outputs(self, lse=None, lse_tau=None):
-        """Rows' statistics: given (backward) or to be written (forward)."""
+    def statistics(self, lse, lse_tau):
+        """The forward pass's, for a backward pass."""
         T, p = self.T, self.p
-        if p.labels or not self.distill:
-            lse = self.new(T) if lse is None else _vector(lse, "lse", torch.float32, T, self.device)
-            p.lse = lse.data_ptr()
+        if self.labels:
+            p.lse = _vector(lse, "lse", torch.float32, T, self.device)
         if self.distill:
-            lse_tau = self.new(T) if lse_tau is None else \
-                _vector(lse_tau, "lse_tau", torch.float32, T, self.device)
-            p.lse_tau = lse_tau.data_ptr()
-        return lse, lse_tau
+            p.lse_tau = _vector(lse_tau, "lse_tau", torch.float32, T, self.device)
+        self.keep += [lse, lse_tau]
 
     def losses(self):
-        loss = self.new(*self.shape[:-1])
-        self.p.loss = loss.data_ptr()
-        reduced = None
-        if self.p.reduction != abi.ZERO_REDUCE_NONE:
-            reduced = self.new()
-            self.p.reduced = reduced.data_ptr()
-        return loss, reduced
+        """loss, reduced, lse, lse_tau, to be written."""
+        p, T = self.p, self.T
+        loss = self.new(self.shape[:-1])
+        p.loss = loss.data_ptr()
+        reduced = lse = lse_tau = None
+        if not self.none:
+            reduced = self.new(())
+            p.reduced = reduced.data_ptr()
+        if self.labels:
+            lse = self.new(T)
+            p.lse = lse.data_ptr()
+        if self.distill:
+            lse_tau = self.new(T)
+            p.lse_tau = lse_tau.data_ptr()
+        return loss, reduced, lse, lse_tau
 
     def gradients(self, dloss, grad_scale, dhidden, dweight, accumulate):
         """dhidden / dweight: a tensor to write, None to allocate one, False to leave it out."""
         p = self.p
-        p.grad_scale = float(grad_scale)
-        p.accumulate = 1 if accumulate else 0
+        p.grad_scale = grad_scale
+        if accumulate:
+            p.accumulate = 1
         if dloss is not None:
-            count = self.T if p.reduction == abi.ZERO_REDUCE_NONE else 1
-            p.dloss = _vector(dloss, "dloss", torch.float32, count, self.device).data_ptr()
+            p.dloss = _vector(dloss, "dloss", torch.float32, self.T if self.none else 1, self.device)
             self.keep.append(dloss)
         if dhidden is None:
-            dhidden = self.new(*self.shape, dtype=self.dtype)
+            dhidden = self.new(self.shape, self.dtype)
+            p.dhidden, p.dhidden_stride = dhidden.data_ptr(), self.D
+        elif dhidden is False:
+            dhidden = None
+        else:
+            m, stride = _matrix(dhidden, "dhidden", self.dtype, self.T, self.D, self.device)
+            p.dhidden, p.dhidden_stride = m.data_ptr(), stride
+            self.keep.append(m)
         if dweight is None:
             if accumulate:
                 raise ValueError("accumulate adds to a dweight that is given")
-            dweight = self.new(self.V, self.D, dtype=self.dtype)
-        if dhidden is not False:
-            m, stride = _matrix(dhidden, "dhidden", self.dtype, self.T, self.D, self.device)
-            p.dhidden, p.dhidden_stride = m.data_ptr(), stride
-        if dweight is not False:
+            dweight = self.new((self.V, self.D), self.dtype)
+            p.dweight, p.dweight_stride = dweight.data_ptr(), self.D
+        elif dweight is False:
+            dweight = None
+        else:
             m, stride = _matrix(dweight, "dweight", self.dtype, self.V, self.D, self.device)
             p.dweight, p.dweight_stride = m.data_ptr(), stride
-        self.keep += [dhidden, dweight]
-        return (None if dhidden is False else dhidden), (None if dweight is False else dweight)
+            self.keep.append(m)
+        return dhidden, dweight
 
-    def run(self, name: str):
-        if self.device.index != torch.cuda.current_device():
-            with torch.cuda.device(self.device):
-                return self.run(name)
-        kind = "distill" if self.distill else "xent"
-        size = getattr(abi, f"zero_{kind}_workspace_bytes")(self.p)
-        space = self.new(size, dtype=torch.uint8)
-        self.p.workspace, self.p.workspace_bytes = space.data_ptr(), size
-        getattr(abi, f"zero_{kind}_{name}")(self.p, self.stream)
-        if isinstance(self.stream, torch.cuda.Stream):
+    def run(self, xent, distill):
+        """Queues the call: ``xent`` or ``distill`` of abi, with its workspace."""
+        index = self.device.index
+        if index != torch.cuda.current_device():
+            with torch.cuda.device(index):
+                return self.run(xent, distill)
+        p = self.p
+        if self.distill:
+            size, call = abi.zero_distill_workspace_bytes(p), distill
+        else:
+            size, call = abi.zero_xent_workspace_bytes(p), xent
+        space = self.new(size, torch.uint8)
+        p.workspace, p.workspace_bytes = space.data_ptr(), size
+        stream = self.stream
+        # the current stream's handle, without the object around it
+        call(p, torch._C._cuda_getCurrentRawStream(index) if stream is None else stream)
+        if isinstance(stream, torch.cuda.Stream):
             for t in self.keep:
-                if isinstance(t, torch.Tensor):
+                if t is not None:
                     t.record_stream(self.stream)
 
 
@@ -194,10 +216,9 @@ def xent_forward(hidden, weight, labels, *, reduction: str = "mean", ignore_inde
                  stream=None) -> Losses:
     """Cross entropy of every row against ``labels`` (int64 [T])."""
     c = _Call(hidden, weight, labels, reduction, ignore_index, stream)
-    lse, _ = c.outputs()
-    loss, reduced = c.losses()
-    c.run("forward")
-    return Losses(loss, reduced, lse, None)
+    out = c.losses()
+    c.run(abi.zero_xent_forward, None)
+    return Losses(*out)
 
 
 def xent_backward(hidden, weight, labels, lse, *, reduction: str = "mean",
@@ -207,9 +228,9 @@ def xent_backward(hidden, weight, labels, lse, *, reduction: str = "mean",
     ``dloss`` (float32): the gradient of the total with respect to ``loss``
     (reduction "none") or to ``reduced``; ones when None."""
     c = _Call(hidden, weight, labels, reduction, ignore_index, stream)
-    c.outputs(lse)
+    c.statistics(lse, None)
     dh, dw = c.gradients(dloss, grad_scale, dhidden, dweight, accumulate)
-    c.run("backward")
+    c.run(abi.zero_xent_backward, None)
     return Losses(None, None, lse, None, dh, dw)
 
 
@@ -218,11 +239,10 @@ def xent_step(hidden, weight, labels, *, reduction: str = "mean", ignore_index: 
               accumulate: bool = False, stream=None) -> Losses:
     """xent_forward and xent_backward in one call."""
     c = _Call(hidden, weight, labels, reduction, ignore_index, stream)
-    lse, _ = c.outputs()
-    loss, reduced = c.losses()
-    dh, dw = c.gradients(dloss, grad_scale, dhidden, dweight, accumulate)
-    c.run("step")
-    return Losses(loss, reduced, lse, None, dh, dw)
+    out = c.losses()
+    grads = c.gradients(dloss, grad_scale, dhidden, dweight, accumulate)
+    c.run(abi.zero_xent_step, None)
+    return Losses(*out, *grads)
 
 
 def distill_forward(hidden, weight, teacher_ids, teacher_logits, *, temperature: float = 1.0,
@@ -234,10 +254,9 @@ def distill_forward(hidden, weight, teacher_ids, teacher_logits, *, temperature:
     weighted ``1 - alpha``."""
     c = _Call(hidden, weight, labels, reduction, ignore_index, stream,
               (teacher_ids, teacher_logits, temperature, alpha))
-    lse, lse_tau = c.outputs()
-    loss, reduced = c.losses()
-    c.run("forward")
-    return Losses(loss, reduced, lse, lse_tau)
+    out = c.losses()
+    c.run(None, abi.zero_distill_forward)
+    return Losses(*out)
 
 
 def distill_backward(hidden, weight, teacher_ids, teacher_logits, lse, lse_tau, *,
@@ -249,9 +268,9 @@ def distill_backward(hidden, weight, teacher_ids, teacher_logits, lse, lse_tau, 
     same inputs; ``dloss`` as in xent_backward."""
     c = _Call(hidden, weight, labels, reduction, ignore_index, stream,
               (teacher_ids, teacher_logits, temperature, alpha))
-    c.outputs(lse, lse_tau)
+    c.statistics(lse, lse_tau)
     dh, dw = c.gradients(dloss, grad_scale, dhidden, dweight, accumulate)
-    c.run("backward")
+    c.run(None, abi.zero_distill_backward)
     return Losses(None, None, lse, lse_tau, dh, dw)
 
 
@@ -262,11 +281,10 @@ def distill_step(hidden, weight, teacher_ids, teacher_logits, *, temperature: fl
     """distill_forward and distill_backward in one call."""
     c = _Call(hidden, weight, labels, reduction, ignore_index, stream,
               (teacher_ids, teacher_logits, temperature, alpha))
-    lse, lse_tau = c.outputs()
-    loss, reduced = c.losses()
-    dh, dw = c.gradients(dloss, grad_scale, dhidden, dweight, accumulate)
-    c.run("step")
-    return Losses(loss, reduced, lse, lse_tau, dh, dw)
+    out = c.losses()
+    grads = c.gradients(dloss, grad_scale, dhidden, dweight, accumulate)
+    c.run(None, abi.zero_distill_step)
+    return Losses(*out, *grads)
 
 
 # -------------------------------------------------------------- autograd --
