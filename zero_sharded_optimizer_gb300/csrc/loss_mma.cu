@@ -104,6 +104,12 @@ __device__ __forceinline__ void barrier_expect(uint32_t bar, uint32_t bytes) {
 __device__ __forceinline__ void barrier_arrive_remote(uint32_t cluster_bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
+// Without an order for the thread's earlier memory accesses: for what it has
+// read, which needs none. (A release waits for its stores on their way out:
+// 8 % of a forward pass of width 768.)
+__device__ __forceinline__ void barrier_arrive_read(uint32_t cluster_bar) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
 // `Cluster`: the wait also orders memory that threads of the other CTA wrote.
 template <bool Cluster>
 __device__ __forceinline__ bool barrier_try(uint32_t bar, uint32_t parity) {
@@ -133,11 +139,12 @@ struct Waiter {
   Head* head;
   template <bool Cluster = false>
   __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity) const {
-    if (barrier_try<Cluster>(bar, parity)) return true;
+    for (uint32_t n = 0; n < 1; ++n)
+      if (barrier_try<Cluster>(bar, parity)) return true;
     const uint64_t begin = timer_ns();
     for (uint32_t n = 1;; ++n) {
       if (barrier_try<Cluster>(bar, parity)) return true;
-      if ((n & 63) == 0 && (*given_up || timer_ns() - begin > kWaitLimitNs)) {
+      if ((n & 1023) == 0 && (*given_up || timer_ns() - begin > kWaitLimitNs)) {
         *given_up = 1;
         head->fault = 1;
         return false;
@@ -395,7 +402,8 @@ struct Row {
   int e, end;              // its sparse entries in the thread's columns
   int32_t id, next_id;     // of entry e and the one after it
   float w, next_w;         // their weights (kGradient)
-  float scale, w_ce, w_kd, lse, lse_kd;  // kGradient
+  float2 f;                // weights of the two terms (kGradient, with scale, lse and lse_kd)
+  float scale, lse, lse_kd;
 };
 
 __device__ __forceinline__ void entry_ahead(const Args& a, const Unit& u, const Row& r, int e, int32_t& id, float& w) {
@@ -409,19 +417,15 @@ __device__ __forceinline__ Row row_of(const Args& a, int rows, const Unit& u, co
   r.i = u.m0 + int(rank) * kHalf + th.row;
   r.there = r.i < rows;
   r.id = r.next_id = kNoId;
-  r.lse = r.lse_kd = INFINITY;
   if (!r.there) return r;
   r.t = a.rowmap[r.i];
-  if (u.mode == kGradient) {
-    const float2 f = a.coef[r.t];
-    // A term that the row does not have is 2^-inf = 0, whatever the accumulator holds.
-    if (CE && f.x != 0.0f) r.lse = a.lse[r.t];
-    if (KD && f.y != 0.0f) r.lse_kd = a.lse_tau[r.t];
-    r.scale = a.reduction == ZERO_REDUCE_NONE && a.dloss ? a.dloss[r.t] : 1.0f;
-    r.w_ce = f.x * r.scale;
-    r.w_kd = f.y * r.scale;
-  }
   const int64_t v = u.piece * a.piece + u.n0 + th.half * 128;
+  if (u.mode == kGradient) {
+    r.f = a.coef[r.t];
+    if (CE) r.lse = a.lse[r.t];
+    if (KD) r.lse_kd = a.lse_tau[r.t];
+    r.scale = a.reduction == ZERO_REDUCE_NONE && a.dloss ? a.dloss[r.t] : 1.0f;
+  }
   if (a.K == 0) {
     r.id = a.ids[r.t];
     if (u.mode == kGradient) r.w = a.weights[r.t];
@@ -444,7 +448,8 @@ template <typename F>
 __device__ __forceinline__ void each_entry(const Args& a, const Unit& u, Row& r, int64_t v0, int end, uint32_t acc,
                                            F f) {
   for (;;) {
-    const int mine = r.id < v0 + end ? int(r.id - v0) : 0x7fffffff;
+    const int64_t at = r.id - v0;
+    const int mine = at >= 0 && at < end ? int(at) : 0x7fffffff;
     const int c = __reduce_min_sync(~0u, mine);
     if (c == 0x7fffffff) break;
     const float z = tmem_load1(acc + c);
@@ -459,20 +464,42 @@ __device__ __forceinline__ void each_entry(const Args& a, const Unit& u, Row& r,
   }
 }
 
-// sum of 2^(c z - m) with m moved to the maximum. m is the rounded product, the
-// reference that the sum is stored with, so its rounding cancels.
-__device__ __forceinline__ void add_exponentials(const float (&z)[32], float top, float c, float& m, float& sum) {
-  const float next = __fmul_rn(top, c);
-  const float base = next == -INFINITY ? 0.0f : next;
-  float s0 = m == -INFINITY ? 0.0f : sum * exp2_fast(m - base), s1 = 0.0f;
-#pragma unroll
-  for (int j = 0; j < 32; j += 2) {
-    s0 += exp2_fast(fmaf(z[j], c, -base));
-    s1 += exp2_fast(fmaf(z[j + 1], c, -base));
-  }
-  sum = s0 + s1;
-  m = next;
+// x to the power of P.
+template <int P>
+__device__ __forceinline__ float power(float x) {
+  return P == 1 ? x : P == 2 ? x * x : (x * x) * (x * x);
 }
+
+// Sums of 2^(c z - m) with m moved to the maximum. m is the rounded product,
+// the reference that the sum is stored with, so its rounding cancels. Where tau
+// is 1, 2 or 4 the values of z are powers of those of z / tau, and with m_ce
+// = tau m_kd so are the references: one exponential serves both sums (P).
+struct Sums {
+  float m_ce, ce, m_kd, kd;
+};
+
+template <bool CE, bool KD, int P>
+__device__ __forceinline__ void add_exponentials(const float (&z)[32], float top, float c_ce, float c_kd, Sums& s) {
+  const bool begun = (CE && P == 0 ? s.m_ce : s.m_kd) != -INFINITY;
+  const float next_kd = __fmul_rn(top, c_kd);
+  const float next_ce = P ? float(P) * next_kd : __fmul_rn(top, c_ce);
+  const float base_kd = next_kd == -INFINITY ? 0.0f : next_kd, base_ce = next_ce == -INFINITY ? 0.0f : next_ce;
+  float ce[2] = {begun && CE ? s.ce * exp2_fast(s.m_ce - base_ce) : 0.0f, 0.0f};
+  float kd[2] = {begun && KD ? s.kd * exp2_fast(s.m_kd - base_kd) : 0.0f, 0.0f};
+#pragma unroll
+  for (int j = 0; j < 32; ++j) {
+    float x = 0.0f;
+    if (KD) {
+      x = exp2_fast(fmaf(z[j], c_kd, -base_kd));
+      kd[j & 1] += x;
+    }
+    if (CE) ce[j & 1] += KD && P ? power<P>(x) : exp2_fast(fmaf(z[j], c_ce, -base_ce));
+  }
+  s = Sums{next_ce, ce[0] + ce[1], next_kd, kd[0] + kd[1]};
+}
+
+// The power of tau that add_exponentials and the gradient use, 0 for none.
+__device__ __forceinline__ int shared_power(float tau) { return tau == 1.0f ? 1 : tau == 2.0f ? 2 : tau == 4.0f ? 4 : 0; }
 
 template <bool CE, bool KD>
 __device__ __forceinline__ void forward_epilogue(const Args& a, const Unit& u, const Thread& th, Row& r,
@@ -480,9 +507,10 @@ __device__ __forceinline__ void forward_epilogue(const Args& a, const Unit& u, c
   const int64_t v0 = u.n0;
   const int begin = th.half * 128;
   const int cols = int(min(int64_t(256), a.V - v0));
-  const float c_ce = kLog2e, c_kd = a.inv_tau * kLog2e;
-  // Running maximum, and sums relative to it, in powers of two: exp(z) = 2^(c z).
-  float top = -INFINITY, sum = 0.0f, sum_kd = 0.0f, m_ce = -INFINITY, m_kd = -INFINITY;
+  const float c_ce = kLog2e, c_kd = KD ? a.inv_tau * kLog2e : kLog2e;
+  const int p = CE && KD ? shared_power(float(a.tau)) : 0;
+  float top = -INFINITY;
+  Sums s = {-INFINITY, 0.0f, -INFINITY, 0.0f};
 #pragma unroll 1
   for (int k = 0; k < 4; ++k) {
     const int valid = cols - begin - 32 * k;
@@ -501,15 +529,21 @@ __device__ __forceinline__ void forward_epilogue(const Args& a, const Unit& u, c
       t1 = fmaxf(t1, z[j + 1]);
     }
     top = fmaxf(t0, t1);
-    if (CE) add_exponentials(z, top, c_ce, m_ce, sum);
-    if (KD) add_exponentials(z, top, c_kd, m_kd, sum_kd);
+    if (CE && KD) {
+      if (p == 1) add_exponentials<CE, KD, 1>(z, top, c_ce, c_kd, s);
+      else if (p == 2) add_exponentials<CE, KD, 2>(z, top, c_ce, c_kd, s);
+      else if (p == 4) add_exponentials<CE, KD, 4>(z, top, c_ce, c_kd, s);
+      else add_exponentials<CE, KD, 0>(z, top, c_ce, c_kd, s);
+    } else {
+      add_exponentials<CE, KD, 0>(z, top, c_ce, c_kd, s);
+    }
   }
   each_entry(a, u, r, v0, begin + 128, acc, [&](int, float z) { a.zent[r.t * a.L + r.e] = z; });
   if (!r.there) return;
   const int64_t at = (v0 / 256 * 2 + th.half) * a.Tp + r.i;
-  const bool nan = isnan(sum + sum_kd);
-  if (CE) a.stats[at] = make_float2(nan ? NAN : m_ce, sum);
-  if (KD) a.stats_tau[at] = make_float2(nan ? NAN : m_kd, sum_kd);
+  const bool nan = isnan(s.ce + s.kd);
+  if (CE) a.stats[at] = make_float2(nan ? NAN : s.m_ce, s.ce);
+  if (KD) a.stats_tau[at] = make_float2(nan ? NAN : s.m_kd, s.kd);
 }
 
 // Two neighbouring values of G as their words of the operand's parts.
@@ -550,7 +584,7 @@ __device__ __forceinline__ void stage_fp32(uint8_t* box, int lane, const float (
 // The logits' gradient without the factor that all rows share, as the bf16
 // operand of the two products: rounded once (fp32 storage: in three parts).
 // Each warp stages boxes of its 32 rows by 64 columns and stores them by TMA.
-template <int PLANES, bool CE, bool KD>
+template <int PLANES, bool CE, bool KD, int P>
 __device__ __forceinline__ void gradient_epilogue(const Args& a, const CUtensorMap* out, const Unit& u,
                                                   const Thread& th, Row& r, uint32_t acc, uint32_t rank,
                                                   uint8_t* staging) {
@@ -558,15 +592,25 @@ __device__ __forceinline__ void gradient_epilogue(const Args& a, const CUtensorM
   const int begin = th.half * 128, lane = th.row & 31;
   const int cols = int(min(int64_t(256), a.V - v0));
   const float c_ce = kLog2e, c_kd = a.inv_tau * kLog2e;
-  const float m_ce = r.lse * kLog2e, m_kd = r.lse_kd * kLog2e;
+  // Terms that the row does not have are 2^-inf = 0, whatever the accumulator holds.
+  const float lse = CE && r.f.x != 0.0f ? r.lse : INFINITY, lse_kd = KD && r.f.y != 0.0f ? r.lse_kd : INFINITY;
+  // P: p_v = softmax(z)_v is softmax(z / tau)_v^tau times a factor of the row.
+  const float m_kd = (KD && P && lse_kd == INFINITY ? lse * a.inv_tau : lse_kd) * kLog2e, m_ce = lse * kLog2e;
+  const float w_kd = r.f.y * r.scale;
+  const float w_ce = r.f.x == 0.0f ? 0.0f : r.f.x * r.scale * (P ? exp2_fast(float(P) * m_kd - m_ce) : 1.0f);
+  const float lse_shared = KD && P && lse_kd == INFINITY ? lse * a.inv_tau : lse_kd;
   auto value = [&](float z) {
     float g = 0.0f;
-    if (PLANES == 1) {
-      if (CE) g = r.w_ce * exp2_fast(fmaf(z, c_ce, -m_ce));
-      if (KD) g = fmaf(r.w_kd, exp2_fast(fmaf(z, c_kd, -m_kd)), g);
-    } else {  // the difference first: its rounding is relative to it, not to the logit
-      if (CE) g = r.w_ce * exp2_fast((z - r.lse) * kLog2e);
-      if (KD) g = fmaf(r.w_kd, exp2_fast(fmaf(z, a.inv_tau, -r.lse_kd) * kLog2e), g);
+    if (KD) {
+      // fp32: the difference first, whose rounding is relative to it, not to the logit
+      const float x = PLANES == 1 ? exp2_fast(fmaf(z, c_kd, -m_kd))
+                                  : exp2_fast(fmaf(z, a.inv_tau, -lse_shared) * kLog2e);
+      g = w_kd * x;
+      if (CE && P) return fmaf(w_ce, power<P>(x), g);
+    }
+    if (CE) {
+      const float x = PLANES == 1 ? exp2_fast(fmaf(z, c_ce, -m_ce)) : exp2_fast((z - lse) * kLog2e);
+      g = KD ? fmaf(w_ce, x, g) : w_ce * x;
     }
     return g;
   };
@@ -948,14 +992,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     auto give_back = [&] {
       fence_before();
       __syncwarp();
-      if (lane == 0) barrier_arrive_remote(acc_empty0 + 8 * buffer);
+      if (lane == 0) barrier_arrive_read(acc_empty0 + 8 * buffer);
       if (++buffer == 2) {
         buffer = 0;
         phase ^= 1;
       }
     };
-    // A finished unit is counted once its stores are complete, which is waited
-    // for when the next unit is at hand.
+    // A finished unit is counted once its stores are complete: at the end of
+    // the next unit where both are kGradient, so that nothing waits for the
+    // stores; else before the next unit's accumulator is waited for, since what
+    // that waits for may be this.
     uint32_t* finished = nullptr;
     auto count_finished = [&] {
       if (lane == 0 && finished) {
@@ -967,21 +1013,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     for (;;) {
       const uint32_t entry = in_cta(ring_empty + 8 * slot, 0);
       if (!__all_sync(~0u, next_unit()) || u.mode < 0) break;
-      const bool logits = u.mode == kForward || u.mode == kGradient;
+      if (u.mode != kGradient) count_finished();
       Row r{};
       bool ok = true;
       const int segments = segments_of<PLANES>(u);
-      if (logits && segments == 1) r = row_of<CE, KD>(a, rows, u, th, rank);
-      count_finished();
+      if (u.mode == kForward || u.mode == kGradient) r = row_of<CE, KD>(a, rows, u, th, rank);
       if (segments == 1) {
         ok = __all_sync(~0u, full_accumulator());
-        if (lane == 0) barrier_arrive_remote(entry);
+        if (lane == 0) barrier_arrive_read(entry);
       } else {
         const int begin = th.half * 128;
         float sum[4][32] = {};
         for (int s = 0; ok && s < segments; ++s) {
           if (!(ok = __all_sync(~0u, full_accumulator()))) break;
-          if (s == 0 && lane == 0) barrier_arrive_remote(entry);
+          if (s == 0 && lane == 0) barrier_arrive_read(entry);
           const uint32_t acc = lanes + buffer * 256 + begin;
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
@@ -996,13 +1041,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
           if (s < segments - 1) give_back();
         }
-        if (logits) r = row_of<CE, KD>(a, rows, u, th, rank);
       }
       if (!ok) break;
       // The buffer that G goes to has been read by both products of the piece
       // that was there; dH's sums have their earlier additions.
       const int earlier = u.mode == kGradient ? u.piece - kBuffers : u.mode == kHidden ? u.piece - 1 : -1;
       if (earlier >= 0 && earlier > used) {
+        count_finished();
         ok = progress.reached(a.used + earlier, 16 * (weight_units(a, earlier) + hidden_units(a, rows)));
         if (!__all_sync(~0u, ok)) break;
         used = earlier;
@@ -1011,7 +1056,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (u.mode == kForward) {
         forward_epilogue<CE, KD>(a, u, th, r, acc);
       } else if (u.mode == kGradient) {
-        gradient_epilogue<PLANES, CE, KD>(a, &prog.g_out[u.piece % kBuffers], u, th, r, acc, rank, boxes);
+        const CUtensorMap* out = &prog.g_out[u.piece % kBuffers];
+        const int p = CE && KD ? shared_power(float(a.tau)) : 0;
+        if (CE && KD && p == 1) gradient_epilogue<PLANES, CE, KD, 1>(a, out, u, th, r, acc, rank, boxes);
+        else if (CE && KD && p == 2) gradient_epilogue<PLANES, CE, KD, 2>(a, out, u, th, r, acc, rank, boxes);
+        else if (CE && KD && p == 4) gradient_epilogue<PLANES, CE, KD, 4>(a, out, u, th, r, acc, rank, boxes);
+        else gradient_epilogue<PLANES, CE, KD, 0>(a, out, u, th, r, acc, rank, boxes);
+        if (lane == 0 && finished) {  // the unit before: its stores are the older ones
+          asm volatile("cp.async.bulk.wait_group %0;" ::"n"(2) : "memory");
+          progress.arrive(finished);
+        }
         finished = a.formed + u.piece;
       } else {
         if (u.mode == kHidden) hidden_epilogue(&prog.dh, u, th, acc, rank, boxes);
