@@ -242,10 +242,25 @@ int plan(const zero_head_loss_t* p, bool distill, int pass, Args* a, __nv_bfloat
     a->piece = round_up((a->V + pieces - 1) / pieces, zl::kTileN);
     pieces = (a->V + a->piece - 1) / a->piece;
   }
-  a->counters = w.take<int32_t>(2 + 2 * pieces);
+  if (pass & kBackward) {
+    // dhidden's sums over a piece are split where one of its tiles would be
+    // more than half of what each of 76 CTA pairs has to do for the piece, while
+    // two blocks of K are left to a part.
+    const int64_t blocks_t = (a->T + 63) / 64, blocks_v = a->piece / 64, blocks_d = a->Dp / 64;
+    const int64_t wide = (a->D + zl::kTileN - 1) / zl::kTileN;
+    const int64_t rows = a->Tp / zl::kTileM, cols = a->piece / zl::kTileN;
+    const int64_t work = rows * wide * blocks_v + (p->dweight ? cols * wide * blocks_t : 0) +
+                         (pieces > 1 ? rows * cols * blocks_d : 0);
+    a->splits = 1;
+    while (a->splits < 64 && blocks_v / a->splits > std::max<int64_t>(work / (2 * 76), 2)) a->splits *= 2;
+  }
+  // The words that begin as zero.
+  const int64_t tiles = pass & kBackward ? a->splits * (a->Tp / zl::kTileM) * ((a->D + 255) / 256) : 0;
+  a->zeros = 2 + 2 * pieces + tiles;
+  a->counters = w.take<int32_t>(a->zeros);
   a->formed = reinterpret_cast<uint32_t*>(a->counters + 2);
   a->used = a->formed + pieces;
-  a->zeros = 2 + 2 * pieces;
+  a->added = a->used + pieces;
   // The forward pass's arrays and the backward pass's lie over one another.
   const int64_t common = w.at;
   a->sums = w.take<double>(zl::kLossBlocks);
@@ -257,16 +272,6 @@ int plan(const zero_head_loss_t* p, bool distill, int pass, Args* a, __nv_bfloat
     w.at = common;
     for (int b = 0; b < zl::kBuffers; ++b)
       a->g[b] = b < pieces ? w.take<__nv_bfloat16>(a->Tp * a->planes, a->piece) : a->g[0];
-    // dhidden's sums over a piece are split where one of its tiles would be
-    // more than half of what each of 76 CTA pairs has to do for the piece, while
-    // two blocks of K are left to a part.
-    const int64_t blocks_t = (a->T + 63) / 64, blocks_v = a->piece / 64, blocks_d = a->Dp / 64;
-    const int64_t wide = (a->D + zl::kTileN - 1) / zl::kTileN;
-    const int64_t rows = a->Tp / zl::kTileM, cols = a->piece / zl::kTileN;
-    const int64_t work = rows * wide * blocks_v + (p->dweight ? cols * wide * blocks_t : 0) +
-                         (pieces > 1 ? rows * cols * blocks_d : 0);
-    a->splits = 1;
-    while (a->splits < 64 && blocks_v / a->splits > std::max<int64_t>(work / (2 * 76), 2)) a->splits *= 2;
     if (p->dhidden) a->dh = w.take<float>(a->splits * a->Tp, a->Dp);
     most = std::max(most, w.at);
   }

@@ -89,6 +89,7 @@ struct Args {
   int32_t* counters;      // [2] units handed out, forward and backward
   uint32_t* formed;       // [pieces] finished units of a piece's gradient
   uint32_t* used;         // [pieces] finished units of the products with it
+  uint32_t* added;        // [tiles of dh] finished units of a tile
   int64_t zeros;          // 32-bit words from `counters` on that begin as zero
   __nv_bfloat16* g[kBuffers];  // [planes][Tp][piece] gradients of pieces of the logits
   int64_t piece;          // columns of a piece, a multiple of kTileN

@@ -153,8 +153,8 @@ struct Waiter {
   }
 };
 
-// Counts of finished units, one arrival of each epilogue warp (16 a unit),
-// made when the warp's stores are complete. A unit waits only for units that
+// Counts of finished units, one arrival of each CTA (two a unit), made when its
+// stores are complete. A unit waits only for units that
 // were handed out before it and a pair works its units off in order, so the
 // first unfinished unit never waits: no wait is for ever, however few of the
 // grid's pairs run.
@@ -328,60 +328,64 @@ __device__ __forceinline__ int hidden_units(const Args& a, int rows) {
   return a.dhidden ? tiles_of(rows) * tiles_of(int(a.D)) * a.splits : 0;
 }
 
+// The count of pieces' parts in a tile of dH's sums.
+__device__ __forceinline__ uint32_t* hidden_tile(const Args& a, int rows, const Unit& u) {
+  return a.added + (u.split * tiles_of(int(a.D)) + u.n0 / 256) * tiles_of(rows) + u.m0 / 256;
+}
+
 // The phases in order; the units are numbered through them.
 struct Phases {
   int phase = 0, base = 0;
-  // The phase's mode and piece; false after the last.
-  __device__ __forceinline__ bool at(const Args& a, const Program& prog, int* mode, int* piece) const {
-    if (prog.forward) {
-      *mode = kForward;
-      *piece = 0;
-      return phase < 1;
-    }
-    const int lead = min(2, prog.pieces);
-    if (phase < lead) {
-      *mode = kGradient;
-      *piece = phase;
-      return true;
-    }
-    const int p = (phase - lead) / 3, which = (phase - lead) % 3;
-    *mode = which == 0 ? kWeight : which == 1 ? kHidden : kGradient;
-    *piece = which == 2 ? p + 2 : p;
-    return p < prog.pieces;
-  }
+
   __device__ __forceinline__ Unit unit(const Args& a, const Program& prog, int rows, int u) {
-    Unit x{};
-    x.mode = -1;
-    int mode, p;
-    for (; at(a, prog, &mode, &p); ++phase) {
-      const int cols = mode == kForward ? int(a.V) : p < prog.pieces ? piece_cols(a, p) : 0;
-      const int mt = mode == kWeight ? tiles_of(cols) : tiles_of(rows);
-      const int nt = mode == kForward || mode == kGradient ? tiles_of(cols) : tiles_of(int(a.D));
-      const int splits = mode == kHidden ? a.splits : 1;
-      const int count = mode == kWeight && !a.dweight || mode == kHidden && !a.dhidden ? 0 : mt * nt * splits;
-      if (u >= base + count) {
+    const int lead = min(2, prog.pieces);
+    for (;; ++phase) {
+      if (prog.forward) {
+        if (phase > 0) break;
+        const int count = tiles_of(rows) * tiles_of(int(a.V));
+        if (u < count) return tile(a, rows, kForward, 0, u);
+        break;
+      }
+      if (phase < lead) {
+        const int count = gradient_units(a, rows, phase);
+        if (u < base + count) return tile(a, rows, kGradient, phase, u - base);
         base += count;
         continue;
       }
-      u -= base;
-      const int tile = u % (mt * nt);
-      x.split = u / (mt * nt);
-      const int m = mode == kWeight ? tile / nt : tile % mt;
-      const int n = mode == kWeight ? tile % nt : tile / mt;
-      x.mode = mode;
-      x.piece = p;
-      x.m0 = m * 256;
-      x.n0 = n * 256;
-      const int width = mode == kForward || mode == kGradient ? cols : int(a.D);
-      x.n = min(256, (width - x.n0 + 31) / 32 * 32);
-      const int depth = mode == kWeight ? rows : mode == kHidden ? cols : int(a.D);
-      const int blocks = (depth + kBlockK - 1) / kBlockK;
-      const int first = int(int64_t(blocks) * x.split / splits);
-      x.k0 = first * kBlockK;
-      x.blocks = int(int64_t(blocks) * (x.split + 1) / splits) - first;
-      if (x.blocks == 0) x.blocks = -1;
-      break;
+      const int p = (phase - lead) / 3, which = (phase - lead) % 3;
+      if (p >= prog.pieces) break;
+      const Mode mode = which == 0 ? kWeight : which == 1 ? kHidden : kGradient;
+      const int q = which == 2 ? p + 2 : p;
+      const int count = mode == kWeight ? weight_units(a, q) : mode == kHidden ? hidden_units(a, rows)
+                        : q < prog.pieces ? gradient_units(a, rows, q) : 0;
+      if (u < base + count) return tile(a, rows, mode, q, u - base);
+      base += count;
     }
+    Unit none{};
+    none.mode = -1;
+    return none;
+  }
+
+  __device__ __forceinline__ static Unit tile(const Args& a, int rows, Mode mode, int p, int u) {
+    const bool logits = mode == kForward || mode == kGradient;
+    const int cols = mode == kForward ? int(a.V) : piece_cols(a, p);
+    const int width = logits ? cols : int(a.D);
+    const int depth = mode == kWeight ? rows : mode == kHidden ? cols : int(a.D);
+    const int mt = tiles_of(mode == kWeight ? cols : rows), nt = tiles_of(width);
+    const int splits = mode == kHidden ? a.splits : 1;
+    const int at = u % (mt * nt);
+    Unit x;
+    x.mode = mode;
+    x.piece = p;
+    x.split = u / (mt * nt);
+    x.m0 = (mode == kWeight ? at / nt : at % mt) * 256;
+    x.n0 = (mode == kWeight ? at % nt : at / mt) * 256;
+    x.n = min(256, (width - x.n0 + 31) / 32 * 32);
+    const int blocks = (depth + kBlockK - 1) / kBlockK;
+    const int first = int(int64_t(blocks) * x.split / splits);
+    x.k0 = first * kBlockK;
+    x.blocks = int(int64_t(blocks) * (x.split + 1) / splits) - first;
+    if (x.blocks == 0) x.blocks = -1;
     return x;
   }
 };
@@ -785,8 +789,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                  acc_empty = acc_full + 16, ring_full = acc_empty + 16, ring_empty = ring_full + 8 * kRing;
   int4* ring = reinterpret_cast<int4*>(bars + 2 * kStages + 4 + 2 * kRing);
   static_assert((2 * kStages + 4 + 2 * kRing) % 2 == 0, "the ring is read 16 bytes at a time");
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ring + 2 * kRing);
+  uint64_t* stored_bars = reinterpret_cast<uint64_t*>(ring + 2 * kRing);
+  const uint32_t stored = smem_u32(stored_bars);
+  uint32_t** counts = reinterpret_cast<uint32_t**>(stored_bars + 2);  // [2][2]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(counts + 4);
   volatile uint32_t* given_up = tmem_slot + 1;
+  volatile int* counted = reinterpret_cast<volatile int*>(tmem_slot + 2);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
 
@@ -804,7 +812,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       barrier_init(ring_full + 8 * q, 1);
       barrier_init(ring_empty + 8 * q, 16);
     }
+    barrier_init(stored, 8);
+    barrier_init(stored + 8, 8);
     *given_up = 0;
+    *counted = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) {
@@ -853,7 +864,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (!(ok = next_unit()) || u.mode < 0) break;
           const bool a_mn = u.mode == kWeight, b_mn = u.mode == kWeight || u.mode == kHidden;
           if (b_mn && u.piece > formed) {
-            if (!(ok = progress.reached(a.formed + u.piece, 16 * gradient_units(a, rows, u.piece)))) break;
+            if (!(ok = progress.reached(a.formed + u.piece, 2 * gradient_units(a, rows, u.piece)))) break;
             formed = u.piece;
           }
           const int c0 = int(u.piece * a.piece), buffer = u.piece % kBuffers;
@@ -971,6 +982,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (x.mode < 0) break;
         }
       }
+    } else if (warp == 3 && !prog.forward) {
+      // ---- counts the finished units, off the epilogues' path: a release waits
+      // for stores still on their way, and theirs were 7 % of a backward pass
+      if (elect_one()) {
+        for (int n = 0; wait(stored + 8 * (n & 1), (n >> 1) & 1); ++n) {
+          uint32_t *const unit = counts[2 * (n & 1)], *const tile = counts[2 * (n & 1) + 1];
+          if (!unit) break;
+          if (tile) progress.arrive(tile);
+          progress.arrive(unit);
+          *counted = n + 1;
+        }
+      }
     }
   } else {
     // ---- epilogues
@@ -1001,14 +1024,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // A finished unit is counted once its stores are complete: at the end of
     // the next unit where both are kGradient, so that nothing waits for the
     // stores; else before the next unit's accumulator is waited for, since what
-    // that waits for may be this.
-    uint32_t* finished = nullptr;
+    // that waits for may be this. Each warp reports to warp 3; two units may be
+    // on their way there.
+    uint32_t *finished = nullptr, *finished_tile = nullptr;
+    int reports = 0;
+    auto report = [&](uint32_t* unit, uint32_t* tile) {
+      for (uint32_t n = 0; *counted < reports - 1 && !*given_up; ++n) __nanosleep(20);
+      if (warp == kEpilogueWarp) {
+        counts[2 * (reports & 1)] = unit;
+        counts[2 * (reports & 1) + 1] = tile;
+      }
+      asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(stored + 8 * (reports & 1)) : "memory");
+      ++reports;
+    };
     auto count_finished = [&] {
       if (lane == 0 && finished) {
         store_wait();
-        progress.arrive(finished);
+        report(finished, finished_tile);
       }
-      finished = nullptr;
+      finished = finished_tile = nullptr;
     };
     for (;;) {
       const uint32_t entry = in_cta(ring_empty + 8 * slot, 0);
@@ -1044,14 +1078,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       // The buffer that G goes to has been read by both products of the piece
-      // that was there; dH's sums have their earlier additions.
-      const int earlier = u.mode == kGradient ? u.piece - kBuffers : u.mode == kHidden ? u.piece - 1 : -1;
-      if (earlier >= 0 && earlier > used) {
+      // that was there; a tile of dH has its earlier pieces.
+      const int earlier = u.mode == kGradient ? u.piece - kBuffers : -1;
+      if (earlier > used) {
         count_finished();
-        ok = progress.reached(a.used + earlier, 16 * (weight_units(a, earlier) + hidden_units(a, rows)));
-        if (!__all_sync(~0u, ok)) break;
+        ok = progress.reached(a.used + earlier, 2 * (weight_units(a, earlier) + hidden_units(a, rows)));
         used = earlier;
       }
+      uint32_t* const tile = u.mode == kHidden ? hidden_tile(a, rows, u) : nullptr;
+      if (tile && u.piece > 0) {
+        count_finished();
+        ok = progress.reached(tile, 2 * u.piece);
+      }
+      if (!__all_sync(~0u, ok)) break;
       const uint32_t acc = lanes + buffer * 256;
       if (u.mode == kForward) {
         forward_epilogue<CE, KD>(a, u, th, r, acc);
@@ -1064,18 +1103,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         else gradient_epilogue<PLANES, CE, KD, 0>(a, out, u, th, r, acc, rank, boxes);
         if (lane == 0 && finished) {  // the unit before: its stores are the older ones
           asm volatile("cp.async.bulk.wait_group %0;" ::"n"(2) : "memory");
-          progress.arrive(finished);
+          report(finished, finished_tile);
         }
         finished = a.formed + u.piece;
+        finished_tile = nullptr;
       } else {
         if (u.mode == kHidden) hidden_epilogue(&prog.dh, u, th, acc, rank, boxes);
         else weight_epilogue<PLANES>(a, prog, u, th, factor, acc, rank, boxes);
         finished = a.used + u.piece;
+        finished_tile = tile;
       }
       give_back();
     }
     count_finished();
-    if (lane == 0) store_wait();
+    if (lane == 0) {
+      report(nullptr, nullptr);
+      store_wait();
+    }
   }
   __syncwarp();
   fence_before();
