@@ -14,13 +14,10 @@ using zl::Args;
 using zl::Program;
 using zl::set_error;
 
-#ifndef PIECEMB
-#define PIECEMB 40
-#endif
 constexpr int64_t kMostSize = 0x7fffffff - 1024;  // T, V and D: 32-bit tile coordinates
 // A piece of the logits' gradient is at most this many bytes (one tile's width
 // of columns at least); kBuffers of them are held.
-constexpr int64_t kPieceBytes = int64_t(PIECEMB) << 20;
+constexpr int64_t kPieceBytes = int64_t(54) << 20;
 
 int64_t round_up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
 

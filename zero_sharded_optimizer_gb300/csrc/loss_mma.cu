@@ -55,16 +55,16 @@ constexpr int kWarpBox = 32 * 64 * 2;      // 32 rows x 64 columns of G on their
 constexpr int kRing = 3;                   // units on their way to the warps
 constexpr int kRegsCopies = 88, kRegsEpilogue = 208;  // 128 x 88 + 256 x 208 = 384 x 168, the launch's
 
+// 192 KB of stages and 32 KB of boxes fill the 227 KB of shared memory. (Five
+// stages and two boxes a warp: 2 % slower on the backward pass.)
+constexpr int kStages = 6;
+constexpr int kSharedBytes = kStages * kStageBytes + 8 * kWarpBox + 1024 + 512;
+
+// 64-element blocks of K in a segment.
 template <int PLANES>
-struct Shape {
-  static constexpr int stages = PLANES == 1 ? 5 : 3;
-  static constexpr int boxes = PLANES == 1 ? 2 : PLANES;  // of each epilogue warp
-  static constexpr int bytes = stages * kStageBytes + 8 * boxes * kWarpBox + 1024 + 512;
-  // 64-element blocks of K in a segment.
-  __host__ __device__ static constexpr int segment(Mode mode) {
-    return PLANES == 3 ? 8 : mode == kForward ? 16 : 1 << 24;
-  }
-};
+__host__ __device__ constexpr int segment_of(int mode) {
+  return PLANES == 3 ? 8 : mode == kForward ? 16 : 1 << 24;
+}
 
 // ------------------------------------------------------------------- PTX --
 
@@ -308,7 +308,7 @@ __device__ __forceinline__ int blocks_of(const Unit& u) { return u.blocks < 0 ? 
 
 template <int PLANES>
 __device__ __forceinline__ int segments_of(const Unit& u) {
-  const int segment = Shape<PLANES>::segment(Mode(u.mode));
+  const int segment = segment_of<PLANES>(u.mode);
   return (blocks_of(u) + segment - 1) / segment;
 }
 
@@ -378,8 +378,8 @@ struct Phases {
     x.mode = mode;
     x.piece = p;
     x.split = u / (mt * nt);
-    x.m0 = (mode == kWeight ? at / nt : at % mt) * 256;
-    x.n0 = (mode == kWeight ? at % nt : at / mt) * 256;
+    x.m0 = (logits ? at % mt : at / nt) * 256;
+    x.n0 = (logits ? at / mt : at % nt) * 256;
     x.n = min(256, (width - x.n0 + 31) / 32 * 32);
     const int blocks = (depth + kBlockK - 1) / kBlockK;
     const int first = int(int64_t(blocks) * x.split / splits);
@@ -550,30 +550,23 @@ __device__ __forceinline__ void forward_epilogue(const Args& a, const Unit& u, c
   if (KD) a.stats_tau[at] = make_float2(nan ? NAN : s.m_kd, s.kd);
 }
 
-// Two neighbouring values of G as their words of the operand's parts.
+// Two neighbouring values of G as a word of the operand's part p.
 template <int PLANES>
-__device__ __forceinline__ void pack_parts(float x0, float x1, uint32_t (&word)[PLANES]) {
+__device__ __forceinline__ uint32_t pack_part(float x0, float x1, int p) {
   if (PLANES == 1) {
-    __nv_bfloat162 h = __floats2bfloat162_rn(x0, x1);
-    word[0] = *reinterpret_cast<uint32_t*>(&h);
-  } else {
-    __nv_bfloat16 p0[3], p1[3];
-    split(x0, p0);
-    split(x1, p1);
-#pragma unroll
-    for (int p = 0; p < PLANES; ++p)
-      word[p] = uint32_t(__bfloat16_as_ushort(p0[p])) | uint32_t(__bfloat16_as_ushort(p1[p])) << 16;
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x0, x1);
+    return *reinterpret_cast<const uint32_t*>(&h);
   }
+  __nv_bfloat16 p0[3], p1[3];
+  split(x0, p0);
+  split(x1, p1);
+  const __nv_bfloat16 h0 = p == 0 ? p0[0] : p == 1 ? p0[1] : p0[2], h1 = p == 0 ? p1[0] : p == 1 ? p1[1] : p1[2];
+  return uint32_t(__bfloat16_as_ushort(h0)) | uint32_t(__bfloat16_as_ushort(h1)) << 16;
 }
 
-// A warp's staging box may be written again: its last store has read it.
-// `Two`: boxes are used in turn, the other one's store may still be reading.
-template <bool Two>
+// The warp's staging box may be written again: its last store has read it.
 __device__ __forceinline__ void box_free(int lane) {
-  if (lane == 0) {
-    if (Two) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-    else asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-  }
+  if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
   __syncwarp();
 }
 
@@ -591,7 +584,7 @@ __device__ __forceinline__ void stage_fp32(uint8_t* box, int lane, const float (
 template <int PLANES, bool CE, bool KD, int P>
 __device__ __forceinline__ void gradient_epilogue(const Args& a, const CUtensorMap* out, const Unit& u,
                                                   const Thread& th, Row& r, uint32_t acc, uint32_t rank,
-                                                  uint8_t* staging) {
+                                                  uint8_t* box) {
   const int64_t v0 = u.piece * a.piece + u.n0;
   const int begin = th.half * 128, lane = th.row & 31;
   const int cols = int(min(int64_t(256), a.V - v0));
@@ -619,9 +612,10 @@ __device__ __forceinline__ void gradient_epilogue(const Args& a, const CUtensorM
     return g;
   };
 #pragma unroll 1
-  for (int b = 0; b < 2; ++b) {
-    uint8_t* box = staging + (PLANES == 1 ? b * kWarpBox : 0);
-    box_free<PLANES == 1>(lane);
+  for (int n = 0; n < 2 * PLANES; ++n) {
+    const int b = n / PLANES, p = n % PLANES;  // 64 columns; the part of them
+    const Row start = r;                       // each part goes through the entries
+    box_free(lane);
 #pragma unroll 1
     for (int k = 0; k < 2; ++k) {
       const int c0 = begin + 64 * b + 32 * k;
@@ -637,32 +631,23 @@ __device__ __forceinline__ void gradient_epilogue(const Args& a, const CUtensorM
       }
 #pragma unroll
       for (int j = 0; j < 32; j += 8) {
-        uint32_t word[4][PLANES];
+        uint32_t word[4];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) pack_parts<PLANES>(z[j + 2 * q], z[j + 2 * q + 1], word[q]);
-        const int chunk = (4 * k + j / 8) ^ (lane & 7);
-#pragma unroll
-        for (int p = 0; p < PLANES; ++p)
-          *reinterpret_cast<uint4*>(box + p * kWarpBox + lane * 128 + chunk * 16) =
-              make_uint4(word[0][p], word[1][p], word[2][p], word[3][p]);
+        for (int q = 0; q < 4; ++q) word[q] = pack_part<PLANES>(z[j + 2 * q], z[j + 2 * q + 1], p);
+        *reinterpret_cast<uint4*>(box + lane * 128 + (((4 * k + j / 8) ^ (lane & 7)) * 16)) =
+            make_uint4(word[0], word[1], word[2], word[3]);
       }
     }
     each_entry(a, u, r, v0, begin + 64 * (b + 1), acc, [&](int c, float z) {
-      const float g = value(z) - r.scale * r.w;
       const int at = c - begin - 64 * b;
-      uint8_t* to = box + lane * 128 + (((at / 8) ^ (lane & 7)) * 16) + (at % 8) * 2;
-      uint32_t word[PLANES];
-      pack_parts<PLANES>(g, 0.0f, word);
-#pragma unroll
-      for (int p = 0; p < PLANES; ++p) *reinterpret_cast<uint16_t*>(to + p * kWarpBox) = uint16_t(word[p]);
+      *reinterpret_cast<uint16_t*>(box + lane * 128 + (((at / 8) ^ (lane & 7)) * 16) + (at % 8) * 2) =
+          uint16_t(pack_part<PLANES>(value(z) - r.scale * r.w, 0.0f, p));
     });
+    if (p < PLANES - 1) r = start;
     proxy_fence();
     __syncwarp();
     if (lane == 0) {
-#pragma unroll
-      for (int p = 0; p < PLANES; ++p)
-        tma_store(out, smem_u32(box + p * kWarpBox), u.n0 + begin + 64 * b, u.m0 + int(rank) * kHalf + th.row,
-                  p);
+      tma_store(out, smem_u32(box), u.n0 + begin + 64 * b, u.m0 + int(rank) * kHalf + th.row, p);
       store_commit();
     }
   }
@@ -682,16 +667,15 @@ __device__ __forceinline__ void load_terms(const Unit& u, uint32_t addr, float (
 // reductions). An element gets one addition of each piece, and a piece's come
 // after the one before is complete, so the order is fixed.
 __device__ __forceinline__ void hidden_epilogue(const CUtensorMap* out, const Unit& u, const Thread& th, uint32_t acc,
-                                                uint32_t rank, uint8_t* staging) {
+                                                uint32_t rank, uint8_t* box) {
   const int lane = th.row & 31, begin = th.half * 128;
 #pragma unroll 1
   for (int k = 0; k < 4; ++k) {
     const int c = begin + 32 * k;
     if (c >= u.n) break;
-    uint8_t* box = staging + (k & 1) * kWarpBox;
     float x[32];
     load_terms(u, acc + c, x);
-    box_free<true>(lane);
+    box_free(lane);
     stage_fp32(box, lane, x);
     proxy_fence();
     __syncwarp();
@@ -709,7 +693,7 @@ __device__ __forceinline__ void hidden_epilogue(const CUtensorMap* out, const Un
 // by the threads.
 template <int PLANES>
 __device__ __forceinline__ void weight_epilogue(const Args& a, const Program& prog, const Unit& u, const Thread& th,
-                                                float factor, uint32_t acc, uint32_t rank, uint8_t* staging) {
+                                                float factor, uint32_t acc, uint32_t rank, uint8_t* box) {
   using T = typename std::conditional<PLANES == 1, __nv_bfloat16, float>::type;
   const int lane = th.row & 31, begin = th.half * 128;
   const int64_t v = u.piece * a.piece + u.m0 + int(rank) * kHalf + th.row;
@@ -719,8 +703,7 @@ __device__ __forceinline__ void weight_epilogue(const Args& a, const Program& pr
     for (int k = 0; k < 128 / wide; ++k) {
       const int c = begin + wide * k;
       if (c >= u.n) break;
-      uint8_t* box = staging + (k & 1) * kWarpBox;
-      box_free<true>(lane);
+      box_free(lane);
 #pragma unroll
       for (int h = 0; h < wide / 32; ++h) {
         float x[32];
@@ -732,11 +715,11 @@ __device__ __forceinline__ void weight_epilogue(const Args& a, const Program& pr
         } else {
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            uint32_t word[4][1];
+            uint32_t word[4];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) pack_parts<1>(x[8 * j + 2 * q], x[8 * j + 2 * q + 1], word[q]);
+            for (int q = 0; q < 4; ++q) word[q] = pack_part<1>(x[8 * j + 2 * q], x[8 * j + 2 * q + 1], 0);
             *reinterpret_cast<uint4*>(box + lane * 128 + (((4 * h + j) ^ (lane & 7)) * 16)) =
-                make_uint4(word[0][0], word[1][0], word[2][0], word[3][0]);
+                make_uint4(word[0], word[1], word[2], word[3]);
           }
         }
       }
@@ -754,20 +737,21 @@ __device__ __forceinline__ void weight_epilogue(const Args& a, const Program& pr
   // 32 columns at a time through shared memory, so that a warp's accesses run
   // along a row.
   const int64_t v_warp = v - lane;
-  float* box = reinterpret_cast<float*>(staging);
+  const float* values = reinterpret_cast<const float*>(box);
+  box_free(lane);
 #pragma unroll 1
   for (int c = begin; c < min(u.n, begin + 128); c += 32) {
     float x[32];
     load_terms(u, acc + c, x);
     __syncwarp();
-    stage_fp32(staging, lane, x);
+    stage_fp32(box, lane, x);
     __syncwarp();
     const bool in = u.n0 + c + lane < a.D;
     T* to = static_cast<T*>(a.dweight) + v_warp * a.dweight_stride + u.n0 + c + lane;
 #pragma unroll 4
     for (int i = 0; i < 32; ++i, to += a.dweight_stride) {
       if (!in || v_warp + i >= a.V) continue;
-      const float y = factor * box[i * 32 + (((lane / 4) ^ (i & 7)) * 4) + lane % 4];
+      const float y = factor * values[i * 32 + (((lane / 4) ^ (i & 7)) * 4) + lane % 4];
       *to = T(a.accumulate ? float(*to) + y : y);
     }
   }
@@ -778,12 +762,11 @@ __device__ __forceinline__ void weight_epilogue(const Args& a, const Program& pr
 template <int PLANES, bool CE, bool KD>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     products_kernel(const __grid_constant__ Args a, const __grid_constant__ Program prog) {
-  constexpr int kStages = Shape<PLANES>::stages;
   constexpr int kTerms = PLANES == 1 ? 1 : 6;
   extern __shared__ uint8_t raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   uint8_t* staging = base + kStages * kStageBytes;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(staging + 8 * Shape<PLANES>::boxes * kWarpBox);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(staging + 8 * kWarpBox);
   // Barriers: stage full and empty, accumulator full and empty, ring full and empty.
   const uint32_t full = smem_u32(bars), empty = full + 8 * kStages, acc_full = empty + 8 * kStages,
                  acc_empty = acc_full + 16, ring_full = acc_empty + 16, ring_empty = ring_full + 8 * kRing;
@@ -879,7 +862,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const uint32_t bytes = 2 * ((a_mn ? kOperandBytes : prog.box_rows * kBlockK * 2) +
                                       (b_mn ? b_boxes * 64 * kBlockK * 2 : kOperandBytes));
           const int segments = segments_of<PLANES>(u);
-          const int segment = Shape<PLANES>::segment(Mode(u.mode));
+          const int segment = segment_of<PLANES>(u.mode);
           for (int s = 0; ok && s < segments; ++s) {
             const int k_begin = s * segment, k_end = min(blocks_of(u), k_begin + segment);
             for (int term = 0; ok && term < kTerms; ++term) {
@@ -930,7 +913,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const uint32_t idesc = 1u << 4 | 1u << 7 | 1u << 10 | uint32_t(a_mn) << 15 | uint32_t(b_mn) << 16 |
                                  uint32_t(u.n / 8) << 17 | uint32_t(256 / 16) << 24;
           const uint64_t a_step = (a_mn ? 16 * 128 : 32) >> 4, b_step = (b_mn ? 16 * 128 : 32) >> 4;
-          const int segment = Shape<PLANES>::segment(Mode(u.mode));
+          const int segment = segment_of<PLANES>(u.mode);
           for (int s = 0; ok && s < segments; ++s) {
             const uint32_t d = tmem + buffer * 256;
             if (!(ok = wait(acc_empty + 8 * buffer, acc_phase ^ 1))) break;
@@ -1001,7 +984,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     Thread th;
     th.row = (warp & 3) * 32 + lane;
     th.half = (warp - kEpilogueWarp) / 4;
-    uint8_t* boxes = staging + (warp - kEpilogueWarp) * Shape<PLANES>::boxes * kWarpBox;
+    uint8_t* box = staging + (warp - kEpilogueWarp) * kWarpBox;
     const uint32_t lanes = tmem + (uint32_t((warp & 3) * 32) << 16);
     const uint32_t acc_empty0 = in_cta(acc_empty, 0);
     const float factor = a.head->factor;
@@ -1097,19 +1080,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       } else if (u.mode == kGradient) {
         const CUtensorMap* out = &prog.g_out[u.piece % kBuffers];
         const int p = CE && KD ? shared_power(float(a.tau)) : 0;
-        if (CE && KD && p == 1) gradient_epilogue<PLANES, CE, KD, 1>(a, out, u, th, r, acc, rank, boxes);
-        else if (CE && KD && p == 2) gradient_epilogue<PLANES, CE, KD, 2>(a, out, u, th, r, acc, rank, boxes);
-        else if (CE && KD && p == 4) gradient_epilogue<PLANES, CE, KD, 4>(a, out, u, th, r, acc, rank, boxes);
-        else gradient_epilogue<PLANES, CE, KD, 0>(a, out, u, th, r, acc, rank, boxes);
+        if (CE && KD && p == 1) gradient_epilogue<PLANES, CE, KD, 1>(a, out, u, th, r, acc, rank, box);
+        else if (CE && KD && p == 2) gradient_epilogue<PLANES, CE, KD, 2>(a, out, u, th, r, acc, rank, box);
+        else if (CE && KD && p == 4) gradient_epilogue<PLANES, CE, KD, 4>(a, out, u, th, r, acc, rank, box);
+        else gradient_epilogue<PLANES, CE, KD, 0>(a, out, u, th, r, acc, rank, box);
         if (lane == 0 && finished) {  // the unit before: its stores are the older ones
-          asm volatile("cp.async.bulk.wait_group %0;" ::"n"(2) : "memory");
+          asm volatile("cp.async.bulk.wait_group %0;" ::"n"(2 * PLANES) : "memory");
           report(finished, finished_tile);
         }
         finished = a.formed + u.piece;
         finished_tile = nullptr;
       } else {
-        if (u.mode == kHidden) hidden_epilogue(&prog.dh, u, th, acc, rank, boxes);
-        else weight_epilogue<PLANES>(a, prog, u, th, factor, acc, rank, boxes);
+        if (u.mode == kHidden) hidden_epilogue(&prog.dh, u, th, acc, rank, box);
+        else weight_epilogue<PLANES>(a, prog, u, th, factor, acc, rank, box);
         finished = a.used + u.piece;
         finished_tile = tile;
       }
@@ -1139,13 +1122,13 @@ cudaError_t launch(const Args& a, const Program& prog, int sms, cudaStream_t s) 
     cudaError_t e = cudaFuncGetAttributes(&at, kernel);
     if (e != cudaSuccess) return e;
     if (at.numRegs * kThreads < 128 * kRegsCopies + 256 * kRegsEpilogue) return cudaErrorLaunchOutOfResources;
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<PLANES>::bytes);
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSharedBytes);
   }();
   if (ready != cudaSuccess) return ready;
   cudaLaunchConfig_t c = {};
   c.gridDim = dim3(unsigned(sms / 2 * 2));
   c.blockDim = dim3(kThreads);
-  c.dynamicSmemBytes = Shape<PLANES>::bytes;
+  c.dynamicSmemBytes = kSharedBytes;
   c.stream = s;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
