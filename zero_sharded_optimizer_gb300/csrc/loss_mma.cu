@@ -56,7 +56,8 @@ constexpr int kRing = 3;                   // units on their way to the warps
 constexpr int kRegsCopies = 88, kRegsEpilogue = 208;  // 128 x 88 + 256 x 208 = 384 x 168, the launch's
 
 // 192 KB of stages and 32 KB of boxes fill the 227 KB of shared memory. (Five
-// stages and two boxes a warp: 2 % slower on the backward pass.)
+// stages and two boxes a warp: 2 % slower on a backward pass in bf16, the same
+// in fp32.)
 constexpr int kStages = 6;
 constexpr int kSharedBytes = kStages * kStageBytes + 8 * kWarpBox + 1024 + 512;
 
@@ -264,13 +265,6 @@ __device__ __forceinline__ void tmem_store32(uint32_t addr, const float (&v)[32]
       "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(addr)
       : "memory");
 }
-__device__ __forceinline__ float tmem_load1(uint32_t addr) {
-  float v;
-  __syncwarp();
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\ntcgen05.wait::ld.sync.aligned;"
-               : "=f"(v) : "r"(addr) : "memory");
-  return v;
-}
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -445,26 +439,22 @@ __device__ __forceinline__ Row row_of(const Args& a, int rows, const Unit& u, co
   return r;
 }
 
-// Calls f(column, logit) for each of the row's sparse entries (r.e, weight
-// r.w) with a column below `end` relative to v0, the logit read from the
-// accumulator: all lanes of the warp read the same column, lowest first.
+// Calls f(at) while a row of the warp has a sparse entry (r.e, of weight r.w)
+// among the 32 columns from v on: `at` is the thread's own entry's column among
+// them, or -1. (The columns are registers, so f picks by comparing.)
 template <typename F>
-__device__ __forceinline__ void each_entry(const Args& a, const Unit& u, Row& r, int64_t v0, int end, uint32_t acc,
-                                           F f) {
+__device__ __forceinline__ void each_entry(const Args& a, const Unit& u, Row& r, int64_t v, F f) {
   for (;;) {
-    const int64_t at = r.id - v0;
-    const int mine = at >= 0 && at < end ? int(at) : 0x7fffffff;
-    const int c = __reduce_min_sync(~0u, mine);
-    if (c == 0x7fffffff) break;
-    const float z = tmem_load1(acc + c);
-    if (mine == c) {
-      f(c, z);
+    const int64_t c = r.id - v;
+    const int at = c >= 0 && c < 32 ? int(c) : -1;
+    if (!__any_sync(~0u, at >= 0)) break;
+    f(at);
+    if (at >= 0) {
       ++r.e;
       r.id = r.next_id;
       r.w = r.next_w;
       entry_ahead(a, u, r, r.e + 1, r.next_id, r.next_w);
     }
-    __syncwarp();
   }
 }
 
@@ -526,6 +516,13 @@ __device__ __forceinline__ void forward_epilogue(const Args& a, const Unit& u, c
       for (int j = 0; j < 32; ++j)
         if (j >= valid) z[j] = -INFINITY;
     }
+    each_entry(a, u, r, v0 + begin + 32 * k, [&](int at) {
+      float x = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        if (j == at) x = z[j];
+      if (at >= 0) a.zent[r.t * a.L + r.e] = x;
+    });
     float t0 = top, t1 = -INFINITY;
 #pragma unroll
     for (int j = 0; j < 32; j += 2) {
@@ -542,7 +539,6 @@ __device__ __forceinline__ void forward_epilogue(const Args& a, const Unit& u, c
       add_exponentials<CE, KD, 0>(z, top, c_ce, c_kd, s);
     }
   }
-  each_entry(a, u, r, v0, begin + 128, acc, [&](int, float z) { a.zent[r.t * a.L + r.e] = z; });
   if (!r.there) return;
   const int64_t at = (v0 / 256 * 2 + th.half) * a.Tp + r.i;
   const bool nan = isnan(s.ce + s.kd);
@@ -583,8 +579,7 @@ __device__ __forceinline__ void stage_fp32(uint8_t* box, int lane, const float (
 // Each warp stages boxes of its 32 rows by 64 columns and stores them by TMA.
 template <int PLANES, bool CE, bool KD, int P>
 __device__ __forceinline__ void gradient_epilogue(const Args& a, const CUtensorMap* out, const Unit& u,
-                                                  const Thread& th, Row& r, uint32_t acc, uint32_t rank,
-                                                  uint8_t* box) {
+                                                  const Thread& th, Row& r, uint32_t acc, uint32_t rank, uint8_t* box) {
   const int64_t v0 = u.piece * a.piece + u.n0;
   const int begin = th.half * 128, lane = th.row & 31;
   const int cols = int(min(int64_t(256), a.V - v0));
@@ -611,44 +606,64 @@ __device__ __forceinline__ void gradient_epilogue(const Args& a, const CUtensorM
     }
     return g;
   };
-#pragma unroll 1
-  for (int n = 0; n < 2 * PLANES; ++n) {
-    const int b = n / PLANES, p = n % PLANES;  // 64 columns; the part of them
-    const Row start = r;                       // each part goes through the entries
-    box_free(lane);
-#pragma unroll 1
-    for (int k = 0; k < 2; ++k) {
-      const int c0 = begin + 64 * b + 32 * k;
-      float z[32];
-      tmem_load32(acc + c0, z);
-      const int valid = cols - c0;
+  // 32 columns of the row.
+  auto columns = [&](int c0, float (&g)[32]) {
+    tmem_load32(acc + c0, g);
+    const int valid = cols - c0;
 #pragma unroll
-      for (int j = 0; j < 32; ++j) z[j] = value(z[j]);
-      if (valid < 32 || !r.there) {
+    for (int j = 0; j < 32; ++j) g[j] = value(g[j]);
+    if (valid < 32 || !r.there) {
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
-          if (j >= valid || !r.there) z[j] = 0.0f;
-      }
-#pragma unroll
-      for (int j = 0; j < 32; j += 8) {
-        uint32_t word[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) word[q] = pack_part<PLANES>(z[j + 2 * q], z[j + 2 * q + 1], p);
-        *reinterpret_cast<uint4*>(box + lane * 128 + (((4 * k + j / 8) ^ (lane & 7)) * 16)) =
-            make_uint4(word[0], word[1], word[2], word[3]);
-      }
+      for (int j = 0; j < 32; ++j)
+        if (j >= valid || !r.there) g[j] = 0.0f;
     }
-    each_entry(a, u, r, v0, begin + 64 * (b + 1), acc, [&](int c, float z) {
-      const int at = c - begin - 64 * b;
-      *reinterpret_cast<uint16_t*>(box + lane * 128 + (((at / 8) ^ (lane & 7)) * 16) + (at % 8) * 2) =
-          uint16_t(pack_part<PLANES>(value(z) - r.scale * r.w, 0.0f, p));
+    each_entry(a, u, r, v0 + c0, [&](int at) {
+      const float d = r.scale * r.w;
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        if (j == at) g[j] -= d;
     });
-    if (p < PLANES - 1) r = start;
+  };
+  // Their part p into half a box.
+  auto stage = [&](int half, int p, const float (&g)[32]) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const float* x = &g[8 * q];
+      *reinterpret_cast<uint4*>(box + lane * 128 + (((4 * half + q) ^ (lane & 7)) * 16)) =
+          make_uint4(pack_part<PLANES>(x[0], x[1], p), pack_part<PLANES>(x[2], x[3], p),
+                     pack_part<PLANES>(x[4], x[5], p), pack_part<PLANES>(x[6], x[7], p));
+    }
+  };
+  auto store = [&](int b, int p) {
     proxy_fence();
     __syncwarp();
     if (lane == 0) {
       tma_store(out, smem_u32(box), u.n0 + begin + 64 * b, u.m0 + int(rank) * kHalf + th.row, p);
       store_commit();
+    }
+  };
+#pragma unroll 1
+  for (int b = 0; b < 2; ++b) {  // 64 columns at a time
+    if (PLANES == 1) {
+      box_free(lane);
+#pragma unroll 1
+      for (int k = 0; k < 2; ++k) {
+        float g[32];
+        columns(begin + 64 * b + 32 * k, g);
+        stage(k, 0, g);
+      }
+      store(b, 0);
+    } else {
+      float g[2][32];
+      columns(begin + 64 * b, g[0]);
+      columns(begin + 64 * b + 32, g[1]);
+#pragma unroll
+      for (int p = 0; p < PLANES; ++p) {
+        box_free(lane);
+        stage(0, p, g[0]);
+        stage(1, p, g[1]);
+        store(b, p);
+      }
     }
   }
 }
@@ -725,10 +740,12 @@ __device__ __forceinline__ void weight_epilogue(const Args& a, const Program& pr
       }
       proxy_fence();
       __syncwarp();
-      if (lane == 0 && v < a.V) {
+      if (lane == 0) {
         // Rows and columns past the matrix are not written.
-        if (a.accumulate) tma_add(&prog.dweight, smem_u32(box), u.n0 + c, int(v), 0);
-        else tma_store(&prog.dweight, smem_u32(box), u.n0 + c, int(v), 0);
+        if (v < a.V) {
+          if (a.accumulate) tma_add(&prog.dweight, smem_u32(box), u.n0 + c, int(v), 0);
+          else tma_store(&prog.dweight, smem_u32(box), u.n0 + c, int(v), 0);
+        }
         store_commit();
       }
     }
@@ -737,8 +754,8 @@ __device__ __forceinline__ void weight_epilogue(const Args& a, const Program& pr
   // 32 columns at a time through shared memory, so that a warp's accesses run
   // along a row.
   const int64_t v_warp = v - lane;
-  const float* values = reinterpret_cast<const float*>(box);
   box_free(lane);
+  const float* values = reinterpret_cast<const float*>(box);
 #pragma unroll 1
   for (int c = begin; c < min(u.n, begin + 128); c += 32) {
     float x[32];
