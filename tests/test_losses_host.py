@@ -114,7 +114,8 @@ def test_workspace_sizes(abi):
     assert size(**big) < 8192 * 50257 * 2 / 4
     forward = size(**dict(big, dhidden=None, dweight=None))
     assert forward < size(**big)
-    assert forward < 8192 * 768 * 2 + 8192 * 200 * 8 + (1 << 20)
+    # packed rows, and 8 bytes of statistics for each half tile of 128 columns
+    assert forward < 8192 * 768 * 2 + 8192 * 400 * 8 + (1 << 20)
     # rows that 16-byte copies cannot read are packed first
     assert size(**dict(big, weight_stride=769)) >= size(**big) + 50257 * 768 * 2
     assert size(T=0) > 0

@@ -208,7 +208,19 @@ int plan(const zero_head_loss_t* p, bool distill, int pass, Args* a, __nv_bfloat
   a->dhidden_stride = p->dhidden_stride;
   a->dweight = p->dweight;
   a->dweight_stride = p->dweight_stride;
-  a->tiles = (p->V + zl::kTileN - 1) / zl::kTileN;
+  // With few tiles, narrower ones where they fill the last round of 76 CTA
+  // pairs better: the rounds times the width decide (one token of a vocabulary
+  // of 50257: three rounds of 224 columns instead of three of 256).
+  a->tile_n = zl::kTileN;
+  int64_t least = INT64_MAX;
+  for (int32_t n = zl::kTileN; n >= 160; n -= 32) {
+    const int64_t units = a->Tp / zl::kTileM * ((p->V + n - 1) / n), rounds = (units + 75) / 76;
+    if (rounds * n < least && (n == zl::kTileN || rounds <= 8)) {
+      least = rounds * n;
+      a->tile_n = n;
+    }
+  }
+  a->tiles = (p->V + a->tile_n - 1) / a->tile_n;
 
   Layout w{static_cast<uint8_t*>(p->workspace)};
   a->head = w.take<zl::Head>(1);
@@ -218,7 +230,12 @@ int plan(const zero_head_loss_t* p, bool distill, int pass, Args* a, __nv_bfloat
   a->konst = w.take<float>(a->T);
   a->ids = w.take<int32_t>(a->T, a->L);
   a->weights = w.take<float>(a->T, a->L);
-  if (a->K) a->starts = w.take<uint16_t>(2 * a->tiles + 1, a->T);
+  if (a->K) {
+    const int64_t back = (p->V + zl::kTileN - 1) / zl::kTileN;
+    if (pass & kForward) a->starts = w.take<uint16_t>(2 * a->tiles + 1, a->T);
+    if (pass & kBackward)
+      a->starts_back = a->starts && a->tile_n == zl::kTileN ? a->starts : w.take<uint16_t>(2 * back + 1, a->T);
+  }
   a->hp = w.take<__nv_bfloat16>(a->Tp * a->planes, a->Dp);
   if (weight_in_place(p)) {
     *packed_weight = nullptr;

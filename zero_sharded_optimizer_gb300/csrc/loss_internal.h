@@ -77,13 +77,17 @@ struct Args {
   float* konst;           // [T] the loss's part that no logit enters
   int32_t* ids;           // [T][L] ascending, kNoId after the last
   float* weights;         // [T][L] weight of each entry's logit in loss and gradient
-  uint16_t* starts;       // distillation: [2 tiles + 1][T] first entry of each half tile
+  // Distillation: [2 tiles + 1][T] first entry of each half tile, of the forward
+  // pass's tiles and of the backward pass's.
+  uint16_t* starts;
+  uint16_t* starts_back;
   double* sums;           // [kLossBlocks] parts of the reduced loss
   float* zent;            // [T][L] logits of the entries
   __nv_bfloat16* hp;      // [planes][Tp][Dp] packed hidden states
   const __nv_bfloat16* wp;  // [planes][V][Dp], or the caller's weight (then wp_ld)
   int64_t wp_ld, wp_plane;
-  int64_t tiles;          // vocabulary tiles
+  int32_t tile_n;         // columns of a tile of the forward pass: up to kTileN
+  int64_t tiles;          // its tiles of the vocabulary
   float2* stats;          // [2 tiles][Tp] half a tile's (m, sum of 2^(z log2(e) - m))
   float2* stats_tau;      // [2 tiles][Tp] of z / tau
   int32_t* counters;      // [2] units handed out, forward and backward

@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(256) label_rows_kernel(const Args a) {
 }
 
 // A block's rows, one a warp, and where each half tile's entries begin in
-// them: starts[h][t] is the first entry with an id of 128 h at least.
+// them: starts[h][t] is the first entry from the half tile's first column on.
 __global__ void teacher_rows_kernel(const Args a) {
   extern __shared__ __align__(16) int32_t sh[];
   __shared__ int kept[16];
@@ -176,12 +176,24 @@ __global__ void teacher_rows_kernel(const Args a) {
     if (lane == 0) kept[warp] = n;
   }
   __syncthreads();
-  const int halves = int(2 * a.tiles + 1), r = threadIdx.x & (rows - 1);  // rows: a power of two
+  const int r = threadIdx.x & (rows - 1);  // rows: a power of two
   if (t0 + r >= a.T) return;
   const int32_t* ids = sh + r * 4 * n4;
   const int n = kept[r];
-  for (int h = threadIdx.x / rows; h < halves; h += 32)
-    a.starts[h * a.T + t0 + r] = uint16_t(first_entry(ids, n, h * 128));
+  auto fill = [&](uint16_t* starts, int wide) {
+    // 32 threads a row, each a stretch of the half tiles.
+    const int halves = 2 * int((a.V + wide - 1) / wide) + 1, stretch = (halves + 31) / 32;
+    const int h0 = threadIdx.x / rows * stretch, h1 = min(halves, h0 + stretch);
+    int e = -1;
+    for (int h = h0; h < h1; ++h) {
+      const int column = h / 2 * wide + h % 2 * 128;
+      if (e < 0) e = first_entry(ids, n, column);
+      while (e < n && ids[e] < column) ++e;
+      starts[h * a.T + t0 + r] = uint16_t(e);
+    }
+  };
+  if (a.starts) fill(a.starts, a.tile_n);
+  if (a.starts_back && a.starts_back != a.starts) fill(a.starts_back, 256);
 }
 
 // ------------------------------------------------------------------- pack --
@@ -335,6 +347,7 @@ __global__ void __launch_bounds__(256) dhidden_out_kernel(const Args a) {
     const int32_t i = a.rowpos[t];
     float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (i >= 0) {
+#pragma unroll 8
       for (int p = 0; p < a.splits; ++p) {
         const float4 y = *reinterpret_cast<const float4*>(a.dh + (p * a.Tp + i) * a.Dp + d);
         x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
@@ -427,18 +440,26 @@ __global__ void __launch_bounds__(256) losses_kernel(const Args a, int block_row
     const int64_t i = min(i0 + r, int64_t(rows) - 1);
     const int64_t t = a.rowmap[i];
     double entries = 0.0;
-    for (int e = lane; e < a.L; e += lanes)
-      if (a.ids[t * a.L + e] != kNoId) entries += double(a.weights[t * a.L + e]) * double(a.zent[t * a.L + e]);
-    part[threadIdx.x] = entries;
+#pragma unroll 4
+    for (int e = lane; e < a.L; e += lanes) {
+      const int64_t at = t * a.L + e;
+      if (a.ids[at] != kNoId) entries += double(a.weights[at]) * double(a.zent[at]);
+    }
     const double lse = a.has_ce ? row_lse(a.stats, 2 * a.tiles, a.Tp, i, lane, lanes, sh, r, block_rows) : 0.0;
     const double lse_tau =
         a.has_kd ? row_lse(a.stats_tau, 2 * a.tiles, a.Tp, i, lane, lanes, sh, r, block_rows) : 0.0;
+    part[threadIdx.x] = entries;
+    __syncthreads();
+    for (int w = lanes / 2; w; w >>= 1) {
+      if (lane < w) part[threadIdx.x] += part[threadIdx.x + w * block_rows];
+      __syncthreads();
+    }
     if (lane == 0 && i0 + r < rows) {
       const float2 f = a.coef[t];
       double loss = double(a.konst[t]);
       if (f.x != 0.0f) loss += double(f.x) * lse;
       if (f.y != 0.0f) loss += double(f.y) * a.tau * lse_tau;
-      for (int q = 0; q < min(lanes, a.L); ++q) loss -= part[q * block_rows + r];
+      loss -= part[r];
       if (a.head->fault) loss = NAN;
       a.loss[t] = float(loss);
       if (a.has_ce) a.lse[t] = float(lse);
@@ -516,7 +537,8 @@ cudaError_t launch_rows(const Args& a, bool pack_weight, bool* packed, cudaStrea
       e = launch(label_rows_kernel, unsigned((a.T + 255) / 256), 256, 0, s, false, a);
     } else {
       const size_t row = size_t(16) * ((a.K + 4) / 4 * 4);
-      const int rows = 16 * row <= 48 * 1024 ? 16 : 2;
+      int rows = 16 * row <= 48 * 1024 ? 16 : 2;
+      while (rows > 2 && a.T / rows < 152) rows /= 2;
       e = launch(teacher_rows_kernel, unsigned((a.T + rows - 1) / rows), rows * 32, rows * row, s, false, a);
     }
   }

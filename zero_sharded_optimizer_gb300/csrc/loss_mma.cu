@@ -336,7 +336,7 @@ struct Phases {
     for (;; ++phase) {
       if (prog.forward) {
         if (phase > 0) break;
-        const int count = tiles_of(rows) * tiles_of(int(a.V));
+        const int count = tiles_of(rows) * int(a.tiles);
         if (u < count) return tile(a, rows, kForward, 0, u);
         break;
       }
@@ -365,7 +365,8 @@ struct Phases {
     const int cols = mode == kForward ? int(a.V) : piece_cols(a, p);
     const int width = logits ? cols : int(a.D);
     const int depth = mode == kWeight ? rows : mode == kHidden ? cols : int(a.D);
-    const int mt = tiles_of(mode == kWeight ? cols : rows), nt = tiles_of(width);
+    const int wide = mode == kForward ? a.tile_n : 256;
+    const int mt = tiles_of(mode == kWeight ? cols : rows), nt = (width + wide - 1) / wide;
     const int splits = mode == kHidden ? a.splits : 1;
     const int at = u % (mt * nt);
     Unit x;
@@ -373,8 +374,8 @@ struct Phases {
     x.piece = p;
     x.split = u / (mt * nt);
     x.m0 = (logits ? at % mt : at / nt) * 256;
-    x.n0 = (logits ? at / mt : at % nt) * 256;
-    x.n = min(256, (width - x.n0 + 31) / 32 * 32);
+    x.n0 = (logits ? at / mt : at % nt) * wide;
+    x.n = min(wide, (width - x.n0 + 31) / 32 * 32);
     const int blocks = (depth + kBlockK - 1) / kBlockK;
     const int first = int(int64_t(blocks) * x.split / splits);
     x.k0 = first * kBlockK;
@@ -430,7 +431,9 @@ __device__ __forceinline__ Row row_of(const Args& a, int rows, const Unit& u, co
     r.end = 1;
     if (r.id < v) r.id = kNoId;
   } else {
-    const uint16_t* at = a.starts + v / 128 * a.T + r.t;
+    // starts counts half tiles: of the forward pass's tiles, or of 256 columns
+    const uint16_t* at = (u.mode == kForward ? a.starts + (int64_t(u.n0) / a.tile_n * 2 + th.half) * a.T
+                                             : a.starts_back + v / 128 * a.T) + r.t;
     r.e = at[0];
     r.end = at[a.T];
     entry_ahead(a, u, r, r.e, r.id, r.w);
@@ -500,7 +503,7 @@ __device__ __forceinline__ void forward_epilogue(const Args& a, const Unit& u, c
                                                  uint32_t acc) {
   const int64_t v0 = u.n0;
   const int begin = th.half * 128;
-  const int cols = int(min(int64_t(256), a.V - v0));
+  const int cols = int(min(int64_t(a.tile_n), a.V - v0));
   const float c_ce = kLog2e, c_kd = KD ? a.inv_tau * kLog2e : kLog2e;
   const int p = CE && KD ? shared_power(float(a.tau)) : 0;
   float top = -INFINITY;
@@ -540,7 +543,7 @@ __device__ __forceinline__ void forward_epilogue(const Args& a, const Unit& u, c
     }
   }
   if (!r.there) return;
-  const int64_t at = (v0 / 256 * 2 + th.half) * a.Tp + r.i;
+  const int64_t at = (v0 / a.tile_n * 2 + th.half) * a.Tp + r.i;
   const bool nan = isnan(s.ce + s.kd);
   if (CE) a.stats[at] = make_float2(nan ? NAN : s.m_ce, s.ce);
   if (KD) a.stats_tau[at] = make_float2(nan ? NAN : s.m_kd, s.kd);
