@@ -16,8 +16,11 @@ using zl::set_error;
 
 constexpr int64_t kMostSize = 0x7fffffff - 1024;  // T, V and D: 32-bit tile coordinates
 // A piece of the logits' gradient is at most this many bytes (one tile's width
-// of columns at least); kBuffers of them are held.
-constexpr int64_t kPieceBytes = int64_t(54) << 20;
+// of columns at least); kBuffers of them are held. More bytes mean fewer
+// additions to dhidden's sums, fewer bytes a shorter pipeline: a step of 8192
+// rows of width 768 took 1.92 ms with 16 MB, 1.57 with 32, 1.47 with 40 and 1.46
+// with 128; one of 2048 rows 352, 354, 356 and 422 us.
+constexpr int64_t kPieceBytes = int64_t(40) << 20;
 
 int64_t round_up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
 
@@ -289,6 +292,12 @@ int plan(const zero_head_loss_t* p, bool distill, int pass, Args* a, __nv_bfloat
     if (p->dhidden) a->dh = w.take<float>(a->splits * a->Tp, a->Dp);
     most = std::max(most, w.at);
   }
+  // The matrix kernel numbers its tiles in 32 bits.
+  const double row_tiles = double(a->Tp / zl::kTileM), wide_tiles = double((a->D + 255) / 256);
+  if (row_tiles * double(a->tiles) > 1e9 ||
+      (pass & kBackward && (row_tiles + wide_tiles) * double((a->V + 255) / 256) +
+                                   double(pieces) * row_tiles * wide_tiles * double(a->splits) > 1e9))
+    return set_error(ZERO_EINVAL, "the problem has more than 1e9 tiles");
   if (!w.fits) return set_error(ZERO_EINVAL, "the problem's workspace overflows 64 bits");
   *bytes = most;
   return ZERO_OK;
@@ -396,13 +405,13 @@ int run(const zero_head_loss_t* p, bool distill, int pass, cudaStream_t s) {
   if (pass & kForward) {
     program.forward = 1;
     program.counter = a.counters;
-    next("logits", [&] { return zl::launch_products(a, program, sms, s); });
+    next("logits", [&] { return zl::launch_products(a, program, device, sms, s); });
     next("losses", [&] { return zl::launch_losses(a, s); });
   }
   if (pass & kBackward) {
     program.forward = 0;
     program.counter = a.counters + 1;
-    next("the gradients", [&] { return zl::launch_products(a, program, sms, s); });
+    next("the gradients", [&] { return zl::launch_products(a, program, device, sms, s); });
     if (p->dhidden && p->T) next("dhidden", [&] { return zl::launch_dhidden_out(a, s); });
   }
   if (e != cudaSuccess)

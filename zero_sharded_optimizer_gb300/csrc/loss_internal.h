@@ -124,6 +124,6 @@ cudaError_t launch_rows(const Args& a, bool pack_weight, bool* packed, cudaStrea
 cudaError_t launch_pack(const Args& a, __nv_bfloat16* weight, cudaStream_t s);
 cudaError_t launch_losses(const Args& a, cudaStream_t s);
 cudaError_t launch_dhidden_out(const Args& a, cudaStream_t s);
-cudaError_t launch_products(const Args& a, const Program& prog, int sms, cudaStream_t s);
+cudaError_t launch_products(const Args& a, const Program& prog, int device, int sms, cudaStream_t s);
 
 }  // namespace zl

@@ -28,6 +28,13 @@
 // fp32 storage: each operand is three bf16 parts and the products of the parts
 // are summed into one accumulator, smallest first, in six passes over K.
 //
+// What bounds it: the tensor pipes, 95 % busy in the forward pass and 82 % in
+// the backward pass of 8192 rows of width 768 and a vocabulary of 50257 (312 us,
+// 2.0 PFLOP/s, and 1.10 ms, 1.7 PFLOP/s), and over many calls the power limit,
+// which lowers the clock: 1.70 PFLOP/s forward, where cuBLAS keeps 1.74. What
+// the backward pass loses: dH's additions 4 %, waits between phases 4 %, G's
+// stores 2 %, the rest to operands that come from DRAM instead of L2.
+//
 // The tensor cores' fp32 accumulators truncate: a chain of n additions of one
 // sign loses about n 2^-24 of the sum (measured: 1.4e-5 over K = 4096, where
 // fp32 additions that round lose 5e-8). Where the sum is kept in fp32 -- the
@@ -37,6 +44,7 @@
 #include <cuda.h>
 #include <math.h>
 
+#include <atomic>
 #include <type_traits>
 
 #include "loss_device.cuh"
@@ -50,7 +58,6 @@ constexpr int kBlockK = 64;        // elements of K a stage holds: 128 bytes
 constexpr int kHalf = 128;         // rows of A, and of B, that a CTA holds
 constexpr int kOperandBytes = kHalf * kBlockK * 2;
 constexpr int kStageBytes = 2 * kOperandBytes;
-
 constexpr int kWarpBox = 32 * 64 * 2;      // 32 rows x 64 columns of G on their way out
 constexpr int kRing = 3;                   // units on their way to the warps
 constexpr int kRegsCopies = 88, kRegsEpilogue = 208;  // 128 x 88 + 256 x 208 = 384 x 168, the launch's
@@ -106,8 +113,8 @@ __device__ __forceinline__ void barrier_arrive_remote(uint32_t cluster_bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
 // Without an order for the thread's earlier memory accesses: for what it has
-// read, which needs none. (A release waits for its stores on their way out:
-// 8 % of a forward pass of width 768.)
+// read, which needs none. (A release waits for its stores on their way out: with
+// it a forward pass of width 768 took 22 % longer.)
 __device__ __forceinline__ void barrier_arrive_read(uint32_t cluster_bar) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
@@ -140,8 +147,7 @@ struct Waiter {
   Head* head;
   template <bool Cluster = false>
   __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity) const {
-    for (uint32_t n = 0; n < 1; ++n)
-      if (barrier_try<Cluster>(bar, parity)) return true;
+    if (barrier_try<Cluster>(bar, parity)) return true;
     const uint64_t begin = timer_ns();
     for (uint32_t n = 1;; ++n) {
       if (barrier_try<Cluster>(bar, parity)) return true;
@@ -155,10 +161,9 @@ struct Waiter {
 };
 
 // Counts of finished units, one arrival of each CTA (two a unit), made when its
-// stores are complete. A unit waits only for units that
-// were handed out before it and a pair works its units off in order, so the
-// first unfinished unit never waits: no wait is for ever, however few of the
-// grid's pairs run.
+// stores are complete. A unit waits only for units that were handed out before
+// it and a pair works its units off in order, so the first unfinished unit never
+// waits: no wait is for ever, however few of the grid's pairs run.
 struct Progress {
   volatile uint32_t* given_up;
   Head* head;
@@ -682,8 +687,11 @@ __device__ __forceinline__ void load_terms(const Unit& u, uint32_t addr, float (
 }
 
 // dH of a piece, fp32: stored by the first piece, added by the others (TMA
-// reductions). An element gets one addition of each piece, and a piece's come
-// after the one before is complete, so the order is fixed.
+// reductions in L2, 2.6 TB/s where all tiles leave at once). An element gets one
+// addition of each piece, and a piece's comes after the one before is complete,
+// so the order is fixed. (The earlier sum read by the threads while the products
+// ran, then a plain store: 30 % slower on the whole pass. H's tiles spread among
+// the next piece's G: no faster.)
 __device__ __forceinline__ void hidden_epilogue(const CUtensorMap* out, const Unit& u, const Thread& th, uint32_t acc,
                                                 uint32_t rank, uint8_t* box) {
   const int lane = th.row & 31, begin = th.half * 128;
@@ -838,8 +846,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   Unit u;
   // The ring's next entry. The epilogue warps give it back to the pair's first
   // CTA once the unit's first accumulator is full: by then the copies and the
-  // products have read it too. (Arrivals of theirs, across the pair, cost the
-  // forward pass of width 768 a further 13 %.)
+  // products have read it too. (Arrivals of theirs as well, across the pair, cost
+  // the forward pass of width 768 11 %.)
   int slot = 0;
   uint32_t slot_phase = 0;
   auto next_unit = [&] {
@@ -987,7 +995,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
     } else if (warp == 3 && !prog.forward) {
       // ---- counts the finished units, off the epilogues' path: a release waits
-      // for stores still on their way, and theirs were 7 % of a backward pass
+      // for stores still on their way (5 % of a backward pass of 8192 rows)
       if (elect_one()) {
         for (int n = 0; wait(stored + 8 * (n & 1), (n >> 1) & 1); ++n) {
           uint32_t *const unit = counts[2 * (n & 1)], *const tile = counts[2 * (n & 1) + 1];
@@ -1134,17 +1142,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 }
 
 template <int PLANES, bool CE, bool KD>
-cudaError_t launch(const Args& a, const Program& prog, int sms, cudaStream_t s) {
+cudaError_t launch(const Args& a, const Program& prog, int device, int sms, cudaStream_t s) {
   auto* kernel = products_kernel<PLANES, CE, KD>;
-  // The register shares of the warps must not exceed what the launch brings.
-  static const cudaError_t ready = [&] {
+  // Once per device (a race only does it twice): the kernel's shared memory, and
+  // a check that the register shares of its warps do not exceed what a launch
+  // brings.
+  static std::atomic<bool> ready[64];
+  if (device < 0 || device >= 64 || !ready[device].load(std::memory_order_acquire)) {
     cudaFuncAttributes at;
     cudaError_t e = cudaFuncGetAttributes(&at, kernel);
     if (e != cudaSuccess) return e;
     if (at.numRegs * kThreads < 128 * kRegsCopies + 256 * kRegsEpilogue) return cudaErrorLaunchOutOfResources;
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSharedBytes);
-  }();
-  if (ready != cudaSuccess) return ready;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSharedBytes);
+    if (e != cudaSuccess) return e;
+    if (device >= 0 && device < 64) ready[device].store(true, std::memory_order_release);
+  }
   cudaLaunchConfig_t c = {};
   c.gridDim = dim3(unsigned(sms / 2 * 2));
   c.blockDim = dim3(kThreads);
@@ -1160,13 +1172,13 @@ cudaError_t launch(const Args& a, const Program& prog, int sms, cudaStream_t s) 
 
 }  // namespace
 
-cudaError_t launch_products(const Args& a, const Program& prog, int sms, cudaStream_t s) {
+cudaError_t launch_products(const Args& a, const Program& prog, int device, int sms, cudaStream_t s) {
   if (a.planes == 1) {
-    if (!a.has_kd) return launch<1, true, false>(a, prog, sms, s);
-    return a.has_ce ? launch<1, true, true>(a, prog, sms, s) : launch<1, false, true>(a, prog, sms, s);
+    if (!a.has_kd) return launch<1, true, false>(a, prog, device, sms, s);
+    return a.has_ce ? launch<1, true, true>(a, prog, device, sms, s) : launch<1, false, true>(a, prog, device, sms, s);
   }
-  if (!a.has_kd) return launch<3, true, false>(a, prog, sms, s);
-  return a.has_ce ? launch<3, true, true>(a, prog, sms, s) : launch<3, false, true>(a, prog, sms, s);
+  if (!a.has_kd) return launch<3, true, false>(a, prog, device, sms, s);
+  return a.has_ce ? launch<3, true, true>(a, prog, device, sms, s) : launch<3, false, true>(a, prog, device, sms, s);
 }
 
 }  // namespace zl
