@@ -506,6 +506,7 @@ __device__ __forceinline__ int shared_power(float tau) { return tau == 1.0f ? 1 
 template <bool CE, bool KD>
 __device__ __forceinline__ void forward_epilogue(const Args& a, const Unit& u, const Thread& th, Row& r,
                                                  uint32_t acc) {
+  if (!__any_sync(~0u, r.there)) return;
   const int64_t v0 = u.n0;
   const int begin = th.half * 128;
   const int cols = int(min(int64_t(a.tile_n), a.V - v0));
@@ -587,9 +588,15 @@ __device__ __forceinline__ void stage_fp32(uint8_t* box, int lane, const float (
 // Each warp stages boxes of its 32 rows by 64 columns and stores them by TMA.
 template <int PLANES, bool CE, bool KD, int P>
 __device__ __forceinline__ void gradient_epilogue(const Args& a, const CUtensorMap* out, const Unit& u,
-                                                  const Thread& th, Row& r, uint32_t acc, uint32_t rank, uint8_t* box) {
-  const int64_t v0 = u.piece * a.piece + u.n0;
+                                                  const Thread& th, int rows, Row& r, uint32_t acc, uint32_t rank,
+                                                  uint8_t* box) {
   const int begin = th.half * 128, lane = th.row & 31;
+  if (r.i - lane >= (rows + kBlockK - 1) / kBlockK * kBlockK) {  // rows that no product's terms reach
+    if (lane == 0)
+      for (int n = 0; n < 2 * PLANES; ++n) store_commit();  // the groups are counted
+    return;
+  }
+  const int64_t v0 = u.piece * a.piece + u.n0;
   const int cols = int(min(int64_t(256), a.V - v0));
   const float c_ce = kLog2e, c_kd = a.inv_tau * kLog2e;
   // Terms that the row does not have are 2^-inf = 0, whatever the accumulator holds.
@@ -692,9 +699,11 @@ __device__ __forceinline__ void load_terms(const Unit& u, uint32_t addr, float (
 // so the order is fixed. (The earlier sum read by the threads while the products
 // ran, then a plain store: 30 % slower on the whole pass. H's tiles spread among
 // the next piece's G: no faster.)
-__device__ __forceinline__ void hidden_epilogue(const CUtensorMap* out, const Unit& u, const Thread& th, uint32_t acc,
-                                                uint32_t rank, uint8_t* box) {
+__device__ __forceinline__ void hidden_epilogue(const CUtensorMap* out, const Unit& u, const Thread& th, int rows,
+                                                uint32_t acc, uint32_t rank, uint8_t* box) {
   const int lane = th.row & 31, begin = th.half * 128;
+  const int row = u.m0 + int(rank) * kHalf + th.row;
+  if (row - lane >= rows) return;
 #pragma unroll 1
   for (int k = 0; k < 4; ++k) {
     const int c = begin + 32 * k;
@@ -706,7 +715,6 @@ __device__ __forceinline__ void hidden_epilogue(const CUtensorMap* out, const Un
     proxy_fence();
     __syncwarp();
     if (lane == 0) {
-      const int row = u.m0 + int(rank) * kHalf + th.row;
       if (u.piece == 0) tma_store(out, smem_u32(box), u.n0 + c, row, u.split);
       else tma_add(out, smem_u32(box), u.n0 + c, row, u.split);
       store_commit();
@@ -1108,21 +1116,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       } else if (u.mode == kGradient) {
         const CUtensorMap* out = &prog.g_out[u.piece % kBuffers];
         const int p = CE && KD ? shared_power(float(a.tau)) : 0;
-        if (CE && KD && p == 1) gradient_epilogue<PLANES, CE, KD, 1>(a, out, u, th, r, acc, rank, box);
-        else if (CE && KD && p == 2) gradient_epilogue<PLANES, CE, KD, 2>(a, out, u, th, r, acc, rank, box);
-        else if (CE && KD && p == 4) gradient_epilogue<PLANES, CE, KD, 4>(a, out, u, th, r, acc, rank, box);
-        else gradient_epilogue<PLANES, CE, KD, 0>(a, out, u, th, r, acc, rank, box);
+        if (CE && KD && p == 1) gradient_epilogue<PLANES, CE, KD, 1>(a, out, u, th, rows, r, acc, rank, box);
+        else if (CE && KD && p == 2) gradient_epilogue<PLANES, CE, KD, 2>(a, out, u, th, rows, r, acc, rank, box);
+        else if (CE && KD && p == 4) gradient_epilogue<PLANES, CE, KD, 4>(a, out, u, th, rows, r, acc, rank, box);
+        else gradient_epilogue<PLANES, CE, KD, 0>(a, out, u, th, rows, r, acc, rank, box);
         if (lane == 0 && finished) {  // the unit before: its stores are the older ones
           asm volatile("cp.async.bulk.wait_group %0;" ::"n"(2 * PLANES) : "memory");
           report(finished, finished_tile);
         }
         finished = a.formed + u.piece;
         finished_tile = nullptr;
-      } else {
-        if (u.mode == kHidden) hidden_epilogue(&prog.dh, u, th, acc, rank, box);
-        else weight_epilogue<PLANES>(a, prog, u, th, factor, acc, rank, box);
+      } else if (u.mode == kHidden) {
+        hidden_epilogue(&prog.dh, u, th, rows, acc, rank, box);
         finished = a.used + u.piece;
         finished_tile = tile;
+      } else {
+        // G has been read, and nothing in the launch waits for dW itself.
+        if (lane == 0) report(a.used + u.piece, nullptr);
+        weight_epilogue<PLANES>(a, prog, u, th, factor, acc, rank, box);
       }
       give_back();
     }
