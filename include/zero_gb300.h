@@ -15,7 +15,9 @@
  * as the optimizer (zero_step_sgd), ZeRO stage 3 (owner-only steps and
  * zero_gather), 25 MiB bucket streaming, host-memory gradients
  * (zero_step_from_host, zero_step_from_host_ex), the DDP mean (also from host
- * memory: ddp_allreduce_mean_from_host) and per-stage memory accounting.
+ * memory: ddp_allreduce_mean_from_host) and per-stage memory accounting; and,
+ * where a language model's gradients begin, the losses at the vocabulary
+ * (zero_xent_*, zero_distill_*).
  *
  * Conventions for every call:
  *  - Return value: ZERO_OK (0) or a negative ZERO_E* code. zero_strerror()
@@ -504,7 +506,8 @@ int ddp_allreduce_mean_from_host_h(zero_ddp_host_t *h, const void *const *host_g
  * products keep fp32's precision); softmax statistics, losses and the sums of
  * both gradients are fp32 or wider; in ZERO_BF16_MIXED the gradient of the
  * logits is rounded to bf16 once, as the operand of the two gradient products.
- * No atomics add values: equal inputs give equal bits. */
+ * Every sum has a fixed order: equal inputs give equal bits, and a step the
+ * bits of a forward and a backward call. */
 
 /* Reduction of the rows' losses, and what dloss is a gradient of. */
 enum {

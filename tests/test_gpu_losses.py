@@ -83,7 +83,7 @@ def test_xent_step(losses, cuda, kind, T, V, D):
 @pytest.mark.parametrize("kind", TYPES)
 def test_strides_and_alignment(losses, cuda, kind, pad, offset):
     dt = TYPES[kind]
-    for T, V, D in [(70, 515, 72), (33, 300, 67)]:
+    for T, V, D in [(70, 515, 72), (33, 300, 67), (40, 300, 201)]:
         h, w, y, g = inputs(T, V, D, dt, 7 + pad + offset, cuda, masked=0.3)
         h = matrix(h, cuda, pad, offset, "hidden")
         w = matrix(w, cuda, pad, offset, "weight")
