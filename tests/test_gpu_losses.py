@@ -345,6 +345,50 @@ def test_several_pieces_of_the_vocabulary(losses, cuda, kind, T, V, D):
     check(got, r, dt)
 
 
+def test_many_rows_few_of_them_labelled(losses, cuda):
+    """More rows than the numbering takes at a time, most without a label."""
+    T, V, D = 40_003, 300, 24
+    h, w, y, g = inputs(T, V, D, torch.bfloat16, 61, cuda, masked=0.97)
+    y[:17_000] = IGNORE
+    r = reference(h, w, y)
+    check(losses.xent_step(h, w, y), r, torch.bfloat16)
+    ids, logits = torch.randint(-1, V, (T, 3), generator=g).to(cuda), torch.randn(T, 3, generator=g).to(cuda)
+    ids[:, 0] = torch.where(y == IGNORE, -1, ids[:, 0])
+    ids[:, 1:] = torch.where((y == IGNORE).unsqueeze(1), -1, ids[:, 1:])
+    r = reference(h, w, None, ids, logits, reduction="sum")
+    check(losses.distill_step(h, w, ids, logits, reduction="sum"), r, torch.bfloat16)
+
+
+def test_equal_inputs_give_equal_bits(losses, cuda):
+    """Several pieces and split sums, four times over, on two streams at once."""
+    T, V, D = 5000, 20_000, 96
+    h, w, y, _ = inputs(T, V, D, torch.bfloat16, 62, cuda, masked=0.1)
+    first = losses.xent_step(h, w, y)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    again = [losses.xent_step(h, w, y, stream=streams[i % 2]) for i in range(4)]
+    torch.cuda.synchronize()
+    for r in again:
+        for name in ("loss", "reduced", "lse", "dhidden", "dweight"):
+            assert torch.equal(getattr(r, name), getattr(first, name)), name
+
+
+def test_in_a_graph(losses, cuda):
+    """Captured once and replayed on new values of the same tensors."""
+    T, V, D = 90, 700, 64
+    h, w, y, g = inputs(T, V, D, torch.bfloat16, 63, cuda)
+    losses.xent_step(h, w, y)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = losses.xent_step(h, w, y)
+    h2, w2, y2, _ = inputs(T, V, D, torch.bfloat16, 64, cuda, masked=0.3)
+    h.copy_(h2), w.copy_(w2), y.copy_(y2)
+    graph.replay()
+    torch.cuda.synchronize()
+    check(got, reference(h2, w2, y2), torch.bfloat16)
+
+
 def test_offsets_beyond_32_bits(losses, cuda):
     """A weight whose last rows lie more than 2^32 bytes from its first."""
     V, D, stride = 600, 64, 4_000_000

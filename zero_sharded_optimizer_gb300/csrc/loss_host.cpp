@@ -211,19 +211,7 @@ int plan(const zero_head_loss_t* p, bool distill, int pass, Args* a, __nv_bfloat
   a->dhidden_stride = p->dhidden_stride;
   a->dweight = p->dweight;
   a->dweight_stride = p->dweight_stride;
-  // With few tiles, narrower ones where they fill the last round of 76 CTA
-  // pairs better: the rounds times the width decide (one token of a vocabulary
-  // of 50257: three rounds of 224 columns instead of three of 256).
-  a->tile_n = zl::kTileN;
-  int64_t least = INT64_MAX;
-  for (int32_t n = zl::kTileN; n >= 160; n -= 32) {
-    const int64_t units = a->Tp / zl::kTileM * ((p->V + n - 1) / n), rounds = (units + 75) / 76;
-    if (rounds * n < least && (n == zl::kTileN || rounds <= 8)) {
-      least = rounds * n;
-      a->tile_n = n;
-    }
-  }
-  a->tiles = (p->V + a->tile_n - 1) / a->tile_n;
+  a->tiles = (p->V + zl::kTileN - 1) / zl::kTileN;
 
   Layout w{static_cast<uint8_t*>(p->workspace)};
   a->head = w.take<zl::Head>(1);
@@ -233,12 +221,7 @@ int plan(const zero_head_loss_t* p, bool distill, int pass, Args* a, __nv_bfloat
   a->konst = w.take<float>(a->T);
   a->ids = w.take<int32_t>(a->T, a->L);
   a->weights = w.take<float>(a->T, a->L);
-  if (a->K) {
-    const int64_t back = (p->V + zl::kTileN - 1) / zl::kTileN;
-    if (pass & kForward) a->starts = w.take<uint16_t>(2 * a->tiles + 1, a->T);
-    if (pass & kBackward)
-      a->starts_back = a->starts && a->tile_n == zl::kTileN ? a->starts : w.take<uint16_t>(2 * back + 1, a->T);
-  }
+  if (a->K) a->starts = w.take<uint16_t>(2 * a->tiles + 1, a->T);
   a->hp = w.take<__nv_bfloat16>(a->Tp * a->planes, a->Dp);
   if (weight_in_place(p)) {
     *packed_weight = nullptr;
@@ -262,7 +245,9 @@ int plan(const zero_head_loss_t* p, bool distill, int pass, Args* a, __nv_bfloat
   if (pass & kBackward) {
     // dhidden's sums over a piece are split where one of its tiles would be
     // more than half of what each of 76 CTA pairs has to do for the piece, while
-    // two blocks of K are left to a part.
+    // two blocks of K are left to a part (37 rows x 1009 x 96 in fp32: a step of
+    // 68 us, 87 unsplit; 333 x 10007 x 512: 197 and 419; twice the parts on 1638
+    // rows x 32000 x 2048: 543 instead of 534).
     const int64_t blocks_t = (a->T + 63) / 64, blocks_v = a->piece / 64, blocks_d = a->Dp / 64;
     const int64_t wide = (a->D + zl::kTileN - 1) / zl::kTileN;
     const int64_t rows = a->Tp / zl::kTileM, cols = a->piece / zl::kTileN;
@@ -338,17 +323,14 @@ bool tensor_map(CUtensorMap* map, const void* base, int64_t cols, int64_t rows, 
 bool make_program(const Args& a, bool backward, Program* p) {
   const bool f32 = a.planes == 3;
   const int64_t wide = a.wp_plane ? a.Dp : a.D;
-  // With few rows the rest of a tile's rows is not fetched: what the products
-  // make of whatever lies there is not read.
-  p->box_rows = int32_t(std::min<int64_t>(round_up(std::max<int64_t>(a.T, 1), 8), 128));
-  bool ok = tensor_map(&p->hidden, a.hp, a.Dp, a.Tp, a.Dp, a.planes, a.Tp * a.Dp, p->box_rows) &&
+  bool ok = tensor_map(&p->hidden, a.hp, a.Dp, a.Tp, a.Dp, a.planes, a.Tp * a.Dp, 128) &&
             tensor_map(&p->weight, a.wp, wide, a.V, a.wp_ld, a.planes, a.wp_plane, 128);
   if (!backward) return ok;
   ok = ok && tensor_map(&p->hidden_mn, a.hp, a.Dp, a.Tp, a.Dp, a.planes, a.Tp * a.Dp, 64) &&
        tensor_map(&p->weight_mn, a.wp, wide, a.V, a.wp_ld, a.planes, a.wp_plane, 64);
   for (int b = 0; b < zl::kBuffers; ++b) {
     CUtensorMap* const to[3] = {&p->g[b], &p->g_mn[b], &p->g_out[b]};
-    const uint32_t box[3] = {uint32_t(p->box_rows), 64, 32};
+    const uint32_t box[3] = {128, 64, 32};
     for (int i = 0; i < 3; ++i)
       ok = ok && tensor_map(to[i], a.g[b], a.piece, a.Tp, a.piece, a.planes, a.Tp * a.piece, box[i]);
   }

@@ -77,17 +77,13 @@ struct Args {
   float* konst;           // [T] the loss's part that no logit enters
   int32_t* ids;           // [T][L] ascending, kNoId after the last
   float* weights;         // [T][L] weight of each entry's logit in loss and gradient
-  // Distillation: [2 tiles + 1][T] first entry of each half tile, of the forward
-  // pass's tiles and of the backward pass's.
-  uint16_t* starts;
-  uint16_t* starts_back;
+  uint16_t* starts;       // distillation: [2 tiles + 1][T] first entry of each half tile
   double* sums;           // [kLossBlocks] parts of the reduced loss
   float* zent;            // [T][L] logits of the entries
   __nv_bfloat16* hp;      // [planes][Tp][Dp] packed hidden states
   const __nv_bfloat16* wp;  // [planes][V][Dp], or the caller's weight (then wp_ld)
   int64_t wp_ld, wp_plane;
-  int32_t tile_n;         // columns of a tile of the forward pass: up to kTileN
-  int64_t tiles;          // its tiles of the vocabulary
+  int64_t tiles;          // vocabulary tiles
   float2* stats;          // [2 tiles][Tp] half a tile's (m, sum of 2^(z log2(e) - m))
   float2* stats_tau;      // [2 tiles][Tp] of z / tau
   int32_t* counters;      // [2] units handed out, forward and backward
@@ -105,13 +101,12 @@ struct Args {
 enum Mode : int32_t { kForward, kGradient, kHidden, kWeight };
 
 struct Program {
-  // Operands read along K (boxes of 128 rows, box_rows of them for the rows with
-  // a target) and across it (_mn, boxes of 64 rows of K); G, the sums of dhidden and dweight as a warp writes them.
+  // Operands read along K (boxes of 128 rows) and across it (_mn, boxes of 64
+  // rows of K); G, the sums of dhidden and dweight as a warp writes them.
   CUtensorMap hidden, hidden_mn, weight, weight_mn;
   CUtensorMap g[kBuffers], g_mn[kBuffers], g_out[kBuffers];
   CUtensorMap dh, dweight;
   int32_t forward;     // the forward pass (else the backward pass)
-  int32_t box_rows;    // rows of the boxes of `hidden` and `g`: 128, or fewer for few rows
   int32_t pieces;
   int32_t weight_tma;  // dweight can be written by TMA
   int32_t* counter;    // units handed out
