@@ -553,18 +553,18 @@ __device__ __forceinline__ void forward_epilogue(const Args& a, const Unit& u, c
   if (KD) a.stats_tau[at] = make_float2(nan ? NAN : s.m_kd, s.kd);
 }
 
-// Two neighbouring values of G as a word of the operand's part p.
-template <int PLANES>
-__device__ __forceinline__ uint32_t pack_part(float x0, float x1, int p) {
-  if (PLANES == 1) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(x0, x1);
-    return *reinterpret_cast<const uint32_t*>(&h);
-  }
-  __nv_bfloat16 p0[3], p1[3];
-  split(x0, p0);
-  split(x1, p1);
-  const __nv_bfloat16 h0 = p == 0 ? p0[0] : p == 1 ? p0[1] : p0[2], h1 = p == 0 ? p1[0] : p == 1 ? p1[1] : p1[2];
-  return uint32_t(__bfloat16_as_ushort(h0)) | uint32_t(__bfloat16_as_ushort(h1)) << 16;
+// Two values as a word of bf16, rounded to nearest.
+__device__ __forceinline__ uint32_t pack_bf16(float x0, float x1) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(x0, x1);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+// The same, with what the rounding left over in place of the values: called
+// three times it gives the three parts of fp32 values.
+__device__ __forceinline__ uint32_t next_part(float& x0, float& x1) {
+  const uint32_t w = pack_bf16(x0, x1);
+  x0 -= __uint_as_float(w << 16);
+  x1 -= __uint_as_float(w & 0xffff0000u);
+  return w;
 }
 
 // The warp's staging box may be written again: its last store has read it.
@@ -637,14 +637,18 @@ __device__ __forceinline__ void gradient_epilogue(const Args& a, const CUtensorM
         if (j == at) g[j] -= d;
     });
   };
-  // Their part p into half a box.
-  auto stage = [&](int half, int p, const float (&g)[32]) {
+  // They, or their next part, into half a box.
+  auto stage = [&](int half, float (&g)[32]) {
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      const float* x = &g[8 * q];
+      uint32_t w[4];
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        float &x0 = g[8 * q + 2 * n], &x1 = g[8 * q + 2 * n + 1];
+        w[n] = PLANES == 1 ? pack_bf16(x0, x1) : next_part(x0, x1);
+      }
       *reinterpret_cast<uint4*>(box + lane * 128 + (((4 * half + q) ^ (lane & 7)) * 16)) =
-          make_uint4(pack_part<PLANES>(x[0], x[1], p), pack_part<PLANES>(x[2], x[3], p),
-                     pack_part<PLANES>(x[4], x[5], p), pack_part<PLANES>(x[6], x[7], p));
+          make_uint4(w[0], w[1], w[2], w[3]);
     }
   };
   auto store = [&](int b, int p) {
@@ -663,7 +667,7 @@ __device__ __forceinline__ void gradient_epilogue(const Args& a, const CUtensorM
       for (int k = 0; k < 2; ++k) {
         float g[32];
         columns(begin + 64 * b + 32 * k, g);
-        stage(k, 0, g);
+        stage(k, g);
       }
       store(b, 0);
     } else {
@@ -673,8 +677,8 @@ __device__ __forceinline__ void gradient_epilogue(const Args& a, const CUtensorM
 #pragma unroll
       for (int p = 0; p < PLANES; ++p) {
         box_free(lane);
-        stage(0, p, g[0]);
-        stage(1, p, g[1]);
+        stage(0, g[0]);
+        stage(1, g[1]);
         store(b, p);
       }
     }
@@ -749,7 +753,7 @@ __device__ __forceinline__ void weight_epilogue(const Args& a, const Program& pr
           for (int j = 0; j < 4; ++j) {
             uint32_t word[4];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) word[q] = pack_part<1>(x[8 * j + 2 * q], x[8 * j + 2 * q + 1], 0);
+            for (int q = 0; q < 4; ++q) word[q] = pack_bf16(x[8 * j + 2 * q], x[8 * j + 2 * q + 1]);
             *reinterpret_cast<uint4*>(box + lane * 128 + (((4 * h + j) ^ (lane & 7)) * 16)) =
                 make_uint4(word[0], word[1], word[2], word[3]);
           }
