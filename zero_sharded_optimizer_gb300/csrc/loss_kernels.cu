@@ -345,25 +345,44 @@ __global__ void __launch_bounds__(256) pack_kernel(const Args a, __nv_bfloat16* 
   pack_rows<F32>(a, a.head->rows, hidden_vector, first, step);
 }
 
-// The rows' sums over all pieces, with the common factor, four elements a thread.
-template <bool F32, bool Vector>
+// The rows' sums over all pieces, with the common factor: a block takes
+// 256 / Lanes groups of four elements of a row at a time, each group's `Lanes`
+// threads share the parts that the sums are split in.
+template <bool F32, bool Vector, int Lanes>
 __global__ void __launch_bounds__(256) dhidden_out_kernel(const Args a) {
+  constexpr int kGroups = 256 / Lanes;
+  __shared__ float4 part[Lanes][kGroups];
   let_next_start();
   wait_for_previous();
   const float f = a.head->fault ? NAN : a.head->factor;
-  const int32_t wide = int32_t((a.D + 3) / 4);
-  for (int64_t n = int64_t(blockIdx.x) * 256 + threadIdx.x; n < a.T * wide; n += int64_t(gridDim.x) * 256) {
-    const int64_t t = n / wide, d = n % wide * 4;
+  const int group = threadIdx.x % kGroups, lane = threadIdx.x / kGroups;
+  const int64_t wide = (a.D + 3) / 4;
+  const int64_t stretches = (wide + kGroups - 1) / kGroups;  // of a row
+  for (int64_t b = blockIdx.x; b < a.T * stretches; b += gridDim.x) {
+    const int64_t t = b / stretches, d = (b % stretches * kGroups + group) * 4;
     const int32_t i = a.rowpos[t];
     float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (i >= 0) {
+    if (i >= 0 && d < a.D) {
 #pragma unroll 8
-      for (int p = 0; p < a.splits; ++p) {
+      for (int p = lane; p < a.splits; p += Lanes) {
         const float4 y = *reinterpret_cast<const float4*>(a.dh + (p * a.Tp + i) * a.Dp + d);
         x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
       }
-      x = make_float4(f * x.x, f * x.y, f * x.z, f * x.w);
     }
+    if (Lanes > 1) {
+      part[lane][group] = x;
+      __syncthreads();
+      if (lane == 0) {
+#pragma unroll
+        for (int p = 1; p < Lanes; ++p) {
+          const float4 y = part[p][group];
+          x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+        }
+      }
+      __syncthreads();
+    }
+    if (lane > 0 || d >= a.D) continue;
+    if (i >= 0) x = make_float4(f * x.x, f * x.y, f * x.z, f * x.w);
     const int64_t at = t * a.dhidden_stride + d;
     const float v[4] = {x.x, x.y, x.z, x.w};
     if (F32) {
@@ -580,10 +599,19 @@ cudaError_t launch_losses(const Args& a, cudaStream_t s) {
 
 cudaError_t launch_dhidden_out(const Args& a, cudaStream_t s) {
   const bool vector = aligned16(a.dhidden, a.dhidden_stride * (a.planes == 3 ? 4 : 2));
-  const unsigned blocks = blocks_for(a.T * ((a.D + 3) / 4));
-  auto* kernel = a.planes == 3 ? (vector ? dhidden_out_kernel<true, true> : dhidden_out_kernel<true, false>)
-                               : (vector ? dhidden_out_kernel<false, true> : dhidden_out_kernel<false, false>);
-  return launch(kernel, blocks, 256, 0, s, true, a);
+  // Eight lanes where the sums come in that many parts (one row of width 768 in
+  // 64 parts: 6 us instead of 18).
+  const bool lanes = a.splits >= 8;
+  const int64_t groups = lanes ? 32 : 256;
+  const int64_t stretches = a.T * (((a.D + 3) / 4 + groups - 1) / groups);
+  const unsigned blocks = unsigned(stretches < 152 * 32 ? stretches : 152 * 32);
+  const auto run = [&](auto* kernel) { return launch(kernel, blocks, 256, 0, s, true, a); };
+  if (a.planes == 3) {
+    if (vector) return lanes ? run(dhidden_out_kernel<true, true, 8>) : run(dhidden_out_kernel<true, true, 1>);
+    return lanes ? run(dhidden_out_kernel<true, false, 8>) : run(dhidden_out_kernel<true, false, 1>);
+  }
+  if (vector) return lanes ? run(dhidden_out_kernel<false, true, 8>) : run(dhidden_out_kernel<false, true, 1>);
+  return lanes ? run(dhidden_out_kernel<false, false, 8>) : run(dhidden_out_kernel<false, false, 1>);
 }
 
 }  // namespace zl
