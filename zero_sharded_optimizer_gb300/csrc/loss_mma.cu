@@ -68,10 +68,15 @@ constexpr int kRegsCopies = 88, kRegsEpilogue = 208;  // 128 x 88 + 256 x 208 = 
 constexpr int kStages = 6;
 constexpr int kSharedBytes = kStages * kStageBytes + 8 * kWarpBox + 1024 + 512;
 
-// 64-element blocks of K in a segment.
+// 64-element blocks of K in a segment. Finer ones cost time where the tensor
+// pipes are busy (16384 rows of width 768: 644 us, 685 with two segments of six
+// blocks, 821 with three of four); up to a tile of rows, where the weight's way
+// from memory is waited for anyway, they cost little (one token: 40 us, 42 with
+// segments of four blocks) and a loss, being the difference of a sum and one
+// logit, gains most (one token: 7e-7 of it, 1.8e-7 with four blocks).
 template <int PLANES>
-__host__ __device__ constexpr int segment_of(int mode) {
-  return PLANES == 3 ? 8 : mode == kForward ? 16 : 1 << 24;
+__device__ __forceinline__ int segment_of(const Args& a, int mode) {
+  return PLANES == 3 ? 8 : mode == kForward ? (a.Tp <= kTileM ? 4 : 16) : 1 << 24;
 }
 
 // ------------------------------------------------------------------- PTX --
@@ -306,8 +311,8 @@ struct Unit {
 __device__ __forceinline__ int blocks_of(const Unit& u) { return u.blocks < 0 ? 1 : u.blocks; }
 
 template <int PLANES>
-__device__ __forceinline__ int segments_of(const Unit& u) {
-  const int segment = segment_of<PLANES>(u.mode);
+__device__ __forceinline__ int segments_of(const Args& a, const Unit& u) {
+  const int segment = segment_of<PLANES>(a, u.mode);
   return (blocks_of(u) + segment - 1) / segment;
 }
 
@@ -501,49 +506,64 @@ __device__ __forceinline__ void add_exponentials(const float (&z)[32], float top
 // The power of tau that add_exponentials and the gradient use, 0 for none.
 __device__ __forceinline__ int shared_power(float tau) { return tau == 1.0f ? 1 : tau == 2.0f ? 2 : tau == 4.0f ? 4 : 0; }
 
+// 32 columns of a row into its statistics, and the logits of the entries among them.
 template <bool CE, bool KD>
-__device__ __forceinline__ void forward_epilogue(const Args& a, const Unit& u, const Thread& th, Row& r,
-                                                 uint32_t acc) {
+__device__ __forceinline__ void forward_columns(const Args& a, const Unit& u, Row& r, int64_t v, int valid, int p,
+                                                float (&z)[32], float& top, Sums& s) {
+  const float c_ce = kLog2e, c_kd = KD ? a.inv_tau * kLog2e : kLog2e;
+  if (valid < 32) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      if (j >= valid) z[j] = -INFINITY;
+  }
+  each_entry(a, u, r, v, [&](int at) {
+    float x = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      if (j == at) x = z[j];
+    if (at >= 0) a.zent[r.t * a.L + r.e] = x;
+  });
+  float t0 = top, t1 = -INFINITY;
+#pragma unroll
+  for (int j = 0; j < 32; j += 2) {
+    t0 = fmaxf(t0, z[j]);
+    t1 = fmaxf(t1, z[j + 1]);
+  }
+  top = fmaxf(t0, t1);
+  if (CE && KD) {
+    if (p == 1) add_exponentials<CE, KD, 1>(z, top, c_ce, c_kd, s);
+    else if (p == 2) add_exponentials<CE, KD, 2>(z, top, c_ce, c_kd, s);
+    else if (p == 4) add_exponentials<CE, KD, 4>(z, top, c_ce, c_kd, s);
+    else add_exponentials<CE, KD, 0>(z, top, c_ce, c_kd, s);
+  } else {
+    add_exponentials<CE, KD, 0>(z, top, c_ce, c_kd, s);
+  }
+}
+
+// `Held`: the logits are in registers already (the segments' sum), else they
+// are in the accumulator.
+template <bool CE, bool KD, bool Held>
+__device__ __forceinline__ void forward_epilogue(const Args& a, const Unit& u, const Thread& th, Row& r, uint32_t acc,
+                                                 float (&held)[4][32]) {
   if (!__any_sync(~0u, r.there)) return;
   const int64_t v0 = u.n0;
   const int begin = th.half * 128;
   const int cols = int(min(int64_t(256), a.V - v0));
-  const float c_ce = kLog2e, c_kd = KD ? a.inv_tau * kLog2e : kLog2e;
   const int p = CE && KD ? shared_power(float(a.tau)) : 0;
   float top = -INFINITY;
   Sums s = {-INFINITY, 0.0f, -INFINITY, 0.0f};
+  if (Held) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int c = begin + 32 * k;
+      if (c < cols) forward_columns<CE, KD>(a, u, r, v0 + c, cols - c, p, held[k], top, s);
+    }
+  } else {
 #pragma unroll 1
-  for (int k = 0; k < 4; ++k) {
-    const int valid = cols - begin - 32 * k;
-    if (valid <= 0) break;
-    float z[32];
-    tmem_load32(acc + begin + 32 * k, z);
-    if (valid < 32) {
-#pragma unroll
-      for (int j = 0; j < 32; ++j)
-        if (j >= valid) z[j] = -INFINITY;
-    }
-    each_entry(a, u, r, v0 + begin + 32 * k, [&](int at) {
-      float x = 0.0f;
-#pragma unroll
-      for (int j = 0; j < 32; ++j)
-        if (j == at) x = z[j];
-      if (at >= 0) a.zent[r.t * a.L + r.e] = x;
-    });
-    float t0 = top, t1 = -INFINITY;
-#pragma unroll
-    for (int j = 0; j < 32; j += 2) {
-      t0 = fmaxf(t0, z[j]);
-      t1 = fmaxf(t1, z[j + 1]);
-    }
-    top = fmaxf(t0, t1);
-    if (CE && KD) {
-      if (p == 1) add_exponentials<CE, KD, 1>(z, top, c_ce, c_kd, s);
-      else if (p == 2) add_exponentials<CE, KD, 2>(z, top, c_ce, c_kd, s);
-      else if (p == 4) add_exponentials<CE, KD, 4>(z, top, c_ce, c_kd, s);
-      else add_exponentials<CE, KD, 0>(z, top, c_ce, c_kd, s);
-    } else {
-      add_exponentials<CE, KD, 0>(z, top, c_ce, c_kd, s);
+    for (int c = begin; c < min(cols, begin + 128); c += 32) {
+      float z[32];
+      tmem_load32(acc + c, z);
+      forward_columns<CE, KD>(a, u, r, v0 + c, cols - c, p, z, top, s);
     }
   }
   if (!r.there) return;
@@ -898,8 +918,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const int b_k0 = u.mode == kHidden ? c0 : 0;
           const int b_boxes = b_mn ? (u.n / 2 + 63) / 64 : 0;
           const uint32_t bytes = 2 * (kOperandBytes + (b_mn ? b_boxes * 64 * kBlockK * 2 : kOperandBytes));
-          const int segments = segments_of<PLANES>(u);
-          const int segment = segment_of<PLANES>(u.mode);
+          const int segments = segments_of<PLANES>(a, u);
+          const int segment = segment_of<PLANES>(a, u.mode);
           for (int s = 0; ok && s < segments; ++s) {
             const int k_begin = s * segment, k_end = min(blocks_of(u), k_begin + segment);
             for (int term = 0; ok && term < kTerms; ++term) {
@@ -945,12 +965,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         bool ok = true;
         while (ok && next_unit() && u.mode >= 0) {
           const bool a_mn = u.mode == kWeight, b_mn = u.mode == kWeight || u.mode == kHidden;
-          const int segments = segments_of<PLANES>(u);
+          const int segments = segments_of<PLANES>(a, u);
           // fp32 accumulator, bf16 operands, majors, N, M = 256
           const uint32_t idesc = 1u << 4 | 1u << 7 | 1u << 10 | uint32_t(a_mn) << 15 | uint32_t(b_mn) << 16 |
                                  uint32_t(u.n / 8) << 17 | uint32_t(256 / 16) << 24;
           const uint64_t a_step = (a_mn ? 16 * 128 : 32) >> 4, b_step = (b_mn ? 16 * 128 : 32) >> 4;
-          const int segment = segment_of<PLANES>(u.mode);
+          const int segment = segment_of<PLANES>(a, u.mode);
           for (int s = 0; ok && s < segments; ++s) {
             const uint32_t d = tmem + buffer * 256;
             if (!(ok = wait(acc_empty + 8 * buffer, acc_phase ^ 1))) break;
@@ -1070,7 +1090,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (u.mode != kGradient) count_finished();
       Row r{};
       bool ok = true;
-      const int segments = segments_of<PLANES>(u);
+      const int segments = segments_of<PLANES>(a, u);
       if (u.mode == kForward || u.mode == kGradient) r = row_of<CE, KD>(a, rows, u, th, rank);
       if (segments == 1) {
         ok = __all_sync(~0u, full_accumulator());
@@ -1089,11 +1109,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int j = 0; j < 16; ++j) sum[k / 2][k % 2 * 16 + j] += x[j];
           }
-          if (s == segments - 1) {
+          if (s < segments - 1 || u.mode == kForward) {
+            give_back();
+          } else {
 #pragma unroll
             for (int k = 0; k < 4; ++k) tmem_store32(acc + 32 * k, sum[k]);
           }
-          if (s < segments - 1) give_back();
+        }
+        if (ok && u.mode == kForward) {  // both accumulators are the next unit's already
+          forward_epilogue<CE, KD, true>(a, u, th, r, 0, sum);
+          continue;
         }
       }
       if (!ok) break;
@@ -1113,7 +1138,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (!__all_sync(~0u, ok)) break;
       const uint32_t acc = lanes + buffer * 256;
       if (u.mode == kForward) {
-        forward_epilogue<CE, KD>(a, u, th, r, acc);
+        float none[4][32];
+        forward_epilogue<CE, KD, false>(a, u, th, r, acc, none);
       } else if (u.mode == kGradient) {
         const CUtensorMap* out = &prog.g_out[u.piece % kBuffers];
         const int p = CE && KD ? shared_power(float(a.tau)) : 0;
