@@ -9,8 +9,9 @@ arithmetic allows:
   drops products below 2^-24 of the value: one more 2^-22 of the same sum);
 - a softmax value is off by a factor exp(2 |dz|) and a few fp32 roundings of
   its argument and value: 2 |dz| + 2^-20 (1 + |z - lse| 2^-2) of itself;
-- the gradient of a logit is rounded once to bf16 (2^-8 of itself; the fp32
-  mode keeps 2^-21), and the sums of products with it are in fp32;
+- the gradient of a logit is rounded once to bf16 (2^-8 of itself; up to 256
+  rows a second bf16 value keeps what that left over, 2^-16; the fp32 mode
+  keeps 2^-21), and the sums of products with it are in fp32;
 - the result is rounded to its type.
 """
 
@@ -85,15 +86,16 @@ def reference(hidden, weight, labels=None, ids=None, logits=None, tau=1.0, alpha
     return out
 
 
-def bounds(r, dtype):
-    """Elementwise error allowed of loss, dhidden and dweight."""
+def bounds(r, dtype, parts=1):
+    """Elementwise error allowed of loss, dhidden and dweight; `parts`: bf16 values that the
+    gradient of a logit is kept in, each rounding to nearest what the one before left over."""
     T, V = r["g"].shape
     D = r["w"].shape[1]
     f32 = dtype == torch.float32
     unit = 2.0 ** -24 if f32 else 2.0 ** -8
     dz = (2 * D * 2.0 ** -24 + (2.0 ** -22 if f32 else 0.0)) * r["absz"]
     loss = 4 * dz + 2.0 ** -20 * (1 + r["absz"]) + 2.0 ** -22 * r["loss"].abs()
-    g = r["g"].abs() * (2.0 ** -21 if f32 else 2.0 ** -8) + \
+    g = r["g"].abs() * (2.0 ** -21 if f32 else 2.0 ** (-8 * parts)) + \
         r["size"] * (2 * dz + 2.0 ** -20 * (1 + r["absz"] / 4)).unsqueeze(1)
     dh = g @ r["w"].abs() + 2 * V * 2.0 ** -24 * (r["g"].abs() @ r["w"].abs())
     dw = g.T @ r["h"].abs() + 2 * T * 2.0 ** -24 * (r["g"].abs().T @ r["h"].abs())
@@ -103,9 +105,9 @@ def bounds(r, dtype):
             "dweight": dw * 1.01 + unit * 1.01 * r["dweight"].abs() + tiny}
 
 
-def check(got, r, dtype, what=""):
+def check(got, r, dtype, what="", parts=1):
     """``got``: a losses.Losses; fields that are None are not checked."""
-    b = bounds(r, dtype)
+    b = bounds(r, dtype, parts)
     for name in ("loss", "dhidden", "dweight"):
         x = getattr(got, name)
         if x is None:

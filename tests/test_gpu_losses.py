@@ -345,6 +345,25 @@ def test_several_pieces_of_the_vocabulary(losses, cuda, kind, T, V, D):
     check(got, r, dt)
 
 
+@pytest.mark.parametrize("T,V,D", [(1, 31, 64), (1, 50257, 96), (3, 1009, 65), (16, 2000, 448),
+                                   (64, 41217, 200), (200, 300, 771), (256, 777, 128)])
+@pytest.mark.parametrize("op", ["xent", "distill", "both"])
+def test_few_rows_lose_nothing_to_the_logits_gradient(losses, cuda, op, T, V, D):
+    """Up to 256 rows of bf16 the gradients' error is the rounding of the results: the
+    logits' gradient is kept in two bf16 parts."""
+    h, w, y, g = inputs(T, V, D, torch.bfloat16, 41 * T + D, cuda, masked=0.0)
+    hm, wm = matrix(h, cuda), matrix(w, cuda)
+    if op == "xent":
+        got = losses.xent_step(hm, wm, y)
+        r = reference(h, w, y)
+    else:
+        ids, logits = teacher(T, V, min(V, 12), g, cuda, absent=0.2)
+        labels, alpha = (y, 0.5) if op == "both" else (None, 1.0)
+        got = losses.distill_step(hm, wm, ids, logits, temperature=2.0, labels=labels, alpha=alpha)
+        r = reference(h, w, labels, ids, logits, tau=2.0, alpha=alpha)
+    check(got, r, torch.bfloat16, f"{op} {T}x{V}x{D}", parts=2)
+
+
 def test_many_rows_few_of_them_labelled(losses, cuda):
     """More rows than the numbering takes at a time, most without a label."""
     T, V, D = 40_003, 300, 24

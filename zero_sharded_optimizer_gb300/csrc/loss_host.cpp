@@ -22,6 +22,15 @@ constexpr int64_t kMostSize = 0x7fffffff - 1024;  // T, V and D: 32-bit tile coo
 // with 128; one of 2048 rows 352, 354, 356 and 422 us.
 constexpr int64_t kPieceBytes = int64_t(40) << 20;
 
+// Up to this many rows of bf16 G is kept in two bf16 parts instead of one. With
+// one, the gradients are 1.0 to 1.5 times as far from the exact ones as their own
+// rounding makes them, and up to 2.6 times where a few rows hang on one value of
+// G; with two it is 1.00 times. The second part costs 3 to 22 % of a step while
+// a row tile's products wait for the weight anyway, but 21 to 33 % at 512 rows
+// and 34 to 49 % at 1000 (widths 768 and 2048, vocabularies 50257 and 32000),
+// where many rows' errors even out.
+constexpr int64_t kFineRows = 256;
+
 int64_t round_up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
 
 int elem_size(int32_t precision) { return precision == ZERO_FP32 ? 4 : 2; }
@@ -182,6 +191,7 @@ int plan(const zero_head_loss_t* p, bool distill, int pass, Args* a, __nv_bfloat
   a->Tp = std::max<int64_t>(round_up(p->T, zl::kTileM), zl::kTileM);
   a->Dp = round_up(p->D, zl::kPadD);
   a->planes = p->precision == ZERO_FP32 ? 3 : 1;
+  a->parts = a->planes == 3 ? 3 : p->T <= kFineRows ? 2 : 1;
   a->has_ce = p->labels != nullptr || !distill;
   a->has_kd = distill;
   a->K = distill ? int32_t(p->teacher_k) : 0;
@@ -237,7 +247,7 @@ int plan(const zero_head_loss_t* p, bool distill, int pass, Args* a, __nv_bfloat
   int64_t pieces = 0;
   if (pass & kBackward) {
     const int64_t widest = std::max<int64_t>(
-        kPieceBytes / (2 * a->planes * a->Tp) / zl::kTileN * zl::kTileN, zl::kTileN);
+        kPieceBytes / (2 * a->parts * a->Tp) / zl::kTileN * zl::kTileN, zl::kTileN);
     pieces = (a->V + widest - 1) / widest;
     a->piece = round_up((a->V + pieces - 1) / pieces, zl::kTileN);
     pieces = (a->V + a->piece - 1) / a->piece;
@@ -251,10 +261,11 @@ int plan(const zero_head_loss_t* p, bool distill, int pass, Args* a, __nv_bfloat
     const int64_t blocks_t = (a->T + 63) / 64, blocks_v = a->piece / 64, blocks_d = a->Dp / 64;
     const int64_t wide = (a->D + zl::kTileN - 1) / zl::kTileN;
     const int64_t rows = a->Tp / zl::kTileM, cols = a->piece / zl::kTileN;
-    const int64_t work = rows * wide * blocks_v + (p->dweight ? cols * wide * blocks_t : 0) +
+    const int64_t terms = a->planes == 1 ? a->parts : 1;  // of a product with G, to one of the logits
+    const int64_t work = terms * (rows * wide * blocks_v + (p->dweight ? cols * wide * blocks_t : 0)) +
                          (pieces > 1 ? rows * cols * blocks_d : 0);
     a->splits = 1;
-    while (a->splits < 64 && blocks_v / a->splits > std::max<int64_t>(work / (2 * 76), 2)) a->splits *= 2;
+    while (a->splits < 64 && terms * blocks_v / a->splits > std::max<int64_t>(work / (2 * 76), 2 * terms)) a->splits *= 2;
   }
   // The words that begin as zero.
   const int64_t tiles = pass & kBackward ? a->splits * (a->Tp / zl::kTileM) * ((a->D + 255) / 256) : 0;
@@ -273,7 +284,7 @@ int plan(const zero_head_loss_t* p, bool distill, int pass, Args* a, __nv_bfloat
   if (pass & kBackward) {
     w.at = common;
     for (int b = 0; b < zl::kBuffers; ++b)
-      a->g[b] = b < pieces ? w.take<__nv_bfloat16>(a->Tp * a->planes, a->piece) : a->g[0];
+      a->g[b] = b < pieces ? w.take<__nv_bfloat16>(a->Tp * a->parts, a->piece) : a->g[0];
     if (p->dhidden) a->dh = w.take<float>(a->splits * a->Tp, a->Dp);
     most = std::max(most, w.at);
   }
@@ -332,7 +343,7 @@ bool make_program(const Args& a, bool backward, Program* p) {
     CUtensorMap* const to[3] = {&p->g[b], &p->g_mn[b], &p->g_out[b]};
     const uint32_t box[3] = {128, 64, 32};
     for (int i = 0; i < 3; ++i)
-      ok = ok && tensor_map(to[i], a.g[b], a.piece, a.Tp, a.piece, a.planes, a.Tp * a.piece, box[i]);
+      ok = ok && tensor_map(to[i], a.g[b], a.piece, a.Tp, a.piece, a.parts, a.Tp * a.piece, box[i]);
   }
   if (a.dhidden) ok = ok && tensor_map(&p->dh, a.dh, a.Dp, a.Tp, a.Dp, a.splits, a.Tp * a.Dp, 32, true);
   const int es = f32 ? 4 : 2;

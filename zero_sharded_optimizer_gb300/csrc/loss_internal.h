@@ -40,6 +40,7 @@ struct Args {
   int64_t T, V, D;
   int64_t Tp, Dp;         // T and D padded to the tiles
   int32_t planes;         // bf16 parts of a value: 1, or 3 for fp32 storage
+  int32_t parts;          // bf16 parts of G: 1 or 2, or 3 for fp32 storage
   int32_t L;              // sparse entries per row
   int32_t K;              // teacher entries per row
   int32_t has_ce, has_kd;
@@ -91,7 +92,7 @@ struct Args {
   uint32_t* used;         // [pieces] finished units of the products with it
   uint32_t* added;        // [tiles of dh] finished units of a tile
   int64_t zeros;          // 32-bit words from `counters` on that begin as zero
-  __nv_bfloat16* g[kBuffers];  // [planes][Tp][piece] gradients of pieces of the logits
+  __nv_bfloat16* g[kBuffers];  // [parts][Tp][piece] gradients of pieces of the logits
   int64_t piece;          // columns of a piece, a multiple of kTileN
   int32_t splits;         // parts of a piece's columns that dhidden is summed in
   float* dh;              // [splits][Tp][Dp] running sums of dhidden over the pieces

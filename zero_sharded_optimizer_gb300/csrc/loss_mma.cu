@@ -579,7 +579,7 @@ __device__ __forceinline__ uint32_t pack_bf16(float x0, float x1) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 // The same, with what the rounding left over in place of the values: called
-// three times it gives the three parts of fp32 values.
+// again and again it gives the parts of the values.
 __device__ __forceinline__ uint32_t next_part(float& x0, float& x1) {
   const uint32_t w = pack_bf16(x0, x1);
   x0 -= __uint_as_float(w << 16);
@@ -602,16 +602,17 @@ __device__ __forceinline__ void stage_fp32(uint8_t* box, int lane, const float (
 }
 
 // The logits' gradient without the factor that all rows share, as the bf16
-// operand of the two products: rounded once (fp32 storage: in three parts).
-// Each warp stages boxes of its 32 rows by 64 columns and stores them by TMA.
-template <int PLANES, bool CE, bool KD, int P>
+// operand of the two products: rounded once, or in PARTS parts (fp32 storage and
+// a few rows of bf16: loss_host.cpp says when). Each warp stages boxes of its 32
+// rows by 64 columns and stores them by TMA.
+template <int PLANES, int PARTS, bool CE, bool KD, int P>
 __device__ __forceinline__ void gradient_epilogue(const Args& a, const CUtensorMap* out, const Unit& u,
                                                   const Thread& th, int rows, Row& r, uint32_t acc, uint32_t rank,
                                                   uint8_t* box) {
   const int begin = th.half * 128, lane = th.row & 31;
   if (r.i - lane >= (rows + kBlockK - 1) / kBlockK * kBlockK) {  // rows that no product's terms reach
     if (lane == 0)
-      for (int n = 0; n < 2 * PLANES; ++n) store_commit();  // the groups are counted
+      for (int n = 0; n < 2 * PARTS; ++n) store_commit();  // the groups are counted
     return;
   }
   const int64_t v0 = u.piece * a.piece + u.n0;
@@ -665,7 +666,7 @@ __device__ __forceinline__ void gradient_epilogue(const Args& a, const CUtensorM
 #pragma unroll
       for (int n = 0; n < 4; ++n) {
         float &x0 = g[8 * q + 2 * n], &x1 = g[8 * q + 2 * n + 1];
-        w[n] = PLANES == 1 ? pack_bf16(x0, x1) : next_part(x0, x1);
+        w[n] = PARTS == 1 ? pack_bf16(x0, x1) : next_part(x0, x1);
       }
       *reinterpret_cast<uint4*>(box + lane * 128 + (((4 * half + q) ^ (lane & 7)) * 16)) =
           make_uint4(w[0], w[1], w[2], w[3]);
@@ -681,7 +682,7 @@ __device__ __forceinline__ void gradient_epilogue(const Args& a, const CUtensorM
   };
 #pragma unroll 1
   for (int b = 0; b < 2; ++b) {  // 64 columns at a time
-    if (PLANES == 1) {
+    if (PARTS == 1) {
       box_free(lane);
 #pragma unroll 1
       for (int k = 0; k < 2; ++k) {
@@ -695,7 +696,7 @@ __device__ __forceinline__ void gradient_epilogue(const Args& a, const CUtensorM
       columns(begin + 64 * b, g[0]);
       columns(begin + 64 * b + 32, g[1]);
 #pragma unroll
-      for (int p = 0; p < PLANES; ++p) {
+      for (int p = 0; p < PARTS; ++p) {
         box_free(lane);
         stage(0, g[0]);
         stage(1, g[1]);
@@ -817,10 +818,15 @@ __device__ __forceinline__ void weight_epilogue(const Args& a, const Program& pr
 
 // ----------------------------------------------------------------- kernel --
 
-template <int PLANES, bool CE, bool KD>
+template <int PLANES, int PARTS, bool CE, bool KD>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     products_kernel(const __grid_constant__ Args a, const __grid_constant__ Program prog) {
-  constexpr int kTerms = PLANES == 1 ? 1 : 6;
+  static_assert(PLANES == 1 ? PARTS <= 2 : PLANES == 3 && PARTS == 3, "the products of the parts");
+  // Products of parts that a block of K stands for: with two parts of G one
+  // after the other, so that the block of the other operand stays in L2.
+  auto terms_of = [](const Unit& x) {
+    return PLANES == 3 ? 6 : PARTS == 2 && (x.mode == kWeight || x.mode == kHidden) ? 2 : 1;
+  };
   extern __shared__ uint8_t raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   uint8_t* staging = base + kStages * kStageBytes;
@@ -922,9 +928,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const int segment = segment_of<PLANES>(a, u.mode);
           for (int s = 0; ok && s < segments; ++s) {
             const int k_begin = s * segment, k_end = min(blocks_of(u), k_begin + segment);
-            for (int term = 0; ok && term < kTerms; ++term) {
-              const int pa = kTerms == 1 ? 0 : kTermA[term], pb = kTerms == 1 ? 0 : kTermB[term];
-              for (int k = k_begin; k < k_end; ++k) {
+            for (int term = 0; ok && term < (PLANES == 3 ? 6 : 1); ++term) {
+              const int pb = PLANES == 3 ? kTermB[term] : 0;
+              const int each = PLANES == 3 ? 1 : terms_of(u);  // 1 or 2
+              for (int i = k_begin * each; i < k_end * each; ++i) {
+                const int k = i >> (each - 1);
+                const int pa = PLANES == 3 ? kTermA[term] : (i + 1) & (each - 1);
                 if (!(ok = wait(empty + 8 * stage, phase ^ 1))) break;
                 const uint32_t sa = smem_u32(base + stage * kStageBytes), sb = sa + kOperandBytes;
                 const uint32_t bar = full0 + 8 * stage;
@@ -976,7 +985,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (!(ok = wait(acc_empty + 8 * buffer, acc_phase ^ 1))) break;
             fence_after();
             bool add = false;
-            const int count = (min(blocks_of(u), (s + 1) * segment) - s * segment) * kTerms;
+            const int count = (min(blocks_of(u), (s + 1) * segment) - s * segment) * terms_of(u);
             for (int k = 0; k < count; ++k) {
               if (!(ok = wait(full + 8 * stage, phase))) break;
               fence_after();
@@ -1143,12 +1152,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       } else if (u.mode == kGradient) {
         const CUtensorMap* out = &prog.g_out[u.piece % kBuffers];
         const int p = CE && KD ? shared_power(float(a.tau)) : 0;
-        if (CE && KD && p == 1) gradient_epilogue<PLANES, CE, KD, 1>(a, out, u, th, rows, r, acc, rank, box);
-        else if (CE && KD && p == 2) gradient_epilogue<PLANES, CE, KD, 2>(a, out, u, th, rows, r, acc, rank, box);
-        else if (CE && KD && p == 4) gradient_epilogue<PLANES, CE, KD, 4>(a, out, u, th, rows, r, acc, rank, box);
-        else gradient_epilogue<PLANES, CE, KD, 0>(a, out, u, th, rows, r, acc, rank, box);
+        if (CE && KD && p == 1) gradient_epilogue<PLANES, PARTS, CE, KD, 1>(a, out, u, th, rows, r, acc, rank, box);
+        else if (CE && KD && p == 2) gradient_epilogue<PLANES, PARTS, CE, KD, 2>(a, out, u, th, rows, r, acc, rank, box);
+        else if (CE && KD && p == 4) gradient_epilogue<PLANES, PARTS, CE, KD, 4>(a, out, u, th, rows, r, acc, rank, box);
+        else gradient_epilogue<PLANES, PARTS, CE, KD, 0>(a, out, u, th, rows, r, acc, rank, box);
         if (lane == 0 && finished) {  // the unit before: its stores are the older ones
-          asm volatile("cp.async.bulk.wait_group %0;" ::"n"(2 * PLANES) : "memory");
+          asm volatile("cp.async.bulk.wait_group %0;" ::"n"(2 * PARTS) : "memory");
           report(finished, finished_tile);
         }
         finished = a.formed + u.piece;
@@ -1179,9 +1188,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
 
-template <int PLANES, bool CE, bool KD>
+template <int PLANES, int PARTS, bool CE, bool KD>
 cudaError_t launch(const Args& a, const Program& prog, int device, int sms, cudaStream_t s) {
-  auto* kernel = products_kernel<PLANES, CE, KD>;
+  auto* kernel = products_kernel<PLANES, PARTS, CE, KD>;
   // Once per device (a race only does it twice): the kernel's shared memory, and
   // a check that the register shares of its warps do not exceed what a launch
   // brings.
@@ -1210,13 +1219,18 @@ cudaError_t launch(const Args& a, const Program& prog, int device, int sms, cuda
 
 }  // namespace
 
+template <int PLANES, int PARTS>
+static cudaError_t launch_terms(const Args& a, const Program& prog, int device, int sms, cudaStream_t s) {
+  if (!a.has_kd) return launch<PLANES, PARTS, true, false>(a, prog, device, sms, s);
+  return a.has_ce ? launch<PLANES, PARTS, true, true>(a, prog, device, sms, s)
+                  : launch<PLANES, PARTS, false, true>(a, prog, device, sms, s);
+}
+
 cudaError_t launch_products(const Args& a, const Program& prog, int device, int sms, cudaStream_t s) {
-  if (a.planes == 1) {
-    if (!a.has_kd) return launch<1, true, false>(a, prog, device, sms, s);
-    return a.has_ce ? launch<1, true, true>(a, prog, device, sms, s) : launch<1, false, true>(a, prog, device, sms, s);
-  }
-  if (!a.has_kd) return launch<3, true, false>(a, prog, device, sms, s);
-  return a.has_ce ? launch<3, true, true>(a, prog, device, sms, s) : launch<3, false, true>(a, prog, device, sms, s);
+  if (a.planes == 3) return launch_terms<3, 3>(a, prog, device, sms, s);
+  // The forward pass forms no G: one kernel serves it for any number of rows.
+  return a.parts == 2 && !prog.forward ? launch_terms<1, 2>(a, prog, device, sms, s)
+                                       : launch_terms<1, 1>(a, prog, device, sms, s);
 }
 
 }  // namespace zl
