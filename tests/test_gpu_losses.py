@@ -392,6 +392,26 @@ def test_equal_inputs_give_equal_bits(losses, cuda):
             assert torch.equal(getattr(r, name), getattr(first, name)), name
 
 
+def test_beside_other_launches_of_other_priorities(losses, cuda):
+    """Steps that compete for the SMs with each other and with other kernels: their pairs of
+    blocks begin at different times, and some only after others have worked for a while."""
+    T, V, D = 3000, 9_000, 96
+    h, w, y, _ = inputs(T, V, D, torch.bfloat16, 63, cuda, masked=0.1)
+    busy = torch.randn(1 << 26, device=cuda)
+    first = losses.xent_step(h, w, y)
+    torch.cuda.synchronize()
+    other, streams = torch.cuda.Stream(), [torch.cuda.Stream(priority=p) for p in (0, -1, 0, -1)]
+    again = []
+    for i in range(16):
+        with torch.cuda.stream(other):
+            busy.mul_(0.5)
+        again.append(losses.xent_step(h, w, y, stream=streams[i % 4]))
+    torch.cuda.synchronize()
+    for r in again:
+        for name in ("loss", "dhidden", "dweight"):
+            assert torch.equal(getattr(r, name), getattr(first, name)), name
+
+
 def test_in_a_graph(losses, cuda):
     """Captured once and replayed on new values of the same tensors."""
     T, V, D = 90, 700, 64

@@ -1013,9 +1013,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     } else if (warp == 2 && rank == 0) {
       // ---- hands out the units
       if (elect_one()) {
-        const int32_t pairs = int32_t(gridDim.x / 2);
+        // In the forward pass, where no unit waits for another, a pair's first one
+        // is its own number. In the backward pass that would give units to pairs
+        // that do not run yet, and the others could wait for them while holding
+        // the SMs that they need (beside another such launch).
+        const int32_t given = prog.forward ? int32_t(gridDim.x / 2) : 0;
         Phases phases;
-        for (int32_t n = int32_t(blockIdx.x / 2);; n = pairs + atomicAdd(prog.counter, 1)) {
+        for (int32_t n = prog.forward ? int32_t(blockIdx.x / 2) : atomicAdd(prog.counter, 1);;
+             n = given + atomicAdd(prog.counter, 1)) {
           const Unit x = phases.unit(a, prog, rows, n);
           if (!wait(ring_empty + 8 * slot, slot_phase ^ 1)) break;
           for (uint32_t c = 0; c < 2; ++c) {
