@@ -219,6 +219,17 @@ def test_distill_many_entries(losses, cuda):
           torch.bfloat16)
 
 
+@pytest.mark.parametrize("K", [184, 187, 188, 191, 192, 255])
+def test_distill_many_rows_around_what_a_block_holds(losses, cuda, K):
+    """Lists of K entries on both sides of what a block of 16 rows keeps in shared memory, and
+    enough rows (16 for each of 152 SMs) that a block would take as many."""
+    T, V, D = 2435, 300, 16
+    h, w, y, g = inputs(T, V, D, torch.bfloat16, 300 + K, cuda, masked=0.1)
+    ids, logits = teacher(T, V, K, g, cuda, absent=0.1)
+    r = reference(h, w, y, ids, logits, tau=2.0, alpha=0.5)
+    check(losses.distill_step(h, w, ids, logits, temperature=2.0, labels=y, alpha=0.5), r, torch.bfloat16)
+
+
 @pytest.mark.parametrize("kind", TYPES)
 def test_backward_alone_equals_step(losses, cuda, kind):
     dt = TYPES[kind]

@@ -160,11 +160,14 @@ __global__ void __launch_bounds__(256) label_rows_kernel(const Args a) {
   if (t < a.T) prepare_label(a, t);
 }
 
+constexpr int kTeacherRows = 16;                  // most rows of a block of teacher_rows_kernel
+constexpr size_t kSharedWithoutAsking = 48 << 10;  // static and dynamic shared memory of a launch
+
 // A block's rows, one a warp, and where each half tile's entries begin in
 // them: starts[h][t] is the first entry with an id of 128 h at least.
 __global__ void teacher_rows_kernel(const Args a) {
   extern __shared__ __align__(16) int32_t sh[];
-  __shared__ int kept[16];
+  __shared__ int kept[kTeacherRows];
   let_next_start();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rows = blockDim.x >> 5;
   const int n4 = (a.K + 4) / 4 * 4;
@@ -569,9 +572,9 @@ cudaError_t launch_rows(const Args& a, bool pack_weight, bool* packed, cudaStrea
     } else {
       const size_t row = size_t(16) * ((a.K + 4) / 4 * 4);
       // Rows of a block: 16, whose places in the table fill a 32-byte sector, or
-      // what shared memory holds, and fewer where they leave SMs idle (333 rows:
-      // 197 us a step instead of 200).
-      int rows = 16 * row <= 48 * 1024 ? 16 : 2;
+      // what shared memory holds beside `kept`, and fewer where they leave SMs idle
+      // (333 rows: 197 us a step instead of 200).
+      int rows = kTeacherRows * (row + sizeof(int)) <= kSharedWithoutAsking ? kTeacherRows : 2;
       while (rows > 2 && a.T / rows < 152) rows /= 2;
       e = launch(teacher_rows_kernel, unsigned((a.T + rows - 1) / rows), rows * 32, rows * row, s, false, a);
     }
