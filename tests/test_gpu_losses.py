@@ -289,6 +289,48 @@ def test_another_stream(losses, cuda):
     check(got, r, torch.bfloat16)
 
 
+def spy_on(monkeypatch, losses, name):
+    """The problems passed to the library's call `name`, as (address, bytes) of their workspace."""
+    seen, call = [], getattr(losses.abi, name)
+
+    def spy(p, stream=None):
+        seen.append((p.workspace, p.workspace_bytes))
+        return call(p, stream)
+
+    monkeypatch.setattr(losses.abi, name, spy)
+    return seen
+
+
+def test_a_handle_keeps_its_workspace(losses, cuda, monkeypatch):
+    """A stream given as a raw handle: while its work is still queued, no new tensor of the
+    current stream gets the workspace."""
+    T, V, D = 300, 3000, 128
+    h, w, y, _ = inputs(T, V, D, torch.bfloat16, 65, cuda)
+    seen = spy_on(monkeypatch, losses, "zero_xent_step")
+    for side in (torch.cuda.Stream(), torch.cuda.Stream()):
+        losses.xent_step(h, w, y)          # memory to hand out again is there
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(400_000_000)
+        got = losses.xent_step(h, w, y, stream=side.cuda_stream)
+        at, size = seen[-1]
+        fresh = [torch.empty(n, dtype=torch.uint8, device=cuda) for n in (size, size // 2, 4096) for _ in range(4)]
+        assert not side.query(), "the work is still queued"
+        for t in fresh:
+            assert t.data_ptr() + t.numel() <= at or at + size <= t.data_ptr()
+        side.synchronize()
+        check(got, reference(h, w, y), torch.bfloat16)
+
+
+def test_the_default_stream_by_its_handles(losses, cuda):
+    T, V, D = 70, 500, 64
+    h, w, y, _ = inputs(T, V, D, torch.bfloat16, 66, cuda)
+    for handle in (0, 1):
+        got = losses.xent_step(h, w, y, stream=handle)
+        torch.cuda.synchronize()
+        check(got, reference(h, w, y), torch.bfloat16)
+
+
 @pytest.mark.parametrize("kind", TYPES)
 def test_gradient_against_differences(losses, cuda, kind):
     """The losses' own central difference along a direction, against the

@@ -19,9 +19,10 @@ reads -- and are allocated otherwise; ``accumulate`` adds to ``dweight``.
 ``linear_cross_entropy`` and ``linear_distillation`` are the same losses as
 differentiable functions for torch.autograd.
 
-Work is queued on ``stream`` (the current stream by default). The workspace is
-taken from PyTorch's allocator for each call, on the current stream; another
-``stream`` is told of it, as of every tensor the call allocates.
+Work is queued on ``stream``: a ``torch.cuda.Stream``, a raw handle, or None for
+the current stream. The workspace is taken from PyTorch's allocator for each
+call, on the current stream; another ``stream`` is told of it, as of every tensor
+the call allocates.
 """
 
 from __future__ import annotations
@@ -88,6 +89,16 @@ def _vector(t, what: str, dtype, count: int, device) -> int:
     return t.data_ptr()
 
 
+def _named(stream, device):
+    """``stream`` as the allocator knows it: a handle's memory is given back behind
+    its work only if the allocator is told of the stream."""
+    if stream is None or isinstance(stream, torch.cuda.Stream):
+        return stream
+    handle = int(stream)
+    # 1 names the legacy default stream, PyTorch's own default, whose handle is 0.
+    return torch.cuda.ExternalStream(0 if handle == 1 else handle, device=device)
+
+
 class _Call:
     """One call's zero_head_loss_t and the tensors behind its pointers."""
 
@@ -101,7 +112,7 @@ class _Call:
         V = weight2.shape[0]
         self.T, self.V, self.D = T, V, D
         self.shape = hidden.shape
-        self.stream = stream
+        self.stream = _named(stream, self.device)
         self.distill = teacher is not None
         self.labels = labels is not None
         self.none = reduction == "none"
@@ -206,10 +217,10 @@ class _Call:
         stream = self.stream
         # the current stream's handle, without the object around it
         call(p, torch._C._cuda_getCurrentRawStream(index) if stream is None else stream)
-        if isinstance(stream, torch.cuda.Stream):
+        if stream is not None:
             for t in self.keep:
                 if t is not None:
-                    t.record_stream(self.stream)
+                    t.record_stream(stream)
 
 
 def xent_forward(hidden, weight, labels, *, reduction: str = "mean", ignore_index: int = -100,
