@@ -322,6 +322,56 @@ def test_a_handle_keeps_its_workspace(losses, cuda, monkeypatch):
         check(got, reference(h, w, y), torch.bfloat16)
 
 
+def apart(t, at, size):
+    return t.data_ptr() + t.numel() * t.element_size() <= at or at + size <= t.data_ptr()
+
+
+@pytest.mark.parametrize("op", ["xent", "distill"])
+def test_memory_that_the_current_stream_still_uses(losses, cuda, monkeypatch, op):
+    """A call on another stream gets neither its workspace nor its results from memory whose
+    last use is still queued on the current stream; nor does a later call there from results
+    that the current stream still reads."""
+    T, V, D = 300, 3000, 128
+    h, w, y, g = inputs(T, V, D, torch.bfloat16, 67, cuda)
+    ids, logits = teacher(T, V, 5, g, cuda)
+    args = (h, w, y) if op == "xent" else (h, w, ids, logits)
+    step = getattr(losses, op + "_step")
+    r = reference(h, w, y) if op == "xent" else reference(h, w, None, ids, logits)
+    seen = spy_on(monkeypatch, losses, f"zero_{op}_step")
+    side = torch.cuda.Stream()
+    step(*args)                            # the sizes that a call asks for
+    size = seen[-1][1]
+    torch.cuda.synchronize()
+    torch.cuda._sleep(400_000_000)
+    freed = []
+    for n in (size, V * D * 2, T * D * 2, T * 4, T * 4, T * 4, 4):
+        t = torch.empty(n, dtype=torch.uint8, device=cuda)
+        t.fill_(1)
+        freed.append((t.data_ptr(), n))
+        del t
+    got = step(*args, stream=side)
+    assert not torch.cuda.current_stream().query(), "the memory's last use is still queued"
+    for at, n in freed:
+        assert seen[-1][0] + size <= at or at + n <= seen[-1][0]
+        assert all(apart(t, at, n) for t in got if t is not None)
+    side.synchronize()
+    check(got, r, torch.bfloat16)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(400_000_000)
+    used = [(t.data_ptr(), t.numel() * t.element_size()) for t in got if t is not None]
+    sums = [t.double().sum() for t in got if t is not None]
+    del got
+    again = step(*args, stream=side)
+    assert not torch.cuda.current_stream().query(), "the results' last use is still queued"
+    for at, n in used:
+        assert seen[-1][0] + size <= at or at + n <= seen[-1][0]
+        assert all(apart(t, at, n) for t in again if t is not None)
+    side.synchronize()
+    check(again, r, torch.bfloat16)
+    torch.cuda.synchronize()
+    assert [float(x) for x in sums] == [float(t.double().sum()) for t in again if t is not None]
+
+
 def test_the_default_stream_by_its_handles(losses, cuda):
     T, V, D = 70, 500, 64
     h, w, y, _ = inputs(T, V, D, torch.bfloat16, 66, cuda)

@@ -20,9 +20,11 @@ reads -- and are allocated otherwise; ``accumulate`` adds to ``dweight``.
 differentiable functions for torch.autograd.
 
 Work is queued on ``stream``: a ``torch.cuda.Stream``, a raw handle, or None for
-the current stream. The workspace is taken from PyTorch's allocator for each
-call, on the current stream; another ``stream`` is told of it, as of every tensor
-the call allocates.
+the current stream. The workspace and the results that are not given are taken
+from PyTorch's allocator for each call, as that stream's, so what the current
+stream still does with memory that it has given back is not run into. The
+allocator is told that ``stream`` uses the inputs and that the current stream
+uses the results; to order the two streams' work is left to the caller.
 """
 
 from __future__ import annotations
@@ -116,7 +118,8 @@ class _Call:
         self.distill = teacher is not None
         self.labels = labels is not None
         self.none = reduction == "none"
-        self.keep = [hidden2, weight2, labels]
+        self.keep = [hidden2, weight2, labels]   # the caller's tensors
+        self.made = []                           # its results
         y = None
         if labels is not None:
             y = _vector(labels, "labels", torch.int64, T, self.device)
@@ -139,9 +142,15 @@ class _Call:
             p.temperature, p.alpha = float(temperature), float(alpha)
             self.keep += [ids, logits]
 
+    def empty(self, shape, dtype):
+        if self.stream is None:
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        with torch.cuda.stream(self.stream):
+            return torch.empty(shape, dtype=dtype, device=self.device)
+
     def new(self, shape, dtype=torch.float32):
-        t = torch.empty(shape, dtype=dtype, device=self.device)
-        self.keep.append(t)
+        t = self.empty(shape, dtype)
+        self.made.append(t)
         return t
 
     def statistics(self, lse, lse_tau):
@@ -212,15 +221,18 @@ class _Call:
             size, call = abi.zero_distill_workspace_bytes(p), distill
         else:
             size, call = abi.zero_xent_workspace_bytes(p), xent
-        space = self.new(size, torch.uint8)
+        space = self.empty(size, torch.uint8)
         p.workspace, p.workspace_bytes = space.data_ptr(), size
         stream = self.stream
-        # the current stream's handle, without the object around it
-        call(p, torch._C._cuda_getCurrentRawStream(index) if stream is None else stream)
         if stream is not None:
             for t in self.keep:
                 if t is not None:
                     t.record_stream(stream)
+            current = torch.cuda.current_stream(self.device)
+            for t in self.made:
+                t.record_stream(current)
+        # the current stream's handle, without the object around it
+        call(p, torch._C._cuda_getCurrentRawStream(index) if stream is None else stream)
 
 
 def xent_forward(hidden, weight, labels, *, reduction: str = "mean", ignore_index: int = -100,
