@@ -372,6 +372,36 @@ def test_memory_that_the_current_stream_still_uses(losses, cuda, monkeypatch, op
     assert [float(x) for x in sums] == [float(t.double().sum()) for t in again if t is not None]
 
 
+def test_bf16_teacher_logits(losses, cuda):
+    """They give the bits of the same values in float32 -- also on a named stream while the
+    current one is busy, when they come from work on that stream that is still queued."""
+    T, V, D, K = 140, 700, 64, 6
+    h, w, y, g = inputs(T, V, D, torch.bfloat16, 68, cuda, masked=0.1)
+    ids, logits = teacher(T, V, K, g, cuda, absent=0.1)
+    logits = logits.bfloat16()
+    more = dict(temperature=2.0, labels=y, alpha=0.5)
+    want = losses.distill_step(h, w, ids, logits.float(), **more)
+    r = reference(h, w, y, ids, logits.float(), tau=2.0, alpha=0.5)
+    got = losses.distill_step(h, w, ids, logits, **more)
+    check(got, r, torch.bfloat16)
+    torch.cuda.synchronize()
+    for side in (torch.cuda.Stream(), torch.cuda.Stream()):
+        for stream in (side, side.cuda_stream):
+            with torch.cuda.stream(side):
+                late = torch.full_like(logits, -50.0)
+            side.synchronize()
+            with torch.cuda.stream(side):
+                torch.cuda._sleep(20_000_000)
+                late.copy_(logits)
+            torch.cuda._sleep(400_000_000)
+            got = losses.distill_step(h, w, ids, late, stream=stream, **more)
+            side.synchronize()
+            assert not torch.cuda.current_stream().query(), "nothing of the call waits for the current stream"
+            for a, b in zip(got, want):
+                assert torch.equal(a, b)
+            torch.cuda.synchronize()
+
+
 def test_the_default_stream_by_its_handles(losses, cuda):
     T, V, D = 70, 500, 64
     h, w, y, _ = inputs(T, V, D, torch.bfloat16, 66, cuda)

@@ -29,12 +29,14 @@ uses the results; to order the two streams' work is left to the caller.
 
 from __future__ import annotations
 
+import contextlib
 from typing import NamedTuple
 
 import torch
 
 from . import abi
 
+_AS_IT_IS = contextlib.nullcontext()
 _REDUCE = {"none": abi.ZERO_REDUCE_NONE, "mean": abi.ZERO_REDUCE_MEAN, "sum": abi.ZERO_REDUCE_SUM}
 
 
@@ -135,17 +137,21 @@ class _Call:
                 raise ValueError("teacher_ids must have at least 2 dimensions")
             K = ids.shape[-1]
             p.teacher_ids = _vector(ids, "teacher_ids", torch.int64, T * K, self.device)
-            if isinstance(logits, torch.Tensor) and logits.dtype == torch.bfloat16:
-                logits = logits.float()
+            self.keep += [ids, logits]
+            if isinstance(logits, torch.Tensor) and logits.is_cuda and logits.dtype == torch.bfloat16:
+                with self.on_stream():
+                    logits = logits.float()
+            self.wide = logits               # held until the call is queued
             p.teacher_logits = _vector(logits, "teacher_logits", torch.float32, T * K, self.device)
             p.teacher_k = K
             p.temperature, p.alpha = float(temperature), float(alpha)
-            self.keep += [ids, logits]
+
+    def on_stream(self):
+        """Where the call's own work is queued and its memory is taken."""
+        return _AS_IT_IS if self.stream is None else torch.cuda.stream(self.stream)
 
     def empty(self, shape, dtype):
-        if self.stream is None:
-            return torch.empty(shape, dtype=dtype, device=self.device)
-        with torch.cuda.stream(self.stream):
+        with self.on_stream():
             return torch.empty(shape, dtype=dtype, device=self.device)
 
     def new(self, shape, dtype=torch.float32):
