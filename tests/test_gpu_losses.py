@@ -468,6 +468,21 @@ def test_autograd(losses, cuda):
     assert bool(((a.grad.double() - r["dhidden"]).abs() <= bounds(r, torch.float32)["dhidden"]).all())
 
 
+def test_a_graph_of_the_gradients(losses, cuda):
+    """Under create_graph the gradients are those without; to differentiate them again raises."""
+    T, V, D = 60, 500, 64
+    x, w, y, g = inputs(T, V, D, torch.float32, 42, cuda, masked=0.2)
+    ids, logits = teacher(T, V, 6, g, cuda)
+    for loss in (lambda h: losses.linear_cross_entropy(h, w, y),
+                 lambda h: losses.linear_distillation(h, w, ids, logits, 2.0, y, 0.5)):
+        a = x.clone().requires_grad_()
+        plain, = torch.autograd.grad(loss(a * a), a)
+        once, = torch.autograd.grad(loss(a * a), a, create_graph=True)
+        assert torch.equal(plain, once)
+        with pytest.raises(RuntimeError, match="no second derivatives"):
+            once.square().sum().backward()
+
+
 @pytest.mark.parametrize("kind,T,V,D", [("bf16", 8200, 21000, 64), ("fp32", 4100, 13000, 64)])
 def test_several_pieces_of_the_vocabulary(losses, cuda, kind, T, V, D):
     """Enough rows that the gradient of the logits is formed in several pieces."""

@@ -122,3 +122,89 @@ def test_workspace_sizes(abi):
     with pytest.raises(abi.ZeroError):
         size(**dict(big, D=2 ** 30, hidden_stride=2 ** 30, weight_stride=2 ** 30, dhidden_stride=2 ** 30,
                     dweight_stride=2 ** 30, V=2 ** 31 - 2000, T=2 ** 31 - 2000, precision=0))
+
+
+@pytest.fixture
+def on_the_cpu(abi, monkeypatch):
+    """losses, with its four autograd calls replaced by the definition on CPU tensors."""
+    import torch
+    from zero_sharded_optimizer_gb300 import losses
+
+    def value(h, w, y, ids=None, u=None, temperature=1.0, alpha=1.0, reduction="mean", ignore_index=-100):
+        z = h @ w.T
+        loss = torch.zeros(h.shape[0], dtype=h.dtype)
+        if y is not None:
+            ce = torch.nn.functional.cross_entropy(z, y, reduction="none", ignore_index=ignore_index)
+            loss = loss + (ce if ids is None else (1 - alpha) * ce)
+        if ids is not None:
+            logq = torch.log_softmax(u / temperature, 1)
+            logp = torch.log_softmax(z / temperature, 1).gather(1, ids)
+            loss = loss + alpha * temperature ** 2 * (logq.exp() * (logq - logp)).sum(1)
+        return loss, (loss.mean() if reduction == "mean" else loss.sum())
+
+    def result(loss, reduced, distill, **grads):
+        lse = torch.zeros(loss.shape[0])
+        return losses.Losses(loss.detach(), reduced.detach(), lse, lse if distill else None, **grads)
+
+    def gradients(h, w, distill, dloss, dhidden, dweight, *args, **more):
+        with torch.enable_grad():
+            a, b = h.detach().requires_grad_(), w.detach().requires_grad_()
+            loss, reduced = value(a, b, *args, **more)
+            total = loss @ dloss if more["reduction"] == "none" else reduced * dloss
+            gh, gw = torch.autograd.grad(total, (a, b))
+        return result(loss, reduced, distill, dhidden=None if dhidden is False else gh,
+                      dweight=None if dweight is False else gw)
+
+    monkeypatch.setattr(losses, "xent_forward", lambda h, w, y, **m: result(*value(h, w, y, **m), False))
+    monkeypatch.setattr(losses, "distill_forward", lambda h, w, ids, u, labels, **m:
+                        result(*value(h, w, labels, ids, u, **m), True))
+    monkeypatch.setattr(losses, "xent_backward", lambda h, w, y, lse, dloss, dhidden, dweight, **m:
+                        gradients(h, w, False, dloss, dhidden, dweight, y, **m))
+    monkeypatch.setattr(losses, "distill_backward",
+                        lambda h, w, ids, u, lse, lse_tau, labels, dloss, dhidden, dweight, **m:
+                        gradients(h, w, True, dloss, dhidden, dweight, labels, ids, u, **m))
+    return losses, value
+
+
+@pytest.mark.parametrize("op", ["xent", "distill"])
+@pytest.mark.parametrize("reduction", ["mean", "none"])
+@pytest.mark.parametrize("wrt", ["hidden", "weight", "both"])
+def test_second_derivatives_raise(on_the_cpu, op, reduction, wrt):
+    """Gradients with a graph are the right ones; a penalty on them, whose gradient runs
+    through the losses' own second derivatives, raises instead of losing that part."""
+    import torch
+    losses, value = on_the_cpu
+    g = torch.Generator().manual_seed(5)
+    T, V, D, K = 6, 20, 4, 3
+
+    def fresh():
+        p = [torch.randn(T, D, generator=g, dtype=torch.float64), torch.randn(V, D, generator=g, dtype=torch.float64)]
+        return [x.requires_grad_(wrt in (name, "both")) for x, name in zip(p, ("hidden", "weight"))]
+
+    a, b = fresh()
+    taken = [x for x in (a, b) if x.requires_grad]
+    y = torch.randint(0, V, (T,), generator=g)
+    ids, u = torch.randint(0, V, (T, K), generator=g), torch.randn(T, K, generator=g, dtype=torch.float64)
+    rows = torch.randn(T, generator=g, dtype=torch.float64)
+    h, w = a * a, b * b + b          # what the penalty's gradient also runs through
+    if op == "xent":
+        got = losses.linear_cross_entropy(h, w, y, reduction=reduction)
+        loss, reduced = value(h, w, y)
+    else:
+        got = losses.linear_distillation(h, w, ids, u, 2.0, y, 0.5, reduction=reduction)
+        loss, reduced = value(h, w, y, ids, u, 2.0, 0.5)
+    got, want = (got @ rows, loss @ rows) if reduction == "none" else (got, reduced)
+    once = torch.autograd.grad(got, taken, create_graph=True)
+    exact = torch.autograd.grad(want, taken)
+    for x, e in zip(once, exact):
+        assert torch.allclose(x, e, rtol=1e-9, atol=1e-12)
+    penalty = sum(x.square().sum() for x in once)
+    with pytest.raises(RuntimeError, match="no second derivatives"):
+        penalty.backward()
+    # through the incoming gradient alone, too
+    scale = torch.ones((), dtype=torch.float64, requires_grad=True)
+    h = a.detach().requires_grad_()
+    loss = losses.linear_cross_entropy(h, b.detach(), y)
+    d, = torch.autograd.grad(loss * scale, h, create_graph=True)
+    with pytest.raises(RuntimeError, match="no second derivatives"):
+        d.sum().backward()

@@ -17,7 +17,8 @@ the head's view into a rank's flat gradient buffer, which the ZeRO step then
 reads -- and are allocated otherwise; ``accumulate`` adds to ``dweight``.
 
 ``linear_cross_entropy`` and ``linear_distillation`` are the same losses as
-differentiable functions for torch.autograd.
+differentiable functions for torch.autograd. Their gradients can be part of a
+graph (``create_graph``), but to differentiate them again raises a RuntimeError.
 
 Work is queued on ``stream``: a ``torch.cuda.Stream``, a raw handle, or None for
 the current stream. The workspace and the results that are not given are taken
@@ -318,6 +319,27 @@ def distill_step(hidden, weight, teacher_ids, teacher_logits, *, temperature: fl
 
 # -------------------------------------------------------------- autograd --
 
+class _Once(torch.autograd.Function):
+    """Passes gradients on; to differentiate them again raises. ``inputs`` are what they
+    depend on: without that tie autograd would take the gradients for constants, and a
+    second derivative would lose their part without a word."""
+
+    @staticmethod
+    def forward(ctx, dhidden, dweight, *inputs):
+        return dhidden, dweight
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise RuntimeError("the vocabulary losses have no second derivatives")
+
+
+def _once(r, *inputs):
+    """dhidden and dweight of ``r`` as a backward function returns them."""
+    if torch.is_grad_enabled():      # create_graph
+        return _Once.apply(r.dhidden, r.dweight, *inputs)
+    return r.dhidden, r.dweight
+
+
 class _Xent(torch.autograd.Function):
     @staticmethod
     def forward(ctx, hidden, weight, labels, reduction, ignore_index):
@@ -331,10 +353,11 @@ class _Xent(torch.autograd.Function):
         hidden, weight, labels, lse = ctx.saved_tensors
         if not any(ctx.needs_input_grad[:2]):
             return None, None, None, None, None
-        r = xent_backward(hidden, weight, labels, lse, dloss=dloss.contiguous(),
-                          dhidden=None if ctx.needs_input_grad[0] else False,
-                          dweight=None if ctx.needs_input_grad[1] else False, **ctx.options)
-        return r.dhidden, r.dweight, None, None, None
+        with torch.no_grad():
+            r = xent_backward(hidden, weight, labels, lse, dloss=dloss.contiguous(),
+                              dhidden=None if ctx.needs_input_grad[0] else False,
+                              dweight=None if ctx.needs_input_grad[1] else False, **ctx.options)
+        return *_once(r, hidden, weight, dloss), None, None, None
 
 
 class _Distill(torch.autograd.Function):
@@ -350,11 +373,12 @@ class _Distill(torch.autograd.Function):
         hidden, weight, ids, logits, labels, lse, lse_tau = ctx.saved_tensors
         if not any(ctx.needs_input_grad[:2]):
             return None, None, None, None, None, None
-        r = distill_backward(hidden, weight, ids, logits, lse, lse_tau, labels=labels,
-                             dloss=dloss.contiguous(),
-                             dhidden=None if ctx.needs_input_grad[0] else False,
-                             dweight=None if ctx.needs_input_grad[1] else False, **ctx.options)
-        return r.dhidden, r.dweight, None, None, None, None
+        with torch.no_grad():
+            r = distill_backward(hidden, weight, ids, logits, lse, lse_tau, labels=labels,
+                                 dloss=dloss.contiguous(),
+                                 dhidden=None if ctx.needs_input_grad[0] else False,
+                                 dweight=None if ctx.needs_input_grad[1] else False, **ctx.options)
+        return *_once(r, hidden, weight, dloss), None, None, None, None
 
 
 def linear_cross_entropy(hidden, weight, labels, reduction: str = "mean",
