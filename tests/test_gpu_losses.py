@@ -620,3 +620,49 @@ def test_refusals_of_the_binding(losses, cuda):
     wide[:, :16] = h
     got = losses.xent_step(wide[:, :16], w, y, dhidden=wide[:, 16:])
     check(got, reference(h, w, y), torch.bfloat16)
+
+
+def test_shapes_that_do_not_fit_the_rows(losses, cuda):
+    """As many elements in another order are refused; the rows' own dimensions, the rows in one
+    dimension, dimensions of one element, and any dimensions beside rows in one are not."""
+    B, S, V, D, K = 4, 6, 50, 16, 3
+    T = B * S
+    h, w, y, g = inputs(T, V, D, torch.bfloat16, 69, cuda)
+    ids, logits = teacher(T, V, K, g, cuda)
+    r = reference(h, w, y, ids, logits, alpha=0.5)
+    h3, dloss = h.view(B, S, D), torch.rand(T, generator=g).to(cuda)
+
+    def distill(y=y, ids=ids, logits=logits, h=h3, **more):
+        return losses.distill_step(h, w, ids, logits, labels=y, alpha=0.5, **more)
+
+    for shape in ((T,), (B, S), (T, 1), (1, T), (B, 1, S), (B, S, 1)):
+        for rows in ((T,), (B, S)):
+            check(distill(y.view(shape), ids.view(*rows, K), logits.view(B, S, K)), r, torch.bfloat16)
+    more = dict(reduction="none")
+    each = losses.xent_step(h3, w, y, dloss=dloss.view(B, S), **more)
+    for bad in ((S, B), (B // 2, 2 * S), (B, 2, S // 2)):
+        with pytest.raises(ValueError, match="labels"):
+            losses.xent_forward(h3, w, y.view(bad))
+        with pytest.raises(ValueError, match="labels"):
+            distill(y.view(bad))
+        with pytest.raises(ValueError, match="dloss"):
+            losses.xent_step(h3, w, y, dloss=dloss.view(bad), **more)
+        with pytest.raises(ValueError, match="lse"):
+            losses.xent_backward(h3, w, y, each.lse.view(bad), dloss=dloss, **more)
+        with pytest.raises(ValueError, match="teacher_ids"):
+            distill(ids=ids.view(*bad, K))
+        with pytest.raises(ValueError, match="teacher_logits"):
+            distill(logits=logits.view(*bad, K))
+    for rows in ((B, S), (S, B), (2, 2, S)):
+        check(distill(y.view(rows), ids.view(*rows, K), logits.view(*rows, K), h), r, torch.bfloat16)
+        check(distill(y.view(rows), ids, logits.view(*rows, K), h), r, torch.bfloat16)
+    with pytest.raises(ValueError, match="teacher_logits"):
+        distill(y, ids.view(B, S, K), logits.view(S, B, K), h)
+    with pytest.raises(ValueError, match="teacher_ids"):
+        distill(y.view(B, S), ids.view(S, B, K), logits, h)
+    with pytest.raises(ValueError, match="teacher_logits"):
+        distill(logits=logits.t().contiguous())
+    with pytest.raises(ValueError, match="teacher_logits"):
+        distill(logits=logits.view(B, S, K).transpose(1, 2).contiguous())
+    with pytest.raises(ValueError, match="teacher_ids"):
+        distill(ids=ids.t().contiguous())

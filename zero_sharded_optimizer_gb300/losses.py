@@ -12,6 +12,9 @@ at ``zero_head_loss_t``). Each comes as
 
 ``hidden`` is a [T, D] (or [..., D]) and ``weight`` a [V, D] CUDA tensor, both
 float32 or both bfloat16, with adjacent elements in a row and any row stride.
+What goes with the rows -- labels, the teacher's entries, ``dloss``, ``lse`` -- has
+hidden's leading dimensions or the rows in one dimension; beside a [T, D]
+``hidden`` it may have any leading dimensions, the same for all.
 ``dhidden`` and ``dweight`` may be given as outputs -- for ``dweight`` typically
 the head's view into a rank's flat gradient buffer, which the ZeRO step then
 reads -- and are allocated otherwise; ``accumulate`` adds to ``dweight``.
@@ -117,6 +120,10 @@ class _Call:
         V = weight2.shape[0]
         self.T, self.V, self.D = T, V, D
         self.shape = hidden.shape
+        self.lead = hidden.shape[:-1]            # the rows' dimensions
+        self.order = None                        # those longer than one, where they are several
+        if len(self.lead) > 1:
+            self.agree(self.lead, "hidden")
         self.stream = _named(stream, self.device)
         self.distill = teacher is not None
         self.labels = labels is not None
@@ -125,7 +132,7 @@ class _Call:
         self.made = []                           # its results
         y = None
         if labels is not None:
-            y = _vector(labels, "labels", torch.int64, T, self.device)
+            y = self.vector(labels, "labels", torch.int64)
         elif teacher is None:
             raise TypeError("labels must be a torch.int64 CUDA tensor")
         # the fields in order: up to ignore_index
@@ -137,15 +144,36 @@ class _Call:
             if not isinstance(ids, torch.Tensor) or ids.dim() < 2:
                 raise ValueError("teacher_ids must have at least 2 dimensions")
             K = ids.shape[-1]
-            p.teacher_ids = _vector(ids, "teacher_ids", torch.int64, T * K, self.device)
+            p.teacher_ids = self.vector(ids, "teacher_ids", torch.int64, K)
             self.keep += [ids, logits]
             if isinstance(logits, torch.Tensor) and logits.is_cuda and logits.dtype == torch.bfloat16:
                 with self.on_stream():
                     logits = logits.float()
             self.wide = logits               # held until the call is queued
-            p.teacher_logits = _vector(logits, "teacher_logits", torch.float32, T * K, self.device)
+            p.teacher_logits = self.vector(logits, "teacher_logits", torch.float32, K)
             p.teacher_k = K
             p.temperature, p.alpha = float(temperature), float(alpha)
+
+    def agree(self, rows, what):
+        """Checks that rows of dimensions ``rows`` come in the order of the others': one dimension
+        (beside such of one element) agrees with every other form, several only with the same."""
+        long = [n for n in rows if n != 1]
+        if len(long) > 1:
+            if self.order is not None and long != self.order:
+                raise ValueError(f"{what}'s rows have the dimensions {tuple(rows)}, others' {tuple(self.order)}")
+            self.order = long
+
+    def vector(self, t, what: str, dtype, last: int | None = None) -> int:
+        """The address of contiguous elements, one (or ``last``) for each row."""
+        address = _vector(t, what, dtype, self.T if last is None else self.T * last, self.device)
+        rows = t.shape
+        if last is not None:
+            if rows[-1:] != (last,):
+                raise ValueError(f"{what} has shape {tuple(rows)}, expected {last} entries for each row")
+            rows = rows[:-1]
+        if rows != self.lead:
+            self.agree(rows, what)
+        return address
 
     def on_stream(self):
         """Where the call's own work is queued and its memory is taken."""
@@ -162,17 +190,17 @@ class _Call:
 
     def statistics(self, lse, lse_tau):
         """The forward pass's, for a backward pass."""
-        T, p = self.T, self.p
+        p = self.p
         if self.labels:
-            p.lse = _vector(lse, "lse", torch.float32, T, self.device)
+            p.lse = self.vector(lse, "lse", torch.float32)
         if self.distill:
-            p.lse_tau = _vector(lse_tau, "lse_tau", torch.float32, T, self.device)
+            p.lse_tau = self.vector(lse_tau, "lse_tau", torch.float32)
         self.keep += [lse, lse_tau]
 
     def losses(self):
         """loss, reduced, lse, lse_tau, to be written."""
         p, T = self.p, self.T
-        loss = self.new(self.shape[:-1])
+        loss = self.new(self.lead)
         p.loss = loss.data_ptr()
         reduced = lse = lse_tau = None
         if not self.none:
@@ -193,7 +221,8 @@ class _Call:
         if accumulate:
             p.accumulate = 1
         if dloss is not None:
-            p.dloss = _vector(dloss, "dloss", torch.float32, self.T if self.none else 1, self.device)
+            p.dloss = (self.vector(dloss, "dloss", torch.float32) if self.none else
+                       _vector(dloss, "dloss", torch.float32, 1, self.device))
             self.keep.append(dloss)
         if dhidden is None:
             dhidden = self.new(self.shape, self.dtype)
