@@ -579,8 +579,8 @@ int zero_distill_workspace_bytes(const zero_head_loss_t *p, int64_t *bytes);
  * inputs once; the same bits. Everything is queued on `stream`.
  * Errors: EINVAL (sizes, strides below D, precision or reduction, a NULL
  * input or output, teacher_k, temperature, alpha or grad_scale out of range,
- * teacher fields given to zero_xent_*, neither gradient asked for, a workspace
- * that is too small, an output or the workspace overlapping another buffer),
+ * teacher fields given to zero_xent_*, neither gradient asked for (T > 0), a
+ * workspace that is too small, an output or the workspace overlapping another buffer),
  * EALIGN (a pointer not aligned to its element, a workspace not to 256 bytes),
  * ECUDA. */
 int zero_xent_forward(const zero_head_loss_t *p, zero_stream_t stream);

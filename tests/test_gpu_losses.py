@@ -147,6 +147,21 @@ def test_no_rows(losses, cuda, kind):
 
 
 @pytest.mark.parametrize("kind", TYPES)
+def test_no_rows_and_a_weight_that_is_not_trained(losses, cuda, kind):
+    """The gradient of the hidden states alone, of an empty batch."""
+    dt = TYPES[kind]
+    h = torch.empty(0, 40, dtype=dt, device=cuda, requires_grad=True)
+    w = torch.ones(300, 40, dtype=dt, device=cuda)
+    y = torch.empty(0, dtype=torch.int64, device=cuda)
+    ids, logits = torch.empty(0, 3, dtype=torch.int64, device=cuda), torch.empty(0, 3, device=cuda)
+    for loss in (losses.linear_cross_entropy(h, w, y), losses.linear_distillation(h, w, ids, logits, 2.0)):
+        got, = torch.autograd.grad(loss, h)
+        assert float(loss.detach()) == 0.0 and got.shape == (0, 40)
+    got = losses.xent_step(h.detach(), w, y, dweight=False)
+    assert got.dhidden.shape == (0, 40) and got.dweight is None and float(got.reduced) == 0.0
+
+
+@pytest.mark.parametrize("kind", TYPES)
 def test_a_row_that_is_not_finite_shows(losses, cuda, kind):
     """A NaN in a row with a target makes that row's loss NaN, and no other's."""
     dt = TYPES[kind]

@@ -96,6 +96,15 @@ def test_misaligned_pointers(abi, change, text):
     refused(abi, "xent", "step", problem(abi, **change), abi.ZERO_EALIGN, text)
 
 
+def test_an_empty_dhidden_may_be_null(abi):
+    """Without rows dhidden has no elements: a backward call for it alone has nothing to do, a
+    step needs what a forward call does."""
+    changes = dict(T=0, dhidden=None, dweight=None, workspace_bytes=1000)
+    p = problem(abi, **changes)
+    assert abi.raw_call("zero_xent_backward", ctypes.byref(p), None) == abi.ZERO_OK
+    refused(abi, "xent", "step", p, abi.ZERO_EINVAL, f"{abi.zero_xent_workspace_bytes(p)} are needed")
+
+
 def test_null_problem_and_output(abi):
     for kind in ("xent", "distill"):
         for name in ("forward", "backward", "step"):

@@ -127,7 +127,7 @@ int check_buffers(const zero_head_loss_t* p, bool distill, int pass) {
     if (reduce && (e = check_pointer(p->reduced, 1, 4, "reduced"))) return e;
   }
   if (pass & kBackward) {
-    if (!p->dhidden && !p->dweight) return set_error(ZERO_EINVAL, "neither dhidden nor dweight is given");
+    if (!p->dhidden && !p->dweight && T > 0) return set_error(ZERO_EINVAL, "neither dhidden nor dweight is given");
     if ((e = check_pointer(p->dhidden, 0, es, "dhidden"))) return e;
     if ((e = check_pointer(p->dweight, 0, es, "dweight"))) return e;
     if ((e = check_pointer(p->dloss, 0, 4, "dloss"))) return e;
@@ -368,6 +368,8 @@ int workspace_bytes(const zero_head_loss_t* p, bool distill, int64_t* bytes) {
 int run(const zero_head_loss_t* p, bool distill, int pass, cudaStream_t s) {
   if (int e = check_sizes(p, distill)) return e;
   if (int e = check_buffers(p, distill, pass)) return e;
+  if (!p->dhidden && !p->dweight) pass &= ~kBackward;  // without rows: an empty dhidden, if any
+  if (!pass) return ZERO_OK;
   if (reinterpret_cast<uintptr_t>(p->workspace) % 256)
     return set_error(ZERO_EALIGN, "the workspace is not aligned to 256 bytes");
   Args a;
