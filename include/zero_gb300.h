@@ -543,7 +543,7 @@ typedef struct zero_head_loss {
   const float *teacher_logits;  /* [T][teacher_k]                              */
   int64_t teacher_k;            /* 1 .. ZERO_DISTILL_MAX_K                     */
   double temperature;           /* tau: finite, > 0                            */
-  double alpha;                 /* in [0, 1]; 1 when labels is NULL            */
+  double alpha;                 /* in [0, 1]; 1 when labels is NULL (T > 0)    */
   /* Written by the forward pass, read by the backward pass (lse, lse_tau). */
   float *loss;            /* [T]; 0 for an empty row                           */
   float *lse;             /* [T]: lse_t; needed with labels                    */

@@ -162,6 +162,17 @@ def test_no_rows_and_a_weight_that_is_not_trained(losses, cuda, kind):
 
 
 @pytest.mark.parametrize("kind", TYPES)
+def test_no_rows_of_distillation_mixed_with_labels(losses, cuda, kind):
+    dt = TYPES[kind]
+    h, w = torch.empty(0, 40, dtype=dt, device=cuda), torch.ones(300, 40, dtype=dt, device=cuda)
+    y = torch.empty(0, dtype=torch.int64, device=cuda)
+    ids, logits = torch.empty(0, 3, dtype=torch.int64, device=cuda), torch.empty(0, 3, device=cuda)
+    got = losses.distill_step(h, w, ids, logits, temperature=2.0, labels=y, alpha=0.5)
+    assert float(got.reduced) == 0.0 and got.loss.shape == (0,) and got.dhidden.shape == (0, 40)
+    assert not got.dweight.any()
+
+
+@pytest.mark.parametrize("kind", TYPES)
 def test_a_row_that_is_not_finite_shows(losses, cuda, kind):
     """A NaN in a row with a target makes that row's loss NaN, and no other's."""
     dt = TYPES[kind]

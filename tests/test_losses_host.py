@@ -105,6 +105,12 @@ def test_an_empty_dhidden_may_be_null(abi):
     refused(abi, "xent", "step", p, abi.ZERO_EINVAL, f"{abi.zero_xent_workspace_bytes(p)} are needed")
 
 
+def test_empty_labels_may_be_null(abi):
+    """Without rows the labels have no elements either, whatever alpha."""
+    p = problem(abi, True, T=0, labels=None, workspace_bytes=1000)
+    refused(abi, "distill", "step", p, abi.ZERO_EINVAL, "are needed")
+
+
 def test_null_problem_and_output(abi):
     for kind in ("xent", "distill"):
         for name in ("forward", "backward", "step"):

@@ -92,7 +92,7 @@ int check_sizes(const zero_head_loss_t* p, bool distill) {
         !std::isfinite(float(1.0 / p->temperature)))
       return set_error(ZERO_EINVAL, "temperature must be finite and > 0");
     if (!(p->alpha >= 0.0 && p->alpha <= 1.0)) return set_error(ZERO_EINVAL, "alpha must lie in [0, 1]");
-    if (!p->labels && p->alpha != 1.0)
+    if (!p->labels && p->alpha != 1.0 && p->T > 0)
       return set_error(ZERO_EINVAL, "without labels alpha must be 1");
   } else if (p->teacher_ids || p->teacher_logits || p->teacher_k || p->lse_tau) {
     return set_error(ZERO_EINVAL, "teacher fields are set: use the zero_distill calls");
