@@ -111,6 +111,15 @@ def test_empty_labels_may_be_null(abi):
     refused(abi, "distill", "step", p, abi.ZERO_EINVAL, "are needed")
 
 
+def test_empty_buffers_overlap_nothing(abi):
+    """Without rows, a pointer into another buffer (an arena's) shares no byte with it."""
+    for change in (dict(labels=(8 << 20) + 64), dict(loss=(8 << 20) + 64), dict(lse=(9 << 20) + 64)):
+        refused(abi, "xent", "step", problem(abi, T=0, workspace_bytes=1000, **change), abi.ZERO_EINVAL, "are needed")
+    change = dict(teacher_ids=(8 << 20) + 64, teacher_logits=(8 << 20) + 64)
+    refused(abi, "distill", "step", problem(abi, True, T=0, workspace_bytes=1000, **change), abi.ZERO_EINVAL,
+            "are needed")
+
+
 def test_null_problem_and_output(abi):
     for kind in ("xent", "distill"):
         for name in ("forward", "backward", "step"):

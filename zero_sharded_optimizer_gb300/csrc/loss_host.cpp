@@ -48,7 +48,7 @@ struct Span {
 // Whether two buffers share a byte. Rows of equal stride are compared by their
 // phase, so that column blocks of one wider buffer pass.
 bool overlap(const Span& x, const Span& y) {
-  if (!x.p || !y.p || !x.rows || !y.rows) return false;
+  if (!x.p || !y.p || !x.rows || !y.rows || !x.bytes || !y.bytes) return false;
   const uintptr_t a = reinterpret_cast<uintptr_t>(x.p), b = reinterpret_cast<uintptr_t>(y.p);
   const uintptr_t a1 = a + uintptr_t((x.rows - 1) * x.stride + x.bytes);
   const uintptr_t b1 = b + uintptr_t((y.rows - 1) * y.stride + y.bytes);
