@@ -236,6 +236,31 @@ def test_teacher_entries_at_their_edges(losses, cuda, kind):
         check(got, r, dt, f"{kind} {alpha}")
 
 
+@pytest.mark.parametrize("tau", [0.5, 0.25, 1.0])
+@pytest.mark.parametrize("logits_type", TYPES)
+@pytest.mark.parametrize("kind", TYPES)
+def test_teacher_logits_at_the_end_of_the_range(losses, cuda, kind, logits_type, tau):
+    """Logits near the type's lowest and largest value, which the division by a temperature
+    below one takes out of fp32: they are present, and only -inf is absent."""
+    dt, lt = TYPES[kind], TYPES[logits_type]
+    T, V, D, K = 12, 300, 64, 5
+    h, w, y, g = inputs(T, V, D, dt, 22, cuda)
+    ids, logits = teacher(T, V, K, g, cuda)
+    logits = logits.to(lt)
+    lowest = torch.finfo(lt).min
+    logits[0] = lowest                            # uniform
+    logits[1, 1:] = lowest                        # one entry has everything
+    logits[2], logits[2, 0] = lowest, -math.inf   # four, uniform
+    logits[3] = -lowest                           # uniform
+    logits[4], logits[4, :2] = lowest, -lowest    # two share it
+    logits[5] = -math.inf                         # absent
+    logits[6, 1:] = 0.9 * lowest
+    for labels, alpha in [(y, 0.5), (None, 1.0)]:
+        r = reference(h, w, labels, ids, logits, tau=tau, alpha=alpha, reduction="sum")
+        got = losses.distill_step(h, w, ids, logits, temperature=tau, labels=labels, alpha=alpha, reduction="sum")
+        check(got, r, dt, f"{kind} {alpha}", parts=2)
+
+
 def test_distill_many_entries(losses, cuda):
     T, V, D, K = 9, 5000, 64, 1024
     h, w, y, g = inputs(T, V, D, torch.bfloat16, 2, cuda)

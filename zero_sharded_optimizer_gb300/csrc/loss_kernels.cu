@@ -72,7 +72,7 @@ __device__ __forceinline__ int prepare_teacher(const Args& a, int64_t t, int n4,
   float top = -INFINITY;
   for (int k = lane; k < K; k += 32) {
     const int64_t v = a.teacher_ids[t * K + k];
-    const float u = a.teacher_logits[t * K + k] / float(a.tau);
+    const float u = a.teacher_logits[t * K + k];
     const bool there = v >= 0 && v < a.V && u != -INFINITY;
     id[k] = there ? int32_t(v) : kNoId;  // (ids end below kNoId - 1, so that one can be added)
     c[k] = u;
@@ -89,7 +89,9 @@ __device__ __forceinline__ int prepare_teacher(const Args& a, int64_t t, int n4,
   top = warp_max(top);
   float sum = 0.0f;
   for (int k = lane; k < K; k += 32) {
-    const float e = id[k] == kNoId ? 0.0f : expf(c[k] - top);
+    // From the maximum before the division: a temperature below one takes large
+    // finite logits past fp32's range.
+    const float e = id[k] == kNoId ? 0.0f : expf((c[k] - top) / float(a.tau));
     c[k] = e;
     sum += e;
   }
