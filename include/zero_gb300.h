@@ -507,7 +507,13 @@ int ddp_allreduce_mean_from_host_h(zero_ddp_host_t *h, const void *const *host_g
  * both gradients are fp32 or wider; in ZERO_BF16_MIXED the gradient of the
  * logits is rounded to bf16 once, as the operand of the two gradient products.
  * Every sum has a fixed order: equal inputs give equal bits, and a step the
- * bits of a forward and a backward call. */
+ * bits of a forward and a backward call.
+ *
+ * Failure: a wait inside the matrix kernels that lasts ten seconds (none does
+ * under normal running) gives up, and the kernels end. What the call writes is
+ * NaN then: the losses and log-sum-exps of all rows that are not empty, reduced,
+ * those rows of dhidden, and all of dweight. The call has returned ZERO_OK by
+ * that time, and the context stays usable. */
 
 /* Reduction of the rows' losses, and what dloss is a gradient of. */
 enum {
@@ -629,6 +635,13 @@ const char *zero_last_error(void);
  * count <= 0 clears a pending injection. Other threads are unaffected.
  * Returns ZERO_OK. */
 int zero_debug_fail_host_allocs(int32_t count);
+
+/* Failure injection for callers' tests: in the calling thread's next vocabulary
+ * loss call the matrix kernels of the forward pass (passes 1), the backward pass
+ * (2) or both (3) wait for a word that nothing sets, and give up after limit_ns
+ * (at most ten seconds, which is also the limit of every other call): the
+ * failure stated above. passes 0 clears it. EINVAL: out of range. */
+int zero_debug_withhold_head_loss(int32_t passes, int64_t limit_ns);
 
 #ifdef __cplusplus
 }

@@ -462,6 +462,65 @@ def test_the_default_stream_by_its_handles(losses, cuda):
         check(got, reference(h, w, y), torch.bfloat16)
 
 
+@pytest.mark.parametrize("T,V,D", [(90, 700, 64), (600, 9000, 72)])
+@pytest.mark.parametrize("op", ["xent", "distill"])
+@pytest.mark.parametrize("kind", TYPES)
+def test_a_wait_that_runs_out(losses, cuda, kind, op, T, V, D):
+    """A word that nothing sets: the waits give up at their limit, everything that the call
+    writes is NaN (but what belongs to empty rows), and the next call is right."""
+    import time
+    abi, dt = losses.abi, TYPES[kind]
+    h, w, y, g = inputs(T, V, D, dt, 71, cuda, masked=0.2)
+    ids, logits = teacher(T, V, 5, g, cuda)
+    ids[y == IGNORE] = -1
+    there = y != IGNORE
+    args = (h, w, y) if op == "xent" else (h, w, ids, logits)
+    more = {} if op == "xent" else dict(temperature=2.0, labels=y, alpha=0.5)
+    forward, backward, step = (getattr(losses, f"{op}_{name}") for name in ("forward", "backward", "step"))
+
+    def nan(x):
+        return bool(torch.isnan(x).all())
+
+    def withheld(passes, call, *a, **m):
+        torch.cuda.synchronize()
+        abi.zero_debug_withhold_head_loss(passes, 50_000_000)
+        begin = time.perf_counter()
+        r = call(*a, **m)
+        torch.cuda.synchronize()
+        took = time.perf_counter() - begin
+        assert 0.05 <= took < 10.0, took
+        if r.loss is not None:
+            assert nan(r.loss[there]) and nan(r.reduced) and not r.loss[~there].any()
+            assert nan(r.lse[there]) and (r.lse_tau is None or nan(r.lse_tau[there]))
+        if r.dhidden is not None:
+            assert nan(r.dhidden[there]) and not r.dhidden[~there].any()
+        assert r.dweight is None or nan(r.dweight)
+        return r
+
+    good = step(*args, **more)
+    stats = (good.lse,) if op == "xent" else (good.lse, good.lse_tau)
+    failed = withheld(1, forward, *args, **more)
+    # a backward call from it shows it
+    bad = backward(*args, *((failed.lse,) if op == "xent" else (failed.lse, failed.lse_tau)), **more)
+    assert nan(bad.dhidden[there]) and nan(bad.dweight)
+    for passes in (1, 2, 3):
+        withheld(passes, step, *args, **more)
+    withheld(2, step, *args, dhidden=False, **more)
+    withheld(2, backward, *args, *stats, **more)
+    withheld(2, backward, *args, *stats, dhidden=False, **more)
+    withheld(2, backward, *args, *stats, dweight=False, **more)
+    for pad, accumulate in ((0, True), (1, False), (1, True)):
+        dw, buf = empty_matrix(V, D, dt, cuda, pad)
+        dw.fill_(1.0)
+        withheld(2, step, *args, dweight=dw, accumulate=accumulate, **more)
+        gaps_untouched(buf, V, D, pad)
+    abi.zero_debug_withhold_head_loss(3, 50_000_000)
+    abi.zero_debug_withhold_head_loss(0)       # cleared
+    again = step(*args, **more)
+    for a, b in zip(again, good):
+        assert (a is None and b is None) or torch.equal(a, b)
+
+
 @pytest.mark.parametrize("kind", TYPES)
 def test_gradient_against_differences(losses, cuda, kind):
     """The losses' own central difference along a direction, against the

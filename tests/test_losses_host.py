@@ -120,6 +120,13 @@ def test_empty_buffers_overlap_nothing(abi):
             "are needed")
 
 
+def test_withholding_is_checked(abi):
+    for passes, limit in ((-1, 1), (4, 1), (1, 0), (1, -5), (1, 10_000_000_001)):
+        assert abi.raw_call("zero_debug_withhold_head_loss", passes, ctypes.c_int64(limit)) == abi.ZERO_EINVAL
+    abi.zero_debug_withhold_head_loss(3, 1)
+    abi.zero_debug_withhold_head_loss(0)
+
+
 def test_null_problem_and_output(abi):
     for kind in ("xent", "distill"):
         for name in ("forward", "backward", "step"):

@@ -82,6 +82,7 @@ _SIGNATURES = {
                                                     _i64, _vp, _vp, _vp]),
     "zero_ddp_host_create": (ctypes.c_int, [_P(_vp)]),
     "zero_debug_fail_host_allocs": (ctypes.c_int, [_i32]),
+    "zero_debug_withhold_head_loss": (ctypes.c_int, [_i32, _i64]),
     "zero_ddp_host_reset": (ctypes.c_int, [_vp]),
     "zero_ddp_host_free": (ctypes.c_int, [_vp]),
     "ddp_allreduce_mean_from_host_h": (ctypes.c_int, [_vp, _P(_vp), _P(_vp), _i64, _i32, _i32,
@@ -634,6 +635,12 @@ def zero_debug_fail_host_allocs(count: int) -> None:
     """Failure injection: the calling thread's next ``count`` handle
     allocations fail with ZERO_ENOMEM (count <= 0 clears it)."""
     _check(_lib.zero_debug_fail_host_allocs(count), "zero_debug_fail_host_allocs")
+
+
+def zero_debug_withhold_head_loss(passes: int, limit_ns: int = 10_000_000_000) -> None:
+    """Failure injection: in the calling thread's next vocabulary loss call the forward pass (1),
+    the backward pass (2) or both (3) wait in vain and give up after ``limit_ns``."""
+    _check(_lib.zero_debug_withhold_head_loss(passes, limit_ns), "zero_debug_withhold_head_loss")
 
 
 def raw_call(name: str, *args) -> int:

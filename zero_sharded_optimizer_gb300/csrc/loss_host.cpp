@@ -31,6 +31,17 @@ constexpr int64_t kPieceBytes = int64_t(40) << 20;
 // where many rows' errors even out.
 constexpr int64_t kFineRows = 256;
 
+// A wait inside the matrix kernel gives up after this long; under normal running
+// none is longer than a few tiles.
+constexpr int64_t kWaitLimitNs = int64_t(10) * 1000 * 1000 * 1000;
+
+// Failure injection for this thread's next call (zero_debug_withhold_head_loss).
+struct Withheld {
+  int32_t passes = 0;
+  int64_t limit_ns = kWaitLimitNs;
+};
+thread_local Withheld g_withheld;
+
 int64_t round_up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
 
 int elem_size(int32_t precision) { return precision == ZERO_FP32 ? 4 : 2; }
@@ -269,9 +280,10 @@ int plan(const zero_head_loss_t* p, bool distill, int pass, Args* a, __nv_bfloat
   }
   // The words that begin as zero.
   const int64_t tiles = pass & kBackward ? a->splits * (a->Tp / zl::kTileM) * ((a->D + 255) / 256) : 0;
-  a->zeros = 2 + 2 * pieces + tiles;
+  a->zeros = 3 + 2 * pieces + tiles;
   a->counters = w.take<int32_t>(a->zeros);
-  a->formed = reinterpret_cast<uint32_t*>(a->counters + 2);
+  a->never = reinterpret_cast<uint32_t*>(a->counters + 2);
+  a->formed = a->never + 1;
   a->used = a->formed + pieces;
   a->added = a->used + pieces;
   // The forward pass's arrays and the backward pass's lie over one another.
@@ -388,6 +400,9 @@ int run(const zero_head_loss_t* p, bool distill, int pass, cudaStream_t s) {
   if (q == cudaSuccess) q = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device);
   if (q != cudaSuccess)
     return set_error(ZERO_ECUDA, "device: %s (%s)", cudaGetErrorString(q), cudaGetErrorName(q));
+  const Withheld withheld = g_withheld;
+  g_withheld = Withheld{};
+  program.wait_limit_ns = uint64_t(withheld.limit_ns);
   const char* what = "rows";
   bool rows_packed = false;
   cudaError_t e = zl::launch_rows(a, packed != nullptr, &rows_packed, s);
@@ -400,14 +415,17 @@ int run(const zero_head_loss_t* p, bool distill, int pass, cudaStream_t s) {
   if (pass & kForward) {
     program.forward = 1;
     program.counter = a.counters;
+    program.withheld = withheld.passes & kForward ? a.never : nullptr;
     next("logits", [&] { return zl::launch_products(a, program, device, sms, s); });
     next("losses", [&] { return zl::launch_losses(a, s); });
   }
   if (pass & kBackward) {
     program.forward = 0;
     program.counter = a.counters + 1;
+    program.withheld = withheld.passes & kBackward ? a.never : nullptr;
     next("the gradients", [&] { return zl::launch_products(a, program, device, sms, s); });
     if (p->dhidden && p->T) next("dhidden", [&] { return zl::launch_dhidden_out(a, s); });
+    else next("the mark", [&] { return zl::launch_mark(a, s); });
   }
   if (e != cudaSuccess)
     return set_error(ZERO_ECUDA, "%s: %s (%s)", what, cudaGetErrorString(e), cudaGetErrorName(e));
@@ -441,6 +459,13 @@ int zero_distill_backward(const zero_head_loss_t* p, zero_stream_t stream) {
 }
 int zero_distill_step(const zero_head_loss_t* p, zero_stream_t stream) {
   return run(p, true, kForward | kBackward, stream);
+}
+int zero_debug_withhold_head_loss(int32_t passes, int64_t limit_ns) {
+  if (passes < 0 || passes > 3) return set_error(ZERO_EINVAL, "passes=%d is not in [0, 3]", passes);
+  if (limit_ns < 1 || limit_ns > kWaitLimitNs)
+    return set_error(ZERO_EINVAL, "limit_ns=%lld is not in [1, %lld]", (long long)limit_ns, (long long)kWaitLimitNs);
+  g_withheld = Withheld{passes, limit_ns};
+  return ZERO_OK;
 }
 
 }  // extern "C"

@@ -28,7 +28,7 @@ constexpr int kLossBlocks = 608; // most blocks of the losses' kernel
 struct Head {
   int32_t rows;    // rows with a target (the compact rows)
   int32_t ticket;  // blocks of the reduction that are done
-  int32_t fault;   // a wait of the matrix kernel ran out: the results are not valid
+  int32_t fault;   // a wait of the matrix kernel ran out: what the call writes becomes NaN
   float factor;    // of both gradients, the same for every row
 };
 
@@ -88,6 +88,7 @@ struct Args {
   float2* stats;          // [2 tiles][Tp] half a tile's (m, sum of 2^(z log2(e) - m))
   float2* stats_tau;      // [2 tiles][Tp] of z / tau
   int32_t* counters;      // [2] units handed out, forward and backward
+  uint32_t* never;        // stays zero
   uint32_t* formed;       // [pieces] finished units of a piece's gradient
   uint32_t* used;         // [pieces] finished units of the products with it
   uint32_t* added;        // [tiles of dh] finished units of a tile
@@ -111,6 +112,8 @@ struct Program {
   int32_t pieces;
   int32_t weight_tma;  // dweight can be written by TMA
   int32_t* counter;    // units handed out
+  uint64_t wait_limit_ns;    // after which a wait gives up
+  const uint32_t* withheld;  // NULL, or a word that the kernel waits for (failure injection)
 };
 
 // Prepares and numbers the rows. `packed`: they are packed too (a few rows of
@@ -119,7 +122,10 @@ cudaError_t launch_rows(const Args& a, bool pack_weight, bool* packed, cudaStrea
 // Rows with a target side by side, and the weight's rows to `weight` (NULL: read in place).
 cudaError_t launch_pack(const Args& a, __nv_bfloat16* weight, cudaStream_t s);
 cudaError_t launch_losses(const Args& a, cudaStream_t s);
+// dhidden from its sums; a call whose waits ran out is marked.
 cudaError_t launch_dhidden_out(const Args& a, cudaStream_t s);
+// The mark alone, where there is no dhidden to write.
+cudaError_t launch_mark(const Args& a, cudaStream_t s);
 cudaError_t launch_products(const Args& a, const Program& prog, int device, int sms, cudaStream_t s);
 
 }  // namespace zl

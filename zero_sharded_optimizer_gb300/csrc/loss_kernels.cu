@@ -350,6 +350,33 @@ __global__ void __launch_bounds__(256) pack_kernel(const Args a, __nv_bfloat16* 
   pack_rows<F32>(a, a.head->rows, hidden_vector, first, step);
 }
 
+// Where a wait of the matrix kernel ran out, the call's results become NaN --
+// dweight, which may be half written, and a step's losses, which were formed
+// before the backward pass -- so that nothing goes on with them unnoticed.
+__device__ __noinline__ void mark_fault(const Args& a, bool f32, int64_t first, int64_t step) {
+  if (a.dweight) {
+    for (int64_t n = first; n < a.V * a.D; n += step) {
+      const int64_t at = n / a.D * a.dweight_stride + n % a.D;
+      if (f32) static_cast<float*>(a.dweight)[at] = NAN;
+      else static_cast<__nv_bfloat16*>(a.dweight)[at] = __float2bfloat16_rn(NAN);
+    }
+  }
+  if (!a.forward) return;
+  for (int64_t t = first; t < a.T; t += step) {
+    if (a.rowpos[t] < 0) continue;
+    a.loss[t] = NAN;
+    if (a.has_ce) a.lse[t] = NAN;
+    if (a.has_kd) a.lse_tau[t] = NAN;
+  }
+  if (first == 0 && a.reduction != ZERO_REDUCE_NONE) *a.reduced = NAN;
+}
+
+__global__ void __launch_bounds__(256) mark_kernel(const Args a) {
+  let_next_start();
+  wait_for_previous();
+  if (a.head->fault) mark_fault(a, a.planes == 3, int64_t(blockIdx.x) * 256 + threadIdx.x, int64_t(gridDim.x) * 256);
+}
+
 // The rows' sums over all pieces, with the common factor: a block takes
 // 256 / Lanes groups of four elements of a row at a time, each group's `Lanes`
 // threads share the parts that the sums are split in.
@@ -359,7 +386,8 @@ __global__ void __launch_bounds__(256) dhidden_out_kernel(const Args a) {
   __shared__ float4 part[Lanes][kGroups];
   let_next_start();
   wait_for_previous();
-  const float f = a.head->fault ? NAN : a.head->factor;
+  const bool fault = a.head->fault;
+  const float f = fault ? NAN : a.head->factor;
   const int group = threadIdx.x % kGroups, lane = threadIdx.x / kGroups;
   const int64_t wide = (a.D + 3) / 4;
   const int64_t stretches = (wide + kGroups - 1) / kGroups;  // of a row
@@ -414,6 +442,7 @@ __global__ void __launch_bounds__(256) dhidden_out_kernel(const Args a) {
       }
     }
   }
+  if (fault) mark_fault(a, F32, int64_t(blockIdx.x) * 256 + threadIdx.x, int64_t(gridDim.x) * 256);
 }
 
 // ------------------------------------------------------------------- losses --
@@ -494,10 +523,11 @@ __global__ void __launch_bounds__(256) losses_kernel(const Args a, int block_row
       if (f.x != 0.0f) loss += double(f.x) * lse;
       if (f.y != 0.0f) loss += double(f.y) * a.tau * lse_tau;
       loss -= part[r];
-      if (a.head->fault) loss = NAN;
+      const bool fault = a.head->fault;  // NaN in lse too: a backward call's gradients show it then
+      if (fault) loss = NAN;
       a.loss[t] = float(loss);
-      if (a.has_ce) a.lse[t] = float(lse);
-      if (a.has_kd) a.lse_tau[t] = float(lse_tau);
+      if (a.has_ce) a.lse[t] = fault ? NAN : float(lse);
+      if (a.has_kd) a.lse_tau[t] = fault ? NAN : float(lse_tau);
       mine += double(float(loss));
     }
     __syncthreads();
@@ -600,6 +630,10 @@ cudaError_t launch_losses(const Args& a, cudaStream_t s) {
   const int64_t blocks = (a.T + rows - 1) / rows;
   return launch(losses_kernel, unsigned(blocks < 1 ? 1 : blocks < kLossBlocks ? blocks : kLossBlocks), 256, 0, s,
                 true, a, rows);
+}
+
+cudaError_t launch_mark(const Args& a, cudaStream_t s) {
+  return launch(mark_kernel, 152, 256, 0, s, true, a);
 }
 
 cudaError_t launch_dhidden_out(const Args& a, cudaStream_t s) {

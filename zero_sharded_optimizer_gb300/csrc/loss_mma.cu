@@ -142,21 +142,20 @@ __device__ __forceinline__ bool barrier_try(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 
-// A wait gives up after ten seconds, or when another warp of the CTA has: the
-// kernel then ends without its results, the fault is kept in the workspace's
-// head and the losses become NaN.
-constexpr uint64_t kWaitLimitNs = 10ull * 1000 * 1000 * 1000;
-
+// A wait gives up after the program's limit, or when another warp of the CTA has:
+// the kernel then ends without its results, the fault is kept in the workspace's
+// head, and the call's last kernels set what it writes to NaN.
 struct Waiter {
   volatile uint32_t* given_up;  // shared
   Head* head;
+  const uint64_t& limit_ns;
   template <bool Cluster = false>
   __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity) const {
     if (barrier_try<Cluster>(bar, parity)) return true;
     const uint64_t begin = timer_ns();
     for (uint32_t n = 1;; ++n) {
       if (barrier_try<Cluster>(bar, parity)) return true;
-      if ((n & 1023) == 0 && (*given_up || timer_ns() - begin > kWaitLimitNs)) {
+      if ((n & 1023) == 0 && (*given_up || timer_ns() - begin > limit_ns)) {
         *given_up = 1;
         head->fault = 1;
         return false;
@@ -172,6 +171,7 @@ struct Waiter {
 struct Progress {
   volatile uint32_t* given_up;
   Head* head;
+  const uint64_t& limit_ns;
   __device__ __forceinline__ bool reached(const uint32_t* count, uint32_t target) const {
     uint64_t begin = 0;
     for (uint32_t n = 0;; ++n) {
@@ -180,7 +180,7 @@ struct Progress {
       if (x >= target) break;
       if (n == 0) begin = timer_ns();
       __nanosleep(100);
-      if ((n & 63) == 63 && (*given_up || timer_ns() - begin > kWaitLimitNs)) {
+      if ((n & 63) == 63 && (*given_up || timer_ns() - begin > limit_ns)) {
         *given_up = 1;
         head->fault = 1;
         return false;
@@ -877,8 +877,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tmem_slot;
   wait_for_previous();
   const int rows = a.head->rows;
-  const Waiter wait{given_up, a.head};
-  const Progress progress{given_up, a.head};
+  const Waiter wait{given_up, a.head, prog.wait_limit_ns};
+  const Progress progress{given_up, a.head, prog.wait_limit_ns};
   Unit u;
   // The ring's next entry. The epilogue warps give it back to the pair's first
   // CTA once the unit's first accumulator is full: by then the copies and the
@@ -907,7 +907,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         uint32_t phase = 0;
         bool ok = true;
         int formed = -1;  // the last piece known to be there
-        for (;;) {
+        if (prog.withheld) ok = progress.reached(prog.withheld, 1);
+        while (ok) {
           if (!(ok = next_unit()) || u.mode < 0) break;
           const bool a_mn = u.mode == kWeight, b_mn = u.mode == kWeight || u.mode == kHidden;
           if (b_mn && u.piece > formed) {
@@ -958,11 +959,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               }
             }
           }
-          if (!ok) break;
-        }
-        if (!ok) {  // let the copies in flight land before the CTA's memory goes
-          const uint64_t begin = timer_ns();
-          while (timer_ns() - begin < 2000000) __nanosleep(1000);
         }
       }
     } else if (warp == 1 && rank == 0) {
@@ -1187,6 +1183,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   __syncwarp();
   fence_before();
   __syncthreads();
+  if (*given_up) {  // let the copies and products in flight end before the CTA's memory goes
+    const uint64_t begin = timer_ns();
+    while (timer_ns() - begin < 2000000) __nanosleep(1000);
+  }
   cluster_sync();
   fence_after();
   if (warp == 1)
