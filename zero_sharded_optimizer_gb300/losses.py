@@ -33,14 +33,12 @@ uses the results; to order the two streams' work is left to the caller.
 
 from __future__ import annotations
 
-import contextlib
 from typing import NamedTuple
 
 import torch
 
 from . import abi
 
-_AS_IT_IS = contextlib.nullcontext()
 _REDUCE = {"none": abi.ZERO_REDUCE_NONE, "mean": abi.ZERO_REDUCE_MEAN, "sum": abi.ZERO_REDUCE_SUM}
 
 
@@ -147,7 +145,7 @@ class _Call:
             p.teacher_ids = self.vector(ids, "teacher_ids", torch.int64, K)
             self.keep += [ids, logits]
             if isinstance(logits, torch.Tensor) and logits.is_cuda and logits.dtype == torch.bfloat16:
-                with self.on_stream():
+                with torch.cuda.stream(self.stream):     # None: the current one
                     logits = logits.float()
             self.wide = logits               # held until the call is queued
             p.teacher_logits = self.vector(logits, "teacher_logits", torch.float32, K)
@@ -171,16 +169,14 @@ class _Call:
             if rows[-1:] != (last,):
                 raise ValueError(f"{what} has shape {tuple(rows)}, expected {last} entries for each row")
             rows = rows[:-1]
-        if rows != self.lead:
+        if len(rows) > 1 and rows != self.lead:
             self.agree(rows, what)
         return address
 
-    def on_stream(self):
-        """Where the call's own work is queued and its memory is taken."""
-        return _AS_IT_IS if self.stream is None else torch.cuda.stream(self.stream)
-
     def empty(self, shape, dtype):
-        with self.on_stream():
+        if self.stream is None:
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        with torch.cuda.stream(self.stream):
             return torch.empty(shape, dtype=dtype, device=self.device)
 
     def new(self, shape, dtype=torch.float32):
