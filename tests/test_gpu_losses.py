@@ -622,6 +622,15 @@ def test_few_rows_lose_nothing_to_the_logits_gradient(losses, cuda, op, T, V, D)
     check(got, r, torch.bfloat16, f"{op} {T}x{V}x{D}", parts=2)
 
 
+@pytest.mark.parametrize("T", [1023, 1024, 1025, 2049])
+def test_around_the_rows_that_one_kernel_prepares(losses, cuda, T):
+    V, D = 300, 40
+    h, w, y, g = inputs(T, V, D, torch.bfloat16, 72, cuda, masked=0.3)
+    bad = h.clone()
+    bad[y == IGNORE] = math.nan
+    check(losses.xent_step(bad, w, y), reference(bad, w, y), torch.bfloat16)
+
+
 def test_many_rows_few_of_them_labelled(losses, cuda):
     """More rows than the numbering takes at a time, most without a label."""
     T, V, D = 40_003, 300, 24

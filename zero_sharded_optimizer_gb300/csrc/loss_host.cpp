@@ -404,14 +404,13 @@ int run(const zero_head_loss_t* p, bool distill, int pass, cudaStream_t s) {
   g_withheld = Withheld{};
   program.wait_limit_ns = uint64_t(withheld.limit_ns);
   const char* what = "rows";
-  bool rows_packed = false;
-  cudaError_t e = zl::launch_rows(a, packed != nullptr, &rows_packed, s);
+  cudaError_t e = zl::launch_rows(a, s);
   auto next = [&](const char* name, auto&& launch) {
     if (e != cudaSuccess) return;
     what = name;
     e = launch();
   };
-  if (!rows_packed) next("packing", [&] { return zl::launch_pack(a, packed, s); });
+  next("packing", [&] { return zl::launch_pack(a, packed, s); });
   if (pass & kForward) {
     program.forward = 1;
     program.counter = a.counters;

@@ -116,9 +116,8 @@ struct Program {
   const uint32_t* withheld;  // NULL, or a word that the kernel waits for (failure injection)
 };
 
-// Prepares and numbers the rows. `packed`: they are packed too (a few rows of
-// bf16, if the weight need not be packed).
-cudaError_t launch_rows(const Args& a, bool pack_weight, bool* packed, cudaStream_t s);
+// Prepares and numbers the rows.
+cudaError_t launch_rows(const Args& a, cudaStream_t s);
 // Rows with a target side by side, and the weight's rows to `weight` (NULL: read in place).
 cudaError_t launch_pack(const Args& a, __nv_bfloat16* weight, cudaStream_t s);
 cudaError_t launch_losses(const Args& a, cudaStream_t s);

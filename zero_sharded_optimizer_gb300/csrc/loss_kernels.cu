@@ -268,9 +268,9 @@ __device__ __forceinline__ void pack_rows(const Args& a, int32_t rows, bool vect
 
 // One block: numbers the rows that have a target, in order, up to 16 times
 // 1024 rows at a time. With `Prepare` (few rows, labels alone) it prepares them
-// first, with `Pack` (very few, bf16) it also packs them: a launch saved each.
-template <bool Prepare, bool Pack>
-__global__ void __launch_bounds__(1024) number_rows_kernel(const Args a, bool vector) {
+// first: a launch saved.
+template <bool Prepare>
+__global__ void __launch_bounds__(1024) number_rows_kernel(const Args a) {
   __shared__ int32_t before[16][32], total[16];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   let_next_start();
@@ -324,10 +324,6 @@ __global__ void __launch_bounds__(1024) number_rows_kernel(const Args a, bool ve
     if (a.reduction == ZERO_REDUCE_MEAN) f /= double(max(1, base));
     if (a.reduction != ZERO_REDUCE_NONE && a.dloss) f *= double(*a.dloss);
     *a.head = Head{base, 0, 0, float(f)};
-  }
-  if (Pack) {
-    __syncthreads();
-    pack_rows<false>(a, base, vector, threadIdx.x, 1024);
   }
 }
 
@@ -590,13 +586,14 @@ bool aligned16(const void* p, int64_t stride_bytes) {
 
 }  // namespace
 
-cudaError_t launch_rows(const Args& a, bool pack_weight, bool* packed, cudaStream_t s) {
-  // One kernel instead of two or three while its single block is no longer than
-  // their launches (one token, loss alone: 38.6 us; two 39.6, three 40.6).
-  const bool vector = aligned16(a.hidden, a.hidden_stride * 2);
-  *packed = a.K == 0 && a.T <= 16 && a.planes == 1 && !pack_weight;
-  if (*packed) return launch(number_rows_kernel<true, true>, 1, 1024, 0, s, false, a, vector);
-  if (a.K == 0 && a.T <= 2048) return launch(number_rows_kernel<true, false>, 1, 1024, 0, s, false, a, vector);
+cudaError_t launch_rows(const Args& a, cudaStream_t s) {
+  // Up to as many rows as its block has threads, the numbering kernel prepares
+  // them itself. A loss of a vocabulary of 1009 at width 96, replayed: 18.0 us
+  // for one row, 18.1 with two kernels; 21.1 and 21.1 for 1024 rows; 21.3 and
+  // 20.9 for 2048; 22.7 and 21.6 for 4096. A call that is waited for (one row,
+  // GPT-2-small's head): 67 and 70 us. (Packing the rows there too: 33.4 us
+  // instead of 31.2, replayed; 39.1 instead of 39.0 from the host.)
+  if (a.K == 0 && a.T <= 1024) return launch(number_rows_kernel<true>, 1, 1024, 0, s, false, a);
   cudaError_t e = cudaSuccess;
   if (a.T > 0) {
     if (a.K == 0) {
@@ -611,7 +608,7 @@ cudaError_t launch_rows(const Args& a, bool pack_weight, bool* packed, cudaStrea
       e = launch(teacher_rows_kernel, unsigned((a.T + rows - 1) / rows), rows * 32, rows * row, s, false, a);
     }
   }
-  return e != cudaSuccess ? e : launch(number_rows_kernel<false, false>, 1, 1024, 0, s, a.T > 0, a, vector);
+  return e != cudaSuccess ? e : launch(number_rows_kernel<false>, 1, 1024, 0, s, a.T > 0, a);
 }
 
 cudaError_t launch_pack(const Args& a, __nv_bfloat16* weight, cudaStream_t s) {
