@@ -322,6 +322,25 @@ def test_accumulate_adds_with_one_rounding(losses, cuda, kind):
     assert bool(((dw.double() - want).abs() <= allowed).all())
 
 
+@pytest.mark.parametrize("pad", [0, 1])
+@pytest.mark.parametrize("kind,T,V,D", [("bf16", 8200, 21000, 64), ("fp32", 4100, 13000, 72)])
+def test_accumulate_over_several_pieces(losses, cuda, kind, T, V, D, pad):
+    """As above, with dweight's rows in several pieces of the vocabulary, on 16 bytes and off them."""
+    dt = TYPES[kind]
+    h, w, y, g = inputs(T, V, D, dt, 32, cuda, masked=0.1)
+    r = reference(h, w, y)
+    before = (torch.randn(V, D, generator=g) * 1e-4).to(dt).to(cuda)
+    dw, buf = empty_matrix(V, D, dt, cuda, pad)
+    dw.copy_(before)
+    got = losses.xent_step(h, w, y, dweight=dw, accumulate=True)
+    want = before.double() + r["dweight"]
+    unit = 2.0 ** -24 if dt == torch.float32 else 2.0 ** -8
+    allowed = bounds(r, dt)["dweight"] + unit * 1.01 * want.abs()
+    assert bool(((dw.double() - want).abs() <= allowed).all())
+    gaps_untouched(buf, V, D, pad)
+    check(got._replace(dweight=None), r, dt)
+
+
 def test_another_stream(losses, cuda):
     """Inputs made and outputs used on a side stream, named or current."""
     side = torch.cuda.Stream()
@@ -603,6 +622,18 @@ def test_several_pieces_of_the_vocabulary(losses, cuda, kind, T, V, D):
     check(got, r, dt)
 
 
+@pytest.mark.parametrize("kind,T,V,D", [("bf16", 8200, 21000, 64), ("fp32", 4100, 13000, 64)])
+def test_distillation_over_several_pieces(losses, cuda, kind, T, V, D):
+    dt = TYPES[kind]
+    h, w, y, g = inputs(T, V, D, dt, 52, cuda, masked=0.1)
+    ids = (torch.randint(0, V - 4000, (T, 1), generator=g) + torch.arange(0, 4000, 500)).to(cuda)
+    logits = 3.0 * torch.randn(T, 8, generator=g).to(cuda)
+    ids[::7] = -1
+    r = reference(h, w, y, ids, logits, tau=2.0, alpha=0.5)
+    got = losses.distill_step(h, w, ids, logits, temperature=2.0, labels=y, alpha=0.5)
+    check(got, r, dt)
+
+
 @pytest.mark.parametrize("T,V,D", [(1, 31, 64), (1, 50257, 96), (3, 1009, 65), (16, 2000, 448),
                                    (64, 41217, 200), (200, 300, 771), (256, 777, 128)])
 @pytest.mark.parametrize("op", ["xent", "distill", "both"])
@@ -693,6 +724,29 @@ def test_in_a_graph(losses, cuda):
     graph.replay()
     torch.cuda.synchronize()
     check(got, reference(h2, w2, y2), torch.bfloat16)
+
+
+@pytest.mark.parametrize("kind", TYPES)
+def test_distillation_in_a_graph(losses, cuda, kind):
+    """Captured once, in both storage types, and replayed on new values of the same tensors."""
+    dt = TYPES[kind]
+    T, V, D, K = 90, 700, 64, 6
+    h, w, y, g = inputs(T, V, D, dt, 73, cuda)
+    ids, logits = teacher(T, V, K, g, cuda)
+    more = dict(temperature=2.0, labels=y, alpha=0.5)
+    losses.distill_step(h, w, ids, logits, **more)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = losses.distill_step(h, w, ids, logits, **more)
+    for seed in (74, 75):
+        h2, w2, y2, g = inputs(T, V, D, dt, seed, cuda, masked=0.3)
+        ids2, logits2 = teacher(T, V, K, g, cuda, absent=0.3)
+        for to, value in ((h, h2), (w, w2), (y, y2), (ids, ids2), (logits, logits2)):
+            to.copy_(value)
+        graph.replay()
+        torch.cuda.synchronize()
+        check(got, reference(h2, w2, y2, ids2, logits2, tau=2.0, alpha=0.5), dt)
 
 
 def test_offsets_beyond_32_bits(losses, cuda):

@@ -265,7 +265,7 @@ int plan(const zero_head_loss_t* p, bool distill, int pass, Args* a, __nv_bfloat
   }
   if (pass & kBackward) {
     // dhidden's sums over a piece are split where one of its tiles would be
-    // more than half of what each of 76 CTA pairs has to do for the piece, while
+    // more than half of what each CTA pair of the card has to do for the piece, while
     // two blocks of K are left to a part (37 rows x 1009 x 96 in fp32: a step of
     // 68 us, 87 unsplit; 333 x 10007 x 512: 197 and 419; twice the parts on 1638
     // rows x 32000 x 2048: 543 instead of 534).
@@ -276,7 +276,7 @@ int plan(const zero_head_loss_t* p, bool distill, int pass, Args* a, __nv_bfloat
     const int64_t work = terms * (rows * wide * blocks_v + (p->dweight ? cols * wide * blocks_t : 0)) +
                          (pieces > 1 ? rows * cols * blocks_d : 0);
     a->splits = 1;
-    while (a->splits < 64 && terms * blocks_v / a->splits > std::max<int64_t>(work / (2 * 76), 2 * terms)) a->splits *= 2;
+    while (a->splits < 64 && terms * blocks_v / a->splits > std::max<int64_t>(work / zl::kSms, 2 * terms)) a->splits *= 2;
   }
   // The words that begin as zero.
   const int64_t tiles = pass & kBackward ? a->splits * (a->Tp / zl::kTileM) * ((a->D + 255) / 256) : 0;

@@ -21,6 +21,8 @@ constexpr int kTileM = 256;
 constexpr int kTileN = 256;
 constexpr int kPadD = 64;       // packed operands are padded to this width
 constexpr int32_t kNoId = 0x7ffffffe;  // above every id, and so is kNoId + 1
+constexpr int kSms = 152;        // GB300's multiprocessors. (The layout is planned for them, not for
+                                 // what a device reports: the workspace query runs without one.)
 constexpr int kBuffers = 3;      // of G
 constexpr int kLossBlocks = 608; // most blocks of the losses' kernel
 

@@ -560,7 +560,7 @@ namespace {
 // A grid for `n` items of 256 threads, a few blocks a thread at most.
 unsigned blocks_for(int64_t n) {
   const int64_t blocks = (n + 255) / 256;
-  return unsigned(blocks < 1 ? 1 : blocks > 152 * 32 ? 152 * 32 : blocks);
+  return unsigned(blocks < 1 ? 1 : blocks > kSms * 32 ? kSms * 32 : blocks);
 }
 
 // `dependent`: a programmatic launch behind the kernel before it.
@@ -604,7 +604,7 @@ cudaError_t launch_rows(const Args& a, cudaStream_t s) {
       // what shared memory holds beside `kept`, and fewer where they leave SMs idle
       // (333 rows: 197 us a step instead of 200).
       int rows = kTeacherRows * (row + sizeof(int)) <= kSharedWithoutAsking ? kTeacherRows : 2;
-      while (rows > 2 && a.T / rows < 152) rows /= 2;
+      while (rows > 2 && a.T / rows < kSms) rows /= 2;
       e = launch(teacher_rows_kernel, unsigned((a.T + rows - 1) / rows), rows * 32, rows * row, s, false, a);
     }
   }
@@ -623,14 +623,14 @@ cudaError_t launch_losses(const Args& a, cudaStream_t s) {
   // As many lanes to a row as leave a block for each SM (333 rows with two
   // softmaxes and 100 entries: a step of 197 us, 227 with 32 rows a block).
   int rows = 32;
-  while (rows > 1 && a.T / rows < 152) rows /= 2;
+  while (rows > 1 && a.T / rows < kSms) rows /= 2;
   const int64_t blocks = (a.T + rows - 1) / rows;
   return launch(losses_kernel, unsigned(blocks < 1 ? 1 : blocks < kLossBlocks ? blocks : kLossBlocks), 256, 0, s,
                 true, a, rows);
 }
 
 cudaError_t launch_mark(const Args& a, cudaStream_t s) {
-  return launch(mark_kernel, 152, 256, 0, s, true, a);
+  return launch(mark_kernel, kSms, 256, 0, s, true, a);
 }
 
 cudaError_t launch_dhidden_out(const Args& a, cudaStream_t s) {
@@ -640,7 +640,7 @@ cudaError_t launch_dhidden_out(const Args& a, cudaStream_t s) {
   const bool lanes = a.splits >= 8;
   const int64_t groups = lanes ? 32 : 256;
   const int64_t stretches = a.T * (((a.D + 3) / 4 + groups - 1) / groups);
-  const unsigned blocks = unsigned(stretches < 152 * 32 ? stretches : 152 * 32);
+  const unsigned blocks = unsigned(stretches < kSms * 32 ? stretches : kSms * 32);
   const auto run = [&](auto* kernel) { return launch(kernel, blocks, 256, 0, s, true, a); };
   if (a.planes == 3) {
     if (vector) return lanes ? run(dhidden_out_kernel<true, true, 8>) : run(dhidden_out_kernel<true, true, 1>);
