@@ -164,13 +164,13 @@ class _Call:
     def vector(self, t, what: str, dtype, last: int | None = None) -> int:
         """The address of contiguous elements, one (or ``last``) for each row."""
         address = _vector(t, what, dtype, self.T if last is None else self.T * last, self.device)
-        rows = t.shape
-        if last is not None:
-            if rows[-1:] != (last,):
-                raise ValueError(f"{what} has shape {tuple(rows)}, expected {last} entries for each row")
-            rows = rows[:-1]
-        if len(rows) > 1 and rows != self.lead:
-            self.agree(rows, what)
+        if last is None:
+            if t.dim() > 1:
+                self.agree(t.shape, what)
+        elif t.dim() < 1 or t.shape[-1] != last:
+            raise ValueError(f"{what} has shape {tuple(t.shape)}, expected {last} entries for each row")
+        elif t.dim() > 2:
+            self.agree(t.shape[:-1], what)
         return address
 
     def empty(self, shape, dtype):
