@@ -504,8 +504,12 @@ int ddp_allreduce_mean_from_host_h(zero_ddp_host_t *h, const void *const *host_g
  * Arithmetic: products of the stored values summed in fp32 on the tensor cores
  * (ZERO_FP32 values are split into three bf16 parts, whose six largest
  * products keep fp32's precision); softmax statistics, losses and the sums of
- * both gradients are fp32 or wider; in ZERO_BF16_MIXED the gradient of the
- * logits is rounded to bf16 once, as the operand of the two gradient products.
+ * both gradients are fp32 or wider. In ZERO_BF16_MIXED the gradient of the
+ * logits is a bf16 operand of the two gradient products: with T above 256 it is
+ * rounded to bf16 once (the gradients are then 1.1 to 1.5 times as far from the
+ * exact ones as the rounding of the results alone makes them), up to T = 256 it
+ * is kept in two bf16 parts and only the rounding of the results is left. Which
+ * of the two is decided by T alone, empty rows included.
  * Every sum has a fixed order: equal inputs give equal bits, and a step the
  * bits of a forward and a backward call.
  *
@@ -544,8 +548,11 @@ typedef struct zero_head_loss {
   int64_t ignore_index;
   /* Distillation; NULL, 0 and unused for zero_xent_*. */
   const int64_t *teacher_ids;   /* [T][teacher_k]; an id outside [0, V) is an
-                                   absent entry, and so is a logit of -inf;
-                                   entries of equal id add their q             */
+                                   absent entry, and so is a logit of -inf.
+                                   Entries of equal id are entries of their own
+                                   in the formulas: z gets the gradient of all,
+                                   and log q is each one's, not that of their
+                                   sum                                         */
   const float *teacher_logits;  /* [T][teacher_k]                              */
   int64_t teacher_k;            /* 1 .. ZERO_DISTILL_MAX_K                     */
   double temperature;           /* tau: finite, > 0                            */

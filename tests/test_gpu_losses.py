@@ -261,6 +261,20 @@ def test_teacher_logits_at_the_end_of_the_range(losses, cuda, kind, logits_type,
         check(got, r, dt, f"{kind} {alpha}", parts=2)
 
 
+def test_entries_of_equal_id_are_entries_of_their_own(losses, cuda):
+    """The loss that the formula gives for them, written out for one row: six entries of one id
+    and equal logits have q = 1/6 each, so log q is -log 6 in every term."""
+    V, D, K, tau = 40, 16, 6, 2.0
+    h, w, _, _ = inputs(1, V, D, torch.float32, 23, cuda)
+    z = (h.double() @ w.double().T)[0] / tau
+    got = losses.distill_step(h, w, torch.full((1, K), 7, device=cuda), torch.zeros(1, K, device=cuda), temperature=tau)
+    want = tau * tau * (-math.log(K) - float(z[7]) + float(torch.logsumexp(z, 0)))
+    assert float(got.loss[0]) == pytest.approx(want, rel=1e-5, abs=1e-5)
+    p = torch.softmax(z, 0)
+    p[7] -= 1.0                             # the six add their q
+    assert torch.allclose(got.dhidden[0].double(), tau * (p @ w.double()), rtol=1e-4, atol=1e-6)
+
+
 def test_distill_many_entries(losses, cuda):
     T, V, D, K = 9, 5000, 64, 1024
     h, w, y, g = inputs(T, V, D, torch.bfloat16, 2, cuda)

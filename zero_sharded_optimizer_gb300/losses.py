@@ -305,8 +305,8 @@ def distill_forward(hidden, weight, teacher_ids, teacher_logits, *, temperature:
                     ignore_index: int = -100, stream=None) -> Losses:
     """Distillation from the teacher's top logits (``teacher_ids`` int64 [T, K],
     ``teacher_logits`` float32 or bfloat16 [T, K]; an id outside [0, V) is an
-    absent entry), weighted ``alpha``, and with ``labels`` the cross entropy,
-    weighted ``1 - alpha``."""
+    absent entry, and so is a logit of -inf), weighted ``alpha``, and with ``labels``
+    the cross entropy, weighted ``1 - alpha``."""
     c = _Call(hidden, weight, labels, reduction, ignore_index, stream,
               (teacher_ids, teacher_logits, temperature, alpha))
     out = c.losses()
