@@ -31,7 +31,7 @@
 // What bounds it: the tensor pipes, 95 % busy in the forward pass and 82 % in
 // the backward pass of 8192 rows of width 768 and a vocabulary of 50257 (312 us,
 // 2.0 PFLOP/s, and 1.10 ms, 1.7 PFLOP/s), and over many calls the power limit,
-// which lowers the clock: 1.70 PFLOP/s forward, where cuBLAS keeps 1.74. What
+// which lowers the clock: 1.72 PFLOP/s forward, where cuBLAS keeps 1.75. What
 // the backward pass loses: dH's additions 4 %, waits between phases 4 %, G's
 // stores 2 %, the rest to operands that come from DRAM instead of L2.
 //
