@@ -17,7 +17,8 @@
  * (zero_step_from_host, zero_step_from_host_ex), the DDP mean (also from host
  * memory: ddp_allreduce_mean_from_host) and per-stage memory accounting; and,
  * where a language model's gradients begin, the losses at the vocabulary
- * (zero_xent_*, zero_distill_*).
+ * (zero_xent_*, zero_distill_*), and where they end, the embedding
+ * (zero_embedding_*).
  *
  * Conventions for every call:
  *  - Return value: ZERO_OK (0) or a negative ZERO_E* code. zero_strerror()
@@ -602,6 +603,58 @@ int zero_xent_step(const zero_head_loss_t *p, zero_stream_t stream);
 int zero_distill_forward(const zero_head_loss_t *p, zero_stream_t stream);
 int zero_distill_backward(const zero_head_loss_t *p, zero_stream_t stream);
 int zero_distill_step(const zero_head_loss_t *p, zero_stream_t stream);
+
+/* --------------------------------------------------------- embedding -- */
+
+/* The other end of a model whose embedding and head are one matrix: the lookup
+ * of token ids, and its gradient, which goes where the head's does -- into the
+ * same rows of a rank's flat gradient buffer.
+ *
+ * zero_embedding_forward:  out[t] = scale * weight[ids[t]], a row of zeros for
+ *     an id outside [0, V).
+ * zero_embedding_backward: dweight[v] = scale * sum over the tokens t with
+ *     ids[t] = v, in ascending t, of dout[t]; nothing is added for an id outside
+ *     [0, V) or equal to padding_id, and those tokens' rows of dout are not read.
+ *     With `accumulate` the sum is added to dweight, whose rows without a token
+ *     are neither read nor written; else those rows become zero.
+ *
+ * Arithmetic: in fp32, each result rounded once to its type. The backward
+ * pass's sums have a fixed order: equal inputs give equal bits. */
+typedef struct zero_embedding {
+  int64_t T, V, D;        /* tokens (may be 0), vocabulary, width; below 2^31  */
+  int32_t precision;      /* of the matrices: ZERO_FP32 (float) or
+                             ZERO_BF16_MIXED (bf16)                            */
+  int32_t accumulate;     /* backward, nonzero: dweight += its gradient        */
+  const int64_t *ids;     /* [T]                                               */
+  int64_t padding_id;     /* backward: an id without a gradient; -1: none      */
+  double scale;           /* finite, also as a float                           */
+  /* Matrices: DEVICE pointers to rows `stride` elements apart (at least D), the
+   * elements of a row adjacent. Any alignment down to the element's own is
+   * served; rows that start on 16 bytes are accessed 16 bytes at a time. */
+  const void *weight;     /* forward: [V][D]                                   */
+  int64_t weight_stride;
+  void *out;              /* forward: [T][D]                                   */
+  int64_t out_stride;
+  const void *dout;       /* backward: [T][D]                                  */
+  int64_t dout_stride;
+  void *dweight;          /* backward: [V][D]                                  */
+  int64_t dweight_stride;
+  /* Backward: caller-owned scratch, 256-byte aligned, at least the bytes that
+   * the query gives; contents overwritten, nothing kept between calls. */
+  void *workspace;
+  int64_t workspace_bytes;
+} zero_embedding_t;
+
+/* Workspace of a backward call on a problem of these sizes. */
+int zero_embedding_workspace_bytes(const zero_embedding_t *p, int64_t *bytes);
+
+/* Everything is queued on `stream`.
+ * Errors: EINVAL (sizes, strides below D, precision, scale, a NULL buffer that
+ * is needed, a workspace that is too small, an output or the workspace
+ * overlapping another buffer), EALIGN (a pointer not aligned to its element, a
+ * workspace not to 256 bytes), ECUDA. */
+int zero_embedding_forward(const zero_embedding_t *p, zero_stream_t stream);
+int zero_embedding_backward(const zero_embedding_t *p, zero_stream_t stream);
 
 /* ---------------------------------------------------------------- memory -- */
 

@@ -103,6 +103,9 @@ _SIGNATURES = {
     "zero_distill_forward": (ctypes.c_int, [_vp, _vp]),
     "zero_distill_backward": (ctypes.c_int, [_vp, _vp]),
     "zero_distill_step": (ctypes.c_int, [_vp, _vp]),
+    "zero_embedding_workspace_bytes": (ctypes.c_int, [_vp, _P(_i64)]),
+    "zero_embedding_forward": (ctypes.c_int, [_vp, _vp]),
+    "zero_embedding_backward": (ctypes.c_int, [_vp, _vp]),
     "zero_strerror": (ctypes.c_char_p, [ctypes.c_int]),
     "zero_last_error": (ctypes.c_char_p, []),
 }
@@ -624,6 +627,33 @@ def zero_distill_backward(p: HeadLoss, stream=None):
 
 def zero_distill_step(p: HeadLoss, stream=None):
     _check(_lib.zero_distill_step(ctypes.byref(p), _stream(stream)), "zero_distill_step")
+
+
+# ------------------------------------------------------------- embedding --
+
+class Embedding(ctypes.Structure):
+    """zero_embedding_t."""
+    _fields_ = [("T", _i64), ("V", _i64), ("D", _i64), ("precision", _i32), ("accumulate", _i32),
+                ("ids", _vp), ("padding_id", _i64), ("scale", _dbl), ("weight", _vp),
+                ("weight_stride", _i64), ("out", _vp), ("out_stride", _i64), ("dout", _vp),
+                ("dout_stride", _i64), ("dweight", _vp), ("dweight_stride", _i64),
+                ("workspace", _vp), ("workspace_bytes", _i64)]
+
+
+def zero_embedding_workspace_bytes(p: Embedding) -> int:
+    out = _i64()
+    _check(_lib.zero_embedding_workspace_bytes(ctypes.byref(p), ctypes.byref(out)),
+           "zero_embedding_workspace_bytes")
+    return out.value
+
+
+def zero_embedding_forward(p: Embedding, stream=None):
+    _check(_lib.zero_embedding_forward(ctypes.byref(p), _stream(stream)), "zero_embedding_forward")
+
+
+def zero_embedding_backward(p: Embedding, stream=None):
+    _check(_lib.zero_embedding_backward(ctypes.byref(p), _stream(stream)),
+           "zero_embedding_backward")
 
 
 def zero_last_error() -> str:

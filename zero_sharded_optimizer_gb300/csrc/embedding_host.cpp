@@ -1,0 +1,164 @@
+// Host side of the embedding: argument checks, the workspace's layout and the
+// order of the launches. Device work is in embedding_kernels.cu.
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "embedding_internal.h"
+#include "host_checks.h"
+
+namespace {
+
+using ze::Args;
+using zl::Layout;
+using zl::Span;
+using zl::check_pointer;
+using zl::elem_size;
+using zl::overlap;
+using zl::round_up;
+using zl::set_error;
+
+constexpr int64_t kMostSize = 0x7fffffff - 1024;  // T, V and D: 32-bit ids and positions
+
+int check_sizes(const zero_embedding_t* p) {
+  if (!p) return set_error(ZERO_EINVAL, "the problem is NULL");
+  if (p->T < 0 || p->T > kMostSize) return set_error(ZERO_EINVAL, "T=%lld is out of range", (long long)p->T);
+  if (p->V < 1 || p->V > kMostSize) return set_error(ZERO_EINVAL, "V=%lld is out of range", (long long)p->V);
+  if (p->D < 1 || p->D > kMostSize) return set_error(ZERO_EINVAL, "D=%lld is out of range", (long long)p->D);
+  if (p->precision != ZERO_FP32 && p->precision != ZERO_BF16_MIXED)
+    return set_error(ZERO_EINVAL, "precision %d is neither ZERO_FP32 nor ZERO_BF16_MIXED", p->precision);
+  if (!std::isfinite(p->scale) || !std::isfinite(float(p->scale)))
+    return set_error(ZERO_EINVAL, "scale must be finite");
+  return ZERO_OK;
+}
+
+int check_stride(int64_t stride, int64_t rows, int64_t D, const char* what) {
+  if (stride < D)
+    return set_error(ZERO_EINVAL, "%s=%lld is below D=%lld", what, (long long)stride, (long long)D);
+  if (rows > 1 && stride > INT64_MAX / 8 / rows)
+    return set_error(ZERO_EINVAL, "%s=%lld is out of range", what, (long long)stride);
+  return ZERO_OK;
+}
+
+int check_spans(const Span* spans, int n) {
+  for (int i = 0; i < n; ++i)
+    for (int j = 0; j < i; ++j)
+      if ((spans[i].written || spans[j].written) && overlap(spans[i], spans[j]))
+        return set_error(ZERO_EINVAL, "buffers overlap (%s and %s)", spans[j].what, spans[i].what);
+  return ZERO_OK;
+}
+
+void common(const zero_embedding_t* p, const void* table, int64_t table_stride, void* out, int64_t out_stride,
+            Args* a) {
+  *a = Args{};
+  a->T = p->T;
+  a->V = p->V;
+  a->D = p->D;
+  a->f32 = p->precision == ZERO_FP32;
+  a->ids = p->ids;
+  a->padding_id = p->padding_id;
+  a->scale = float(p->scale);
+  a->table = table;
+  a->table_stride = table_stride;
+  a->out = out;
+  a->out_stride = out_stride;
+  const int es = elem_size(p->precision);
+  a->vector = reinterpret_cast<uintptr_t>(table) % 16 == 0 && table_stride * es % 16 == 0 &&
+              reinterpret_cast<uintptr_t>(out) % 16 == 0 && out_stride * es % 16 == 0;
+}
+
+// The gradient's arrays in the workspace.
+int plan(const zero_embedding_t* p, Args* a, int64_t* bytes) {
+  common(p, p->dout, p->dout_stride, p->dweight, p->dweight_stride, a);
+  a->accumulate = p->accumulate != 0;
+  // The fewest digits, of equal width, that hold the ids and V itself.
+  int bits = 1;
+  while (p->V >> bits) ++bits;
+  a->passes = (bits + ze::kMostBits - 1) / ze::kMostBits;
+  a->bits = (bits + a->passes - 1) / a->passes;
+  const int64_t least = 4096;
+  a->tile = std::max(least, round_up((p->T + ze::kMostTiles - 1) / ze::kMostTiles, 512));
+  a->tiles = int32_t((p->T + a->tile - 1) / a->tile);
+  const int64_t block = p->precision == ZERO_FP32 ? 128 : 256;
+  a->blocks = int32_t((p->D + block - 1) / block);
+  a->Dp = a->blocks * block;
+  a->run = 32;
+  while (a->run > 8 && (p->T + a->run - 1) / a->run * a->blocks < ze::kSms * 32) a->run /= 2;
+  a->runs = (p->T + a->run - 1) / a->run;
+  Layout w{static_cast<uint8_t*>(p->workspace)};
+  a->counts = w.take<int32_t>(int64_t(a->tiles) << a->bits);
+  for (auto& l : a->list) l = w.take<ze::Entry>(p->T);
+  a->part = w.take<float>(2 * a->runs, a->Dp);
+  if (!w.fits) return set_error(ZERO_EINVAL, "the problem's workspace overflows 64 bits");
+  *bytes = w.at;
+  return ZERO_OK;
+}
+
+int launched(cudaError_t e, const char* what) {
+  if (e == cudaSuccess) return ZERO_OK;
+  return set_error(ZERO_ECUDA, "%s: %s (%s)", what, cudaGetErrorString(e), cudaGetErrorName(e));
+}
+
+}  // namespace
+
+extern "C" {
+
+int zero_embedding_workspace_bytes(const zero_embedding_t* p, int64_t* bytes) {
+  if (!bytes) return set_error(ZERO_EINVAL, "bytes is NULL");
+  if (int e = check_sizes(p)) return e;
+  zero_embedding_t q = *p;
+  q.workspace = nullptr;
+  Args a;
+  return plan(&q, &a, bytes);
+}
+
+int zero_embedding_forward(const zero_embedding_t* p, zero_stream_t stream) {
+  if (int e = check_sizes(p)) return e;
+  const int64_t T = p->T, V = p->V, D = p->D;
+  const int es = elem_size(p->precision);
+  int e;
+  if ((e = check_stride(p->weight_stride, V, D, "weight_stride"))) return e;
+  if ((e = check_stride(p->out_stride, T, D, "out_stride"))) return e;
+  if ((e = check_pointer(p->ids, T, 8, "ids"))) return e;
+  if ((e = check_pointer(p->weight, V, es, "weight"))) return e;
+  if ((e = check_pointer(p->out, T, es, "out"))) return e;
+  const Span spans[] = {{p->ids, 1, 8 * T, 8 * T, "ids", false},
+                        {p->weight, V, D * es, p->weight_stride * es, "weight", false},
+                        {p->out, T, D * es, p->out_stride * es, "out", true}};
+  if ((e = check_spans(spans, 3))) return e;
+  if (T == 0) return ZERO_OK;
+  Args a;
+  common(p, p->weight, p->weight_stride, p->out, p->out_stride, &a);
+  return launched(ze::launch_lookup(a, stream), "the lookup");
+}
+
+int zero_embedding_backward(const zero_embedding_t* p, zero_stream_t stream) {
+  if (int e = check_sizes(p)) return e;
+  const int64_t T = p->T, V = p->V, D = p->D;
+  const int es = elem_size(p->precision);
+  int e;
+  if ((e = check_stride(p->dout_stride, T, D, "dout_stride"))) return e;
+  if ((e = check_stride(p->dweight_stride, V, D, "dweight_stride"))) return e;
+  if ((e = check_pointer(p->ids, T, 8, "ids"))) return e;
+  if ((e = check_pointer(p->dout, T, es, "dout"))) return e;
+  if ((e = check_pointer(p->dweight, V, es, "dweight"))) return e;
+  const Span spans[] = {{p->ids, 1, 8 * T, 8 * T, "ids", false},
+                        {p->dout, T, D * es, p->dout_stride * es, "dout", false},
+                        {p->dweight, V, D * es, p->dweight_stride * es, "dweight", true},
+                        {p->workspace, 1, p->workspace_bytes, p->workspace_bytes, "workspace", true}};
+  if ((e = check_spans(spans, 4))) return e;
+  if (reinterpret_cast<uintptr_t>(p->workspace) % 256)
+    return set_error(ZERO_EALIGN, "the workspace is not aligned to 256 bytes");
+  Args a;
+  int64_t bytes = 0;
+  if ((e = plan(p, &a, &bytes))) return e;
+  if (bytes && (!p->workspace || p->workspace_bytes < bytes))
+    return set_error(ZERO_EINVAL, "the workspace has %lld bytes, %lld are needed",
+                     (long long)(p->workspace ? p->workspace_bytes : 0), (long long)bytes);
+  if (T == 0 && a.accumulate) return ZERO_OK;
+  if (T > 0 && (e = launched(ze::launch_sort(a, stream), "the sort"))) return e;
+  return launched(ze::launch_sums(a, stream), "the sums");
+}
+
+}  // extern "C"

@@ -6,12 +6,19 @@
 #include <cmath>
 #include <cstdint>
 
+#include "host_checks.h"
 #include "loss_internal.h"
 
 namespace {
 
 using zl::Args;
+using zl::Layout;
 using zl::Program;
+using zl::Span;
+using zl::check_pointer;
+using zl::elem_size;
+using zl::overlap;
+using zl::round_up;
 using zl::set_error;
 
 constexpr int64_t kMostSize = 0x7fffffff - 1024;  // T, V and D: 32-bit tile coordinates
@@ -42,35 +49,7 @@ struct Withheld {
 };
 thread_local Withheld g_withheld;
 
-int64_t round_up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
-
-int elem_size(int32_t precision) { return precision == ZERO_FP32 ? 4 : 2; }
-
 enum Pass { kForward = 1, kBackward = 2 };
-
-// A buffer the call touches: `rows` rows of `bytes` bytes, `stride` bytes apart.
-struct Span {
-  const void* p;
-  int64_t rows, bytes, stride;
-  const char* what;
-  bool written;
-};
-
-// Whether two buffers share a byte. Rows of equal stride are compared by their
-// phase, so that column blocks of one wider buffer pass.
-bool overlap(const Span& x, const Span& y) {
-  if (!x.p || !y.p || !x.rows || !y.rows || !x.bytes || !y.bytes) return false;
-  const uintptr_t a = reinterpret_cast<uintptr_t>(x.p), b = reinterpret_cast<uintptr_t>(y.p);
-  const uintptr_t a1 = a + uintptr_t((x.rows - 1) * x.stride + x.bytes);
-  const uintptr_t b1 = b + uintptr_t((y.rows - 1) * y.stride + y.bytes);
-  if (a1 <= b || b1 <= a) return false;
-  if (x.stride == y.stride && x.rows > 1 && y.rows > 1) {
-    const uintptr_t s = uintptr_t(x.stride);
-    const uintptr_t d = b >= a ? (b - a) % s : (s - (a - b) % s) % s;
-    if (d >= uintptr_t(x.bytes) && s - d >= uintptr_t(y.bytes)) return false;
-  }
-  return true;
-}
 
 int check_sizes(const zero_head_loss_t* p, bool distill) {
   if (!p) return set_error(ZERO_EINVAL, "the problem is NULL");
@@ -108,13 +87,6 @@ int check_sizes(const zero_head_loss_t* p, bool distill) {
   } else if (p->teacher_ids || p->teacher_logits || p->teacher_k || p->lse_tau) {
     return set_error(ZERO_EINVAL, "teacher fields are set: use the zero_distill calls");
   }
-  return ZERO_OK;
-}
-
-int check_pointer(const void* ptr, int64_t count, size_t align, const char* what) {
-  if (!ptr && count > 0) return set_error(ZERO_EINVAL, "%s is NULL", what);
-  if (reinterpret_cast<uintptr_t>(ptr) % align)
-    return set_error(ZERO_EALIGN, "%s is not aligned to %zu bytes", what, align);
   return ZERO_OK;
 }
 
@@ -166,26 +138,6 @@ int check_buffers(const zero_head_loss_t* p, bool distill, int pass) {
         return set_error(ZERO_EINVAL, "buffers overlap (%s and %s)", spans[j].what, spans[i].what);
   return ZERO_OK;
 }
-
-// Places the call's arrays in the workspace (base NULL: only counts bytes).
-// Returns false when the size overflows.
-struct Layout {
-  uint8_t* base;
-  int64_t at = 0;
-  bool fits = true;
-  template <typename T>
-  T* take(int64_t count, int64_t times = 1) {
-    const int64_t size = int64_t(sizeof(T));
-    if (!fits || (times && count > (INT64_MAX / 4) / times / size)) {
-      fits = false;
-      return nullptr;
-    }
-    T* p = reinterpret_cast<T*>(base + at);
-    at = round_up(at + count * times * size, 256);
-    if (at > INT64_MAX / 4) fits = false;
-    return p;
-  }
-};
 
 // The weight can be read in place by 16-byte copies of whole rows.
 bool weight_in_place(const zero_head_loss_t* p) {

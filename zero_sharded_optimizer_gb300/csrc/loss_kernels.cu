@@ -563,27 +563,6 @@ unsigned blocks_for(int64_t n) {
   return unsigned(blocks < 1 ? 1 : blocks > kSms * 32 ? kSms * 32 : blocks);
 }
 
-// `dependent`: a programmatic launch behind the kernel before it.
-template <typename... P, typename... A>
-cudaError_t launch(void (*kernel)(P...), unsigned blocks, int threads, size_t shared, cudaStream_t s, bool dependent,
-                   const A&... args) {
-  cudaLaunchConfig_t c = {};
-  c.gridDim = dim3(blocks);
-  c.blockDim = dim3(unsigned(threads));
-  c.dynamicSmemBytes = shared;
-  c.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  c.attrs = at;
-  c.numAttrs = dependent ? 1 : 0;
-  return cudaLaunchKernelEx(&c, kernel, P(args)...);
-}
-
-bool aligned16(const void* p, int64_t stride_bytes) {
-  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && stride_bytes % 16 == 0;
-}
-
 }  // namespace
 
 cudaError_t launch_rows(const Args& a, cudaStream_t s) {
