@@ -17,8 +17,8 @@
  * (zero_step_from_host, zero_step_from_host_ex), the DDP mean (also from host
  * memory: ddp_allreduce_mean_from_host) and per-stage memory accounting; and,
  * where a language model's gradients begin, the losses at the vocabulary
- * (zero_xent_*, zero_distill_*), and where they end, the embedding
- * (zero_embedding_*).
+ * (zero_xent_*, zero_distill_*, zero_policy_*, zero_preference_*), and where
+ * they end, the embedding (zero_embedding_*).
  *
  * Conventions for every call:
  *  - Return value: ZERO_OK (0) or a negative ZERO_E* code. zero_strerror()
@@ -603,6 +603,95 @@ int zero_xent_step(const zero_head_loss_t *p, zero_stream_t stream);
 int zero_distill_forward(const zero_head_loss_t *p, zero_stream_t stream);
 int zero_distill_backward(const zero_head_loss_t *p, zero_stream_t stream);
 int zero_distill_step(const zero_head_loss_t *p, zero_stream_t stream);
+
+/* ------------------------------------ policy and preference losses -- */
+
+/* Losses of the log-probability that a model gives to sampled or preferred
+ * tokens, on the same products as the losses above: with
+ *     l_t = z[t][y_t] - lse_t
+ * of the labelled rows (the empty rows are those without a label), the gradient
+ * of the logits is slope_t (onehot(y_t) - softmax(z_t)) for the loss's slope by
+ * l_t. Rows whose slope is zero -- a clipped ratio, an advantage of zero -- take
+ * no part in the gradients' products: their dhidden is zero.
+ *
+ * zero_policy_*: the clipped policy loss with a term that keeps the policy near
+ * a reference,
+ *     r_t = exp(l_t - old_logps[t]),  d_t = ref_logps[t] - l_t,
+ *     loss_t = max(-A_t r_t, -A_t min(max(r_t, 1 - clip_low), 1 + clip_high))
+ *              + kl_weight (e^d_t - d_t - 1),
+ *     slope_t = (-A_t r_t where that is not the smaller one) + kl_weight (1 - e^d_t);
+ * a row of advantage A_t = 0 has no first term, whatever its ratio.
+ *
+ * zero_preference_*: pairs of a preferred sequence i and a rejected one
+ * pairs + i. With S_s the sum of l_t over the labelled rows of sequence s, n_s
+ * their number and x_s = (S_s, or S_s / n_s with `average`) - ref_logps[s],
+ *     u_i = beta (x_i - x_{pairs + i}) - margin,
+ *     loss_i = (1 - smoothing) log(1 + e^-u_i) + smoothing log(1 + e^u_i)
+ *              or u_i^2,
+ *     plus nll_weight times the preferred sequence's mean of -l_t.
+ * A sequence without labelled rows has S = 0 (and S / n = 0); a pair of two such
+ * is empty: its loss is 0 and the mean does not count it.
+ *
+ * The label's logit is summed a second time, in fp32 with rounding, and its part
+ * of lse corrected, because these losses hang on small differences of
+ * log-probabilities; the sums over a sequence and the losses are formed in
+ * double. Everything else -- arithmetic, equal bits, what a wait that runs out
+ * does -- is as stated above.
+ *
+ * Of the zero_head_loss_t they take: labels (no teacher fields), loss (T values,
+ * or `pairs`), lse, reduced, dloss (NONE: as many as loss) and the gradients. */
+
+typedef struct zero_policy {
+  const float *old_logps;  /* [T] forward: log-probabilities when sampled      */
+  const float *advantages; /* [T] forward                                      */
+  const float *ref_logps;  /* [T] forward: the reference's; not read, and may
+                              be NULL, when kl_weight is 0                     */
+  double clip_low, clip_high; /* at least 0, finite                            */
+  double kl_weight;        /* finite                                           */
+  float *logps;            /* [T] written by the forward pass: l_t; 0 for an
+                              empty row                                        */
+  float *slopes;           /* [T] written by the forward pass, read by the
+                              backward pass: dloss_t/dl_t                      */
+} zero_policy_t;
+
+enum { ZERO_PREFERENCE_SIGMOID = 0, ZERO_PREFERENCE_SQUARED = 1 };
+
+typedef struct zero_preference {
+  int64_t pairs;           /* may be 0                                         */
+  const int64_t *offsets;  /* [2 pairs + 1]: sequence s is the rows [offsets[s],
+                              offsets[s + 1]); rows before the first and behind
+                              the last add nothing. They ascend, not strictly,
+                              from 0 at least to T at most; a call whose offsets
+                              do not writes NaN wherever it writes a result
+                              (counts 0). NULL: 2 pairs sequences of equal length */
+  const float *ref_logps;  /* [2 pairs] forward, or NULL: zeros                */
+  int32_t kind;            /* ZERO_PREFERENCE_*                                */
+  int32_t average;         /* nonzero: x_s from the mean                       */
+  double beta, smoothing, margin, nll_weight; /* finite; smoothing in [0, 1],
+                              and 0 for the squared loss                       */
+  float *logps;            /* [2 pairs] written by the forward pass: S_s       */
+  float *slopes;           /* [2 pairs] written by the forward pass, read by the
+                              backward pass: dloss_i/dl_t of a labelled row of
+                              the sequence                                     */
+  int32_t *counts;         /* [2 pairs] written by the forward pass: n_s       */
+} zero_preference_t;
+
+/* As zero_xent_*. The backward calls read p->lse and q->slopes of a forward call
+ * on the same inputs, and of the rest of *q only `pairs` and `offsets`.
+ * Errors: as zero_xent_*, plus EINVAL for a NULL q, options out of range, a
+ * number of rows that 2 pairs sequences of equal length do not make. */
+int zero_policy_workspace_bytes(const zero_head_loss_t *p, const zero_policy_t *q, int64_t *bytes);
+int zero_policy_forward(const zero_head_loss_t *p, const zero_policy_t *q, zero_stream_t stream);
+int zero_policy_backward(const zero_head_loss_t *p, const zero_policy_t *q, zero_stream_t stream);
+int zero_policy_step(const zero_head_loss_t *p, const zero_policy_t *q, zero_stream_t stream);
+int zero_preference_workspace_bytes(const zero_head_loss_t *p, const zero_preference_t *q,
+                                    int64_t *bytes);
+int zero_preference_forward(const zero_head_loss_t *p, const zero_preference_t *q,
+                            zero_stream_t stream);
+int zero_preference_backward(const zero_head_loss_t *p, const zero_preference_t *q,
+                             zero_stream_t stream);
+int zero_preference_step(const zero_head_loss_t *p, const zero_preference_t *q,
+                         zero_stream_t stream);
 
 /* --------------------------------------------------------- embedding -- */
 

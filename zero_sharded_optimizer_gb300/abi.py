@@ -45,6 +45,9 @@ ZERO_REDUCE_MEAN = 1
 ZERO_REDUCE_SUM = 2
 ZERO_DISTILL_MAX_K = 1024
 
+ZERO_PREFERENCE_SIGMOID = 0
+ZERO_PREFERENCE_SQUARED = 1
+
 _i64 = ctypes.c_int64
 _i32 = ctypes.c_int32
 _u64 = ctypes.c_uint64
@@ -103,6 +106,14 @@ _SIGNATURES = {
     "zero_distill_forward": (ctypes.c_int, [_vp, _vp]),
     "zero_distill_backward": (ctypes.c_int, [_vp, _vp]),
     "zero_distill_step": (ctypes.c_int, [_vp, _vp]),
+    "zero_policy_workspace_bytes": (ctypes.c_int, [_vp, _vp, _P(_i64)]),
+    "zero_policy_forward": (ctypes.c_int, [_vp, _vp, _vp]),
+    "zero_policy_backward": (ctypes.c_int, [_vp, _vp, _vp]),
+    "zero_policy_step": (ctypes.c_int, [_vp, _vp, _vp]),
+    "zero_preference_workspace_bytes": (ctypes.c_int, [_vp, _vp, _P(_i64)]),
+    "zero_preference_forward": (ctypes.c_int, [_vp, _vp, _vp]),
+    "zero_preference_backward": (ctypes.c_int, [_vp, _vp, _vp]),
+    "zero_preference_step": (ctypes.c_int, [_vp, _vp, _vp]),
     "zero_embedding_workspace_bytes": (ctypes.c_int, [_vp, _P(_i64)]),
     "zero_embedding_forward": (ctypes.c_int, [_vp, _vp]),
     "zero_embedding_backward": (ctypes.c_int, [_vp, _vp]),
@@ -627,6 +638,63 @@ def zero_distill_backward(p: HeadLoss, stream=None):
 
 def zero_distill_step(p: HeadLoss, stream=None):
     _check(_lib.zero_distill_step(ctypes.byref(p), _stream(stream)), "zero_distill_step")
+
+
+class Policy(ctypes.Structure):
+    """zero_policy_t."""
+    _fields_ = [("old_logps", _vp), ("advantages", _vp), ("ref_logps", _vp), ("clip_low", _dbl),
+                ("clip_high", _dbl), ("kl_weight", _dbl), ("logps", _vp), ("slopes", _vp)]
+
+
+class Preference(ctypes.Structure):
+    """zero_preference_t."""
+    _fields_ = [("pairs", _i64), ("offsets", _vp), ("ref_logps", _vp), ("kind", _i32),
+                ("average", _i32), ("beta", _dbl), ("smoothing", _dbl), ("margin", _dbl),
+                ("nll_weight", _dbl), ("logps", _vp), ("slopes", _vp), ("counts", _vp)]
+
+
+def zero_policy_workspace_bytes(p: HeadLoss, q: Policy) -> int:
+    out = _i64()
+    _check(_lib.zero_policy_workspace_bytes(ctypes.byref(p), ctypes.byref(q), ctypes.byref(out)),
+           "zero_policy_workspace_bytes")
+    return out.value
+
+
+def zero_policy_forward(p: HeadLoss, q: Policy, stream=None):
+    _check(_lib.zero_policy_forward(ctypes.byref(p), ctypes.byref(q), _stream(stream)),
+           "zero_policy_forward")
+
+
+def zero_policy_backward(p: HeadLoss, q: Policy, stream=None):
+    _check(_lib.zero_policy_backward(ctypes.byref(p), ctypes.byref(q), _stream(stream)),
+           "zero_policy_backward")
+
+
+def zero_policy_step(p: HeadLoss, q: Policy, stream=None):
+    _check(_lib.zero_policy_step(ctypes.byref(p), ctypes.byref(q), _stream(stream)),
+           "zero_policy_step")
+
+
+def zero_preference_workspace_bytes(p: HeadLoss, q: Preference) -> int:
+    out = _i64()
+    _check(_lib.zero_preference_workspace_bytes(ctypes.byref(p), ctypes.byref(q), ctypes.byref(out)),
+           "zero_preference_workspace_bytes")
+    return out.value
+
+
+def zero_preference_forward(p: HeadLoss, q: Preference, stream=None):
+    _check(_lib.zero_preference_forward(ctypes.byref(p), ctypes.byref(q), _stream(stream)),
+           "zero_preference_forward")
+
+
+def zero_preference_backward(p: HeadLoss, q: Preference, stream=None):
+    _check(_lib.zero_preference_backward(ctypes.byref(p), ctypes.byref(q), _stream(stream)),
+           "zero_preference_backward")
+
+
+def zero_preference_step(p: HeadLoss, q: Preference, stream=None):
+    _check(_lib.zero_preference_step(ctypes.byref(p), ctypes.byref(q), _stream(stream)),
+           "zero_preference_step")
 
 
 # ------------------------------------------------------------- embedding --

@@ -51,7 +51,49 @@ thread_local Withheld g_withheld;
 
 enum Pass { kForward = 1, kBackward = 2 };
 
-int check_sizes(const zero_head_loss_t* p, bool distill) {
+// A call's problem: the common part, and what its loss has besides.
+struct Problem {
+  const zero_head_loss_t* p;
+  zl::Kind kind;
+  const zero_policy_t* policy = nullptr;
+  const zero_preference_t* preference = nullptr;
+
+  bool distill() const { return kind == zl::kDistill; }
+  bool slopes() const { return policy || preference; }
+  int64_t losses() const { return preference ? preference->pairs : p->T; }  // that `loss` and `dloss` have
+};
+
+int check_options(const zero_policy_t* q) {
+  if (!std::isfinite(q->clip_low) || q->clip_low < 0.0 || !std::isfinite(q->clip_high) || q->clip_high < 0.0)
+    return set_error(ZERO_EINVAL, "clip_low and clip_high must be finite and at least 0");
+  if (!std::isfinite(q->kl_weight)) return set_error(ZERO_EINVAL, "kl_weight must be finite");
+  return ZERO_OK;
+}
+
+int check_options(const zero_preference_t* q, int64_t T) {
+  if (q->pairs < 0 || q->pairs > kMostSize / 2)
+    return set_error(ZERO_EINVAL, "pairs=%lld is out of range", (long long)q->pairs);
+  if (!q->offsets && (q->pairs ? T % (2 * q->pairs) : T) != 0)
+    return set_error(ZERO_EINVAL, "T=%lld rows are not 2 * %lld sequences of equal length", (long long)T,
+                     (long long)q->pairs);
+  if (q->kind != ZERO_PREFERENCE_SIGMOID && q->kind != ZERO_PREFERENCE_SQUARED)
+    return set_error(ZERO_EINVAL, "unknown kind %d of preference loss", q->kind);
+  if (!std::isfinite(q->beta)) return set_error(ZERO_EINVAL, "beta must be finite");
+  if (!(q->smoothing >= 0.0 && q->smoothing <= 1.0))
+    return set_error(ZERO_EINVAL, "smoothing must lie in [0, 1]");
+  if (q->kind != ZERO_PREFERENCE_SIGMOID && q->smoothing != 0.0)
+    return set_error(ZERO_EINVAL, "smoothing is the sigmoid loss's");
+  if (!std::isfinite(q->margin)) return set_error(ZERO_EINVAL, "margin must be finite");
+  if (!std::isfinite(q->nll_weight)) return set_error(ZERO_EINVAL, "nll_weight must be finite");
+  return ZERO_OK;
+}
+
+int check_sizes(const Problem& problem) {
+  const zero_head_loss_t* p = problem.p;
+  const bool distill = problem.distill();
+  if (problem.kind == zl::kPolicy && !problem.policy) return set_error(ZERO_EINVAL, "the policy's part is NULL");
+  if (problem.kind == zl::kPreference && !problem.preference)
+    return set_error(ZERO_EINVAL, "the preference's part is NULL");
   if (!p) return set_error(ZERO_EINVAL, "the problem is NULL");
   if (p->T < 0 || p->T > kMostSize) return set_error(ZERO_EINVAL, "T=%lld is out of range", (long long)p->T);
   if (p->V < 1 || p->V > kMostSize) return set_error(ZERO_EINVAL, "V=%lld is out of range", (long long)p->V);
@@ -87,12 +129,16 @@ int check_sizes(const zero_head_loss_t* p, bool distill) {
   } else if (p->teacher_ids || p->teacher_logits || p->teacher_k || p->lse_tau) {
     return set_error(ZERO_EINVAL, "teacher fields are set: use the zero_distill calls");
   }
+  if (problem.policy) return check_options(problem.policy);
+  if (problem.preference) return check_options(problem.preference, p->T);
   return ZERO_OK;
 }
 
-int check_buffers(const zero_head_loss_t* p, bool distill, int pass) {
+int check_buffers(const Problem& problem, int pass) {
+  const zero_head_loss_t* p = problem.p;
+  const bool distill = problem.distill();
   const int es = elem_size(p->precision);
-  const int64_t T = p->T, V = p->V, D = p->D;
+  const int64_t T = p->T, V = p->V, D = p->D, losses = problem.losses();
   int e;
   if ((e = check_pointer(p->hidden, T, es, "hidden"))) return e;
   if ((e = check_pointer(p->weight, V, es, "weight"))) return e;
@@ -105,37 +151,66 @@ int check_buffers(const zero_head_loss_t* p, bool distill, int pass) {
   }
   if ((e = check_pointer(p->lse, ce ? T : 0, 4, "lse"))) return e;
   const bool reduce = p->reduction != ZERO_REDUCE_NONE;
-  if (pass & kForward) {
-    if ((e = check_pointer(p->loss, T, 4, "loss"))) return e;
+  const bool fwd = pass & kForward, bwd = pass & kBackward;
+  if (fwd) {
+    if ((e = check_pointer(p->loss, losses, 4, "loss"))) return e;
     if (reduce && (e = check_pointer(p->reduced, 1, 4, "reduced"))) return e;
   }
-  if (pass & kBackward) {
+  if (bwd) {
     if (!p->dhidden && !p->dweight && T > 0) return set_error(ZERO_EINVAL, "neither dhidden nor dweight is given");
     if ((e = check_pointer(p->dhidden, 0, es, "dhidden"))) return e;
     if ((e = check_pointer(p->dweight, 0, es, "dweight"))) return e;
     if ((e = check_pointer(p->dloss, 0, 4, "dloss"))) return e;
     if (!std::isfinite(p->grad_scale)) return set_error(ZERO_EINVAL, "grad_scale must be finite");
   }
-  const bool fwd = pass & kForward, bwd = pass & kBackward;
+  // What the policy and the preference loss have besides: nothing, an entry for
+  // each row, or for each sequence.
+  const zero_policy_t* po = problem.policy;
+  const zero_preference_t* pr = problem.preference;
+  const int64_t each = po ? T : pr ? 2 * pr->pairs : 0;
+  const float* ref = !fwd ? nullptr : po ? (po->kl_weight != 0.0 ? po->ref_logps : nullptr) : pr ? pr->ref_logps : nullptr;
+  float* const slopes = po ? po->slopes : pr ? pr->slopes : nullptr;
+  float* const logps = !fwd ? nullptr : po ? po->logps : pr ? pr->logps : nullptr;
+  if ((e = check_pointer(slopes, each, 4, "slopes"))) return e;
+  if (fwd && (e = check_pointer(logps, each, 4, "logps"))) return e;
+  if ((e = check_pointer(ref, fwd && po && po->kl_weight != 0.0 ? T : 0, 4, "ref_logps"))) return e;
+  if (fwd && po) {
+    if ((e = check_pointer(po->old_logps, T, 4, "old_logps"))) return e;
+    if ((e = check_pointer(po->advantages, T, 4, "advantages"))) return e;
+  }
+  if (pr) {
+    if ((e = check_pointer(pr->offsets, 0, 8, "offsets"))) return e;
+    if (fwd && (e = check_pointer(pr->counts, each, 4, "counts"))) return e;
+  }
+  const int64_t offsets = pr ? 8 * (each + 1) : 0;
   const Span spans[] = {
       {p->hidden, T, D * es, p->hidden_stride * es, "hidden", false},
       {p->weight, V, D * es, p->weight_stride * es, "weight", false},
       {p->labels, 1, 8 * T, 8 * T, "labels", false},
       {distill ? p->teacher_ids : nullptr, 1, 8 * T * p->teacher_k, 8 * T * p->teacher_k, "teacher_ids", false},
       {distill ? p->teacher_logits : nullptr, 1, 4 * T * p->teacher_k, 4 * T * p->teacher_k, "teacher_logits", false},
-      {fwd ? p->loss : nullptr, 1, 4 * T, 4 * T, "loss", true},
+      {fwd ? p->loss : nullptr, 1, 4 * losses, 4 * losses, "loss", true},
       {ce ? p->lse : nullptr, 1, 4 * T, 4 * T, "lse", fwd},
       {distill ? p->lse_tau : nullptr, 1, 4 * T, 4 * T, "lse_tau", fwd},
       {fwd && reduce ? p->reduced : nullptr, 1, 4, 4, "reduced", true},
-      {bwd ? p->dloss : nullptr, 1, reduce ? 4 : 4 * T, reduce ? 4 : 4 * T, "dloss", false},
+      {bwd ? p->dloss : nullptr, 1, reduce ? 4 : 4 * losses, reduce ? 4 : 4 * losses, "dloss", false},
       {bwd ? p->dhidden : nullptr, T, D * es, p->dhidden_stride * es, "dhidden", true},
       {bwd ? p->dweight : nullptr, V, D * es, p->dweight_stride * es, "dweight", true},
+      {fwd && po ? po->old_logps : nullptr, 1, 4 * T, 4 * T, "old_logps", false},
+      {fwd && po ? po->advantages : nullptr, 1, 4 * T, 4 * T, "advantages", false},
+      {ref, 1, 4 * each, 4 * each, "ref_logps", false},
+      {pr ? pr->offsets : nullptr, 1, offsets, offsets, "offsets", false},
+      {logps, 1, 4 * each, 4 * each, "logps", true},
+      {slopes, 1, 4 * each, 4 * each, "slopes", fwd},
+      {fwd && pr ? pr->counts : nullptr, 1, 4 * each, 4 * each, "counts", true},
       {p->workspace, 1, p->workspace_bytes, p->workspace_bytes, "workspace", true}};
   const int n = int(sizeof(spans) / sizeof(spans[0]));
-  for (int i = 0; i < n; ++i)
+  for (int i = 0; i < n; ++i) {
+    if (!spans[i].p) continue;
     for (int j = 0; j < i; ++j)
       if ((spans[i].written || spans[j].written) && overlap(spans[i], spans[j]))
         return set_error(ZERO_EINVAL, "buffers overlap (%s and %s)", spans[j].what, spans[i].what);
+  }
   return ZERO_OK;
 }
 
@@ -145,9 +220,11 @@ bool weight_in_place(const zero_head_loss_t* p) {
          p->weight_stride % 8 == 0 && p->weight_stride < (int64_t(1) << 39);
 }
 
-int plan(const zero_head_loss_t* p, bool distill, int pass, Args* a, __nv_bfloat16** packed_weight,
-         int64_t* bytes) {
+int plan(const Problem& problem, int pass, Args* a, __nv_bfloat16** packed_weight, int64_t* bytes) {
+  const zero_head_loss_t* p = problem.p;
+  const bool distill = problem.distill();
   *a = Args{};
+  a->kind = problem.kind;
   a->T = p->T;
   a->V = p->V;
   a->D = p->D;
@@ -180,6 +257,31 @@ int plan(const zero_head_loss_t* p, bool distill, int pass, Args* a, __nv_bfloat
   a->lse_tau = p->lse_tau;
   a->reduced = p->reduced;
   a->dloss = p->dloss;
+  a->row_scale = p->reduction == ZERO_REDUCE_NONE ? p->dloss : nullptr;
+  if (const zero_policy_t* q = problem.policy) {
+    a->old_logps = q->old_logps;
+    a->advantages = q->advantages;
+    a->ref_logps = q->ref_logps;
+    a->low = 1.0 - q->clip_low;
+    a->high = 1.0 + q->clip_high;
+    a->kl_weight = q->kl_weight;
+    a->logps = q->logps;
+    a->slopes = q->slopes;
+  }
+  if (const zero_preference_t* q = problem.preference) {
+    a->pairs = q->pairs;
+    a->offsets = q->offsets;
+    a->ref_logps = q->ref_logps;
+    a->squared = q->kind == ZERO_PREFERENCE_SQUARED;
+    a->average = q->average != 0;
+    a->beta = q->beta;
+    a->smoothing = q->smoothing;
+    a->margin = q->margin;
+    a->nll_weight = q->nll_weight;
+    a->logps = q->logps;
+    a->slopes = q->slopes;
+    a->seq_counts = q->counts;
+  }
   a->dhidden = p->dhidden;
   a->dhidden_stride = p->dhidden_stride;
   a->dweight = p->dweight;
@@ -195,6 +297,7 @@ int plan(const zero_head_loss_t* p, bool distill, int pass, Args* a, __nv_bfloat
   a->ids = w.take<int32_t>(a->T, a->L);
   a->weights = w.take<float>(a->T, a->L);
   if (a->K) a->starts = w.take<uint16_t>(2 * a->tiles + 1, a->T);
+  if (problem.slopes() && (pass & kBackward)) a->row_scale = a->scales = w.take<float>(a->T);
   a->hp = w.take<__nv_bfloat16>(a->Tp * a->planes, a->Dp);
   if (weight_in_place(p)) {
     *packed_weight = nullptr;
@@ -242,6 +345,7 @@ int plan(const zero_head_loss_t* p, bool distill, int pass, Args* a, __nv_bfloat
   const int64_t common = w.at;
   a->sums = w.take<double>(zl::kLossBlocks);
   a->zent = w.take<float>(a->T, a->L);
+  if (problem.preference) a->row_logps = w.take<double>(a->T);
   if (a->has_ce) a->stats = w.take<float2>(2 * a->tiles, a->Tp);
   if (a->has_kd) a->stats_tau = w.take<float2>(2 * a->tiles, a->Tp);
   int64_t most = w.at;
@@ -319,19 +423,22 @@ bool make_program(const Args& a, bool backward, Program* p) {
   return ok;
 }
 
-int workspace_bytes(const zero_head_loss_t* p, bool distill, int64_t* bytes) {
+int workspace_bytes(const Problem& problem, int64_t* bytes) {
   if (!bytes) return set_error(ZERO_EINVAL, "bytes is NULL");
-  if (int e = check_sizes(p, distill)) return e;
+  if (int e = check_sizes(problem)) return e;
   Args a;
   __nv_bfloat16* packed;
-  zero_head_loss_t q = *p;
+  zero_head_loss_t q = *problem.p;
   q.workspace = nullptr;
-  return plan(&q, distill, kForward | (p->dhidden || p->dweight ? kBackward : 0), &a, &packed, bytes);
+  Problem without = problem;
+  without.p = &q;
+  return plan(without, kForward | (q.dhidden || q.dweight ? kBackward : 0), &a, &packed, bytes);
 }
 
-int run(const zero_head_loss_t* p, bool distill, int pass, cudaStream_t s) {
-  if (int e = check_sizes(p, distill)) return e;
-  if (int e = check_buffers(p, distill, pass)) return e;
+int run(const Problem& problem, int pass, cudaStream_t s) {
+  if (int e = check_sizes(problem)) return e;
+  if (int e = check_buffers(problem, pass)) return e;
+  const zero_head_loss_t* p = problem.p;
   if (!p->dhidden && !p->dweight) pass &= ~kBackward;  // without rows: an empty dhidden, if any
   if (!pass) return ZERO_OK;
   if (reinterpret_cast<uintptr_t>(p->workspace) % 256)
@@ -339,7 +446,7 @@ int run(const zero_head_loss_t* p, bool distill, int pass, cudaStream_t s) {
   Args a;
   __nv_bfloat16* packed;
   int64_t bytes = 0;
-  if (int e = plan(p, distill, pass, &a, &packed, &bytes)) return e;
+  if (int e = plan(problem, pass, &a, &packed, &bytes)) return e;
   if (!p->workspace || p->workspace_bytes < bytes)
     return set_error(ZERO_EINVAL, "the workspace has %lld bytes, %lld are needed",
                      (long long)(p->workspace ? p->workspace_bytes : 0), (long long)bytes);
@@ -362,13 +469,22 @@ int run(const zero_head_loss_t* p, bool distill, int pass, cudaStream_t s) {
     what = name;
     e = launch();
   };
-  next("packing", [&] { return zl::launch_pack(a, packed, s); });
+  if (problem.slopes() && !(pass & kForward)) {
+    next("scales", [&] { return zl::launch_scales(a, s); });
+    next("rows with a slope", [&] { return zl::launch_sloped_rows(a, s); });
+  }
+  next("packing", [&] { return zl::launch_pack(a, packed, false, s); });
   if (pass & kForward) {
     program.forward = 1;
     program.counter = a.counters;
     program.withheld = withheld.passes & kForward ? a.never : nullptr;
     next("logits", [&] { return zl::launch_products(a, program, device, sms, s); });
     next("losses", [&] { return zl::launch_losses(a, s); });
+    if (problem.preference) next("pairs", [&] { return zl::launch_pairs(a, s); });
+    if (problem.slopes() && (pass & kBackward)) {
+      next("rows with a slope", [&] { return zl::launch_sloped_rows(a, s); });
+      next("packing", [&] { return zl::launch_pack(a, nullptr, true, s); });
+    }
   }
   if (pass & kBackward) {
     program.forward = 0;
@@ -388,28 +504,52 @@ int run(const zero_head_loss_t* p, bool distill, int pass, cudaStream_t s) {
 extern "C" {
 
 int zero_xent_workspace_bytes(const zero_head_loss_t* p, int64_t* bytes) {
-  return workspace_bytes(p, false, bytes);
-}
-int zero_distill_workspace_bytes(const zero_head_loss_t* p, int64_t* bytes) {
-  return workspace_bytes(p, true, bytes);
+  return workspace_bytes(Problem{p, zl::kXent}, bytes);
 }
 int zero_xent_forward(const zero_head_loss_t* p, zero_stream_t stream) {
-  return run(p, false, kForward, stream);
+  return run(Problem{p, zl::kXent}, kForward, stream);
 }
 int zero_xent_backward(const zero_head_loss_t* p, zero_stream_t stream) {
-  return run(p, false, kBackward, stream);
+  return run(Problem{p, zl::kXent}, kBackward, stream);
 }
 int zero_xent_step(const zero_head_loss_t* p, zero_stream_t stream) {
-  return run(p, false, kForward | kBackward, stream);
+  return run(Problem{p, zl::kXent}, kForward | kBackward, stream);
+}
+int zero_distill_workspace_bytes(const zero_head_loss_t* p, int64_t* bytes) {
+  return workspace_bytes(Problem{p, zl::kDistill}, bytes);
 }
 int zero_distill_forward(const zero_head_loss_t* p, zero_stream_t stream) {
-  return run(p, true, kForward, stream);
+  return run(Problem{p, zl::kDistill}, kForward, stream);
 }
 int zero_distill_backward(const zero_head_loss_t* p, zero_stream_t stream) {
-  return run(p, true, kBackward, stream);
+  return run(Problem{p, zl::kDistill}, kBackward, stream);
 }
 int zero_distill_step(const zero_head_loss_t* p, zero_stream_t stream) {
-  return run(p, true, kForward | kBackward, stream);
+  return run(Problem{p, zl::kDistill}, kForward | kBackward, stream);
+}
+int zero_policy_workspace_bytes(const zero_head_loss_t* p, const zero_policy_t* q, int64_t* bytes) {
+  return workspace_bytes(Problem{p, zl::kPolicy, q}, bytes);
+}
+int zero_policy_forward(const zero_head_loss_t* p, const zero_policy_t* q, zero_stream_t stream) {
+  return run(Problem{p, zl::kPolicy, q}, kForward, stream);
+}
+int zero_policy_backward(const zero_head_loss_t* p, const zero_policy_t* q, zero_stream_t stream) {
+  return run(Problem{p, zl::kPolicy, q}, kBackward, stream);
+}
+int zero_policy_step(const zero_head_loss_t* p, const zero_policy_t* q, zero_stream_t stream) {
+  return run(Problem{p, zl::kPolicy, q}, kForward | kBackward, stream);
+}
+int zero_preference_workspace_bytes(const zero_head_loss_t* p, const zero_preference_t* q, int64_t* bytes) {
+  return workspace_bytes(Problem{p, zl::kPreference, nullptr, q}, bytes);
+}
+int zero_preference_forward(const zero_head_loss_t* p, const zero_preference_t* q, zero_stream_t stream) {
+  return run(Problem{p, zl::kPreference, nullptr, q}, kForward, stream);
+}
+int zero_preference_backward(const zero_head_loss_t* p, const zero_preference_t* q, zero_stream_t stream) {
+  return run(Problem{p, zl::kPreference, nullptr, q}, kBackward, stream);
+}
+int zero_preference_step(const zero_head_loss_t* p, const zero_preference_t* q, zero_stream_t stream) {
+  return run(Problem{p, zl::kPreference, nullptr, q}, kForward | kBackward, stream);
 }
 int zero_debug_withhold_head_loss(int32_t passes, int64_t limit_ns) {
   if (passes < 0 || passes > 3) return set_error(ZERO_EINVAL, "passes=%d is not in [0, 3]", passes);

@@ -26,12 +26,19 @@ constexpr int kSms = 152;        // GB300's multiprocessors. (The layout is plan
 constexpr int kBuffers = 3;      // of G
 constexpr int kLossBlocks = 608; // most blocks of the losses' kernel
 
+// Which loss a call takes.
+enum Kind : int32_t { kXent, kDistill, kPolicy, kPreference };
+
 // Device-side scalars of a call, at the start of the workspace.
 struct Head {
-  int32_t rows;    // rows with a target (the compact rows)
+  int32_t rows;    // rows with a target (the compact rows); of a backward pass that goes by
+                   // slopes, those whose slope is not zero
   int32_t ticket;  // blocks of the reduction that are done
-  int32_t fault;   // a wait of the matrix kernel ran out: what the call writes becomes NaN
+  int32_t fault;   // a wait of the matrix kernel ran out, or a preference call's offsets do not
+                   // ascend: what the call writes becomes NaN
   float factor;    // of both gradients, the same for every row
+  int32_t pairs;   // pairs that are not empty
+  int32_t repack;  // the backward pass has other rows than the forward pass
 };
 
 // Everything the kernels read or write. Rows with a target are packed densely:
@@ -67,20 +74,40 @@ struct Args {
   float* lse_tau;
   float* reduced;
   const float* dloss;
+  const float* row_scale; // [T] factor of each row's gradient, or NULL: dloss where it has an entry a
+                          // row, or (in the workspace, `scales`) less the loss's slope by the label's
+                          // log-probability
   void* dhidden;
   int64_t dhidden_stride;
   void* dweight;
   int64_t dweight_stride;
 
+  // The policy and the preference loss.
+  Kind kind;
+  const float* old_logps;
+  const float* advantages;
+  const float* ref_logps; // [T], [2 pairs] or NULL
+  double low, high;       // bounds of the ratio
+  double kl_weight;
+  int64_t pairs;
+  const int64_t* offsets; // [2 pairs + 1], or NULL: sequences of equal length
+  int32_t squared, average;
+  double beta, smoothing, margin, nll_weight;
+  float* logps;           // [T] or [2 pairs]
+  float* slopes;
+  int32_t* seq_counts;    // [2 pairs] labelled rows
+
   // workspace
   Head* head;
-  int32_t* rowpos;        // [T] the row's compact row, -1 for an empty row
+  int32_t* rowpos;        // [T] the row's compact row, -1 for an empty row, -2 for one without a slope
   int32_t* rowmap;        // [Tp] the compact row's row
   float2* coef;           // [T] (ce or 0, kd or 0)
   float* konst;           // [T] the loss's part that no logit enters
   int32_t* ids;           // [T][L] ascending, kNoId after the last
   float* weights;         // [T][L] weight of each entry's logit in loss and gradient
   uint16_t* starts;       // distillation: [2 tiles + 1][T] first entry of each half tile
+  float* scales;          // [T] row_scale of a call that goes by slopes
+  double* row_logps;      // [T] a preference call's labels' log-probabilities
   double* sums;           // [kLossBlocks] parts of the reduced loss
   float* zent;            // [T][L] logits of the entries
   __nv_bfloat16* hp;      // [planes][Tp][Dp] packed hidden states
@@ -121,8 +148,15 @@ struct Program {
 // Prepares and numbers the rows.
 cudaError_t launch_rows(const Args& a, cudaStream_t s);
 // Rows with a target side by side, and the weight's rows to `weight` (NULL: read in place).
-cudaError_t launch_pack(const Args& a, __nv_bfloat16* weight, cudaStream_t s);
+// `again`: the rows of the backward pass of a step, where they are others.
+cudaError_t launch_pack(const Args& a, __nv_bfloat16* weight, bool again, cudaStream_t s);
 cudaError_t launch_losses(const Args& a, cudaStream_t s);
+// The preference loss of the pairs from their rows' log-probabilities.
+cudaError_t launch_pairs(const Args& a, cudaStream_t s);
+// A backward call's scales from the slopes that it is given.
+cudaError_t launch_scales(const Args& a, cudaStream_t s);
+// Numbers the rows that have a slope.
+cudaError_t launch_sloped_rows(const Args& a, cudaStream_t s);
 // dhidden from its sums; a call whose waits ran out is marked.
 cudaError_t launch_dhidden_out(const Args& a, cudaStream_t s);
 // The mark alone, where there is no dhidden to write.

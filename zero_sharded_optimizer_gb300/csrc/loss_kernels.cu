@@ -1,4 +1,5 @@
-// Kernels of the vocabulary losses (zero_xent_*, zero_distill_*).
+// Kernels of the vocabulary losses (zero_xent_*, zero_distill_*, zero_policy_*,
+// zero_preference_*).
 #include <math.h>
 
 #include "loss_device.cuh"
@@ -44,8 +45,10 @@ __device__ __forceinline__ void finish_row(const Args& a, int64_t t, bool has_y,
   a.konst[t] = konst;
   a.coef[t] = make_float2(has_y ? a.ce : 0.0f, has_kd ? a.kd : 0.0f);
   a.rowpos[t] = has_y || has_kd ? 0 : -1;
+  if (a.scales) a.scales[t] = 0.0f;
   if (a.forward && !(has_y || has_kd)) {
-    a.loss[t] = 0.0f;
+    if (a.kind != kPreference) a.loss[t] = 0.0f;
+    if (a.kind == kPolicy) a.logps[t] = a.slopes[t] = 0.0f;
     if (a.has_ce) a.lse[t] = 0.0f;
     if (a.has_kd) a.lse_tau[t] = 0.0f;
   }
@@ -266,27 +269,48 @@ __device__ __forceinline__ void pack_rows(const Args& a, int32_t rows, bool vect
   }
 }
 
-// One block: numbers the rows that have a target, in order, up to 16 times
-// 1024 rows at a time. With `Prepare` (few rows, labels alone) it prepares them
-// first: a launch saved.
-template <bool Prepare>
+// Whether a preference call's offsets ascend within the rows (all threads of the block).
+__device__ __forceinline__ bool offsets_ascend(const Args& a) {
+  bool good = true;
+  if (a.kind == kPreference && a.offsets) {
+    for (int64_t n = threadIdx.x; n <= 2 * a.pairs; n += blockDim.x) {
+      const int64_t x = a.offsets[n];
+      good &= x >= 0 && x <= a.T && (n == 0 || a.offsets[n - 1] <= x);
+    }
+  }
+  return __syncthreads_and(good);
+}
+
+// Which rows number_rows_kernel numbers: those with a target, prepared before or
+// (few rows, labels alone: a launch saved) by itself, or those with a slope.
+enum Numbering { kTargets, kPrepare, kSlopes };
+
+// One block: numbers the rows in order, up to 16 times 1024 rows at a time.
+template <Numbering N>
 __global__ void __launch_bounds__(1024) number_rows_kernel(const Args a) {
-  __shared__ int32_t before[16][32], total[16];
+  __shared__ int32_t before[16][32], total[16], labelled[32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   let_next_start();
-  if (!Prepare) wait_for_previous();
-  if (Prepare) {
+  if (N != kPrepare) wait_for_previous();
+  if (N == kPrepare) {
     for (int64_t t = threadIdx.x; t < a.T; t += 1024) prepare_label(a, t);
     __syncthreads();
   }
-  for (int64_t n = threadIdx.x; n < a.zeros; n += 1024) a.counters[n] = 0;
-  int32_t base = 0;
+  if (N != kSlopes)
+    for (int64_t n = threadIdx.x; n < a.zeros; n += 1024) a.counters[n] = 0;
+  const bool ascend = N == kSlopes || offsets_ascend(a);
+  int32_t base = 0, targets = 0;
   for (int64_t t0 = 0; t0 < a.T; t0 += 16 * 1024) {
     uint32_t mask[16];
 #pragma unroll
     for (int q = 0; q < 16; ++q) {
       const int64_t t = t0 + 1024 * q + threadIdx.x;
       mask[q] = t < a.T && a.rowpos[t] >= 0;
+      if (N == kSlopes && mask[q]) {
+        ++targets;
+        mask[q] = a.scales[t] != 0.0f;  // (also a NaN)
+        if (!mask[q]) a.rowpos[t] = -2;
+      }
     }
 #pragma unroll
     for (int q = 0; q < 16; ++q) {
@@ -317,13 +341,30 @@ __global__ void __launch_bounds__(1024) number_rows_kernel(const Args a) {
     }
     __syncthreads();
   }
+  if (N == kSlopes) {
+    for (int o = 16; o; o >>= 1) targets += __shfl_xor_sync(~0u, targets, o);
+    if (lane == 0) labelled[warp] = targets;
+    __syncthreads();
+  }
   if (threadIdx.x == 0) {
+    if (N == kSlopes) {
+      targets = 0;
+      for (int w = 0; w < 32; ++w) targets += labelled[w];
+    } else {
+      targets = base;
+    }
     // The factor of both gradients that does not depend on the row: grad_scale,
     // the mean's count, and the reduced loss's own gradient.
     double f = a.grad_scale;
-    if (a.reduction == ZERO_REDUCE_MEAN) f /= double(max(1, base));
+    if (a.reduction == ZERO_REDUCE_MEAN) f /= double(max(1, N == kSlopes && a.kind == kPreference ? a.head->pairs : targets));
     if (a.reduction != ZERO_REDUCE_NONE && a.dloss) f *= double(*a.dloss);
-    *a.head = Head{base, 0, 0, float(f)};
+    if (N == kSlopes) {
+      a.head->repack = a.head->rows != base;
+      a.head->rows = base;
+      a.head->factor = float(f);
+    } else {
+      *a.head = Head{base, 0, !ascend, float(f), 0, 0};
+    }
   }
 }
 
@@ -331,7 +372,7 @@ __global__ void __launch_bounds__(1024) number_rows_kernel(const Args a) {
 // kernels before), and the rows with a target.
 template <bool F32>
 __global__ void __launch_bounds__(256) pack_kernel(const Args a, __nv_bfloat16* packed_weight, bool hidden_vector,
-                                                   bool weight_vector) {
+                                                   bool weight_vector, bool again) {
   let_next_start();
   const int32_t wide = int32_t(a.Dp / 8);
   const int64_t first = int64_t(blockIdx.x) * 256 + threadIdx.x, step = int64_t(gridDim.x) * 256;
@@ -343,7 +384,7 @@ __global__ void __launch_bounds__(256) pack_kernel(const Args a, __nv_bfloat16* 
     }
   }
   wait_for_previous();
-  pack_rows<F32>(a, a.head->rows, hidden_vector, first, step);
+  if (!again || a.head->repack) pack_rows<F32>(a, a.head->rows, hidden_vector, first, step);
 }
 
 // Where a wait of the matrix kernel ran out, the call's results become NaN --
@@ -359,10 +400,15 @@ __device__ __noinline__ void mark_fault(const Args& a, bool f32, int64_t first, 
   }
   if (!a.forward) return;
   for (int64_t t = first; t < a.T; t += step) {
-    if (a.rowpos[t] < 0) continue;
-    a.loss[t] = NAN;
+    if (a.rowpos[t] == -1) continue;
+    if (a.kind != kPreference) a.loss[t] = NAN;
+    if (a.kind == kPolicy) a.logps[t] = a.slopes[t] = NAN;
     if (a.has_ce) a.lse[t] = NAN;
     if (a.has_kd) a.lse_tau[t] = NAN;
+  }
+  if (a.kind == kPreference) {
+    for (int64_t i = first; i < a.pairs; i += step) a.loss[i] = NAN;
+    for (int64_t i = first; i < 2 * a.pairs; i += step) a.logps[i] = a.slopes[i] = NAN;
   }
   if (first == 0 && a.reduction != ZERO_REDUCE_NONE) *a.reduced = NAN;
 }
@@ -411,7 +457,7 @@ __global__ void __launch_bounds__(256) dhidden_out_kernel(const Args a) {
       __syncthreads();
     }
     if (lane > 0 || d >= a.D) continue;
-    if (i >= 0) x = make_float4(f * x.x, f * x.y, f * x.z, f * x.w);
+    if (i >= 0 || (fault && i < -1)) x = make_float4(f * x.x, f * x.y, f * x.z, f * x.w);
     const int64_t at = t * a.dhidden_stride + d;
     const float v[4] = {x.x, x.y, x.z, x.w};
     if (F32) {
@@ -485,10 +531,86 @@ __device__ __forceinline__ double row_lse(const float2* stats, int64_t count, in
   return lane == 0 ? (double(x.x) + log2(double(x.y))) * 0.69314718055994530942 : 0.0;
 }
 
+// The product of the row's hidden state and its label's weight in fp32, rounded
+// at every addition: a warp's lanes take every 32nd group of elements.
+template <bool F32>
+__device__ __forceinline__ float label_logit(const Args& a, int64_t t, int32_t y, bool vector, int lane) {
+  constexpr int kWide = F32 ? 4 : 8;
+  float sum[kWide] = {};
+  const int64_t ho = t * a.hidden_stride, wo = y * a.weight_stride;
+  if (F32) {
+    const float *h = static_cast<const float*>(a.hidden) + ho, *w = static_cast<const float*>(a.weight) + wo;
+    if (vector) {
+#pragma unroll 4
+      for (int64_t k = lane * 4; k + 4 <= a.D; k += 128) {
+        const float4 x = *reinterpret_cast<const float4*>(h + k), z = *reinterpret_cast<const float4*>(w + k);
+        sum[0] = fmaf(x.x, z.x, sum[0]);
+        sum[1] = fmaf(x.y, z.y, sum[1]);
+        sum[2] = fmaf(x.z, z.z, sum[2]);
+        sum[3] = fmaf(x.w, z.w, sum[3]);
+      }
+    }
+    for (int64_t k = (vector ? a.D / 4 * 4 : 0) + lane; k < a.D; k += 32) sum[0] = fmaf(h[k], w[k], sum[0]);
+  } else {
+    const __nv_bfloat16 *h = static_cast<const __nv_bfloat16*>(a.hidden) + ho,
+                        *w = static_cast<const __nv_bfloat16*>(a.weight) + wo;
+    if (vector) {
+#pragma unroll 4
+      for (int64_t k = lane * 8; k + 8 <= a.D; k += 256) {
+        const uint4 x = *reinterpret_cast<const uint4*>(h + k), z = *reinterpret_cast<const uint4*>(w + k);
+        const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, zs[4] = {z.x, z.y, z.z, z.w};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          sum[2 * q] = fmaf(__uint_as_float(xs[q] << 16), __uint_as_float(zs[q] << 16), sum[2 * q]);
+          sum[2 * q + 1] = fmaf(__uint_as_float(xs[q] & 0xffff0000u), __uint_as_float(zs[q] & 0xffff0000u),
+                                sum[2 * q + 1]);
+        }
+      }
+    }
+    for (int64_t k = (vector ? a.D / 8 * 8 : 0) + lane; k < a.D; k += 32)
+      sum[0] = fmaf(float(h[k]), float(w[k]), sum[0]);
+  }
+#pragma unroll
+  for (int n = kWide / 2; n; n /= 2)
+#pragma unroll
+    for (int q = 0; q < n; ++q) sum[q] += sum[q + n];
+  return warp_sum(sum[0]);
+}
+
+// The policy loss of a row and its slope by the log-probability l. What is not a
+// number stays none (maxima by comparison, not by fmax). An advantage of zero
+// has no part in the loss, whatever the ratio.
+__device__ __forceinline__ void policy_loss(const Args& a, int64_t t, float l, double* loss, double* slope) {
+  *loss = *slope = 0.0;
+  const double adv = double(a.advantages[t]);
+  if (adv != 0.0) {
+    const double ratio = exp(double(l) - double(a.old_logps[t]));
+    const double bounded = ratio < a.low ? a.low : ratio > a.high ? a.high : ratio;
+    const double free = -adv * ratio, held = -adv * bounded;
+    *loss = free < held ? held : free;
+    *slope = free < held ? 0.0 : free;
+  }
+  if (a.kl_weight != 0.0) {
+    const double d = double(a.ref_logps[t]) - double(l), e = expm1(d);
+    *loss += a.kl_weight * (e - d);
+    *slope -= a.kl_weight * e;
+  }
+}
+
 // 256 threads: `block_rows` rows (a power of two, up to 32), 256 / block_rows lanes each.
-__global__ void __launch_bounds__(256) losses_kernel(const Args a, int block_rows) {
+//
+// `Slopes` (the policy and the preference loss): a row's log-probability, of
+// which those losses are functions, instead of a loss that is its negative. Such
+// a loss hangs on small differences of log-probabilities, and a preference loss
+// on sums of many, so what the tensor cores' truncating sums take from a large
+// logit of the label counts (up to 8e-6 at a logit of 9 and width 768, always of
+// one sign). The label's logit is therefore taken again in rounding fp32, and
+// its share of the log-sum-exp corrected: log(S + e^z' - e^z).
+template <bool Slopes, bool F32>
+__global__ void __launch_bounds__(256) losses_kernel(const Args a, int block_rows, bool vector) {
   __shared__ float2 sh[256];
   __shared__ double part[256];
+  __shared__ float logit[32];
   __shared__ bool last;
   let_next_start();
   wait_for_previous();
@@ -498,6 +620,14 @@ __global__ void __launch_bounds__(256) losses_kernel(const Args a, int block_row
   for (int64_t i0 = int64_t(blockIdx.x) * block_rows; i0 < rows; i0 += int64_t(gridDim.x) * block_rows) {
     const int64_t i = min(i0 + r, int64_t(rows) - 1);
     const int64_t t = a.rowmap[i];
+    if (Slopes) {
+      for (int q = threadIdx.x >> 5; q < block_rows && i0 + q < rows; q += 8) {
+        const int64_t u = a.rowmap[i0 + q];
+        const float z = label_logit<F32>(a, u, a.ids[u], vector, threadIdx.x & 31);
+        if ((threadIdx.x & 31) == 0) logit[q] = z;
+      }
+      __syncthreads();
+    }
     double entries = 0.0;
 #pragma unroll 4
     for (int e = lane; e < a.L; e += lanes) {
@@ -513,13 +643,32 @@ __global__ void __launch_bounds__(256) losses_kernel(const Args a, int block_row
       if (lane < w) part[threadIdx.x] += part[threadIdx.x + w * block_rows];
       __syncthreads();
     }
-    if (lane == 0 && i0 + r < rows) {
+    const bool fault = a.head->fault;  // NaN in lse too: a backward call's gradients show it then
+    if (Slopes && lane == 0 && i0 + r < rows) {
+      const double z = part[r], more = double(logit[r]) - z;
+      const bool finite = isfinite(more) && isfinite(lse);
+      const double sum = finite ? lse + log1p(exp(z - lse) * expm1(more)) : lse;
+      const double logp = fault ? NAN : (finite ? double(logit[r]) : z) - sum;
+      a.lse[t] = fault ? NAN : float(sum);
+      if (a.kind == kPreference) {
+        a.row_logps[t] = logp;
+      } else {
+        const float l = float(logp);
+        double loss, slope;
+        policy_loss(a, t, l, &loss, &slope);
+        a.loss[t] = fault ? NAN : float(loss);
+        a.logps[t] = l;
+        const float s = fault ? NAN : float(slope);
+        a.slopes[t] = s;
+        if (a.scales) a.scales[t] = -s * (a.reduction == ZERO_REDUCE_NONE && a.dloss ? a.dloss[t] : 1.0f);
+        mine += double(fault ? NAN : float(loss));
+      }
+    } else if (!Slopes && lane == 0 && i0 + r < rows) {
       const float2 f = a.coef[t];
       double loss = double(a.konst[t]);
       if (f.x != 0.0f) loss += double(f.x) * lse;
       if (f.y != 0.0f) loss += double(f.y) * a.tau * lse_tau;
       loss -= part[r];
-      const bool fault = a.head->fault;  // NaN in lse too: a backward call's gradients show it then
       if (fault) loss = NAN;
       a.loss[t] = float(loss);
       if (a.has_ce) a.lse[t] = fault ? NAN : float(lse);
@@ -528,7 +677,7 @@ __global__ void __launch_bounds__(256) losses_kernel(const Args a, int block_row
     }
     __syncthreads();
   }
-  if (a.reduction == ZERO_REDUCE_NONE) return;
+  if (a.reduction == ZERO_REDUCE_NONE || a.kind == kPreference) return;
   // Each block's sum in a fixed order; the last block to finish adds the blocks'.
   part[threadIdx.x] = mine;  // zero but for the rows' first lanes
   __syncthreads();
@@ -553,6 +702,156 @@ __global__ void __launch_bounds__(256) losses_kernel(const Args a, int block_row
     *a.reduced = float(a.reduction == ZERO_REDUCE_MEAN ? part[0] / double(max(1, rows)) : part[0]);
 }
 
+// ------------------------------------------------------------------- pairs --
+
+// The sum over the block's 256 threads, in a fixed order, in all of them.
+__device__ __forceinline__ double block_sum(double x, double* sh) {
+  sh[threadIdx.x] = x;
+  __syncthreads();
+  for (int w = 128; w; w >>= 1) {
+    if (int(threadIdx.x) < w) sh[threadIdx.x] += sh[threadIdx.x + w];
+    __syncthreads();
+  }
+  const double sum = sh[0];
+  __syncthreads();
+  return sum;
+}
+
+// The loss of a pair and its slopes by each of its rows' log-probabilities, from
+// the sequences' sums over n[k] labelled rows.
+__device__ __forceinline__ void pair_loss(const Args& a, int64_t i, const double (&sum)[2], const int (&n)[2],
+                                          double* loss, double (&slope)[2]) {
+  double x[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    x[k] = a.average ? sum[k] / max(1, n[k]) : sum[k];
+    if (a.ref_logps) x[k] -= double(a.ref_logps[i + k * a.pairs]);
+  }
+  const double u = a.beta * (x[0] - x[1]) - a.margin;
+  double du;
+  if (a.squared) {
+    *loss = u * u;
+    du = 2.0 * u;
+  } else {
+    // log(1 + e^-u) and log(1 + e^u), and sigmoid(-u), from e^-|u|
+    const double e = exp(-fabs(u)), l = log1p(e), down = (u < 0.0 ? 1.0 : e) / (1.0 + e);
+    *loss = (1.0 - a.smoothing) * ((u < 0.0 ? -u : 0.0) + l) + a.smoothing * ((u > 0.0 ? u : 0.0) + l);
+    if (u != u) *loss = u;
+    du = a.smoothing - down;
+  }
+#pragma unroll
+  for (int k = 0; k < 2; ++k) slope[k] = (k ? -du : du) * a.beta / (a.average ? max(1, n[k]) : 1);
+  if (a.nll_weight != 0.0 && n[0] > 0) {
+    *loss -= a.nll_weight * sum[0] / n[0];
+    slope[0] -= a.nll_weight / n[0];
+  }
+}
+
+// A block for each pair (in turn). `Forward`: sums, losses and slopes, else the
+// slopes are given; then the rows' scales where a backward pass follows.
+template <bool Forward>
+__global__ void __launch_bounds__(256) pairs_kernel(const Args a) {
+  __shared__ double sh[256];
+  __shared__ float slopes[2];
+  __shared__ bool last;
+  let_next_start();
+  wait_for_previous();
+  const bool fault = a.head->fault;
+  if (fault) {
+    // The offsets may point anywhere: nothing is read by them.
+    const int64_t first = int64_t(blockIdx.x) * 256 + threadIdx.x, step = int64_t(gridDim.x) * 256;
+    if (a.scales)
+      for (int64_t t = first; t < a.T; t += step)
+        if (a.rowpos[t] >= 0) a.scales[t] = NAN;
+    if (Forward) {
+      for (int64_t t = first; t < a.T; t += step)
+        if (a.rowpos[t] >= 0) a.lse[t] = NAN;
+      for (int64_t i = first; i < a.pairs; i += step) a.loss[i] = NAN;
+      for (int64_t i = first; i < 2 * a.pairs; i += step) {
+        a.logps[i] = a.slopes[i] = NAN;
+        a.seq_counts[i] = 0;
+      }
+      if (first == 0 && a.reduction != ZERO_REDUCE_NONE) *a.reduced = NAN;
+    }
+    return;
+  }
+  double mine = 0.0;
+  const int64_t length = a.offsets || a.pairs == 0 ? 0 : a.T / (2 * a.pairs);
+  for (int64_t i = blockIdx.x; i < a.pairs; i += gridDim.x) {
+    int64_t begin[2], end[2];
+    double sum[2] = {};
+    int n[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int64_t s = i + k * a.pairs;
+      begin[k] = a.offsets ? a.offsets[s] : s * length;
+      end[k] = a.offsets ? a.offsets[s + 1] : (s + 1) * length;
+      int count = 0;
+#pragma unroll 4
+      for (int64_t t = begin[k] + threadIdx.x; t < end[k]; t += 256) {
+        if (a.rowpos[t] < 0) continue;
+        ++count;
+        if (Forward) sum[k] += a.row_logps[t];
+      }
+      n[k] = int(block_sum(double(count), sh));
+      if (Forward) sum[k] = block_sum(sum[k], sh);
+    }
+    const bool some = n[0] + n[1] > 0;
+    if (threadIdx.x == 0) {
+      if (some) atomicAdd(&a.head->pairs, 1);
+      double loss = 0.0, slope[2] = {};
+      if (Forward) {
+        if (some) pair_loss(a, i, sum, n, &loss, slope);
+        a.loss[i] = float(loss);
+        mine += double(float(loss));
+      }
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int64_t s = i + k * a.pairs;
+        if (Forward) {
+          a.logps[s] = float(sum[k]);
+          a.seq_counts[s] = n[k];
+          a.slopes[s] = n[k] ? float(slope[k]) : 0.0f;
+        }
+        slopes[k] = n[k] ? (Forward ? float(slope[k]) : a.slopes[s]) : 0.0f;
+      }
+    }
+    __syncthreads();
+    if (a.scales && some) {
+      const float d = a.reduction == ZERO_REDUCE_NONE && a.dloss ? a.dloss[i] : 1.0f;
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        for (int64_t t = begin[k] + threadIdx.x; t < end[k]; t += 256)
+          if (a.rowpos[t] >= 0) a.scales[t] = -slopes[k] * d;
+    }
+    __syncthreads();
+  }
+  if (!Forward || a.reduction == ZERO_REDUCE_NONE) return;
+  // The blocks' sums in order, by the last block to finish.
+  if (threadIdx.x == 0) {
+    a.sums[blockIdx.x] = mine;
+    __threadfence();
+    last = atomicAdd(&a.head->ticket, 1) == int32_t(gridDim.x) - 1;
+  }
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
+  double sum = 0.0;
+  for (int b = threadIdx.x; b < int(gridDim.x); b += 256) sum += __ldcg(a.sums + b);
+  sum = block_sum(sum, sh);
+  if (threadIdx.x == 0)
+    *a.reduced = float(a.reduction == ZERO_REDUCE_MEAN ? sum / double(max(1, __ldcg(&a.head->pairs))) : sum);
+}
+
+// The rows' scales of a policy's backward call.
+__global__ void __launch_bounds__(256) scales_kernel(const Args a) {
+  let_next_start();
+  wait_for_previous();
+  const int64_t t = int64_t(blockIdx.x) * 256 + threadIdx.x;
+  if (t < a.T && a.rowpos[t] >= 0)
+    a.scales[t] = -a.slopes[t] * (a.reduction == ZERO_REDUCE_NONE && a.dloss ? a.dloss[t] : 1.0f);
+}
+
 }  // namespace
 
 namespace {
@@ -572,7 +871,7 @@ cudaError_t launch_rows(const Args& a, cudaStream_t s) {
   // 20.9 for 2048; 22.7 and 21.6 for 4096. A call that is waited for (one row,
   // GPT-2-small's head): 67 and 70 us. (Packing the rows there too: 33.4 us
   // instead of 31.2, replayed; 39.1 instead of 39.0 from the host.)
-  if (a.K == 0 && a.T <= 1024) return launch(number_rows_kernel<true>, 1, 1024, 0, s, false, a);
+  if (a.K == 0 && a.T <= 1024) return launch(number_rows_kernel<kPrepare>, 1, 1024, 0, s, false, a);
   cudaError_t e = cudaSuccess;
   if (a.T > 0) {
     if (a.K == 0) {
@@ -587,15 +886,15 @@ cudaError_t launch_rows(const Args& a, cudaStream_t s) {
       e = launch(teacher_rows_kernel, unsigned((a.T + rows - 1) / rows), rows * 32, rows * row, s, false, a);
     }
   }
-  return e != cudaSuccess ? e : launch(number_rows_kernel<false>, 1, 1024, 0, s, a.T > 0, a);
+  return e != cudaSuccess ? e : launch(number_rows_kernel<kTargets>, 1, 1024, 0, s, a.T > 0, a);
 }
 
-cudaError_t launch_pack(const Args& a, __nv_bfloat16* weight, cudaStream_t s) {
+cudaError_t launch_pack(const Args& a, __nv_bfloat16* weight, bool again, cudaStream_t s) {
   const int es = a.planes == 3 ? 4 : 2;
   const bool hv = aligned16(a.hidden, a.hidden_stride * es), wv = aligned16(a.weight, a.weight_stride * es);
   const unsigned blocks = blocks_for((weight && a.V > a.Tp ? a.V : a.Tp) * a.Dp / 8);
-  if (a.planes == 3) return launch(pack_kernel<true>, blocks, 256, 0, s, true, a, weight, hv, wv);
-  return launch(pack_kernel<false>, blocks, 256, 0, s, true, a, weight, hv, wv);
+  if (a.planes == 3) return launch(pack_kernel<true>, blocks, 256, 0, s, true, a, weight, hv, wv, again);
+  return launch(pack_kernel<false>, blocks, 256, 0, s, true, a, weight, hv, wv, again);
 }
 
 cudaError_t launch_losses(const Args& a, cudaStream_t s) {
@@ -603,9 +902,31 @@ cudaError_t launch_losses(const Args& a, cudaStream_t s) {
   // softmaxes and 100 entries: a step of 197 us, 227 with 32 rows a block).
   int rows = 32;
   while (rows > 1 && a.T / rows < kSms) rows /= 2;
-  const int64_t blocks = (a.T + rows - 1) / rows;
-  return launch(losses_kernel, unsigned(blocks < 1 ? 1 : blocks < kLossBlocks ? blocks : kLossBlocks), 256, 0, s,
-                true, a, rows);
+  int64_t blocks = (a.T + rows - 1) / rows;
+  blocks = blocks < 1 ? 1 : blocks < kLossBlocks ? blocks : kLossBlocks;
+  const bool f32 = a.planes == 3;
+  const bool vector = aligned16(a.hidden, a.hidden_stride * (f32 ? 4 : 2)) &&
+                      aligned16(a.weight, a.weight_stride * (f32 ? 4 : 2));
+  auto* kernel = a.kind == kXent || a.kind == kDistill ? losses_kernel<false, false>
+                 : f32 ? losses_kernel<true, true> : losses_kernel<true, false>;
+  return launch(kernel, unsigned(blocks), 256, 0, s, true, a, rows, vector);
+}
+
+cudaError_t launch_pairs(const Args& a, cudaStream_t s) {
+  const int64_t blocks = a.pairs < 1 ? 1 : a.pairs < kLossBlocks ? a.pairs : kLossBlocks;
+  return launch(pairs_kernel<true>, unsigned(blocks), 256, 0, s, true, a);
+}
+
+cudaError_t launch_scales(const Args& a, cudaStream_t s) {
+  if (a.kind == kPreference) {
+    const int64_t blocks = a.pairs < 1 ? 1 : a.pairs < kLossBlocks ? a.pairs : kLossBlocks;
+    return launch(pairs_kernel<false>, unsigned(blocks), 256, 0, s, true, a);
+  }
+  return launch(scales_kernel, unsigned(a.T > 0 ? (a.T + 255) / 256 : 1), 256, 0, s, true, a);
+}
+
+cudaError_t launch_sloped_rows(const Args& a, cudaStream_t s) {
+  return launch(number_rows_kernel<kSlopes>, 1, 1024, 0, s, true, a);
 }
 
 cudaError_t launch_mark(const Args& a, cudaStream_t s) {

@@ -432,7 +432,7 @@ __device__ __forceinline__ Row row_of(const Args& a, int rows, const Unit& u, co
     r.f = a.coef[r.t];
     if (CE) r.lse = a.lse[r.t];
     if (KD) r.lse_kd = a.lse_tau[r.t];
-    r.scale = a.reduction == ZERO_REDUCE_NONE && a.dloss ? a.dloss[r.t] : 1.0f;
+    r.scale = a.row_scale ? a.row_scale[r.t] : 1.0f;
   }
   if (a.K == 0) {
     r.id = a.ids[r.t];

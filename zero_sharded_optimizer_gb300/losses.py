@@ -2,9 +2,11 @@
 their gradients, without ever holding the logits.
 
 ``xent_*`` is softmax cross entropy; ``distill_*`` is distillation from a
-teacher's top-K logits at a temperature, alone or mixed with the cross entropy
-(the definitions, and what an empty row is, stand in ``include/zero_gb300.h``
-at ``zero_head_loss_t``). Each comes as
+teacher's top-K logits at a temperature, alone or mixed with the cross entropy;
+``policy_*`` is the clipped policy loss of sampled tokens, kept near a reference;
+``preference_*`` the loss of pairs of a preferred and a rejected sequence (the
+definitions, and what an empty row is, stand in ``include/zero_gb300.h`` at
+``zero_head_loss_t`` and ``zero_policy_t``). Each comes as
 
 - ``*_forward``: the losses;
 - ``*_backward``: the gradients, from the forward pass's result;
@@ -12,15 +14,16 @@ at ``zero_head_loss_t``). Each comes as
 
 ``hidden`` is a [T, D] (or [..., D]) and ``weight`` a [V, D] CUDA tensor, both
 float32 or both bfloat16, with adjacent elements in a row and any row stride.
-What goes with the rows -- labels, the teacher's entries, ``dloss``, ``lse`` -- has
-hidden's leading dimensions or the rows in one dimension; beside a [T, D]
+What goes with the rows -- labels, the teacher's entries, ``dloss``, ``lse``, what a
+policy loss is given -- has hidden's leading dimensions or the rows in one dimension; beside a [T, D]
 ``hidden`` it may have any leading dimensions, the same for all.
 ``dhidden`` and ``dweight`` may be given as outputs -- for ``dweight`` typically
 the head's view into a rank's flat gradient buffer, which the ZeRO step then
 reads -- and are allocated otherwise; ``accumulate`` adds to ``dweight``.
 
-``linear_cross_entropy`` and ``linear_distillation`` are the same losses as
-differentiable functions for torch.autograd. Their gradients can be part of a
+``linear_cross_entropy``, ``linear_distillation``, ``linear_policy`` and
+``linear_preference`` are the same losses as differentiable functions for
+torch.autograd. Their gradients can be part of a
 graph (``create_graph``), but to differentiate them again raises a RuntimeError.
 
 Work is queued on ``stream``: a ``torch.cuda.Stream``, a raw handle, or None for
@@ -54,6 +57,26 @@ class Losses(NamedTuple):
     dhidden: torch.Tensor | None = None
     dweight: torch.Tensor | None = None
 
+
+class LogpLosses(NamedTuple):
+    """Of the losses that are functions of the labels' log-probabilities: ``loss``
+    float32, of each row (policy; 0 for an empty row) or of each pair
+    (preference); ``reduced`` as in Losses; ``logps`` the log-probabilities of
+    the rows, or their sums over each sequence, and ``counts`` the sequences'
+    labelled rows (int32); ``lse`` and ``slopes``, the losses' derivatives by the
+    log-probabilities of each row (or of a sequence's rows), for a backward pass;
+    the gradients, where they were taken."""
+    loss: torch.Tensor | None
+    reduced: torch.Tensor | None
+    logps: torch.Tensor | None
+    slopes: torch.Tensor | None
+    lse: torch.Tensor | None
+    counts: torch.Tensor | None = None
+    dhidden: torch.Tensor | None = None
+    dweight: torch.Tensor | None = None
+
+
+_KINDS = {"sigmoid": abi.ZERO_PREFERENCE_SIGMOID, "squared": abi.ZERO_PREFERENCE_SQUARED}
 
 _PRECISION = {torch.float32: abi.ZERO_FP32, torch.bfloat16: abi.ZERO_BF16_MIXED}
 
@@ -126,6 +149,9 @@ class _Call:
         self.distill = teacher is not None
         self.labels = labels is not None
         self.none = reduction == "none"
+        self.extra = None                        # a policy's or a preference's part
+        self.count = self.T                      # of losses, and of the entries of dloss
+        self.loss_shape = self.lead
         self.keep = [hidden2, weight2, labels]   # the caller's tensors
         self.made = []                           # its results
         y = None
@@ -196,7 +222,7 @@ class _Call:
     def losses(self):
         """loss, reduced, lse, lse_tau, to be written."""
         p, T = self.p, self.T
-        loss = self.new(self.lead)
+        loss = self.new(self.loss_shape)
         p.loss = loss.data_ptr()
         reduced = lse = lse_tau = None
         if not self.none:
@@ -217,8 +243,8 @@ class _Call:
         if accumulate:
             p.accumulate = 1
         if dloss is not None:
-            p.dloss = (self.vector(dloss, "dloss", torch.float32) if self.none else
-                       _vector(dloss, "dloss", torch.float32, 1, self.device))
+            p.dloss = (self.vector(dloss, "dloss", torch.float32) if self.none and self.loss_shape is self.lead else
+                       _vector(dloss, "dloss", torch.float32, self.count if self.none else 1, self.device))
             self.keep.append(dloss)
         if dhidden is None:
             dhidden = self.new(self.shape, self.dtype)
@@ -249,10 +275,15 @@ class _Call:
             with torch.cuda.device(index):
                 return self.run(xent, distill)
         p = self.p
+        more = () if self.extra is None else (self.extra,)
         if self.distill:
             size, call = abi.zero_distill_workspace_bytes(p), distill
-        else:
+        elif not more:
             size, call = abi.zero_xent_workspace_bytes(p), xent
+        elif isinstance(self.extra, abi.Policy):
+            size, call = abi.zero_policy_workspace_bytes(p, *more), xent
+        else:
+            size, call = abi.zero_preference_workspace_bytes(p, *more), xent
         space = self.empty(size, torch.uint8)
         p.workspace, p.workspace_bytes = space.data_ptr(), size
         stream = self.stream
@@ -264,7 +295,72 @@ class _Call:
             for t in self.made:
                 t.record_stream(current)
         # the current stream's handle, without the object around it
-        call(p, torch._C._cuda_getCurrentRawStream(index) if stream is None else stream)
+        call(p, *more, torch._C._cuda_getCurrentRawStream(index) if stream is None else stream)
+
+    def policy(self, old_logps=None, advantages=None, ref_logps=None, clip=0.0, kl_weight=0.0, forward=True):
+        """Makes it a policy loss; ``forward``: with what a forward pass is given."""
+        q = self.extra = abi.Policy()
+        if not forward:
+            return
+        q.clip_low, q.clip_high = (clip, clip) if isinstance(clip, (int, float)) else clip
+        q.kl_weight = kl_weight
+        q.old_logps = self.vector(old_logps, "old_logps", torch.float32)
+        q.advantages = self.vector(advantages, "advantages", torch.float32)
+        self.keep += [old_logps, advantages]
+        if ref_logps is not None:
+            q.ref_logps = self.vector(ref_logps, "ref_logps", torch.float32)
+            self.keep.append(ref_logps)
+        elif kl_weight != 0.0:
+            raise ValueError("kl_weight weighs the distance from ref_logps, which are not given")
+
+    def preference(self, offsets, **options):
+        """Makes it a preference loss; the options: a forward pass's."""
+        q = self.extra = abi.Preference()
+        if offsets is not None:
+            if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or offsets.shape[0] % 2 == 0:
+                raise ValueError("offsets must have one dimension of 2 * pairs + 1 entries")
+            q.pairs = offsets.shape[0] // 2
+            q.offsets = _vector(offsets, "offsets", torch.int64, 2 * q.pairs + 1, self.device)
+            self.keep.append(offsets)
+        else:
+            if len(self.lead) != 2 or self.lead[0] % 2:
+                raise ValueError("without offsets hidden must be [2 * pairs, length, D]")
+            q.pairs = self.lead[0] // 2
+        self.count, self.loss_shape = q.pairs, (q.pairs,)
+        if not options:
+            return
+        kind, ref_logps = options["kind"], options["ref_logps"]
+        if kind not in _KINDS:
+            raise ValueError('kind must be "sigmoid" or "squared"')
+        q.kind, q.average = _KINDS[kind], 1 if options["average"] else 0
+        q.beta, q.smoothing, q.margin = options["beta"], options["smoothing"], options["margin"]
+        q.nll_weight = options["nll_weight"]
+        if ref_logps is not None:
+            q.ref_logps = _vector(ref_logps, "ref_logps", torch.float32, 2 * q.pairs, self.device)
+            self.keep.append(ref_logps)
+
+    def slopes(self, lse, slopes):
+        """The forward pass's lse and slopes, for a backward pass."""
+        self.p.lse = self.vector(lse, "lse", torch.float32)
+        if isinstance(self.extra, abi.Policy):
+            self.extra.slopes = self.vector(slopes, "slopes", torch.float32)
+        else:
+            self.extra.slopes = _vector(slopes, "slopes", torch.float32, 2 * self.count, self.device)
+        self.keep += [lse, slopes]
+
+    def logp_losses(self):
+        """The fields of a LogpLosses but for the gradients, to be written."""
+        q = self.extra
+        loss, reduced, lse, _ = self.losses()
+        counts = None
+        if isinstance(q, abi.Policy):
+            logps, slopes = self.new(self.lead), self.new(self.lead)
+        else:
+            logps, slopes = self.new(2 * q.pairs), self.new(2 * q.pairs)
+            counts = self.new(2 * q.pairs, torch.int32)
+            q.counts = counts.data_ptr()
+        q.logps, q.slopes = logps.data_ptr(), slopes.data_ptr()
+        return loss, reduced, logps, slopes, lse, counts
 
 
 def xent_forward(hidden, weight, labels, *, reduction: str = "mean", ignore_index: int = -100,
@@ -342,6 +438,95 @@ def distill_step(hidden, weight, teacher_ids, teacher_logits, *, temperature: fl
     return Losses(*out, *grads)
 
 
+def policy_forward(hidden, weight, labels, old_logps, advantages, *, ref_logps=None, clip=0.2,
+                   kl_weight: float = 0.0, reduction: str = "mean", ignore_index: int = -100,
+                   stream=None) -> LogpLosses:
+    """The clipped policy loss of every labelled row: ``old_logps`` float32, the
+    labels' log-probabilities when they were sampled, ``advantages`` float32,
+    ``clip`` how far the ratio may move either way, or a pair for down and up,
+    ``ref_logps`` float32, a reference's log-probabilities, from which
+    ``kl_weight`` holds the policy. The mean is over the labelled rows."""
+    c = _Call(hidden, weight, labels, reduction, ignore_index, stream)
+    c.policy(old_logps, advantages, ref_logps, clip, kl_weight)
+    out = c.logp_losses()
+    c.run(abi.zero_policy_forward, None)
+    return LogpLosses(*out)
+
+
+def policy_backward(hidden, weight, labels, lse, slopes, *, reduction: str = "mean", ignore_index: int = -100,
+                    dloss=None, grad_scale: float = 1.0, dhidden=None, dweight=None, accumulate: bool = False,
+                    stream=None) -> LogpLosses:
+    """The gradients, given ``lse`` and ``slopes`` of policy_forward on the same
+    inputs; ``dloss`` as in xent_backward."""
+    c = _Call(hidden, weight, labels, reduction, ignore_index, stream)
+    c.policy(forward=False)
+    c.slopes(lse, slopes)
+    dh, dw = c.gradients(dloss, grad_scale, dhidden, dweight, accumulate)
+    c.run(abi.zero_policy_backward, None)
+    return LogpLosses(None, None, None, slopes, lse, None, dh, dw)
+
+
+def policy_step(hidden, weight, labels, old_logps, advantages, *, ref_logps=None, clip=0.2, kl_weight: float = 0.0,
+                reduction: str = "mean", ignore_index: int = -100, dloss=None, grad_scale: float = 1.0, dhidden=None,
+                dweight=None, accumulate: bool = False, stream=None) -> LogpLosses:
+    """policy_forward and policy_backward in one call."""
+    c = _Call(hidden, weight, labels, reduction, ignore_index, stream)
+    c.policy(old_logps, advantages, ref_logps, clip, kl_weight)
+    out = c.logp_losses()
+    grads = c.gradients(dloss, grad_scale, dhidden, dweight, accumulate)
+    c.run(abi.zero_policy_step, None)
+    return LogpLosses(*out, *grads)
+
+
+def preference_forward(hidden, weight, labels, offsets=None, *, ref_logps=None, kind: str = "sigmoid",
+                       beta: float = 0.1, smoothing: float = 0.0, margin: float = 0.0, average: bool = False,
+                       nll_weight: float = 0.0, reduction: str = "mean", ignore_index: int = -100,
+                       stream=None) -> LogpLosses:
+    """The loss of pairs of sequences, the preferred ones first, then the rejected
+    in the same order: ``offsets`` int64 [2 * pairs + 1], the sequences' first
+    rows and the end of the last, or None where ``hidden`` is [2 * pairs, length,
+    D]. ``ref_logps`` float32 [2 * pairs]: a reference's sums of
+    log-probabilities (a forward call's ``logps``), with ``average`` their means
+    (``logps / counts``). ``kind`` "sigmoid" or "squared"; with beta = 1,
+    average, and the margin 1 / (2 tau) the squared loss pulls the log-ratio of a
+    pair toward that margin. The mean is over the pairs that have labelled rows."""
+    c = _Call(hidden, weight, labels, reduction, ignore_index, stream)
+    c.preference(offsets, ref_logps=ref_logps, kind=kind, beta=beta, smoothing=smoothing, margin=margin,
+                 average=average, nll_weight=nll_weight)
+    out = c.logp_losses()
+    c.run(abi.zero_preference_forward, None)
+    return LogpLosses(*out)
+
+
+def preference_backward(hidden, weight, labels, lse, slopes, offsets=None, *, reduction: str = "mean",
+                        ignore_index: int = -100, dloss=None, grad_scale: float = 1.0, dhidden=None, dweight=None,
+                        accumulate: bool = False, stream=None) -> LogpLosses:
+    """The gradients, given ``lse`` and ``slopes`` of preference_forward on the same
+    inputs. ``dloss`` (float32): the gradient of the total with respect to
+    ``loss`` [pairs] (reduction "none") or to ``reduced``; ones when None."""
+    c = _Call(hidden, weight, labels, reduction, ignore_index, stream)
+    c.preference(offsets)
+    c.slopes(lse, slopes)
+    dh, dw = c.gradients(dloss, grad_scale, dhidden, dweight, accumulate)
+    c.run(abi.zero_preference_backward, None)
+    return LogpLosses(None, None, None, slopes, lse, None, dh, dw)
+
+
+def preference_step(hidden, weight, labels, offsets=None, *, ref_logps=None, kind: str = "sigmoid",
+                    beta: float = 0.1, smoothing: float = 0.0, margin: float = 0.0, average: bool = False,
+                    nll_weight: float = 0.0, reduction: str = "mean", ignore_index: int = -100, dloss=None,
+                    grad_scale: float = 1.0, dhidden=None, dweight=None, accumulate: bool = False,
+                    stream=None) -> LogpLosses:
+    """preference_forward and preference_backward in one call."""
+    c = _Call(hidden, weight, labels, reduction, ignore_index, stream)
+    c.preference(offsets, ref_logps=ref_logps, kind=kind, beta=beta, smoothing=smoothing, margin=margin,
+                 average=average, nll_weight=nll_weight)
+    out = c.logp_losses()
+    grads = c.gradients(dloss, grad_scale, dhidden, dweight, accumulate)
+    c.run(abi.zero_preference_step, None)
+    return LogpLosses(*out, *grads)
+
+
 # -------------------------------------------------------------- autograd --
 
 class _Once(torch.autograd.Function):
@@ -406,6 +591,50 @@ class _Distill(torch.autograd.Function):
         return *_once(r, hidden, weight, dloss), None, None, None, None
 
 
+class _Policy(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, hidden, weight, labels, old_logps, advantages, ref_logps, options, reduction, ignore_index):
+        r = policy_forward(hidden, weight, labels, old_logps, advantages, ref_logps=ref_logps,
+                           reduction=reduction, ignore_index=ignore_index, **options)
+        ctx.save_for_backward(hidden, weight, labels, r.lse, r.slopes)
+        ctx.options = dict(reduction=reduction, ignore_index=ignore_index)
+        return r.loss if reduction == "none" else r.reduced
+
+    @staticmethod
+    def backward(ctx, dloss):
+        hidden, weight, labels, lse, slopes = ctx.saved_tensors
+        none = (None,) * 7
+        if not any(ctx.needs_input_grad[:2]):
+            return None, None, *none
+        with torch.no_grad():
+            r = policy_backward(hidden, weight, labels, lse, slopes, dloss=dloss.contiguous(),
+                                dhidden=None if ctx.needs_input_grad[0] else False,
+                                dweight=None if ctx.needs_input_grad[1] else False, **ctx.options)
+        return *_once(r, hidden, weight, dloss), *none
+
+
+class _Preference(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, hidden, weight, labels, offsets, ref_logps, options, reduction, ignore_index):
+        r = preference_forward(hidden, weight, labels, offsets, ref_logps=ref_logps, reduction=reduction,
+                               ignore_index=ignore_index, **options)
+        ctx.save_for_backward(hidden, weight, labels, offsets, r.lse, r.slopes)
+        ctx.options = dict(reduction=reduction, ignore_index=ignore_index)
+        return r.loss if reduction == "none" else r.reduced
+
+    @staticmethod
+    def backward(ctx, dloss):
+        hidden, weight, labels, offsets, lse, slopes = ctx.saved_tensors
+        none = (None,) * 6
+        if not any(ctx.needs_input_grad[:2]):
+            return None, None, *none
+        with torch.no_grad():
+            r = preference_backward(hidden, weight, labels, lse, slopes, offsets, dloss=dloss.contiguous(),
+                                    dhidden=None if ctx.needs_input_grad[0] else False,
+                                    dweight=None if ctx.needs_input_grad[1] else False, **ctx.options)
+        return *_once(r, hidden, weight, dloss), *none
+
+
 def linear_cross_entropy(hidden, weight, labels, reduction: str = "mean",
                          ignore_index: int = -100):
     """Cross entropy of ``hidden @ weight.T``, differentiable in ``hidden`` and ``weight``."""
@@ -420,3 +649,20 @@ def linear_distillation(hidden, weight, teacher_ids, teacher_logits, temperature
     options = dict(temperature=temperature, alpha=alpha, reduction=reduction,
                    ignore_index=ignore_index)
     return _Distill.apply(hidden, weight, teacher_ids, teacher_logits, labels, options)
+
+
+def linear_policy(hidden, weight, labels, old_logps, advantages, ref_logps=None, clip=0.2, kl_weight: float = 0.0,
+                  reduction: str = "mean", ignore_index: int = -100):
+    """The clipped policy loss, differentiable in ``hidden`` and ``weight`` (all else is
+    constant)."""
+    return _Policy.apply(hidden, weight, labels, old_logps, advantages, ref_logps,
+                         dict(clip=clip, kl_weight=kl_weight), reduction, ignore_index)
+
+
+def linear_preference(hidden, weight, labels, offsets=None, ref_logps=None, kind: str = "sigmoid", beta: float = 0.1,
+                      smoothing: float = 0.0, margin: float = 0.0, average: bool = False, nll_weight: float = 0.0,
+                      reduction: str = "mean", ignore_index: int = -100):
+    """The preference loss, differentiable in ``hidden`` and ``weight`` (all else is
+    constant)."""
+    options = dict(kind=kind, beta=beta, smoothing=smoothing, margin=margin, average=average, nll_weight=nll_weight)
+    return _Preference.apply(hidden, weight, labels, offsets, ref_logps, options, reduction, ignore_index)
