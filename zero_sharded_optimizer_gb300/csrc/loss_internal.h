@@ -39,6 +39,7 @@ struct Head {
   float factor;    // of both gradients, the same for every row
   int32_t pairs;   // pairs that are not empty
   int32_t repack;  // the backward pass has other rows than the forward pass
+  uint32_t steepest; // the largest size of a scale of a preference call, as bits
 };
 
 // Everything the kernels read or write. Rows with a target are packed densely:
@@ -107,6 +108,7 @@ struct Args {
   float* weights;         // [T][L] weight of each entry's logit in loss and gradient
   uint16_t* starts;       // distillation: [2 tiles + 1][T] first entry of each half tile
   float* scales;          // [T] row_scale of a call that goes by slopes
+  float* left;            // [Tp] what G's one bf16 value leaves of the label's entry, or NULL
   double* row_logps;      // [T] a preference call's labels' log-probabilities
   double* sums;           // [kLossBlocks] parts of the reduced loss
   float* zent;            // [T][L] logits of the entries

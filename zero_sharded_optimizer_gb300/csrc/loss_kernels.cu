@@ -299,6 +299,16 @@ __global__ void __launch_bounds__(1024) number_rows_kernel(const Args a) {
   if (N != kSlopes)
     for (int64_t n = threadIdx.x; n < a.zeros; n += 1024) a.counters[n] = 0;
   const bool ascend = N == kSlopes || offsets_ascend(a);
+  // A preference loss has the same slope in all rows of a sequence, and often
+  // nearly the same in all pairs. Its scales are taken relative to the largest,
+  // which the factor of both gradients gets: G's entries of labels that the model
+  // finds unlikely, s (1 - p), are near powers of two then, and lose nothing to
+  // bf16, where one rounding would go through the whole gradient.
+  float unit = 1.0f;
+  if (N == kSlopes && a.kind == kPreference) {
+    unit = __uint_as_float(a.head->steepest);
+    if (!(unit > 0.0f && unit < INFINITY)) unit = 1.0f;
+  }
   int32_t base = 0, targets = 0;
   for (int64_t t0 = 0; t0 < a.T; t0 += 16 * 1024) {
     uint32_t mask[16];
@@ -308,7 +318,9 @@ __global__ void __launch_bounds__(1024) number_rows_kernel(const Args a) {
       mask[q] = t < a.T && a.rowpos[t] >= 0;
       if (N == kSlopes && mask[q]) {
         ++targets;
-        mask[q] = a.scales[t] != 0.0f;  // (also a NaN)
+        float scale = a.scales[t];
+        if (a.kind == kPreference) a.scales[t] = scale /= unit;
+        mask[q] = scale != 0.0f;  // (also a NaN)
         if (!mask[q]) a.rowpos[t] = -2;
       }
     }
@@ -358,12 +370,13 @@ __global__ void __launch_bounds__(1024) number_rows_kernel(const Args a) {
     double f = a.grad_scale;
     if (a.reduction == ZERO_REDUCE_MEAN) f /= double(max(1, N == kSlopes && a.kind == kPreference ? a.head->pairs : targets));
     if (a.reduction != ZERO_REDUCE_NONE && a.dloss) f *= double(*a.dloss);
+    f *= double(unit);
     if (N == kSlopes) {
       a.head->repack = a.head->rows != base;
       a.head->rows = base;
       a.head->factor = float(f);
     } else {
-      *a.head = Head{base, 0, !ascend, float(f), 0, 0};
+      *a.head = Head{base, 0, !ascend, float(f), 0, 0, 0};
     }
   }
 }
@@ -457,6 +470,14 @@ __global__ void __launch_bounds__(256) dhidden_out_kernel(const Args a) {
       __syncthreads();
     }
     if (lane > 0 || d >= a.D) continue;
+    if (!F32 && a.left && i >= 0) {
+      const float rest = a.left[i];
+      const __nv_bfloat16* w = static_cast<const __nv_bfloat16*>(a.weight) + a.ids[t] * a.weight_stride + d;
+      x.x += rest * float(w[0]);
+      if (d + 1 < a.D) x.y += rest * float(w[1]);
+      if (d + 2 < a.D) x.z += rest * float(w[2]);
+      if (d + 3 < a.D) x.w += rest * float(w[3]);
+    }
     if (i >= 0 || (fault && i < -1)) x = make_float4(f * x.x, f * x.y, f * x.z, f * x.w);
     const int64_t at = t * a.dhidden_stride + d;
     const float v[4] = {x.x, x.y, x.z, x.w};
@@ -823,6 +844,8 @@ __global__ void __launch_bounds__(256) pairs_kernel(const Args a) {
       for (int k = 0; k < 2; ++k)
         for (int64_t t = begin[k] + threadIdx.x; t < end[k]; t += 256)
           if (a.rowpos[t] >= 0) a.scales[t] = -slopes[k] * d;
+      // (sizes of floats are in the order of their bits)
+      if (threadIdx.x < 2) atomicMax(&a.head->steepest, __float_as_uint(fabsf(slopes[threadIdx.x] * d)));
     }
     __syncthreads();
   }
