@@ -72,12 +72,13 @@ void common(const zero_embedding_t* p, const void* table, int64_t table_stride, 
 int plan(const zero_embedding_t* p, Args* a, int64_t* bytes) {
   common(p, p->dout, p->dout_stride, p->dweight, p->dweight_stride, a);
   a->accumulate = p->accumulate != 0;
+  a->few = p->T <= ze::kFewTokens && (p->V <= ze::kFewIds || p->T == 0);
   // The fewest digits, of equal width, that hold the ids and V itself.
   int bits = 1;
   while (p->V >> bits) ++bits;
   a->passes = (bits + ze::kMostBits - 1) / ze::kMostBits;
   a->bits = (bits + a->passes - 1) / a->passes;
-  const int64_t least = 4096;
+  const int64_t least = 1024;
   a->tile = std::max(least, round_up((p->T + ze::kMostTiles - 1) / ze::kMostTiles, 512));
   a->tiles = int32_t((p->T + a->tile - 1) / a->tile);
   const int64_t block = p->precision == ZERO_FP32 ? 128 : 256;
@@ -89,6 +90,7 @@ int plan(const zero_embedding_t* p, Args* a, int64_t* bytes) {
   Layout w{static_cast<uint8_t*>(p->workspace)};
   a->counts = w.take<int32_t>(int64_t(a->tiles) << a->bits);
   for (auto& l : a->list) l = w.take<ze::Entry>(p->T);
+  a->sorted = a->list[a->few ? 0 : (a->passes - 1) & 1];
   a->part = w.take<float>(2 * a->runs, a->Dp);
   if (!w.fits) return set_error(ZERO_EINVAL, "the problem's workspace overflows 64 bits");
   *bytes = w.at;
@@ -157,7 +159,7 @@ int zero_embedding_backward(const zero_embedding_t* p, zero_stream_t stream) {
     return set_error(ZERO_EINVAL, "the workspace has %lld bytes, %lld are needed",
                      (long long)(p->workspace ? p->workspace_bytes : 0), (long long)bytes);
   if (T == 0 && a.accumulate) return ZERO_OK;
-  if (T > 0 && (e = launched(ze::launch_sort(a, stream), "the sort"))) return e;
+  if ((e = launched(ze::launch_sort(a, stream), "the sort"))) return e;
   return launched(ze::launch_sums(a, stream), "the sums");
 }
 

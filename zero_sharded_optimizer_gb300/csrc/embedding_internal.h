@@ -10,11 +10,18 @@
 namespace ze {
 
 constexpr int kSms = 152;        // GB300's multiprocessors
+constexpr int64_t kCacheBytes = int64_t(100) << 20;  // that the L2 cache keeps of a stream of stores
 constexpr int kMostBits = 9;     // of a digit of the sort
 constexpr int kMostBins = 1 << kMostBits;
 constexpr int kMostTiles = 256;  // of the sort
 
-// A token in the sorted list: its id (V: none) and its position.
+// Up to so many tokens, and ids below so many, one kernel sorts (class_sort_kernel).
+constexpr int kPositionBits = 15;
+constexpr int kClassBits = 7;
+constexpr int64_t kFewTokens = int64_t(1) << kPositionBits;
+constexpr int64_t kFewIds = int64_t(1) << (32 - kPositionBits + kClassBits);
+
+// A token in the sorted list: its id (V, at the list's end: none) and its position.
 struct Entry {
   uint32_t id, t;
 };
@@ -33,6 +40,7 @@ struct Args {
   int32_t vector;          // 16-byte accesses fit the rows of both
 
   // Backward: the sort's digits and tiles, and the sums' runs of sorted tokens.
+  int32_t few;             // the tokens are sorted by one kernel, which also writes the zeros
   int32_t bits, passes;    // of a digit; digits
   int64_t tile;            // tokens of a tile, a multiple of the block's threads
   int32_t tiles;
@@ -42,6 +50,7 @@ struct Args {
   int64_t Dp;              // their columns
   int32_t* counts;         // [tiles][bins] tokens of a tile by digit
   Entry* list[2];          // [T] before and after a pass
+  const Entry* sorted;     // the one that the last pass writes
   float* part;             // [runs][2][Dp] a run's share of the segment that began before it, and of
                            // the one that it began and did not end
 };

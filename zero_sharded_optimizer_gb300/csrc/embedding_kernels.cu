@@ -57,41 +57,60 @@ struct Columns {
   }
   __device__ __forceinline__ int64_t at(int j) const { return first + (Vector ? j : 32 * j); }
 
-  __device__ __forceinline__ void load(const void* row, float (&x)[kVec]) const {
+  // The elements as they are stored, those outside the row as zeros. `Once`: they
+  // are not read again, or (store) not soon.
+  template <bool Once = false>
+  __device__ __forceinline__ uint4 load(const void* row) const {
     const E* p = static_cast<const E*>(row);
     if (Vector && count == kVec) {
-      const uint4 w = *reinterpret_cast<const uint4*>(p + first);
-      const uint32_t words[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-      for (int j = 0; j < kVec; ++j)
-        x[j] = F32 ? __uint_as_float(words[j])
-                   : __uint_as_float(j % 2 ? words[j / 2] & 0xffff0000u : words[j / 2] << 16);
-    } else {
-#pragma unroll
-      for (int j = 0; j < kVec; ++j) x[j] = j < count ? float(p[at(j)]) : 0.0f;
+      const uint4* at = reinterpret_cast<const uint4*>(p + first);
+      return Once ? __ldcs(at) : *at;
     }
+    uint32_t words[4] = {};
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) {
+      if (j >= count) continue;
+      if (F32) words[j % 4] = reinterpret_cast<const uint32_t*>(p)[at(j)];
+      else words[j / 2] |= uint32_t(reinterpret_cast<const uint16_t*>(p)[at(j)]) << (j % 2 * 16);
+    }
+    return make_uint4(words[0], words[1], words[2], words[3]);
   }
-  __device__ __forceinline__ void store(void* row, const float (&x)[kVec]) const {
+  template <bool Once = false>
+  __device__ __forceinline__ void store(void* row, uint4 w) const {
     E* p = static_cast<E*>(row);
     if (Vector && count == kVec) {
-      uint4 w;
-      if (F32) {
-        w = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
-      } else {
-        uint32_t words[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * j % kVec], x[(2 * j + 1) % kVec]);
-          words[j] = *reinterpret_cast<const uint32_t*>(&h);
-        }
-        w = make_uint4(words[0], words[1], words[2], words[3]);
-      }
-      *reinterpret_cast<uint4*>(p + first) = w;
-    } else {
-#pragma unroll
-      for (int j = 0; j < kVec; ++j)
-        if (j < count) p[at(j)] = E(x[j]);
+      uint4* to = reinterpret_cast<uint4*>(p + first);
+      if (Once) __stcs(to, w);
+      else *to = w;
+      return;
     }
+    const uint32_t words[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) {
+      if (j >= count) continue;
+      if (F32) reinterpret_cast<uint32_t*>(p)[at(j)] = words[j % 4];
+      else reinterpret_cast<uint16_t*>(p)[at(j)] = uint16_t(words[j / 2] >> (j % 2 * 16));
+    }
+  }
+  __device__ __forceinline__ static void unpack(uint4 w, float (&x)[kVec]) {
+    const uint32_t words[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int j = 0; j < kVec; ++j)
+      x[j] = __uint_as_float(F32 ? words[j % 4] : j % 2 ? words[j / 2] & 0xffff0000u : words[j / 2] << 16);
+  }
+  // Each value rounded once.
+  __device__ __forceinline__ static uint4 pack(const float (&x)[kVec]) {
+    uint32_t words[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (F32) {
+        words[j] = __float_as_uint(x[j]);
+      } else {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * j % kVec], x[(2 * j + 1) % kVec]);
+        words[j] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+    }
+    return make_uint4(words[0], words[1], words[2], words[3]);
   }
 };
 
@@ -106,9 +125,12 @@ __device__ __forceinline__ void* row_of(void* base, int64_t stride, int64_t row)
 
 // ----------------------------------------------------------------- lookup --
 
-template <bool F32, bool Vector>
+// `Stream`: the result is larger than the L2 cache, where it would displace the
+// rows that are looked up again.
+template <bool F32, bool Vector, bool Stream>
 __global__ void __launch_bounds__(256) lookup_kernel(const Args a) {
   using C = Columns<F32, Vector>;
+  constexpr int kAhead = 4;  // loads in flight
   const int lane = threadIdx.x & 31;
   const int64_t step = int64_t(gridDim.x) * 8;
   for (int64_t t = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5); t < a.T; t += step) {
@@ -116,24 +138,138 @@ __global__ void __launch_bounds__(256) lookup_kernel(const Args a) {
     const bool there = id >= 0 && id < a.V;
     const void* from = row_of<F32>(a.table, a.table_stride, there ? id : 0);
     void* to = row_of<F32>(a.out, a.out_stride, t);
-#pragma unroll 4
-    for (int64_t c0 = 0; c0 < a.D; c0 += C::kBlock) {
-      const C c(c0, a.D, lane);
-      float x[C::kVec] = {};
-      if (there) c.load(from, x);
+    for (int64_t c0 = 0; c0 < a.D; c0 += kAhead * C::kBlock) {
+      uint4 w[kAhead];
 #pragma unroll
-      for (int j = 0; j < C::kVec; ++j) x[j] = there ? x[j] * a.scale : 0.0f;
-      c.store(to, x);
+      for (int q = 0; q < kAhead; ++q) {
+        const C c(c0 + q * C::kBlock, a.D, lane);
+        w[q] = there && c.count > 0 ? c.load(from) : make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int q = 0; q < kAhead; ++q) {
+        const C c(c0 + q * C::kBlock, a.D, lane);
+        if (c.count == 0) break;
+        if (there && a.scale != 1.0f) {
+          float x[C::kVec];
+          C::unpack(w[q], x);
+#pragma unroll
+          for (int j = 0; j < C::kVec; ++j) x[j] *= a.scale;
+          w[q] = C::pack(x);
+        }
+        c.template store<Stream>(to, w[q]);
+      }
     }
   }
 }
 
 // ------------------------------------------------------------------- sort --
 //
-// By digits from the lowest, each pass stable: a tile's tokens are counted by
-// digit, and the next kernel's block of that tile adds up what comes before --
-// smaller digits of all tiles, its digit in earlier tiles -- and places its
-// tokens, each warp a stretch of them in order.
+// Few tokens: one kernel, a block for each class of ids (their low bits, so that
+// the frequent ids of a vocabulary in order of frequency are spread). Each block
+// reads all ids, counts those of smaller classes -- its place in the list --
+// gathers its own and sorts them by id and position in shared memory. The list is
+// in order of class, then of id. Blocks behind those write dweight's zeros
+// meanwhile.
+//
+// More tokens: by digits of the id from the lowest, each pass stable: a tile's
+// tokens are counted by digit, and the next kernel's block of that tile adds up
+// what comes before -- smaller digits of all tiles, its digit in earlier tiles --
+// and places its tokens, each warp a stretch of them in order.
+
+constexpr int kClasses = 1 << kClassBits;
+constexpr int kClassThreads = 1024;
+
+template <bool F32, bool Vector>
+__device__ __forceinline__ void zero_rows(const Args& a, int64_t first, int64_t step) {
+  using C = Columns<F32, Vector>;
+  for (int64_t v = first; v < a.V; v += step) {
+    void* row = row_of<F32>(a.out, a.out_stride, v);
+    for (int64_t c0 = 0; c0 < a.D; c0 += C::kBlock)
+      C(c0, a.D, threadIdx.x & 31).store(row, make_uint4(0, 0, 0, 0));
+  }
+}
+
+template <bool F32, bool Vector>
+__global__ void __launch_bounds__(kClassThreads) class_sort_kernel(const Args a) {
+  extern __shared__ uint32_t keys[];  // id without its class, then position
+  __shared__ int32_t found, less_of[32], none_of[32];
+  let_next_start();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (blockIdx.x >= kClasses) {
+    zero_rows<F32, Vector>(a, int64_t(blockIdx.x - kClasses) * 32 + warp, int64_t(gridDim.x - kClasses) * 32);
+    return;
+  }
+  if (threadIdx.x == 0) found = 0;
+  __syncthreads();
+  const int T = int(a.T), mine = blockIdx.x;
+  int less = 0, none = 0;
+  for (int t0 = 0; t0 < T; t0 += 8 * kClassThreads) {
+    int64_t id[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      const int t = t0 + q * kClassThreads + threadIdx.x;
+      id[q] = t < T ? a.ids[t] : -2;
+    }
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      const int t = t0 + q * kClassThreads + threadIdx.x;
+      const bool valid = t < T && id[q] >= 0 && id[q] < a.V && id[q] != a.padding_id;
+      const int its = int(id[q] & (kClasses - 1));
+      none += t < T && !valid;
+      less += valid && its < mine;
+      const unsigned in = __ballot_sync(~0u, valid && its == mine);
+      if (in) {
+        int at = 0;
+        if (lane == 0) at = atomicAdd(&found, __popc(in));
+        at = __shfl_sync(~0u, at, 0) + __popc(in & ((1u << lane) - 1));
+        if (in >> lane & 1) keys[at] = uint32_t(id[q] >> kClassBits) << kPositionBits | uint32_t(t);
+      }
+    }
+  }
+  for (int o = 16; o; o >>= 1) {
+    less += __shfl_xor_sync(~0u, less, o);
+    none += __shfl_xor_sync(~0u, none, o);
+  }
+  if (lane == 0) {
+    less_of[warp] = less;
+    none_of[warp] = none;
+  }
+  __syncthreads();
+  const int n = found;
+  int size = 32;  // a power of two
+  while (size < n) size *= 2;
+  for (int i = n + threadIdx.x; i < size; i += kClassThreads) keys[i] = ~0u;
+  less = less_of[lane];
+  none = none_of[lane];
+  for (int o = 16; o; o >>= 1) {
+    less += __shfl_xor_sync(~0u, less, o);
+    none += __shfl_xor_sync(~0u, none, o);
+  }
+  __syncthreads();
+  // A bitonic network: all keys differ, so the order in which they were found
+  // leaves no trace.
+  for (int k = 2; k <= size; k *= 2) {
+    for (int j = k / 2; j; j /= 2) {
+      for (int p = threadIdx.x; p < size / 2; p += kClassThreads) {
+        const int lo = (p & ~(j - 1)) * 2 | (p & (j - 1)), hi = lo | j;
+        const uint32_t x = keys[lo], y = keys[hi];
+        if ((x > y) == ((lo & k) == 0)) {
+          keys[lo] = y;
+          keys[hi] = x;
+        }
+      }
+      // Up to 64 keys are one warp's, whose lanes run together.
+      if (size > 64) __syncthreads();
+      else __syncwarp();
+    }
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < n; i += kClassThreads)
+    a.list[0][less + i] = Entry{keys[i] >> kPositionBits << kClassBits | uint32_t(mine),
+                                keys[i] & uint32_t(kFewTokens - 1)};
+  if (mine == 0)
+    for (int i = threadIdx.x; i < none; i += kClassThreads) a.list[0][T - none + i] = Entry{uint32_t(a.V), 0};
+}
 
 constexpr int kSortThreads = 512;
 constexpr int kSortWarps = kSortThreads / 32;
@@ -170,7 +306,7 @@ __global__ void __launch_bounds__(kSortThreads) place_kernel(const Args a, int p
   static_assert(kSortThreads >= kMostBins, "a thread for each digit");
   int32_t before = 0, all = 0;
   if (int(threadIdx.x) < bins) {
-#pragma unroll 8
+#pragma unroll 32
     for (int j = 0; j < a.tiles; ++j) {
       const int32_t n = a.counts[int64_t(j) * bins + threadIdx.x];
       all += n;
@@ -223,37 +359,82 @@ constexpr uint32_t kNone = 0xffffffffu;  // no key: above V
 template <bool F32, bool Vector>
 __device__ __forceinline__ void finish(const Args& a, const Columns<F32, Vector>& c, uint32_t id,
                                        const float (&sum)[Columns<F32, Vector>::kVec]) {
-  constexpr int kVec = Columns<F32, Vector>::kVec;
+  using C = Columns<F32, Vector>;
+  if (c.count == 0) return;
   void* row = row_of<F32>(a.out, a.out_stride, id);
-  float x[kVec];
+  float x[C::kVec];
   if (a.accumulate) {
-    c.load(row, x);
+    C::unpack(c.load(row), x);
 #pragma unroll
-    for (int j = 0; j < kVec; ++j) x[j] = fmaf(a.scale, sum[j], x[j]);
+    for (int j = 0; j < C::kVec; ++j) x[j] = fmaf(a.scale, sum[j], x[j]);
   } else {
 #pragma unroll
-    for (int j = 0; j < kVec; ++j) x[j] = a.scale * sum[j];
+    for (int j = 0; j < C::kVec; ++j) x[j] = a.scale * sum[j];
   }
-  c.store(row, x);
+  c.store(row, C::pack(x));
 }
 
-template <bool F32, bool Vector>
-__device__ __forceinline__ float* share(const Args& a, int64_t run, int which, const Columns<F32, Vector>& c) {
-  return a.part + (2 * run + which) * a.Dp + c.first;
+// A run's share of a segment: kVec floats of each lane side by side, whatever
+// columns they are.
+template <int kVec>
+__device__ __forceinline__ float4* share(const Args& a, int64_t run, int which, int64_t block, int lane) {
+  return reinterpret_cast<float4*>(a.part + (2 * run + which) * a.Dp + block * 32 * kVec + lane * kVec);
+}
+template <int kVec>
+__device__ __forceinline__ void add_share(const float4* from, float (&sum)[kVec]) {
+#pragma unroll
+  for (int q = 0; q < kVec / 4; ++q) {
+    const float4 x = from[q];
+    sum[4 * q] += x.x;
+    sum[4 * q + 1] += x.y;
+    sum[4 * q + 2] += x.z;
+    sum[4 * q + 3] += x.w;
+  }
+}
+template <int kVec>
+__device__ __forceinline__ void put_share(float4* to, const float (&sum)[kVec]) {
+#pragma unroll
+  for (int q = 0; q < kVec / 4; ++q) to[q] = make_float4(sum[4 * q], sum[4 * q + 1], sum[4 * q + 2], sum[4 * q + 3]);
 }
 
+// Rows of dweight that no token has: zeros. A warp for 32 ids, each lane looks
+// its own up in the list (in order of id).
 template <bool F32, bool Vector>
-__global__ void __launch_bounds__(256) sum_kernel(const Args a) {
+__device__ __forceinline__ void zero_absent_rows(const Args& a, int64_t v0) {
+  using C = Columns<F32, Vector>;
+  const int lane = threadIdx.x & 31;
+  const int64_t v = v0 + lane;
+  int64_t lo = 0, hi = a.T;
+  while (lo < hi) {
+    const int64_t mid = (lo + hi) / 2;
+    if (a.sorted[mid].id < v) lo = mid + 1;
+    else hi = mid;
+  }
+  const bool absent = v < a.V && !(lo < a.T && a.sorted[lo].id == v);
+  for (unsigned left = __ballot_sync(~0u, absent); left; left &= left - 1) {
+    void* row = row_of<F32>(a.out, a.out_stride, v0 + __ffs(left) - 1);
+    for (int64_t c0 = 0; c0 < a.D; c0 += C::kBlock) C(c0, a.D, lane).store(row, make_uint4(0, 0, 0, 0));
+  }
+}
+
+// A warp for a run and a block of columns, and after those one for 32 ids whose
+// rows may have to become zero.
+template <bool F32, bool Vector>
+__global__ void __launch_bounds__(256, 3) sum_kernel(const Args a, int64_t zero_warps) {
   using C = Columns<F32, Vector>;
   constexpr int kVec = C::kVec, kAhead = 8;
   let_next_start();
   wait_for_previous();
   const int lane = threadIdx.x & 31;
-  const Entry* const list = a.list[(a.passes - 1) & 1];
-  const int64_t step = int64_t(gridDim.x) * 8;
-  for (int64_t g = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5); g < a.runs * a.blocks; g += step) {
-    const int64_t run = g / a.blocks, first = run * a.run;
-    const C c(g % a.blocks * C::kBlock, a.D, lane);
+  const Entry* const list = a.sorted;
+  const int64_t step = int64_t(gridDim.x) * 8, sums = a.runs * a.blocks;
+  for (int64_t g = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5); g < sums + zero_warps; g += step) {
+    if (g >= sums) {
+      zero_absent_rows<F32, Vector>(a, (g - sums) * 32);
+      continue;
+    }
+    const int64_t run = g / a.blocks, first = run * a.run, block = g % a.blocks;
+    const C c(block * C::kBlock, a.D, lane);
     const int count = int(min(int64_t(a.run), a.T - first));
     const Entry e = lane < count ? list[first + lane] : Entry{kNone, 0};
     const uint32_t prev = first > 0 ? list[first - 1].id : kNone;
@@ -262,28 +443,25 @@ __global__ void __launch_bounds__(256) sum_kernel(const Args a) {
     bool begun = __shfl_sync(~0u, e.id, 0) != prev;  // the segment begins in this run
     float sum[kVec] = {};
     for (int i0 = 0; i0 < n; i0 += kAhead) {
-      float x[kAhead][kVec];
+      uint4 w[kAhead];
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
         const uint32_t t = __shfl_sync(~0u, e.t, (i0 + i) & 31);
-        if (i0 + i < n) c.load(row_of<F32>(a.table, a.table_stride, t), x[i]);
+        if (i0 + i < n) w[i] = c.template load<true>(row_of<F32>(a.table, a.table_stride, t));
       }
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
         const uint32_t id = __shfl_sync(~0u, e.id, (i0 + i) & 31);
         const uint32_t following = __shfl_sync(~0u, e.id, (i0 + i + 1) & 31);
         if (i0 + i >= n) break;
+        float x[kVec];
+        C::unpack(w[i], x);
 #pragma unroll
-        for (int j = 0; j < kVec; ++j) sum[j] += x[i][j];
+        for (int j = 0; j < kVec; ++j) sum[j] += x[j];
         const bool last = i0 + i + 1 == count;
         const bool ends = (last ? next : following) != id;
-        if (ends && begun) {
-          finish(a, c, id, sum);
-        } else if (ends || last) {
-          float* to = share(a, run, begun ? 1 : 0, c);
-#pragma unroll
-          for (int j = 0; j < kVec; ++j) to[Vector ? j : 32 * j] = sum[j];
-        }
+        if (ends && begun) finish(a, c, id, sum);
+        else if (ends || last) put_share(share<kVec>(a, run, begun ? 1 : 0, block, lane), sum);
         if (ends) {
           begun = true;
 #pragma unroll
@@ -294,64 +472,79 @@ __global__ void __launch_bounds__(256) sum_kernel(const Args a) {
   }
 }
 
-// The segments that a run began and did not end: the runs' shares in order.
+// The segments that a run began and did not end: the runs' shares in order. A
+// warp looks for one in a run and block of columns and adds up to kShort shares
+// itself; longer ones are added by the block's eight warps together, each a
+// stretch of the shares in order, and the stretches in order. (A block has
+// neighbouring runs, of which few begin a long segment, not the columns of one.)
 template <bool F32, bool Vector>
 __global__ void __launch_bounds__(256) join_kernel(const Args a) {
   using C = Columns<F32, Vector>;
-  constexpr int kVec = C::kVec;
+  constexpr int kVec = C::kVec, kShort = 8;
+  __shared__ int64_t long_run[8], long_block[8], long_end[8];
+  __shared__ float4 parts[8][32 * kVec / 4];
   let_next_start();
   wait_for_previous();
-  const int lane = threadIdx.x & 31;
-  const Entry* const list = a.list[(a.passes - 1) & 1];
-  const int64_t step = int64_t(gridDim.x) * 8;
-  for (int64_t g = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5); g < (a.runs - 1) * a.blocks; g += step) {
-    const int64_t run = g / a.blocks, next = (run + 1) * a.run;
-    const uint32_t id = list[next].id;
-    if (id >= a.V || list[next - 1].id != id) continue;
-    if (run > 0 && list[next - a.run - 1].id == id) continue;  // an earlier run began it
-    const C c(g % a.blocks * C::kBlock, a.D, lane);
-    float sum[kVec];
-#pragma unroll
-    for (int j = 0; j < kVec; ++j) sum[j] = share(a, run, 1, c)[Vector ? j : 32 * j];
-    for (int64_t r = run + 1; r < a.runs;) {
-      // The runs from r on that begin with the segment, up to 32 of them.
-      const unsigned in = __ballot_sync(~0u, r + lane < a.runs && list[min(r + lane, a.runs - 1) * a.run].id == id);
-      const int n = __ffs(~in) ? __ffs(~in) - 1 : 32;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const Entry* const list = a.sorted;
+  const int64_t all = (a.runs - 1) * a.blocks;
+  for (int64_t g0 = int64_t(blockIdx.x) * 8; g0 < all; g0 += int64_t(gridDim.x) * 8) {
+    const int64_t g = g0 + warp;
+    const int64_t run = g % (a.runs - 1), block = g / (a.runs - 1), next = (run + 1) * a.run;
+    bool joins = false;
+    uint32_t id = 0;
+    if (g < all) {
+      id = list[next].id;
+      joins = id < a.V && list[next - 1].id == id && !(run > 0 && list[next - a.run - 1].id == id);
+    }
+    int64_t end = run + 1;  // behind the last run with a share
+    if (joins) {
+      // The runs that begin with the segment, first by 32s, then one by one.
+      for (;;) {
+        const int64_t r = end + lane * 32 + 31;
+        const unsigned in = __ballot_sync(~0u, r < a.runs && list[r * a.run].id == id);
+        const int n = in == ~0u ? 32 : __ffs(~in) - 1;
+        end += 32 * n;
+        if (n < 32) break;
+      }
+      const int64_t r = end + lane;
+      const unsigned in = __ballot_sync(~0u, r < a.runs && list[r * a.run].id == id);
+      end += in == ~0u ? 32 : __ffs(~in) - 1;
+    }
+    const bool together = joins && end - run > kShort;
+    if (joins && !together) {
+      float sum[kVec] = {};
+      add_share<kVec>(share<kVec>(a, run, 1, block, lane), sum);
 #pragma unroll 4
-      for (int q = 0; q < n; ++q)
+      for (int64_t r = run + 1; r < end; ++r) add_share<kVec>(share<kVec>(a, r, 0, block, lane), sum);
+      finish(a, C(block * C::kBlock, a.D, lane), id, sum);
+    }
+    if (lane == 0) {
+      long_run[warp] = together ? run : -1;
+      long_block[warp] = block;
+      long_end[warp] = end;
+    }
+    if (!__syncthreads_or(together)) continue;
+    for (int q = 0; q < 8; ++q) {
+      const int64_t r0 = long_run[q], r1 = long_end[q], b = long_block[q];
+      if (r0 < 0) continue;
+      const int64_t each = (r1 - r0 + 7) / 8;
+      float sum[kVec] = {};
+      const int64_t from = r0 + warp * each, to = min(r1, from + each);
+#pragma unroll 8
+      for (int64_t r = from; r < to; ++r) add_share<kVec>(share<kVec>(a, r, r == r0 ? 1 : 0, b, lane), sum);
+      put_share<kVec>(&parts[warp][lane * kVec / 4], sum);
+      __syncthreads();
+      if (warp == q) {
 #pragma unroll
-        for (int j = 0; j < kVec; ++j) sum[j] += share(a, r + q, 0, c)[Vector ? j : 32 * j];
-      r += n;
-      if (n < 32) break;
+        for (int j = 0; j < kVec; ++j) sum[j] = 0.0f;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) add_share<kVec>(&parts[w][lane * kVec / 4], sum);
+        finish(a, C(b * C::kBlock, a.D, lane), id, sum);
+      }
+      __syncthreads();
     }
-    finish(a, c, id, sum);
-  }
-}
-
-// Rows of dweight that no token has: zeros. A warp for 32 ids, each lane looks
-// its own up in the list.
-template <bool F32, bool Vector>
-__global__ void __launch_bounds__(256) absent_kernel(const Args a) {
-  using C = Columns<F32, Vector>;
-  let_next_start();
-  wait_for_previous();
-  const int lane = threadIdx.x & 31;
-  const Entry* const list = a.list[(a.passes - 1) & 1];
-  const int64_t step = int64_t(gridDim.x) * 8 * 32;
-  for (int64_t v0 = (int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5)) * 32; v0 < a.V; v0 += step) {
-    const int64_t v = v0 + lane;
-    int64_t lo = 0, hi = a.T;
-    while (lo < hi) {
-      const int64_t mid = (lo + hi) / 2;
-      if (list[mid].id < v) lo = mid + 1;
-      else hi = mid;
-    }
-    const bool absent = v < a.V && !(lo < a.T && list[lo].id == v);
-    for (unsigned left = __ballot_sync(~0u, absent); left; left &= left - 1) {
-      void* row = row_of<F32>(a.out, a.out_stride, v0 + __ffs(left) - 1);
-      const float zero[C::kVec] = {};
-      for (int64_t c0 = 0; c0 < a.D; c0 += C::kBlock) C(c0, a.D, lane).store(row, zero);
-    }
+    __syncthreads();
   }
 }
 
@@ -362,15 +555,34 @@ unsigned blocks_of(int64_t warps) {
 }
 
 template <bool F32, bool Vector>
-cudaError_t sums(const Args& a, cudaStream_t s) {
+cudaError_t sort(const Args& a, cudaStream_t s) {
   cudaError_t e = cudaSuccess;
-  bool behind = a.T > 0;  // the sort
-  if (!a.accumulate) {
-    e = launch(absent_kernel<F32, Vector>, blocks_of((a.V + 31) / 32), 256, 0, s, behind, a);
-    behind = true;
+  if (a.few) {
+    // Zeros: as many rows a warp as leave each SM one block of them at most.
+    const int64_t rows = a.accumulate ? 0 : (a.V + 31) / 32;
+    const unsigned blocks = unsigned(kClasses + (rows < kSms ? rows : kSms));
+    int size = 32;
+    while (size < a.T) size *= 2;
+    if (size * sizeof(uint32_t) > (32 << 10)) {  // what a launch has without asking holds its static part too
+      e = cudaFuncSetAttribute(class_sort_kernel<F32, Vector>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               int(size * sizeof(uint32_t)));
+      if (e != cudaSuccess) return e;
+    }
+    return launch(class_sort_kernel<F32, Vector>, blocks, kClassThreads, size * sizeof(uint32_t), s, false, a);
   }
-  if (e == cudaSuccess && a.T > 0)
-    e = launch(sum_kernel<F32, Vector>, blocks_of(a.runs * a.blocks), 256, 0, s, behind, a);
+  for (int p = 0; e == cudaSuccess && p < a.passes; ++p) {
+    e = launch(count_kernel, unsigned(a.tiles), kSortThreads, 0, s, p > 0, a, p);
+    if (e == cudaSuccess) e = launch(place_kernel, unsigned(a.tiles), kSortThreads, 0, s, true, a, p);
+  }
+  return e;
+}
+
+template <bool F32, bool Vector>
+cudaError_t sums(const Args& a, cudaStream_t s) {
+  if (a.T == 0) return cudaSuccess;
+  const int64_t zero_warps = a.few || a.accumulate ? 0 : (a.V + 31) / 32;
+  cudaError_t e = launch(sum_kernel<F32, Vector>, blocks_of(a.runs * a.blocks + zero_warps), 256, 0, s, true, a,
+                         zero_warps);
   if (e == cudaSuccess && a.runs > 1)
     e = launch(join_kernel<F32, Vector>, blocks_of((a.runs - 1) * a.blocks), 256, 0, s, true, a);
   return e;
@@ -379,18 +591,19 @@ cudaError_t sums(const Args& a, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_lookup(const Args& a, cudaStream_t s) {
-  const unsigned blocks = blocks_of(a.T);
-  if (a.f32) return launch(a.vector ? lookup_kernel<true, true> : lookup_kernel<true, false>, blocks, 256, 0, s, false, a);
-  return launch(a.vector ? lookup_kernel<false, true> : lookup_kernel<false, false>, blocks, 256, 0, s, false, a);
+  const bool stream = a.T * a.D * (a.f32 ? 4 : 2) > kCacheBytes;
+  const auto run = [&](auto* kernel) { return launch(kernel, blocks_of(a.T), 256, 0, s, false, a); };
+  if (a.f32) {
+    if (a.vector) return stream ? run(lookup_kernel<true, true, true>) : run(lookup_kernel<true, true, false>);
+    return run(lookup_kernel<true, false, false>);
+  }
+  if (a.vector) return stream ? run(lookup_kernel<false, true, true>) : run(lookup_kernel<false, true, false>);
+  return run(lookup_kernel<false, false, false>);
 }
 
 cudaError_t launch_sort(const Args& a, cudaStream_t s) {
-  cudaError_t e = cudaSuccess;
-  for (int p = 0; e == cudaSuccess && p < a.passes; ++p) {
-    e = launch(count_kernel, unsigned(a.tiles), kSortThreads, 0, s, p > 0, a, p);
-    if (e == cudaSuccess) e = launch(place_kernel, unsigned(a.tiles), kSortThreads, 0, s, true, a, p);
-  }
-  return e;
+  if (a.f32) return a.vector ? sort<true, true>(a, s) : sort<true, false>(a, s);
+  return a.vector ? sort<false, true>(a, s) : sort<false, false>(a, s);
 }
 
 cudaError_t launch_sums(const Args& a, cudaStream_t s) {
