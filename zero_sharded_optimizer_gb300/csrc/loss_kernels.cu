@@ -2,6 +2,8 @@
 // zero_preference_*).
 #include <math.h>
 
+#include <type_traits>
+
 #include "loss_device.cuh"
 
 namespace zl {
@@ -288,7 +290,7 @@ enum Numbering { kTargets, kPrepare, kSlopes };
 // One block: numbers the rows in order, up to 16 times 1024 rows at a time.
 template <Numbering N>
 __global__ void __launch_bounds__(1024) number_rows_kernel(const Args a) {
-  __shared__ int32_t before[16][32], total[16], labelled[32];
+  __shared__ int32_t before[16][32], total[16];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   let_next_start();
   if (N != kPrepare) wait_for_previous();
@@ -309,18 +311,25 @@ __global__ void __launch_bounds__(1024) number_rows_kernel(const Args a) {
     unit = __uint_as_float(a.head->steepest);
     if (!(unit > 0.0f && unit < INFINITY)) unit = 1.0f;
   }
-  int32_t base = 0, targets = 0;
+  const int32_t targets = N == kSlopes ? a.head->rows : 0;
+  int32_t base = 0;
   for (int64_t t0 = 0; t0 < a.T; t0 += 16 * 1024) {
     uint32_t mask[16];
+    int32_t pos[16];
+    float scale[16];
 #pragma unroll
     for (int q = 0; q < 16; ++q) {
       const int64_t t = t0 + 1024 * q + threadIdx.x;
-      mask[q] = t < a.T && a.rowpos[t] >= 0;
+      pos[q] = t < a.T ? a.rowpos[t] : -1;
+      if (N == kSlopes) scale[q] = t < a.T ? a.scales[t] : 0.0f;
+    }
+#pragma unroll
+    for (int q = 0; q < 16; ++q) {
+      const int64_t t = t0 + 1024 * q + threadIdx.x;
+      mask[q] = pos[q] >= 0;
       if (N == kSlopes && mask[q]) {
-        ++targets;
-        float scale = a.scales[t];
-        if (a.kind == kPreference) a.scales[t] = scale /= unit;
-        mask[q] = scale != 0.0f;  // (also a NaN)
+        if (unit != 1.0f) a.scales[t] = scale[q] /= unit;
+        mask[q] = scale[q] != 0.0f;  // (also a NaN)
         if (!mask[q]) a.rowpos[t] = -2;
       }
     }
@@ -353,26 +362,15 @@ __global__ void __launch_bounds__(1024) number_rows_kernel(const Args a) {
     }
     __syncthreads();
   }
-  if (N == kSlopes) {
-    for (int o = 16; o; o >>= 1) targets += __shfl_xor_sync(~0u, targets, o);
-    if (lane == 0) labelled[warp] = targets;
-    __syncthreads();
-  }
   if (threadIdx.x == 0) {
-    if (N == kSlopes) {
-      targets = 0;
-      for (int w = 0; w < 32; ++w) targets += labelled[w];
-    } else {
-      targets = base;
-    }
     // The factor of both gradients that does not depend on the row: grad_scale,
     // the mean's count, and the reduced loss's own gradient.
     double f = a.grad_scale;
-    if (a.reduction == ZERO_REDUCE_MEAN) f /= double(max(1, N == kSlopes && a.kind == kPreference ? a.head->pairs : targets));
+    if (a.reduction == ZERO_REDUCE_MEAN) f /= double(max(1, N != kSlopes ? base : a.kind == kPreference ? a.head->pairs : targets));
     if (a.reduction != ZERO_REDUCE_NONE && a.dloss) f *= double(*a.dloss);
     f *= double(unit);
     if (N == kSlopes) {
-      a.head->repack = a.head->rows != base;
+      a.head->repack = targets != base;
       a.head->rows = base;
       a.head->factor = float(f);
     } else {
@@ -535,88 +533,117 @@ __device__ __forceinline__ double row_lse(const float2* stats, int64_t count, in
     for (int q = 0; q < 8; ++q) s += x[q].y * exp2f(x[q].x - top);  // 0 where x is -inf
     m = top;
   }
-  // A tree over the lanes, in a fixed order.
-  sh[lane * rows + r] = make_float2(m, s);
-  __syncthreads();
-  for (int w = lanes / 2; w; w >>= 1) {
-    if (lane < w) {
-      const float2 x = sh[lane * rows + r], y = sh[(lane + w) * rows + r];
-      const float top = fmaxf(x.x, y.x);
-      const float sum = top == -INFINITY ? x.y + y.y : x.y * exp2f(x.x - top) + y.y * exp2f(y.x - top);
-      sh[lane * rows + r] = make_float2(top, sum);
+  // A tree over the lanes, in a fixed order: between warps through shared memory,
+  // then (row r's lanes are `rows` threads apart) within the first.
+  const auto join = [](float2 x, float2 y) {
+    const float top = fmaxf(x.x, y.x);
+    const float sum = top == -INFINITY ? x.y + y.y : x.y * exp2f(x.x - top) + y.y * exp2f(y.x - top);
+    return make_float2(top, sum);
+  };
+  float2 x = make_float2(m, s);
+  int w = lanes / 2;
+  if (w * rows >= 32) {
+    sh[lane * rows + r] = x;
+    __syncthreads();
+    for (; w * rows >= 32; w >>= 1) {
+      if (lane < w) sh[lane * rows + r] = join(sh[lane * rows + r], sh[(lane + w) * rows + r]);
+      __syncthreads();
     }
+    x = sh[lane * rows + r];
     __syncthreads();
   }
-  const float2 x = sh[r];
-  __syncthreads();
+  for (; w; w >>= 1) {
+    const float2 y = make_float2(__shfl_down_sync(~0u, x.x, w * rows), __shfl_down_sync(~0u, x.y, w * rows));
+    if (lane < w) x = join(x, y);
+  }
   return lane == 0 ? (double(x.x) + log2(double(x.y))) * 0.69314718055994530942 : 0.0;
 }
 
-// The product of the row's hidden state and its label's weight in fp32, rounded
-// at every addition: a warp's lanes take every 32nd group of elements.
-template <bool F32>
-__device__ __forceinline__ float label_logit(const Args& a, int64_t t, int32_t y, bool vector, int lane) {
+// The products of N rows' hidden states and their labels' weights in fp32, rounded
+// at every addition: a warp's lanes take every 32nd group of elements, all rows'
+// loads in flight together. Rows t (and labels y) below zero are left out.
+template <bool F32, int N>
+__device__ __forceinline__ void label_logits(const Args& a, const int64_t (&t)[N], const int32_t (&y)[N], bool vector,
+                                             int lane, float (&logit)[N]) {
+  using E = typename std::conditional<F32, float, __nv_bfloat16>::type;
   constexpr int kWide = F32 ? 4 : 8;
-  float sum[kWide] = {};
-  const int64_t ho = t * a.hidden_stride, wo = y * a.weight_stride;
-  if (F32) {
-    const float *h = static_cast<const float*>(a.hidden) + ho, *w = static_cast<const float*>(a.weight) + wo;
-    if (vector) {
-#pragma unroll 4
-      for (int64_t k = lane * 4; k + 4 <= a.D; k += 128) {
-        const float4 x = *reinterpret_cast<const float4*>(h + k), z = *reinterpret_cast<const float4*>(w + k);
-        sum[0] = fmaf(x.x, z.x, sum[0]);
-        sum[1] = fmaf(x.y, z.y, sum[1]);
-        sum[2] = fmaf(x.z, z.z, sum[2]);
-        sum[3] = fmaf(x.w, z.w, sum[3]);
-      }
-    }
-    for (int64_t k = (vector ? a.D / 4 * 4 : 0) + lane; k < a.D; k += 32) sum[0] = fmaf(h[k], w[k], sum[0]);
-  } else {
-    const __nv_bfloat16 *h = static_cast<const __nv_bfloat16*>(a.hidden) + ho,
-                        *w = static_cast<const __nv_bfloat16*>(a.weight) + wo;
-    if (vector) {
-#pragma unroll 4
-      for (int64_t k = lane * 8; k + 8 <= a.D; k += 256) {
-        const uint4 x = *reinterpret_cast<const uint4*>(h + k), z = *reinterpret_cast<const uint4*>(w + k);
-        const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, zs[4] = {z.x, z.y, z.z, z.w};
+  const E *h[N], *w[N];
+  float sum[N][kWide] = {};
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          sum[2 * q] = fmaf(__uint_as_float(xs[q] << 16), __uint_as_float(zs[q] << 16), sum[2 * q]);
-          sum[2 * q + 1] = fmaf(__uint_as_float(xs[q] & 0xffff0000u), __uint_as_float(zs[q] & 0xffff0000u),
-                                sum[2 * q + 1]);
+  for (int q = 0; q < N; ++q) {
+    h[q] = static_cast<const E*>(a.hidden) + (t[q] < 0 ? 0 : t[q]) * a.hidden_stride;
+    w[q] = static_cast<const E*>(a.weight) + (t[q] < 0 ? 0 : y[q]) * a.weight_stride;
+  }
+  const int64_t whole = vector ? a.D / kWide * kWide : 0;
+#pragma unroll 2
+  for (int64_t k = lane * kWide; k < whole; k += 32 * kWide) {
+#pragma unroll
+    for (int q = 0; q < N; ++q) {
+      if (t[q] < 0) continue;
+      const uint4 x = *reinterpret_cast<const uint4*>(h[q] + k), z = *reinterpret_cast<const uint4*>(w[q] + k);
+      const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, zs[4] = {z.x, z.y, z.z, z.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (F32) {
+          sum[q][j] = fmaf(__uint_as_float(xs[j]), __uint_as_float(zs[j]), sum[q][j]);
+        } else {
+          sum[q][2 * j % kWide] =
+              fmaf(__uint_as_float(xs[j] << 16), __uint_as_float(zs[j] << 16), sum[q][2 * j % kWide]);
+          sum[q][(2 * j + 1) % kWide] = fmaf(__uint_as_float(xs[j] & 0xffff0000u),
+                                             __uint_as_float(zs[j] & 0xffff0000u), sum[q][(2 * j + 1) % kWide]);
         }
       }
     }
-    for (int64_t k = (vector ? a.D / 8 * 8 : 0) + lane; k < a.D; k += 32)
-      sum[0] = fmaf(float(h[k]), float(w[k]), sum[0]);
+  }
+  for (int64_t k = whole + lane; k < a.D; k += 32) {
+#pragma unroll
+    for (int q = 0; q < N; ++q)
+      if (t[q] >= 0) sum[q][0] = fmaf(float(h[q][k]), float(w[q][k]), sum[q][0]);
   }
 #pragma unroll
-  for (int n = kWide / 2; n; n /= 2)
+  for (int q = 0; q < N; ++q) {
 #pragma unroll
-    for (int q = 0; q < n; ++q) sum[q] += sum[q + n];
-  return warp_sum(sum[0]);
+    for (int n = kWide / 2; n; n /= 2)
+#pragma unroll
+      for (int j = 0; j < n; ++j) sum[q][j] += sum[q][j + n];
+    logit[q] = warp_sum(sum[q][0]);
+  }
+}
+
+// log(1 + p (e^d - 1)) for a probability p = e^l: what a logit's change by d adds
+// to a log-sum-exp. d is a rounding error as a rule, where two terms of the
+// series leave out less than d^3.
+__device__ __forceinline__ double corrected(double d, float l) {
+  const double p = expf(l);
+  return fabs(d) < 0.001 ? p * d * (1.0 + 0.5 * (1.0 - p) * d) : log1p(p * expm1(d));
 }
 
 // The policy loss of a row and its slope by the log-probability l. What is not a
 // number stays none (maxima by comparison, not by fmax). An advantage of zero
-// has no part in the loss, whatever the ratio.
-__device__ __forceinline__ void policy_loss(const Args& a, int64_t t, float l, double* loss, double* slope) {
+// has no part in the loss, whatever the ratio. (The exponentials are fp32's, off
+// by 2^-22 of themselves, less than l's own error makes them.)
+struct PolicyRow {
+  float advantage, old_logp, ref_logp, dloss;
+};
+__device__ __forceinline__ void policy_loss(const Args& a, const PolicyRow& row, float l, double* loss,
+                                            double* slope) {
   *loss = *slope = 0.0;
-  const double adv = double(a.advantages[t]);
+  const double adv = double(row.advantage);
   if (adv != 0.0) {
-    const double ratio = exp(double(l) - double(a.old_logps[t]));
+    const double ratio = expf(float(double(l) - double(row.old_logp)));
     const double bounded = ratio < a.low ? a.low : ratio > a.high ? a.high : ratio;
     const double free = -adv * ratio, held = -adv * bounded;
     *loss = free < held ? held : free;
     *slope = free < held ? 0.0 : free;
   }
   if (a.kl_weight != 0.0) {
-    const double d = double(a.ref_logps[t]) - double(l), e = expm1(d);
+    const double d = double(row.ref_logp) - double(l), e = expm1f(float(d));
     *loss += a.kl_weight * (e - d);
     *slope -= a.kl_weight * e;
   }
 }
+
+constexpr int kSlopeRows = 16;  // most rows of a block of losses_kernel that goes by slopes
 
 // 256 threads: `block_rows` rows (a power of two, up to 32), 256 / block_rows lanes each.
 //
@@ -628,10 +655,11 @@ __device__ __forceinline__ void policy_loss(const Args& a, int64_t t, float l, d
 // one sign). The label's logit is therefore taken again in rounding fp32, and
 // its share of the log-sum-exp corrected: log(S + e^z' - e^z).
 template <bool Slopes, bool F32>
-__global__ void __launch_bounds__(256) losses_kernel(const Args a, int block_rows, bool vector) {
+__global__ void __launch_bounds__(256, 4) losses_kernel(const Args a, int block_rows, bool vector) {
   __shared__ float2 sh[256];
   __shared__ double part[256];
-  __shared__ float logit[32];
+  constexpr int kLogits = kSlopeRows / 8;
+  __shared__ float logit[kSlopeRows];
   __shared__ bool last;
   let_next_start();
   wait_for_previous();
@@ -641,12 +669,29 @@ __global__ void __launch_bounds__(256) losses_kernel(const Args a, int block_row
   for (int64_t i0 = int64_t(blockIdx.x) * block_rows; i0 < rows; i0 += int64_t(gridDim.x) * block_rows) {
     const int64_t i = min(i0 + r, int64_t(rows) - 1);
     const int64_t t = a.rowmap[i];
+    PolicyRow row{0.0f, 0.0f, 0.0f, 1.0f};  // read ahead of its use
+    if (Slopes && a.kind == kPolicy && lane == 0) {
+      row.advantage = a.advantages[t];
+      row.old_logp = a.old_logps[t];
+      if (a.kl_weight != 0.0) row.ref_logp = a.ref_logps[t];
+      if (a.scales && a.reduction == ZERO_REDUCE_NONE && a.dloss) row.dloss = a.dloss[t];
+    }
     if (Slopes) {
-      for (int q = threadIdx.x >> 5; q < block_rows && i0 + q < rows; q += 8) {
-        const int64_t u = a.rowmap[i0 + q];
-        const float z = label_logit<F32>(a, u, a.ids[u], vector, threadIdx.x & 31);
-        if ((threadIdx.x & 31) == 0) logit[q] = z;
+      // The block's warps take the rows in turn, each up to kLogits.
+      int64_t u[kLogits];
+      int32_t y[kLogits];
+      float z[kLogits];
+#pragma unroll
+      for (int n = 0; n < kLogits; ++n) {
+        const int q = (threadIdx.x >> 5) + 8 * n;
+        u[n] = q < block_rows && i0 + q < rows ? a.rowmap[i0 + q] : -1;
       }
+#pragma unroll
+      for (int n = 0; n < kLogits; ++n) y[n] = u[n] >= 0 ? a.ids[u[n]] : 0;
+      if (u[0] >= 0) label_logits<F32, kLogits>(a, u, y, vector, threadIdx.x & 31, z);
+#pragma unroll
+      for (int n = 0; n < kLogits; ++n)
+        if ((threadIdx.x & 31) == 0 && u[n] >= 0) logit[(threadIdx.x >> 5) + 8 * n] = z[n];
       __syncthreads();
     }
     double entries = 0.0;
@@ -658,17 +703,20 @@ __global__ void __launch_bounds__(256) losses_kernel(const Args a, int block_row
     const double lse = a.has_ce ? row_lse(a.stats, 2 * a.tiles, a.Tp, i, lane, lanes, sh, r, block_rows) : 0.0;
     const double lse_tau =
         a.has_kd ? row_lse(a.stats_tau, 2 * a.tiles, a.Tp, i, lane, lanes, sh, r, block_rows) : 0.0;
-    part[threadIdx.x] = entries;
-    __syncthreads();
-    for (int w = lanes / 2; w; w >>= 1) {
-      if (lane < w) part[threadIdx.x] += part[threadIdx.x + w * block_rows];
+    if (a.L > 1) {
+      part[threadIdx.x] = entries;
       __syncthreads();
+      for (int w = lanes / 2; w; w >>= 1) {
+        if (lane < w) part[threadIdx.x] += part[threadIdx.x + w * block_rows];
+        __syncthreads();
+      }
+      entries = part[r];
     }
     const bool fault = a.head->fault;  // NaN in lse too: a backward call's gradients show it then
     if (Slopes && lane == 0 && i0 + r < rows) {
-      const double z = part[r], more = double(logit[r]) - z;
+      const double z = entries, more = double(logit[r]) - z;
       const bool finite = isfinite(more) && isfinite(lse);
-      const double sum = finite ? lse + log1p(exp(z - lse) * expm1(more)) : lse;
+      const double sum = finite ? lse + corrected(more, float(z - lse)) : lse;
       const double logp = fault ? NAN : (finite ? double(logit[r]) : z) - sum;
       a.lse[t] = fault ? NAN : float(sum);
       if (a.kind == kPreference) {
@@ -676,12 +724,12 @@ __global__ void __launch_bounds__(256) losses_kernel(const Args a, int block_row
       } else {
         const float l = float(logp);
         double loss, slope;
-        policy_loss(a, t, l, &loss, &slope);
+        policy_loss(a, row, l, &loss, &slope);
         a.loss[t] = fault ? NAN : float(loss);
         a.logps[t] = l;
         const float s = fault ? NAN : float(slope);
         a.slopes[t] = s;
-        if (a.scales) a.scales[t] = -s * (a.reduction == ZERO_REDUCE_NONE && a.dloss ? a.dloss[t] : 1.0f);
+        if (a.scales) a.scales[t] = -s * row.dloss;
         mine += double(fault ? NAN : float(loss));
       }
     } else if (!Slopes && lane == 0 && i0 + r < rows) {
@@ -689,7 +737,7 @@ __global__ void __launch_bounds__(256) losses_kernel(const Args a, int block_row
       double loss = double(a.konst[t]);
       if (f.x != 0.0f) loss += double(f.x) * lse;
       if (f.y != 0.0f) loss += double(f.y) * a.tau * lse_tau;
-      loss -= part[r];
+      loss -= entries;
       if (fault) loss = NAN;
       a.loss[t] = float(loss);
       if (a.has_ce) a.lse[t] = fault ? NAN : float(lse);
@@ -725,17 +773,23 @@ __global__ void __launch_bounds__(256) losses_kernel(const Args a, int block_row
 
 // ------------------------------------------------------------------- pairs --
 
-// The sum over the block's 256 threads, in a fixed order, in all of them.
-__device__ __forceinline__ double block_sum(double x, double* sh) {
-  sh[threadIdx.x] = x;
-  __syncthreads();
-  for (int w = 128; w; w >>= 1) {
-    if (int(threadIdx.x) < w) sh[threadIdx.x] += sh[threadIdx.x + w];
-    __syncthreads();
+// The sums over the block's 256 threads, in a fixed order, in all of them.
+template <int N>
+__device__ __forceinline__ void block_sums(double (&x)[N], double (*sh)[8]) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int q = 0; q < N; ++q) {
+    for (int o = 16; o; o >>= 1) x[q] += __shfl_xor_sync(~0u, x[q], o);
+    if (lane == 0) sh[q][warp] = x[q];
   }
-  const double sum = sh[0];
   __syncthreads();
-  return sum;
+#pragma unroll
+  for (int q = 0; q < N; ++q) {
+    x[q] = sh[q][0];
+#pragma unroll
+    for (int w = 1; w < 8; ++w) x[q] += sh[q][w];
+  }
+  __syncthreads();
 }
 
 // The loss of a pair and its slopes by each of its rows' log-probabilities, from
@@ -754,8 +808,9 @@ __device__ __forceinline__ void pair_loss(const Args& a, int64_t i, const double
     *loss = u * u;
     du = 2.0 * u;
   } else {
-    // log(1 + e^-u) and log(1 + e^u), and sigmoid(-u), from e^-|u|
-    const double e = exp(-fabs(u)), l = log1p(e), down = (u < 0.0 ? 1.0 : e) / (1.0 + e);
+    // log(1 + e^-u) and log(1 + e^u), and sigmoid(-u), from e^-|u|; fp32's
+    // functions are off by 2^-22 of themselves, as the results' own type is
+    const float e = expf(-fabsf(float(u))), l = log1pf(e), down = (u < 0.0 ? 1.0f : e) / (1.0f + e);
     *loss = (1.0 - a.smoothing) * ((u < 0.0 ? -u : 0.0) + l) + a.smoothing * ((u > 0.0 ? u : 0.0) + l);
     if (u != u) *loss = u;
     du = a.smoothing - down;
@@ -772,7 +827,7 @@ __device__ __forceinline__ void pair_loss(const Args& a, int64_t i, const double
 // slopes are given; then the rows' scales where a backward pass follows.
 template <bool Forward>
 __global__ void __launch_bounds__(256) pairs_kernel(const Args a) {
-  __shared__ double sh[256];
+  __shared__ double sh[4][8];
   __shared__ float slopes[2];
   __shared__ bool last;
   let_next_start();
@@ -800,23 +855,26 @@ __global__ void __launch_bounds__(256) pairs_kernel(const Args a) {
   const int64_t length = a.offsets || a.pairs == 0 ? 0 : a.T / (2 * a.pairs);
   for (int64_t i = blockIdx.x; i < a.pairs; i += gridDim.x) {
     int64_t begin[2], end[2];
-    double sum[2] = {};
-    int n[2];
+    double x[4] = {};  // the sequences' labelled rows and their log-probabilities
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const int64_t s = i + k * a.pairs;
       begin[k] = a.offsets ? a.offsets[s] : s * length;
       end[k] = a.offsets ? a.offsets[s + 1] : (s + 1) * length;
-      int count = 0;
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
 #pragma unroll 4
       for (int64_t t = begin[k] + threadIdx.x; t < end[k]; t += 256) {
-        if (a.rowpos[t] < 0) continue;
-        ++count;
-        if (Forward) sum[k] += a.row_logps[t];
+        const bool labelled = a.rowpos[t] >= 0;
+        const double l = Forward ? a.row_logps[t] : 0.0;  // (of a row without a label: anything)
+        x[k] += labelled ? 1.0 : 0.0;
+        if (Forward) x[2 + k] += labelled ? l : 0.0;
       }
-      n[k] = int(block_sum(double(count), sh));
-      if (Forward) sum[k] = block_sum(sum[k], sh);
     }
+    block_sums(x, sh);
+    const int n[2] = {int(x[0]), int(x[1])};
+    const double sum[2] = {x[2], x[3]};
     const bool some = n[0] + n[1] > 0;
     if (threadIdx.x == 0) {
       if (some) atomicAdd(&a.head->pairs, 1);
@@ -859,11 +917,11 @@ __global__ void __launch_bounds__(256) pairs_kernel(const Args a) {
   __syncthreads();
   if (!last) return;
   __threadfence();
-  double sum = 0.0;
-  for (int b = threadIdx.x; b < int(gridDim.x); b += 256) sum += __ldcg(a.sums + b);
-  sum = block_sum(sum, sh);
+  double sum[1] = {};
+  for (int b = threadIdx.x; b < int(gridDim.x); b += 256) sum[0] += __ldcg(a.sums + b);
+  block_sums(sum, sh);
   if (threadIdx.x == 0)
-    *a.reduced = float(a.reduction == ZERO_REDUCE_MEAN ? sum / double(max(1, __ldcg(&a.head->pairs))) : sum);
+    *a.reduced = float(a.reduction == ZERO_REDUCE_MEAN ? sum[0] / double(max(1, __ldcg(&a.head->pairs))) : sum[0]);
 }
 
 // The rows' scales of a policy's backward call.
@@ -923,15 +981,15 @@ cudaError_t launch_pack(const Args& a, __nv_bfloat16* weight, bool again, cudaSt
 cudaError_t launch_losses(const Args& a, cudaStream_t s) {
   // As many lanes to a row as leave a block for each SM (333 rows with two
   // softmaxes and 100 entries: a step of 197 us, 227 with 32 rows a block).
-  int rows = 32;
+  const bool slopes = a.kind == kPolicy || a.kind == kPreference;
+  int rows = slopes ? kSlopeRows : 32;
   while (rows > 1 && a.T / rows < kSms) rows /= 2;
   int64_t blocks = (a.T + rows - 1) / rows;
   blocks = blocks < 1 ? 1 : blocks < kLossBlocks ? blocks : kLossBlocks;
   const bool f32 = a.planes == 3;
   const bool vector = aligned16(a.hidden, a.hidden_stride * (f32 ? 4 : 2)) &&
                       aligned16(a.weight, a.weight_stride * (f32 ? 4 : 2));
-  auto* kernel = a.kind == kXent || a.kind == kDistill ? losses_kernel<false, false>
-                 : f32 ? losses_kernel<true, true> : losses_kernel<true, false>;
+  auto* kernel = !slopes ? losses_kernel<false, false> : f32 ? losses_kernel<true, true> : losses_kernel<true, false>;
   return launch(kernel, unsigned(blocks), 256, 0, s, true, a, rows, vector);
 }
 
