@@ -84,7 +84,9 @@ int plan(const zero_embedding_t* p, Args* a, int64_t* bytes) {
   const int64_t block = p->precision == ZERO_FP32 ? 128 : 256;
   a->blocks = int32_t((p->D + block - 1) / block);
   a->Dp = a->blocks * block;
-  a->run = 32;
+  // Long runs mean few shares of segments to be written, read and joined, short
+  // ones work for all SMs.
+  a->run = 128;
   while (a->run > 8 && (p->T + a->run - 1) / a->run * a->blocks < ze::kSms * 32) a->run /= 2;
   a->runs = (p->T + a->run - 1) / a->run;
   Layout w{static_cast<uint8_t*>(p->workspace)};

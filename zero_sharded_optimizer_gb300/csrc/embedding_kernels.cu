@@ -417,8 +417,8 @@ __device__ __forceinline__ void zero_absent_rows(const Args& a, int64_t v0) {
   }
 }
 
-// A warp for a run and a block of columns, and after those one for 32 ids whose
-// rows may have to become zero.
+// A warp for 32 ids whose rows may have to become zero -- the long pieces of work
+// first -- and one for each run and block of columns.
 template <bool F32, bool Vector>
 __global__ void __launch_bounds__(256, 3) sum_kernel(const Args a, int64_t zero_warps) {
   using C = Columns<F32, Vector>;
@@ -428,46 +428,51 @@ __global__ void __launch_bounds__(256, 3) sum_kernel(const Args a, int64_t zero_
   const int lane = threadIdx.x & 31;
   const Entry* const list = a.sorted;
   const int64_t step = int64_t(gridDim.x) * 8, sums = a.runs * a.blocks;
-  for (int64_t g = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5); g < sums + zero_warps; g += step) {
-    if (g >= sums) {
-      zero_absent_rows<F32, Vector>(a, (g - sums) * 32);
+  for (int64_t g = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5) - zero_warps; g < sums; g += step) {
+    if (g < 0) {
+      zero_absent_rows<F32, Vector>(a, (g + zero_warps) * 32);
       continue;
     }
     const int64_t run = g / a.blocks, first = run * a.run, block = g % a.blocks;
     const C c(block * C::kBlock, a.D, lane);
     const int count = int(min(int64_t(a.run), a.T - first));
-    const Entry e = lane < count ? list[first + lane] : Entry{kNone, 0};
     const uint32_t prev = first > 0 ? list[first - 1].id : kNone;
-    const uint32_t next = first + count < a.T ? list[first + count].id : kNone;
-    const int n = __popc(__ballot_sync(~0u, e.id < a.V));  // those without a row come last
-    bool begun = __shfl_sync(~0u, e.id, 0) != prev;  // the segment begins in this run
     float sum[kVec] = {};
-    for (int i0 = 0; i0 < n; i0 += kAhead) {
-      uint4 w[kAhead];
+    bool begun = true;  // the segment begins in this run
+    for (int s0 = 0; s0 < count; s0 += 32) {  // 32 entries at a time, one a lane
+      const int held = min(32, count - s0);
+      const Entry e = lane < held ? list[first + s0 + lane] : Entry{kNone, 0};
+      const uint32_t next = first + s0 + held < a.T ? list[first + s0 + held].id : kNone;
+      const int n = __popc(__ballot_sync(~0u, e.id < a.V));  // those without a row come last
+      if (s0 == 0) begun = __shfl_sync(~0u, e.id, 0) != prev;
+      for (int i0 = 0; i0 < n; i0 += kAhead) {
+        uint4 w[kAhead];
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        const uint32_t t = __shfl_sync(~0u, e.t, (i0 + i) & 31);
-        if (i0 + i < n) w[i] = c.template load<true>(row_of<F32>(a.table, a.table_stride, t));
-      }
+        for (int i = 0; i < kAhead; ++i) {
+          const uint32_t t = __shfl_sync(~0u, e.t, (i0 + i) & 31);
+          if (i0 + i < n) w[i] = c.template load<true>(row_of<F32>(a.table, a.table_stride, t));
+        }
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        const uint32_t id = __shfl_sync(~0u, e.id, (i0 + i) & 31);
-        const uint32_t following = __shfl_sync(~0u, e.id, (i0 + i + 1) & 31);
-        if (i0 + i >= n) break;
-        float x[kVec];
-        C::unpack(w[i], x);
+        for (int i = 0; i < kAhead; ++i) {
+          const uint32_t id = __shfl_sync(~0u, e.id, (i0 + i) & 31);
+          const uint32_t following = __shfl_sync(~0u, e.id, (i0 + i + 1) & 31);
+          if (i0 + i >= n) break;
+          float x[kVec];
+          C::unpack(w[i], x);
 #pragma unroll
-        for (int j = 0; j < kVec; ++j) sum[j] += x[j];
-        const bool last = i0 + i + 1 == count;
-        const bool ends = (last ? next : following) != id;
-        if (ends && begun) finish(a, c, id, sum);
-        else if (ends || last) put_share(share<kVec>(a, run, begun ? 1 : 0, block, lane), sum);
-        if (ends) {
-          begun = true;
+          for (int j = 0; j < kVec; ++j) sum[j] += x[j];
+          const bool ends = (i0 + i + 1 == held ? next : following) != id;
+          const bool last = s0 + i0 + i + 1 == count;
+          if (ends && begun) finish(a, c, id, sum);
+          else if (ends || last) put_share(share<kVec>(a, run, begun ? 1 : 0, block, lane), sum);
+          if (ends) {
+            begun = true;
 #pragma unroll
-          for (int j = 0; j < kVec; ++j) sum[j] = 0.0f;
+            for (int j = 0; j < kVec; ++j) sum[j] = 0.0f;
+          }
         }
       }
+      if (n < held) break;
     }
   }
 }
