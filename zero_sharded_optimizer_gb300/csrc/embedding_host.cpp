@@ -73,6 +73,8 @@ int plan(const zero_embedding_t* p, Args* a, int64_t* bytes) {
   common(p, p->dout, p->dout_stride, p->dweight, p->dweight_stride, a);
   a->accumulate = p->accumulate != 0;
   a->few = p->T <= ze::kFewTokens && (p->V <= ze::kFewIds || p->T == 0);
+  // A class's ids in a block's shared memory, and no more blocks than SMs if they fit.
+  a->class_bits = p->V <= int64_t(ze::kClassIds) << 7 ? 7 : ze::kMostClassBits;
   // The fewest digits, of equal width, that hold the ids and V itself.
   int bits = 1;
   while (p->V >> bits) ++bits;
@@ -84,13 +86,13 @@ int plan(const zero_embedding_t* p, Args* a, int64_t* bytes) {
   const int64_t block = p->precision == ZERO_FP32 ? 128 : 256;
   a->blocks = int32_t((p->D + block - 1) / block);
   a->Dp = a->blocks * block;
-  // Long runs mean few shares of segments to be written, read and joined, short
-  // ones work for all SMs.
+  // Long runs mean few shares of segments to be written, read and joined (131072
+  // tokens of width 4096: 400 us, 448 with runs of 32), short ones work for all SMs.
   a->run = 128;
   while (a->run > 8 && (p->T + a->run - 1) / a->run * a->blocks < ze::kSms * 32) a->run /= 2;
   a->runs = (p->T + a->run - 1) / a->run;
   Layout w{static_cast<uint8_t*>(p->workspace)};
-  a->counts = w.take<int32_t>(int64_t(a->tiles) << a->bits);
+  a->counts = w.take<int32_t>(int64_t(a->passes) * a->tiles << a->bits);
   for (auto& l : a->list) l = w.take<ze::Entry>(p->T);
   a->sorted = a->list[a->few ? 0 : (a->passes - 1) & 1];
   a->part = w.take<float>(2 * a->runs, a->Dp);

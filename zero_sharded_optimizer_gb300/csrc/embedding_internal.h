@@ -17,9 +17,10 @@ constexpr int kMostTiles = 256;  // of the sort
 
 // Up to so many tokens, and ids below so many, one kernel sorts (class_sort_kernel).
 constexpr int kPositionBits = 15;
-constexpr int kClassBits = 7;
 constexpr int64_t kFewTokens = int64_t(1) << kPositionBits;
-constexpr int64_t kFewIds = int64_t(1) << (32 - kPositionBits + kClassBits);
+constexpr int kClassIds = 1024;                     // most ids of a class
+constexpr int kMostClassBits = 8;
+constexpr int64_t kFewIds = int64_t(kClassIds) << kMostClassBits;
 
 // A token in the sorted list: its id (V, at the list's end: none) and its position.
 struct Entry {
@@ -41,6 +42,7 @@ struct Args {
 
   // Backward: the sort's digits and tiles, and the sums' runs of sorted tokens.
   int32_t few;             // the tokens are sorted by one kernel, which also writes the zeros
+  int32_t class_bits;      // of an id, that say its class there
   int32_t bits, passes;    // of a digit; digits
   int64_t tile;            // tokens of a tile, a multiple of the block's threads
   int32_t tiles;
@@ -48,7 +50,7 @@ struct Args {
   int64_t runs;
   int32_t blocks;          // blocks of columns
   int64_t Dp;              // their columns
-  int32_t* counts;         // [tiles][bins] tokens of a tile by digit
+  int32_t* counts;         // [passes][tiles][bins] tokens of a tile by digit
   Entry* list[2];          // [T] before and after a pass
   const Entry* sorted;     // the one that the last pass writes
   float* part;             // [runs][2][Dp] a run's share of the segment that began before it, and of

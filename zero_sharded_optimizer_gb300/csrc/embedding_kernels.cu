@@ -12,6 +12,8 @@
 
 #include <cuda_bf16.h>
 
+#include <atomic>
+
 #include "embedding_internal.h"
 #include "launch.cuh"
 
@@ -167,16 +169,17 @@ __global__ void __launch_bounds__(256) lookup_kernel(const Args a) {
 // Few tokens: one kernel, a block for each class of ids (their low bits, so that
 // the frequent ids of a vocabulary in order of frequency are spread). Each block
 // reads all ids, counts those of smaller classes -- its place in the list --
-// gathers its own and sorts them by id and position in shared memory. The list is
-// in order of class, then of id. Blocks behind those write dweight's zeros
-// meanwhile.
+// gathers its own in order and places them by the rest of their ids, counted warp
+// by warp in shared memory: no exchange between blocks, and the same work however
+// often an id comes. The list is in order of class, then of id. Blocks behind those
+// write dweight's zeros meanwhile.
 //
 // More tokens: by digits of the id from the lowest, each pass stable: a tile's
-// tokens are counted by digit, and the next kernel's block of that tile adds up
-// what comes before -- smaller digits of all tiles, its digit in earlier tiles --
-// and places its tokens, each warp a stretch of them in order.
+// tokens are counted by digit, and the block of that tile adds up what comes before
+// -- smaller digits of all tiles, its digit in earlier tiles -- and places its
+// tokens, each warp a stretch of them in order, counting the next digit by the
+// tiles that they go to.
 
-constexpr int kClasses = 1 << kClassBits;
 constexpr int kClassThreads = 1024;
 
 template <bool F32, bool Vector>
@@ -189,84 +192,124 @@ __device__ __forceinline__ void zero_rows(const Args& a, int64_t first, int64_t 
   }
 }
 
+// The numbers of the lane's earlier lanes and of all lanes, added up.
+__device__ __forceinline__ int before_lane(int x, int lane, int* all) {
+  int upto = x;
+  for (int o = 1; o < 32; o *= 2) {
+    const int y = __shfl_up_sync(~0u, upto, o);
+    if (lane >= o) upto += y;
+  }
+  *all = __shfl_sync(~0u, upto, 31);
+  return upto - x;
+}
+
+struct ClassShared {
+  uint16_t count[32][kClassIds];  // tokens of a warp's stretch by id, then their places
+  uint16_t first[kClassIds];      // of an id's tokens among the class's
+  // and behind it the class's tokens in order: the rest of the id, the position
+};
+
 template <bool F32, bool Vector>
 __global__ void __launch_bounds__(kClassThreads) class_sort_kernel(const Args a) {
-  extern __shared__ uint32_t keys[];  // id without its class, then position
-  __shared__ int32_t found, less_of[32], none_of[32];
+  constexpr int kEach = int(kFewTokens / kClassThreads);  // most tokens of a thread
+  static_assert(kClassIds <= kClassThreads, "a thread for each id of a class");
+  extern __shared__ ClassShared sh[];
+  auto& count = sh->count;
+  auto& first = sh->first;
+  uint32_t* const keys = reinterpret_cast<uint32_t*>(sh + 1);
+  __shared__ int32_t own_of[32], less_of[32], none_of[32];
   let_next_start();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (blockIdx.x >= kClasses) {
-    zero_rows<F32, Vector>(a, int64_t(blockIdx.x - kClasses) * 32 + warp, int64_t(gridDim.x - kClasses) * 32);
+  const int classes = 1 << a.class_bits, mine = blockIdx.x;
+  if (mine >= classes) {
+    zero_rows<F32, Vector>(a, int64_t(mine - classes) * 32 + warp, int64_t(gridDim.x - classes) * 32);
     return;
   }
-  if (threadIdx.x == 0) found = 0;
-  __syncthreads();
-  const int T = int(a.T), mine = blockIdx.x;
-  int less = 0, none = 0;
-  for (int t0 = 0; t0 < T; t0 += 8 * kClassThreads) {
-    int64_t id[8];
+  // Each warp's stretch of the tokens; an id that is not the class's becomes -1.
+  const int T = int(a.T), stretch = (T + 1023) / 1024 * 32, begin = warp * stretch;
+  int32_t id[kEach];
+  int less = 0, none = 0, own = 0;
+#pragma unroll
+  for (int q0 = 0; q0 < kEach; q0 += 8) {
+    if (q0 * 32 >= stretch) break;
+    int64_t x[8];
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
-      const int t = t0 + q * kClassThreads + threadIdx.x;
-      id[q] = t < T ? a.ids[t] : -2;
+      const int o = (q0 + q) * 32 + lane, t = begin + o;
+      x[q] = o < stretch && t < T ? a.ids[t] : -2;
+      if (o >= stretch || t >= T) --none;
     }
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
-      const int t = t0 + q * kClassThreads + threadIdx.x;
-      const bool valid = t < T && id[q] >= 0 && id[q] < a.V && id[q] != a.padding_id;
-      const int its = int(id[q] & (kClasses - 1));
-      none += t < T && !valid;
+      const bool valid = x[q] >= 0 && x[q] < a.V && x[q] != a.padding_id;
+      const int its = int(x[q]) & (classes - 1);
+      none += !valid;
       less += valid && its < mine;
-      const unsigned in = __ballot_sync(~0u, valid && its == mine);
-      if (in) {
-        int at = 0;
-        if (lane == 0) at = atomicAdd(&found, __popc(in));
-        at = __shfl_sync(~0u, at, 0) + __popc(in & ((1u << lane) - 1));
-        if (in >> lane & 1) keys[at] = uint32_t(id[q] >> kClassBits) << kPositionBits | uint32_t(t);
-      }
+      id[q0 + q] = valid && its == mine ? int32_t(x[q]) : -1;
+      own += __popc(__ballot_sync(~0u, id[q0 + q] >= 0));
     }
   }
+  for (int n = threadIdx.x; n < 32 * kClassIds / 2; n += kClassThreads) reinterpret_cast<uint32_t*>(count)[n] = 0;
   for (int o = 16; o; o >>= 1) {
     less += __shfl_xor_sync(~0u, less, o);
     none += __shfl_xor_sync(~0u, none, o);
   }
   if (lane == 0) {
+    own_of[warp] = own;
     less_of[warp] = less;
     none_of[warp] = none;
   }
   __syncthreads();
-  const int n = found;
-  int size = 32;  // a power of two
-  while (size < n) size *= 2;
-  for (int i = n + threadIdx.x; i < size; i += kClassThreads) keys[i] = ~0u;
-  less = less_of[lane];
-  none = none_of[lane];
-  for (int o = 16; o; o >>= 1) {
-    less += __shfl_xor_sync(~0u, less, o);
-    none += __shfl_xor_sync(~0u, none, o);
+  int n, place = before_lane(own_of[lane], lane, &n);
+  before_lane(less_of[lane], lane, &less);
+  before_lane(none_of[lane], lane, &none);
+  place = __shfl_sync(~0u, place, warp);
+#pragma unroll
+  for (int q = 0; q < kEach; ++q) {
+    if (q * 32 >= stretch) break;
+    const unsigned in = __ballot_sync(~0u, id[q] >= 0);
+    if (id[q] >= 0)
+      keys[place + __popc(in & ((1u << lane) - 1))] =
+          uint32_t(id[q] >> a.class_bits) << kPositionBits | uint32_t(begin + q * 32 + lane);
+    place += __popc(in);
   }
   __syncthreads();
-  // A bitonic network: all keys differ, so the order in which they were found
-  // leaves no trace.
-  for (int k = 2; k <= size; k *= 2) {
-    for (int j = k / 2; j; j /= 2) {
-      for (int p = threadIdx.x; p < size / 2; p += kClassThreads) {
-        const int lo = (p & ~(j - 1)) * 2 | (p & (j - 1)), hi = lo | j;
-        const uint32_t x = keys[lo], y = keys[hi];
-        if ((x > y) == ((lo & k) == 0)) {
-          keys[lo] = y;
-          keys[hi] = x;
-        }
-      }
-      // Up to 64 keys are one warp's, whose lanes run together.
-      if (size > 64) __syncthreads();
-      else __syncwarp();
-    }
+  // The class's tokens, again a stretch for each warp.
+  const int each = (n + 1023) / 1024 * 32, from = warp * each, to = min(n, from + each);
+  for (int i0 = from; i0 < to; i0 += 32) {
+    const int rest = i0 + lane < to ? int(keys[i0 + lane] >> kPositionBits) : -1;
+    const unsigned same = __match_any_sync(~0u, rest);
+    if (rest >= 0 && lane == __ffs(same) - 1) count[warp][rest] += uint16_t(__popc(same));
+    __syncwarp();
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < n; i += kClassThreads)
-    a.list[0][less + i] = Entry{keys[i] >> kPositionBits << kClassBits | uint32_t(mine),
-                                keys[i] & uint32_t(kFewTokens - 1)};
+  int mine_of_id = 0;  // a thread for each id
+#pragma unroll 8
+  for (int w = 0; w < 32; ++w) {
+    const int x = count[w][threadIdx.x];
+    count[w][threadIdx.x] = uint16_t(mine_of_id);
+    mine_of_id += x;
+  }
+  int all;
+  const int before = before_lane(mine_of_id, lane, &all);
+  if (lane == 0) own_of[warp] = all;
+  __syncthreads();
+  const int warps_before = before_lane(own_of[lane], lane, &all);
+  first[threadIdx.x] = uint16_t(before + __shfl_sync(~0u, warps_before, warp));
+  __syncthreads();
+  for (int i0 = from; i0 < to; i0 += 32) {
+    const bool in = i0 + lane < to;
+    const uint32_t key = in ? keys[i0 + lane] : 0;
+    const int rest = in ? int(key >> kPositionBits) : -1;
+    const unsigned same = __match_any_sync(~0u, rest);
+    const int rank = __popc(same & ((1u << lane) - 1));
+    if (in)
+      a.list[0][less + first[rest] + count[warp][rest] + rank] =
+          Entry{uint32_t(rest) << a.class_bits | uint32_t(mine), key & uint32_t(kFewTokens - 1)};
+    __syncwarp();
+    if (in && rank == 0) count[warp][rest] += uint16_t(__popc(same));
+    __syncwarp();
+  }
   if (mine == 0)
     for (int i = threadIdx.x; i < none; i += kClassThreads) a.list[0][T - none + i] = Entry{uint32_t(a.V), 0};
 }
@@ -281,34 +324,47 @@ __device__ __forceinline__ Entry token(const Args& a, int pass, int64_t i) {
   return Entry{id >= 0 && id < a.V && id != a.padding_id ? uint32_t(id) : uint32_t(a.V), uint32_t(i)};
 }
 
-__global__ void __launch_bounds__(kSortThreads) count_kernel(const Args a, int pass) {
+// The first digit's counts; the other digits' begin as zero.
+__global__ void __launch_bounds__(kSortThreads) count_kernel(const Args a) {
   __shared__ int32_t count[kMostBins];
   let_next_start();
-  wait_for_previous();
-  const int bins = 1 << a.bits, shift = pass * a.bits;
+  const int bins = 1 << a.bits;
   for (int b = threadIdx.x; b < bins; b += kSortThreads) count[b] = 0;
   __syncthreads();
   const int64_t begin = blockIdx.x * a.tile, end = min(a.T, begin + a.tile);
   for (int64_t i = begin + threadIdx.x; i < end; i += kSortThreads)
-    atomicAdd(&count[token(a, pass, i).id >> shift & (bins - 1)], 1);
+    atomicAdd(&count[token(a, 0, i).id & (bins - 1)], 1);
   __syncthreads();
-  for (int b = threadIdx.x; b < bins; b += kSortThreads) a.counts[int64_t(blockIdx.x) * bins + b] = count[b];
+  for (int b = threadIdx.x; b < bins; b += kSortThreads) {
+    for (int p = 0; p < a.passes; ++p)
+      a.counts[(int64_t(p) * a.tiles + blockIdx.x) * bins + b] = p == 0 ? count[b] : 0;
+  }
 }
 
 __global__ void __launch_bounds__(kSortThreads) place_kernel(const Args a, int pass) {
+  constexpr int kHeld = 4;  // of a lane's tokens, read once (those of a tile of 2048)
   __shared__ int32_t place[kSortWarps][kMostBins], warp_sum[kSortWarps];
   let_next_start();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int bins = 1 << a.bits, shift = pass * a.bits;
   for (int n = threadIdx.x; n < kSortWarps * kMostBins; n += kSortThreads) place[n / kMostBins][n % kMostBins] = 0;
-  wait_for_previous();
-  // A thread for each digit.
+  // The warps' stretches of the tile, in order.
+  const int64_t stretch = a.tile / kSortWarps;
+  const int64_t begin = blockIdx.x * a.tile + warp * stretch, end = min(a.T, begin + stretch);
+  if (pass > 0) wait_for_previous();  // (the ids are there before)
+  Entry held[kHeld];
+#pragma unroll
+  for (int q = 0; q < kHeld; ++q)
+    held[q] = begin + q * 32 + lane < end ? token(a, pass, begin + q * 32 + lane) : Entry{};
+  if (pass == 0) wait_for_previous();
+  // What comes before the tile: a thread for each digit.
   static_assert(kSortThreads >= kMostBins, "a thread for each digit");
   int32_t before = 0, all = 0;
   if (int(threadIdx.x) < bins) {
+    const int32_t* const counts = a.counts + int64_t(pass) * a.tiles * bins + threadIdx.x;
 #pragma unroll 32
     for (int j = 0; j < a.tiles; ++j) {
-      const int32_t n = a.counts[int64_t(j) * bins + threadIdx.x];
+      const int32_t n = counts[int64_t(j) * bins];
       all += n;
       before += j < int(blockIdx.x) ? n : 0;
     }
@@ -322,11 +378,19 @@ __global__ void __launch_bounds__(kSortThreads) place_kernel(const Args a, int p
   __syncthreads();
   int32_t base = before + upto - all;
   for (int w = 0; w < warp; ++w) base += warp_sum[w];
-  // The warps' stretches: their tokens by digit, then the first place of each.
-  const int64_t stretch = a.tile / kSortWarps;
-  const int64_t begin = blockIdx.x * a.tile + warp * stretch, end = min(a.T, begin + stretch);
-  for (int64_t i = begin + lane; i < end; i += 32)
-    atomicAdd(&place[warp][token(a, pass, i).id >> shift & (bins - 1)], 1);
+  // Each stretch's tokens by digit, then the first place of each.
+  const auto each = [&](auto f) {
+#pragma unroll
+    for (int q = 0; q < kHeld; ++q)
+      if (begin + q * 32 < end) f(begin + q * 32 + lane < end, held[q]);
+    for (int64_t i0 = begin + kHeld * 32; i0 < end; i0 += 32) {
+      const bool in = i0 + lane < end;
+      f(in, in ? token(a, pass, i0 + lane) : Entry{});
+    }
+  };
+  each([&](bool in, Entry e) {
+    if (in) atomicAdd(&place[warp][e.id >> shift & (bins - 1)], 1);
+  });
   __syncthreads();
   if (int(threadIdx.x) < bins) {
 #pragma unroll
@@ -338,17 +402,21 @@ __global__ void __launch_bounds__(kSortThreads) place_kernel(const Args a, int p
   }
   __syncthreads();
   Entry* const to = a.list[pass & 1];
-  for (int64_t i0 = begin; i0 < end; i0 += 32) {
-    const bool in = i0 + lane < end;
-    const Entry e = in ? token(a, pass, i0 + lane) : Entry{};
+  int32_t* const next = pass + 1 < a.passes ? a.counts + int64_t(pass + 1) * a.tiles * bins : nullptr;
+  each([&](bool in, Entry e) {
     const int digit = in ? int(e.id >> shift & (bins - 1)) : -1;
     const unsigned same = __match_any_sync(~0u, digit);
     const int rank = __popc(same & ((1u << lane) - 1));
-    if (in) to[place[warp][digit] + rank] = e;
+    if (in) {
+      const int64_t at = place[warp][digit] + rank;
+      to[at] = e;
+      // the next pass's counts: whole numbers, whose order does not matter
+      if (next) atomicAdd(&next[at / a.tile * bins + (e.id >> (shift + a.bits) & (bins - 1))], 1);
+    }
     __syncwarp();
     if (in && rank == 0) place[warp][digit] += __popc(same);
     __syncwarp();
-  }
+  });
 }
 
 // ------------------------------------------------------------------- sums --
@@ -563,22 +631,25 @@ template <bool F32, bool Vector>
 cudaError_t sort(const Args& a, cudaStream_t s) {
   cudaError_t e = cudaSuccess;
   if (a.few) {
-    // Zeros: as many rows a warp as leave each SM one block of them at most.
+    // Zeros: a block of them for each SM at most.
     const int64_t rows = a.accumulate ? 0 : (a.V + 31) / 32;
-    const unsigned blocks = unsigned(kClasses + (rows < kSms ? rows : kSms));
-    int size = 32;
-    while (size < a.T) size *= 2;
-    if (size * sizeof(uint32_t) > (32 << 10)) {  // what a launch has without asking holds its static part too
+    const unsigned blocks = unsigned((1 << a.class_bits) + (rows < kSms ? rows : kSms));
+    const auto shared = [](int64_t tokens) { return sizeof(ClassShared) + size_t(tokens) * sizeof(uint32_t); };
+    // Once per device (a race only does it twice): the kernel's shared memory.
+    static std::atomic<bool> ready[64];
+    int device = 0;
+    e = cudaGetDevice(&device);
+    if (e == cudaSuccess && (device >= 64 || !ready[device].load(std::memory_order_acquire))) {
       e = cudaFuncSetAttribute(class_sort_kernel<F32, Vector>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               int(size * sizeof(uint32_t)));
-      if (e != cudaSuccess) return e;
+                               int(shared(kFewTokens)));
+      if (e == cudaSuccess && device < 64) ready[device].store(true, std::memory_order_release);
     }
-    return launch(class_sort_kernel<F32, Vector>, blocks, kClassThreads, size * sizeof(uint32_t), s, false, a);
+    if (e != cudaSuccess) return e;
+    return launch(class_sort_kernel<F32, Vector>, blocks, kClassThreads, shared(a.T), s, false, a);
   }
-  for (int p = 0; e == cudaSuccess && p < a.passes; ++p) {
-    e = launch(count_kernel, unsigned(a.tiles), kSortThreads, 0, s, p > 0, a, p);
-    if (e == cudaSuccess) e = launch(place_kernel, unsigned(a.tiles), kSortThreads, 0, s, true, a, p);
-  }
+  e = launch(count_kernel, unsigned(a.tiles), kSortThreads, 0, s, false, a);
+  for (int p = 0; e == cudaSuccess && p < a.passes; ++p)
+    e = launch(place_kernel, unsigned(a.tiles), kSortThreads, 0, s, true, a, p);
   return e;
 }
 
