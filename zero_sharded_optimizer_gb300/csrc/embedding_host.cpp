@@ -64,8 +64,9 @@ void common(const zero_embedding_t* p, const void* table, int64_t table_stride, 
   a->out = out;
   a->out_stride = out_stride;
   const int es = elem_size(p->precision);
-  a->vector = reinterpret_cast<uintptr_t>(table) % 16 == 0 && table_stride * es % 16 == 0 &&
-              reinterpret_cast<uintptr_t>(out) % 16 == 0 && out_stride * es % 16 == 0;
+  const uintptr_t all = reinterpret_cast<uintptr_t>(table) | uintptr_t(table_stride * es) |
+                        reinterpret_cast<uintptr_t>(out) | uintptr_t(out_stride * es);
+  a->width = all % 16 == 0 ? 16 : all % 4 == 0 && p->D * es % 4 == 0 ? 4 : es;
 }
 
 // The gradient's arrays in the workspace.

@@ -38,7 +38,7 @@ struct Args {
   int64_t table_stride;
   void* out;               // forward: out; backward: dweight
   int64_t out_stride;
-  int32_t vector;          // 16-byte accesses fit the rows of both
+  int32_t width;           // of the accesses that fit the rows of both: 16, 4 or an element's bytes
 
   // Backward: the sort's digits and tiles, and the sums' runs of sorted tokens.
   int32_t few;             // the tokens are sorted by one kernel, which also writes the zeros

@@ -37,50 +37,50 @@ struct Type<false> {
   static constexpr int kVec = 8;
 };
 
-// A lane's share of a block of columns of a row: kVec elements side by side where
-// 16-byte accesses fit, else every 32nd one.
-template <bool F32, bool Vector>
+// A lane's share of a block of columns of a row: kVec elements, 16 bytes, in pieces
+// of the widest accesses that all rows allow -- 16 or 4 bytes, or a bf16 value --
+// which the lanes take in turn.
+template <bool F32, int Width>
 struct Columns {
   using E = typename Type<F32>::E;
   static constexpr int kVec = Type<F32>::kVec;
   static constexpr int kBlock = 32 * kVec;
+  static constexpr int kPieces = 16 / Width, kPiece = kVec / kPieces;  // elements of one
 
   int64_t first;  // of the lane
-  int count;      // that lie inside the row
+  int count;      // of its elements that lie inside the row
 
   __device__ __forceinline__ Columns(int64_t c0, int64_t D, int lane) {
-    if (Vector) {
-      first = c0 + lane * kVec;
-      count = int(max(int64_t(0), min(int64_t(kVec), D - first)));
-    } else {
-      first = c0 + lane;
-      count = int(max(int64_t(0), min(int64_t(kVec), (D - first + 31) / 32)));
-    }
+    first = c0 + lane * kPiece;
+    const int64_t left = D - first;
+    count = int(Width == 16 ? max(int64_t(0), min(int64_t(kVec), left))
+                            : max(int64_t(0), min(int64_t(kPieces), (left + 32 * kPiece - 1) / (32 * kPiece))) * kPiece);
   }
-  __device__ __forceinline__ int64_t at(int j) const { return first + (Vector ? j : 32 * j); }
+  __device__ __forceinline__ int64_t at(int j) const { return first + j / kPiece * (32 * kPiece) + j % kPiece; }
 
   // The elements as they are stored, those outside the row as zeros. `Once`: they
   // are not read again, or (store) not soon.
   template <bool Once = false>
   __device__ __forceinline__ uint4 load(const void* row) const {
     const E* p = static_cast<const E*>(row);
-    if (Vector && count == kVec) {
-      const uint4* at = reinterpret_cast<const uint4*>(p + first);
-      return Once ? __ldcs(at) : *at;
+    if (Width == 16 && count == kVec) {
+      const uint4* from = reinterpret_cast<const uint4*>(p + first);
+      return Once ? __ldcs(from) : *from;
     }
     uint32_t words[4] = {};
 #pragma unroll
     for (int j = 0; j < kVec; ++j) {
       if (j >= count) continue;
       if (F32) words[j % 4] = reinterpret_cast<const uint32_t*>(p)[at(j)];
-      else words[j / 2] |= uint32_t(reinterpret_cast<const uint16_t*>(p)[at(j)]) << (j % 2 * 16);
+      else if (Width != 4) words[j / 2] |= uint32_t(reinterpret_cast<const uint16_t*>(p)[at(j)]) << (j % 2 * 16);
+      else if (j % 2 == 0) words[j / 2] = *reinterpret_cast<const uint32_t*>(p + at(j));
     }
     return make_uint4(words[0], words[1], words[2], words[3]);
   }
   template <bool Once = false>
   __device__ __forceinline__ void store(void* row, uint4 w) const {
     E* p = static_cast<E*>(row);
-    if (Vector && count == kVec) {
+    if (Width == 16 && count == kVec) {
       uint4* to = reinterpret_cast<uint4*>(p + first);
       if (Once) __stcs(to, w);
       else *to = w;
@@ -91,7 +91,8 @@ struct Columns {
     for (int j = 0; j < kVec; ++j) {
       if (j >= count) continue;
       if (F32) reinterpret_cast<uint32_t*>(p)[at(j)] = words[j % 4];
-      else reinterpret_cast<uint16_t*>(p)[at(j)] = uint16_t(words[j / 2] >> (j % 2 * 16));
+      else if (Width != 4) reinterpret_cast<uint16_t*>(p)[at(j)] = uint16_t(words[j / 2] >> (j % 2 * 16));
+      else if (j % 2 == 0) *reinterpret_cast<uint32_t*>(p + at(j)) = words[j / 2];
     }
   }
   __device__ __forceinline__ static void unpack(uint4 w, float (&x)[kVec]) {
@@ -129,9 +130,9 @@ __device__ __forceinline__ void* row_of(void* base, int64_t stride, int64_t row)
 
 // `Stream`: the result is larger than the L2 cache, where it would displace the
 // rows that are looked up again.
-template <bool F32, bool Vector, bool Stream>
+template <bool F32, int Width, bool Stream>
 __global__ void __launch_bounds__(256) lookup_kernel(const Args a) {
-  using C = Columns<F32, Vector>;
+  using C = Columns<F32, Width>;
   constexpr int kAhead = 4;  // loads in flight
   const int lane = threadIdx.x & 31;
   const int64_t step = int64_t(gridDim.x) * 8;
@@ -182,9 +183,9 @@ __global__ void __launch_bounds__(256) lookup_kernel(const Args a) {
 
 constexpr int kClassThreads = 1024;
 
-template <bool F32, bool Vector>
+template <bool F32, int Width>
 __device__ __forceinline__ void zero_rows(const Args& a, int64_t first, int64_t step) {
-  using C = Columns<F32, Vector>;
+  using C = Columns<F32, Width>;
   for (int64_t v = first; v < a.V; v += step) {
     void* row = row_of<F32>(a.out, a.out_stride, v);
     for (int64_t c0 = 0; c0 < a.D; c0 += C::kBlock)
@@ -209,7 +210,7 @@ struct ClassShared {
   // and behind it the class's tokens in order: the rest of the id, the position
 };
 
-template <bool F32, bool Vector>
+template <bool F32, int Width>
 __global__ void __launch_bounds__(kClassThreads) class_sort_kernel(const Args a) {
   constexpr int kEach = int(kFewTokens / kClassThreads);  // most tokens of a thread
   static_assert(kClassIds <= kClassThreads, "a thread for each id of a class");
@@ -222,7 +223,7 @@ __global__ void __launch_bounds__(kClassThreads) class_sort_kernel(const Args a)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int classes = 1 << a.class_bits, mine = blockIdx.x;
   if (mine >= classes) {
-    zero_rows<F32, Vector>(a, int64_t(mine - classes) * 32 + warp, int64_t(gridDim.x - classes) * 32);
+    zero_rows<F32, Width>(a, int64_t(mine - classes) * 32 + warp, int64_t(gridDim.x - classes) * 32);
     return;
   }
   // Each warp's stretch of the tokens; an id that is not the class's becomes -1.
@@ -424,10 +425,10 @@ __global__ void __launch_bounds__(kSortThreads) place_kernel(const Args a, int p
 constexpr uint32_t kNone = 0xffffffffu;  // no key: above V
 
 // A segment's sum to its row of dweight, rounded once.
-template <bool F32, bool Vector>
-__device__ __forceinline__ void finish(const Args& a, const Columns<F32, Vector>& c, uint32_t id,
-                                       const float (&sum)[Columns<F32, Vector>::kVec]) {
-  using C = Columns<F32, Vector>;
+template <bool F32, int Width>
+__device__ __forceinline__ void finish(const Args& a, const Columns<F32, Width>& c, uint32_t id,
+                                       const float (&sum)[Columns<F32, Width>::kVec]) {
+  using C = Columns<F32, Width>;
   if (c.count == 0) return;
   void* row = row_of<F32>(a.out, a.out_stride, id);
   float x[C::kVec];
@@ -467,9 +468,9 @@ __device__ __forceinline__ void put_share(float4* to, const float (&sum)[kVec]) 
 
 // Rows of dweight that no token has: zeros. A warp for 32 ids, each lane looks
 // its own up in the list (in order of id).
-template <bool F32, bool Vector>
+template <bool F32, int Width>
 __device__ __forceinline__ void zero_absent_rows(const Args& a, int64_t v0) {
-  using C = Columns<F32, Vector>;
+  using C = Columns<F32, Width>;
   const int lane = threadIdx.x & 31;
   const int64_t v = v0 + lane;
   int64_t lo = 0, hi = a.T;
@@ -487,9 +488,9 @@ __device__ __forceinline__ void zero_absent_rows(const Args& a, int64_t v0) {
 
 // A warp for 32 ids whose rows may have to become zero -- the long pieces of work
 // first -- and one for each run and block of columns.
-template <bool F32, bool Vector>
+template <bool F32, int Width>
 __global__ void __launch_bounds__(256, 3) sum_kernel(const Args a, int64_t zero_warps) {
-  using C = Columns<F32, Vector>;
+  using C = Columns<F32, Width>;
   constexpr int kVec = C::kVec, kAhead = 8;
   let_next_start();
   wait_for_previous();
@@ -498,7 +499,7 @@ __global__ void __launch_bounds__(256, 3) sum_kernel(const Args a, int64_t zero_
   const int64_t step = int64_t(gridDim.x) * 8, sums = a.runs * a.blocks;
   for (int64_t g = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5) - zero_warps; g < sums; g += step) {
     if (g < 0) {
-      zero_absent_rows<F32, Vector>(a, (g + zero_warps) * 32);
+      zero_absent_rows<F32, Width>(a, (g + zero_warps) * 32);
       continue;
     }
     const int64_t run = g / a.blocks, first = run * a.run, block = g % a.blocks;
@@ -550,9 +551,9 @@ __global__ void __launch_bounds__(256, 3) sum_kernel(const Args a, int64_t zero_
 // itself; longer ones are added by the block's eight warps together, each a
 // stretch of the shares in order, and the stretches in order. (A block has
 // neighbouring runs, of which few begin a long segment, not the columns of one.)
-template <bool F32, bool Vector>
+template <bool F32, int Width>
 __global__ void __launch_bounds__(256) join_kernel(const Args a) {
-  using C = Columns<F32, Vector>;
+  using C = Columns<F32, Width>;
   constexpr int kVec = C::kVec, kShort = 8;
   __shared__ int64_t long_run[8], long_block[8], long_end[8];
   __shared__ float4 parts[8][32 * kVec / 4];
@@ -627,7 +628,7 @@ unsigned blocks_of(int64_t warps) {
   return unsigned(blocks < 1 ? 1 : blocks > (1 << 30) ? 1 << 30 : blocks);
 }
 
-template <bool F32, bool Vector>
+template <bool F32, int Width>
 cudaError_t sort(const Args& a, cudaStream_t s) {
   cudaError_t e = cudaSuccess;
   if (a.few) {
@@ -640,12 +641,12 @@ cudaError_t sort(const Args& a, cudaStream_t s) {
     int device = 0;
     e = cudaGetDevice(&device);
     if (e == cudaSuccess && (device >= 64 || !ready[device].load(std::memory_order_acquire))) {
-      e = cudaFuncSetAttribute(class_sort_kernel<F32, Vector>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+      e = cudaFuncSetAttribute(class_sort_kernel<F32, Width>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                int(shared(kFewTokens)));
       if (e == cudaSuccess && device < 64) ready[device].store(true, std::memory_order_release);
     }
     if (e != cudaSuccess) return e;
-    return launch(class_sort_kernel<F32, Vector>, blocks, kClassThreads, shared(a.T), s, false, a);
+    return launch(class_sort_kernel<F32, Width>, blocks, kClassThreads, shared(a.T), s, false, a);
   }
   e = launch(count_kernel, unsigned(a.tiles), kSortThreads, 0, s, false, a);
   for (int p = 0; e == cudaSuccess && p < a.passes; ++p)
@@ -653,14 +654,14 @@ cudaError_t sort(const Args& a, cudaStream_t s) {
   return e;
 }
 
-template <bool F32, bool Vector>
+template <bool F32, int Width>
 cudaError_t sums(const Args& a, cudaStream_t s) {
   if (a.T == 0) return cudaSuccess;
   const int64_t zero_warps = a.few || a.accumulate ? 0 : (a.V + 31) / 32;
-  cudaError_t e = launch(sum_kernel<F32, Vector>, blocks_of(a.runs * a.blocks + zero_warps), 256, 0, s, true, a,
+  cudaError_t e = launch(sum_kernel<F32, Width>, blocks_of(a.runs * a.blocks + zero_warps), 256, 0, s, true, a,
                          zero_warps);
   if (e == cudaSuccess && a.runs > 1)
-    e = launch(join_kernel<F32, Vector>, blocks_of((a.runs - 1) * a.blocks), 256, 0, s, true, a);
+    e = launch(join_kernel<F32, Width>, blocks_of((a.runs - 1) * a.blocks), 256, 0, s, true, a);
   return e;
 }
 
@@ -670,21 +671,21 @@ cudaError_t launch_lookup(const Args& a, cudaStream_t s) {
   const bool stream = a.T * a.D * (a.f32 ? 4 : 2) > kCacheBytes;
   const auto run = [&](auto* kernel) { return launch(kernel, blocks_of(a.T), 256, 0, s, false, a); };
   if (a.f32) {
-    if (a.vector) return stream ? run(lookup_kernel<true, true, true>) : run(lookup_kernel<true, true, false>);
-    return run(lookup_kernel<true, false, false>);
+    if (a.width == 16) return stream ? run(lookup_kernel<true, 16, true>) : run(lookup_kernel<true, 16, false>);
+    return run(lookup_kernel<true, 4, false>);
   }
-  if (a.vector) return stream ? run(lookup_kernel<false, true, true>) : run(lookup_kernel<false, true, false>);
-  return run(lookup_kernel<false, false, false>);
+  if (a.width == 16) return stream ? run(lookup_kernel<false, 16, true>) : run(lookup_kernel<false, 16, false>);
+  return a.width == 4 ? run(lookup_kernel<false, 4, false>) : run(lookup_kernel<false, 2, false>);
 }
 
 cudaError_t launch_sort(const Args& a, cudaStream_t s) {
-  if (a.f32) return a.vector ? sort<true, true>(a, s) : sort<true, false>(a, s);
-  return a.vector ? sort<false, true>(a, s) : sort<false, false>(a, s);
+  if (a.f32) return a.width == 16 ? sort<true, 16>(a, s) : sort<true, 4>(a, s);
+  return a.width == 16 ? sort<false, 16>(a, s) : a.width == 4 ? sort<false, 4>(a, s) : sort<false, 2>(a, s);
 }
 
 cudaError_t launch_sums(const Args& a, cudaStream_t s) {
-  if (a.f32) return a.vector ? sums<true, true>(a, s) : sums<true, false>(a, s);
-  return a.vector ? sums<false, true>(a, s) : sums<false, false>(a, s);
+  if (a.f32) return a.width == 16 ? sums<true, 16>(a, s) : sums<true, 4>(a, s);
+  return a.width == 16 ? sums<false, 16>(a, s) : a.width == 4 ? sums<false, 4>(a, s) : sums<false, 2>(a, s);
 }
 
 }  // namespace ze
