@@ -41,7 +41,10 @@ struct Args {
   int32_t width;           // of the accesses that fit the rows of both: 16, 4 or an element's bytes
 
   // Backward: the sort's digits and tiles, and the sums' runs of sorted tokens.
-  int32_t few;             // the tokens are sorted by one kernel, which also writes the zeros
+  int64_t zero_from;       // rows of dweight from here on become zero while the tokens are sorted, rows
+                           // below that no token has while the sums are taken (V, and none, where the
+                           // sums are added to dweight)
+  int32_t few;             // the tokens are sorted by one kernel
   int32_t class_bits;      // of an id, that say its class there
   int32_t bits, passes;    // of a digit; digits
   int64_t tile;            // tokens of a tile, a multiple of the block's threads

@@ -184,9 +184,9 @@ __global__ void __launch_bounds__(256) lookup_kernel(const Args a) {
 constexpr int kClassThreads = 1024;
 
 template <bool F32, int Width>
-__device__ __forceinline__ void zero_rows(const Args& a, int64_t first, int64_t step) {
+__device__ __forceinline__ void zero_rows(const Args& a, int64_t first, int64_t end, int64_t step) {
   using C = Columns<F32, Width>;
-  for (int64_t v = first; v < a.V; v += step) {
+  for (int64_t v = first; v < end; v += step) {
     void* row = row_of<F32>(a.out, a.out_stride, v);
     for (int64_t c0 = 0; c0 < a.D; c0 += C::kBlock)
       C(c0, a.D, threadIdx.x & 31).store(row, make_uint4(0, 0, 0, 0));
@@ -223,7 +223,8 @@ __global__ void __launch_bounds__(kClassThreads) class_sort_kernel(const Args a)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int classes = 1 << a.class_bits, mine = blockIdx.x;
   if (mine >= classes) {
-    zero_rows<F32, Width>(a, int64_t(mine - classes) * 32 + warp, int64_t(gridDim.x - classes) * 32);
+    zero_rows<F32, Width>(a, a.zero_from + int64_t(mine - classes) * 32 + warp, a.V,
+                          int64_t(gridDim.x - classes) * 32);
     return;
   }
   // Each warp's stretch of the tokens; an id that is not the class's becomes -1.
@@ -342,11 +343,18 @@ __global__ void __launch_bounds__(kSortThreads) count_kernel(const Args a) {
   }
 }
 
+template <bool F32, int Width>
 __global__ void __launch_bounds__(kSortThreads) place_kernel(const Args a, int pass) {
   constexpr int kHeld = 4;  // of a lane's tokens, read once (those of a tile of 2048)
   __shared__ int32_t place[kSortWarps][kMostBins], warp_sum[kSortWarps];
   let_next_start();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (int(blockIdx.x) >= a.tiles) {  // a pass's part of the zeros
+    const int64_t part = (a.V - a.zero_from + a.passes - 1) / a.passes, from = a.zero_from + pass * part;
+    zero_rows<F32, Width>(a, from + int64_t(blockIdx.x - a.tiles) * kSortWarps + warp, min(a.V, from + part),
+                          int64_t(gridDim.x - a.tiles) * kSortWarps);
+    return;
+  }
   const int bins = 1 << a.bits, shift = pass * a.bits;
   for (int n = threadIdx.x; n < kSortWarps * kMostBins; n += kSortThreads) place[n / kMostBins][n % kMostBins] = 0;
   // The warps' stretches of the tile, in order.
@@ -466,8 +474,8 @@ __device__ __forceinline__ void put_share(float4* to, const float (&sum)[kVec]) 
   for (int q = 0; q < kVec / 4; ++q) to[q] = make_float4(sum[4 * q], sum[4 * q + 1], sum[4 * q + 2], sum[4 * q + 3]);
 }
 
-// Rows of dweight that no token has: zeros. A warp for 32 ids, each lane looks
-// its own up in the list (in order of id).
+// Rows of dweight that no token has, below zero_from: zeros. A warp for 32 ids, each
+// lane looks its own up in the list (in order of id).
 template <bool F32, int Width>
 __device__ __forceinline__ void zero_absent_rows(const Args& a, int64_t v0) {
   using C = Columns<F32, Width>;
@@ -479,7 +487,7 @@ __device__ __forceinline__ void zero_absent_rows(const Args& a, int64_t v0) {
     if (a.sorted[mid].id < v) lo = mid + 1;
     else hi = mid;
   }
-  const bool absent = v < a.V && !(lo < a.T && a.sorted[lo].id == v);
+  const bool absent = v < a.zero_from && !(lo < a.T && a.sorted[lo].id == v);
   for (unsigned left = __ballot_sync(~0u, absent); left; left &= left - 1) {
     void* row = row_of<F32>(a.out, a.out_stride, v0 + __ffs(left) - 1);
     for (int64_t c0 = 0; c0 < a.D; c0 += C::kBlock) C(c0, a.D, lane).store(row, make_uint4(0, 0, 0, 0));
@@ -633,7 +641,7 @@ cudaError_t sort(const Args& a, cudaStream_t s) {
   cudaError_t e = cudaSuccess;
   if (a.few) {
     // Zeros: a block of them for each SM at most.
-    const int64_t rows = a.accumulate ? 0 : (a.V + 31) / 32;
+    const int64_t rows = (a.V - a.zero_from + 31) / 32;
     const unsigned blocks = unsigned((1 << a.class_bits) + (rows < kSms ? rows : kSms));
     const auto shared = [](int64_t tokens) { return sizeof(ClassShared) + size_t(tokens) * sizeof(uint32_t); };
     // Once per device (a race only does it twice): the kernel's shared memory.
@@ -648,16 +656,18 @@ cudaError_t sort(const Args& a, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     return launch(class_sort_kernel<F32, Width>, blocks, kClassThreads, shared(a.T), s, false, a);
   }
+  const int64_t part = (a.V - a.zero_from + a.passes - 1) / a.passes;
+  const int64_t zero_blocks = part / kSortWarps < 2 * kSms ? (part + kSortWarps - 1) / kSortWarps : 2 * kSms;
   e = launch(count_kernel, unsigned(a.tiles), kSortThreads, 0, s, false, a);
   for (int p = 0; e == cudaSuccess && p < a.passes; ++p)
-    e = launch(place_kernel, unsigned(a.tiles), kSortThreads, 0, s, true, a, p);
+    e = launch(place_kernel<F32, Width>, unsigned(a.tiles + zero_blocks), kSortThreads, 0, s, true, a, p);
   return e;
 }
 
 template <bool F32, int Width>
 cudaError_t sums(const Args& a, cudaStream_t s) {
   if (a.T == 0) return cudaSuccess;
-  const int64_t zero_warps = a.few || a.accumulate ? 0 : (a.V + 31) / 32;
+  const int64_t zero_warps = a.accumulate ? 0 : (a.zero_from + 31) / 32;
   cudaError_t e = launch(sum_kernel<F32, Width>, blocks_of(a.runs * a.blocks + zero_warps), 256, 0, s, true, a,
                          zero_warps);
   if (e == cudaSuccess && a.runs > 1)
