@@ -1,6 +1,8 @@
 // Kernels of the embedding (zero_embedding_*).
 //
-// The lookup copies rows by id, one warp a row.
+// The lookup copies rows by id, one warp a row. It is bound by memory: 131072 rows
+// of width 4096 in bf16, 32620 of them distinct, take 224 us (6.0 TB/s; 266 with
+// one access of a lane on its way instead of four).
 //
 // The gradient adds the rows of dout that have the same id. The tokens are
 // sorted by id, stably, so that an id's rows are a segment of the list, in the
@@ -8,7 +10,11 @@
 // and block of columns, whatever the segments' lengths: a segment within a run
 // goes to its row of dweight, and the shares of one that spans runs are kept in
 // fp32 and joined in the order of the runs. No atomics touch a value, so equal
-// inputs give equal bits.
+// inputs give equal bits. Large ones are bound by memory: 131072 tokens of width
+// 4096 and as many ids, bf16, 396 us, of which the sums and zeros take 345 (2.15 GB
+// at 6.2 TB/s) and the sort 35; small ones by the latency of three kernels and by
+// the zeros: 8192 tokens of a table of 50257 x 768 take 29 us, 21 added to a
+// dweight that is there.
 
 #include <cuda_bf16.h>
 
@@ -173,13 +179,16 @@ __global__ void __launch_bounds__(256) lookup_kernel(const Args a) {
 // gathers its own in order and places them by the rest of their ids, counted warp
 // by warp in shared memory: no exchange between blocks, and the same work however
 // often an id comes. The list is in order of class, then of id. Blocks behind those
-// write dweight's zeros meanwhile.
+// write dweight's zeros meanwhile: 17 us for 8192 tokens beside 77 MB of zeros,
+// which alone take 12. (Keys exchanged in shared memory instead of counted: 30 us for
+// the whole gradient instead of 29, 76 instead of 44 where all tokens are one id.)
 //
 // More tokens: by digits of the id from the lowest, each pass stable: a tile's
 // tokens are counted by digit, and the block of that tile adds up what comes before
 // -- smaller digits of all tiles, its digit in earlier tiles -- and places its
 // tokens, each warp a stretch of them in order, counting the next digit by the
-// tiles that they go to.
+// tiles that they go to. A pass takes 13 us for 131072 tokens, all of it latency:
+// the columns of the counts, then the warps' two walks.
 
 constexpr int kClassThreads = 1024;
 
@@ -495,7 +504,8 @@ __device__ __forceinline__ void zero_absent_rows(const Args& a, int64_t v0) {
 }
 
 // A warp for 32 ids whose rows may have to become zero -- the long pieces of work
-// first -- and one for each run and block of columns.
+// first -- and one for each run and block of columns, with eight rows on their way at
+// a time, as they are stored: 80 registers, three blocks an SM.
 template <bool F32, int Width>
 __global__ void __launch_bounds__(256, 3) sum_kernel(const Args a, int64_t zero_warps) {
   using C = Columns<F32, Width>;
@@ -558,7 +568,8 @@ __global__ void __launch_bounds__(256, 3) sum_kernel(const Args a, int64_t zero_
 // warp looks for one in a run and block of columns and adds up to kShort shares
 // itself; longer ones are added by the block's eight warps together, each a
 // stretch of the shares in order, and the stretches in order. (A block has
-// neighbouring runs, of which few begin a long segment, not the columns of one.)
+// neighbouring runs, of which few begin a long segment, not the columns of one:
+// 131072 tokens of width 4096 15 us instead of 97.)
 template <bool F32, int Width>
 __global__ void __launch_bounds__(256) join_kernel(const Args a) {
   using C = Columns<F32, Width>;

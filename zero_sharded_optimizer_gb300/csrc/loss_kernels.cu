@@ -284,7 +284,9 @@ __device__ __forceinline__ bool offsets_ascend(const Args& a) {
 }
 
 // Which rows number_rows_kernel numbers: those with a target, prepared before or
-// (few rows, labels alone: a launch saved) by itself, or those with a slope.
+// (few rows, labels alone: a launch saved) by itself, or, before a backward pass by
+// slopes, those whose slope is not zero. (8192 rows: 7 us, beside which 30 % fewer
+// rows in a policy step's backward products save 350.)
 enum Numbering { kTargets, kPrepare, kSlopes };
 
 // One block: numbers the rows in order, up to 16 times 1024 rows at a time.
@@ -653,7 +655,8 @@ constexpr int kSlopeRows = 16;  // most rows of a block of losses_kernel that go
 // on sums of many, so what the tensor cores' truncating sums take from a large
 // logit of the label counts (up to 8e-6 at a logit of 9 and width 768, always of
 // one sign). The label's logit is therefore taken again in rounding fp32, and
-// its share of the log-sum-exp corrected: log(S + e^z' - e^z).
+// its share of the log-sum-exp corrected: log(S + e^z' - e^z). (8192 rows of width
+// 768: 21 us, bound by latency: the statistics' columns, then two rows a warp.)
 template <bool Slopes, bool F32>
 __global__ void __launch_bounds__(256, 4) losses_kernel(const Args a, int block_rows, bool vector) {
   __shared__ float2 sh[256];
@@ -824,7 +827,8 @@ __device__ __forceinline__ void pair_loss(const Args& a, int64_t i, const double
 }
 
 // A block for each pair (in turn). `Forward`: sums, losses and slopes, else the
-// slopes are given; then the rows' scales where a backward pass follows.
+// slopes are given; then the rows' scales where a backward pass follows. (16 pairs
+// of 8192 rows: 13 us of dependent reads and double arithmetic.)
 template <bool Forward>
 __global__ void __launch_bounds__(256) pairs_kernel(const Args a) {
   __shared__ double sh[4][8];
