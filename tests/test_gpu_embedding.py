@@ -132,6 +132,42 @@ def test_digits_of_the_sort(embedding, cuda, V, T):
     check_gradient(got, ids, dout, V, 1.0, what=str(V))
 
 
+@pytest.mark.parametrize("V", [1024, 131072, 131073, 262144, 262145])
+@pytest.mark.parametrize("T", [1023, 1024, 1025, 16384, 32767, 32768, 32769, 33000])
+def test_around_what_one_kernel_sorts(embedding, cuda, T, V):
+    """Numbers of tokens and sizes of the vocabulary on both sides of the sorts' limits."""
+    g = torch.Generator().manual_seed(T + V)
+    dout = torch.randn(T, 12, generator=g).to(cuda)
+    for order in ("frequent", "any", "one"):
+        ids = tokens(T, V, g, order)
+        ids[::17] = -1
+        ids[3::29] = V - 1
+        ids = ids.to(cuda)
+        got = torch.full((V, 12), math.nan, device=cuda)
+        embedding.embedding_backward(ids, dout, dweight=got, padding_id=0)
+        check_gradient(got, ids, dout, V, 1.0, padding_id=0, what=order)
+
+
+@pytest.mark.parametrize("V,D,dt", [(300000, 128, torch.float32), (5, 20000, torch.bfloat16), (700, 40001, torch.float32)])
+def test_zeros_of_many_tokens(embedding, cuda, V, D, dt):
+    """More rows than the sort has the time to clear, and rows of which it clears few or one."""
+    g = torch.Generator().manual_seed(V)
+    T = 40000 if V > 1000 else 33000
+    ids = tokens(T, V, g)
+    ids[::2] = V // 3
+    ids[1::4] = V - 1 - (torch.arange(len(ids[1::4])) % 3) * (V // 5)
+    ids = ids.to(cuda)
+    if V < 1000:        # few tokens with a gradient, of long rows
+        ids[200:] = -1
+    dout = torch.randn(200 if V < 1000 else T, D, generator=g).to(dt).to(cuda)
+    if V < 1000:
+        dout = torch.cat([dout, torch.zeros(1, D, dtype=dt, device=cuda).expand(T - 200, D)])
+    got = torch.full((V, D), math.nan, dtype=dt, device=cuda)
+    embedding.embedding_backward(ids, dout, dweight=got)
+    kept = torch.nonzero(ids >= 0)[:, 0]
+    check_gradient(got, ids[kept], dout[kept], V, 1.0)
+
+
 @pytest.mark.parametrize("pad,offset", [(0, 1), (1, 0), (3, 5), (8, 0), (8, 8), (5, 3), (4, 4), (13, 0)])
 @pytest.mark.parametrize("kind", TYPES)
 def test_strides_and_alignment(embedding, cuda, kind, pad, offset):
