@@ -635,8 +635,10 @@ int zero_distill_step(const zero_head_loss_t *p, zero_stream_t stream);
  * The label's logit is summed a second time, in fp32 with rounding, and its part
  * of lse corrected, because these losses hang on small differences of
  * log-probabilities; the sums over a sequence and the losses are formed in
- * double. Everything else -- arithmetic, equal bits, what a wait that runs out
- * does -- is as stated above.
+ * double. A few rows (which depends on sizes and type alone) are worked on in fp32
+ * multiply-adds, with the T x V logits in the workspace and no wait that could run
+ * out. Everything else -- arithmetic, equal bits, what a wait that runs out does --
+ * is as stated above.
  *
  * Of the zero_head_loss_t they take: labels (no teacher fields), loss (T values,
  * or `pairs`), lse, reduced, dloss (NONE: as many as loss) and the gradients. */
@@ -789,7 +791,8 @@ int zero_debug_fail_host_allocs(int32_t count);
  * loss call the matrix kernels of the forward pass (passes 1), the backward pass
  * (2) or both (3) wait for a word that nothing sets, and give up after limit_ns
  * (at most ten seconds, which is also the limit of every other call): the
- * failure stated above. passes 0 clears it. EINVAL: out of range. */
+ * failure stated above. (A policy or preference call of a few rows has no such
+ * wait.) passes 0 clears it. EINVAL: out of range. */
 int zero_debug_withhold_head_loss(int32_t passes, int64_t limit_ns);
 
 #ifdef __cplusplus

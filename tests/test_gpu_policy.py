@@ -58,6 +58,56 @@ def test_policy_step(losses, cuda, kind, T, V, D):
         assert torch.equal(got.dhidden[r["slopes"] == 0], torch.zeros_like(h)[r["slopes"] == 0])
 
 
+@pytest.mark.parametrize("T", [4, 5, 8, 9, 16, 17, 31, 32, 33, 64, 65])
+@pytest.mark.parametrize("kind", TYPES)
+def test_around_what_counts_as_few_rows(losses, cuda, kind, T):
+    """Rows on both sides of the limits and of the groups of eight, small and larger vocabularies and
+    widths, columns off the blocks of four, 32 and 64; rows without a label or a slope between."""
+    dt = TYPES[kind]
+    for n, (V, D) in enumerate([(97, 33), (1027, 264), (5000, 520), (20001, 96), (130, 5200), (67, 10300)]):
+        h, w, y, g = inputs(T, V, D, dt, 40 + T + V, cuda, masked=0.2)
+        old, adv, ref = sampled(h, w, y, g, still=0.3)
+        kl, reduction = (0.05, "none") if n % 2 else (0.0, "mean")
+        dloss = torch.rand(T, generator=g).to(cuda) if n % 2 else None
+        r = policy(h, w, y, old, adv, ref if kl else None, (0.2, 0.2), kl, reduction, dloss)
+        for pad in (0, 3):
+            before = torch.randn(V, D, generator=g).to(dt).to(cuda)
+            dw, buf = empty_matrix(V, D, dt, cuda, pad)
+            dh, dh_buf = empty_matrix(T, D, dt, cuda, pad)
+            got = losses.policy_step(matrix(h, cuda, pad), matrix(w, cuda, pad), y, old, adv, clip=0.2, kl_weight=kl,
+                                     ref_logps=ref if kl else None, reduction=reduction, dloss=dloss, dhidden=dh,
+                                     dweight=dw)
+            check(got, r, dt, f"{kind} {V} {D} {pad}", 2)
+            gaps_untouched(buf, V, D, pad)
+            gaps_untouched(dh_buf, T, D, pad)
+            alone = dw.double()
+            dw.copy_(before)
+            losses.policy_step(matrix(h, cuda, pad), matrix(w, cuda, pad), y, old, adv, clip=0.2, kl_weight=kl,
+                               ref_logps=ref if kl else None, reduction=reduction, dloss=dloss, dweight=dw,
+                               accumulate=True)
+            # as far as the gradient alone, which is rounded too, and one rounding
+            unit = 2.0 ** -24 if kind == "fp32" else 2.0 ** -8
+            want = before.double() + r["dweight"]
+            off = (dw.double() - want).abs()
+            assert bool((off <= (alone - r["dweight"]).abs() + 1.01 * unit * (alone.abs() + want.abs()) + 1e-7).all())
+
+
+@pytest.mark.parametrize("T", [3, 20, 300])
+@pytest.mark.parametrize("kind", TYPES)
+def test_rows_without_a_slope_bring_nothing_in(losses, cuda, kind, T):
+    """A hidden state that is not a number, in a row of advantage zero."""
+    dt = TYPES[kind]
+    h, w, y, g = inputs(T, 300, 64, dt, 50 + T, cuda)
+    old, adv, _ = sampled(h, w, y, g)
+    adv[1] = 0.0
+    r = policy(h, w, y, old, adv, reduction="sum")
+    bad = h.clone()
+    bad[1] = math.nan
+    got = losses.policy_step(bad, w, y, old, adv, reduction="sum")
+    assert math.isnan(float(got.logps[1])) and float(got.loss[1]) == 0.0 and not got.dhidden[1].any()
+    check(got._replace(logps=None), r, dt, "", parts_of(dt, T))
+
+
 def test_policy_clip_of_one_number(losses, cuda):
     h, w, y, g = inputs(50, 300, 64, torch.bfloat16, 1, cuda)
     old, adv, _ = sampled(h, w, y, g)
@@ -289,7 +339,7 @@ def both(losses, T, V, D, dt, seed, device, masked=0.2):
              dict(nll_weight=0.1), (offsets,), lambda **m: preference(h, w, y, bounds, nll=0.1, **m))]
 
 
-@pytest.mark.parametrize("T,V,D", [(200, 1000, 72), (1200, 3000, 64), (8200, 21000, 64)])
+@pytest.mark.parametrize("T,V,D", [(3, 1000, 72), (20, 1001, 200), (200, 1000, 72), (1200, 3000, 64), (8200, 21000, 64)])
 @pytest.mark.parametrize("kind", TYPES)
 def test_backward_alone_equals_step(losses, cuda, kind, T, V, D):
     dt = TYPES[kind]
@@ -383,8 +433,8 @@ def test_equal_inputs_give_equal_bits(losses, cuda):
 @pytest.mark.parametrize("kind", TYPES)
 def test_in_a_graph(losses, cuda, kind):
     dt = TYPES[kind]
-    for n in (0, 1):
-        step, _, _, args, more, _, _ = both(losses, 700, 2000, 72, dt, 26, cuda)[n]
+    for T, n in ((700, 0), (700, 1), (20, 0), (20, 1)):
+        step, _, _, args, more, _, _ = both(losses, T, 2000, 72, dt, 26, cuda)[n]
         args = tuple(t.clone() for t in args)
         step(*args, **more)
         torch.cuda.synchronize()
@@ -395,13 +445,13 @@ def test_in_a_graph(losses, cuda, kind):
                 outs.append(step(*args, **more))
             graphs.append(graph)
         for seed in (27, 28):
-            _, _, _, new, _, _, exact = both(losses, 700, 2000, 72, dt, seed, cuda)[n]
+            _, _, _, new, _, _, exact = both(losses, T, 2000, 72, dt, seed, cuda)[n]
             for a, b in zip(args, new):
                 a.copy_(b)
             for graph, out in zip(graphs, outs):
                 graph.replay()
                 torch.cuda.synchronize()
-                check(out, exact(), dt, f"{seed}")
+                check(out, exact(), dt, f"{T} {seed}", parts_of(dt, T))
 
 
 def test_another_stream(losses, cuda, monkeypatch):

@@ -19,7 +19,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libzero_gb300.so")
 
-SOURCES = ["zero_kernels.cu", "zero_host.cpp", "loss_kernels.cu", "loss_mma.cu",
+SOURCES = ["zero_kernels.cu", "zero_host.cpp", "loss_kernels.cu", "loss_mma.cu", "loss_few.cu",
            "loss_host.cpp", "embedding_kernels.cu", "embedding_host.cpp"]
 HEADERS = [os.path.join(CSRC, "zero_internal.h"), os.path.join(CSRC, "loss_internal.h"),
            os.path.join(CSRC, "loss_device.cuh"), os.path.join(CSRC, "embedding_internal.h"),

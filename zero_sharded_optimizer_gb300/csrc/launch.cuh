@@ -14,10 +14,10 @@ __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontr
 
 // `dependent`: a programmatic launch behind the kernel before it.
 template <typename... P, typename... A>
-inline cudaError_t launch(void (*kernel)(P...), unsigned blocks, int threads, size_t shared, cudaStream_t s, bool dependent,
+inline cudaError_t launch(void (*kernel)(P...), dim3 blocks, int threads, size_t shared, cudaStream_t s, bool dependent,
                    const A&... args) {
   cudaLaunchConfig_t c = {};
-  c.gridDim = dim3(blocks);
+  c.gridDim = blocks;
   c.blockDim = dim3(unsigned(threads));
   c.dynamicSmemBytes = shared;
   c.stream = s;

@@ -220,6 +220,28 @@ bool weight_in_place(const zero_head_loss_t* p) {
          p->weight_stride % 8 == 0 && p->weight_stride < (int64_t(1) << 39);
 }
 
+// Whether a call's products are better made without the tensor cores (loss_few.cu):
+// for a few rows, whose work is the weight's traffic, and some more where they are
+// small with the weight and latency is all. GPU time of a policy's step in a replayed
+// graph, here and on the tensor cores, us (V x D):
+//   rows            1          4          8          16         32         64
+//   bf16 1009 x 96       29, 48     29, 49     32, 49     37, 49     45, 50     58, 50
+//   bf16 8000 x 512      40, 63     43, 64     48, 64     55, 64     70, 64     96, 65
+//   bf16 50257 x 768     90, 138    100, 134   123, 136   192, 137
+//   bf16 131072 x 4096   671, 962   753, 963   1046, 964
+//   fp32 1009 x 96       27, 55     27, 56     29, 56     31, 58     37, 57     46, 58
+//   fp32 8000 x 512      42, 93     44, 93     49, 93     57, 95     76, 95     113, 96
+//   fp32 50257 x 768     137, 365   137, 365   158, 364   244, 363   409, 363
+//   fp32 131072 x 4096   1174, 3772 1272, 3770 1604, 3765 2993, 3779 5912, 3785
+// (A call that is issued by the host takes 47 us here and 63 on the tensor cores.)
+bool few_rows(const zero_head_loss_t* p) {
+  const bool f32 = p->precision == ZERO_FP32;
+  const int64_t bytes = round_up(p->D, f32 ? 128 : 256) * (f32 ? 4 : 2);
+  if (p->T < 1 || bytes > zl::kFewHiddenBytes / zl::kFewGroup) return false;  // (a group's hidden states)
+  const double work = double(p->T) * double(p->V) * double(p->D);
+  return p->T <= (f32 ? 16 : 4) || (p->T <= (f32 ? 64 : 32) && work <= (f32 ? 2e8 : 1e8));
+}
+
 int plan(const Problem& problem, int pass, Args* a, __nv_bfloat16** packed_weight, int64_t* bytes) {
   const zero_head_loss_t* p = problem.p;
   const bool distill = problem.distill();
@@ -287,6 +309,14 @@ int plan(const Problem& problem, int pass, Args* a, __nv_bfloat16** packed_weigh
   a->dweight = p->dweight;
   a->dweight_stride = p->dweight_stride;
   a->tiles = (p->V + zl::kTileN - 1) / zl::kTileN;
+  a->partials = 2 * a->tiles;
+  a->few = problem.slopes() && few_rows(p);
+  const int64_t groups = (p->T + zl::kFewGroup - 1) / zl::kFewGroup;
+  if (a->few) {
+    // Blocks that go through the vocabulary, each with its own share of the statistics.
+    a->Tp = std::max<int64_t>(groups, 1) * zl::kFewGroup;
+    a->partials = std::max<int64_t>(std::min<int64_t>(2 * zl::kSms / std::max<int64_t>(groups, 1), (p->V + 31) / 32), 1);
+  }
 
   Layout w{static_cast<uint8_t*>(p->workspace)};
   a->head = w.take<zl::Head>(1);
@@ -301,9 +331,12 @@ int plan(const Problem& problem, int pass, Args* a, __nv_bfloat16** packed_weigh
   // G in one bf16 part: dhidden hangs on the label's entry, whose rounding it
   // gets back at the end (8192 rows of GPT-2-small's head: 1.41 times as far
   // from the exact one as its own rounding makes it without, 1.00 with).
-  if (a->scales && a->parts == 1) a->left = w.take<float>(a->Tp);
-  a->hp = w.take<__nv_bfloat16>(a->Tp * a->planes, a->Dp);
-  if (weight_in_place(p)) {
+  if (a->scales && a->parts == 1 && !a->few) a->left = w.take<float>(a->Tp);
+  if (!a->few) a->hp = w.take<__nv_bfloat16>(a->Tp * a->planes, a->Dp);
+  if (a->few) {
+    *packed_weight = nullptr;
+    a->z = w.take<float>(a->Tp, a->V);
+  } else if (weight_in_place(p)) {
     *packed_weight = nullptr;
     a->wp = static_cast<const __nv_bfloat16*>(p->weight);
     a->wp_ld = p->weight_stride;
@@ -315,14 +348,18 @@ int plan(const Problem& problem, int pass, Args* a, __nv_bfloat16** packed_weigh
     a->wp_plane = a->V * a->Dp;
   }
   int64_t pieces = 0;
-  if (pass & kBackward) {
+  if (a->few) {
+    // dhidden's parts: as many as make blocks for the card.
+    const int64_t block = a->planes == 3 ? 128 : 256, each = std::max<int64_t>(groups, 1) * ((p->D + block - 1) / block);
+    a->splits = int32_t(std::max<int64_t>(std::min<int64_t>(2 * zl::kSms / each, (p->V + 31) / 32), 1));
+  } else if (pass & kBackward) {
     const int64_t widest = std::max<int64_t>(
         kPieceBytes / (2 * a->parts * a->Tp) / zl::kTileN * zl::kTileN, zl::kTileN);
     pieces = (a->V + widest - 1) / widest;
     a->piece = round_up((a->V + pieces - 1) / pieces, zl::kTileN);
     pieces = (a->V + a->piece - 1) / a->piece;
   }
-  if (pass & kBackward) {
+  if (pass & kBackward && !a->few) {
     // dhidden's sums over a piece are split where one of its tiles would be
     // more than half of what each CTA pair of the card has to do for the piece, while
     // two blocks of K are left to a part (37 rows x 1009 x 96 in fp32: a step of
@@ -338,7 +375,7 @@ int plan(const Problem& problem, int pass, Args* a, __nv_bfloat16** packed_weigh
     while (a->splits < 64 && terms * blocks_v / a->splits > std::max<int64_t>(work / zl::kSms, 2 * terms)) a->splits *= 2;
   }
   // The words that begin as zero.
-  const int64_t tiles = pass & kBackward ? a->splits * (a->Tp / zl::kTileM) * ((a->D + 255) / 256) : 0;
+  const int64_t tiles = pass & kBackward && !a->few ? a->splits * (a->Tp / zl::kTileM) * ((a->D + 255) / 256) : 0;
   a->zeros = 3 + 2 * pieces + tiles;
   a->counters = w.take<int32_t>(a->zeros);
   a->never = reinterpret_cast<uint32_t*>(a->counters + 2);
@@ -350,18 +387,18 @@ int plan(const Problem& problem, int pass, Args* a, __nv_bfloat16** packed_weigh
   a->sums = w.take<double>(zl::kLossBlocks);
   a->zent = w.take<float>(a->T, a->L);
   if (problem.preference) a->row_logps = w.take<double>(a->T);
-  if (a->has_ce) a->stats = w.take<float2>(2 * a->tiles, a->Tp);
-  if (a->has_kd) a->stats_tau = w.take<float2>(2 * a->tiles, a->Tp);
+  if (a->has_ce) a->stats = w.take<float2>(a->partials, a->Tp);
+  if (a->has_kd) a->stats_tau = w.take<float2>(a->partials, a->Tp);
   int64_t most = w.at;
   if (pass & kBackward) {
     w.at = common;
-    for (int b = 0; b < zl::kBuffers; ++b)
+    for (int b = 0; b < zl::kBuffers && !a->few; ++b)
       a->g[b] = b < pieces ? w.take<__nv_bfloat16>(a->Tp * a->parts, a->piece) : a->g[0];
     if (p->dhidden) a->dh = w.take<float>(a->splits * a->Tp, a->Dp);
     most = std::max(most, w.at);
   }
   // The matrix kernel numbers its tiles in 32 bits.
-  const double row_tiles = double(a->Tp / zl::kTileM), wide_tiles = double((a->D + 255) / 256);
+  const double row_tiles = double((a->Tp + zl::kTileM - 1) / zl::kTileM), wide_tiles = double((a->D + 255) / 256);
   if (row_tiles * double(a->tiles) > 1e9 ||
       (pass & kBackward && (row_tiles + wide_tiles) * double((a->V + 255) / 256) +
                                    double(pieces) * row_tiles * wide_tiles * double(a->splits) > 1e9))
@@ -454,10 +491,12 @@ int run(const Problem& problem, int pass, cudaStream_t s) {
   if (!p->workspace || p->workspace_bytes < bytes)
     return set_error(ZERO_EINVAL, "the workspace has %lld bytes, %lld are needed",
                      (long long)(p->workspace ? p->workspace_bytes : 0), (long long)bytes);
-  if (!encoder()) return set_error(ZERO_ECUDA, "the CUDA driver has no cuTensorMapEncodeTiled");
   Program program{};
-  if (!make_program(a, pass & kBackward, &program))
-    return set_error(ZERO_EINVAL, "the problem's arrays are too large for tensor maps");
+  if (!a.few) {
+    if (!encoder()) return set_error(ZERO_ECUDA, "the CUDA driver has no cuTensorMapEncodeTiled");
+    if (!make_program(a, pass & kBackward, &program))
+      return set_error(ZERO_EINVAL, "the problem's arrays are too large for tensor maps");
+  }
   int device = 0, sms = 0;
   cudaError_t q = cudaGetDevice(&device);
   if (q == cudaSuccess) q = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device);
@@ -475,17 +514,20 @@ int run(const Problem& problem, int pass, cudaStream_t s) {
   };
   if (problem.slopes() && !(pass & kForward)) {
     next("scales", [&] { return zl::launch_scales(a, s); });
-    next("rows with a slope", [&] { return zl::launch_sloped_rows(a, s); });
+    if (!a.few) next("rows with a slope", [&] { return zl::launch_sloped_rows(a, s); });
   }
-  next("packing", [&] { return zl::launch_pack(a, packed, false, s); });
+  if (a.few)
+    next("logits", [&] { return zl::launch_few_logits(a, device, s); });
+  else
+    next("packing", [&] { return zl::launch_pack(a, packed, false, s); });
   if (pass & kForward) {
     program.forward = 1;
     program.counter = a.counters;
     program.withheld = withheld.passes & kForward ? a.never : nullptr;
-    next("logits", [&] { return zl::launch_products(a, program, device, sms, s); });
+    if (!a.few) next("logits", [&] { return zl::launch_products(a, program, device, sms, s); });
     next("losses", [&] { return zl::launch_losses(a, s); });
     if (problem.preference) next("pairs", [&] { return zl::launch_pairs(a, s); });
-    if (problem.slopes() && (pass & kBackward)) {
+    if (problem.slopes() && !a.few && (pass & kBackward)) {
       next("rows with a slope", [&] { return zl::launch_sloped_rows(a, s); });
       next("packing", [&] { return zl::launch_pack(a, nullptr, true, s); });
     }
@@ -494,7 +536,9 @@ int run(const Problem& problem, int pass, cudaStream_t s) {
     program.forward = 0;
     program.counter = a.counters + 1;
     program.withheld = withheld.passes & kBackward ? a.never : nullptr;
-    next("the gradients", [&] { return zl::launch_products(a, program, device, sms, s); });
+    next("the gradients", [&] {
+      return a.few ? zl::launch_few_gradients(a, s) : zl::launch_products(a, program, device, sms, s);
+    });
     if (p->dhidden && p->T) next("dhidden", [&] { return zl::launch_dhidden_out(a, s); });
     else next("the mark", [&] { return zl::launch_mark(a, s); });
   }

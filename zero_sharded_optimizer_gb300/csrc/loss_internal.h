@@ -25,6 +25,8 @@ constexpr int kSms = 152;        // GB300's multiprocessors. (The layout is plan
                                  // what a device reports: the workspace query runs without one.)
 constexpr int kBuffers = 3;      // of G
 constexpr int kLossBlocks = 608; // most blocks of the losses' kernel
+constexpr int kFewGroup = 8;     // few rows are worked on in groups of these
+constexpr int kFewHiddenBytes = 160 << 10;  // most shared memory for a group's hidden states
 
 // Which loss a call takes.
 enum Kind : int32_t { kXent, kDistill, kPolicy, kPreference };
@@ -85,6 +87,7 @@ struct Args {
 
   // The policy and the preference loss.
   Kind kind;
+  int32_t few;            // few rows: the products are loss_few.cu's
   const float* old_logps;
   const float* advantages;
   const float* ref_logps; // [T], [2 pairs] or NULL
@@ -116,8 +119,10 @@ struct Args {
   const __nv_bfloat16* wp;  // [planes][V][Dp], or the caller's weight (then wp_ld)
   int64_t wp_ld, wp_plane;
   int64_t tiles;          // vocabulary tiles
-  float2* stats;          // [2 tiles][Tp] half a tile's (m, sum of 2^(z log2(e) - m))
-  float2* stats_tau;      // [2 tiles][Tp] of z / tau
+  int64_t partials;       // of a row's statistics: 2 tiles, or the few rows' blocks
+  float2* stats;          // [partials][Tp] some columns' (half a tile's) (m, sum of 2^(z log2(e) - m))
+  float2* stats_tau;      // [partials][Tp] of z / tau
+  float* z;               // [groups][V][kFewGroup] the logits, for few rows
   int32_t* counters;      // [2] units handed out, forward and backward
   uint32_t* never;        // stays zero
   uint32_t* formed;       // [pieces] finished units of a piece's gradient
@@ -153,6 +158,9 @@ cudaError_t launch_rows(const Args& a, cudaStream_t s);
 // `again`: the rows of the backward pass of a step, where they are others.
 cudaError_t launch_pack(const Args& a, __nv_bfloat16* weight, bool again, cudaStream_t s);
 cudaError_t launch_losses(const Args& a, cudaStream_t s);
+// The logits, their statistics and both gradients, for few rows.
+cudaError_t launch_few_logits(const Args& a, int device, cudaStream_t s);
+cudaError_t launch_few_gradients(const Args& a, cudaStream_t s);
 // The preference loss of the pairs from their rows' log-probabilities.
 cudaError_t launch_pairs(const Args& a, cudaStream_t s);
 // A backward call's scales from the slopes that it is given.

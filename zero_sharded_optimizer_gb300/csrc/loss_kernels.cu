@@ -703,9 +703,9 @@ __global__ void __launch_bounds__(256, 4) losses_kernel(const Args a, int block_
       const int64_t at = t * a.L + e;
       if (a.ids[at] != kNoId) entries += double(a.weights[at]) * double(a.zent[at]);
     }
-    const double lse = a.has_ce ? row_lse(a.stats, 2 * a.tiles, a.Tp, i, lane, lanes, sh, r, block_rows) : 0.0;
+    const double lse = a.has_ce ? row_lse(a.stats, a.partials, a.Tp, i, lane, lanes, sh, r, block_rows) : 0.0;
     const double lse_tau =
-        a.has_kd ? row_lse(a.stats_tau, 2 * a.tiles, a.Tp, i, lane, lanes, sh, r, block_rows) : 0.0;
+        a.has_kd ? row_lse(a.stats_tau, a.partials, a.Tp, i, lane, lanes, sh, r, block_rows) : 0.0;
     if (a.L > 1) {
       part[threadIdx.x] = entries;
       __syncthreads();
@@ -797,14 +797,11 @@ __device__ __forceinline__ void block_sums(double (&x)[N], double (*sh)[8]) {
 
 // The loss of a pair and its slopes by each of its rows' log-probabilities, from
 // the sequences' sums over n[k] labelled rows.
-__device__ __forceinline__ void pair_loss(const Args& a, int64_t i, const double (&sum)[2], const int (&n)[2],
-                                          double* loss, double (&slope)[2]) {
+__device__ __forceinline__ void pair_loss(const Args& a, const double (&sum)[2], const int (&n)[2],
+                                          const float (&ref)[2], double* loss, double (&slope)[2]) {
   double x[2];
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    x[k] = a.average ? sum[k] / max(1, n[k]) : sum[k];
-    if (a.ref_logps) x[k] -= double(a.ref_logps[i + k * a.pairs]);
-  }
+  for (int k = 0; k < 2; ++k) x[k] = (a.average ? sum[k] / max(1, n[k]) : sum[k]) - double(ref[k]);
   const double u = a.beta * (x[0] - x[1]) - a.margin;
   double du;
   if (a.squared) {
@@ -860,9 +857,11 @@ __global__ void __launch_bounds__(256) pairs_kernel(const Args a) {
   for (int64_t i = blockIdx.x; i < a.pairs; i += gridDim.x) {
     int64_t begin[2], end[2];
     double x[4] = {};  // the sequences' labelled rows and their log-probabilities
+    float ref[2] = {};
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const int64_t s = i + k * a.pairs;
+      if (Forward && a.ref_logps && threadIdx.x == 0) ref[k] = a.ref_logps[s];  // ahead of its use
       begin[k] = a.offsets ? a.offsets[s] : s * length;
       end[k] = a.offsets ? a.offsets[s + 1] : (s + 1) * length;
     }
@@ -884,7 +883,7 @@ __global__ void __launch_bounds__(256) pairs_kernel(const Args a) {
       if (some) atomicAdd(&a.head->pairs, 1);
       double loss = 0.0, slope[2] = {};
       if (Forward) {
-        if (some) pair_loss(a, i, sum, n, &loss, slope);
+        if (some) pair_loss(a, sum, n, ref, &loss, slope);
         a.loss[i] = float(loss);
         mine += double(float(loss));
       }
@@ -911,8 +910,11 @@ __global__ void __launch_bounds__(256) pairs_kernel(const Args a) {
     }
     __syncthreads();
   }
-  if (!Forward || a.reduction == ZERO_REDUCE_NONE) return;
-  // The blocks' sums in order, by the last block to finish.
+  // The blocks' sums in order, by the last block to finish; and, where no rows are
+  // numbered after this, the mean's part in the factor of both gradients.
+  const bool reduce = Forward && a.reduction != ZERO_REDUCE_NONE;
+  const bool factor = a.few && a.scales && a.reduction == ZERO_REDUCE_MEAN;
+  if (!reduce && !factor) return;
   if (threadIdx.x == 0) {
     a.sums[blockIdx.x] = mine;
     __threadfence();
@@ -921,11 +923,13 @@ __global__ void __launch_bounds__(256) pairs_kernel(const Args a) {
   __syncthreads();
   if (!last) return;
   __threadfence();
+  const double pairs = double(max(1, __ldcg(&a.head->pairs)));
+  if (factor && threadIdx.x == 0) a.head->factor = float(a.grad_scale / pairs * (a.dloss ? double(*a.dloss) : 1.0));
+  if (!reduce) return;
   double sum[1] = {};
   for (int b = threadIdx.x; b < int(gridDim.x); b += 256) sum[0] += __ldcg(a.sums + b);
   block_sums(sum, sh);
-  if (threadIdx.x == 0)
-    *a.reduced = float(a.reduction == ZERO_REDUCE_MEAN ? sum[0] / double(max(1, __ldcg(&a.head->pairs))) : sum[0]);
+  if (threadIdx.x == 0) *a.reduced = float(a.reduction == ZERO_REDUCE_MEAN ? sum[0] / pairs : sum[0]);
 }
 
 // The rows' scales of a policy's backward call.
