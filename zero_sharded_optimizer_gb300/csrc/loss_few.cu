@@ -115,7 +115,7 @@ struct Sum {
   float m = -INFINITY, s = 0.0f;
   __device__ __forceinline__ void join(float m2, float s2) {
     const float top = fmaxf(m, m2);
-    s = top == -INFINITY ? s + s2 : s * exp2f(m - top) + s2 * exp2f(m2 - top);
+    s = top == -INFINITY ? s + s2 : s * exp2_even(m - top) + s2 * exp2_even(m2 - top);
     m = top;
   }
 };
@@ -200,7 +200,8 @@ __global__ void __launch_bounds__(256, 2) few_logits_kernel(const Args a, int wi
       a.z[logit_at(a, group, v, i)] = z;
       if (y == v && a.forward) a.zent[t] = z;
       const float m = __fmul_rn(z, kLog2e), top = fmaxf(sum.m, m), base = top == -INFINITY ? 0.0f : top;
-      sum.s = sum.s * exp2f(sum.m == -INFINITY ? -INFINITY : sum.m - base) + exp2f(fmaf(z, kLog2e, -base));
+      sum.s = sum.s * exp2_even(sum.m == -INFINITY ? -INFINITY : sum.m - base) +
+              exp2_even(fmaf(z, kLog2eRest, fmaf(z, kLog2e, -base)));
       sum.m = top;
     }
   }

@@ -512,9 +512,11 @@ __global__ void __launch_bounds__(256) dhidden_out_kernel(const Args a) {
 
 // The row's log-sum-exp from its partial maxima and sums (maxima in powers of
 // two): each of the row's lanes takes every lanes-th partial, eight loads in
-// flight; the first lane joins them.
+// flight; the first lane joins them. `Even`: by exponentials without a mean error.
+template <bool Even>
 __device__ __forceinline__ double row_lse(const float2* stats, int64_t count, int64_t Tp, int64_t i, int lane,
                                           int lanes, float2* sh, int r, int rows) {
+  const auto exp2_of = [](float x) { return Even ? exp2_even(x) : exp2f(x); };
   float m = -INFINITY, s = 0.0f;
   for (int64_t j0 = lane; j0 < count; j0 += 8 * lanes) {
     float2 x[8];
@@ -530,16 +532,16 @@ __device__ __forceinline__ double row_lse(const float2* stats, int64_t count, in
       for (int q = 0; q < 8; ++q) s += x[q].y;
       continue;
     }
-    s = m == -INFINITY ? s : s * exp2f(m - top);
+    s = m == -INFINITY ? s : s * exp2_of(m - top);
 #pragma unroll
-    for (int q = 0; q < 8; ++q) s += x[q].y * exp2f(x[q].x - top);  // 0 where x is -inf
+    for (int q = 0; q < 8; ++q) s += x[q].y * exp2_of(x[q].x - top);  // 0 where x is -inf
     m = top;
   }
   // A tree over the lanes, in a fixed order: between warps through shared memory,
   // then (row r's lanes are `rows` threads apart) within the first.
-  const auto join = [](float2 x, float2 y) {
+  const auto join = [&](float2 x, float2 y) {
     const float top = fmaxf(x.x, y.x);
-    const float sum = top == -INFINITY ? x.y + y.y : x.y * exp2f(x.x - top) + y.y * exp2f(y.x - top);
+    const float sum = top == -INFINITY ? x.y + y.y : x.y * exp2_of(x.x - top) + y.y * exp2_of(y.x - top);
     return make_float2(top, sum);
   };
   float2 x = make_float2(m, s);
@@ -647,6 +649,13 @@ __device__ __forceinline__ void policy_loss(const Args& a, const PolicyRow& row,
 
 constexpr int kSlopeRows = 16;  // most rows of a block of losses_kernel that goes by slopes
 
+// What the matrix kernel's exponentials do to a log-sum-exp: they take logits times
+// log2(e) in fp32, that is logits kTaken times as large, and ex2.approx is low by
+// 4.8e-8 of itself on average (over [-16, 0]), once for each logit and again where a
+// half tile's sum is rescaled: by kMeanLow together (measured over 6000 rows of 4931
+// logits of one matrix instruction each, which nothing else rounds off one way).
+constexpr double kTaken = double(kLog2e) * 0.69314718055994530942, kMeanLow = 1.1e-7;
+
 // 256 threads: `block_rows` rows (a power of two, up to 32), 256 / block_rows lanes each.
 //
 // `Slopes` (the policy and the preference loss): a row's log-probability, of
@@ -703,9 +712,9 @@ __global__ void __launch_bounds__(256, 4) losses_kernel(const Args a, int block_
       const int64_t at = t * a.L + e;
       if (a.ids[at] != kNoId) entries += double(a.weights[at]) * double(a.zent[at]);
     }
-    const double lse = a.has_ce ? row_lse(a.stats, a.partials, a.Tp, i, lane, lanes, sh, r, block_rows) : 0.0;
+    const double lse = a.has_ce ? row_lse<Slopes>(a.stats, a.partials, a.Tp, i, lane, lanes, sh, r, block_rows) : 0.0;
     const double lse_tau =
-        a.has_kd ? row_lse(a.stats_tau, a.partials, a.Tp, i, lane, lanes, sh, r, block_rows) : 0.0;
+        a.has_kd ? row_lse<Slopes>(a.stats_tau, a.partials, a.Tp, i, lane, lanes, sh, r, block_rows) : 0.0;
     if (a.L > 1) {
       part[threadIdx.x] = entries;
       __syncthreads();
@@ -717,9 +726,9 @@ __global__ void __launch_bounds__(256, 4) losses_kernel(const Args a, int block_
     }
     const bool fault = a.head->fault;  // NaN in lse too: a backward call's gradients show it then
     if (Slopes && lane == 0 && i0 + r < rows) {
-      const double z = entries, more = double(logit[r]) - z;
+      const double z = a.few ? entries : entries * kTaken, more = double(logit[r]) - z;
       const bool finite = isfinite(more) && isfinite(lse);
-      const double sum = finite ? lse + corrected(more, float(z - lse)) : lse;
+      const double sum = (finite ? lse + corrected(more, float(z - lse)) : lse) + (a.few ? 0.0 : kMeanLow);
       const double logp = fault ? NAN : (finite ? double(logit[r]) : z) - sum;
       a.lse[t] = fault ? NAN : float(sum);
       if (a.kind == kPreference) {
@@ -808,9 +817,9 @@ __device__ __forceinline__ void pair_loss(const Args& a, const double (&sum)[2],
     *loss = u * u;
     du = 2.0 * u;
   } else {
-    // log(1 + e^-u) and log(1 + e^u), and sigmoid(-u), from e^-|u|; fp32's
-    // functions are off by 2^-22 of themselves, as the results' own type is
-    const float e = expf(-fabsf(float(u))), l = log1pf(e), down = (u < 0.0 ? 1.0f : e) / (1.0f + e);
+    // log(1 + e^-u) and log(1 + e^u), and sigmoid(-u), from e^-|u|, in double: with
+    // smoothing the slope is a difference
+    const double e = exp(-fabs(u)), l = log1p(e), down = (u < 0.0 ? 1.0 : e) / (1.0 + e);
     *loss = (1.0 - a.smoothing) * ((u < 0.0 ? -u : 0.0) + l) + a.smoothing * ((u > 0.0 ? u : 0.0) + l);
     if (u != u) *loss = u;
     du = a.smoothing - down;
