@@ -651,7 +651,7 @@ typedef struct zero_policy {
   double clip_low, clip_high; /* at least 0, finite                            */
   double kl_weight;        /* finite                                           */
   float *logps;            /* [T] written by the forward pass: l_t; 0 for an
-                              empty row                                        */
+                              empty row. Read by the backward pass             */
   float *slopes;           /* [T] written by the forward pass, read by the
                               backward pass: dloss_t/dl_t                      */
 } zero_policy_t;
@@ -672,14 +672,19 @@ typedef struct zero_preference {
   double beta, smoothing, margin, nll_weight; /* finite; smoothing in [0, 1],
                               and 0 for the squared loss                       */
   float *logps;            /* [2 pairs] written by the forward pass: S_s       */
+  float *row_logps;        /* [T] written by the forward pass, read by the
+                              backward pass: l_t; 0 for an empty row           */
   float *slopes;           /* [2 pairs] written by the forward pass, read by the
                               backward pass: dloss_i/dl_t of a labelled row of
                               the sequence                                     */
   int32_t *counts;         /* [2 pairs] written by the forward pass: n_s       */
 } zero_preference_t;
 
-/* As zero_xent_*. The backward calls read p->lse and q->slopes of a forward call
- * on the same inputs, and of the rest of *q only `pairs` and `offsets`.
+/* As zero_xent_*. The backward calls read p->lse, q->slopes and the rows'
+ * log-probabilities (q->logps, q->row_logps) of a forward call on the same inputs,
+ * and of the rest of *q only `pairs` and `offsets`. (The label's p - 1 is taken from
+ * its log-probability: from lse, which is rounded to fp32, it would be off by 3e-7
+ * however small it is.)
  * Errors: as zero_xent_*, plus EINVAL for a NULL q, options out of range, a
  * number of rows that 2 pairs sequences of equal length do not make. */
 int zero_policy_workspace_bytes(const zero_head_loss_t *p, const zero_policy_t *q, int64_t *bytes);

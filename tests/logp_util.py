@@ -156,6 +156,9 @@ def check(got, r, dtype, what="", parts=1):
                 f"{what} {name}: {int(bad.sum())} of {x.numel()} outside their bounds; worst at {i}: "
                 f"got {float(x.flatten()[i])!r}, exact {float(r[name].flatten()[i])!r}, "
                 f"bound {float(b.flatten()[i]):.3g}")
+    if got.row_logps is not None and got.loss is not None:
+        off = (got.row_logps.double().flatten() - r["l"]).abs()
+        assert bool((off <= 1.01 * r["e"] + 2.0 ** -23 * r["l"].abs()).all()), f"{what} row_logps"
     if got.counts is not None:
         assert torch.equal(got.counts, r["counts"]), what
     if got.reduced is not None:

@@ -105,7 +105,34 @@ def test_rows_without_a_slope_bring_nothing_in(losses, cuda, kind, T):
     bad[1] = math.nan
     got = losses.policy_step(bad, w, y, old, adv, reduction="sum")
     assert math.isnan(float(got.logps[1])) and float(got.loss[1]) == 0.0 and not got.dhidden[1].any()
-    check(got._replace(logps=None), r, dt, "", parts_of(dt, T))
+    check(got._replace(logps=None, row_logps=None), r, dt, "", parts_of(dt, T))
+
+
+@pytest.mark.parametrize("T", [8, 300])
+@pytest.mark.parametrize("kind", TYPES)
+def test_gradients_of_sure_rows_sum_to_zero(losses, cuda, kind, T):
+    """Rows that are all but certain of their labels. A column of weights that are all one makes its
+    element of dhidden the sum of the row's gradient, which is zero: the label's p - 1 cancels the others'
+    p, 1 - p of it. The others' share of the error is in proportion to 1 - p: 4 dz of the logits, 2^-20 of
+    their exponentials, 2^-23 |lse| of lse, V 2^-23 of their sum, 2^-8 where G is bf16. The label's own is
+    that of a sum of exponentials that is 1 and little more: some roundings of 2^-24 and the mean of what
+    the tensor cores' sums lose that is put back (1.1e-7), 2^-21 in all."""
+    dt, V, D = TYPES[kind], 300, 64
+    g = torch.Generator().manual_seed(58 + T)
+    w = torch.randn(V, D, generator=g)
+    w[:, 0] = 1.0
+    y = torch.randint(V, (T,), generator=g)
+    size = torch.linspace(20.0, 60.0, T).unsqueeze(1)
+    h = size * w[y] / w[y].square().sum(1, keepdim=True)
+    h[:, 0] = 0.0
+    h, w, y = h.to(dt).to(cuda), w.to(dt).to(cuda), y.to(cuda)
+    adv = torch.ones(T, device=cuda)
+    r = policy(h, w, y, torch.zeros_like(adv), adv, reduction="sum")
+    got = losses.policy_step(h, w, y, r["l"].float(), adv, clip=0.5, reduction="sum")
+    others = -torch.expm1(r["l"])
+    off = others * (4 * r["dz"] + 2.0 ** -20 + 2.0 ** -23 * (r["lse"].abs() + V) +
+                    (2.0 ** -8 if kind == "bf16" else 0.0)) + 2.0 ** -21
+    assert bool((got.dhidden[:, 0].double().abs() <= 1.01 * off).all())
 
 
 def test_policy_clip_of_one_number(losses, cuda):
@@ -128,7 +155,7 @@ def test_policy_most_rows_without_a_slope(losses, cuda, kind, T):
         r = policy(h, w, y, old, adv)
         check(losses.policy_step(h, w, y, old, adv), r, dt, f"{still}", parts_of(dt, T))
         out = losses.policy_forward(h, w, y, old, adv)
-        got = losses.policy_backward(h, w, y, out.lse, out.slopes)
+        got = losses.policy_backward(h, w, y, out.lse, out.row_logps, out.slopes)
         check(got, r, dt, f"{still} backward", parts_of(dt, T))
     assert not got.dhidden.any() and not got.dweight.any()
 
@@ -153,7 +180,8 @@ def test_policy_edges(losses, cuda, kind):
         assert not got.slopes[rows].any() and not got.dhidden[rows].any()
     usual = torch.arange(T, device=cuda) % 10 > 3
     r = policy(h, w, torch.where(usual, y, IGNORE), old, adv, reduction="none")
-    check(got._replace(logps=None, slopes=None, dhidden=None, loss=torch.where(usual, got.loss, 0.0)), r, dt)
+    check(got._replace(logps=None, row_logps=None, slopes=None, dhidden=None,
+                       loss=torch.where(usual, got.loss, 0.0)), r, dt)
     # not a number: it shows in its row, and in no other
     for name in ("old", "adv", "ref"):
         o, a, ref = sampled(h, w, y, g)
@@ -276,11 +304,12 @@ def test_preference_offsets_that_do_not_ascend(losses, cuda, kind):
     for bounds in ([0, 61, 61], [-1, 10, 60], [0, 30, 20], [2 ** 40, 5, 60], [0, -2 ** 62, 60], [0, 10, 2 ** 62]):
         offsets = torch.tensor(bounds, device=cuda)
         for got in (losses.preference_step(h, w, y, offsets), losses.preference_forward(h, w, y, offsets),
-                    losses.preference_backward(h, w, y, good.lse, good.slopes, offsets)):
+                    losses.preference_backward(h, w, y, good.lse, good.row_logps, good.slopes, offsets)):
             if got.loss is not None:
                 assert bool(got.loss.isnan().all()) and bool(got.reduced.isnan())
                 assert bool(got.logps.isnan().all()) and bool(got.slopes.isnan().all())
-                assert bool(got.lse[there].isnan().all()) and not got.lse[~there].any()
+                for rows in (got.lse, got.row_logps):
+                    assert bool(rows[there].isnan().all()) and not rows[~there].any()
                 assert not got.counts.any()
             if got.dhidden is not None:
                 assert bool(got.dhidden[there].isnan().all()) and not got.dhidden[~there].any()
@@ -349,13 +378,13 @@ def test_backward_alone_equals_step(losses, cuda, kind, T, V, D):
         for reduction in ("mean", "none"):
             whole = step(*args, reduction=reduction, grad_scale=0.5, **more)
             first = forward(*args, reduction=reduction, **more)
-            for name in ("loss", "reduced", "logps", "slopes", "lse", "counts"):
+            for name in ("loss", "reduced", "logps", "slopes", "lse", "row_logps", "counts"):
                 a, b = getattr(whole, name), getattr(first, name)
                 assert a is None and b is None or torch.equal(a, b), name
-            then = backward(*args[:3], first.lse, first.slopes, *extra, reduction=reduction, grad_scale=0.5)
+            then = backward(*args[:3], first.lse, first.row_logps, first.slopes, *extra, reduction=reduction, grad_scale=0.5)
             assert torch.equal(then.dhidden, whole.dhidden) and torch.equal(then.dweight, whole.dweight)
             for left in ("dhidden", "dweight"):
-                then = backward(*args[:3], first.lse, first.slopes, *extra, reduction=reduction, grad_scale=0.5,
+                then = backward(*args[:3], first.lse, first.row_logps, first.slopes, *extra, reduction=reduction, grad_scale=0.5,
                                 **{left: False})
                 assert getattr(then, left) is None
                 if left == "dhidden":
@@ -494,13 +523,13 @@ def test_a_wait_that_runs_out(losses, cuda, kind):
         good = step(*args, **more)
         for passes, call, a, m in ((1, forward, args, more), (1, step, args, more), (2, step, args, more),
                                    (3, step, args, more), (2, step, args, dict(more, dhidden=False)),
-                                   (2, backward, (*args[:3], good.lse, good.slopes, *extra), {})):
+                                   (2, backward, (*args[:3], good.lse, good.row_logps, good.slopes, *extra), {})):
             torch.cuda.synchronize()
             abi.zero_debug_withhold_head_loss(passes, 50_000_000)
             r = call(*a, **m)
             torch.cuda.synchronize()
             if r.loss is not None:
-                assert nan(r.reduced) and nan(r.lse[there])
+                assert nan(r.reduced) and nan(r.lse[there]) and nan(r.row_logps[there])
                 for x in (r.loss, r.logps, r.slopes):
                     assert nan(x[there] if rows else x)
                     assert not rows or not x[~there].any()
@@ -562,7 +591,7 @@ def test_autograd(losses, cuda):
                                dloss=dloss if reduction == "none" else 2.0)
             total = (loss * dloss).sum() if reduction == "none" else 2.0 * loss
             gh, gw = torch.autograd.grad(total, (a, b), create_graph=True)
-            check(losses.LogpLosses(None, None, None, None, None, None, gh.detach(), gw.detach()), r, torch.float32,
+            check(losses.LogpLosses(*[None] * 7, gh.detach(), gw.detach()), r, torch.float32,
                   f"{name} {reduction}")
             with pytest.raises(RuntimeError, match="no second derivatives"):
                 gh.square().sum().backward()

@@ -30,7 +30,7 @@ def preference(abi, **changes):
     q = abi.Preference()
     q.pairs, q.beta = 5, 0.1
     at = 1 << 33
-    for name in ("offsets", "logps", "slopes", "counts"):
+    for name in ("offsets", "logps", "row_logps", "slopes", "counts"):
         setattr(q, name, at)
         at += 1 << 20
     for k, v in changes.items():
@@ -93,6 +93,7 @@ def test_policy_refusals(abi, change, text):
     (dict(smoothing=0.1, kind=1), "smoothing"), (dict(margin=math.nan), "margin"),
     (dict(nll_weight=math.inf), "nll_weight"), (dict(logps=None), "logps is NULL"),
     (dict(slopes=None), "slopes is NULL"), (dict(counts=None), "counts is NULL"),
+    (dict(row_logps=None), "row_logps is NULL"), (dict(row_logps=(1 << 33) + 40), "overlap"),
     (dict(counts=(1 << 33) + 40), "overlap"), (dict(ref_logps=(1 << 33) + (1 << 20)), "overlap")])
 def test_preference_refusals(abi, change, text):
     refused(abi, "preference", "step", problem(abi), preference(abi, **change), abi.ZERO_EINVAL, text)
@@ -115,10 +116,10 @@ def test_null_problem_and_output(abi):
 
 
 def test_a_backward_call_needs_little(abi):
-    """lse, the slopes and, for pairs, their number and offsets."""
+    """lse, the rows' log-probabilities, the slopes and, for pairs, their number and offsets."""
     p = problem(abi, loss=None, reduced=None, workspace_bytes=1000)
-    refused(abi, "policy", "backward", p, policy(abi, old_logps=None, advantages=None, logps=None), abi.ZERO_EINVAL,
-            "are needed")
+    refused(abi, "policy", "backward", p, policy(abi, old_logps=None, advantages=None), abi.ZERO_EINVAL, "are needed")
+    refused(abi, "policy", "backward", p, policy(abi, logps=None), abi.ZERO_EINVAL, "logps is NULL")
     refused(abi, "preference", "backward", p, preference(abi, logps=None, counts=None), abi.ZERO_EINVAL, "are needed")
 
 
@@ -148,14 +149,13 @@ def test_second_derivatives_raise(abi, monkeypatch, op, wrt):
 
     def forward(h, w, *a, **m):
         none = torch.zeros(T)
-        return losses.LogpLosses(none, value(h, w).detach(), none, none, none)
+        return losses.LogpLosses(none, value(h, w).detach(), none, none, none, none)
 
     def backward(h, w, *a, dloss, dhidden, dweight, **m):
         with torch.enable_grad():
             x, z = h.detach().requires_grad_(), w.detach().requires_grad_()
             gh, gw = torch.autograd.grad(value(x, z) * dloss, (x, z))
-        return losses.LogpLosses(None, None, None, None, None, None, None if dhidden is False else gh,
-                                 None if dweight is False else gw)
+        return losses.LogpLosses(*[None] * 7, None if dhidden is False else gh, None if dweight is False else gw)
 
     monkeypatch.setattr(losses, f"{op}_forward", forward)
     monkeypatch.setattr(losses, f"{op}_backward", backward)

@@ -650,7 +650,8 @@ class Preference(ctypes.Structure):
     """zero_preference_t."""
     _fields_ = [("pairs", _i64), ("offsets", _vp), ("ref_logps", _vp), ("kind", _i32),
                 ("average", _i32), ("beta", _dbl), ("smoothing", _dbl), ("margin", _dbl),
-                ("nll_weight", _dbl), ("logps", _vp), ("slopes", _vp), ("counts", _vp)]
+                ("nll_weight", _dbl), ("logps", _vp), ("row_logps", _vp), ("slopes", _vp),
+                ("counts", _vp)]
 
 
 def zero_policy_workspace_bytes(p: HeadLoss, q: Policy) -> int:

@@ -226,20 +226,20 @@ constexpr int kTileV = 64;  // rows of dweight's tiles
 // What a lane needs of its row (of a group of eight) for G.
 struct FewRow {
   int64_t t = -1;
-  float scale = 0.0f, lse = 0.0f;
+  float scale = 0.0f, lse = 0.0f, gap = 0.0f;  // gap: p - 1 of the label
   int32_t y = -1;
   __device__ __forceinline__ FewRow(const Args& a, int i, int rows) {
     if (i >= rows) return;
     t = a.rowmap[i];
     scale = a.scales[t];
     lse = a.lse[t];
+    gap = expm1f(a.row_logps[t]);
     y = a.ids[t];
   }
   // G of the row at column v with logit z, without the common factor; a row without a
   // slope has none, whatever its logits.
   __device__ __forceinline__ float gradient(float z, int64_t v) const {
-    const float p = expf(z - lse);
-    return scale == 0.0f ? 0.0f : scale * (y == v ? p - 1.0f : p);
+    return scale == 0.0f ? 0.0f : scale * (y == v ? gap : expf(z - lse));
   }
 };
 

@@ -170,9 +170,11 @@ int check_buffers(const Problem& problem, int pass) {
   const int64_t each = po ? T : pr ? 2 * pr->pairs : 0;
   const float* ref = !fwd ? nullptr : po ? (po->kl_weight != 0.0 ? po->ref_logps : nullptr) : pr ? pr->ref_logps : nullptr;
   float* const slopes = po ? po->slopes : pr ? pr->slopes : nullptr;
-  float* const logps = !fwd ? nullptr : po ? po->logps : pr ? pr->logps : nullptr;
+  float* const rows = po ? po->logps : pr ? pr->row_logps : nullptr;  // [T], written and read as lse is
+  float* const logps = fwd && pr ? pr->logps : nullptr;
   if ((e = check_pointer(slopes, each, 4, "slopes"))) return e;
-  if (fwd && (e = check_pointer(logps, each, 4, "logps"))) return e;
+  if ((e = check_pointer(rows, po || pr ? T : 0, 4, po ? "logps" : "row_logps"))) return e;
+  if (fwd && pr && (e = check_pointer(logps, each, 4, "logps"))) return e;
   if ((e = check_pointer(ref, fwd && po && po->kl_weight != 0.0 ? T : 0, 4, "ref_logps"))) return e;
   if (fwd && po) {
     if ((e = check_pointer(po->old_logps, T, 4, "old_logps"))) return e;
@@ -200,6 +202,7 @@ int check_buffers(const Problem& problem, int pass) {
       {fwd && po ? po->advantages : nullptr, 1, 4 * T, 4 * T, "advantages", false},
       {ref, 1, 4 * each, 4 * each, "ref_logps", false},
       {pr ? pr->offsets : nullptr, 1, offsets, offsets, "offsets", false},
+      {rows, 1, 4 * T, 4 * T, po ? "logps" : "row_logps", fwd},
       {logps, 1, 4 * each, 4 * each, "logps", true},
       {slopes, 1, 4 * each, 4 * each, "slopes", fwd},
       {fwd && pr ? pr->counts : nullptr, 1, 4 * each, 4 * each, "counts", true},
@@ -287,7 +290,7 @@ int plan(const Problem& problem, int pass, Args* a, __nv_bfloat16** packed_weigh
     a->low = 1.0 - q->clip_low;
     a->high = 1.0 + q->clip_high;
     a->kl_weight = q->kl_weight;
-    a->logps = q->logps;
+    a->logps = a->row_logps = q->logps;
     a->slopes = q->slopes;
   }
   if (const zero_preference_t* q = problem.preference) {
@@ -301,6 +304,7 @@ int plan(const Problem& problem, int pass, Args* a, __nv_bfloat16** packed_weigh
     a->margin = q->margin;
     a->nll_weight = q->nll_weight;
     a->logps = q->logps;
+    a->row_logps = q->row_logps;
     a->slopes = q->slopes;
     a->seq_counts = q->counts;
   }
@@ -386,7 +390,7 @@ int plan(const Problem& problem, int pass, Args* a, __nv_bfloat16** packed_weigh
   const int64_t common = w.at;
   a->sums = w.take<double>(zl::kLossBlocks);
   a->zent = w.take<float>(a->T, a->L);
-  if (problem.preference) a->row_logps = w.take<double>(a->T);
+  if (problem.preference) a->terms = w.take<double>(a->T);
   if (a->has_ce) a->stats = w.take<float2>(a->partials, a->Tp);
   if (a->has_kd) a->stats_tau = w.take<float2>(a->partials, a->Tp);
   int64_t most = w.at;

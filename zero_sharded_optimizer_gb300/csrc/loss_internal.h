@@ -98,6 +98,7 @@ struct Args {
   int32_t squared, average;
   double beta, smoothing, margin, nll_weight;
   float* logps;           // [T] or [2 pairs]
+  float* row_logps;       // [T] the labels' log-probabilities: logps, or a preference loss's own
   float* slopes;
   int32_t* seq_counts;    // [2 pairs] labelled rows
 
@@ -112,7 +113,7 @@ struct Args {
   uint16_t* starts;       // distillation: [2 tiles + 1][T] first entry of each half tile
   float* scales;          // [T] row_scale of a call that goes by slopes
   float* left;            // [Tp] what G's one bf16 value leaves of the label's entry, or NULL
-  double* row_logps;      // [T] a preference call's labels' log-probabilities
+  double* terms;          // [T] a preference call's labels' log-probabilities in double
   double* sums;           // [kLossBlocks] parts of the reduced loss
   float* zent;            // [T][L] logits of the entries
   __nv_bfloat16* hp;      // [planes][Tp][Dp] packed hidden states

@@ -50,7 +50,8 @@ __device__ __forceinline__ void finish_row(const Args& a, int64_t t, bool has_y,
   if (a.scales) a.scales[t] = 0.0f;
   if (a.forward && !(has_y || has_kd)) {
     if (a.kind != kPreference) a.loss[t] = 0.0f;
-    if (a.kind == kPolicy) a.logps[t] = a.slopes[t] = 0.0f;
+    if (a.row_logps) a.row_logps[t] = 0.0f;
+    if (a.kind == kPolicy) a.slopes[t] = 0.0f;
     if (a.has_ce) a.lse[t] = 0.0f;
     if (a.has_kd) a.lse_tau[t] = 0.0f;
   }
@@ -415,7 +416,8 @@ __device__ __noinline__ void mark_fault(const Args& a, bool f32, int64_t first, 
   for (int64_t t = first; t < a.T; t += step) {
     if (a.rowpos[t] == -1) continue;
     if (a.kind != kPreference) a.loss[t] = NAN;
-    if (a.kind == kPolicy) a.logps[t] = a.slopes[t] = NAN;
+    if (a.row_logps) a.row_logps[t] = NAN;
+    if (a.kind == kPolicy) a.slopes[t] = NAN;
     if (a.has_ce) a.lse[t] = NAN;
     if (a.has_kd) a.lse_tau[t] = NAN;
   }
@@ -730,15 +732,15 @@ __global__ void __launch_bounds__(256, 4) losses_kernel(const Args a, int block_
       const bool finite = isfinite(more) && isfinite(lse);
       const double sum = (finite ? lse + corrected(more, float(z - lse)) : lse) + (a.few ? 0.0 : kMeanLow);
       const double logp = fault ? NAN : (finite ? double(logit[r]) : z) - sum;
+      const float l = float(logp);
       a.lse[t] = fault ? NAN : float(sum);
+      a.row_logps[t] = l;
       if (a.kind == kPreference) {
-        a.row_logps[t] = logp;
+        a.terms[t] = logp;
       } else {
-        const float l = float(logp);
         double loss, slope;
         policy_loss(a, row, l, &loss, &slope);
         a.loss[t] = fault ? NAN : float(loss);
-        a.logps[t] = l;
         const float s = fault ? NAN : float(slope);
         a.slopes[t] = s;
         if (a.scales) a.scales[t] = -s * row.dloss;
@@ -851,7 +853,7 @@ __global__ void __launch_bounds__(256) pairs_kernel(const Args a) {
         if (a.rowpos[t] >= 0) a.scales[t] = NAN;
     if (Forward) {
       for (int64_t t = first; t < a.T; t += step)
-        if (a.rowpos[t] >= 0) a.lse[t] = NAN;
+        if (a.rowpos[t] >= 0) a.lse[t] = a.row_logps[t] = NAN;
       for (int64_t i = first; i < a.pairs; i += step) a.loss[i] = NAN;
       for (int64_t i = first; i < 2 * a.pairs; i += step) {
         a.logps[i] = a.slopes[i] = NAN;
@@ -879,7 +881,7 @@ __global__ void __launch_bounds__(256) pairs_kernel(const Args a) {
 #pragma unroll 4
       for (int64_t t = begin[k] + threadIdx.x; t < end[k]; t += 256) {
         const bool labelled = a.rowpos[t] >= 0;
-        const double l = Forward ? a.row_logps[t] : 0.0;  // (of a row without a label: anything)
+        const double l = Forward ? a.terms[t] : 0.0;  // (of a row without a label: anything)
         x[k] += labelled ? 1.0 : 0.0;
         if (Forward) x[2 + k] += labelled ? l : 0.0;
       }

@@ -63,14 +63,15 @@ class LogpLosses(NamedTuple):
     float32, of each row (policy; 0 for an empty row) or of each pair
     (preference); ``reduced`` as in Losses; ``logps`` the log-probabilities of
     the rows, or their sums over each sequence, and ``counts`` the sequences'
-    labelled rows (int32); ``lse`` and ``slopes``, the losses' derivatives by the
-    log-probabilities of each row (or of a sequence's rows), for a backward pass;
-    the gradients, where they were taken."""
+    labelled rows (int32); for a backward pass ``lse``, ``row_logps``, the rows'
+    log-probabilities, and ``slopes``, the losses' derivatives by them, of each row
+    or of a sequence's rows; the gradients, where they were taken."""
     loss: torch.Tensor | None
     reduced: torch.Tensor | None
     logps: torch.Tensor | None
     slopes: torch.Tensor | None
     lse: torch.Tensor | None
+    row_logps: torch.Tensor | None
     counts: torch.Tensor | None = None
     dhidden: torch.Tensor | None = None
     dweight: torch.Tensor | None = None
@@ -339,28 +340,33 @@ class _Call:
             q.ref_logps = _vector(ref_logps, "ref_logps", torch.float32, 2 * q.pairs, self.device)
             self.keep.append(ref_logps)
 
-    def slopes(self, lse, slopes):
-        """The forward pass's lse and slopes, for a backward pass."""
+    def slopes(self, lse, row_logps, slopes):
+        """The forward pass's, for a backward pass."""
+        q = self.extra
         self.p.lse = self.vector(lse, "lse", torch.float32)
-        if isinstance(self.extra, abi.Policy):
-            self.extra.slopes = self.vector(slopes, "slopes", torch.float32)
+        rows = self.vector(row_logps, "row_logps", torch.float32)
+        if isinstance(q, abi.Policy):
+            q.logps, q.slopes = rows, self.vector(slopes, "slopes", torch.float32)
         else:
-            self.extra.slopes = _vector(slopes, "slopes", torch.float32, 2 * self.count, self.device)
-        self.keep += [lse, slopes]
+            q.row_logps = rows
+            q.slopes = _vector(slopes, "slopes", torch.float32, 2 * self.count, self.device)
+        self.keep += [lse, row_logps, slopes]
 
     def logp_losses(self):
         """The fields of a LogpLosses but for the gradients, to be written."""
         q = self.extra
         loss, reduced, lse, _ = self.losses()
+        logps = rows = self.new(self.lead)
         counts = None
         if isinstance(q, abi.Policy):
-            logps, slopes = self.new(self.lead), self.new(self.lead)
+            slopes = self.new(self.lead)
         else:
+            q.row_logps = rows.data_ptr()
             logps, slopes = self.new(2 * q.pairs), self.new(2 * q.pairs)
             counts = self.new(2 * q.pairs, torch.int32)
             q.counts = counts.data_ptr()
         q.logps, q.slopes = logps.data_ptr(), slopes.data_ptr()
-        return loss, reduced, logps, slopes, lse, counts
+        return loss, reduced, logps, slopes, lse, rows, counts
 
 
 def xent_forward(hidden, weight, labels, *, reduction: str = "mean", ignore_index: int = -100,
@@ -453,17 +459,17 @@ def policy_forward(hidden, weight, labels, old_logps, advantages, *, ref_logps=N
     return LogpLosses(*out)
 
 
-def policy_backward(hidden, weight, labels, lse, slopes, *, reduction: str = "mean", ignore_index: int = -100,
-                    dloss=None, grad_scale: float = 1.0, dhidden=None, dweight=None, accumulate: bool = False,
-                    stream=None) -> LogpLosses:
-    """The gradients, given ``lse`` and ``slopes`` of policy_forward on the same
-    inputs; ``dloss`` as in xent_backward."""
+def policy_backward(hidden, weight, labels, lse, row_logps, slopes, *, reduction: str = "mean",
+                    ignore_index: int = -100, dloss=None, grad_scale: float = 1.0, dhidden=None, dweight=None,
+                    accumulate: bool = False, stream=None) -> LogpLosses:
+    """The gradients, given ``lse``, ``row_logps`` and ``slopes`` of policy_forward
+    on the same inputs; ``dloss`` as in xent_backward."""
     c = _Call(hidden, weight, labels, reduction, ignore_index, stream)
     c.policy(forward=False)
-    c.slopes(lse, slopes)
+    c.slopes(lse, row_logps, slopes)
     dh, dw = c.gradients(dloss, grad_scale, dhidden, dweight, accumulate)
     c.run(abi.zero_policy_backward, None)
-    return LogpLosses(None, None, None, slopes, lse, None, dh, dw)
+    return LogpLosses(None, None, None, slopes, lse, row_logps, None, dh, dw)
 
 
 def policy_step(hidden, weight, labels, old_logps, advantages, *, ref_logps=None, clip=0.2, kl_weight: float = 0.0,
@@ -498,18 +504,19 @@ def preference_forward(hidden, weight, labels, offsets=None, *, ref_logps=None, 
     return LogpLosses(*out)
 
 
-def preference_backward(hidden, weight, labels, lse, slopes, offsets=None, *, reduction: str = "mean",
+def preference_backward(hidden, weight, labels, lse, row_logps, slopes, offsets=None, *, reduction: str = "mean",
                         ignore_index: int = -100, dloss=None, grad_scale: float = 1.0, dhidden=None, dweight=None,
                         accumulate: bool = False, stream=None) -> LogpLosses:
-    """The gradients, given ``lse`` and ``slopes`` of preference_forward on the same
-    inputs. ``dloss`` (float32): the gradient of the total with respect to
-    ``loss`` [pairs] (reduction "none") or to ``reduced``; ones when None."""
+    """The gradients, given ``lse``, ``row_logps`` and ``slopes`` of
+    preference_forward on the same inputs. ``dloss`` (float32): the gradient of
+    the total with respect to ``loss`` [pairs] (reduction "none") or to
+    ``reduced``; ones when None."""
     c = _Call(hidden, weight, labels, reduction, ignore_index, stream)
     c.preference(offsets)
-    c.slopes(lse, slopes)
+    c.slopes(lse, row_logps, slopes)
     dh, dw = c.gradients(dloss, grad_scale, dhidden, dweight, accumulate)
     c.run(abi.zero_preference_backward, None)
-    return LogpLosses(None, None, None, slopes, lse, None, dh, dw)
+    return LogpLosses(None, None, None, slopes, lse, row_logps, None, dh, dw)
 
 
 def preference_step(hidden, weight, labels, offsets=None, *, ref_logps=None, kind: str = "sigmoid",
@@ -596,18 +603,18 @@ class _Policy(torch.autograd.Function):
     def forward(ctx, hidden, weight, labels, old_logps, advantages, ref_logps, options, reduction, ignore_index):
         r = policy_forward(hidden, weight, labels, old_logps, advantages, ref_logps=ref_logps,
                            reduction=reduction, ignore_index=ignore_index, **options)
-        ctx.save_for_backward(hidden, weight, labels, r.lse, r.slopes)
+        ctx.save_for_backward(hidden, weight, labels, r.lse, r.row_logps, r.slopes)
         ctx.options = dict(reduction=reduction, ignore_index=ignore_index)
         return r.loss if reduction == "none" else r.reduced
 
     @staticmethod
     def backward(ctx, dloss):
-        hidden, weight, labels, lse, slopes = ctx.saved_tensors
+        hidden, weight, labels, lse, logps, slopes = ctx.saved_tensors
         none = (None,) * 7
         if not any(ctx.needs_input_grad[:2]):
             return None, None, *none
         with torch.no_grad():
-            r = policy_backward(hidden, weight, labels, lse, slopes, dloss=dloss.contiguous(),
+            r = policy_backward(hidden, weight, labels, lse, logps, slopes, dloss=dloss.contiguous(),
                                 dhidden=None if ctx.needs_input_grad[0] else False,
                                 dweight=None if ctx.needs_input_grad[1] else False, **ctx.options)
         return *_once(r, hidden, weight, dloss), *none
@@ -618,18 +625,18 @@ class _Preference(torch.autograd.Function):
     def forward(ctx, hidden, weight, labels, offsets, ref_logps, options, reduction, ignore_index):
         r = preference_forward(hidden, weight, labels, offsets, ref_logps=ref_logps, reduction=reduction,
                                ignore_index=ignore_index, **options)
-        ctx.save_for_backward(hidden, weight, labels, offsets, r.lse, r.slopes)
+        ctx.save_for_backward(hidden, weight, labels, offsets, r.lse, r.row_logps, r.slopes)
         ctx.options = dict(reduction=reduction, ignore_index=ignore_index)
         return r.loss if reduction == "none" else r.reduced
 
     @staticmethod
     def backward(ctx, dloss):
-        hidden, weight, labels, offsets, lse, slopes = ctx.saved_tensors
+        hidden, weight, labels, offsets, lse, logps, slopes = ctx.saved_tensors
         none = (None,) * 6
         if not any(ctx.needs_input_grad[:2]):
             return None, None, *none
         with torch.no_grad():
-            r = preference_backward(hidden, weight, labels, lse, slopes, offsets, dloss=dloss.contiguous(),
+            r = preference_backward(hidden, weight, labels, lse, logps, slopes, offsets, dloss=dloss.contiguous(),
                                     dhidden=None if ctx.needs_input_grad[0] else False,
                                     dweight=None if ctx.needs_input_grad[1] else False, **ctx.options)
         return *_once(r, hidden, weight, dloss), *none
