@@ -64,8 +64,9 @@ class LogpLosses(NamedTuple):
     (preference); ``reduced`` as in Losses; ``logps`` the log-probabilities of
     the rows, or their sums over each sequence, and ``counts`` the sequences'
     labelled rows (int32); for a backward pass ``lse``, ``row_logps``, the rows'
-    log-probabilities, and ``slopes``, the losses' derivatives by them, of each row
-    or of a sequence's rows; the gradients, where they were taken."""
+    log-probabilities (policy: ``logps`` itself), and ``slopes``, the losses'
+    derivatives by them, of each row or of a sequence's rows; the gradients, where
+    they were taken."""
     loss: torch.Tensor | None
     reduced: torch.Tensor | None
     logps: torch.Tensor | None
