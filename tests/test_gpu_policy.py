@@ -381,11 +381,11 @@ def test_backward_alone_equals_step(losses, cuda, kind, T, V, D):
             for name in ("loss", "reduced", "logps", "slopes", "lse", "row_logps", "counts"):
                 a, b = getattr(whole, name), getattr(first, name)
                 assert a is None and b is None or torch.equal(a, b), name
-            then = backward(*args[:3], first.lse, first.row_logps, first.slopes, *extra, reduction=reduction, grad_scale=0.5)
+            saved = (first.lse, first.row_logps, first.slopes)
+            then = backward(*args[:3], *saved, *extra, reduction=reduction, grad_scale=0.5)
             assert torch.equal(then.dhidden, whole.dhidden) and torch.equal(then.dweight, whole.dweight)
             for left in ("dhidden", "dweight"):
-                then = backward(*args[:3], first.lse, first.row_logps, first.slopes, *extra, reduction=reduction, grad_scale=0.5,
-                                **{left: False})
+                then = backward(*args[:3], *saved, *extra, reduction=reduction, grad_scale=0.5, **{left: False})
                 assert getattr(then, left) is None
                 if left == "dhidden":
                     assert torch.equal(then.dweight, whole.dweight)
@@ -598,6 +598,45 @@ def test_autograd(losses, cuda):
             only, = torch.autograd.grad(losses.linear_policy(h, b, y, old, adv) if name == "policy" else
                                         losses.linear_preference(h, b, y, offsets), b)
             assert only.shape == w.shape
+
+
+@pytest.mark.parametrize("T", [20, 500])
+def test_autograd_in_a_graph(losses, cuda, T):
+    """A tied model's forward and backward pass, captured while an eager graph of the same storage lives:
+    replays on new values give what eager calls give."""
+    from zero_sharded_optimizer_gb300.embedding import embedding
+    V, D = 1500, 96
+    _, w, y, g = inputs(T, V, D, torch.bfloat16, 34, cuda, masked=0.2)
+    ids = torch.randint(V, (T,), generator=g).to(cuda)
+    old, adv = torch.full((T,), -7.0, device=cuda), torch.randn(T, generator=g).to(cuda)
+    offsets = torch.tensor([0, T // 5, T // 2, T - 3, T], device=cuda)
+
+    def gradients():
+        wte = w.detach().requires_grad_()
+        x = embedding(ids, wte)
+        total = losses.linear_policy(x, wte, y, old, adv) + losses.linear_preference(x, wte, y, offsets, beta=0.5)
+        return total.detach(), *torch.autograd.grad(total, wte)
+
+    leaf = w.detach().requires_grad_()
+    alive = losses.linear_policy(embedding(ids, leaf), leaf, y, old, adv)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        gradients()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = gradients()
+    assert alive.requires_grad
+    for _ in range(2):
+        w.copy_(torch.randn(V, D, generator=g))
+        ids.copy_(torch.randint(V, (T,), generator=g))
+        adv.copy_(torch.randn(T, generator=g))
+        offsets[1:4] = torch.randint(T + 1, (3,), generator=g).sort().values.to(cuda)
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(out, gradients()):
+            assert torch.equal(a, b)
 
 
 def test_refusals_of_the_binding(losses, cuda):

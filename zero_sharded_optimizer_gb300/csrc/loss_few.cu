@@ -233,7 +233,7 @@ struct FewRow {
     t = a.rowmap[i];
     scale = a.scales[t];
     lse = a.lse[t];
-    gap = expm1f(a.row_logps[t]);
+    gap = a.weights[t];
     y = a.ids[t];
   }
   // G of the row at column v with logit z, without the common factor; a row without a

@@ -109,7 +109,8 @@ struct Args {
   float2* coef;           // [T] (ce or 0, kd or 0)
   float* konst;           // [T] the loss's part that no logit enters
   int32_t* ids;           // [T][L] ascending, kNoId after the last
-  float* weights;         // [T][L] weight of each entry's logit in loss and gradient
+  float* weights;         // [T][L] weight of each entry's logit in loss and gradient; a loss by
+                          // slopes: p - 1 of the label, from its log-probability, for the gradient
   uint16_t* starts;       // distillation: [2 tiles + 1][T] first entry of each half tile
   float* scales;          // [T] row_scale of a call that goes by slopes
   float* left;            // [Tp] what G's one bf16 value leaves of the label's entry, or NULL

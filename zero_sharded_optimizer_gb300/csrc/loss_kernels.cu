@@ -735,6 +735,7 @@ __global__ void __launch_bounds__(256, 4) losses_kernel(const Args a, int block_
       const float l = float(logp);
       a.lse[t] = fault ? NAN : float(sum);
       a.row_logps[t] = l;
+      if (a.scales) a.weights[t] = expm1f(l);
       if (a.kind == kPreference) {
         a.terms[t] = logp;
       } else {
@@ -915,7 +916,10 @@ __global__ void __launch_bounds__(256) pairs_kernel(const Args a) {
 #pragma unroll
       for (int k = 0; k < 2; ++k)
         for (int64_t t = begin[k] + threadIdx.x; t < end[k]; t += 256)
-          if (a.rowpos[t] >= 0) a.scales[t] = -slopes[k] * d;
+          if (a.rowpos[t] >= 0) {
+            a.scales[t] = -slopes[k] * d;
+            if (!Forward) a.weights[t] = expm1f(a.row_logps[t]);
+          }
       // (sizes of floats are in the order of their bits)
       if (threadIdx.x < 2) atomicMax(&a.head->steepest, __float_as_uint(fabsf(slopes[threadIdx.x] * d)));
     }
@@ -943,13 +947,14 @@ __global__ void __launch_bounds__(256) pairs_kernel(const Args a) {
   if (threadIdx.x == 0) *a.reduced = float(a.reduction == ZERO_REDUCE_MEAN ? sum[0] / pairs : sum[0]);
 }
 
-// The rows' scales of a policy's backward call.
+// The rows' scales and weights of a policy's backward call.
 __global__ void __launch_bounds__(256) scales_kernel(const Args a) {
   let_next_start();
   wait_for_previous();
   const int64_t t = int64_t(blockIdx.x) * 256 + threadIdx.x;
-  if (t < a.T && a.rowpos[t] >= 0)
-    a.scales[t] = -a.slopes[t] * (a.reduction == ZERO_REDUCE_NONE && a.dloss ? a.dloss[t] : 1.0f);
+  if (t >= a.T || a.rowpos[t] < 0) return;
+  a.scales[t] = -a.slopes[t] * (a.reduction == ZERO_REDUCE_NONE && a.dloss ? a.dloss[t] : 1.0f);
+  a.weights[t] = expm1f(a.row_logps[t]);
 }
 
 }  // namespace

@@ -414,7 +414,6 @@ struct Row {
   float w, next_w;         // their weights (kGradient)
   float2 f;                // weights of the two terms (kGradient, with scale, lse and lse_kd)
   float scale, lse, lse_kd;
-  float gap;               // p - 1 of the label, of a loss by slopes
 };
 
 __device__ __forceinline__ void entry_ahead(const Args& a, const Unit& u, const Row& r, int e, int32_t& id, float& w) {
@@ -436,7 +435,6 @@ __device__ __forceinline__ Row row_of(const Args& a, int rows, const Unit& u, co
     if (CE) r.lse = a.lse[r.t];
     if (KD) r.lse_kd = a.lse_tau[r.t];
     r.scale = a.row_scale ? a.row_scale[r.t] : 1.0f;
-    if (CE && !KD && a.row_logps) r.gap = expm1f(a.row_logps[r.t]);
   }
   if (a.K == 0) {
     r.id = a.ids[r.t];
@@ -660,7 +658,7 @@ __device__ __forceinline__ void gradient_epilogue(const Args& a, const CUtensorM
       float label = 0.0f;
 #pragma unroll
       for (int j = 0; j < 32; ++j)
-        if (j == at) label = g[j] = CE && !KD && a.row_logps ? r.scale * r.gap : g[j] - d;
+        if (j == at) label = g[j] = CE && !KD && a.scales ? d : g[j] - d;  // (by slopes: d is s (p - 1))
       if (PLANES == 1 && PARTS == 1 && CE && !KD && a.left && at >= 0)
         a.left[r.i] = label - __bfloat162float(__float2bfloat16_rn(label));
     });
