@@ -168,6 +168,21 @@ def test_zeros_of_many_tokens(embedding, cuda, V, D, dt):
     check_gradient(got, ids[kept], dout[kept], V, 1.0)
 
 
+@pytest.mark.parametrize("T", [5, 33000])
+@pytest.mark.parametrize("kind", TYPES)
+def test_zeros_of_rows_without_gaps(embedding, cuda, kind, T):
+    """Rows off 16 bytes side by side are cleared as one array, from any address to any."""
+    g = torch.Generator().manual_seed(35)
+    for V, D in [(1, 1), (2, 1), (2, 3), (5, 7), (40, 37), (3000, 257)]:
+        ids = (torch.randint(V, (T,), generator=g) if V < 5 else torch.randint(2, V - 2, (T,), generator=g)).to(cuda)
+        dout = torch.randn(T, D, generator=g).to(TYPES[kind]).to(cuda)
+        nan = torch.full((V, D), math.nan, dtype=TYPES[kind], device=cuda)
+        for offset in range(9):
+            dw, _ = matrix(nan, 0, offset, "dweight")
+            embedding.embedding_backward(ids, dout, dweight=dw)
+            check_gradient(dw, ids, dout, V, 1.0, what=f"{V} {D} {offset}")
+
+
 @pytest.mark.parametrize("pad,offset", [(0, 1), (1, 0), (3, 5), (8, 0), (8, 8), (5, 3), (4, 4), (13, 0)])
 @pytest.mark.parametrize("kind", TYPES)
 def test_strides_and_alignment(embedding, cuda, kind, pad, offset):

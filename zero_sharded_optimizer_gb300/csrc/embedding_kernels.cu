@@ -192,13 +192,34 @@ __global__ void __launch_bounds__(256) lookup_kernel(const Args a) {
 
 constexpr int kClassThreads = 1024;
 
-template <bool F32, int Width>
-__device__ __forceinline__ void zero_rows(const Args& a, int64_t first, int64_t end, int64_t step) {
+// Rows `from` to `end` of dweight, by `warps` warps of which this is number `warp`.
+// `Array`: rows off 16 bytes without a gap between them are one array of 16-byte words
+// and an edge of less than one on either side (145 tokens of 100295 x 1729 in fp32: 118
+// us instead of 175, 8192 of 50257 x 769 in bf16 38 instead of 43; beside the passes of
+// a longer sort, 100000 of 50257 x 900 in bf16, 95 instead of 92, so not there).
+template <bool F32, int Width, bool Array>
+__device__ __forceinline__ void zero_rows(const Args& a, int64_t from, int64_t end, int64_t warp, int64_t warps) {
   using C = Columns<F32, Width>;
-  for (int64_t v = first; v < end; v += step) {
+  const int lane = threadIdx.x & 31;
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  if (Array && Width != 16 && a.out_stride == a.D) {
+    using E = typename C::E;
+    if (from >= end) return;
+    const auto begin = reinterpret_cast<uintptr_t>(row_of<F32>(a.out, a.D, from));
+    const auto stop = reinterpret_cast<uintptr_t>(row_of<F32>(a.out, a.D, end));
+    const uintptr_t first = (begin + 15) / 16 * 16, last = stop / 16 * 16;  // of the words
+    for (uintptr_t p = first + uintptr_t(warp * 32 + lane) * 16; p < last; p += uintptr_t(warps) * 512)
+      *reinterpret_cast<uint4*>(p) = zero;
+    if (warp == 0) {
+      const uintptr_t head = begin + lane * sizeof(E), tail = (first > last ? first : last) + lane * sizeof(E);
+      if (head < first && head < stop) *reinterpret_cast<E*>(head) = E(0.0f);
+      if (tail < stop) *reinterpret_cast<E*>(tail) = E(0.0f);
+    }
+    return;
+  }
+  for (int64_t v = from + warp; v < end; v += warps) {
     void* row = row_of<F32>(a.out, a.out_stride, v);
-    for (int64_t c0 = 0; c0 < a.D; c0 += C::kBlock)
-      C(c0, a.D, threadIdx.x & 31).store(row, make_uint4(0, 0, 0, 0));
+    for (int64_t c0 = 0; c0 < a.D; c0 += C::kBlock) C(c0, a.D, lane).store(row, zero);
   }
 }
 
@@ -232,8 +253,8 @@ __global__ void __launch_bounds__(kClassThreads) class_sort_kernel(const Args a)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int classes = 1 << a.class_bits, mine = blockIdx.x;
   if (mine >= classes) {
-    zero_rows<F32, Width>(a, a.zero_from + int64_t(mine - classes) * 32 + warp, a.V,
-                          int64_t(gridDim.x - classes) * 32);
+    zero_rows<F32, Width, true>(a, a.zero_from, a.V, int64_t(mine - classes) * 32 + warp,
+                                int64_t(gridDim.x - classes) * 32);
     return;
   }
   // Each warp's stretch of the tokens; an id that is not the class's becomes -1.
@@ -360,8 +381,8 @@ __global__ void __launch_bounds__(kSortThreads) place_kernel(const Args a, int p
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (int(blockIdx.x) >= a.tiles) {  // a pass's part of the zeros
     const int64_t part = (a.V - a.zero_from + a.passes - 1) / a.passes, from = a.zero_from + pass * part;
-    zero_rows<F32, Width>(a, from + int64_t(blockIdx.x - a.tiles) * kSortWarps + warp, min(a.V, from + part),
-                          int64_t(gridDim.x - a.tiles) * kSortWarps);
+    zero_rows<F32, Width, false>(a, from, min(a.V, from + part), int64_t(blockIdx.x - a.tiles) * kSortWarps + warp,
+                                 int64_t(gridDim.x - a.tiles) * kSortWarps);
     return;
   }
   const int bins = 1 << a.bits, shift = pass * a.bits;
