@@ -632,10 +632,11 @@ int zero_distill_step(const zero_head_loss_t *p, zero_stream_t stream);
  * A sequence without labelled rows has S = 0 (and S / n = 0); a pair of two such
  * is empty: its loss is 0 and the mean does not count it.
  *
- * The label's logit is summed a second time, in fp32 with rounding, and its part
- * of lse corrected, because these losses hang on small differences of
- * log-probabilities; the sums over a sequence and the losses are formed in
- * double. A few rows (which depends on sizes and type alone) are worked on in fp32
+ * The label's logit is summed a second time, in fp32 with rounding, and l_t taken as
+ * -log(1 + sum over the other columns of e^(z - z_y)), because these losses hang on
+ * small differences of log-probabilities: what l_t is off by is in proportion to
+ * the probability that the model leaves to the other columns. The sums over a
+ * sequence and the losses are formed in double. A few rows (which depends on sizes and type alone) are worked on in fp32
  * multiply-adds, with the T x V logits in the workspace and no wait that could run
  * out. Everything else -- arithmetic, equal bits, what a wait that runs out does --
  * is as stated above.

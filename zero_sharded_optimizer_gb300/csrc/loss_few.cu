@@ -198,11 +198,12 @@ __global__ void __launch_bounds__(256, 2) few_logits_kernel(const Args a, int wi
     for (int j = 0; j < 32; ++j) dot[j] = 0.0f;
     if (v < a.V && t >= 0) {
       a.z[logit_at(a, group, v, i)] = z;
-      if (y == v && a.forward) a.zent[t] = z;
-      const float m = __fmul_rn(z, kLog2e), top = fmaxf(sum.m, m), base = top == -INFINITY ? 0.0f : top;
-      sum.s = sum.s * exp2_even(sum.m == -INFINITY ? -INFINITY : sum.m - base) +
-              exp2_even(fmaf(z, kLog2eRest, fmaf(z, kLog2e, -base)));
-      sum.m = top;
+      if (y != v) {  // the statistics are those of the other columns
+        const float m = __fmul_rn(z, kLog2e), top = fmaxf(sum.m, m), base = top == -INFINITY ? 0.0f : top;
+        sum.s = sum.s * exp2_even(sum.m == -INFINITY ? -INFINITY : sum.m - base) +
+                exp2_even(fmaf(z, kLog2eRest, fmaf(z, kLog2e, -base)));
+        sum.m = top;
+      }
     }
   }
   if (!a.forward) return;

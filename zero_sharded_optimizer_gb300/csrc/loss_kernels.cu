@@ -512,11 +512,11 @@ __global__ void __launch_bounds__(256) dhidden_out_kernel(const Args a) {
 
 // ------------------------------------------------------------------- losses --
 
-// The row's log-sum-exp from its partial maxima and sums (maxima in powers of
-// two): each of the row's lanes takes every lanes-th partial, eight loads in
+// The row's maximum (in powers of two) and sum of exponentials from its partial
+// ones: each of the row's lanes takes every lanes-th partial, eight loads in
 // flight; the first lane joins them. `Even`: by exponentials without a mean error.
 template <bool Even>
-__device__ __forceinline__ double row_lse(const float2* stats, int64_t count, int64_t Tp, int64_t i, int lane,
+__device__ __forceinline__ float2 row_sum(const float2* stats, int64_t count, int64_t Tp, int64_t i, int lane,
                                           int lanes, float2* sh, int r, int rows) {
   const auto exp2_of = [](float x) { return Even ? exp2_even(x) : exp2f(x); };
   float m = -INFINITY, s = 0.0f;
@@ -562,8 +562,13 @@ __device__ __forceinline__ double row_lse(const float2* stats, int64_t count, in
     const float2 y = make_float2(__shfl_down_sync(~0u, x.x, w * rows), __shfl_down_sync(~0u, x.y, w * rows));
     if (lane < w) x = join(x, y);
   }
-  return lane == 0 ? (double(x.x) + log2(double(x.y))) * 0.69314718055994530942 : 0.0;
+  return x;
 }
+
+constexpr double kLn2 = 0.69314718055994530942;
+
+// The log-sum-exp of a row's joined statistics.
+__device__ __forceinline__ double lse_of(float2 x) { return (double(x.x) + log2(double(x.y))) * kLn2; }
 
 // The products of N rows' hidden states and their labels' weights in fp32, rounded
 // at every addition: a warp's lanes take every 32nd group of elements, all rows'
@@ -616,12 +621,9 @@ __device__ __forceinline__ void label_logits(const Args& a, const int64_t (&t)[N
   }
 }
 
-// log(1 + p (e^d - 1)) for a probability p = e^l: what a logit's change by d adds
-// to a log-sum-exp. d is a rounding error as a rule, where two terms of the
-// series leave out less than d^3.
-__device__ __forceinline__ double corrected(double d, float l) {
-  const double p = expf(l);
-  return fabs(d) < 0.001 ? p * d * (1.0 + 0.5 * (1.0 - p) * d) : log1p(p * expm1(d));
+// log(1 + s 2^e).
+__device__ __forceinline__ double log1p_of(double s, double e) {
+  return e > 512.0 ? (e + log2(s)) * kLn2 : log1p(s * exp2(e));
 }
 
 // The policy loss of a row and its slope by the log-probability l. What is not a
@@ -651,12 +653,15 @@ __device__ __forceinline__ void policy_loss(const Args& a, const PolicyRow& row,
 
 constexpr int kSlopeRows = 16;  // most rows of a block of losses_kernel that goes by slopes
 
-// What the matrix kernel's exponentials do to a log-sum-exp: they take logits times
-// log2(e) in fp32, that is logits kTaken times as large, and ex2.approx is low by
-// 4.8e-8 of itself on average (over [-16, 0]), once for each logit and again where a
-// half tile's sum is rescaled: by kMeanLow together (measured over 6000 rows of 4931
-// logits of one matrix instruction each, which nothing else rounds off one way).
-constexpr double kTaken = double(kLog2e) * 0.69314718055994530942, kMeanLow = 1.1e-7;
+// What the matrix kernel does to a sum of exponentials. It takes logits times log2(e)
+// in fp32: a maximum in powers of two is one of the logit by this factor. And ex2.approx
+// cuts its results off, that is takes half a step of 2^-23 on average, relative to a
+// value of [1, 2) whose logarithm is spread evenly 2^-24 / (2 ln 2) = 4.3e-8: from every
+// term once, and again where a half tile's sum is rescaled, which of its four stretches
+// of 32 columns the k-th finds 1/2 + ... + 1/4 of a time behind it: (1/2 + 2/3 + 3/4) / 4
+// = 0.48 times a term. (The joins of the half tiles have no mean error.)
+constexpr double kOfLogit = 1.0 / double(kLog2e);
+constexpr double kCutOff = 1.48 * 4.3e-8;
 
 // 256 threads: `block_rows` rows (a power of two, up to 32), 256 / block_rows lanes each.
 //
@@ -665,9 +670,12 @@ constexpr double kTaken = double(kLog2e) * 0.69314718055994530942, kMeanLow = 1.
 // a loss hangs on small differences of log-probabilities, and a preference loss
 // on sums of many, so what the tensor cores' truncating sums take from a large
 // logit of the label counts (up to 8e-6 at a logit of 9 and width 768, always of
-// one sign). The label's logit is therefore taken again in rounding fp32, and
-// its share of the log-sum-exp corrected: log(S + e^z' - e^z). (8192 rows of width
-// 768: 21 us, bound by latency: the statistics' columns, then two rows a warp.)
+// one sign). The label's logit z is therefore taken in rounding fp32, and the
+// statistics are those of the other columns: l = -log(1 + S e^-z), whose error is in
+// proportion to what the model leaves to the others. (With the label's exponential in
+// S, l and the label's p - 1 were off by S's last bits, up to 2e-7, however sure the
+// model was.) (8192 rows of width 768: 21 us, bound by latency: the statistics'
+// columns, then two rows a warp.)
 template <bool Slopes, bool F32>
 __global__ void __launch_bounds__(256, 4) losses_kernel(const Args a, int block_rows, bool vector) {
   __shared__ float2 sh[256];
@@ -709,15 +717,18 @@ __global__ void __launch_bounds__(256, 4) losses_kernel(const Args a, int block_
       __syncthreads();
     }
     double entries = 0.0;
+    if (!Slopes) {
 #pragma unroll 4
-    for (int e = lane; e < a.L; e += lanes) {
-      const int64_t at = t * a.L + e;
-      if (a.ids[at] != kNoId) entries += double(a.weights[at]) * double(a.zent[at]);
+      for (int e = lane; e < a.L; e += lanes) {
+        const int64_t at = t * a.L + e;
+        if (a.ids[at] != kNoId) entries += double(a.weights[at]) * double(a.zent[at]);
+      }
     }
-    const double lse = a.has_ce ? row_lse<Slopes>(a.stats, a.partials, a.Tp, i, lane, lanes, sh, r, block_rows) : 0.0;
-    const double lse_tau =
-        a.has_kd ? row_lse<Slopes>(a.stats_tau, a.partials, a.Tp, i, lane, lanes, sh, r, block_rows) : 0.0;
-    if (a.L > 1) {
+    const float2 none = make_float2(0.0f, 1.0f);
+    const float2 sum = a.has_ce ? row_sum<Slopes>(a.stats, a.partials, a.Tp, i, lane, lanes, sh, r, block_rows) : none;
+    const float2 sum_tau =
+        !Slopes && a.has_kd ? row_sum<false>(a.stats_tau, a.partials, a.Tp, i, lane, lanes, sh, r, block_rows) : none;
+    if (!Slopes && a.L > 1) {
       part[threadIdx.x] = entries;
       __syncthreads();
       for (int w = lanes / 2; w; w >>= 1) {
@@ -728,12 +739,16 @@ __global__ void __launch_bounds__(256, 4) losses_kernel(const Args a, int block_
     }
     const bool fault = a.head->fault;  // NaN in lse too: a backward call's gradients show it then
     if (Slopes && lane == 0 && i0 + r < rows) {
-      const double z = a.few ? entries : entries * kTaken, more = double(logit[r]) - z;
-      const bool finite = isfinite(more) && isfinite(lse);
-      const double sum = (finite ? lse + corrected(more, float(z - lse)) : lse) + (a.few ? 0.0 : kMeanLow);
-      const double logp = fault ? NAN : (finite ? double(logit[r]) : z) - sum;
+      const double z = logit[r], others = a.few ? sum.y : sum.y * (1.0 + kCutOff);
+      const double top = double(sum.x) * (a.few ? kLn2 : kOfLogit);
+      double more = log1p_of(others, (top - z) / kLn2), lse = z + more;
+      if (!isfinite(z)) {
+        lse = z < 0.0 ? top + log(others) : z;
+        more = lse - z;
+      }
+      const double logp = fault ? NAN : -more;
       const float l = float(logp);
-      a.lse[t] = fault ? NAN : float(sum);
+      a.lse[t] = fault ? NAN : float(lse);
       a.row_logps[t] = l;
       if (a.scales) a.weights[t] = expm1f(l);
       if (a.kind == kPreference) {
@@ -749,6 +764,7 @@ __global__ void __launch_bounds__(256, 4) losses_kernel(const Args a, int block_
       }
     } else if (!Slopes && lane == 0 && i0 + r < rows) {
       const float2 f = a.coef[t];
+      const double lse = lse_of(sum), lse_tau = lse_of(sum_tau);
       double loss = double(a.konst[t]);
       if (f.x != 0.0f) loss += double(f.x) * lse;
       if (f.y != 0.0f) loss += double(f.y) * a.tau * lse_tau;

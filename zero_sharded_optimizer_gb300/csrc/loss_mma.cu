@@ -508,7 +508,8 @@ __device__ __forceinline__ void add_exponentials(const float (&z)[32], float top
 // The power of tau that add_exponentials and the gradient use, 0 for none.
 __device__ __forceinline__ int shared_power(float tau) { return tau == 1.0f ? 1 : tau == 2.0f ? 2 : tau == 4.0f ? 4 : 0; }
 
-// 32 columns of a row into its statistics, and the logits of the entries among them.
+// 32 columns of a row into its statistics, and the logits of the entries among them
+// (a loss by slopes: all but the label's column, see losses_kernel).
 template <bool CE, bool KD>
 __device__ __forceinline__ void forward_columns(const Args& a, const Unit& u, Row& r, int64_t v, int valid, int p,
                                                 float (&z)[32], float& top, Sums& s) {
@@ -519,6 +520,12 @@ __device__ __forceinline__ void forward_columns(const Args& a, const Unit& u, Ro
       if (j >= valid) z[j] = -INFINITY;
   }
   each_entry(a, u, r, v, [&](int at) {
+    if (a.kind >= kPolicy) {  // the statistics are those of the other columns
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        if (j == at) z[j] = -INFINITY;
+      return;
+    }
     float x = 0.0f;
 #pragma unroll
     for (int j = 0; j < 32; ++j)
