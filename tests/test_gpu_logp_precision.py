@@ -66,3 +66,19 @@ def test_sure_rows_are_off_in_proportion_to_what_is_left(losses, cuda, kind, T):
     assert bool(((got.logps.double() - exact).abs() <= 1.01 * off).all())
     off = others * (4 * r["dz"] + 2.0 ** -20 + 2.0 ** -23 * (r["lse"].abs() + V) + (2.0 ** -8 if kind == "bf16" else 0.0))
     assert bool((got.dhidden[:, 0].double().abs() <= 1.01 * off).all())
+
+
+@pytest.mark.parametrize("top", [2 ** 33 + 1024 * 5, 2 ** 33 + 1024 * 8, 2 ** 33 + 1024 * 34])
+@pytest.mark.parametrize("T", [1, 3, 16])
+def test_logits_beyond_a_billion(losses, cuda, T, top):
+    """Few rows of fp32, whose logits are whole numbers that fp32 holds, 2^20 apart: nothing but the largest counts, and
+    every difference is exact. (Times log2(e) they are off by up to 512 in fp32: no exponent.)"""
+    V = 40
+    z = top - 2.0 ** 20 * torch.arange(V, dtype=torch.float64)
+    assert torch.equal(z.float().double(), z)
+    w, h = torch.zeros(V, 4), torch.zeros(T, 4)
+    w[:, 0], h[:, 0] = z.float() * 2.0 ** -20, 2.0 ** 20
+    y = torch.arange(T) * 2 % V
+    got = policy_logps(losses, h.to(cuda), w.to(cuda), y.to(cuda))
+    assert torch.equal(got.logps.cpu().double(), z[y] - top)
+    assert bool((got.lse == float(top)).all())

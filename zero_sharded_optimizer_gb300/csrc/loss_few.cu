@@ -110,12 +110,17 @@ __device__ __forceinline__ int64_t logit_at(const Args& a, int group, int64_t v,
   return (int64_t(group) * a.V + v) * kGroup + i;
 }
 
-// A running maximum (in powers of two) and sum of exponentials.
+// e^d for d <= 0.
+__device__ __forceinline__ float exp_even(float d) { return exp2_even(fmaf(d, kLog2e, d * kLog2eRest)); }
+
+// A running maximum and sum of exponentials. (Of differences of logits: a logit times
+// log2(e), taken from a rounded maximum of such, would leave its rounding in the
+// exponent, which for logits beyond 1e9 goes past fp32's range.)
 struct Sum {
   float m = -INFINITY, s = 0.0f;
   __device__ __forceinline__ void join(float m2, float s2) {
     const float top = fmaxf(m, m2);
-    s = top == -INFINITY ? s + s2 : s * exp2_even(m - top) + s2 * exp2_even(m2 - top);
+    s = top == -INFINITY ? s + s2 : s * exp_even(m - top) + s2 * exp_even(m2 - top);
     m = top;
   }
 };
@@ -198,12 +203,7 @@ __global__ void __launch_bounds__(256, 2) few_logits_kernel(const Args a, int wi
     for (int j = 0; j < 32; ++j) dot[j] = 0.0f;
     if (v < a.V && t >= 0) {
       a.z[logit_at(a, group, v, i)] = z;
-      if (y != v) {  // the statistics are those of the other columns
-        const float m = __fmul_rn(z, kLog2e), top = fmaxf(sum.m, m), base = top == -INFINITY ? 0.0f : top;
-        sum.s = sum.s * exp2_even(sum.m == -INFINITY ? -INFINITY : sum.m - base) +
-                exp2_even(fmaf(z, kLog2eRest, fmaf(z, kLog2e, -base)));
-        sum.m = top;
-      }
+      if (y != v) sum.join(z, 1.0f);  // the statistics are those of the other columns
     }
   }
   if (!a.forward) return;

@@ -512,13 +512,13 @@ __global__ void __launch_bounds__(256) dhidden_out_kernel(const Args a) {
 
 // ------------------------------------------------------------------- losses --
 
-// The row's maximum (in powers of two) and sum of exponentials from its partial
-// ones: each of the row's lanes takes every lanes-th partial, eight loads in
-// flight; the first lane joins them. `Even`: by exponentials without a mean error.
+// The row's maximum (in powers of two, or of 2^unit) and sum of exponentials from
+// its partial ones: each of the row's lanes takes every lanes-th partial, eight loads
+// in flight; the first lane joins them. `Even`: by exponentials without a mean error.
 template <bool Even>
-__device__ __forceinline__ float2 row_sum(const float2* stats, int64_t count, int64_t Tp, int64_t i, int lane,
-                                          int lanes, float2* sh, int r, int rows) {
-  const auto exp2_of = [](float x) { return Even ? exp2_even(x) : exp2f(x); };
+__device__ __forceinline__ float2 row_sum(const float2* stats, float unit, int64_t count, int64_t Tp, int64_t i,
+                                          int lane, int lanes, float2* sh, int r, int rows) {
+  const auto exp2_of = [&](float x) { return Even ? exp2_even(x * unit) : exp2f(x); };
   float m = -INFINITY, s = 0.0f;
   for (int64_t j0 = lane; j0 < count; j0 += 8 * lanes) {
     float2 x[8];
@@ -725,9 +725,10 @@ __global__ void __launch_bounds__(256, 4) losses_kernel(const Args a, int block_
       }
     }
     const float2 none = make_float2(0.0f, 1.0f);
-    const float2 sum = a.has_ce ? row_sum<Slopes>(a.stats, a.partials, a.Tp, i, lane, lanes, sh, r, block_rows) : none;
-    const float2 sum_tau =
-        !Slopes && a.has_kd ? row_sum<false>(a.stats_tau, a.partials, a.Tp, i, lane, lanes, sh, r, block_rows) : none;
+    const float2 sum = a.has_ce ? row_sum<Slopes>(a.stats, a.few ? kLog2e : 1.0f, a.partials, a.Tp, i, lane, lanes,
+                                                  sh, r, block_rows) : none;
+    const float2 sum_tau = !Slopes && a.has_kd ? row_sum<false>(a.stats_tau, 1.0f, a.partials, a.Tp, i, lane, lanes,
+                                                                sh, r, block_rows) : none;
     if (!Slopes && a.L > 1) {
       part[threadIdx.x] = entries;
       __syncthreads();
@@ -740,7 +741,7 @@ __global__ void __launch_bounds__(256, 4) losses_kernel(const Args a, int block_
     const bool fault = a.head->fault;  // NaN in lse too: a backward call's gradients show it then
     if (Slopes && lane == 0 && i0 + r < rows) {
       const double z = logit[r], others = a.few ? sum.y : sum.y * (1.0 + kCutOff);
-      const double top = double(sum.x) * (a.few ? kLn2 : kOfLogit);
+      const double top = a.few ? double(sum.x) : double(sum.x) * kOfLogit;
       double more = log1p_of(others, (top - z) / kLn2), lse = z + more;
       if (!isfinite(z)) {
         lse = z < 0.0 ? top + log(others) : z;
