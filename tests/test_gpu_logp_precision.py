@@ -82,3 +82,18 @@ def test_logits_beyond_a_billion(losses, cuda, T, top):
     got = policy_logps(losses, h.to(cuda), w.to(cuda), y.to(cuda))
     assert torch.equal(got.logps.cpu().double(), z[y] - top)
     assert bool((got.lse == float(top)).all())
+
+
+@pytest.mark.parametrize("T", [3, 20, 300])
+@pytest.mark.parametrize("kind", TYPES)
+def test_rows_without_a_slope_beside_an_infinite_factor(losses, cuda, kind, T):
+    """The gradient of the reduced loss is infinite: rows that have no part in it stay at zero."""
+    dt, g = TYPES[kind], torch.Generator().manual_seed(T)
+    h, w = torch.randn(T, 64, generator=g).to(dt).to(cuda), torch.randn(500, 64, generator=g).to(dt).to(cuda)
+    y, adv = torch.arange(T, device=cuda), torch.ones(T, device=cuda)
+    adv[::3] = 0.0
+    old = policy_logps(losses, h, w, y).logps
+    for factor in (math.inf, math.nan):
+        got = losses.policy_step(h, w, y, old, adv, dloss=torch.tensor(factor, device=cuda))
+        assert not got.dhidden[::3].any()
+        assert not got.dhidden[1::3].isfinite().any() and not got.dhidden[2::3].isfinite().any()

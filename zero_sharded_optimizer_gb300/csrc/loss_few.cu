@@ -387,7 +387,6 @@ __device__ __forceinline__ void hidden_part(const Args& a, int part, int64_t d0,
 #pragma unroll
   for (int i = 0; i < R; ++i) {
     if (i >= count) break;
-    const bool sloped = __shfl_sync(~0u, row.scale, i) != 0.0f;
     __syncthreads();
 #pragma unroll
     for (int j = 0; j < W; ++j) sums[(warp * 32 + lane) * W + j] = sum[i][j];
@@ -396,7 +395,7 @@ __device__ __forceinline__ void hidden_part(const Args& a, int part, int64_t d0,
       float x = 0.0f;
 #pragma unroll
       for (int q = 0; q < 8; ++q) x += sums[q * 32 * W + n];
-      if (d0 + n < a.Dp) a.dh[(int64_t(part) * a.Tp + group * kGroup + i) * a.Dp + d0 + n] = sloped ? x : 0.0f;
+      if (d0 + n < a.Dp) a.dh[(int64_t(part) * a.Tp + group * kGroup + i) * a.Dp + d0 + n] = x;
     }
   }
 }

@@ -450,7 +450,8 @@ __global__ void __launch_bounds__(256) dhidden_out_kernel(const Args a) {
   const int64_t stretches = (wide + kGroups - 1) / kGroups;  // of a row
   for (int64_t b = blockIdx.x; b < a.T * stretches; b += gridDim.x) {
     const int64_t t = b / stretches, d = (b % stretches * kGroups + group) * 4;
-    const int32_t i = a.rowpos[t];
+    int32_t i = a.rowpos[t];
+    if (a.few && i >= 0 && a.scales[t] == 0.0f) i = -2;  // without a slope; few rows are not numbered again
     float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (i >= 0 && d < a.D) {
 #pragma unroll 8
