@@ -635,8 +635,9 @@ int zero_distill_step(const zero_head_loss_t *p, zero_stream_t stream);
  * The label's logit is summed a second time, in fp32 with rounding, and l_t taken as
  * -log(1 + sum over the other columns of e^(z - z_y)), because these losses hang on
  * small differences of log-probabilities: what l_t is off by is in proportion to
- * the probability that the model leaves to the other columns. The sums over a
- * sequence and the losses are formed in double. A few rows (which depends on sizes and type alone) are worked on in fp32
+ * the probability that the model leaves to the other columns. Of these the largest
+ * logit is summed again too. The sums over a sequence and the losses are formed in
+ * double. A few rows (which depends on sizes and type alone) are worked on in fp32
  * multiply-adds, with the T x V logits in the workspace and no wait that could run
  * out. Everything else -- arithmetic, equal bits, what a wait that runs out does --
  * is as stated above.

@@ -97,3 +97,45 @@ def test_rows_without_a_slope_beside_an_infinite_factor(losses, cuda, kind, T):
         got = losses.policy_step(h, w, y, old, adv, dloss=torch.tensor(factor, device=cuda))
         assert not got.dhidden[::3].any()
         assert not got.dhidden[1::3].isfinite().any() and not got.dhidden[2::3].isfinite().any()
+
+
+def favoured(T, V, D, dt, favour, other, g, device):
+    """Hidden states that favour a token by `favour`: their label, or another one."""
+    w = torch.randn(V, D, generator=g) * 0.6 / math.sqrt(D)
+    y, f = torch.randint(V, (T,), generator=g), torch.randint(V, (T,), generator=g)
+    h = torch.randn(T, D, generator=g) + favour / 0.36 * w[f if other else y]
+    return h.to(dt).to(device), w.to(dt).to(device), y.to(device)
+
+
+def exact_logps(h, w, y):
+    out = []
+    for a in range(0, len(y), 1024):
+        z = h[a:a + 1024].double() @ w.double().T
+        out.append(z.gather(1, y[a:a + 1024, None])[:, 0] - torch.logsumexp(z, 1))
+    return torch.cat(out)
+
+
+@pytest.mark.parametrize("favour,other", [(0.0, False), (9.0, False), (14.0, False), (9.0, True), (14.0, True)])
+@pytest.mark.parametrize("few", [False, True])
+@pytest.mark.parametrize("kind", TYPES)
+def test_errors_of_one_sign(losses, cuda, kind, few, favour, other):
+    """Over thousands of rows the mean error is what the arithmetic loses one way, and the loss and the sums
+    over a sequence have all of it. What rounds, evens out: l of 8 to 16 is rounded by steps of 2^-20, 2.8e-7 as
+    rms; two logits of size 14 are sums of 3 rounded products each in 256 chains and 8 halvings, of a partial
+    sum's step 2^-20 at most: sqrt(8) 2.8e-7 would be all of them at the largest, and most are far below. 1e-6
+    holds them together. What does not even out: sums on the tensor cores, cut off at each of 24 instructions of
+    a segment, half a step of 2^-24 of a partial sum: 8e-6 at a logit of 14. That is corrected for the label and for the
+    largest logit beside it; what is left is that of the other columns, whose logits are 5 at most and
+    share their mass: 24 2^-25 of 2.5 as a mean, 1.8e-6, were all of it there, and a tenth of that
+    for the logits around 0 to 2 that have most of the mass. 2.5e-7 holds it, and 1e-7 of chance for 200 rows."""
+    dt, g = TYPES[kind], torch.Generator().manual_seed(int(favour) + 2 * other)
+    T, V, D, calls = 6000, 5000, 768, 1
+    if few:
+        T, calls = (16 if kind == "fp32" else 4), 50
+    off = []
+    for _ in range(calls):
+        h, w, y = favoured(T, V, D, dt, favour, other, g, cuda)
+        off.append(policy_logps(losses, h, w, y).logps.double() - exact_logps(h, w, y))
+    off = torch.cat(off)
+    assert abs(float(off.mean())) < (3.5e-7 if few and kind == "bf16" else 2.5e-7)
+    assert float(off.square().mean().sqrt()) < 1e-6

@@ -392,6 +392,7 @@ int plan(const Problem& problem, int pass, Args* a, __nv_bfloat16** packed_weigh
   a->zent = w.take<float>(a->T, a->L);
   if (problem.preference) a->terms = w.take<double>(a->T);
   if (a->has_ce) a->stats = w.take<float2>(a->partials, a->Tp);
+  if (problem.slopes() && !a->few) a->places = w.take<uint8_t>(a->partials, a->Tp);
   if (a->has_kd) a->stats_tau = w.take<float2>(a->partials, a->Tp);
   int64_t most = w.at;
   if (pass & kBackward) {

@@ -123,8 +123,10 @@ struct Args {
   int64_t tiles;          // vocabulary tiles
   int64_t partials;       // of a row's statistics: 2 tiles, or the few rows' blocks
   float2* stats;          // [partials][Tp] some columns' (half a tile's) (m, sum of 2^(z log2(e) - m));
-                          // a loss by slopes: of the columns but the label's; few rows: (m, sum of e^(z - m))
+                          // a loss by slopes: of the columns but the label's, and the largest logit z' in m's
+                          // place, which is z' log2(e), rounded; few rows: (z', sum of e^(z - z'))
   float2* stats_tau;      // [partials][Tp] of z / tau
+  uint8_t* places;        // [partials][Tp] a loss by slopes: which of the half tile's columns z' is in
   float* z;               // [groups][V][kFewGroup] the logits, for few rows
   int32_t* counters;      // [2] units handed out, forward and backward
   uint32_t* never;        // stays zero

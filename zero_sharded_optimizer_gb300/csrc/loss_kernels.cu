@@ -513,41 +513,53 @@ __global__ void __launch_bounds__(256) dhidden_out_kernel(const Args a) {
 
 // ------------------------------------------------------------------- losses --
 
-// The row's maximum (in powers of two, or of 2^unit) and sum of exponentials from
-// its partial ones: each of the row's lanes takes every lanes-th partial, eight loads
-// in flight; the first lane joins them. `Even`: by exponentials without a mean error.
-template <bool Even>
-__device__ __forceinline__ float2 row_sum(const float2* stats, float unit, int64_t count, int64_t Tp, int64_t i,
-                                          int lane, int lanes, float2* sh, int r, int rows) {
-  const auto exp2_of = [&](float x) { return Even ? exp2_even(x * unit) : exp2f(x); };
+// A row's maximum (in powers of two) and sum of exponentials; `Slopes`: and which
+// partial has the maximum.
+template <bool Slopes>
+struct RowSum {
   float m = -INFINITY, s = 0.0f;
+  int32_t best = 0;
+};
+
+// The same from the partial ones: each of the row's lanes takes every lanes-th, eight
+// loads in flight; the first lane joins them. `Slopes`: by exponentials without a mean
+// error, of maxima that are logits, in powers of two (mma) or as they are (few rows).
+template <bool Slopes>
+__device__ __forceinline__ RowSum<Slopes> row_sum(const float2* stats, bool few, int64_t count, int64_t Tp, int64_t i,
+                                                  int lane, int lanes, RowSum<Slopes>* sh, int r, int rows) {
+  const float unit = few ? kLog2e : 1.0f;
+  const auto exp2_of = [&](float x) { return Slopes ? exp2_even(x * unit) : exp2f(x); };
+  RowSum<Slopes> x;
   for (int64_t j0 = lane; j0 < count; j0 += 8 * lanes) {
-    float2 x[8];
-    float top = m;
+    float2 p[8];
+    float top = x.m;
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
-      x[q] = j0 + lanes * q < count ? stats[(j0 + lanes * q) * Tp + i] : make_float2(-INFINITY, 0.0f);
-      top = fmaxf(top, x[q].x);
+      p[q] = j0 + lanes * q < count ? stats[(j0 + lanes * q) * Tp + i] : make_float2(-INFINITY, 0.0f);
+      if (Slopes && !few) p[q].x = __fmul_rn(p[q].x, kLog2e);
+      if (Slopes && p[q].x > top) x.best = int32_t(j0 + lanes * q);
+      top = fmaxf(top, p[q].x);
     }
     if (top == -INFINITY) {
       // Nothing yet -- unless a partial is NaN (fmaxf passes it over).
 #pragma unroll
-      for (int q = 0; q < 8; ++q) s += x[q].y;
+      for (int q = 0; q < 8; ++q) x.s += p[q].y;
       continue;
     }
-    s = m == -INFINITY ? s : s * exp2_of(m - top);
+    x.s = x.m == -INFINITY ? x.s : x.s * exp2_of(x.m - top);
 #pragma unroll
-    for (int q = 0; q < 8; ++q) s += x[q].y * exp2_of(x[q].x - top);  // 0 where x is -inf
-    m = top;
+    for (int q = 0; q < 8; ++q) x.s += p[q].y * exp2_of(p[q].x - top);  // 0 where x is -inf
+    x.m = top;
   }
   // A tree over the lanes, in a fixed order: between warps through shared memory,
   // then (row r's lanes are `rows` threads apart) within the first.
-  const auto join = [&](float2 x, float2 y) {
-    const float top = fmaxf(x.x, y.x);
-    const float sum = top == -INFINITY ? x.y + y.y : x.y * exp2_of(x.x - top) + y.y * exp2_of(y.x - top);
-    return make_float2(top, sum);
+  const auto join = [&](const RowSum<Slopes>& x, const RowSum<Slopes>& y) {
+    RowSum<Slopes> z;
+    z.m = fmaxf(x.m, y.m);
+    z.s = z.m == -INFINITY ? x.s + y.s : x.s * exp2_of(x.m - z.m) + y.s * exp2_of(y.m - z.m);
+    if (Slopes) z.best = y.m > x.m ? y.best : x.best;
+    return z;
   };
-  float2 x = make_float2(m, s);
   int w = lanes / 2;
   if (w * rows >= 32) {
     sh[lane * rows + r] = x;
@@ -560,7 +572,10 @@ __device__ __forceinline__ float2 row_sum(const float2* stats, float unit, int64
     __syncthreads();
   }
   for (; w; w >>= 1) {
-    const float2 y = make_float2(__shfl_down_sync(~0u, x.x, w * rows), __shfl_down_sync(~0u, x.y, w * rows));
+    RowSum<Slopes> y;
+    y.m = __shfl_down_sync(~0u, x.m, w * rows);
+    y.s = __shfl_down_sync(~0u, x.s, w * rows);
+    if (Slopes) y.best = __shfl_down_sync(~0u, x.best, w * rows);
     if (lane < w) x = join(x, y);
   }
   return x;
@@ -569,13 +584,13 @@ __device__ __forceinline__ float2 row_sum(const float2* stats, float unit, int64
 constexpr double kLn2 = 0.69314718055994530942;
 
 // The log-sum-exp of a row's joined statistics.
-__device__ __forceinline__ double lse_of(float2 x) { return (double(x.x) + log2(double(x.y))) * kLn2; }
+__device__ __forceinline__ double lse_of(RowSum<false> x) { return (double(x.m) + log2(double(x.s))) * kLn2; }
 
-// The products of N rows' hidden states and their labels' weights in fp32, rounded
+// The products of N rows' hidden states t and one row y each of the weight in fp32, rounded
 // at every addition: a warp's lanes take every 32nd group of elements, all rows'
-// loads in flight together. Rows t (and labels y) below zero are left out.
+// loads in flight together. Rows t below zero are left out.
 template <bool F32, int N>
-__device__ __forceinline__ void label_logits(const Args& a, const int64_t (&t)[N], const int32_t (&y)[N], bool vector,
+__device__ __forceinline__ void column_logits(const Args& a, const int64_t (&t)[N], const int32_t (&y)[N], bool vector,
                                              int lane, float (&logit)[N]) {
   using E = typename std::conditional<F32, float, __nv_bfloat16>::type;
   constexpr int kWide = F32 ? 4 : 8;
@@ -675,14 +690,18 @@ constexpr double kCutOff = 1.48 * 4.3e-8;
 // statistics are those of the other columns: l = -log(1 + S e^-z), whose error is in
 // proportion to what the model leaves to the others. (With the label's exponential in
 // S, l and the label's p - 1 were off by S's last bits, up to 2e-7, however sure the
-// model was.) (8192 rows of width 768: 21 us, bound by latency: the statistics'
-// columns, then two rows a warp.)
+// model was.) Of the others the one with the largest logit is taken again likewise and
+// corrected in S, most of which it is where the model expects it: 6000 rows of width
+// 768 with a logit of 14 beside their label were 5.6e-6 too large on average, and are
+// 8e-8 too small. (8192 rows of width 768: 31 us, 21 without that, bound by latency:
+// twice two rows a warp, and between them the statistics' columns.)
 template <bool Slopes, bool F32>
 __global__ void __launch_bounds__(256, 4) losses_kernel(const Args a, int block_rows, bool vector) {
-  __shared__ float2 sh[256];
+  __shared__ RowSum<Slopes> sh[256];
   __shared__ double part[256];
   constexpr int kLogits = kSlopeRows / 8;
-  __shared__ float logit[kSlopeRows];
+  __shared__ float logit[kSlopeRows], largest[kSlopeRows];
+  __shared__ int32_t column[kSlopeRows];
   __shared__ bool last;
   let_next_start();
   wait_for_previous();
@@ -699,8 +718,9 @@ __global__ void __launch_bounds__(256, 4) losses_kernel(const Args a, int block_
       if (a.kl_weight != 0.0) row.ref_logp = a.ref_logps[t];
       if (a.scales && a.reduction == ZERO_REDUCE_NONE && a.dloss) row.dloss = a.dloss[t];
     }
-    if (Slopes) {
-      // The block's warps take the rows in turn, each up to kLogits.
+    // One logit of each row, of its label or its column: the block's warps take the rows
+    // in turn, each up to kLogits.
+    const auto logits = [&](bool label, float* to) {
       int64_t u[kLogits];
       int32_t y[kLogits];
       float z[kLogits];
@@ -710,13 +730,14 @@ __global__ void __launch_bounds__(256, 4) losses_kernel(const Args a, int block_
         u[n] = q < block_rows && i0 + q < rows ? a.rowmap[i0 + q] : -1;
       }
 #pragma unroll
-      for (int n = 0; n < kLogits; ++n) y[n] = u[n] >= 0 ? a.ids[u[n]] : 0;
-      if (u[0] >= 0) label_logits<F32, kLogits>(a, u, y, vector, threadIdx.x & 31, z);
+      for (int n = 0; n < kLogits; ++n) y[n] = u[n] < 0 ? 0 : label ? a.ids[u[n]] : column[(threadIdx.x >> 5) + 8 * n];
+      if (u[0] >= 0) column_logits<F32, kLogits>(a, u, y, vector, threadIdx.x & 31, z);
 #pragma unroll
       for (int n = 0; n < kLogits; ++n)
-        if ((threadIdx.x & 31) == 0 && u[n] >= 0) logit[(threadIdx.x >> 5) + 8 * n] = z[n];
+        if ((threadIdx.x & 31) == 0 && u[n] >= 0) to[(threadIdx.x >> 5) + 8 * n] = z[n];
       __syncthreads();
-    }
+    };
+    if (Slopes) logits(true, logit);
     double entries = 0.0;
     if (!Slopes) {
 #pragma unroll 4
@@ -725,11 +746,21 @@ __global__ void __launch_bounds__(256, 4) losses_kernel(const Args a, int block_
         if (a.ids[at] != kNoId) entries += double(a.weights[at]) * double(a.zent[at]);
       }
     }
-    const float2 none = make_float2(0.0f, 1.0f);
-    const float2 sum = a.has_ce ? row_sum<Slopes>(a.stats, a.few ? kLog2e : 1.0f, a.partials, a.Tp, i, lane, lanes,
-                                                  sh, r, block_rows) : none;
-    const float2 sum_tau = !Slopes && a.has_kd ? row_sum<false>(a.stats_tau, 1.0f, a.partials, a.Tp, i, lane, lanes,
-                                                                sh, r, block_rows) : none;
+    RowSum<Slopes> sum;
+    RowSum<false> sum_tau;
+    if (a.has_ce) sum = row_sum<Slopes>(a.stats, a.few, a.partials, a.Tp, i, lane, lanes, sh, r, block_rows);
+    if constexpr (!Slopes)
+      if (a.has_kd) sum_tau = row_sum<false>(a.stats_tau, false, a.partials, a.Tp, i, lane, lanes, sh, r, block_rows);
+    float seen = 0.0f;  // the largest logit, as the matrix kernel has it
+    if (Slopes && !a.few) {
+      if (lane == 0) {
+        const int64_t at = sum.best * a.Tp + i;
+        seen = a.stats[at].x;
+        column[r] = int32_t(min(int64_t(sum.best) * (kTileN / 2) + a.places[at], a.V - 1));
+      }
+      __syncthreads();
+      logits(false, largest);
+    }
     if (!Slopes && a.L > 1) {
       part[threadIdx.x] = entries;
       __syncthreads();
@@ -741,8 +772,13 @@ __global__ void __launch_bounds__(256, 4) losses_kernel(const Args a, int block_
     }
     const bool fault = a.head->fault;  // NaN in lse too: a backward call's gradients show it then
     if (Slopes && lane == 0 && i0 + r < rows) {
-      const double z = logit[r], others = a.few ? sum.y : sum.y * (1.0 + kCutOff);
-      const double top = a.few ? double(sum.x) : double(sum.x) * kOfLogit;
+      const double z = logit[r], top = a.few ? double(sum.m) : double(sum.m) * kOfLogit;
+      double others = sum.s;
+      if (!a.few) {
+        const double off = double(largest[r]) - double(seen);  // small: e^off - 1 by two terms
+        others *= 1.0 + kCutOff;
+        if (fabs(off) < 0.001) others += off + 0.5 * off * off;
+      }
       double more = log1p_of(others, (top - z) / kLn2), lse = z + more;
       if (!isfinite(z)) {
         lse = z < 0.0 ? top + log(others) : z;
@@ -766,7 +802,11 @@ __global__ void __launch_bounds__(256, 4) losses_kernel(const Args a, int block_
       }
     } else if (!Slopes && lane == 0 && i0 + r < rows) {
       const float2 f = a.coef[t];
-      const double lse = lse_of(sum), lse_tau = lse_of(sum_tau);
+      double lse = 0.0, lse_tau = 0.0;
+      if constexpr (!Slopes) {
+        if (a.has_ce) lse = lse_of(sum);
+        if (a.has_kd) lse_tau = lse_of(sum_tau);
+      }
       double loss = double(a.konst[t]);
       if (f.x != 0.0f) loss += double(f.x) * lse;
       if (f.y != 0.0f) loss += double(f.y) * a.tau * lse_tau;
