@@ -139,3 +139,25 @@ def test_errors_of_one_sign(losses, cuda, kind, few, favour, other):
     off = torch.cat(off)
     assert abs(float(off.mean())) < (3.5e-7 if few and kind == "bf16" else 2.5e-7)
     assert float(off.square().mean().sqrt()) < 1e-6
+
+
+@pytest.mark.parametrize("other", [False, True])
+@pytest.mark.parametrize("T", [16, 100, 600])
+def test_gradients_of_rows_that_expect_a_token(losses, cuda, T, other):
+    """fp32: the rows of dhidden beside 64 bits, as means over the rows. Sums on the tensor cores are cut off at
+    each of a segment's 32 instructions, half a step of 2^-24 of a partial sum: 1e-6 of a sum of one sign; slopes
+    and probabilities are off by 2^-22 of themselves each, 2.4e-7. 2.5e-6 holds twice that."""
+    V, D, g = 5000, 768, torch.Generator().manual_seed(T + other)
+    h, w, y = favoured(T, V, D, torch.float32, 14.0, other, g, cuda)
+    z = h.double() @ w.double().T
+    l = torch.log_softmax(z, 1)
+    ly = l.gather(1, y[:, None])[:, 0]
+    G = torch.exp(l)
+    G[torch.arange(T), y] = torch.expm1(ly)
+    if not other:       # what a sure row leaves to the others, without the cancellation
+        G[torch.arange(T), y] = -G.scatter(1, y[:, None], 0.0).sum(1)
+    old = ly.float()
+    want = G * torch.exp(ly - old.double())[:, None] @ w.double()
+    got = losses.policy_step(h, w, y, old, torch.ones(T, device=cuda), clip=0.5, reduction="sum")
+    off = (got.dhidden.double() - want).norm(dim=1) / want.norm(dim=1)
+    assert float(off.mean()) < 2.5e-6

@@ -773,11 +773,11 @@ __global__ void __launch_bounds__(256, 4) losses_kernel(const Args a, int block_
     const bool fault = a.head->fault;  // NaN in lse too: a backward call's gradients show it then
     if (Slopes && lane == 0 && i0 + r < rows) {
       const double z = logit[r], top = a.few ? double(sum.m) : double(sum.m) * kOfLogit;
-      double others = sum.s;
+      double others = sum.s, added = 0.0;
       if (!a.few) {
         const double off = double(largest[r]) - double(seen);  // small: e^off - 1 by two terms
-        others *= 1.0 + kCutOff;
-        if (fabs(off) < 0.001) others += off + 0.5 * off * off;
+        if (fabs(off) < 0.001) added = off + 0.5 * off * off;
+        others = others * (1.0 + kCutOff) + added;
       }
       double more = log1p_of(others, (top - z) / kLn2), lse = z + more;
       if (!isfinite(z)) {
@@ -785,10 +785,14 @@ __global__ void __launch_bounds__(256, 4) losses_kernel(const Args a, int block_
         more = lse - z;
       }
       const double logp = fault ? NAN : -more;
-      const float l = float(logp);
+      const float l = float(logp), gap = expm1f(l);
+      // The backward pass forms the matrix kernel's logits again: their lse, without what
+      // was added to the largest (with it, fp32 gradients of rows that expect another token
+      // are 5e-6 off, as the largest probability is then).
+      if (added != 0.0) lse += double(gap) * added / others;
       a.lse[t] = fault ? NAN : float(lse);
       a.row_logps[t] = l;
-      if (a.scales) a.weights[t] = expm1f(l);
+      if (a.scales) a.weights[t] = gap;
       if (a.kind == kPreference) {
         a.terms[t] = logp;
       } else {
