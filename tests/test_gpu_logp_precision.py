@@ -7,8 +7,8 @@ import math
 import pytest
 import torch
 
-from logp_util import policy
-from test_gpu_losses import TYPES
+from logp_util import IGNORE, policy
+from test_gpu_losses import TYPES, empty_matrix, gaps_untouched, matrix
 
 pytestmark = pytest.mark.gpu
 
@@ -161,3 +161,102 @@ def test_gradients_of_rows_that_expect_a_token(losses, cuda, T, other):
     got = losses.policy_step(h, w, y, old, torch.ones(T, device=cuda), clip=0.5, reduction="sum")
     off = (got.dhidden.double() - want).norm(dim=1) / want.norm(dim=1)
     assert float(off.mean()) < 2.5e-6
+
+
+def labelled(T, V, D, labels, g, device):
+    """bf16 rows that favour their labels, a tenth without one."""
+    w = torch.randn(V, D, generator=g) * 0.6 / math.sqrt(D)
+    y = {"any": lambda: torch.randint(V, (T,), generator=g), "one": lambda: torch.full((T,), V // 3),
+         "frequent": lambda: (torch.rand(T, generator=g) * math.log(V)).exp().long().sub_(1).clamp_(0, V - 1)}[labels]()
+    h = torch.randn(T, D, generator=g) + 10.0 * torch.rand(T, 1, generator=g) * w[y]
+    y[torch.rand(T, generator=g) < 0.1] = IGNORE
+    return h.bfloat16().to(device), w.bfloat16().to(device), y.to(device)
+
+
+def exact_gradients(h, w, y, slope):
+    """Of the sum of slopes times log-probabilities, in 64 bits, a block of rows at a time."""
+    dh, dw = torch.zeros(h.shape, dtype=torch.float64, device=h.device), torch.zeros(w.shape, dtype=torch.float64, device=h.device)
+    for a in range(0, len(y), 2048):
+        k = a + torch.nonzero(slope[a:a + 2048]).squeeze(1)
+        G = torch.softmax(h[k].double() @ w.double().T, 1).neg_()
+        G[torch.arange(len(k)), y[k]] += 1.0
+        G *= slope[k, None]
+        dh[k] = G @ w.double()
+        dw += G.T @ h[k].double()
+    return dh, dw
+
+
+def as_near_as_rounded(got, want, what):
+    """Off by little more than what the result's own rounding makes it, in 2-norm."""
+    own = (want.bfloat16().double() - want).norm()
+    assert float((got.double() - want).norm()) <= 1.05 * float(own), what
+
+
+@pytest.mark.parametrize("T,V,D,labels", [
+    (300, 2000, 72, "any"), (500, 3000, 70, "one"), (512, 3000, 264, "frequent"), (513, 3000, 64, "frequent"), (1000, 6000, 97, "frequent"), (3000, 5000, 256, "frequent"), (3000, 5000, 64, "one"),
+    (2100, 300001, 16, "frequent"), (33000, 3000, 40, "frequent"), (40000, 1500, 33, "any")])
+@pytest.mark.parametrize("op", ["policy", "preference"])
+def test_bf16_gradients_are_as_near_as_their_rounding(losses, cuda, op, T, V, D, labels):
+    """More than 256 rows, whose G is bf16. The labels' entries, which are most of both gradients, get their rounding
+    back, so what is left of G's is that of entries p of columns that are not the label's: the rows' other
+    99.9 % of columns, each off by 2^-9 of a p that is a thousandth of 1 - p, and many together where a row has
+    no more than that. 5 % holds them (with the labels' rounding: 20 to 45 %)."""
+    g = torch.Generator().manual_seed(T + V)
+    h, w, y = labelled(T, V, D, labels, g, cuda)
+    l = exact_logps(h, w, torch.where(y >= 0, y, 0))
+    if op == "policy":
+        adv = torch.randn(T, generator=g).to(cuda)
+        adv[torch.arange(T, device=cuda) % 5 == 0] = 0.0
+        old = l.float()
+        slope = torch.where(y >= 0, -adv.double() * torch.exp(l - old.double()), 0.0)
+
+        def step(h, w, **more):
+            return losses.policy_step(h, w, y, old, adv, clip=0.5, reduction="sum", **more)
+    else:
+        cuts = [0, T // 5, T // 2, T - 7, T]
+        offsets = torch.tensor(cuts, device=cuda)
+        S = torch.stack([torch.where(y >= 0, l, 0.0)[a:b].sum() for a, b in zip(cuts, cuts[1:])])
+        ref = S.float()
+        u = 0.1 * ((S[:2] - S[2:]) - (ref[:2].double() - ref[2:].double()))
+        du = -0.1 / (1.0 + torch.exp(u))
+        per = torch.cat([du, -du])
+        slope = torch.where(y >= 0, torch.repeat_interleave(per, offsets.diff()), 0.0)
+
+        def step(h, w, **more):
+            return losses.preference_step(h, w, y, offsets, ref_logps=ref, reduction="sum", **more)
+    dh, dw = exact_gradients(h, w, y, slope)
+    got = step(h, w)
+    as_near_as_rounded(got.dhidden, dh, "dhidden")
+    as_near_as_rounded(got.dweight, dw, "dweight")
+    # rows off 16 bytes, and without dhidden, where the labels' sums need a place of their own
+    for pad in (0, 1, 3):
+        to, buf = empty_matrix(V, D, torch.bfloat16, cuda, pad)
+        dh_to, dh_buf = empty_matrix(T, D, torch.bfloat16, cuda, pad)
+        step(matrix(h, cuda, pad), matrix(w, cuda, pad), dhidden=dh_to, dweight=to)
+        as_near_as_rounded(to, dw, f"dweight {pad}")
+        as_near_as_rounded(dh_to, dh, f"dhidden {pad}")
+        gaps_untouched(buf, V, D, pad)
+        gaps_untouched(dh_buf, T, D, pad)
+        to.fill_(math.nan)
+        step(matrix(h, cuda, pad), matrix(w, cuda, pad), dhidden=False, dweight=to)
+        as_near_as_rounded(to, dw, f"dweight alone {pad}")
+        before = torch.randn(V, D, generator=g).bfloat16().to(cuda) * dw.abs().max().float().bfloat16()
+        to.copy_(before)
+        step(matrix(h, cuda, pad), matrix(w, cuda, pad), dweight=to, accumulate=True)
+        as_near_as_rounded(to, before.double() + dw, f"dweight added {pad}")
+    only = step(h, w, dweight=False)
+    as_near_as_rounded(only.dhidden, dh, "dhidden alone")
+
+
+def test_labels_sums_with_rows_that_are_not_numbers(losses, cuda):
+    """Rows without a slope, and without a label, bring nothing into the labels' sums."""
+    T, V, D, g = 700, 900, 64, torch.Generator().manual_seed(5)
+    h, w, y = labelled(T, V, D, "frequent", g, cuda)
+    adv = torch.randn(T, generator=g).to(cuda)
+    old = exact_logps(h, w, torch.where(y >= 0, y, 0)).float()
+    adv[::3] = 0.0
+    good = losses.policy_step(h, w, y, old, adv, reduction="sum")
+    bad = h.clone()
+    bad[::3], bad[y < 0] = math.nan, math.inf
+    got = losses.policy_step(bad, w, y, old, adv, reduction="sum")
+    assert torch.equal(got.dweight, good.dweight) and torch.equal(got.dhidden, good.dhidden)

@@ -65,46 +65,21 @@ void common(const zero_embedding_t* p, const void* table, int64_t table_stride, 
   a->table_stride = table_stride;
   a->out = out;
   a->out_stride = out_stride;
-  const int es = elem_size(p->precision);
-  const uintptr_t all = reinterpret_cast<uintptr_t>(table) | uintptr_t(table_stride * es) |
-                        reinterpret_cast<uintptr_t>(out) | uintptr_t(out_stride * es);
-  a->width = all % 16 == 0 ? 16 : all % 4 == 0 && p->D * es % 4 == 0 ? 4 : es;
+  a->width = ze::width_of(*a, elem_size(p->precision));
 }
 
 // The gradient's arrays in the workspace.
 int plan(const zero_embedding_t* p, Args* a, int64_t* bytes) {
   common(p, p->dout, p->dout_stride, p->dweight, p->dweight_stride, a);
   a->accumulate = p->accumulate != 0;
-  a->few = p->T <= ze::kFewTokens && (p->V <= ze::kFewIds || p->T == 0);
-  // A class's ids in a block's shared memory, and no more blocks than SMs if they fit.
-  a->class_bits = p->V <= int64_t(ze::kClassIds) << 7 ? 7 : ze::kMostClassBits;
+  Layout w{static_cast<uint8_t*>(p->workspace)};
+  ze::plan_sums(a, &w);
   // Zeros that the sort, which leaves memory idle, has the time to write: all rows
   // from zero_from on, whatever tokens there are. (131072 tokens of GPT-2-small's
   // table: 86.5 us with 64 MB of them, 93 with 1 MB or 88 with 128; few tokens, where
   // most rows stay zero: 8192 tokens 29 us with all, 41 with 32 MB.)
   const int64_t rows = a->few ? p->V : kZeroBytes / (p->D * elem_size(p->precision));
   a->zero_from = a->accumulate ? p->V : std::max<int64_t>(p->V - rows, 0);
-  // The fewest digits, of equal width, that hold the ids and V itself.
-  int bits = 1;
-  while (p->V >> bits) ++bits;
-  a->passes = (bits + ze::kMostBits - 1) / ze::kMostBits;
-  a->bits = (bits + a->passes - 1) / a->passes;
-  const int64_t least = 1024;
-  a->tile = std::max(least, round_up((p->T + ze::kMostTiles - 1) / ze::kMostTiles, 512));
-  a->tiles = int32_t((p->T + a->tile - 1) / a->tile);
-  const int64_t block = p->precision == ZERO_FP32 ? 128 : 256;
-  a->blocks = int32_t((p->D + block - 1) / block);
-  a->Dp = a->blocks * block;
-  // Long runs mean few shares of segments to be written, read and joined (131072
-  // tokens of width 4096: 400 us, 448 with runs of 32), short ones work for all SMs.
-  a->run = 128;
-  while (a->run > 8 && (p->T + a->run - 1) / a->run * a->blocks < ze::kSms * 32) a->run /= 2;
-  a->runs = (p->T + a->run - 1) / a->run;
-  Layout w{static_cast<uint8_t*>(p->workspace)};
-  a->counts = w.take<int32_t>(int64_t(a->passes) * a->tiles << a->bits);
-  for (auto& l : a->list) l = w.take<ze::Entry>(p->T);
-  a->sorted = a->list[a->few ? 0 : (a->passes - 1) & 1];
-  a->part = w.take<float>(2 * a->runs, a->Dp);
   if (!w.fits) return set_error(ZERO_EINVAL, "the problem's workspace overflows 64 bits");
   *bytes = w.at;
   return ZERO_OK;
@@ -116,6 +91,38 @@ int launched(cudaError_t e, const char* what) {
 }
 
 }  // namespace
+
+int32_t ze::width_of(const Args& a, int es) {
+  const uintptr_t all = reinterpret_cast<uintptr_t>(a.table) | uintptr_t(a.table_stride * es) |
+                        reinterpret_cast<uintptr_t>(a.out) | uintptr_t(a.out_stride * es);
+  return all % 16 == 0 ? 16 : all % 4 == 0 && a.D * es % 4 == 0 ? 4 : es;
+}
+
+void ze::plan_sums(Args* a, Layout* w) {
+  a->few = a->T <= kFewTokens && (a->V <= kFewIds || a->T == 0);
+  // A class's ids in a block's shared memory, and no more blocks than SMs if they fit.
+  a->class_bits = a->V <= int64_t(kClassIds) << 7 ? 7 : kMostClassBits;
+  // The fewest digits, of equal width, that hold the ids and V itself.
+  int bits = 1;
+  while (a->V >> bits) ++bits;
+  a->passes = (bits + kMostBits - 1) / kMostBits;
+  a->bits = (bits + a->passes - 1) / a->passes;
+  const int64_t least = 1024;
+  a->tile = std::max(least, round_up((a->T + kMostTiles - 1) / kMostTiles, 512));
+  a->tiles = int32_t((a->T + a->tile - 1) / a->tile);
+  const int64_t block = a->f32 ? 128 : 256;
+  a->blocks = int32_t((a->D + block - 1) / block);
+  a->Dp = a->blocks * block;
+  // Long runs mean few shares of segments to be written, read and joined (131072
+  // tokens of width 4096: 400 us, 448 with runs of 32), short ones work for all SMs.
+  a->run = 128;
+  while (a->run > 8 && (a->T + a->run - 1) / a->run * a->blocks < kSms * 32) a->run /= 2;
+  a->runs = (a->T + a->run - 1) / a->run;
+  a->counts = w->take<int32_t>(int64_t(a->passes) * a->tiles << a->bits);
+  for (auto& l : a->list) l = w->take<Entry>(a->T);
+  a->sorted = a->list[a->few ? 0 : (a->passes - 1) & 1];
+  a->part = w->take<float>(2 * a->runs, a->Dp);
+}
 
 extern "C" {
 

@@ -2,9 +2,11 @@
 // and its kernels (embedding_kernels.cu). Not part of the public C ABI.
 #pragma once
 
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "host_checks.h"
 #include "zero_gb300.h"
 
 namespace ze {
@@ -58,10 +60,36 @@ struct Args {
   const Entry* sorted;     // the one that the last pass writes
   float* part;             // [runs][2][Dp] a run's share of the segment that began before it, and of
                            // the one that it began and did not end
+
+  // The sums of the vocabulary losses' rests (loss_kernels.cu): a token's row counts
+  // rest_of(scales[t], weights[t]) times, and an id's sum goes to the row of `out` that
+  // its slot says.
+  const float *scales, *weights;
+  const uint2* slots;
 };
+
+#ifdef __CUDACC__
+// Of 32 ids: which have a slot, and how many slots are before theirs. Slots are in order of id.
+__device__ __forceinline__ int32_t slot_of(uint2 slots, int id) {
+  return slots.x >> id & 1 ? int32_t(slots.y + __popc(slots.x & ((1u << id) - 1))) : -1;
+}
+
+// What the rounding of a label's entry of G to bf16 leaves of it (its weight may be anything
+// where its row has no scale).
+__device__ __forceinline__ float rest_of(float scale, float weight) {
+  const float x = scale == 0.0f ? 0.0f : scale * weight;
+  return x - __bfloat162float(__float2bfloat16_rn(x));
+}
+#endif
+
+// The widest accesses that the rows of table and out allow, of elements of `es` bytes.
+int32_t width_of(const Args& a, int es);
+// Sets the sort's and the sums' plan for the problem that `a` has, and takes their arrays.
+void plan_sums(Args* a, zl::Layout* w);
 
 cudaError_t launch_lookup(const Args& a, cudaStream_t s);
 cudaError_t launch_sort(const Args& a, cudaStream_t s);
 cudaError_t launch_sums(const Args& a, cudaStream_t s);
+cudaError_t launch_rests(const Args& a, cudaStream_t s);
 
 }  // namespace ze

@@ -462,13 +462,15 @@ __global__ void __launch_bounds__(kSortThreads) place_kernel(const Args a, int p
 
 constexpr uint32_t kNone = 0xffffffffu;  // no key: above V
 
-// A segment's sum to its row of dweight, rounded once.
-template <bool F32, int Width>
+// A segment's sum to its row of dweight, rounded once. `Rests`: to its slot's.
+template <bool F32, int Width, bool Rests>
 __device__ __forceinline__ void finish(const Args& a, const Columns<F32, Width>& c, uint32_t id,
                                        const float (&sum)[Columns<F32, Width>::kVec]) {
   using C = Columns<F32, Width>;
   if (c.count == 0) return;
-  void* row = row_of<F32>(a.out, a.out_stride, id);
+  const int64_t to = Rests ? slot_of(a.slots[id / 32], id % 32) : int64_t(id);
+  if (Rests && to < 0) return;
+  void* row = row_of<F32>(a.out, a.out_stride, to);
   float x[C::kVec];
   if (a.accumulate) {
     C::unpack(c.load(row), x);
@@ -526,8 +528,10 @@ __device__ __forceinline__ void zero_absent_rows(const Args& a, int64_t v0) {
 
 // A warp for 32 ids whose rows may have to become zero -- the long pieces of work
 // first -- and one for each run and block of columns, with eight rows on their way at
-// a time, as they are stored: 80 registers, three blocks an SM.
-template <bool F32, int Width>
+// a time, as they are stored: 80 registers, three blocks an SM. `Rests`: each row
+// counts a number of times that is the token's own, and rows that count none are not
+// read.
+template <bool F32, int Width, bool Rests = false>
 __global__ void __launch_bounds__(256, 3) sum_kernel(const Args a, int64_t zero_warps) {
   using C = Columns<F32, Width>;
   constexpr int kVec = C::kVec, kAhead = 8;
@@ -552,26 +556,31 @@ __global__ void __launch_bounds__(256, 3) sum_kernel(const Args a, int64_t zero_
       const Entry e = lane < held ? list[first + s0 + lane] : Entry{kNone, 0};
       const uint32_t next = first + s0 + held < a.T ? list[first + s0 + held].id : kNone;
       const int n = __popc(__ballot_sync(~0u, e.id < a.V));  // those without a row come last
+      const float rest = Rests && lane < n ? rest_of(a.scales[e.t], a.weights[e.t]) : 0.0f;
       if (s0 == 0) begun = __shfl_sync(~0u, e.id, 0) != prev;
       for (int i0 = 0; i0 < n; i0 += kAhead) {
         uint4 w[kAhead];
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
           const uint32_t t = __shfl_sync(~0u, e.t, (i0 + i) & 31);
-          if (i0 + i < n) w[i] = c.template load<true>(row_of<F32>(a.table, a.table_stride, t));
+          const bool counts = !Rests || __shfl_sync(~0u, rest, (i0 + i) & 31) != 0.0f;  // (also a NaN)
+          if (i0 + i < n && counts) w[i] = c.template load<true>(row_of<F32>(a.table, a.table_stride, t));
         }
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
           const uint32_t id = __shfl_sync(~0u, e.id, (i0 + i) & 31);
           const uint32_t following = __shfl_sync(~0u, e.id, (i0 + i + 1) & 31);
           if (i0 + i >= n) break;
-          float x[kVec];
-          C::unpack(w[i], x);
+          const float times = Rests ? __shfl_sync(~0u, rest, (i0 + i) & 31) : 1.0f;
+          if (times != 0.0f) {
+            float x[kVec];
+            C::unpack(w[i], x);
 #pragma unroll
-          for (int j = 0; j < kVec; ++j) sum[j] += x[j];
+            for (int j = 0; j < kVec; ++j) sum[j] = Rests ? fmaf(times, x[j], sum[j]) : sum[j] + x[j];
+          }
           const bool ends = (i0 + i + 1 == held ? next : following) != id;
           const bool last = s0 + i0 + i + 1 == count;
-          if (ends && begun) finish(a, c, id, sum);
+          if (ends && begun) finish<F32, Width, Rests>(a, c, id, sum);
           else if (ends || last) put_share(share<kVec>(a, run, begun ? 1 : 0, block, lane), sum);
           if (ends) {
             begun = true;
@@ -591,7 +600,7 @@ __global__ void __launch_bounds__(256, 3) sum_kernel(const Args a, int64_t zero_
 // stretch of the shares in order, and the stretches in order. (A block has
 // neighbouring runs, of which few begin a long segment, not the columns of one:
 // 131072 tokens of width 4096 15 us instead of 97.)
-template <bool F32, int Width>
+template <bool F32, int Width, bool Rests = false>
 __global__ void __launch_bounds__(256) join_kernel(const Args a) {
   using C = Columns<F32, Width>;
   constexpr int kVec = C::kVec, kShort = 8;
@@ -631,7 +640,7 @@ __global__ void __launch_bounds__(256) join_kernel(const Args a) {
       add_share<kVec>(share<kVec>(a, run, 1, block, lane), sum);
 #pragma unroll 4
       for (int64_t r = run + 1; r < end; ++r) add_share<kVec>(share<kVec>(a, r, 0, block, lane), sum);
-      finish(a, C(block * C::kBlock, a.D, lane), id, sum);
+      finish<F32, Width, Rests>(a, C(block * C::kBlock, a.D, lane), id, sum);
     }
     if (lane == 0) {
       long_run[warp] = together ? run : -1;
@@ -654,7 +663,7 @@ __global__ void __launch_bounds__(256) join_kernel(const Args a) {
         for (int j = 0; j < kVec; ++j) sum[j] = 0.0f;
 #pragma unroll
         for (int w = 0; w < 8; ++w) add_share<kVec>(&parts[w][lane * kVec / 4], sum);
-        finish(a, C(b * C::kBlock, a.D, lane), id, sum);
+        finish<F32, Width, Rests>(a, C(b * C::kBlock, a.D, lane), id, sum);
       }
       __syncthreads();
     }
@@ -696,14 +705,14 @@ cudaError_t sort(const Args& a, cudaStream_t s) {
   return e;
 }
 
-template <bool F32, int Width>
+template <bool F32, int Width, bool Rests = false>
 cudaError_t sums(const Args& a, cudaStream_t s) {
   if (a.T == 0) return cudaSuccess;
-  const int64_t zero_warps = a.accumulate ? 0 : (a.zero_from + 31) / 32;
-  cudaError_t e = launch(sum_kernel<F32, Width>, blocks_of(a.runs * a.blocks + zero_warps), 256, 0, s, true, a,
+  const int64_t zero_warps = a.accumulate || Rests ? 0 : (a.zero_from + 31) / 32;
+  cudaError_t e = launch(sum_kernel<F32, Width, Rests>, blocks_of(a.runs * a.blocks + zero_warps), 256, 0, s, true, a,
                          zero_warps);
   if (e == cudaSuccess && a.runs > 1)
-    e = launch(join_kernel<F32, Width>, blocks_of((a.runs - 1) * a.blocks), 256, 0, s, true, a);
+    e = launch(join_kernel<F32, Width, Rests>, blocks_of((a.runs - 1) * a.blocks), 256, 0, s, true, a);
   return e;
 }
 
@@ -728,6 +737,11 @@ cudaError_t launch_sort(const Args& a, cudaStream_t s) {
 cudaError_t launch_sums(const Args& a, cudaStream_t s) {
   if (a.f32) return a.width == 16 ? sums<true, 16>(a, s) : sums<true, 4>(a, s);
   return a.width == 16 ? sums<false, 16>(a, s) : a.width == 4 ? sums<false, 4>(a, s) : sums<false, 2>(a, s);
+}
+
+// (Of bf16 rows; fp32's are never cut down to bf16.)
+cudaError_t launch_rests(const Args& a, cudaStream_t s) {
+  return a.width == 16 ? sums<false, 16, true>(a, s) : a.width == 4 ? sums<false, 4, true>(a, s) : sums<false, 2, true>(a, s);
 }
 
 }  // namespace ze

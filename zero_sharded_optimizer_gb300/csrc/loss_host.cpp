@@ -6,6 +6,7 @@
 #include <cmath>
 #include <cstdint>
 
+#include "embedding_internal.h"
 #include "host_checks.h"
 #include "loss_internal.h"
 
@@ -35,7 +36,8 @@ constexpr int64_t kPieceBytes = int64_t(40) << 20;
 // G; with two it is 1.00 times. The second part costs 3 to 22 % of a step while
 // a row tile's products wait for the weight anyway, but 21 to 33 % at 512 rows
 // and 34 to 49 % at 1000 (widths 768 and 2048, vocabularies 50257 and 32000),
-// where many rows' errors even out.
+// where many rows' errors even out. (The policy and the preference loss get back what
+// one part loses where it counts: see `rests` below.)
 constexpr int64_t kFineRows = 256;
 
 // A wait inside the matrix kernel gives up after this long; under normal running
@@ -245,7 +247,30 @@ bool few_rows(const zero_head_loss_t* p) {
   return p->T <= (f32 ? 16 : 4) || (p->T <= (f32 ? 64 : 32) && work <= (f32 ? 2e8 : 1e8));
 }
 
-int plan(const Problem& problem, int pass, Args* a, __nv_bfloat16** packed_weight, int64_t* bytes) {
+// The sums of the rests: the embedding's gradient of the labels, whose rows are the hidden
+// states, each as many times as its rest is.
+ze::Args rests_of(const Args& a, Layout* w) {
+  ze::Args r{};
+  r.T = a.T;
+  r.V = a.V;
+  r.D = a.D;
+  r.ids = a.labels;
+  r.padding_id = a.ignore_index;
+  r.scale = 1.0f;
+  r.table = a.hidden;
+  r.table_stride = a.hidden_stride;
+  r.out = a.rest_rows;
+  r.out_stride = a.rest_stride;
+  r.width = ze::width_of(r, 2);
+  r.zero_from = a.V;  // none
+  r.scales = a.scales;
+  r.weights = a.weights;
+  r.slots = a.slots;
+  ze::plan_sums(&r, w);
+  return r;
+}
+
+int plan(const Problem& problem, int pass, Args* a, __nv_bfloat16** packed_weight, ze::Args* rests, int64_t* bytes) {
   const zero_head_loss_t* p = problem.p;
   const bool distill = problem.distill();
   *a = Args{};
@@ -332,10 +357,12 @@ int plan(const Problem& problem, int pass, Args* a, __nv_bfloat16** packed_weigh
   a->weights = w.take<float>(a->T, a->L);
   if (a->K) a->starts = w.take<uint16_t>(2 * a->tiles + 1, a->T);
   if (problem.slopes() && (pass & kBackward)) a->row_scale = a->scales = w.take<float>(a->T);
-  // G in one bf16 part: dhidden hangs on the label's entry, whose rounding it
-  // gets back at the end (8192 rows of GPT-2-small's head: 1.41 times as far
-  // from the exact one as its own rounding makes it without, 1.00 with).
-  if (a->scales && a->parts == 1 && !a->few) a->left = w.take<float>(a->Tp);
+  // G in one bf16 part: both gradients hang on the labels' entries, whose rounding
+  // they get back: dhidden at the end, dweight from sums over each label's rows, taken
+  // before the products. (8192 rows of GPT-2-small's head: without, dhidden is 1.41 and
+  // dweight 1.2 to 1.46 times as far from the exact ones as their own rounding makes
+  // them, with them 1.00 times; the sums take 27 us of a step of 1515.)
+  a->rests = a->scales && a->parts == 1 && !a->few;
   if (!a->few) a->hp = w.take<__nv_bfloat16>(a->Tp * a->planes, a->Dp);
   if (a->few) {
     *packed_weight = nullptr;
@@ -380,12 +407,14 @@ int plan(const Problem& problem, int pass, Args* a, __nv_bfloat16** packed_weigh
   }
   // The words that begin as zero.
   const int64_t tiles = pass & kBackward && !a->few ? a->splits * (a->Tp / zl::kTileM) * ((a->D + 255) / 256) : 0;
-  a->zeros = 3 + 2 * pieces + tiles;
+  const int64_t slots = a->rests && p->dweight ? (p->V + 31) / 32 : 0, before = 3 + 2 * pieces + tiles;
+  a->zeros = round_up(before, 2) + 2 * slots;
   a->counters = w.take<int32_t>(a->zeros);
   a->never = reinterpret_cast<uint32_t*>(a->counters + 2);
   a->formed = a->never + 1;
   a->used = a->formed + pieces;
   a->added = a->used + pieces;
+  if (slots) a->slots = reinterpret_cast<uint2*>(a->counters + round_up(before, 2));
   // The forward pass's arrays and the backward pass's lie over one another.
   const int64_t common = w.at;
   a->sums = w.take<double>(zl::kLossBlocks);
@@ -400,7 +429,16 @@ int plan(const Problem& problem, int pass, Args* a, __nv_bfloat16** packed_weigh
     for (int b = 0; b < zl::kBuffers && !a->few; ++b)
       a->g[b] = b < pieces ? w.take<__nv_bfloat16>(a->Tp * a->parts, a->piece) : a->g[0];
     if (p->dhidden) a->dh = w.take<float>(a->splits * a->Tp, a->Dp);
+    if (slots) {
+      a->rest_rows = p->dhidden ? static_cast<__nv_bfloat16*>(p->dhidden) : w.take<__nv_bfloat16>(p->T, a->Dp);
+      a->rest_stride = p->dhidden ? p->dhidden_stride : a->Dp;
+    }
     most = std::max(most, w.at);
+    if (slots && p->T > zl::kRestRows) {  // over the products' arrays, before them
+      w.at = common;
+      *rests = rests_of(*a, &w);
+      most = std::max(most, w.at);
+    }
   }
   // The matrix kernel numbers its tiles in 32 bits.
   const double row_tiles = double((a->Tp + zl::kTileM - 1) / zl::kTileM), wide_tiles = double((a->D + 255) / 256);
@@ -474,11 +512,12 @@ int workspace_bytes(const Problem& problem, int64_t* bytes) {
   if (int e = check_sizes(problem)) return e;
   Args a;
   __nv_bfloat16* packed;
+  ze::Args rests;
   zero_head_loss_t q = *problem.p;
   q.workspace = nullptr;
   Problem without = problem;
   without.p = &q;
-  return plan(without, kForward | (q.dhidden || q.dweight ? kBackward : 0), &a, &packed, bytes);
+  return plan(without, kForward | (q.dhidden || q.dweight ? kBackward : 0), &a, &packed, &rests, bytes);
 }
 
 int run(const Problem& problem, int pass, cudaStream_t s) {
@@ -491,8 +530,9 @@ int run(const Problem& problem, int pass, cudaStream_t s) {
     return set_error(ZERO_EALIGN, "the workspace is not aligned to 256 bytes");
   Args a;
   __nv_bfloat16* packed;
+  ze::Args rests;
   int64_t bytes = 0;
-  if (int e = plan(problem, pass, &a, &packed, &bytes)) return e;
+  if (int e = plan(problem, pass, &a, &packed, &rests, &bytes)) return e;
   if (!p->workspace || p->workspace_bytes < bytes)
     return set_error(ZERO_EINVAL, "the workspace has %lld bytes, %lld are needed",
                      (long long)(p->workspace ? p->workspace_bytes : 0), (long long)bytes);
@@ -541,6 +581,12 @@ int run(const Problem& problem, int pass, cudaStream_t s) {
     program.forward = 0;
     program.counter = a.counters + 1;
     program.withheld = withheld.passes & kBackward ? a.never : nullptr;
+    if (a.slots && a.T <= zl::kRestRows) {
+      next("the rests", [&] { return zl::launch_rests(a, s); });
+    } else if (a.slots) {
+      next("the labels", [&] { return ze::launch_sort(rests, s); });
+      next("the rests", [&] { return ze::launch_rests(rests, s); });
+    }
     next("the gradients", [&] {
       return a.few ? zl::launch_few_gradients(a, s) : zl::launch_products(a, program, device, sms, s);
     });

@@ -26,6 +26,7 @@ constexpr int kSms = 152;        // GB300's multiprocessors. (The layout is plan
 constexpr int kBuffers = 3;      // of G
 constexpr int kLossBlocks = 608; // most blocks of the losses' kernel
 constexpr int kFewGroup = 8;     // few rows are worked on in groups of these
+constexpr int kRestRows = 512;   // most rows whose labels' sums are taken without sorting the labels
 constexpr int kFewHiddenBytes = 160 << 10;  // most shared memory for a group's hidden states
 
 // Which loss a call takes.
@@ -113,7 +114,11 @@ struct Args {
                           // slopes: p - 1 of the label, from its log-probability, for the gradient
   uint16_t* starts;       // distillation: [2 tiles + 1][T] first entry of each half tile
   float* scales;          // [T] row_scale of a call that goes by slopes
-  float* left;            // [Tp] what G's one bf16 value leaves of the label's entry, or NULL
+  int32_t rests;          // G is one bf16 value, and what that leaves of the labels' entries (ze::rest_of of
+                          // scale and weight) is put back
+  uint2* slots;           // [V / 32] with `rests` and dweight: where the labels' rows of `rest_rows` are
+  __nv_bfloat16* rest_rows;    // what the rests add to the rows of dweight that are labels', less the common
+  int64_t rest_stride;         // factor: in dhidden, which is written last, or in the workspace
   double* terms;          // [T] a preference call's labels' log-probabilities in double
   double* sums;           // [kLossBlocks] parts of the reduced loss
   float* zent;            // [T][L] logits of the entries
@@ -172,6 +177,8 @@ cudaError_t launch_pairs(const Args& a, cudaStream_t s);
 cudaError_t launch_scales(const Args& a, cudaStream_t s);
 // Numbers the rows that have a slope.
 cudaError_t launch_sloped_rows(const Args& a, cudaStream_t s);
+// The labels' sums of the rests, for up to kRestRows rows.
+cudaError_t launch_rests(const Args& a, cudaStream_t s);
 // dhidden from its sums; a call whose waits ran out is marked.
 cudaError_t launch_dhidden_out(const Args& a, cudaStream_t s);
 // The mark alone, where there is no dhidden to write.

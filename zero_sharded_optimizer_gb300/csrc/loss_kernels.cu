@@ -4,6 +4,7 @@
 
 #include <type_traits>
 
+#include "embedding_internal.h"
 #include "loss_device.cuh"
 
 namespace zl {
@@ -293,7 +294,7 @@ enum Numbering { kTargets, kPrepare, kSlopes };
 // One block: numbers the rows in order, up to 16 times 1024 rows at a time.
 template <Numbering N>
 __global__ void __launch_bounds__(1024) number_rows_kernel(const Args a) {
-  __shared__ int32_t before[16][32], total[16];
+  __shared__ int32_t before[16][32], total[16], total_of[32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   let_next_start();
   if (N != kPrepare) wait_for_previous();
@@ -360,10 +361,36 @@ __global__ void __launch_bounds__(1024) number_rows_kernel(const Args a) {
         const int32_t i = base + before[q][warp] + __popc(mask[q] & ((1u << lane) - 1));
         a.rowpos[t] = i;
         a.rowmap[i] = int32_t(t);
+        if (N == kSlopes && a.slots) atomicOr(&a.slots[a.ids[t] / 32].x, 1u << a.ids[t] % 32);
       }
       base += total[q];
     }
     __syncthreads();
+  }
+  if (N == kSlopes && a.slots) {  // the labels in order of id, before each 32 of them
+    __threadfence();
+    __syncthreads();
+    const int64_t words = (a.V + 31) / 32;
+    int32_t first = 0;
+    for (int64_t w0 = 0; w0 < words; w0 += 1024) {
+      const int64_t w = w0 + threadIdx.x;
+      const int32_t mine = w < words ? __popc(__ldcg(&a.slots[w].x)) : 0;
+      int32_t upto = mine;
+      for (int o = 1; o < 32; o *= 2) {
+        const int32_t x = __shfl_up_sync(~0u, upto, o);
+        if (lane >= o) upto += x;
+      }
+      if (lane == 31) total_of[warp] = upto;
+      __syncthreads();
+      int32_t all = 0;
+      for (int q = 0; q < 32; ++q) {
+        if (q < warp) upto += total_of[q];
+        all += total_of[q];
+      }
+      if (w < words) a.slots[w].y = uint32_t(first + upto - mine);
+      first += all;
+      __syncthreads();
+    }
   }
   if (threadIdx.x == 0) {
     // The factor of both gradients that does not depend on the row: grad_scale,
@@ -473,8 +500,8 @@ __global__ void __launch_bounds__(256) dhidden_out_kernel(const Args a) {
       __syncthreads();
     }
     if (lane > 0 || d >= a.D) continue;
-    if (!F32 && a.left && i >= 0) {
-      const float rest = a.left[i];
+    if (!F32 && a.rests && i >= 0) {
+      const float rest = ze::rest_of(a.scales[t], a.weights[t]);
       const __nv_bfloat16* w = static_cast<const __nv_bfloat16*>(a.weight) + a.ids[t] * a.weight_stride + d;
       x.x += rest * float(w[0]);
       if (d + 1 < a.D) x.y += rest * float(w[1]);
@@ -1019,6 +1046,78 @@ __global__ void __launch_bounds__(256) scales_kernel(const Args a) {
   a.weights[t] = expm1f(a.row_logps[t]);
 }
 
+// What G's rounding left of the labels' entries, times their rows of the hidden states,
+// added up by label: a block for each row and 256 columns, which goes on if no earlier row
+// has the row's label; its warps take a stretch of the rows each, whose sums are added
+// in order. More rows are sorted by their labels and added up as the embedding's gradient
+// is. (A step of GPT-2-small's head, this way and by sorting: 257 rows 178 and 194 us, 512
+// 194 and 206, 1024 286 and 293, 2048 457 and 453; where all rows have one label 188 and
+// 191, 204 and 204, 307 and 293, 494 and 458.)
+template <bool Vector>
+__global__ void __launch_bounds__(256) rests_kernel(const Args a) {
+  constexpr int kAhead = 4;
+  __shared__ uint32_t same[kRestRows / 32];
+  __shared__ float part[8][256];
+  let_next_start();
+  wait_for_previous();
+  const int t = blockIdx.x, T = int(a.T), lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (a.rowpos[t] < 0) return;
+  const int32_t y = a.ids[t];
+  bool earlier = false;
+  for (int j0 = 0; j0 < T; j0 += 256) {
+    const int j = j0 + threadIdx.x;
+    const bool has = j < T && a.ids[j] == y && a.rowpos[j] >= 0;
+    earlier |= has && j < t;
+    const unsigned mask = __ballot_sync(~0u, has);
+    if (lane == 0 && j < T) same[j / 32] = mask;
+  }
+  if (__syncthreads_or(earlier)) return;
+  const int64_t d = int64_t(blockIdx.y) * 256 + lane * 8;
+  const int words = (T + 31) / 32, each = (words + 7) / 8, end = min(words, (warp + 1) * each);
+  float sum[8] = {};
+  for (int w = warp * each; w < end; ++w) {
+    for (uint32_t left = same[w]; left;) {
+      uint4 x[kAhead];
+      float times[kAhead];
+#pragma unroll
+      for (int q = 0; q < kAhead; ++q) {
+        times[q] = 0.0f;
+        if (!left) continue;
+        const int64_t u = w * 32 + __ffs(left) - 1;
+        left &= left - 1;
+        times[q] = ze::rest_of(a.scales[u], a.weights[u]);
+        const __nv_bfloat16* row = static_cast<const __nv_bfloat16*>(a.hidden) + u * a.hidden_stride + d;
+        if (Vector && d + 8 <= a.D) {
+          x[q] = *reinterpret_cast<const uint4*>(row);
+        } else {
+          uint32_t words[4] = {};
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (d + j < a.D) words[j / 2] |= uint32_t(reinterpret_cast<const uint16_t*>(row)[j]) << (j % 2 * 16);
+          x[q] = make_uint4(words[0], words[1], words[2], words[3]);
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < kAhead; ++q) {
+        if (times[q] == 0.0f) continue;
+        const uint32_t words[4] = {x[q].x, x[q].y, x[q].z, x[q].w};
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          sum[j] = fmaf(times[q], __uint_as_float(j % 2 ? words[j / 2] & 0xffff0000u : words[j / 2] << 16), sum[j]);
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) part[warp][lane * 8 + j] = sum[j];
+  __syncthreads();
+  const int64_t column = int64_t(blockIdx.y) * 256 + threadIdx.x;
+  if (column >= a.D) return;
+  float all = part[0][threadIdx.x];
+#pragma unroll
+  for (int w = 1; w < 8; ++w) all += part[w][threadIdx.x];
+  a.rest_rows[ze::slot_of(a.slots[y / 32], y % 32) * a.rest_stride + column] = __float2bfloat16_rn(all);
+}
+
 }  // namespace
 
 namespace {
@@ -1098,6 +1197,12 @@ cudaError_t launch_sloped_rows(const Args& a, cudaStream_t s) {
 
 cudaError_t launch_mark(const Args& a, cudaStream_t s) {
   return launch(mark_kernel, kSms, 256, 0, s, true, a);
+}
+
+cudaError_t launch_rests(const Args& a, cudaStream_t s) {
+  const dim3 blocks(unsigned(a.T), unsigned((a.D + 255) / 256));
+  return aligned16(a.hidden, a.hidden_stride * 2) ? launch(rests_kernel<true>, blocks, 256, 0, s, true, a)
+                                                  : launch(rests_kernel<false>, blocks, 256, 0, s, true, a);
 }
 
 cudaError_t launch_dhidden_out(const Args& a, cudaStream_t s) {

@@ -47,6 +47,7 @@
 #include <atomic>
 #include <type_traits>
 
+#include "embedding_internal.h"
 #include "loss_device.cuh"
 
 namespace zl {
@@ -627,7 +628,7 @@ __device__ __forceinline__ void stage_fp32(uint8_t* box, int lane, const float (
 // operand of the two products: rounded once, or in PARTS parts (fp32 storage and
 // a few rows of bf16: loss_host.cpp says when). Each warp stages boxes of its 32
 // rows by 64 columns and stores them by TMA.
-template <int PLANES, int PARTS, bool CE, bool KD, int P>
+template <int PLANES, int PARTS, bool CE, bool KD, int P, bool Slopes>
 __device__ __forceinline__ void gradient_epilogue(const Args& a, const CUtensorMap* out, const Unit& u,
                                                   const Thread& th, int rows, Row& r, uint32_t acc, uint32_t rank,
                                                   uint8_t* box) {
@@ -675,12 +676,9 @@ __device__ __forceinline__ void gradient_epilogue(const Args& a, const CUtensorM
     }
     each_entry(a, u, r, v0 + c0, [&](int at) {
       const float d = r.scale * r.w;
-      float label = 0.0f;
 #pragma unroll
       for (int j = 0; j < 32; ++j)
-        if (j == at) label = g[j] = CE && !KD && a.scales ? d : g[j] - d;  // (by slopes: d is s (p - 1))
-      if (PLANES == 1 && PARTS == 1 && CE && !KD && a.left && at >= 0)
-        a.left[r.i] = label - __bfloat162float(__float2bfloat16_rn(label));
+        if (j == at) g[j] = Slopes ? d : g[j] - d;  // (by slopes: d is s (p - 1))
     });
   };
   // They, or their next part, into half a box.
@@ -770,15 +768,38 @@ __device__ __forceinline__ void hidden_epilogue(const CUtensorMap* out, const Un
   }
 }
 
+// Adds 32 columns of a row of the rests from d on.
+__device__ __forceinline__ void add_rests(const Args& a, const __nv_bfloat16* row, int64_t d, float (&x)[32]) {
+  if (d + 32 <= a.D && (reinterpret_cast<uintptr_t>(row) & 15) == 0) {  // (d: a multiple of 32)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const uint4 w = reinterpret_cast<const uint4*>(row + d)[q];
+      const uint32_t words[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        x[8 * q + 2 * n] += __uint_as_float(words[n] << 16);
+        x[8 * q + 2 * n + 1] += __uint_as_float(words[n] & 0xffff0000u);
+      }
+    }
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 32; ++j)
+    if (d + j < a.D) x[j] += __bfloat162float(row[d + j]);
+}
+
 // dW of a piece's rows, by TMA where the caller's rows are 16-byte aligned
 // (fp32: also the addition to what is there; bf16 would round it twice), else
-// by the threads.
-template <int PLANES>
+// by the threads. `Rests`: to labels' rows what G's rounding left of their entries is
+// added, from their slots. (A warp's rows share a word of `slots`.)
+template <int PLANES, bool Rests>
 __device__ __forceinline__ void weight_epilogue(const Args& a, const Program& prog, const Unit& u, const Thread& th,
                                                 float factor, uint32_t acc, uint32_t rank, uint8_t* box) {
   using T = typename std::conditional<PLANES == 1, __nv_bfloat16, float>::type;
   const int lane = th.row & 31, begin = th.half * 128;
   const int64_t v = u.piece * a.piece + u.m0 + int(rank) * kHalf + th.row;
+  const int64_t slot = Rests && v < a.V ? ze::slot_of(a.slots[v / 32], int(v % 32)) : -1;
+  const __nv_bfloat16* const rests = Rests ? a.rest_rows + max(slot, int64_t(0)) * a.rest_stride : nullptr;
   if (prog.weight_tma) {
     constexpr int wide = 128 / sizeof(T);  // columns of a box
 #pragma unroll 1
@@ -790,6 +811,7 @@ __device__ __forceinline__ void weight_epilogue(const Args& a, const Program& pr
       for (int h = 0; h < wide / 32; ++h) {
         float x[32];
         load_terms(u, acc + c + 32 * h, x);
+        if (Rests && slot >= 0) add_rests(a, rests, u.n0 + c + 32 * h, x);
 #pragma unroll
         for (int j = 0; j < 32; ++j) x[j] *= factor;
         if (PLANES == 3) {
@@ -827,6 +849,7 @@ __device__ __forceinline__ void weight_epilogue(const Args& a, const Program& pr
   for (int c = begin; c < min(u.n, begin + 128); c += 32) {
     float x[32];
     load_terms(u, acc + c, x);
+    if (Rests && slot >= 0) add_rests(a, rests, u.n0 + c, x);
     __syncwarp();
     stage_fp32(box, lane, x);
     __syncwarp();
@@ -843,7 +866,7 @@ __device__ __forceinline__ void weight_epilogue(const Args& a, const Program& pr
 
 // ----------------------------------------------------------------- kernel --
 
-// `Slopes`: the forward pass of a loss by slopes.
+// `Slopes`: of a loss by slopes.
 template <int PLANES, int PARTS, bool CE, bool KD, bool Slopes>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     products_kernel(const __grid_constant__ Args a, const __grid_constant__ Program prog) {
@@ -1179,10 +1202,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       } else if (u.mode == kGradient) {
         const CUtensorMap* out = &prog.g_out[u.piece % kBuffers];
         const int p = CE && KD ? shared_power(float(a.tau)) : 0;
-        if (CE && KD && p == 1) gradient_epilogue<PLANES, PARTS, CE, KD, 1>(a, out, u, th, rows, r, acc, rank, box);
-        else if (CE && KD && p == 2) gradient_epilogue<PLANES, PARTS, CE, KD, 2>(a, out, u, th, rows, r, acc, rank, box);
-        else if (CE && KD && p == 4) gradient_epilogue<PLANES, PARTS, CE, KD, 4>(a, out, u, th, rows, r, acc, rank, box);
-        else gradient_epilogue<PLANES, PARTS, CE, KD, 0>(a, out, u, th, rows, r, acc, rank, box);
+        if (CE && KD && p == 1) gradient_epilogue<PLANES, PARTS, CE, KD, 1, Slopes>(a, out, u, th, rows, r, acc, rank, box);
+        else if (CE && KD && p == 2) gradient_epilogue<PLANES, PARTS, CE, KD, 2, Slopes>(a, out, u, th, rows, r, acc, rank, box);
+        else if (CE && KD && p == 4) gradient_epilogue<PLANES, PARTS, CE, KD, 4, Slopes>(a, out, u, th, rows, r, acc, rank, box);
+        else gradient_epilogue<PLANES, PARTS, CE, KD, 0, Slopes>(a, out, u, th, rows, r, acc, rank, box);
         if (lane == 0 && finished) {  // the unit before: its stores are the older ones
           asm volatile("cp.async.bulk.wait_group %0;" ::"n"(2 * PARTS) : "memory");
           report(finished, finished_tile);
@@ -1196,7 +1219,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       } else {
         // G has been read, and nothing in the launch waits for dW itself.
         if (lane == 0) report(a.used + u.piece, nullptr);
-        weight_epilogue<PLANES>(a, prog, u, th, factor, acc, rank, box);
+        weight_epilogue<PLANES, Slopes && PLANES == 1 && PARTS == 1>(a, prog, u, th, factor, acc, rank, box);
       }
       give_back();
     }
@@ -1252,15 +1275,13 @@ cudaError_t launch(const Args& a, const Program& prog, int device, int sms, cuda
 
 template <int PLANES, int PARTS>
 static cudaError_t launch_terms(const Args& a, const Program& prog, int device, int sms, cudaStream_t s) {
+  if (a.kind >= kPolicy) return launch<PLANES, PARTS, true, false, true>(a, prog, device, sms, s);
   if (!a.has_kd) return launch<PLANES, PARTS, true, false>(a, prog, device, sms, s);
   return a.has_ce ? launch<PLANES, PARTS, true, true>(a, prog, device, sms, s)
                   : launch<PLANES, PARTS, false, true>(a, prog, device, sms, s);
 }
 
 cudaError_t launch_products(const Args& a, const Program& prog, int device, int sms, cudaStream_t s) {
-  if (prog.forward && a.kind >= kPolicy)
-    return a.planes == 3 ? launch<3, 3, true, false, true>(a, prog, device, sms, s)
-                         : launch<1, 1, true, false, true>(a, prog, device, sms, s);
   if (a.planes == 3) return launch_terms<3, 3>(a, prog, device, sms, s);
   // The forward pass forms no G: one kernel serves it for any number of rows.
   return a.parts == 2 && !prog.forward ? launch_terms<1, 2>(a, prog, device, sms, s)
