@@ -638,7 +638,7 @@ int zero_distill_step(const zero_head_loss_t *p, zero_stream_t stream);
  * the probability that the model leaves to the other columns. Of these the largest
  * logit is summed again too. (lse is that of the products' own logits, which a backward
  * call forms again; l_t is not to be taken from it.) The sums over a sequence and the losses are formed in
- * double. A few rows (which depends on sizes and type alone) are worked on in fp32
+ * double. A few rows (which depends on sizes, type and the weight's alignment alone) are worked on in fp32
  * multiply-adds, with the T x V logits in the workspace and no wait that could run
  * out. Everything else -- arithmetic, equal bits, what a wait that runs out does --
  * is as stated above.

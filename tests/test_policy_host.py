@@ -132,6 +132,29 @@ def test_workspaces_are_near_the_cross_entropys(abi):
         assert size <= other <= size + 8192 * 12 + 1024
 
 
+@pytest.mark.parametrize("f32,T,V,D,pad,few", [
+    (0, 8, 50257, 768, 0, True), (0, 16, 50257, 768, 0, False), (0, 8, 131072, 4096, 0, False),
+    (0, 4, 131072, 4096, 0, True), (0, 32, 8000, 512, 0, True), (0, 16, 50257, 64, 0, False),
+    (0, 32, 50257, 8, 0, False), (0, 1, 50257, 769, 0, False), (0, 1, 50257, 768, 1, False), (0, 8, 8000, 513, 0, True),
+    (0, 32, 1009, 97, 0, True), (1, 16, 131072, 4096, 0, True), (1, 32, 50257, 64, 0, False),
+    (1, 32, 8000, 512, 0, True), (1, 64, 8000, 512, 0, False), (1, 8, 50257, 769, 0, True),
+    (1, 16, 50257, 769, 0, False), (1, 64, 1009, 96, 0, True)])
+def test_few_rows_go_by_their_own_work(abi, f32, T, V, D, pad, few):
+    """Which calls are worked on without the tensor cores: those that gain by it, as measured. Their logits are kept,
+    in groups of eight rows; else the packed hidden states, the pieces of G and, for fp32, the weight's parts."""
+    more = dict(T=T, V=V, D=D, precision=abi.ZERO_FP32 if f32 else abi.ZERO_BF16_MIXED, hidden_stride=D,
+                weight_stride=D + pad, dhidden_stride=D, dweight_stride=D)
+    kept = (T + 7) // 8 * 8 * 4 * V
+    parts = 304 * 4 * D + T * 4 * D * 304 + (1 << 20)         # at most: dhidden's sums, statistics, rows
+    for own in (abi.zero_policy_workspace_bytes(problem(abi, **more), policy(abi)),
+                abi.zero_preference_workspace_bytes(problem(abi, **more), preference(abi))):
+        other = abi.zero_xent_workspace_bytes(problem(abi, **more))
+        if few:
+            assert own != other and kept <= own <= kept + parts
+        else:
+            assert other <= own <= other + 16 * T + V // 2 + 4096
+
+
 @pytest.mark.parametrize("op", ["policy", "preference"])
 @pytest.mark.parametrize("wrt", ["hidden", "weight", "both"])
 def test_second_derivatives_raise(abi, monkeypatch, op, wrt):

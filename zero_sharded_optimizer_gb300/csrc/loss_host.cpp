@@ -230,21 +230,40 @@ bool weight_in_place(const zero_head_loss_t* p) {
 // small with the weight and latency is all. GPU time of a policy's step in a replayed
 // graph, here and on the tensor cores, us (V x D):
 //   rows            1          4          8          16         32         64
-//   bf16 1009 x 96       29, 48     29, 49     32, 49     37, 49     45, 50     58, 50
-//   bf16 8000 x 512      40, 63     43, 64     48, 64     55, 64     70, 64     96, 65
-//   bf16 50257 x 768     90, 138    100, 134   123, 136   192, 137
-//   bf16 131072 x 4096   671, 962   753, 963   1046, 964
-//   fp32 1009 x 96       27, 55     27, 56     29, 56     31, 58     37, 57     46, 58
-//   fp32 8000 x 512      42, 93     44, 93     49, 93     57, 95     76, 95     113, 96
-//   fp32 50257 x 768     137, 365   137, 365   158, 364   244, 363   409, 363
-//   fp32 131072 x 4096   1174, 3772 1272, 3770 1604, 3765 2993, 3779 5912, 3785
-// (A call that is issued by the host takes 47 us here and 63 on the tensor cores.)
+//   bf16 1009 x 96       29, 55     31, 56     35, 57     39, 57     47, 57
+//   bf16 8000 x 512      41, 70     43, 71     48, 71     53, 72     68, 71
+//   bf16 50257 x 64      57, 83     62, 84     72, 84     109, 84    174, 83
+//   bf16 50257 x 256     53, 99     58, 100    68, 100    91, 101    140, 100
+//   bf16 50257 x 768     96, 144    104, 144   131, 144   198, 145   332, 142
+//   bf16 32000 x 2048    134, 203   141, 202   187, 201   298, 201   533, 201
+//   bf16 131072 x 64     90, 141    99, 141    122, 142   216, 142   389, 140
+//   bf16 131072 x 4096   691, 986   770, 982   1069, 983
+//   fp32 1009 x 96       30, 62                32, 63     33, 63     39, 63     47, 64
+//   fp32 8000 x 512      41, 100               47, 100    57, 103    78, 100    117, 106
+//   fp32 50257 x 64      51, 122               59, 122    80, 122    123, 121   211, 121
+//   fp32 50257 x 256     78, 165               92, 166    125, 166   186, 166   313, 165
+//   fp32 50257 x 768     137, 375              160, 373   251, 375   422, 374   786, 377
+//   fp32 131072 x 64     76, 204               92, 206    153, 205   271, 203   505, 204
+//   fp32 131072 x 4096   1204, 3789            1618, 3791
+// and with the weight's rows off 16 bytes, which are read element by element here:
+//   bf16 1009 x 97       31, 60     33, 61     37, 62     43, 62     55, 62
+//   bf16 8000 x 513      60, 88     65, 89     72, 89     92, 89     134, 89
+//   bf16 50257 x 769     261, 224   265, 222   290, 222   499, 223   810, 223
+//   fp32 8000 x 513      49, 113               57, 114    76, 114    115, 115   184, 116
+//   fp32 50257 x 769     256, 444              284, 444   518, 443   907, 442   1722, 444
+// A warp takes 256 columns of bf16 or 128 of fp32 at a time and a block eight rows,
+// whatever there is of them, so that is what the work is counted in. (A call that is issued
+// by the host takes 47 us here and 63 on the tensor cores.)
 bool few_rows(const zero_head_loss_t* p) {
   const bool f32 = p->precision == ZERO_FP32;
-  const int64_t bytes = round_up(p->D, f32 ? 128 : 256) * (f32 ? 4 : 2);
-  if (p->T < 1 || bytes > zl::kFewHiddenBytes / zl::kFewGroup) return false;  // (a group's hidden states)
-  const double work = double(p->T) * double(p->V) * double(p->D);
-  return p->T <= (f32 ? 16 : 4) || (p->T <= (f32 ? 64 : 32) && work <= (f32 ? 2e8 : 1e8));
+  const int es = f32 ? 4 : 2;
+  const int64_t wide = round_up(p->D, f32 ? 128 : 256);
+  if (p->T < 1 || wide * es > zl::kFewHiddenBytes / zl::kFewGroup) return false;  // (a group's hidden states)
+  const bool aligned = reinterpret_cast<uintptr_t>(p->weight) % 16 == 0 && p->weight_stride * es % 16 == 0;
+  const double weight = double(p->V) * double(wide);
+  const int64_t most = f32 ? (aligned ? 16 : 8) : !aligned ? 0 : weight <= 1e8 ? 8 : 4;
+  return p->T <= most ||
+         (p->T <= (f32 ? 64 : 32) && double(round_up(p->T, zl::kFewGroup)) * weight <= (aligned ? 1.5e8 : 1e8));
 }
 
 // The sums of the rests: the embedding's gradient of the labels, whose rows are the hidden
