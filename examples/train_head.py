@@ -53,7 +53,7 @@ class Ranks:
 
     def hidden(self, rank: int, tokens, flat=None):
         wte, mix = self.split(self.params[rank] if flat is None else flat)
-        x = embedding.embedding_forward(tokens.contiguous(), wte)
+        x = embedding.embedding_forward(tokens, wte)
         return (x + torch.tanh(x @ mix)) * 2.0
 
     def step(self, batches, loss) -> float:

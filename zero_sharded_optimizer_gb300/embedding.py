@@ -10,7 +10,8 @@ embedding's is then added to the rows that have a token::
     losses.xent_step(hidden, wte, labels, dweight=dwte)
     embedding.embedding_backward(tokens, dx, dweight=dwte, accumulate=True)
 
-``ids`` is an int64 CUDA tensor of any shape, contiguous; ``weight`` a [V, D]
+``ids`` is an int64 CUDA tensor of any shape; of a view, as ``tokens[:, :-1]``, the
+call makes a copy (one that is expanded is taken by ``embedding`` alone). ``weight`` is a [V, D]
 CUDA tensor, float32 or bfloat16, with adjacent elements in a row and any row
 stride; what belongs to the tokens has ids' shape and a last dimension D.
 
@@ -32,15 +33,20 @@ from . import abi
 from .losses import _PRECISION, _matrix, _named
 
 
-def _tokens(ids, device) -> int:
-    """The address of the ids."""
+def _tokens(ids, device, stream):
+    """The ids side by side: themselves, or a copy made on ``stream``."""
     if not isinstance(ids, torch.Tensor) or not ids.is_cuda or ids.dtype is not torch.int64:
         raise TypeError("ids must be a torch.int64 CUDA tensor")
     if ids.device != device:
         raise ValueError(f"ids is on {ids.device}, expected {device}")
-    if not ids.is_contiguous():
-        raise ValueError("ids must be contiguous")
-    return ids.data_ptr()
+    if ids.is_contiguous():
+        return ids
+    if any(step == 0 and n > 1 for step, n in zip(ids.stride(), ids.shape)):
+        raise ValueError("ids must not be expanded")
+    if stream is not None:
+        ids.record_stream(stream)
+    with torch.cuda.stream(stream):     # None: the current one
+        return ids.contiguous()
 
 
 def _rows(t, what: str, ids, D=None, dtype=None, device=None):
@@ -83,9 +89,9 @@ def embedding_forward(ids, weight, *, scale: float = 1.0, out=None, stream=None)
     w, stride = _matrix(weight, "weight")
     device, dtype = w.device, w.dtype
     V, D = w.shape
-    at = _tokens(ids, device)
     stream = _named(stream, device)
-    p = abi.Embedding(ids.numel(), V, D, _PRECISION[dtype], 0, at, -1, scale, w.data_ptr(), stride)
+    ids = _tokens(ids, device, stream)
+    p = abi.Embedding(ids.numel(), V, D, _PRECISION[dtype], 0, ids.data_ptr(), -1, scale, w.data_ptr(), stride)
     made = None
     if out is None:
         out = made = _empty((*ids.shape, D), dtype, device, stream)
@@ -107,8 +113,8 @@ def embedding_backward(ids, dout, vocabulary: int | None = None, *, scale: float
     else:
         raise TypeError("ids and dout must be CUDA tensors")
     device, dtype, D = m.device, m.dtype, m.shape[1]
-    at = _tokens(ids, device)
     stream = _named(stream, device)
+    ids = _tokens(ids, device, stream)
     made = None
     if dweight is None:
         if accumulate:
@@ -117,7 +123,7 @@ def embedding_backward(ids, dout, vocabulary: int | None = None, *, scale: float
             raise ValueError("the vocabulary's size or a dweight must be given")
         dweight = made = _empty((vocabulary, D), dtype, device, stream)
     w, ws = _matrix(dweight, "dweight", dtype, vocabulary, D, device)
-    p = abi.Embedding(ids.numel(), w.shape[0], D, _PRECISION[dtype], 1 if accumulate else 0, at, padding_id, scale,
+    p = abi.Embedding(ids.numel(), w.shape[0], D, _PRECISION[dtype], 1 if accumulate else 0, ids.data_ptr(), padding_id, scale,
                       None, 0, None, 0, m.data_ptr(), stride, w.data_ptr(), ws)
     _run(p, abi.zero_embedding_backward, device, stream, (ids, m) if made is not None else (ids, m, w), made)
     return dweight
@@ -128,6 +134,8 @@ def embedding_backward(ids, dout, vocabulary: int | None = None, *, scale: float
 class _Lookup(torch.autograd.Function):
     @staticmethod
     def forward(ctx, weight, ids, scale, padding_id):
+        if isinstance(ids, torch.Tensor):
+            ids = ids.contiguous()
         ctx.save_for_backward(ids)
         ctx.options = weight.shape[0], scale, padding_id
         return embedding_forward(ids, weight, scale=scale)
