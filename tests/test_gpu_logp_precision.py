@@ -141,6 +141,21 @@ def test_errors_of_one_sign(losses, cuda, kind, few, favour, other):
     assert float(off.square().mean().sqrt()) < 1e-6
 
 
+@pytest.mark.parametrize("kind", TYPES)
+def test_mean_error_of_many_exponentials(losses, cuda, kind):
+    """Log-probabilities of labels that nothing favours are log-sum-exps of 5000 exponentials, beside which nothing is
+    off one way: the logits are sums of 16 products, one instruction of the tensor cores. Exponentials that are
+    cut off take 4.3e-8 of the sum, and half as much again where they are rescaled. l is rounded by steps of 2^-20,
+    an rms of 2.8e-7, or 4e-9 as a mean of 6000; 3e-8 is beyond chance and below what the exponentials would take."""
+    dt, g = TYPES[kind], torch.Generator().manual_seed(12)
+    for T, calls in ((6000, 1), (8 if kind == "bf16" else 16, 400)):
+        off = []
+        for _ in range(calls):
+            h, w, y = favoured(T, 4931, 16, dt, 0.0, False, g, cuda)
+            off.append(policy_logps(losses, h, w, y).logps.double() - exact_logps(h, w, y))
+        assert abs(float(torch.cat(off).mean())) < 3e-8, T
+
+
 @pytest.mark.parametrize("other", [False, True])
 @pytest.mark.parametrize("T", [16, 100, 600])
 def test_gradients_of_rows_that_expect_a_token(losses, cuda, T, other):

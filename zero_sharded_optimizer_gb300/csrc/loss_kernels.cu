@@ -1054,13 +1054,14 @@ __global__ void __launch_bounds__(256) scales_kernel(const Args a) {
 // 194 and 206, 1024 286 and 293, 2048 457 and 453; where all rows have one label 188 and
 // 191, 204 and 204, 307 and 293, 494 and 458.)
 template <bool Vector>
-__global__ void __launch_bounds__(256) rests_kernel(const Args a) {
+__global__ void __launch_bounds__(256) rests_kernel(const Args a, int64_t wide) {
   constexpr int kAhead = 4;
   __shared__ uint32_t same[kRestRows / 32];
   __shared__ float part[8][256];
   let_next_start();
   wait_for_previous();
-  const int t = blockIdx.x, T = int(a.T), lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int t = int(blockIdx.x / wide), T = int(a.T), lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t d0 = blockIdx.x % wide * 256;
   if (a.rowpos[t] < 0) return;
   const int32_t y = a.ids[t];
   bool earlier = false;
@@ -1072,7 +1073,7 @@ __global__ void __launch_bounds__(256) rests_kernel(const Args a) {
     if (lane == 0 && j < T) same[j / 32] = mask;
   }
   if (__syncthreads_or(earlier)) return;
-  const int64_t d = int64_t(blockIdx.y) * 256 + lane * 8;
+  const int64_t d = d0 + lane * 8;
   const int words = (T + 31) / 32, each = (words + 7) / 8, end = min(words, (warp + 1) * each);
   float sum[8] = {};
   for (int w = warp * each; w < end; ++w) {
@@ -1110,7 +1111,7 @@ __global__ void __launch_bounds__(256) rests_kernel(const Args a) {
 #pragma unroll
   for (int j = 0; j < 8; ++j) part[warp][lane * 8 + j] = sum[j];
   __syncthreads();
-  const int64_t column = int64_t(blockIdx.y) * 256 + threadIdx.x;
+  const int64_t column = d0 + threadIdx.x;
   if (column >= a.D) return;
   float all = part[0][threadIdx.x];
 #pragma unroll
@@ -1200,9 +1201,9 @@ cudaError_t launch_mark(const Args& a, cudaStream_t s) {
 }
 
 cudaError_t launch_rests(const Args& a, cudaStream_t s) {
-  const dim3 blocks(unsigned(a.T), unsigned((a.D + 255) / 256));
-  return aligned16(a.hidden, a.hidden_stride * 2) ? launch(rests_kernel<true>, blocks, 256, 0, s, true, a)
-                                                  : launch(rests_kernel<false>, blocks, 256, 0, s, true, a);
+  const int64_t wide = (a.D + 255) / 256;
+  auto* kernel = aligned16(a.hidden, a.hidden_stride * 2) ? rests_kernel<true> : rests_kernel<false>;
+  return launch(kernel, unsigned(a.T * wide), 256, 0, s, true, a, wide);
 }
 
 cudaError_t launch_dhidden_out(const Args& a, cudaStream_t s) {
