@@ -636,13 +636,15 @@ int zero_distill_step(const zero_head_loss_t *p, zero_stream_t stream);
  * -log(1 + sum over the other columns of e^(z - z_y)), because these losses hang on
  * small differences of log-probabilities: what l_t is off by is in proportion to
  * the probability that the model leaves to the other columns. Of these the largest
- * logit is summed again too. (lse is that of the products' own logits, which a backward
- * call forms again; l_t is not to be taken from it. Logits beyond 1e9 in size are a few
- * rows' alone, see below: the matrix kernels' exponents do not hold them.) The sums over a sequence and the losses are formed in
- * double. A few rows (which depends on sizes, type and the weight's alignment alone) are worked on in fp32
- * multiply-adds, with the T x V logits in the workspace and no wait that could run
- * out. Everything else -- arithmetic, equal bits, what a wait that runs out does --
- * is as stated above.
+ * logit is summed again too. (lse is that of the products' own logits, which a
+ * backward call forms again; l_t is not to be taken from it.) The sums over a
+ * sequence and the losses are formed in double. A few rows (which depends on sizes,
+ * type and the weight's alignment alone) are worked on in fp32 multiply-adds, with
+ * the T x V logits in the workspace and no wait that could run out; they may have
+ * finite logits of any size, others up to 1e9, beyond which a matrix kernel's
+ * exponents do not hold them. dhidden holds sums of the call's own until it is
+ * written. Everything else -- arithmetic, equal bits, what a wait that runs out does
+ * -- is as stated above.
  *
  * Of the zero_head_loss_t they take: labels (no teacher fields), loss (T values,
  * or `pairs`), lse, reduced, dloss (NONE: as many as loss) and the gradients. */

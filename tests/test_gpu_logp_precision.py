@@ -275,3 +275,16 @@ def test_labels_sums_with_rows_that_are_not_numbers(losses, cuda):
     bad[::3], bad[y < 0] = math.nan, math.inf
     got = losses.policy_step(bad, w, y, old, adv, reduction="sum")
     assert torch.equal(got.dweight, good.dweight) and torch.equal(got.dhidden, good.dhidden)
+
+
+@pytest.mark.parametrize("T", [300, 900])
+def test_labels_sums_leave_out_an_ignored_id(losses, cuda, T):
+    """An ignore_index inside the vocabulary: its rows are as those without a label."""
+    V, D, g = 700, 48, torch.Generator().manual_seed(T)
+    h, w, y = labelled(T, V, D, "frequent", g, cuda)
+    adv, old = torch.randn(T, generator=g).to(cuda), torch.full((T,), -5.0, device=cuda)
+    for ignored in (0, 3):
+        want = losses.policy_step(h, w, torch.where(y == ignored, IGNORE, y), old, adv, reduction="sum")
+        got = losses.policy_step(h, w, torch.where(y < 0, ignored, y), old, adv, reduction="sum", ignore_index=ignored)
+        for a, b in zip(got, want):
+            assert a is None and b is None or torch.equal(a, b)
